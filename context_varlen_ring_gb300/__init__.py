@@ -20,6 +20,8 @@ __all__ = [
     "zigzag_plan", "zigzag_permute", "zigzag_unpermute", "varlen_attn_partial", "varlen_attn_partial_dev",
     "lse_merge",
     "ring_attn_fwd", "ring_attn_bwd", "ring_rank_pairs", "ring_plan_stats", "device_status", "selftest_wait_timeout",
+    "rope_inv_freq", "rope_axes", "rope_fwd", "rope_bwd", "kv_cache_append", "paged_attn_fwd",
+    "paged_attn_workspace_bytes",
     "RA_ZZ_GLOBAL", "RA_ZZ_PER_DOC", "RA_SCHED_FUSED", "RA_SCHED_STEPWISE", "RA_SCHED_ALLGATHER", "RaError",
 ]
 
@@ -331,3 +333,7 @@ def device_status(stream=None) -> int:
 def selftest_wait_timeout(budget_us: int = 1000):
     check(lib().ra_selftest_wait_timeout(int(budget_us), _stream(torch.device("cuda"))),
           "ra_selftest_wait_timeout")
+
+
+from .serving import (kv_cache_append, paged_attn_fwd, paged_attn_workspace_bytes, rope_axes, rope_bwd,  # noqa: E402
+                      rope_fwd, rope_inv_freq)

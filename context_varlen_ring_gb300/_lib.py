@@ -39,7 +39,23 @@ EXPORTS = (
     "ra_varlen_attn_partial_noalloc", "ra_ring_plan_stats", "ra_partial_table_bytes",
     "ra_ring_workspace_bytes_masked", "ra_ring_attn_fwd_masked", "ra_ring_attn_bwd_masked",
     "ra_ring_plan_stats_masked", "ra_varlen_attn_partial_dev",
+    "ra_rope_fwd", "ra_rope_bwd", "ra_kv_cache_append", "ra_paged_attn_workspace_bytes", "ra_paged_attn_fwd",
 )
+
+
+class Rope(ctypes.Structure):
+    """ra_rope of include/ra.h."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("n_pairs", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32)]
+
+
+class PagedKV(ctypes.Structure):
+    """ra_paged_kv of include/ra.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
 
 _lib = None
 
@@ -78,6 +94,12 @@ def _declare(L):
         "ra_ring_rank_pairs": (i32, [P, i32, i32, i32, i32, i32, P]),
         "ra_ring_plan_stats": (i32, [P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, P]),
         "ra_ring_plan_stats_masked": (i32, [P, i32, i32, i32, i32, i32, P, P, i32, i32, i32, P]),
+        "ra_rope_fwd": (i32, [P, P, P, P, i32, i64, i32, i32, i32, i64, i64, i64, i64, P, P, P]),
+        "ra_rope_bwd": (i32, [P, P, P, P, i32, i64, i32, i32, i32, i64, i64, i64, i64, P, P, P]),
+        "ra_kv_cache_append": (i32, [P, P, i64, i64, i64, P, P, i64, P, P, i32, P, P, i32, i64, i64, P, P, P]),
+        "ra_paged_attn_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32]),
+        "ra_paged_attn_fwd": (i32, [P, i64, i64, i32, P, P, i64, P, P, i32, P, i64, P, P, i32, i32, i32, f32,
+                                    P, i32, P, P, sz, P]),
         "ra_get_device_status": (i32, [P]),
         "ra_selftest_wait_timeout": (i32, [i64, P]),
         "ra_status_string": (ctypes.c_char_p, [i32]),

@@ -29,6 +29,24 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// ---------------------------------------------------------------- segments
+// How many of the n non-decreasing ends are <= t: the segment that holds t.
+// The whole warp searches, 32 probes a round (n <= 1024 in two rounds).  With
+// ends that decrease the result is still in [0, n].
+__device__ __forceinline__ int segment_of(const int32_t *ends, int n, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 0) {
+        const int step = (n + 31) / 32;
+        const int q = (lane + 1) * step - 1;
+        const bool le = q < n && (int64_t)__ldg(ends + lo + q) <= t;
+        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        lo += c * step;
+        n = min(step - 1, n - c * step);
+    }
+    return lo;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

@@ -214,6 +214,77 @@ struct DevTileArgs {
 };
 cudaError_t launch_tile_build(const DevTileArgs &a, cudaStream_t st);
 
+// ------------------------------------------------------------ rotary positions, cache append
+struct RopeJob {
+    const void *x;
+    void *y;
+    int64_t x_stride, y_stride;        // elements between tokens
+    int heads;
+    int rotate;                        // 0: copied
+    int paged;                         // written to the token's cache row instead of its token row
+};
+// Travels with the launch (a kernel parameter), so a captured graph keeps it.
+struct RopeParams {
+    RopeJob jobs[3];
+    int njobs, total_heads, d;
+    int64_t T;
+    const int32_t *pos;                // DEVICE [axes][T]
+    int n_pairs, adjacent, inverse;
+    int units, rot_units, heads_per_block;  // set by launch_rope
+    // cache rows (cu != NULL): logical index kv_lens[b] - n_b + j through the page table
+    const int32_t *cu, *kv_lens, *page_table;
+    int64_t table_width, n_pages, page_stride, token_stride, head_stride;
+    int B, page_size;
+    int *status;
+    uint64_t turns[128];               // inv_freq / (2 pi) modulo 1, in units of 2^-64
+    uint8_t axis[128];
+};
+void rope_table(RopeParams &p, const double *inv_freq, const uint8_t *axes, int n_pairs, int adjacent, int inverse);
+cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st);
+
+// ------------------------------------------------------------ paged attention
+// Families of segments: 0 the sequences' own keys, 1 the groups' prefixes.
+// Each (segment, tile of `rt` query rows, KV head) is a unit of ceil(keys / kt)
+// key tiles; the units' tiles form one line that the family's `n` CTAs split
+// evenly.  What a CTA computes of a unit goes to partial slot unit + CTA.
+struct PagedSeg {
+    int tok0, n, len, w;               // first query token, query tokens, keys, key tiles
+};
+struct PagedHdr {
+    long long W[2], per[2];            // tiles in all, tiles a CTA
+    int err, pad[7];
+};
+struct PagedFamily {
+    int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
+    PagedSeg *seg;                     // [S]
+    long long *cumW;                   // [S + 1]
+    int *cumU;                         // [S + 1]
+    const int32_t *table;
+    int64_t width;
+    float *acc, *ml;                   // [slots][rt][d], [slots][rt][2]: sum p v; running maximum (log2), sum p
+};
+struct PagedArgs {
+    const void *q;
+    int64_t q_stride, T;
+    int Hq, Hkv, G, d, dtype;
+    const void *k, *v;
+    int64_t n_pages, page_stride, token_stride, head_stride;
+    int page_size, B, n_groups, causal;
+    const int32_t *cu, *kv_lens, *prefix_lens, *groups;
+    float scale_log2;
+    PagedHdr *hdr;
+    PagedFamily f[2];
+    void *out;
+    int out_dtype;
+    float *lse;
+    int *status;
+};
+constexpr int kPagedMaxCtas = 1024;
+cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st);
+cudaError_t launch_paged_simt(const PagedArgs &a, int family, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st);
+int paged_simt_ctas(int rt, int d);    // CTAs of the SIMT kernel that the current device holds at once
+
 // Device-wait self-test (see ra_selftest_wait_timeout).
 cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t st);
 

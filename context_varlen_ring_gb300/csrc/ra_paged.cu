@@ -1,0 +1,430 @@
+// ra_paged.cu -- attention over a paged cache with shared prefixes: the plan
+// (who computes what), the SIMT kernel for fp32 and for the shapes that the
+// tensor-core kernels do not take, and the kernel that joins the partials.
+//
+// Mathematics: out = sum_j p_j v_j / sum_j p_j with p_j = 2^(s_j - m), s_j the
+// scaled score in base 2 and m the running maximum, over two key sets: the
+// prefix of the token's group and its sequence's own keys.  Both sets, and
+// the pieces that one set is split into, give partials (m, sum p, sum p v)
+// that add after scaling by 2^(m - M).
+//
+// Split: every (segment, tile of query rows, KV head) is a unit of key tiles.
+// All units' tiles form one line, cut into equal runs of tiles, one a CTA, so
+// the work is even whatever the lengths, and one long sequence fills the GPU
+// as a full batch does.  Unit u and CTA c meet at most once and both only
+// grow along the line, so u + c numbers the partials without a table.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ra_dev.cuh"
+#include "ra_kernels.h"
+#include "ra_paged.cuh"
+
+namespace ra {
+namespace {
+
+using namespace dev;
+
+// ------------------------------------------------------------------ plan
+constexpr int kPlanThreads = 512;
+
+struct UW {
+    int u;
+    long long w;
+};
+
+// Exclusive scan over the block; `total` is the block's sum.
+__device__ __forceinline__ UW block_scan(UW v, UW *warp_sum, UW &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    UW x = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x.u, s);
+        const long long w = __shfl_up_sync(0xffffffffu, x.w, s);
+        if (lane >= s) {
+            x.u += u;
+            x.w += w;
+        }
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    UW before{0, 0};
+    total = UW{0, 0};
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+        if (i < warp) {
+            before.u += warp_sum[i].u;
+            before.w += warp_sum[i].w;
+        }
+        total.u += warp_sum[i].u;
+        total.w += warp_sum[i].w;
+    }
+    __syncthreads();
+    return UW{before.u + x.u - v.u, before.w + x.w - v.w};
+}
+
+// One block: checks the segment arrays, and writes each family's segments,
+// the running counts of units and tiles, and the tiles a CTA.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedArgs a) {
+    __shared__ UW warp_sum[kPlanThreads / 32];
+    int bad = 0;
+    for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
+        const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.kv_lens[b];
+        bad |= c0 < 0 || c1 < c0 || c1 > a.T || len < 0 || len > a.f[0].width * a.page_size;
+    }
+    for (int g = threadIdx.x; g < a.n_groups; g += kPlanThreads) {
+        const int g0 = a.groups[g], g1 = a.groups[g + 1], len = a.prefix_lens[g];
+        bad |= g0 < 0 || g1 < g0 || g1 > a.B || len < 0 || len > a.f[1].width * a.page_size;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        if (threadIdx.x == 0) {
+            record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            a.hdr->W[0] = a.hdr->W[1] = 0;
+            a.hdr->per[0] = a.hdr->per[1] = 1;
+            a.hdr->err = 1;
+        }
+        return;
+    }
+    for (int fi = 0; fi < 2; ++fi) {
+        const PagedFamily &f = a.f[fi];
+        UW base{0, 0};
+        for (int s0 = 0; s0 < f.S; s0 += kPlanThreads) {
+            const int s = s0 + threadIdx.x;
+            UW v{0, 0};
+            if (s < f.S) {
+                const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
+                PagedSeg g;
+                g.tok0 = a.cu[b0];
+                g.n = a.cu[b1] - g.tok0;
+                g.len = fi ? a.prefix_lens[s] : a.kv_lens[s];
+                g.w = g.n > 0 ? (g.len + f.kt - 1) / f.kt : 0;
+                f.seg[s] = g;
+                v.u = (int)(((long long)g.n * a.G + f.rt - 1) / f.rt) * a.Hkv;
+                v.w = (long long)v.u * g.w;
+            }
+            UW total;
+            const UW at = block_scan(v, warp_sum, total);
+            if (s < f.S) {
+                f.cumU[s] = base.u + at.u;
+                f.cumW[s] = base.w + at.w;
+            }
+            base.u += total.u;
+            base.w += total.w;
+        }
+        if (threadIdx.x == 0) {
+            f.cumU[f.S] = base.u;
+            f.cumW[f.S] = base.w;
+            a.hdr->W[fi] = base.w;
+            a.hdr->per[fi] = max(1ll, (base.w + f.n - 1) / f.n);
+        }
+    }
+    if (threadIdx.x == 0) a.hdr->err = 0;
+}
+
+// ------------------------------------------------------------------ SIMT
+constexpr int kKT = 64;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4 *>(p);
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y));
+        return make_float4(x.x, x.y, y.x, y.y);
+    }
+}
+
+template <int NV, int RPW, int WARPS>
+constexpr size_t simt_smem() {
+    return sizeof(float) * ((size_t)kKT * (32 * NV + 4) + (size_t)kKT * 32 * NV + (size_t)RPW * WARPS * 32 * NV +
+                            (size_t)RPW * WARPS * kKT);
+}
+
+// fp32 arithmetic throughout.  A warp owns RPW query rows: a lane scores keys
+// lane and lane + 32 for all of them (K rows padded by one vector, so the
+// 16-byte reads of neighbouring keys spread over the banks; Q is broadcast),
+// then owns columns lane + 32 e of the products.  FMAs per shared-memory
+// wavefront: RPW * 8 / (8 + RPW) in the scores, so 8 rows a warp keep the FMA
+// pipe the limit; 4 rows a warp serve the few rows of single-token steps.
+template <typename T, int NV, int RPW, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_constant__ PagedArgs a, int fi) {
+    constexpr int D = 32 * NV, RT = RPW * WARPS, KS = D + 4;
+    extern __shared__ float4 smem4[];
+    float *Ks = reinterpret_cast<float *>(smem4), *Vs = Ks + kKT * KS, *Qs = Vs + kKT * D, *Ps = Qs + RT * D;
+    const PagedFamily &f = a.f[fi];
+    const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
+    const int cta = blockIdx.x;
+    long long x = cta * per;
+    const long long x1 = min(W, x + per);
+    if (x >= x1) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = paged_find(f, x);
+    while (x < x1) {
+        while (f.cumW[s + 1] <= x) ++s;
+        const PagedSeg g = f.seg[s];
+        const PagedUnit u = paged_unit(a, f, g, s, x, x1);
+        const int R = g.n * a.G, r0 = u.rtile * RT;
+        __syncthreads();  // the last unit's readers are done with Q
+        for (int i = threadIdx.x; i < RT * (D / 4); i += WARPS * 32) {
+            const int r = i / (D / 4), c = i % (D / 4) * 4, row = r0 + r;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < R) {
+                const int64_t t = g.tok0 + row / a.G;
+                v = load4(static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)(u.h * a.G + row % a.G) * D + c);
+                v.x *= a.scale_log2;
+                v.y *= a.scale_log2;
+                v.z *= a.scale_log2;
+                v.w *= a.scale_log2;
+            }
+            *reinterpret_cast<float4 *>(Qs + r * D + c) = v;
+        }
+        float m[RPW], l[RPW], acc[RPW][NV];
+        int limit[RPW];
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < NV; ++e) acc[r][e] = 0.f;
+            limit[r] = paged_limit(a, g, fi, r0 + warp * RPW + r);
+        }
+        for (int tile = u.t0; tile < u.t1; ++tile) {
+            const int k0 = tile * kKT;
+            __syncthreads();
+            for (int i = threadIdx.x; i < kKT * (D / 4); i += WARPS * 32) {
+                const int j = i / (D / 4), c = i % (D / 4) * 4;
+                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+                const int64_t off = paged_row(a, f, s, g.len, k0 + j);
+                if (off >= 0) {
+                    kv = load4(static_cast<const T *>(a.k) + off + u.h * a.head_stride + c);
+                    vv = load4(static_cast<const T *>(a.v) + off + u.h * a.head_stride + c);
+                }
+                *reinterpret_cast<float4 *>(Ks + j * KS + c) = kv;
+                *reinterpret_cast<float4 *>(Vs + j * D + c) = vv;
+            }
+            __syncthreads();
+            float s0[RPW], s1[RPW];
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) s0[r] = s1[r] = 0.f;
+            const float *qw = Qs + warp * RPW * D;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 ka = *reinterpret_cast<const float4 *>(Ks + lane * KS + c);
+                const float4 kb = *reinterpret_cast<const float4 *>(Ks + (lane + 32) * KS + c);
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) {
+                    const float4 qv = *reinterpret_cast<const float4 *>(qw + r * D + c);
+                    s0[r] = fmaf(qv.x, ka.x, fmaf(qv.y, ka.y, fmaf(qv.z, ka.z, fmaf(qv.w, ka.w, s0[r]))));
+                    s1[r] = fmaf(qv.x, kb.x, fmaf(qv.y, kb.y, fmaf(qv.z, kb.z, fmaf(qv.w, kb.w, s1[r]))));
+                }
+            }
+            float *pw = Ps + warp * RPW * kKT;
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) {
+                const float xa = k0 + lane < limit[r] ? s0[r] : -INFINITY;
+                const float xb = k0 + lane + 32 < limit[r] ? s1[r] : -INFINITY;
+                float mx = fmaxf(xa, xb);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[r], mx), use = mn == -INFINITY ? 0.f : mn;
+                const float pa = exp2f(xa - use), pb = exp2f(xb - use), alpha = exp2f(m[r] - use);
+                l[r] = l[r] * alpha + pa + pb;  // a lane's own keys; joined at the end
+                m[r] = mn;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) acc[r][e] *= alpha;
+                pw[r * kKT + lane] = pa;
+                pw[r * kKT + lane + 32] = pb;
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int j = 0; j < kKT; j += 4) {
+                float v0[NV], v1[NV], v2[NV], v3[NV];
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    v0[e] = Vs[j * D + lane + 32 * e];
+                    v1[e] = Vs[(j + 1) * D + lane + 32 * e];
+                    v2[e] = Vs[(j + 2) * D + lane + 32 * e];
+                    v3[e] = Vs[(j + 3) * D + lane + 32 * e];
+                }
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) {
+                    const float4 p = *reinterpret_cast<const float4 *>(pw + r * kKT + j);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+                        acc[r][e] = fmaf(p.x, v0[e], fmaf(p.y, v1[e], fmaf(p.z, v2[e], fmaf(p.w, v3[e], acc[r][e]))));
+                }
+            }
+            __syncwarp();
+        }
+        const int64_t slot = (int64_t)u.unit + cta;
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+            const int64_t at = slot * RT + warp * RPW + r;
+            float sum = l[r];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (r0 + warp * RPW + r < R) {
+#pragma unroll
+                for (int e = 0; e < NV; ++e) f.acc[at * D + lane + 32 * e] = acc[r][e];
+                if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m[r], sum);
+            }
+        }
+        x += u.t1 - u.t0;
+    }
+}
+
+template <typename T, int NV, int RPW, int WARPS>
+cudaError_t simt_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    auto kernel = paged_simt_kernel<T, NV, RPW, WARPS>;
+    constexpr size_t smem = simt_smem<NV, RPW, WARPS>();
+    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, WARPS * 32, smem);
+    kernel<<<a->f[fi].n, WARPS * 32, smem, st>>>(*a, fi);
+    return cudaGetLastError();
+}
+
+template <typename T, int RPW, int WARPS>
+cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    switch (d / 32) {
+        case 1: return simt_launch<T, 1, RPW, WARPS>(a, fi, ctas, st);
+        case 2: return simt_launch<T, 2, RPW, WARPS>(a, fi, ctas, st);
+        case 3: return simt_launch<T, 3, RPW, WARPS>(a, fi, ctas, st);
+        case 4: return simt_launch<T, 4, RPW, WARPS>(a, fi, ctas, st);
+        case 5: return simt_launch<T, 5, RPW, WARPS>(a, fi, ctas, st);
+        case 6: return simt_launch<T, 6, RPW, WARPS>(a, fi, ctas, st);
+        case 7: return simt_launch<T, 7, RPW, WARPS>(a, fi, ctas, st);
+        case 8: return simt_launch<T, 8, RPW, WARPS>(a, fi, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// ------------------------------------------------------------------ join
+// One warp per (token, head) row: the largest maximum of its partials, their
+// weights 2^(m - M), and the weighted sums in the order prefix, own keys,
+// ascending slots.
+template <typename TOut>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= a.T * a.Hq || a.hdr->err) return;
+    const int64_t t = row / a.Hq;
+    const int head = (int)(row % a.Hq), h = head / a.G;
+    const int b = segment_of(a.cu + 1, a.B, t);
+    if (b >= a.B || t < a.cu[b]) return;  // behind the last sequence, or ahead of the first
+    const float *acc[2];
+    const float *ml[2];
+    int cnt[2], rt[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int fi = 1 - k;
+        const PagedFamily &f = a.f[fi];
+        cnt[k] = 0;
+        rt[k] = f.rt;
+        if (f.S == 0) continue;
+        const int s = fi ? segment_of(a.groups + 1, a.n_groups, b) : b;
+        if (s >= f.S || (fi && b < a.groups[s])) continue;  // a sequence outside every group
+        const PagedSeg g = f.seg[s];
+        if (g.w == 0) continue;
+        const int r = (int)(t - g.tok0) * a.G + head % a.G;
+        const int lu = r / f.rt * a.Hkv + h;
+        const long long x = f.cumW[s] + (long long)lu * g.w, per = a.hdr->per[fi];
+        const int c0 = (int)(x / per), c1 = (int)((x + g.w - 1) / per);
+        const int64_t at = ((int64_t)f.cumU[s] + lu + c0) * f.rt + r % f.rt;
+        acc[k] = f.acc + at * a.d;
+        ml[k] = f.ml + at * 2;
+        cnt[k] = c1 - c0 + 1;
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int i = lane; i < cnt[k]; i += 32) M = fmaxf(M, ml[k][(int64_t)i * rt[k] * 2]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float o8[8], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o8[e] = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            for (int i0 = 0; i0 < cnt[k]; i0 += 32) {
+                float w = 0.f;
+                if (i0 + lane < cnt[k]) {
+                    const float2 v = *reinterpret_cast<const float2 *>(ml[k] + (int64_t)(i0 + lane) * rt[k] * 2);
+                    w = exp2f(v.x - M);
+                    L += w * v.y;
+                }
+                const int most = min(32, cnt[k] - i0);
+#pragma unroll 4
+                for (int i = 0; i < most; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, w, i);
+                    const float *p = acc[k] + (int64_t)(i0 + i) * rt[k] * a.d;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (32 * e < a.d) o8[e] = fmaf(wi, p[lane + 32 * e], o8[e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    TOut *out = static_cast<TOut *>(a.out) + row * a.d;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (32 * e < a.d) out[lane + 32 * e] = (TOut)(o8[e] * inv);
+    if (lane == 0) a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st) {
+    paged_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+int paged_sms() {
+    static int sms[128] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
+    if (!sms[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
+        sms[dev] = n;
+    }
+    return sms[dev];
+}
+
+int paged_simt_ctas(int rt, int d) {
+    int n = 0;
+    const cudaError_t e = rt == 16 ? simt_by_d<float, 4, 4>(d, nullptr, 0, &n, nullptr)
+                                   : simt_by_d<float, 8, 8>(d, nullptr, 0, &n, nullptr);
+    if (e != cudaSuccess || n < 1) n = 1;
+    return std::min(kPagedMaxCtas, n * paged_sms());
+}
+
+cudaError_t launch_paged_simt(const PagedArgs &a, int fi, cudaStream_t st) {
+    const bool few = a.f[fi].rt == 16;
+    if (a.dtype == RA_FP32)
+        return few ? simt_by_d<float, 4, 4>(a.d, &a, fi, nullptr, st) : simt_by_d<float, 8, 8>(a.d, &a, fi, nullptr, st);
+    return few ? simt_by_d<__nv_bfloat16, 4, 4>(a.d, &a, fi, nullptr, st)
+               : simt_by_d<__nv_bfloat16, 8, 8>(a.d, &a, fi, nullptr, st);
+}
+
+cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {
+    const int64_t rows = a.T * a.Hq;
+    const unsigned blocks = (unsigned)((rows + 7) / 8);
+    if (a.out_dtype == RA_FP32)
+        paged_combine_kernel<float><<<blocks, 256, 0, st>>>(a);
+    else
+        paged_combine_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

@@ -1,0 +1,304 @@
+// ra_serve.cpp -- the C entries of rotary positions, the paged-cache append
+// and paged attention: argument checks, workspace layout and the choice of
+// kernels.  Host code only.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "ra_internal.h"
+#include "ra_kernels.h"
+
+namespace ra {
+namespace {
+
+ra_status launch_failed(cudaError_t e, const char *what) {
+    return fail(RA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int elem(int dtype) { return dtype == RA_FP32 ? 4 : 2; }
+bool on_elem(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem(dtype) == 0; }
+
+ra_status check_rope(const ra_rope *r, const int32_t *pos, int d) {
+    if (!r->inv_freq || !pos) return fail(RA_ERR_INVALID_ARG, "inv_freq or pos is NULL");
+    if (r->n_axes < 1 || r->n_axes > 8) return fail(RA_ERR_INVALID_ARG, "n_axes must be in [1, 8]");
+    if (r->n_pairs < 1 || 2 * (int64_t)r->n_pairs > d)
+        return fail(RA_ERR_INVALID_ARG, "n_pairs must be at least 1 and 2 * n_pairs at most d");
+    for (int i = 0; i < r->n_pairs; ++i) {
+        if (!std::isfinite(r->inv_freq[i])) return fail(RA_ERR_INVALID_ARG, "inv_freq must be finite");
+        if (r->axes && r->axes[i] >= r->n_axes) return fail(RA_ERR_INVALID_ARG, "an axis lies outside [0, n_axes)");
+    }
+    return RA_OK;
+}
+
+ra_status check_rows(int dtype, int64_t T, int d) {
+    if (dtype != RA_BF16 && dtype != RA_FP32) return fail(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
+    if (T < 0 || T > INT32_MAX) return fail(RA_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+    if (d <= 0) return fail(RA_ERR_INVALID_ARG, "d must be positive");
+    if (d % 4 != 0 || d > 256) return fail(RA_ERR_UNSUPPORTED, "d must be a multiple of 4 and <= 256");
+    return RA_OK;
+}
+
+// Rows of H * d contiguous elements, `stride` apart.
+ra_status check_tensor(const void *x, const void *y, int dtype, int H, int d, int64_t xs, int64_t ys,
+                       const char *name) {
+    if (H <= 0 || H > 4096) return fail(RA_ERR_INVALID_ARG, std::string("bad head count of ") + name);
+    if (!x || !y) return fail(RA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+    if (xs < (int64_t)H * d || ys < (int64_t)H * d)
+        return fail(RA_ERR_INVALID_ARG, std::string("row stride of ") + name + " is smaller than its heads");
+    if (!on_elem(x, dtype) || !on_elem(y, dtype))
+        return fail(RA_ERR_UNSUPPORTED, std::string(name) + " is not aligned to its elements");
+    if (x == y && xs != ys)
+        return fail(RA_ERR_INVALID_ARG, std::string(name) + ": an output on its input needs the input's stride");
+    return RA_OK;
+}
+
+ra_status rope_common(const void *q, const void *k, void *qo, void *ko, int dtype, int64_t T, int Hq, int Hk, int d,
+                      int64_t qs, int64_t ks, int64_t qos, int64_t kos, const int32_t *pos, const ra_rope *rope,
+                      int inverse, void *stream) {
+    ra_status st = check_rows(dtype, T, d);
+    if (st) return st;
+    if (!rope) return fail(RA_ERR_INVALID_ARG, "rope is NULL");
+    if (T == 0) return RA_OK;
+    if ((st = check_rope(rope, pos, d))) return st;
+    if ((st = check_tensor(q, qo, dtype, Hq, d, qs, qos, "q"))) return st;
+    if ((k == nullptr) != (ko == nullptr)) return fail(RA_ERR_INVALID_ARG, "k and k_out go together");
+    if (k && (st = check_tensor(k, ko, dtype, Hk, d, ks, kos, "k"))) return st;
+    RopeParams p{};
+    p.jobs[p.njobs++] = RopeJob{q, qo, qs, qos, Hq, 1, 0};
+    if (k) p.jobs[p.njobs++] = RopeJob{k, ko, ks, kos, Hk, 1, 0};
+    p.d = d;
+    p.T = T;
+    p.pos = pos;
+    rope_table(p, rope->inv_freq, rope->axes, rope->n_pairs, rope->adjacent, inverse);
+    ProfScope ps(inverse ? "ra_rope_bwd" : "ra_rope_fwd", static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RA_OK : launch_failed(e, "rope launch");
+}
+
+ra_status check_cache(const ra_paged_kv *c) {
+    if (!c) return fail(RA_ERR_INVALID_ARG, "cache is NULL");
+    if (c->dtype != RA_BF16 && c->dtype != RA_FP32)
+        return fail(RA_ERR_INVALID_ARG, "the cache's dtype must be RA_BF16 or RA_FP32");
+    if (c->n_pages < 0 || c->n_pages > INT32_MAX || c->page_size < 1 || c->Hkv < 1 || c->Hkv > 4096 || c->d < 1)
+        return fail(RA_ERR_INVALID_ARG, "bad cache shape");
+    if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+        return fail(RA_ERR_INVALID_ARG, "the cache's strides must not be negative");
+    return RA_OK;
+}
+
+// ------------------------------------------------------------ paged attention
+// Rows a unit of each family: 16 where a unit can hold no more, else 64.
+struct PagedLayout {
+    int rt[2];
+    int64_t slots[2];
+    size_t o_hdr, o_seg[2], o_cumW[2], o_cumU[2], o_acc[2], o_ml[2], bytes;
+};
+
+PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, int dtype, int max_q_len) {
+    PagedLayout L{};
+    (void)dtype;
+    const int64_t own = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * G;
+    L.rt[0] = own <= 16 ? 16 : 64;
+    L.rt[1] = T * G <= 16 ? 16 : 64;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at = align_up(at + n, 256);
+        return o;
+    };
+    L.o_hdr = take(sizeof(PagedHdr));
+    for (int f = 0; f < 2; ++f) {
+        const int64_t S = f ? n_groups : B;
+        L.o_seg[f] = take((size_t)S * sizeof(PagedSeg));
+        L.o_cumW[f] = take((size_t)(S + 1) * 8);
+        L.o_cumU[f] = take((size_t)(S + 1) * 4);
+        // every segment ends a row tile of its own at most once
+        L.slots[f] = S ? Hkv * (S + (T * G + L.rt[f] - 1) / L.rt[f]) + kPagedMaxCtas : 0;
+        L.o_acc[f] = take((size_t)L.slots[f] * L.rt[f] * d * 4);
+        L.o_ml[f] = take((size_t)L.slots[f] * L.rt[f] * 8);
+    }
+    L.bytes = at;
+    return L;
+}
+
+ra_status check_paged_shape(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype) {
+    if (dtype != RA_BF16 && dtype != RA_FP32) return fail(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
+    if (T < 0 || B < 1 || n_groups < 0) return fail(RA_ERR_INVALID_ARG, "T and n_groups must be >= 0, B >= 1");
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return fail(RA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hkv");
+    if (d <= 0) return fail(RA_ERR_INVALID_ARG, "d must be positive");
+    if (d % 32 != 0 || d > 256) return fail(RA_ERR_UNSUPPORTED, "d must be a multiple of 32 and <= 256");
+    if (T > INT32_MAX / Hq) return fail(RA_ERR_UNSUPPORTED, "T * Hq must be < 2^31");
+    if (B > (1 << 20) || n_groups > (1 << 20) || (int64_t)Hkv * ((int64_t)B + n_groups) > (1 << 28))
+        return fail(RA_ERR_UNSUPPORTED, "too many sequences");
+    return RA_OK;
+}
+
+}  // namespace
+}  // namespace ra
+
+using namespace ra;
+
+extern "C" {
+
+ra_status ra_rope_fwd(const void *q, const void *k, void *q_out, void *k_out, int dtype, int64_t T, int Hq, int Hk,
+                      int d, int64_t q_stride, int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                      const int32_t *pos, const ra_rope *rope, void *stream) {
+    return rope_common(q, k, q_out, k_out, dtype, T, Hq, Hk, d, q_stride, k_stride, q_out_stride, k_out_stride, pos,
+                       rope, 0, stream);
+}
+
+ra_status ra_rope_bwd(const void *dq, const void *dk, void *dq_out, void *dk_out, int dtype, int64_t T, int Hq,
+                      int Hk, int d, int64_t dq_stride, int64_t dk_stride, int64_t dq_out_stride,
+                      int64_t dk_out_stride, const int32_t *pos, const ra_rope *rope, void *stream) {
+    return rope_common(dq, dk, dq_out, dk_out, dtype, T, Hq, Hk, d, dq_stride, dk_stride, dq_out_stride,
+                       dk_out_stride, pos, rope, 1, stream);
+}
+
+ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t T,
+                             const ra_paged_kv *cache, const int32_t *page_table, int64_t table_width,
+                             const int32_t *cu_seqlens, const int32_t *kv_lens, int B, const void *q, void *q_out,
+                             int Hq, int64_t q_stride, int64_t q_out_stride, const int32_t *pos, const ra_rope *rope,
+                             void *stream) {
+    ra_status st = check_cache(cache);
+    if (st) return st;
+    if ((st = check_rows(cache->dtype, T, cache->d))) return st;
+    if (B < 1 || table_width < 0 || table_width > INT32_MAX)
+        return fail(RA_ERR_INVALID_ARG, "B must be >= 1 and table_width in [0, 2^31)");
+    if ((q == nullptr) != (q_out == nullptr)) return fail(RA_ERR_INVALID_ARG, "q and q_out go together");
+    if (q && !rope) return fail(RA_ERR_INVALID_ARG, "queries are taken along to be rotated: q without rope");
+    if (T == 0) return RA_OK;
+    if (!cu_seqlens || !kv_lens || (table_width > 0 && !page_table))
+        return fail(RA_ERR_INVALID_ARG, "a segment array is NULL");
+    const int d = cache->d, dt = cache->dtype;
+    if (!cache->k || !cache->v) return fail(RA_ERR_INVALID_ARG, "a cache is NULL");
+    if (!on_elem(cache->k, dt) || !on_elem(cache->v, dt))
+        return fail(RA_ERR_UNSUPPORTED, "a cache is not aligned to its elements");
+    if ((st = check_tensor(k, cache->k, dt, cache->Hkv, d, k_stride, (int64_t)cache->Hkv * d, "k"))) return st;
+    if ((st = check_tensor(v, cache->v, dt, cache->Hkv, d, v_stride, (int64_t)cache->Hkv * d, "v"))) return st;
+    if (q && (st = check_tensor(q, q_out, dt, Hq, d, q_stride, q_out_stride, "q"))) return st;
+    if (rope && (st = check_rope(rope, pos, d))) return st;
+    RopeParams p{};
+    if (q) p.jobs[p.njobs++] = RopeJob{q, q_out, q_stride, q_out_stride, Hq, 1, 0};
+    p.jobs[p.njobs++] = RopeJob{k, cache->k, k_stride, 0, cache->Hkv, rope ? 1 : 0, 1};
+    p.jobs[p.njobs++] = RopeJob{v, cache->v, v_stride, 0, cache->Hkv, 0, 1};
+    p.d = d;
+    p.T = T;
+    p.pos = pos;
+    if (rope) rope_table(p, rope->inv_freq, rope->axes, rope->n_pairs, rope->adjacent, 0);
+    p.cu = cu_seqlens;
+    p.kv_lens = kv_lens;
+    p.page_table = page_table;
+    p.table_width = table_width;
+    p.n_pages = cache->n_pages;
+    p.page_stride = cache->page_stride;
+    p.token_stride = cache->token_stride;
+    p.head_stride = cache->head_stride;
+    p.B = B;
+    p.page_size = cache->page_size;
+    p.status = device_status_ptr();
+    ProfScope ps("ra_kv_cache_append", static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_rope(p, dt, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RA_OK : launch_failed(e, "cache append launch");
+}
+
+size_t ra_paged_attn_workspace_bytes(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype,
+                                     int max_q_len) {
+    if (check_paged_shape(T, B, n_groups, Hq, Hkv, d, dtype)) return 0;
+    return paged_layout(T, B, n_groups, Hq / Hkv, Hkv, d, dtype, max_q_len).bytes;
+}
+
+ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, const ra_paged_kv *cache,
+                            const int32_t *page_table, int64_t table_width, const int32_t *cu_seqlens_q,
+                            const int32_t *kv_lens, int B, const int32_t *prefix_table, int64_t prefix_width,
+                            const int32_t *prefix_lens, const int32_t *prefix_groups, int n_groups, int causal,
+                            int max_q_len, float scale, void *out, int out_dtype, float *lse, void *workspace,
+                            size_t ws_bytes, void *stream) {
+    ra_status st = check_cache(cache);
+    if (st) return st;
+    const int Hkv = cache->Hkv, d = cache->d, dtype = cache->dtype;
+    if ((st = check_paged_shape(T, B, n_groups, Hq, Hkv, d, dtype))) return st;
+    if (out_dtype != RA_FP32 && out_dtype != dtype)
+        return fail(RA_ERR_INVALID_ARG, "out_dtype must be RA_FP32 or the cache's dtype");
+    if (!std::isfinite(scale)) return fail(RA_ERR_INVALID_ARG, "scale must be finite");
+    if (table_width < 0 || prefix_width < 0 || table_width > INT32_MAX || prefix_width > INT32_MAX)
+        return fail(RA_ERR_INVALID_ARG, "table widths must be in [0, 2^31)");
+    if (q_stride < (int64_t)Hq * d) return fail(RA_ERR_INVALID_ARG, "q_stride is smaller than the heads");
+    if (T == 0) return RA_OK;
+    if (!q || !out || !lse || !cu_seqlens_q || !kv_lens || (table_width > 0 && !page_table) ||
+        (cache->n_pages > 0 && (!cache->k || !cache->v)))
+        return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+    if (n_groups > 0 && (!prefix_lens || !prefix_groups || (prefix_width > 0 && !prefix_table)))
+        return fail(RA_ERR_INVALID_ARG, "a prefix array is NULL");
+    const int64_t vec = 16 / elem(dtype);
+    if (!on16(q) || !on16(out) || !on16(cache->k) || !on16(cache->v) || q_stride % vec || cache->page_stride % vec ||
+        cache->token_stride % vec || cache->head_stride % vec)
+        return fail(RA_ERR_UNSUPPORTED, "q, out and the cache must be 16-byte aligned, with strides of whole 16 bytes");
+    const PagedLayout L = paged_layout(T, B, n_groups, Hq / Hkv, Hkv, d, dtype, max_q_len);
+    if (!workspace || ws_bytes < L.bytes)
+        return fail(RA_ERR_WORKSPACE, "workspace must be >= " + std::to_string(L.bytes));
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(RA_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    PagedArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.d = d;
+    a.dtype = dtype;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.n_pages = cache->n_pages;
+    a.page_stride = cache->page_stride;
+    a.token_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.page_size = cache->page_size;
+    a.B = B;
+    a.n_groups = n_groups;
+    a.causal = causal != 0;
+    a.cu = cu_seqlens_q;
+    a.kv_lens = kv_lens;
+    a.prefix_lens = prefix_lens;
+    a.groups = prefix_groups;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr);
+    for (int f = 0; f < 2; ++f) {
+        PagedFamily &F = a.f[f];
+        F.S = f ? n_groups : B;
+        F.rt = L.rt[f];
+        F.kt = 64;
+        F.n = paged_simt_ctas(F.rt, d);
+        F.seg = reinterpret_cast<PagedSeg *>(ws + L.o_seg[f]);
+        F.cumW = reinterpret_cast<long long *>(ws + L.o_cumW[f]);
+        F.cumU = reinterpret_cast<int *>(ws + L.o_cumU[f]);
+        F.table = f ? prefix_table : page_table;
+        F.width = f ? prefix_width : table_width;
+        F.acc = reinterpret_cast<float *>(ws + L.o_acc[f]);
+        F.ml = reinterpret_cast<float *>(ws + L.o_ml[f]);
+    }
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.lse = lse;
+    a.status = device_status_ptr();
+    cudaError_t e;
+    {
+        ProfScope ps("ra_paged_plan", s);
+        if ((e = launch_paged_plan(a, s)) != cudaSuccess) return launch_failed(e, "paged plan launch");
+    }
+    for (int f = 1; f >= 0; --f) {
+        if (a.f[f].S == 0) continue;
+        ProfScope ps(f ? "ra_paged_prefix" : "ra_paged_own", s);
+        if ((e = launch_paged_simt(a, f, s)) != cudaSuccess) return launch_failed(e, "paged attention launch");
+    }
+    ProfScope ps("ra_paged_combine", s);
+    if ((e = launch_paged_combine(a, s)) != cudaSuccess) return launch_failed(e, "paged combine launch");
+    return RA_OK;
+}
+
+}  // extern "C"

@@ -349,6 +349,132 @@ ra_status ra_ring_attn_bwd_masked(const void *q, const void *k, const void *v, i
                                   void *workspace, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * ra_rope_fwd / ra_rope_bwd  (DEVICE tensors, HOST frequency table)
+ *
+ * Rotary positions of queries and keys ahead of the attention, and the
+ * gradient behind its backward.  A head has n_pairs rotated pairs: elements
+ * (i, i + n_pairs), or with `adjacent` (2i, 2i + 1); elements from
+ * 2 * n_pairs on pass through.  Pair i turns by the angle
+ *   phi = pos[axes[i]][t] * inv_freq[i]
+ *   forward:  (x, y) -> (x cos phi - y sin phi, x sin phi + y cos phi)
+ *   backward: the same with -phi (the transposed rotation).
+ * Several axes (time, height, width) give each pair the coordinate that
+ * axes[i] names.  The angle is reduced exactly: inv_freq / (2 pi) is kept as
+ * a 64-bit binary fraction of a turn, so positions over the whole int32 range
+ * keep an angle as exact as a 64-bit product.
+ *   q  DEVICE [T, Hq, d], k DEVICE [T, Hk, d] (k and k_out NULL: queries only);
+ *      rows of H*d contiguous elements, q_stride / k_stride elements apart
+ *      (a slice of a packed QKV projection); the same for the outputs.  An
+ *      output may be its own input (same pointer and stride); otherwise they
+ *      must not overlap.
+ *   pos DEVICE int32 [n_axes, T].  1 <= n_axes <= 8.
+ *   rope->inv_freq HOST double [n_pairs], rope->axes HOST uint8 [n_pairs]
+ *      (NULL = axis 0 for every pair).  1 <= n_pairs, 2 * n_pairs <= d.
+ * d a multiple of 4, d <= 256; dtype RA_BF16 or RA_FP32.  Rotation in fp32,
+ * one rounding at the end.  Any alignment of the element type; 16-byte
+ * aligned rows and pair counts of whole 16-byte vectors take the fast path.
+ * Can be captured: the table travels with the launch.
+ * ------------------------------------------------------------------------ */
+typedef struct ra_rope {
+    const double *inv_freq;  /* HOST [n_pairs] */
+    const uint8_t *axes;     /* HOST [n_pairs] or NULL */
+    int32_t n_pairs, n_axes, adjacent;
+} ra_rope;
+ra_status ra_rope_fwd(const void *q, const void *k, void *q_out, void *k_out, int dtype, int64_t T, int Hq, int Hk,
+                      int d, int64_t q_stride, int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                      const int32_t *pos, const ra_rope *rope, void *stream);
+ra_status ra_rope_bwd(const void *dq, const void *dk, void *dq_out, void *dk_out, int dtype, int64_t T, int Hq,
+                      int Hk, int d, int64_t dq_stride, int64_t dk_stride, int64_t dq_out_stride,
+                      int64_t dk_out_stride, const int32_t *pos, const ra_rope *rope, void *stream);
+
+/* A paged cache of keys and values (DEVICE): page p, row r, head h starts at
+ * element p * page_stride + r * token_stride + h * head_stride of k and of v,
+ * with d contiguous elements.  The strides hold [pages, rows, heads, d] as
+ * well as [pages, heads, rows, d] and caches interleaved with each other. */
+typedef struct ra_paged_kv {
+    void *k, *v;
+    int64_t n_pages, page_stride, token_stride, head_stride;
+    int32_t page_size, Hkv, d, dtype;
+} ra_paged_kv;
+
+/* ------------------------------------------------------------------------
+ * ra_kv_cache_append  (DEVICE tensors and DEVICE segment arrays)
+ *
+ * Writes the new tokens of B sequences into their pages, keys rotated on the
+ * way, and rotates the queries beside them, in one launch.  Token j of the
+ * n_b = cu_seqlens[b+1] - cu_seqlens[b] new ones of sequence b gets the row
+ * of logical index i = kv_lens[b] - n_b + j (kv_lens counts the new tokens):
+ * row i % page_size of page page_table[b][i / page_size].
+ *   k, v DEVICE [T, Hkv, d] (rows k_stride / v_stride elements apart)
+ *   page_table DEVICE int32 [B, table_width]; cu_seqlens DEVICE int32 [B+1];
+ *   kv_lens DEVICE int32 [B]
+ *   q, q_out DEVICE [T, Hq, d] or both NULL; q_out may be q
+ *   pos, rope as in ra_rope_fwd (pos DEVICE int32 [n_axes, T]); rope NULL: nothing is rotated
+ *      (q and q_out must then be NULL)
+ * Tokens at or behind cu_seqlens[B] (a padded batch) are left alone: neither
+ * their q_out rows nor any cache row is written for them.  A token whose
+ * logical index or page lies outside the table or the cache is not written
+ * and RA_ERR_DEVICE_BOUNDS is recorded (its q_out row is still written).  Two tokens of
+ * one call must not name the same cache row (distinct sequences' tables must
+ * not share the pages that they append to); which of them a row then holds is
+ * not defined, vector by vector.  Capturable; lengths and tables may change
+ * between replays.  Limits on d, dtype and n_pairs as in ra_rope_fwd.
+ * ------------------------------------------------------------------------ */
+ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t T,
+                             const ra_paged_kv *cache, const int32_t *page_table, int64_t table_width,
+                             const int32_t *cu_seqlens, const int32_t *kv_lens, int B,
+                             const void *q, void *q_out, int Hq, int64_t q_stride, int64_t q_out_stride,
+                             const int32_t *pos, const ra_rope *rope, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ra_paged_attn_fwd  (DEVICE tensors and DEVICE segment arrays)
+ *
+ * Attention of a batch's new tokens over a paged cache, where sequences may
+ * share a prefix whose keys are read once for all of them.  Sequence b has
+ * n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] query tokens, the last n_b of its
+ * kv_lens[b] cached tokens.  Token j sees
+ *   - the whole prefix of its sequence's group, and
+ *   - its own sequence's cached keys with logical index
+ *     < kv_lens[b] - n_b + j + 1 (causal), or < kv_lens[b] (causal == 0).
+ * Groups: sequences prefix_groups[g] .. prefix_groups[g+1] - 1 share the
+ * prefix_lens[g] tokens in the pages prefix_table[g] (a sequence outside
+ * every group has none; n_groups = 0: no prefix at all).  The prefix's pages
+ * are pages of the same cache.
+ *   q DEVICE [T, Hq, d] (rows q_stride elements apart), dtype of the cache
+ *   out DEVICE [T, Hq, d] contiguous, out_dtype RA_FP32 or the cache's dtype;
+ *   lse DEVICE fp32 [Hq, T]: with fp32 the pair is a partial for ra_lse_merge
+ *   page_table [B, table_width], prefix_table [n_groups, prefix_width],
+ *   cu_seqlens_q [B+1], kv_lens [B], prefix_lens [n_groups],
+ *   prefix_groups [n_groups+1]: DEVICE int32
+ *   max_q_len: the most query tokens a sequence is expected to have; it only
+ *      chooses the kernels (<= 0: not known), results hold for any n_b
+ *   workspace DEVICE, 256-byte aligned, >= ra_paged_attn_workspace_bytes(...);
+ *      every byte read from it is written by the same call first.  Calls in
+ *      flight at the same time, and captured graphs that may run so, need
+ *      workspaces of their own.
+ * A row without any visible key has output 0 and lse -inf.  Rows at or behind
+ * cu_seqlens_q[B] (a padded batch) are not written.  Cache rows at or behind
+ * a sequence's length may hold anything (NaN included); a key that some
+ * query tokens of a sequence see and others do not must be finite.
+ * The device arrays are checked on the device: boundaries that decrease or
+ * leave [0, T], groups that decrease or leave [0, B], and lengths outside
+ * [0, width * page_size] are recorded as RA_ERR_DEVICE_BOUNDS and leave out
+ * and lse unwritten; a page index outside [0, n_pages) is recorded too, reads
+ * nothing, and leaves the rows that meet it unspecified.  Capturable; the
+ * arrays' contents may change between replays.  Deterministic: the order of
+ * all sums is fixed by the lengths.  d a multiple of 32, d <= 256; q and the cache 16-byte aligned
+ * with strides of whole 16 bytes; T * Hq < 2^31.
+ * ------------------------------------------------------------------------ */
+size_t ra_paged_attn_workspace_bytes(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype,
+                                     int max_q_len);
+ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, const ra_paged_kv *cache,
+                            const int32_t *page_table, int64_t table_width, const int32_t *cu_seqlens_q,
+                            const int32_t *kv_lens, int B, const int32_t *prefix_table, int64_t prefix_width,
+                            const int32_t *prefix_lens, const int32_t *prefix_groups, int n_groups, int causal,
+                            int max_q_len, float scale, void *out, int out_dtype, float *lse,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * ra_ring_rank_pairs  (HOST, synchronous)
  *
  * Allowed (query, key) pairs each simulated rank computes over the whole
