@@ -1,0 +1,340 @@
+// ra_paged_mma.cu -- paged attention for a few query rows per KV head (bf16,
+// d = 64 or 128): warp-level matrix instructions fed by cp.async.
+//
+// Bound: memory.  A decoding step has G rows (query tokens x the query heads
+// of one KV head) against every cached key, 4 d bytes a key and head, each
+// used once; tensor work is 2 x 2 d flops per row and key, far below the
+// tensor rate even with the rows padded to the 16 of m16n8k16.  So the design
+// is about bytes in flight: every warp streams its own 16-key blocks through
+// a private two-stage ring (8 KB a stage at d = 128), no warp waits for
+// another inside a unit, and rows of any page size are gathered 16 bytes at a
+// time.  Scores, maximum, sum and products stay in registers; the warps'
+// partials are joined in shared memory when the CTA's run of the unit ends.
+//
+// With more rows than 16 the same block step runs with the warps over the
+// rows and the key tile shared (64 rows a CTA).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ra_dev.cuh"
+#include "ra_kernels.h"
+#include "ra_paged.cuh"
+
+namespace ra {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 4;
+constexpr int kKT = 64;      // keys a tile: 16 for each warp
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Shared address of 16-byte chunk c of row r: chunks are exchanged by the
+// row's low bits, so that eight rows of one chunk fall into eight bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int r, int c) {
+    return base + (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+// Starts the copies of 16 key rows (K and V) from logical index kb on; rows
+// that are not there are filled with zeros, so whatever the cache holds
+// behind a sequence's end never meets the products.
+template <int D>
+__device__ __forceinline__ void issue16(const PagedArgs &a, const PagedFamily &f, int s, int len, int h, int kb,
+                                        uint32_t ks, uint32_t vs) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows a warp instruction
+    const int lane = threadIdx.x & 31;
+    long long off = -1;
+    if (lane < 16) off = paged_row(a, f, s, len, kb + lane);
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + h * a.head_stride;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + h * a.head_stride;
+    const int c = lane % CPR;
+#pragma unroll
+    for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + lane / CPR;
+        const long long o = __shfl_sync(0xffffffffu, off, r);
+        const long long at = (o < 0 ? 0 : o) + c * 8;
+        cp16(chunk_at<D>(ks, r, c), k + at, o >= 0);
+        cp16(chunk_at<D>(vs, r, c), v + at, o >= 0);
+    }
+}
+
+template <int D>
+struct Rows {
+    uint32_t q[D / 16][4];  // A fragments of the 16 query rows
+    float o[D / 8][4];      // sum p v of rows lane / 4 and lane / 4 + 8
+    float m[2], l[2];       // running maximum (log2), sum p of the lane's own keys
+    int lim[2];             // keys the rows see
+};
+
+// One block of 16 keys for 16 rows: S = Q K^T, the running maximum, P in
+// bf16 (rounded once: the products' inputs; the sums use the unrounded
+// values), O += P V.
+template <int D>
+__device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, int kb, bool masked, float scale_log2) {
+    const int lane = threadIdx.x & 31, id = lane >> 3, l8 = lane & 7;
+    float s[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4(chunk_at<D>(ks, (id >> 1) * 8 + l8, 2 * k + (id & 1)), b);
+        mma16816(s[0], w.q[k], b[0], b[1]);
+        mma16816(s[1], w.q[k], b[2], b[3]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[n][e] *= scale_log2;
+            if (masked && kb + n * 8 + (lane & 3) * 2 + (e & 1) >= w.lim[e >> 1]) s[n][e] = -INFINITY;
+        }
+    }
+    float mn[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        mn[r] = fmaxf(w.m[r], x);
+    }
+    if (__any_sync(0xffffffffu, mn[0] > w.m[0] || mn[1] > w.m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float alpha = mn[r] == -INFINITY ? 1.f : ex2_approx(w.m[r] - mn[r]);
+            w.m[r] = mn[r];
+            w.l[r] *= alpha;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                w.o[n][2 * r] *= alpha;
+                w.o[n][2 * r + 1] *= alpha;
+            }
+        }
+    }
+    uint32_t p[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const float use = w.m[r] == -INFINITY ? 0.f : w.m[r];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float p0 = ex2_approx(s[n][2 * r] - use), p1 = ex2_approx(s[n][2 * r + 1] - use);
+            w.l[r] += p0 + p1;
+            p[2 * n + r] = pack_bf16x2(p0, p1);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        ldsm4t(chunk_at<D>(vs, (id & 1) * 8 + l8, 2 * n + (id >> 1)), b);
+        mma16816(w.o[2 * n], p, b[0], b[1]);
+        mma16816(w.o[2 * n + 1], p, b[2], b[3]);
+    }
+}
+
+template <int D, bool WIDE>
+constexpr size_t mma_smem() {
+    return (size_t)kWarps * kStages * 2 * 16 * D * 2 + (WIDE ? 0 : kWarps * 16 * 2 * sizeof(float));
+}
+
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_constant__ PagedArgs a, int fi) {
+    constexpr int RT = WIDE ? 16 * kWarps : 16;
+    constexpr uint32_t kBlk = 16 * D * 2;          // bytes of 16 rows
+    constexpr uint32_t kStage = kWarps * 2 * kBlk;  // K blocks of the warps, then V blocks
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const PagedFamily &f = a.f[fi];
+    const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
+    long long x = blockIdx.x * per;
+    const long long x1 = min(W, x + per);
+    if (x >= x1) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = paged_find(f, x);
+    while (x < x1) {
+        while (f.cumW[s + 1] <= x) ++s;
+        const PagedSeg g = f.seg[s];
+        const PagedUnit u = paged_unit(a, f, g, s, x, x1);
+        const int R = g.n * a.G, r0 = u.rtile * RT + (WIDE ? warp * 16 : 0);
+        auto issue = [&](int t) {  // this warp's 16 keys of tile t
+            const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage + warp * kBlk;
+            if (t < u.t1) issue16<D>(a, f, s, g.len, u.h, t * kKT + warp * 16, st, st + kWarps * kBlk);
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue(u.t0 + i);
+        Rows<D> w;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = r0 + (lane >> 2) + 8 * r;
+            // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
+            w.lim[r] = row < R ? paged_limit(a, g, fi, row) : g.len;
+            w.m[r] = -INFINITY;
+            w.l[r] = 0.f;
+            const bool ok = row < R;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                     (ok ? (int64_t)(g.tok0 + row / a.G) * a.q_stride +
+                                               (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                w.q[k][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;
+                w.q[k][2 + r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16 + 8) : 0u;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[n][e] = 0.f;
+        // the warp's rows: the fewest and the most keys any of them sees
+        int lo = min(w.lim[0], w.lim[1]), hi = max(w.lim[0], w.lim[1]);
+#pragma unroll
+        for (int o = 16; o >= 4; o >>= 1) {
+            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        for (int t = u.t0; t < u.t1; ++t) {
+            issue(t + kStages - 1);
+            cp_wait<kStages - 1>();
+            if (WIDE)
+                __syncthreads();
+            else
+                __syncwarp();
+            const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage;
+#pragma unroll 1
+            for (int b = WIDE ? 0 : warp; b < (WIDE ? kWarps : warp + 1); ++b) {
+                const int kb = t * kKT + b * 16;
+                if (kb < hi)
+                    block16<D>(w, st + b * kBlk, st + (kWarps + b) * kBlk, kb, kb + 16 > lo, a.scale_log2);
+            }
+            // the stage may be filled again
+            if (WIDE)
+                __syncthreads();
+            else
+                __syncwarp();
+        }
+        cp_wait<0>();
+        const int64_t slot = ((int64_t)u.unit + blockIdx.x) * RT;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // the four lanes of a row hold different keys
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 2);
+        }
+        if (WIDE) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = (lane >> 2) + 8 * r;
+                if (r0 + row >= R) continue;
+                const int64_t at = slot + warp * 16 + row;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(f.acc + at * D + n * 8 + (lane & 3) * 2) =
+                        make_float2(w.o[n][2 * r], w.o[n][2 * r + 1]);
+                if ((lane & 3) == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(w.m[r], w.l[r]);
+            }
+        } else {
+            // the warps' partials of the 16 rows, joined through shared memory
+            constexpr int OS = D + 8;  // floats a row; a warp's rows fit its two stages
+            float *wo = reinterpret_cast<float *>(smem) + (size_t)warp * 16 * OS;
+            float2 *ml = reinterpret_cast<float2 *>(smem + kStages * kStage);  // [kWarps][16]
+            __syncthreads();  // every warp is done with its stages
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = (lane >> 2) + 8 * r;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(wo + row * OS + n * 8 + (lane & 3) * 2) =
+                        make_float2(w.o[n][2 * r], w.o[n][2 * r + 1]);
+                if ((lane & 3) == 0) ml[warp * 16 + row] = make_float2(w.m[r], w.l[r]);
+            }
+            __syncthreads();
+            const float *all = reinterpret_cast<const float *>(smem);
+            for (int row = warp; row < 16 && r0 + row < R; row += kWarps) {
+                float M = -INFINITY, L = 0.f, acc[D / 32];
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + row].x);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    const float2 v = ml[i * 16 + row];
+                    const float wt = M == -INFINITY ? 0.f : ex2_approx(v.x - M);
+                    L += wt * v.y;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e)
+                        acc[e] = fmaf(wt, all[(i * 16 + row) * OS + lane + 32 * e], acc[e]);
+                }
+                const int64_t at = slot + row;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) f.acc[at * D + lane + 32 * e] = acc[e];
+                if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(M, L);
+            }
+            __syncthreads();  // the stages belong to the next unit
+        }
+        x += u.t1 - u.t0;
+    }
+}
+
+template <int D, bool WIDE>
+cudaError_t mma_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    static_assert(WIDE || (size_t)kWarps * 16 * (D + 8) * 4 <= (size_t)kStages * kWarps * 2 * 16 * D * 2,
+                  "the joined rows lie over the stages");
+    auto kernel = paged_mma_kernel<D, WIDE>;
+    constexpr size_t smem = mma_smem<D, WIDE>();
+    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, kWarps * 32, smem);
+    kernel<<<a->f[fi].n, kWarps * 32, smem, st>>>(*a, fi);
+    return cudaGetLastError();
+}
+
+cudaError_t mma_by_shape(int rt, int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    if (d == 128)
+        return rt == 16 ? mma_launch<128, false>(a, fi, ctas, st) : mma_launch<128, true>(a, fi, ctas, st);
+    if (d == 64) return rt == 16 ? mma_launch<64, false>(a, fi, ctas, st) : mma_launch<64, true>(a, fi, ctas, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+bool paged_mma_supported(int dtype, int d) { return dtype == RA_BF16 && (d == 64 || d == 128); }
+
+int paged_mma_ctas(int rt, int d) {
+    int n = 0;
+    if (mma_by_shape(rt, d, nullptr, 0, &n, nullptr) != cudaSuccess || n < 1) n = 1;
+    return std::min(kPagedMaxCtas, n * paged_sms());
+}
+
+cudaError_t launch_paged_mma(const PagedArgs &a, int fi, cudaStream_t st) {
+    return mma_by_shape(a.f[fi].rt, a.d, &a, fi, nullptr, st);
+}
+
+}  // namespace ra

@@ -268,12 +268,13 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.groups = prefix_groups;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr);
+    const bool mma = paged_mma_supported(dtype, d);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
         F.S = f ? n_groups : B;
         F.rt = L.rt[f];
         F.kt = 64;
-        F.n = paged_simt_ctas(F.rt, d);
+        F.n = mma ? paged_mma_ctas(F.rt, d) : paged_simt_ctas(F.rt, d);
         F.seg = reinterpret_cast<PagedSeg *>(ws + L.o_seg[f]);
         F.cumW = reinterpret_cast<long long *>(ws + L.o_cumW[f]);
         F.cumU = reinterpret_cast<int *>(ws + L.o_cumU[f]);
@@ -294,7 +295,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     for (int f = 1; f >= 0; --f) {
         if (a.f[f].S == 0) continue;
         ProfScope ps(f ? "ra_paged_prefix" : "ra_paged_own", s);
-        if ((e = launch_paged_simt(a, f, s)) != cudaSuccess) return launch_failed(e, "paged attention launch");
+        e = mma ? launch_paged_mma(a, f, s) : launch_paged_simt(a, f, s);
+        if (e != cudaSuccess) return launch_failed(e, "paged attention launch");
     }
     ProfScope ps("ra_paged_combine", s);
     if ((e = launch_paged_combine(a, s)) != cudaSuccess) return launch_failed(e, "paged combine launch");
