@@ -246,7 +246,9 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st);
 // Families of segments: 0 the sequences' own keys, 1 the groups' prefixes.
 // Each (segment, tile of `rt` query rows, KV head) is a unit of ceil(keys / kt)
 // key tiles; the units' tiles form one line that the family's `n` CTAs split
-// evenly.  What a CTA computes of a unit goes to partial slot unit + CTA.
+// evenly.  What CTA c computes of a unit whose rows start at partial row
+// `base` goes to partial rows base + rt * c on: along the line units and CTAs
+// only grow, and no unit has more than rt partial rows, so these never meet.
 struct PagedSeg {
     int tok0, n, len, w;               // first query token, query tokens, keys, key tiles
 };
@@ -256,12 +258,12 @@ struct PagedHdr {
 };
 struct PagedFamily {
     int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
+    int halves;                        // units of at most rt / 2 rows: two partials a row, of alternate key tiles
     PagedSeg *seg;                     // [S]
-    long long *cumW;                   // [S + 1]
-    int *cumU;                         // [S + 1]
+    long long *cumW, *cumR;            // [S + 1] tiles, [S] partial rows ahead of each segment
     const int32_t *table;
     int64_t width;
-    float *acc, *ml;                   // [slots][rt][d], [slots][rt][2]: sum p v; running maximum (log2), sum p
+    float *acc, *ml;                   // [partial rows][d], [partial rows][2]: sum p v; running maximum (log2), sum p
 };
 struct PagedArgs {
     const void *q;
@@ -279,7 +281,9 @@ struct PagedArgs {
     float *lse;
     int *status;
 };
-constexpr int kPagedMaxCtas = 1024;
+constexpr int kPagedMaxCtas = 1024;     // of the warp-level and SIMT kernels
+constexpr int kPagedMaxWide = 256;      // of the tcgen05 kernel (one an SM)
+constexpr int kPagedWideRows = 256;     // its rows a unit
 cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st);
 cudaError_t launch_paged_simt(const PagedArgs &a, int family, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st);
@@ -288,6 +292,12 @@ bool paged_mma_supported(int dtype, int d);
 int paged_mma_ctas(int rt, int d);
 cudaError_t launch_paged_mma(const PagedArgs &a, int family, cudaStream_t st);
 int paged_sms();                       // SMs of the current device
+struct PagedMaps {
+    CUtensorMap q, k, v;
+    int rows_inner;                    // the cache's rows in a page lie closer than its heads
+};
+bool paged_tc_maps(const PagedArgs &a, PagedMaps &m);  // false: not a shape of the tcgen05 kernel
+cudaError_t launch_paged_tc(const PagedArgs &a, int family, const PagedMaps &m, cudaStream_t st);
 
 // Device-wait self-test (see ra_selftest_wait_timeout).
 cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t st);

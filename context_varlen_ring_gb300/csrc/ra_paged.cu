@@ -11,8 +11,7 @@
 // Split: every (segment, tile of query rows, KV head) is a unit of key tiles.
 // All units' tiles form one line, cut into equal runs of tiles, one a CTA, so
 // the work is even whatever the lengths, and one long sequence fills the GPU
-// as a full batch does.  Unit u and CTA c meet at most once and both only
-// grow along the line, so u + c numbers the partials without a table.
+// as a full batch does.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,8 +32,7 @@ using namespace dev;
 constexpr int kPlanThreads = 512;
 
 struct UW {
-    int u;
-    long long w;
+    long long u, w;  // partial rows, key tiles
 };
 
 // Exclusive scan over the block; `total` is the block's sum.
@@ -43,7 +41,7 @@ __device__ __forceinline__ UW block_scan(UW v, UW *warp_sum, UW &total) {
     UW x = v;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, x.u, s);
+        const long long u = __shfl_up_sync(0xffffffffu, x.u, s);
         const long long w = __shfl_up_sync(0xffffffffu, x.w, s);
         if (lane >= s) {
             x.u += u;
@@ -67,9 +65,10 @@ __device__ __forceinline__ UW block_scan(UW v, UW *warp_sum, UW &total) {
 }
 
 // One block: checks the segment arrays, and writes each family's segments,
-// the running counts of units and tiles, and the tiles a CTA.
+// the running counts of partial rows and tiles, and the tiles a CTA.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedArgs a) {
     __shared__ UW warp_sum[kPlanThreads / 32];
+    pdl_launch();
     int bad = 0;
     for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
         const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.kv_lens[b];
@@ -103,20 +102,20 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
                 g.len = fi ? a.prefix_lens[s] : a.kv_lens[s];
                 g.w = g.n > 0 ? (g.len + f.kt - 1) / f.kt : 0;
                 f.seg[s] = g;
-                v.u = (int)(((long long)g.n * a.G + f.rt - 1) / f.rt) * a.Hkv;
-                v.w = (long long)v.u * g.w;
+                const long long R = (long long)g.n * a.G, full = R / f.rt;
+                v.u = a.Hkv * (full * f.rt + paged_alloc(f, (int)(R - full * f.rt)));
+                v.w = (R + f.rt - 1) / f.rt * a.Hkv * g.w;
             }
             UW total;
             const UW at = block_scan(v, warp_sum, total);
             if (s < f.S) {
-                f.cumU[s] = base.u + at.u;
+                f.cumR[s] = base.u + at.u;
                 f.cumW[s] = base.w + at.w;
             }
             base.u += total.u;
             base.w += total.w;
         }
         if (threadIdx.x == 0) {
-            f.cumU[f.S] = base.u;
             f.cumW[f.S] = base.w;
             a.hdr->W[fi] = base.w;
             a.hdr->per[fi] = max(1ll, (base.w + f.n - 1) / f.n);
@@ -158,18 +157,19 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
     extern __shared__ float4 smem4[];
     float *Ks = reinterpret_cast<float *>(smem4), *Vs = Ks + kKT * KS, *Qs = Vs + kKT * D, *Ps = Qs + RT * D;
     const PagedFamily &f = a.f[fi];
+    pdl_wait();
+    pdl_launch();
     const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
     const int cta = blockIdx.x;
     long long x = cta * per;
     const long long x1 = min(W, x + per);
-    if (x >= x1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = paged_find(f, x);
+    int s = x < x1 ? paged_find(f, x) : 0;
     while (x < x1) {
         while (f.cumW[s + 1] <= x) ++s;
         const PagedSeg g = f.seg[s];
         const PagedUnit u = paged_unit(a, f, g, s, x, x1);
-        const int R = g.n * a.G, r0 = u.rtile * RT;
+        const int R = g.n * a.G, r0 = u.r0;
         __syncthreads();  // the last unit's readers are done with Q
         for (int i = threadIdx.x; i < RT * (D / 4); i += WARPS * 32) {
             const int r = i / (D / 4), c = i % (D / 4) * 4, row = r0 + r;
@@ -262,10 +262,9 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
             }
             __syncwarp();
         }
-        const int64_t slot = (int64_t)u.unit + cta;
 #pragma unroll
         for (int r = 0; r < RPW; ++r) {
-            const int64_t at = slot * RT + warp * RPW + r;
+            const int64_t at = u.base + (int64_t)cta * RT + warp * RPW + r;
             float sum = l[r];
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -286,8 +285,7 @@ cudaError_t simt_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) 
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, WARPS * 32, smem);
-    kernel<<<a->f[fi].n, WARPS * 32, smem, st>>>(*a, fi);
-    return cudaGetLastError();
+    return launch_pdl(kernel, a->f[fi].n, WARPS * 32, smem, st, *a, fi);
 }
 
 template <typename T, int RPW, int WARPS>
@@ -306,80 +304,131 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t
 }
 
 // ------------------------------------------------------------------ join
-// One warp per (token, head) row: the largest maximum of its partials, their
-// weights 2^(m - M), and the weighted sums in the order prefix, own keys,
-// ascending slots.
-template <typename TOut>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= a.T * a.Hq || a.hdr->err) return;
-    const int64_t t = row / a.Hq;
-    const int head = (int)(row % a.Hq), h = head / a.G;
-    const int b = segment_of(a.cu + 1, a.B, t);
-    if (b >= a.B || t < a.cu[b]) return;  // behind the last sequence, or ahead of the first
-    const float *acc[2];
-    const float *ml[2];
-    int cnt[2], rt[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int fi = 1 - k;
-        const PagedFamily &f = a.f[fi];
-        cnt[k] = 0;
-        rt[k] = f.rt;
-        if (f.S == 0) continue;
-        const int s = fi ? segment_of(a.groups + 1, a.n_groups, b) : b;
-        if (s >= f.S || (fi && b < a.groups[s])) continue;  // a sequence outside every group
-        const PagedSeg g = f.seg[s];
-        if (g.w == 0) continue;
-        const int r = (int)(t - g.tok0) * a.G + head % a.G;
-        const int lu = r / f.rt * a.Hkv + h;
-        const long long x = f.cumW[s] + (long long)lu * g.w, per = a.hdr->per[fi];
-        const int c0 = (int)(x / per), c1 = (int)((x + g.w - 1) / per);
-        const int64_t at = ((int64_t)f.cumU[s] + lu + c0) * f.rt + r % f.rt;
-        acc[k] = f.acc + at * a.d;
-        ml[k] = f.ml + at * 2;
-        cnt[k] = c1 - c0 + 1;
+// The partials of one (token, head) row in a family: cnt of them, the i-th at
+// partial row `at + i / parts * rt + i % parts * second`.
+struct Parts {
+    const float *acc, *ml;
+    int64_t at;
+    int cnt, rt, parts, second;
+    __device__ __forceinline__ int64_t row(int i) const {
+        return at + (int64_t)(i / parts) * rt + (i % parts) * second;
     }
-    float M = -INFINITY;
+};
+
+__device__ __forceinline__ Parts find_parts(const PagedArgs &a, int fi, int64_t t, int head, int b) {
+    const PagedFamily &f = a.f[fi];
+    Parts p{f.acc, f.ml, 0, 0, f.rt, 1, 0};
+    if (f.S == 0) return p;
+    const int s = fi ? segment_of(a.groups + 1, a.n_groups, b) : b;
+    if (s >= f.S || (fi && b < a.groups[s])) return p;  // a sequence outside every group
+    const PagedSeg g = f.seg[s];
+    if (g.w == 0) return p;
+    const int r = (int)(t - g.tok0) * a.G + head % a.G, rtile = r / f.rt, h = head / a.G;
+    const int rows = min(f.rt, g.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
+    const long long x = f.cumW[s] + (long long)(rtile * a.Hkv + h) * g.w, per = a.hdr->per[fi];
+    const int c0 = (int)(x / per), c1 = (int)((x + g.w - 1) / per);
+    p.at = f.cumR[s] + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
+    p.parts = alloc > rows ? 2 : 1;
+    p.second = rows;
+    p.cnt = (c1 - c0 + 1) * p.parts;
+    return p;
+}
+
+// WPR warps per (token, head) row: the largest maximum M of its partials,
+// their weights 2^(m - M), and the weighted sums.  Warp w adds partials w,
+// w + WPR, ... (own keys first, then the prefix) and the warps' sums are
+// added in order, so the result does not depend on timing.  Latency bound:
+// few rows come with many partials each (a long sequence over all SMs), so
+// the partials of a row are read by several warps at once.
+template <typename TOut, int WPR>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+    __shared__ float sum[8][256];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+    const int64_t row = (int64_t)blockIdx.x * (8 / WPR) + warp / WPR;
+    bool live = row < a.T * a.Hq && !a.hdr->err;
+    const int64_t t = live ? row / a.Hq : 0;
+    const int head = (int)(row % a.Hq);
+    const int b = live ? segment_of(a.cu + 1, a.B, t) : a.B;
+    live = b < a.B && t >= a.cu[b];  // not behind the last sequence, nor ahead of the first
+    float M = -INFINITY, L = 0.f;
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (live) {
+        const Parts p0 = find_parts(a, 0, t, head, b), p1 = find_parts(a, 1, t, head, b);
+        const int cnt = p0.cnt + p1.cnt;
+        auto ml = [&](int i) {
+            return *reinterpret_cast<const float2 *>(i < p0.cnt ? p0.ml + p0.row(i) * 2 : p1.ml + p1.row(i - p0.cnt) * 2);
+        };
+        for (int i = lane; i < cnt; i += 32) M = fmaxf(M, ml(i).x);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (int i = lane; i < cnt[k]; i += 32) M = fmaxf(M, ml[k][(int64_t)i * rt[k] * 2]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float o8[8], L = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o8[e] = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            for (int i0 = 0; i0 < cnt[k]; i0 += 32) {
+        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        if (M != -INFINITY) {
+            const int d4 = a.d / 4;
+            for (int i0 = 0; i0 < cnt; i0 += 32) {
                 float w = 0.f;
-                if (i0 + lane < cnt[k]) {
-                    const float2 v = *reinterpret_cast<const float2 *>(ml[k] + (int64_t)(i0 + lane) * rt[k] * 2);
+                if (i0 + lane < cnt) {
+                    const float2 v = ml(i0 + lane);
                     w = exp2f(v.x - M);
                     L += w * v.y;
                 }
-                const int most = min(32, cnt[k] - i0);
+                const int most = min(32, cnt - i0);
 #pragma unroll 4
-                for (int i = 0; i < most; ++i) {
+                for (int i = sub; i < most; i += WPR) {
                     const float wi = __shfl_sync(0xffffffffu, w, i);
-                    const float *p = acc[k] + (int64_t)(i0 + i) * rt[k] * a.d;
+                    const int k = i0 + i;
+                    const float4 *p = reinterpret_cast<const float4 *>(
+                        k < p0.cnt ? p0.acc + p0.row(k) * a.d : p1.acc + p1.row(k - p0.cnt) * a.d);
+                    // (a partial without weight may never have been written)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (32 * e < a.d) o8[e] = fmaf(wi, p[lane + 32 * e], o8[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        if (wi != 0.f && lane + 32 * e < d4) {
+                            const float4 v = p[lane + 32 * e];
+                            o[e].x = fmaf(wi, v.x, o[e].x);
+                            o[e].y = fmaf(wi, v.y, o[e].y);
+                            o[e].z = fmaf(wi, v.z, o[e].z);
+                            o[e].w = fmaf(wi, v.w, o[e].w);
+                        }
+                    }
                 }
             }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
         }
     }
+    if (WPR > 1) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int e = 0; e < 2; ++e) *reinterpret_cast<float4 *>(&sum[warp][(lane + 32 * e) * 4]) = o[e];
+        __syncthreads();
+    }
+    if (!live) return;
     const float inv = L > 0.f ? 1.f / L : 0.f;
     TOut *out = static_cast<TOut *>(a.out) + row * a.d;
+    for (int c = (WPR > 1 ? sub * 32 + lane : lane) * 4; c < a.d; c += WPR * 128) {
+        float4 v;
+        if (WPR > 1) {
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (32 * e < a.d) out[lane + 32 * e] = (TOut)(o8[e] * inv);
-    if (lane == 0) a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+            for (int i = 0; i < WPR; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sum[warp - sub + i][c]);
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+        } else {
+            v = c < 128 ? o[0] : o[1];
+        }
+        if constexpr (sizeof(TOut) == 4) {
+            *reinterpret_cast<float4 *>(out + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        } else {
+            uint2 pk;
+            pk.x = pack_bf16x2(v.x * inv, v.y * inv);
+            pk.y = pack_bf16x2(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2 *>(out + c) = pk;
+        }
+    }
+    if (sub == 0 && lane == 0)
+        a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
@@ -419,12 +468,16 @@ cudaError_t launch_paged_simt(const PagedArgs &a, int fi, cudaStream_t st) {
 
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {
     const int64_t rows = a.T * a.Hq;
-    const unsigned blocks = (unsigned)((rows + 7) / 8);
-    if (a.out_dtype == RA_FP32)
-        paged_combine_kernel<float><<<blocks, 256, 0, st>>>(a);
-    else
-        paged_combine_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    auto go = [&](auto kernel, int wpr) {
+        return launch_pdl(kernel, (unsigned)((rows * wpr + 7) / 8), 256, 0, st, a);
+    };
+    // few rows: many partials each, and warps to spare
+    if (a.out_dtype == RA_FP32) {
+        if (rows <= 2048) return go(paged_combine_kernel<float, 8>, 8);
+        return rows <= 16384 ? go(paged_combine_kernel<float, 4>, 4) : go(paged_combine_kernel<float, 1>, 1);
+    }
+    if (rows <= 2048) return go(paged_combine_kernel<__nv_bfloat16, 8>, 8);
+    return rows <= 16384 ? go(paged_combine_kernel<__nv_bfloat16, 4>, 4) : go(paged_combine_kernel<__nv_bfloat16, 1>, 1);
 }
 
 }  // namespace ra

@@ -174,17 +174,18 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const PagedFamily &f = a.f[fi];
+    pdl_wait();
+    pdl_launch();
     const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
     long long x = blockIdx.x * per;
     const long long x1 = min(W, x + per);
-    if (x >= x1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = paged_find(f, x);
+    int s = x < x1 ? paged_find(f, x) : 0;
     while (x < x1) {
         while (f.cumW[s + 1] <= x) ++s;
         const PagedSeg g = f.seg[s];
         const PagedUnit u = paged_unit(a, f, g, s, x, x1);
-        const int R = g.n * a.G, r0 = u.rtile * RT + (WIDE ? warp * 16 : 0);
+        const int R = g.n * a.G, r0 = u.r0 + (WIDE ? warp * 16 : 0);
         auto issue = [&](int t) {  // this warp's 16 keys of tile t
             const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage + warp * kBlk;
             if (t < u.t1) issue16<D>(a, f, s, g.len, u.h, t * kKT + warp * 16, st, st + kWarps * kBlk);
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
                 __syncwarp();
         }
         cp_wait<0>();
-        const int64_t slot = ((int64_t)u.unit + blockIdx.x) * RT;
+        const int64_t slot = u.base + (int64_t)blockIdx.x * RT;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // the four lanes of a row hold different keys
             w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
@@ -312,8 +313,7 @@ cudaError_t mma_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, kWarps * 32, smem);
-    kernel<<<a->f[fi].n, kWarps * 32, smem, st>>>(*a, fi);
-    return cudaGetLastError();
+    return launch_pdl(kernel, a->f[fi].n, kWarps * 32, smem, st, *a, fi);
 }
 
 cudaError_t mma_by_shape(int rt, int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {

@@ -1,0 +1,569 @@
+// ra_paged_tc.cu -- paged attention for many query rows per KV head (bf16,
+// d = 128) on the 5th-generation tensor cores: a prefix that a batch shares,
+// and sequences with several query tokens.
+//
+// Mathematics and bound: R rows (query tokens x the G query heads of one KV
+// head) against n keys take 4 d R n flops and read 4 d n bytes of keys, so
+// above about 280 rows the tensor rate bounds it, below that memory.
+//
+// Design, next to tc_fwd_kernel of the packed ring (same products, same
+// softmax): persistent CTAs of 12 warps, one a SM, each with an equal run of
+// the line of key tiles (so no claims and no descriptor ring: every role
+// walks the same run by itself).  A unit has up to 256 rows.
+//  * 129 to 256 rows: two tiles of 128 rows share each K and V tile; softmax
+//    group k (4 warps, a thread a row) owns row tile k.
+//  * up to 128 rows: both softmax groups own the same rows and take alternate
+//    key tiles, with a partial each, so one group's softmax hides behind the
+//    other's products although there is only one tile of rows.
+// Pages: a 4-D tensor map (d, head, row in page, page; head and row in the
+// order of their strides) with a box of min(page, 128) rows; the lanes of the producer warp look up a page each and
+// issue the boxes of a tile side by side.  Keys behind the length come from a
+// page outside the cache, which TMA fills with zeros; what a last page holds
+// behind the length is masked in S, and its V rows are zeroed in shared
+// memory before the product, so it may be anything.
+// Every wait is bounded as in the rest of the library.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "ra_dev.cuh"
+#include "ra_internal.h"
+#include "ra_kernels.h"
+#include "ra_paged.cuh"
+
+namespace ra {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 384;
+constexpr int kSlots = 5;
+constexpr uint32_t kHalf = 16384;      // 128 rows x 128 B (64 bf16), 128-byte swizzle
+constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
+constexpr uint32_t kOffKV = 2 * kTile;
+constexpr uint32_t kOffBar = kOffKV + kSlots * kTile;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;  // + barriers + alignment slack
+
+struct TcParams {
+    CUtensorMap tmQ, tmK, tmV;
+    PagedArgs a;
+    int fi, box, log2G;  // family, rows a box
+    int rows_inner;      // the maps' dimensions: (d, row in page, head, page) instead of (d, head, row in page, page)
+    unsigned long long budget_ns;
+};
+
+// What one CTA does of one unit: steps of one key tile (two row tiles) or of
+// two key tiles (one row tile).
+struct Walk {
+    PagedSeg g;
+    PagedUnit u;
+    int s;
+    bool pair;  // two row tiles
+    int tend;   // key tiles [u.t0, tend): those that any row sees
+};
+
+// Bits [0, n) of the 32 columns starting at `base`.
+__device__ __forceinline__ uint32_t low_bits(int n, int base) {
+    const int k = min(max(n - base, 0), 32);
+    return k == 32 ? 0xffffffffu : (1u << k) - 1u;
+}
+
+__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint32_t q_s, uint32_t k_s, uint32_t idesc) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u;
+        tc_mma_ss_w(d_tmem, sdesc_sw128(q_s + off, 16, 1024), sdesc_sw128(k_s + off, 16, 1024), idesc, ks > 0);
+    }
+}
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_s, uint32_t idesc,
+                                         uint32_t accumulate) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        tc_mma_ts_w(d_tmem, p_tmem + 8u * ks, sdesc_sw128(v_s + (uint32_t)ks * 2048u, kHalf, 1024), idesc,
+                    (accumulate || ks > 0) ? 1u : 0u);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ TcParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
+    uint64_t *q_full = bars + 0;     // Q tiles of a unit landed (one phase per unit)
+    uint64_t *q_empty = bars + 1;    // the unit's last S products are done with Q
+    uint64_t *kv_full = bars + 2;    // [kSlots]
+    uint64_t *kv_empty = bars + 7;   // [kSlots]
+    uint64_t *s_full = bars + 12;    // [2] S of a group computed
+    uint64_t *p_ready = bars + 14;   // [2] P of a group written to TMEM (128 arrivals)
+    uint64_t *o_done = bars + 16;    // [2] PV of a group done
+    uint64_t *mma_done = bars + 18;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 20);
+    const PagedArgs &a = p.a;
+    const PagedFamily &f = a.f[p.fi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_ready + i, 128);
+            mbar_init(o_done + i, 1);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl wc{abort_flag, a.status, p.budget_ns};
+    pdl_wait();
+    pdl_launch();
+    const long long per = a.hdr->per[p.fi];
+    const long long x0 = blockIdx.x * per, x1 = min(a.hdr->W[p.fi], x0 + per);
+
+    // The CTA's units in order, the same for every role.
+    auto first = [&]() { return x0 < x1 ? paged_find(f, x0) : 0; };
+    auto walk_at = [&](long long x, int s) {
+        Walk w;
+        while (f.cumW[s + 1] <= x) ++s;
+        w.s = s;
+        w.g = f.seg[s];
+        w.u = paged_unit(a, f, w.g, s, x, x1);
+        w.pair = w.u.rows > 128;
+        const int sees = paged_limit(a, w.g, p.fi, w.u.r0 + w.u.rows - 1);
+        w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
+        return w;
+    };
+
+    // Registers: 128 x 80 + 256 x 200 = 61440, within the 384 x 168 = 64512 of the launch.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+        if (warp == 0) {
+            // -------------------------------------------- producer
+            uint32_t n = 0;  // K and V tiles loaded
+            int nq = 0, ok = 1;
+            if (lane == 0) {
+                tma_prefetch_desc(&p.tmQ);
+                tma_prefetch_desc(&p.tmK);
+                tma_prefetch_desc(&p.tmV);
+            }
+            const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
+            for (long long x = x0, s = first(); x < x1 && ok;) {
+                const Walk w = walk_at(x, (int)s);
+                s = w.s;
+                const int tok = w.g.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
+                if (lane == 0) {
+                    if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1u, wc);
+                    if (ok) {
+                        mbar_arrive_expect_tx(q_full, (w.pair ? 2u : 1u) * kTile);
+                        for (int k = 0; k < (w.pair ? 2 : 1); ++k) {
+                            tma_load_3d(base + k * kTile, &p.tmQ, q_full, 0, hq, tok + k * (128 >> p.log2G));
+                            tma_load_3d(base + k * kTile + kHalf, &p.tmQ, q_full, 64, hq, tok + k * (128 >> p.log2G));
+                        }
+                        ++nq;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                // page and row of this lane's box of a tile
+                auto look_up = [&](int t, int &page, int &row) {
+                    const int key = t * 128 + (lane >> 1) * p.box;
+                    page = (int)a.n_pages;  // outside the cache: filled with zeros
+                    row = key % a.page_size;
+                    if (lane < boxes && key < w.g.len) {
+                        const int pg = __ldg(f.table + (int64_t)w.s * f.width + key / a.page_size);
+                        if (pg >= 0 && pg < a.n_pages)
+                            page = pg;
+                        else
+                            record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+                    }
+                };
+                auto load = [&](const CUtensorMap *m, int page, int row) {
+                    const uint32_t slot = n % kSlots;
+                    if (lane == 0) {
+                        ok = mbar_wait(kv_empty + slot, ((n / kSlots) & 1u) ^ 1u, wc);
+                        if (ok) mbar_arrive_expect_tx(kv_full + slot, kTile);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) return;
+                    if (lane < boxes)
+                        tma_load_4d(base + kOffKV + slot * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128, m,
+                                    kv_full + slot, (lane & 1) * 64, p.rows_inner ? row : w.u.h,
+                                    p.rows_inner ? w.u.h : row, page);
+                    ++n;
+                };
+                const int by = w.pair ? 1 : 2;
+                int pa = 0, ra = 0, pb = 0, rb = 0;
+                if (w.u.t0 < w.tend) look_up(w.u.t0, pa, ra);
+                if (!w.pair && w.u.t0 + 1 < w.tend) look_up(w.u.t0 + 1, pb, rb);
+                for (int t = w.u.t0; t < w.tend && ok; t += by) {
+                    const bool two = !w.pair && t + 1 < w.tend;
+                    const int pa0 = pa, ra0 = ra, pb0 = pb, rb0 = rb;
+                    // the next step's pages are looked up ahead of this step's waits
+                    if (t + by < w.tend) look_up(t + by, pa, ra);
+                    if (!w.pair && t + 3 < w.tend) look_up(t + 3, pb, rb);
+                    load(&p.tmK, pa0, ra0);
+                    if (two && ok) load(&p.tmK, pb0, rb0);
+                    if (ok) load(&p.tmV, pa0, ra0);
+                    if (two && ok) load(&p.tmV, pb0, rb0);
+                }
+                x += w.u.t1 - w.u.t0;
+            }
+            if (lane == 0) {
+                // the last copies must have landed before the CTA may exit
+                volatile int local_abort = 0;
+                const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+                if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1u, drain);
+                for (uint32_t i = (n > kSlots ? n - kSlots : 0); i < n; ++i)
+                    (void)mbar_wait(kv_full + (i % kSlots), (i / kSlots) & 1u, drain);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------- MMA issuer
+            const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+            const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
+            const uint32_t kvs = base_s + kOffKV;
+            const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+            uint32_t n = 0, np0 = 0, np1 = 0;  // tiles consumed; PVs issued per group (all units)
+            int nu = 0;
+            bool ok = true;
+            auto full = [&](uint32_t i) {
+                ok = ok && mbar_wait_warp(kv_full + i % kSlots, (i / kSlots) & 1u, wc);
+                tc_fence_after();
+                return kvs + (i % kSlots) * kTile;
+            };
+            auto empty = [&](uint32_t i) { tc_commit_w(kv_empty + i % kSlots); };
+            for (long long x = x0, s = first(); x < x1 && ok;) {
+                const Walk w = walk_at(x, (int)s);
+                s = w.s;
+                ok = mbar_wait_warp(q_full, nu & 1u, wc);
+                ++nu;
+                tc_fence_after();
+                const uint32_t q0 = base_s, q1 = base_s + (w.pair ? kTile : 0u);
+                const int by = w.pair ? 1 : 2;
+                // V rows behind the length, up to the end of their page, may hold anything
+                auto clean = [&](int t, uint32_t i) {
+                    const int live = w.g.len - t * 128;
+                    if (live >= 128 || w.g.len % a.page_size == 0) return;
+                    uint8_t *v = base + kOffKV + (i % kSlots) * kTile;
+                    for (int c = live * 8 + lane; c < 1024; c += 32) {
+                        *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(v + kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                if (w.u.t0 >= w.tend || !ok) {
+                    tc_commit_w(q_empty);
+                    x += w.u.t1 - w.u.t0;
+                    continue;
+                }
+                // S of the first step
+                {
+                    const bool two = !w.pair && w.u.t0 + 1 < w.tend;
+                    const uint32_t k0 = full(n);
+                    if (!ok) break;
+                    issue_s(tS[0], q0, k0, idesc_s);
+                    tc_commit_w(s_full + 0);
+                    if (w.pair) {
+                        issue_s(tS[1], q1, k0, idesc_s);
+                        tc_commit_w(s_full + 1);
+                        empty(n);
+                    } else {
+                        empty(n);
+                        if (two) {
+                            const uint32_t k1 = full(n + 1);
+                            if (!ok) break;
+                            issue_s(tS[1], q0, k1, idesc_s);
+                            tc_commit_w(s_full + 1);
+                            empty(n + 1);
+                        }
+                    }
+                }
+                uint32_t pv0 = 0, pv1 = 0;  // this unit's
+                for (int t = w.u.t0; t < w.tend; t += by) {
+                    const bool two = !w.pair && t + 1 < w.tend, one1 = w.pair || two;
+                    const bool next = t + by < w.tend, next1 = w.pair ? next : t + 3 < w.tend;
+                    const uint32_t va = n + (two ? 2u : 1u), vb = w.pair ? va : va + 1;
+                    const uint32_t ka = n + (two ? 4u : 2u), kb = w.pair ? ka : ka + 1;
+                    if (!next) tc_commit_w(q_empty);  // every S of this unit is issued
+                    const uint32_t v0 = full(va);
+                    if (!ok) break;
+                    clean(t, va);
+                    ok = mbar_wait_warp(p_ready + 0, np0 & 1u, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(tO[0], tS[0], v0, idesc_o, pv0 > 0);
+                    tc_commit_w(o_done + 0);
+                    ++np0;
+                    ++pv0;
+                    if (!w.pair) empty(va);
+                    if (next) {
+                        const uint32_t k0 = full(ka);
+                        if (!ok) break;
+                        issue_s(tS[0], q0, k0, idesc_s);
+                        tc_commit_w(s_full + 0);
+                        if (!w.pair) empty(ka);
+                    }
+                    if (one1) {
+                        const uint32_t v1 = full(vb);
+                        if (!ok) break;
+                        if (!w.pair) clean(t + 1, vb);
+                        ok = mbar_wait_warp(p_ready + 1, np1 & 1u, wc);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(tO[1], tS[1], v1, idesc_o, pv1 > 0);
+                        tc_commit_w(o_done + 1);
+                        ++np1;
+                        ++pv1;
+                        empty(vb);
+                    }
+                    if (next1) {
+                        const uint32_t k1 = full(kb);
+                        if (!ok) break;
+                        issue_s(tS[1], q1, k1, idesc_s);
+                        tc_commit_w(s_full + 1);
+                        empty(kb);
+                    }
+                    n += two ? 4u : 2u;
+                }
+                x += w.u.t1 - w.u.t0;
+            }
+            // every MMA issued must have completed before TMEM is released
+            tc_commit_w(mma_done);
+            volatile int local_abort = 0;
+            const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+            (void)mbar_wait_warp(mma_done, 0, drain);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+        // ------------------------------------------------ softmax / epilogue
+        const int k = warp >= 8 ? 1 : 0;
+        const int m = threadIdx.x - 128 - 128 * k;  // TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + 128u * k;
+        const uint32_t tO = tmem + lane_base + 256u + 128u * k;
+        uint32_t nd_all = 0;  // S tiles of this group (all units)
+        bool ok = true;
+        for (long long x = x0, s = first(); x < x1 && ok;) {
+            const Walk w = walk_at(x, (int)s);
+            s = w.s;
+            const int by = w.pair ? 1 : 2;
+            const int row = (w.pair ? 128 * k : 0) + m;  // of the unit
+            const bool valid = row < w.u.rows;
+            // (padding rows hold other tokens' queries or zeros: computed without masks, dropped)
+            const int lim = valid ? paged_limit(a, w.g, p.fi, w.u.r0 + row) : w.g.len;
+            const bool busy = __any_sync(0xffffffffu, valid);  // a warp of padding rows only keeps the barriers going
+            float m_run = -INFINITY, l_run = 0.f;
+            uint32_t nd = 0;
+            for (int t = w.u.t0 + (w.pair ? 0 : k); t < w.tend; t += by) {
+                ok = mbar_wait_warp(s_full + k, nd_all & 1u, wc);
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    float sc[128];
+                    {
+                        uint32_t v[128];
+                        tmem_ld128(tS, v);
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) sc[i] = __uint_as_float(v[i]);
+                    }
+                    const int seen = lim - t * 128;  // columns of this tile that the row sees
+                    if (__any_sync(0xffffffffu, seen < 128)) {
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            const uint32_t bits = low_bits(seen, 32 * ch);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                sc[32 * ch + i] = ((bits >> i) & 1u) ? sc[32 * ch + i] : -INFINITY;
+                        }
+                    }
+                    float mx8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(sc[i], sc[8 + i]);
+#pragma unroll
+                    for (int c = 16; c < 128; c += 16) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mx8[i] = max3f(mx8[i], sc[c + i], sc[c + 8 + i]);
+                    }
+                    const float mx =
+                        max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+                    // the reference maximum moves only when it grew by more than 2^8: the final
+                    // scaling uses the same one, so the result is exact
+                    const float m_new = fmaxf(m_run, mx * a.scale_log2);
+                    const bool need = m_new > m_run + 8.0f;
+                    float alpha = 1.f;
+                    if (need) {
+                        alpha = ex2_approx(m_run - m_new);
+                        m_run = m_new;
+                        l_run *= alpha;
+                    }
+                    const float use = (m_run == -INFINITY) ? 0.f : m_run;
+                    float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                      make_float2(0.f, 0.f)};
+                    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-use, -use);
+                    uint32_t pk[64];
+#pragma unroll
+                    for (int c2 = 0; c2 < 64; ++c2) {
+                        const float2 e = fma2(make_float2(sc[2 * c2], sc[2 * c2 + 1]), sl2, nm2);
+                        const float2 e2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                        sum4[c2 & 3] = add2(sum4[c2 & 3], e2);
+                        pk[c2] = pack_bf16x2(e2.x, e2.y);
+                    }
+                    const float2 sum2 = add2(add2(sum4[0], sum4[1]), add2(sum4[2], sum4[3]));
+                    l_run += sum2.x + sum2.y;
+                    tmem_st64(tS, pk);
+                    // O is rescaled here: its last product finished before this S was computed
+                    if (nd > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + 32u * ch, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                            tmem_st32(tO + 32u * ch, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(p_ready + k);
+                ++nd;
+                ++nd_all;
+            }
+            if (ok && nd > 0) {
+                ok = mbar_wait_warp(o_done + k, (nd_all - 1) & 1u, wc);
+                tc_fence_after();
+            }
+            // the partial: rows of group 1 lie behind group 0's when both have the same rows
+            if (ok && busy) {
+                const int64_t at = w.u.base + (int64_t)blockIdx.x * f.rt + (w.pair ? row : row + k * w.u.rows);
+#pragma unroll 1
+                for (int ch = 0; ch < 4 && nd > 0; ++ch) {
+                    uint32_t v[32];
+                    tmem_ld32(tO + 32u * ch, v);
+                    if (valid) {
+                        float4 *dst = reinterpret_cast<float4 *>(f.acc + at * 128 + 32 * ch);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                    }
+                }
+                if (valid) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m_run, l_run);
+            }
+            // (O is next written by a later unit's first PV, which waits for this
+            // thread's next P: the readout above comes first in program order)
+            x += w.u.t1 - w.u.t0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Boxes of whole 8-row swizzle groups that tile 128 keys or a page; rows of
+// G heads that tile 128 rows; the maximum is taken before the scaling, so a
+// positive scale; and a cache that a tensor map can describe.
+bool paged_tc_maps(const PagedArgs &a, PagedMaps &m) {
+    const int G = a.G, page = a.page_size;
+    if (a.dtype != RA_BF16 || a.d != 128 || G > 128 || (G & (G - 1)) || !(a.scale_log2 > 0.f) || a.n_pages < 1 ||
+        !(page >= 128 ? page % 128 == 0 : page >= 8 && 128 % page == 0))
+        return false;
+    const cuuint64_t qd[3] = {128, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t qs[2] = {256, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    if (!encode(&m.q, a.q, 3, qd, qs, qb)) return false;
+    m.rows_inner = a.head_stride > a.token_stride;
+    const cuuint32_t box = (cuuint32_t)std::min(page, 128);
+    cuuint64_t st[3] = {(cuuint64_t)a.head_stride * 2, (cuuint64_t)a.token_stride * 2, (cuuint64_t)a.page_stride * 2};
+    cuuint64_t kd[4] = {128, (cuuint64_t)a.Hkv, (cuuint64_t)page, (cuuint64_t)a.n_pages};
+    cuuint32_t kb[4] = {64, 1, box, 1};
+    if (m.rows_inner) {
+        std::swap(st[0], st[1]);
+        std::swap(kd[1], kd[2]);
+        std::swap(kb[1], kb[2]);
+    }
+    cuuint64_t least = 256;  // a one-element dimension has no stride: any that fits the others does
+    for (int i = 0; i < 3; ++i) {
+        if (kd[i + 1] == 1) st[i] = least;
+        if (st[i] < least) return false;  // overlapping rows, or pages inside each other
+        least = st[i] * kd[i + 1];
+    }
+    return encode(&m.k, a.k, 4, kd, st, kb) && encode(&m.v, a.v, 4, kd, st, kb);
+}
+
+cudaError_t launch_paged_tc(const PagedArgs &a, int fi, const PagedMaps &m, cudaStream_t st) {
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    p.tmQ = m.q;
+    p.tmK = m.k;
+    p.tmV = m.v;
+    p.rows_inner = m.rows_inner;
+    p.a = a;
+    p.fi = fi;
+    p.box = std::min(a.page_size, 128);
+    while ((1 << p.log2G) < a.G) ++p.log2G;
+    p.budget_ns = wait_budget_ns();
+    static bool attr_set[128] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute((const void *)paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        // The register split draws on the 384 x 168 of the launch: with fewer, the increase could never be granted.
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, (const void *)paged_tc_kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 128) attr_set[dev] = true;
+    }
+    return launch_pdl(paged_tc_kernel, a.f[fi].n, kThreads, kSmem, st, p);
+}
+
+}  // namespace ra

@@ -90,19 +90,20 @@ ra_status check_cache(const ra_paged_kv *c) {
 }
 
 // ------------------------------------------------------------ paged attention
-// Rows a unit of each family: 16 where a unit can hold no more, else 64.
+// Where everything lies in the workspace.  The sizes hold for every kernel
+// that a call of these shapes may choose (the choice also goes by the page
+// size and the scale, which the size query does not know).
 struct PagedLayout {
-    int rt[2];
-    int64_t slots[2];
-    size_t o_hdr, o_seg[2], o_cumW[2], o_cumU[2], o_acc[2], o_ml[2], bytes;
+    size_t o_hdr, o_seg[2], o_cumW[2], o_cumR[2], o_acc[2], o_ml[2], bytes;
 };
+
+// A family whose units hold at most 16 rows is left to the warp-level kernel.
+bool paged_few(int family, int64_t T, int G, int max_q_len) {
+    return (family || max_q_len <= 0 ? T : std::min<int64_t>(max_q_len, T)) * G <= 16;
+}
 
 PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, int dtype, int max_q_len) {
     PagedLayout L{};
-    (void)dtype;
-    const int64_t own = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * G;
-    L.rt[0] = own <= 16 ? 16 : 64;
-    L.rt[1] = T * G <= 16 ? 16 : 64;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -114,11 +115,13 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
         const int64_t S = f ? n_groups : B;
         L.o_seg[f] = take((size_t)S * sizeof(PagedSeg));
         L.o_cumW[f] = take((size_t)(S + 1) * 8);
-        L.o_cumU[f] = take((size_t)(S + 1) * 4);
-        // every segment ends a row tile of its own at most once
-        L.slots[f] = S ? Hkv * (S + (T * G + L.rt[f] - 1) / L.rt[f]) + kPagedMaxCtas : 0;
-        L.o_acc[f] = take((size_t)L.slots[f] * L.rt[f] * d * 4);
-        L.o_ml[f] = take((size_t)L.slots[f] * L.rt[f] * 8);
+        L.o_cumR[f] = take((size_t)(S + 1) * 8);
+        // the rows themselves (twice where units are halved), and one unit more a CTA
+        const bool few = paged_few(f, T, G, max_q_len), wide = !few && dtype == RA_BF16 && d == 128;
+        int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (few ? 16 : 64) : 0;
+        if (S && wide) rows = std::max(rows, 2 * T * G * Hkv + (int64_t)kPagedMaxWide * kPagedWideRows);
+        L.o_acc[f] = take((size_t)rows * d * 4);
+        L.o_ml[f] = take((size_t)rows * 8);
     }
     L.bytes = at;
     return L;
@@ -268,16 +271,26 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.groups = prefix_groups;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr);
-    const bool mma = paged_mma_supported(dtype, d);
+    enum { kSimt, kMma, kWide } kind[2];
+    PagedMaps maps;
+    const bool wide = (!paged_few(0, T, a.G, max_q_len) || (n_groups > 0 && !paged_few(1, T, a.G, max_q_len))) &&
+                      paged_tc_maps(a, maps);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
+        const bool few = paged_few(f, T, a.G, max_q_len);
+        kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
+        if (!few && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
-        F.rt = L.rt[f];
-        F.kt = 64;
-        F.n = mma ? paged_mma_ctas(F.rt, d) : paged_simt_ctas(F.rt, d);
+        F.rt = kind[f] == kWide ? kPagedWideRows : few ? 16 : 64;
+        F.kt = kind[f] == kWide ? 128 : 64;
+        F.halves = kind[f] == kWide;
+        if (F.S)
+            F.n = kind[f] == kWide  ? std::min(kPagedMaxWide, paged_sms())
+                  : kind[f] == kMma ? paged_mma_ctas(F.rt, d)
+                                    : paged_simt_ctas(F.rt, d);
         F.seg = reinterpret_cast<PagedSeg *>(ws + L.o_seg[f]);
         F.cumW = reinterpret_cast<long long *>(ws + L.o_cumW[f]);
-        F.cumU = reinterpret_cast<int *>(ws + L.o_cumU[f]);
+        F.cumR = reinterpret_cast<long long *>(ws + L.o_cumR[f]);
         F.table = f ? prefix_table : page_table;
         F.width = f ? prefix_width : table_width;
         F.acc = reinterpret_cast<float *>(ws + L.o_acc[f]);
@@ -295,7 +308,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     for (int f = 1; f >= 0; --f) {
         if (a.f[f].S == 0) continue;
         ProfScope ps(f ? "ra_paged_prefix" : "ra_paged_own", s);
-        e = mma ? launch_paged_mma(a, f, s) : launch_paged_simt(a, f, s);
+        e = kind[f] == kWide ? launch_paged_tc(a, f, maps, s) : kind[f] == kMma ? launch_paged_mma(a, f, s)
+                                                                          : launch_paged_simt(a, f, s);
         if (e != cudaSuccess) return launch_failed(e, "paged attention launch");
     }
     ProfScope ps("ra_paged_combine", s);
