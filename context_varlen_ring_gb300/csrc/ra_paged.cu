@@ -304,131 +304,149 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t
 }
 
 // ------------------------------------------------------------------ join
-// The partials of one (token, head) row in a family: cnt of them, the i-th at
-// partial row `at + i / parts * rt + i % parts * second`.
+// The partials of a token and KV head in a family: cnt of them a row, the
+// i-th of query head g at partial row  at + g + (i >> two) * rt + (i & two) * second.
 struct Parts {
     const float *acc, *ml;
-    int64_t at;
-    int cnt, rt, parts, second;
-    __device__ __forceinline__ int64_t row(int i) const {
-        return at + (int64_t)(i / parts) * rt + (i % parts) * second;
+    long long at;
+    int cnt, rt, two, second;
+    __device__ __forceinline__ long long row(int i, int g) const {
+        return at + g + (long long)(i >> two) * rt + (i & two) * second;
     }
 };
 
-__device__ __forceinline__ Parts find_parts(const PagedArgs &a, int fi, int64_t t, int head, int b) {
+// G rows may straddle two units (rows a unit need not be a multiple of G), so
+// the place is found per query head g.
+__device__ __forceinline__ Parts find_parts(const PagedArgs &a, int fi, int s, int64_t t, int h, int g) {
     const PagedFamily &f = a.f[fi];
-    Parts p{f.acc, f.ml, 0, 0, f.rt, 1, 0};
-    if (f.S == 0) return p;
-    const int s = fi ? segment_of(a.groups + 1, a.n_groups, b) : b;
-    if (s >= f.S || (fi && b < a.groups[s])) return p;  // a sequence outside every group
-    const PagedSeg g = f.seg[s];
-    if (g.w == 0) return p;
-    const int r = (int)(t - g.tok0) * a.G + head % a.G, rtile = r / f.rt, h = head / a.G;
-    const int rows = min(f.rt, g.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    const long long x = f.cumW[s] + (long long)(rtile * a.Hkv + h) * g.w, per = a.hdr->per[fi];
-    const int c0 = (int)(x / per), c1 = (int)((x + g.w - 1) / per);
-    p.at = f.cumR[s] + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
-    p.parts = alloc > rows ? 2 : 1;
+    Parts p{f.acc, f.ml, 0, 0, f.rt, 0, 0};
+    if (s < 0) return p;
+    const PagedSeg sg = f.seg[s];
+    if (sg.w == 0) return p;
+    const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
+    const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
+    const long long x = f.cumW[s] + (long long)(rtile * a.Hkv + h) * sg.w, per = a.hdr->per[fi];
+    const int c0 = (int)(x / per), c1 = (int)((x + sg.w - 1) / per);
+    p.at = f.cumR[s] + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt - g;
+    p.two = alloc > rows ? 1 : 0;
     p.second = rows;
-    p.cnt = (c1 - c0 + 1) * p.parts;
+    p.cnt = (c1 - c0 + 1) << p.two;
     return p;
 }
 
-// WPR warps per (token, head) row: the largest maximum M of its partials,
-// their weights 2^(m - M), and the weighted sums.  Warp w adds partials w,
-// w + WPR, ... (own keys first, then the prefix) and the warps' sums are
-// added in order, so the result does not depend on timing.  Latency bound:
-// few rows come with many partials each (a long sequence over all SMs), so
-// the partials of a row are read by several warps at once.
-template <typename TOut, int WPR>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ float sum[8][256];
+// A block per (token, KV head), its WARPS warps over the G query heads and,
+// where there are more warps than heads, over a head's partials: the largest
+// maximum M, the weights 2^(m - M), the weighted sums.  Own keys come first,
+// then the prefix; warps' sums are added in order, so the result does not
+// depend on timing.  Latency bound (a chain of dependent loads: segment,
+// place, maxima, sums), so the segments are searched once a block, ahead of the
+// wait for the attention kernels, and few blocks get more warps.
+template <typename TOut, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+    __shared__ float sum[WARPS][256];
+    __shared__ int seg[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = blockIdx.x / a.Hkv;
+    const int h = blockIdx.x % a.Hkv;
+    if (warp == 0) {
+        const int b = segment_of(a.cu + 1, a.B, t);
+        const bool live = b < a.B && t >= a.cu[b];  // not behind the last sequence, nor ahead of the first
+        int g = -1;
+        if (live && a.n_groups > 0) {
+            g = segment_of(a.groups + 1, a.n_groups, b);
+            if (g >= a.n_groups || b < a.groups[g]) g = -1;  // a sequence outside every group
+        }
+        if (lane == 0) {
+            seg[0] = live ? b : -1;
+            seg[1] = g;
+        }
+    }
+    __syncthreads();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
-    const int64_t row = (int64_t)blockIdx.x * (8 / WPR) + warp / WPR;
-    bool live = row < a.T * a.Hq && !a.hdr->err;
-    const int64_t t = live ? row / a.Hq : 0;
-    const int head = (int)(row % a.Hq);
-    const int b = live ? segment_of(a.cu + 1, a.B, t) : a.B;
-    live = b < a.B && t >= a.cu[b];  // not behind the last sequence, nor ahead of the first
-    float M = -INFINITY, L = 0.f;
-    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (live) {
-        const Parts p0 = find_parts(a, 0, t, head, b), p1 = find_parts(a, 1, t, head, b);
-        const int cnt = p0.cnt + p1.cnt;
-        auto ml = [&](int i) {
-            return *reinterpret_cast<const float2 *>(i < p0.cnt ? p0.ml + p0.row(i) * 2 : p1.ml + p1.row(i - p0.cnt) * 2);
-        };
-        for (int i = lane; i < cnt; i += 32) M = fmaxf(M, ml(i).x);
+    if (seg[0] < 0 || a.hdr->err) return;
+    int wpr = 1;  // warps a row: a power of two, heads in turn where there are more
+    while (wpr * 2 * a.G <= WARPS) wpr *= 2;
+    const int sub = warp % wpr, at_once = WARPS / wpr, d4 = a.d / 4;
+    for (int g0 = 0; g0 < a.G; g0 += at_once) {
+        const int g = g0 + warp / wpr;
+        const bool live = g < a.G;
+        float M = -INFINITY, L = 0.f;
+        float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (live) {
+            const Parts p0 = find_parts(a, 0, seg[0], t, h, g), p1 = find_parts(a, 1, seg[1], t, h, g);
+            const int cnt = p0.cnt + p1.cnt;
+            auto ml = [&](int i) {
+                const float *p = i < p0.cnt ? p0.ml + p0.row(i, g) * 2 : p1.ml + p1.row(i - p0.cnt, g) * 2;
+                return *reinterpret_cast<const float2 *>(p);
+            };
+            float2 mine = make_float2(-INFINITY, 0.f);
+            if (lane < cnt) mine = ml(lane);
+            M = mine.x;
+            for (int i = lane + 32; i < cnt; i += 32) M = fmaxf(M, ml(i).x);
 #pragma unroll
-        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        if (M != -INFINITY) {
-            const int d4 = a.d / 4;
-            for (int i0 = 0; i0 < cnt; i0 += 32) {
-                float w = 0.f;
-                if (i0 + lane < cnt) {
-                    const float2 v = ml(i0 + lane);
-                    w = exp2f(v.x - M);
-                    L += w * v.y;
-                }
-                const int most = min(32, cnt - i0);
+            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+            if (M != -INFINITY) {
+                for (int i0 = 0; i0 < cnt; i0 += 32) {
+                    if (i0 > 0) mine = i0 + lane < cnt ? ml(i0 + lane) : make_float2(-INFINITY, 0.f);
+                    const float w = exp2f(mine.x - M);
+                    L += w * mine.y;
+                    const int most = min(32, cnt - i0);
 #pragma unroll 4
-                for (int i = sub; i < most; i += WPR) {
-                    const float wi = __shfl_sync(0xffffffffu, w, i);
-                    const int k = i0 + i;
-                    const float4 *p = reinterpret_cast<const float4 *>(
-                        k < p0.cnt ? p0.acc + p0.row(k) * a.d : p1.acc + p1.row(k - p0.cnt) * a.d);
-                    // (a partial without weight may never have been written)
+                    for (int i = sub; i < most; i += wpr) {
+                        const float wi = __shfl_sync(0xffffffffu, w, i);
+                        const int k = i0 + i;
+                        const float4 *p = reinterpret_cast<const float4 *>(
+                            k < p0.cnt ? p0.acc + p0.row(k, g) * a.d : p1.acc + p1.row(k - p0.cnt, g) * a.d);
+                        // (a partial without weight may never have been written)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (wi != 0.f && lane + 32 * e < d4) {
-                            const float4 v = p[lane + 32 * e];
-                            o[e].x = fmaf(wi, v.x, o[e].x);
-                            o[e].y = fmaf(wi, v.y, o[e].y);
-                            o[e].z = fmaf(wi, v.z, o[e].z);
-                            o[e].w = fmaf(wi, v.w, o[e].w);
+                        for (int e = 0; e < 2; ++e) {
+                            if (wi != 0.f && lane + 32 * e < d4) {
+                                const float4 v = p[lane + 32 * e];
+                                o[e].x = fmaf(wi, v.x, o[e].x);
+                                o[e].y = fmaf(wi, v.y, o[e].y);
+                                o[e].z = fmaf(wi, v.z, o[e].z);
+                                o[e].w = fmaf(wi, v.w, o[e].w);
+                            }
                         }
                     }
                 }
+#pragma unroll
+                for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
             }
-#pragma unroll
-            for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
         }
-    }
-    if (WPR > 1) {
+        if (wpr > 1) {  // (then every head has its warps at once: one trip of the outer loop)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) *reinterpret_cast<float4 *>(&sum[warp][(lane + 32 * e) * 4]) = o[e];
-        __syncthreads();
-    }
-    if (!live) return;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    TOut *out = static_cast<TOut *>(a.out) + row * a.d;
-    for (int c = (WPR > 1 ? sub * 32 + lane : lane) * 4; c < a.d; c += WPR * 128) {
-        float4 v;
-        if (WPR > 1) {
-            v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < WPR; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sum[warp - sub + i][c]);
-                v.x += x.x;
-                v.y += x.y;
-                v.z += x.z;
-                v.w += x.w;
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<float4 *>(&sum[warp][(lane + 32 * e) * 4]) = o[e];
+            __syncthreads();
+        }
+        if (!live) continue;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int head = h * a.G + g;
+        TOut *out = static_cast<TOut *>(a.out) + (t * a.Hq + head) * a.d;
+        for (int c = (sub * 32 + lane) * 4; c < a.d; c += wpr * 128) {
+            float4 v = c < 128 ? o[0] : o[1];
+            if (wpr > 1) {
+                v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < wpr; ++i) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sum[warp - sub + i][c]);
+                    v.x += x.x;
+                    v.y += x.y;
+                    v.z += x.z;
+                    v.w += x.w;
+                }
             }
-        } else {
-            v = c < 128 ? o[0] : o[1];
+            if constexpr (sizeof(TOut) == 4) {
+                *reinterpret_cast<float4 *>(out + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            } else {
+                uint2 pk;
+                pk.x = pack_bf16x2(v.x * inv, v.y * inv);
+                pk.y = pack_bf16x2(v.z * inv, v.w * inv);
+                *reinterpret_cast<uint2 *>(out + c) = pk;
+            }
         }
-        if constexpr (sizeof(TOut) == 4) {
-            *reinterpret_cast<float4 *>(out + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-        } else {
-            uint2 pk;
-            pk.x = pack_bf16x2(v.x * inv, v.y * inv);
-            pk.y = pack_bf16x2(v.z * inv, v.w * inv);
-            *reinterpret_cast<uint2 *>(out + c) = pk;
-        }
+        if (sub == 0 && lane == 0)
+            a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
-    if (sub == 0 && lane == 0)
-        a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
@@ -467,17 +485,12 @@ cudaError_t launch_paged_simt(const PagedArgs &a, int fi, cudaStream_t st) {
 }
 
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {
-    const int64_t rows = a.T * a.Hq;
-    auto go = [&](auto kernel, int wpr) {
-        return launch_pdl(kernel, (unsigned)((rows * wpr + 7) / 8), 256, 0, st, a);
-    };
-    // few rows: many partials each, and warps to spare
-    if (a.out_dtype == RA_FP32) {
-        if (rows <= 2048) return go(paged_combine_kernel<float, 8>, 8);
-        return rows <= 16384 ? go(paged_combine_kernel<float, 4>, 4) : go(paged_combine_kernel<float, 1>, 1);
-    }
-    if (rows <= 2048) return go(paged_combine_kernel<__nv_bfloat16, 8>, 8);
-    return rows <= 16384 ? go(paged_combine_kernel<__nv_bfloat16, 4>, 4) : go(paged_combine_kernel<__nv_bfloat16, 1>, 1);
+    const int64_t blocks = a.T * a.Hkv;  // < 2^31
+    auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, (unsigned)blocks, warps * 32, 0, st, a); };
+    const bool few = blocks <= 2 * paged_sms();
+    if (a.out_dtype == RA_FP32)
+        return few ? go(paged_combine_kernel<float, 16>, 16) : go(paged_combine_kernel<float, 8>, 8);
+    return few ? go(paged_combine_kernel<__nv_bfloat16, 16>, 16) : go(paged_combine_kernel<__nv_bfloat16, 8>, 8);
 }
 
 }  // namespace ra
