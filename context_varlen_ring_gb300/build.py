@@ -1,7 +1,9 @@
-"""Builds libra.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Builds libra.so (the C-ABI library) in-tree for sm_103a with nvcc, and
+the Python module _serving (the torch binding of the serving calls) with g++.
 
 Each translation unit compiles in parallel into _build/, then one link
-step writes context_varlen_ring_gb300/libra.so.  No CMake.
+step writes context_varlen_ring_gb300/libra.so, and one the module, which
+calls into it.  No CMake.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +21,8 @@ LIB = os.path.join(HERE, "libra.so")
 SOURCES = ["ra_api.cpp", "ra_plan.cpp", "ra_stats.cpp", "ra_misc.cu", "ra_simt.cu", "ra_tc_fwd.cu", "ra_tc_bwd.cu",
            "ra_tc_dq.cu", "ra_noalloc.cu", "ra_tile_build.cu", "ra_rope.cu", "ra_paged.cu", "ra_paged_mma.cu",
            "ra_paged_tc.cu", "ra_serve.cpp"]
+MODULE = os.path.join(HERE, "_serving.so")
+MODULE_SRC = os.path.join(CSRC, "py_serving.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I" + os.path.join(HERE, "..", "include")]
@@ -28,6 +33,23 @@ def nvcc() -> str:
         if c and os.path.exists(c):
             return c
     raise RuntimeError("nvcc not found")
+
+
+def _module_job(extra=()):
+    """(object file, compile command, link command) of the Python module, for the installed torch."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    obj = os.path.join(BUILD, f"py_serving-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.o")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+           sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += [x for i in inc for x in ("-isystem", i)] + list(extra) + ["-c", MODULE_SRC, "-o", obj]
+    lib = os.path.join(root, "lib")
+    link = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libra.so",
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    return obj, cmd, ["g++", "-shared", obj, "-o"], link
 
 
 def _stale(out: str, deps) -> bool:
@@ -53,6 +75,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             if s.endswith(".cpp"):
                 cmd = [nvcc(), "-x", "c++"] + COMMON + list(extra) + ["-c", src, "-o", obj]
             jobs.append(cmd)
+    mod_obj, mod_cmd, mod_link, mod_libs = _module_job()
+    if force or _stale(mod_obj, [MODULE_SRC, __file__] + headers):
+        jobs.insert(0, mod_cmd)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -75,6 +100,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    if force or _stale(MODULE, [mod_obj, LIB]):
+        tmp = MODULE + f".tmp{os.getpid()}"
+        cmd = mod_link + [tmp] + mod_libs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("link failed")
+        os.replace(tmp, MODULE)
     return LIB
 
 
