@@ -230,7 +230,7 @@ struct RopeParams {
     int64_t T;
     const int32_t *pos;                // DEVICE [axes][T]
     int n_pairs, adjacent, inverse;
-    int units, rot_units, heads_per_block;  // set by launch_rope
+    int units, rot_units, split;       // set by launch_rope
     // cache rows (cu != NULL): logical index kv_lens[b] - n_b + j through the page table
     const int32_t *cu, *kv_lens, *page_table;
     int64_t table_width, n_pages, page_stride, token_stride, head_stride;

@@ -25,6 +25,8 @@
 namespace ra {
 namespace {
 
+constexpr int kRopeWarps = 4;
+
 template <typename T, int VEC>
 struct Pack;
 template <>
@@ -59,153 +61,152 @@ __device__ __forceinline__ typename Pack<T, VEC>::V repack(const float (&f)[VEC]
     return v;
 }
 
-// A block owns TT tokens; thread (u, hs) owns unit u (a vector, or the two
-// vectors of a half-split pair) of heads hs, hs + hpb, ...  Its sines and
-// cosines are those of unit u for every head, and the TT tokens' vectors are
-// loaded before the angles are computed, so TT (x 2) 16-byte loads per thread
-// hide behind the table work.
-template <typename T, int VEC, bool ADJ, int TT>
-__global__ void __launch_bounds__(1024) rope_kernel(const __grid_constant__ RopeParams p) {
+// A warp owns a token, or where tokens are few every S-th group of its heads.
+// Lane (hh, u) owns unit u (a vector, or the two vectors of a half-split pair)
+// of heads hh, hh + hpi, ...: its sines and cosines stay in registers for all
+// of them, so shared memory carries each angle once a token (with a read per
+// head the shared-memory pipe was the limit, at 81 %: 134 us for 32768 tokens
+// of 40 heads of 128 and 90 us for 8192 of 72; this form takes 128 and 64 us).
+// Two heads a lane are in flight, the first two before the angles are
+// computed; eight blocks an SM beat five with four heads in flight (131 us)
+// and ten that spill (164 us).
+template <typename T, int VEC, bool ADJ>
+__global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Pack<T, VEC>::V;
-    extern __shared__ float2 cs[];  // [TT][n_pairs]: cos, sin
-    __shared__ long long row_off[TT];
-    __shared__ int row_ok[TT];      // 0: leave the token alone, 1: its token rows only, 2: its cache row too
-    const int64_t t0 = (int64_t)blockIdx.x * TT;
-    const int u = threadIdx.x % p.units, hs = threadIdx.x / p.units;
-    const bool rot = u < p.rot_units;
-    int off0, off1 = -1, pb = 0;
-    if (!rot) {
-        off0 = 2 * p.n_pairs + (u - p.rot_units) * VEC;
-    } else if (VEC > 1 && ADJ) {
-        off0 = u * VEC;
-        pb = u * (VEC / 2);
-    } else if (VEC == 1 && p.adjacent) {
-        off0 = 2 * u;
-        off1 = 2 * u + 1;
-        pb = u;
-    } else {
-        off0 = u * VEC;
-        off1 = p.n_pairs + u * VEC;
-        pb = u * VEC;
-    }
+    constexpr int UN = 2, NP = VEC > 1 && ADJ ? VEC / 2 : VEC;  // heads in flight, pairs a unit
+    extern __shared__ float2 cs_all[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2 *cs = cs_all + warp * p.n_pairs;
+    const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t t = gw / p.split;
+    if (t >= p.T) return;
+    const int sub = (int)(gw - t * p.split);
 
     bool first = true;
-    for (int h = hs;; h += p.heads_per_block) {
-        // every thread makes the first trip (it holds the barrier); later
-        // trips are taken by the threads that have a head left
-        const bool have = h < p.total_heads && hs < p.heads_per_block;
-        int j = 0, hl = h;
-        if (have) {
-            while (hl >= p.jobs[j].heads) hl -= p.jobs[j++].heads;
-        }
-        const RopeJob &job = p.jobs[have ? j : 0];
-        V a[TT], b[TT];
-        if (have) {
-            const T *x = static_cast<const T *>(job.x) + (int64_t)hl * p.d;
-#pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                if (t0 + i < p.T) {
-                    const T *r = x + (t0 + i) * job.x_stride;
-                    a[i] = *reinterpret_cast<const V *>(r + off0);
-                    if (off1 >= 0) b[i] = *reinterpret_cast<const V *>(r + off1);
+    int ok = 1;          // 0: leave the token alone, 1: its token rows only, 2: its cache row too
+    long long off = 0;   // its cache row
+    auto prepare = [&]() {
+        if (p.cu) {
+            // the token's sequence: the number of segment ends <= t
+            const int s = dev::segment_of(p.cu + 1, p.B, t);
+            ok = 0;
+            if (s < p.B) {
+                const long long c0 = p.cu[s], n = (long long)p.cu[s + 1] - c0;
+                const long long idx = (long long)p.kv_lens[s] - n + (t - c0);
+                bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
+                if (in) {
+                    const int pg = p.page_table[(int64_t)s * p.table_width + (int)idx / p.page_size];
+                    in = pg >= 0 && pg < p.n_pages;
+                    off = pg * p.page_stride + ((int)idx % p.page_size) * p.token_stride;
                 }
+                ok = in ? 2 : 1;
+                if (!in && lane == 0) dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
             }
         }
-        if (first) {
-            first = false;
-            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
-            if (p.cu) {
-                // the sequence of each token: the number of segment ends <= t
-                for (int i = warp; i < TT; i += warps) {
-                    const int64_t t = t0 + i;
-                    int ok = 0;
-                    long long off = 0;
-                    if (t < p.T) {
-                        const int s = dev::segment_of(p.cu + 1, p.B, t);
-                        if (s < p.B) {
-                            const long long c0 = p.cu[s], n = (long long)p.cu[s + 1] - c0;
-                            const long long idx = (long long)p.kv_lens[s] - n + (t - c0);
-                            ok = 1;
-                            bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
-                            if (in) {
-                                const int pg = p.page_table[(int64_t)s * p.table_width + idx / p.page_size];
-                                in = pg >= 0 && pg < p.n_pages;
-                                off = pg * p.page_stride + (idx % p.page_size) * p.token_stride;
+        for (int w = lane; w < p.n_pairs; w += 32) {
+            const long long pos = p.pos[(int64_t)p.axis[w] * p.T + t];
+            const unsigned long long turn = (unsigned long long)pos * p.turns[w];
+            // the upper half as a signed number of 2^-31 half turns
+            float s, c;
+            sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
+            cs[w] = make_float2(c, p.inverse ? -s : s);
+        }
+        __syncwarp();
+    };
+    for (int u0 = 0; u0 < p.units; u0 += 32) {  // (one trip unless a head has more than 32 units)
+        const int hpi = p.units > 32 ? 1 : 32 / p.units;
+        const int hh = p.units > 32 ? 0 : lane / p.units, u = p.units > 32 ? u0 + lane : lane % p.units;
+        const bool mine = hh < hpi && u < p.units;
+        const bool rot = u < p.rot_units;
+        int off0, off1 = -1, pb = 0;
+        if (!rot) {
+            off0 = 2 * p.n_pairs + (u - p.rot_units) * VEC;
+        } else if (VEC > 1 && ADJ) {
+            off0 = u * VEC;
+            pb = u * (VEC / 2);
+        } else if (VEC == 1 && p.adjacent) {
+            off0 = 2 * u;
+            off1 = 2 * u + 1;
+            pb = u;
+        } else {
+            off0 = u * VEC;
+            off1 = p.n_pairs + u * VEC;
+            pb = u * VEC;
+        }
+        float2 r[NP];
+        bool loaded = false;
+        int skip = sub;  // groups of heads ahead of this warp's first in the next job
+        for (int j = 0; j < p.njobs; ++j) {
+            const RopeJob &jb = p.jobs[j];
+            const int heads = mine ? jb.heads - hh : 0, step = p.split * hpi;  // heads from this lane's on
+            const T *x = static_cast<const T *>(jb.x) + t * jb.x_stride + hh * p.d;
+            const bool turn = rot && jb.rotate;
+            const int groups = (jb.heads + hpi - 1) / hpi;
+            int h = skip * hpi;
+            while (skip < groups) skip += p.split;
+            skip -= groups;
+            for (; h < jb.heads; h += UN * step) {
+                V a[UN], b[UN];
+#pragma unroll
+                for (int i = 0; i < UN; ++i) {
+                    if (h + i * step < heads) {
+                        a[i] = *reinterpret_cast<const V *>(x + (h + i * step) * p.d + off0);
+                        if (off1 >= 0) b[i] = *reinterpret_cast<const V *>(x + (h + i * step) * p.d + off1);
+                    }
+                }
+                if (first) {
+                    first = false;
+                    prepare();
+                }
+                if (!loaded) {
+                    loaded = true;
+                    if (rot && mine) {
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) r[e] = cs[pb + e];
+                    }
+                }
+                if (ok < (jb.paged ? 2 : 1) || (jb.x == jb.y && !turn)) continue;  // (in place and passed through)
+                T *y = static_cast<T *>(jb.y) + (jb.paged ? off : t * jb.y_stride);
+                const int64_t hs = jb.paged ? p.head_stride : p.d;
+#pragma unroll
+                for (int i = 0; i < UN; ++i) {
+                    if (h + i * step >= heads) continue;
+                    if (turn) {
+                        float fa[VEC], fb[VEC];
+                        unpack<T, VEC>(a[i], fa);
+                        if (VEC > 1 && ADJ) {
+#pragma unroll
+                            for (int e = 0; e < NP; ++e) {
+                                const float x0 = fa[(2 * e) % VEC], x1 = fa[(2 * e + 1) % VEC];
+                                fa[(2 * e) % VEC] = x0 * r[e].x - x1 * r[e].y;
+                                fa[(2 * e + 1) % VEC] = x0 * r[e].y + x1 * r[e].x;
                             }
-                            if (in)
-                                ok = 2;
-                            else if (lane == 0)
-                                dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
+                        } else {
+                            unpack<T, VEC>(b[i], fb);
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) {
+                                const float x0 = fa[e], x1 = fb[e];
+                                fa[e] = x0 * r[e % NP].x - x1 * r[e % NP].y;
+                                fb[e] = x0 * r[e % NP].y + x1 * r[e % NP].x;
+                            }
+                            b[i] = repack<T, VEC>(fb);
                         }
+                        a[i] = repack<T, VEC>(fa);
                     }
-                    if (lane == 0) {
-                        row_ok[i] = ok;
-                        row_off[i] = off;
-                    }
-                }
-            } else if (threadIdx.x < TT) {
-                row_ok[threadIdx.x] = t0 + threadIdx.x < p.T ? 1 : 0;
-            }
-            for (int w = threadIdx.x; w < TT * p.n_pairs; w += blockDim.x) {
-                const int i = w / p.n_pairs, pr = w - i * p.n_pairs;
-                if (t0 + i < p.T) {
-                    const long long pos = p.pos[(int64_t)p.axis[pr] * p.T + t0 + i];
-                    const unsigned long long turn = (unsigned long long)pos * p.turns[pr];
-                    // the upper half as a signed number of 2^-31 half turns
-                    float s, c;
-                    sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
-                    cs[w] = make_float2(c, p.inverse ? -s : s);
+                    T *yh = y + (h + i * step + hh) * hs;
+                    *reinterpret_cast<V *>(yh + off0) = a[i];
+                    if (off1 >= 0) *reinterpret_cast<V *>(yh + off1) = b[i];
                 }
             }
-            __syncthreads();
-        }
-        if (!have) break;
-        T *y0 = static_cast<T *>(job.y) + (job.paged ? (int64_t)hl * p.head_stride : (int64_t)hl * p.d);
-        const bool turn = rot && job.rotate;
-        if (job.x == job.y && !turn) continue;  // in place and passed through
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            if (row_ok[i] < (job.paged ? 2 : 1)) continue;
-            T *y = y0 + (job.paged ? (int64_t)row_off[i] : (t0 + i) * job.y_stride);
-            if (turn) {
-                const float2 *t = cs + i * p.n_pairs + pb;
-                float fa[VEC], fb[VEC];
-                unpack<T, VEC>(a[i], fa);
-                if (VEC > 1 && ADJ) {
-#pragma unroll
-                    for (int e = 0; e + 1 < VEC; e += 2) {
-                        const float2 r = t[e / 2];
-                        const float x0 = fa[e], x1 = fa[e + 1];
-                        fa[e] = x0 * r.x - x1 * r.y;
-                        fa[e + 1] = x0 * r.y + x1 * r.x;
-                    }
-                } else {
-                    unpack<T, VEC>(b[i], fb);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float2 r = t[e];
-                        const float x0 = fa[e], x1 = fb[e];
-                        fa[e] = x0 * r.x - x1 * r.y;
-                        fb[e] = x0 * r.y + x1 * r.x;
-                    }
-                    b[i] = repack<T, VEC>(fb);
-                }
-                a[i] = repack<T, VEC>(fa);
-            }
-            *reinterpret_cast<V *>(y + off0) = a[i];
-            if (off1 >= 0) *reinterpret_cast<V *>(y + off1) = b[i];
         }
     }
 }
 
 template <typename T, int VEC, bool ADJ>
-cudaError_t launch_tt(const RopeParams &p, int threads, int tt, cudaStream_t st) {
-    const size_t smem = (size_t)tt * p.n_pairs * sizeof(float2);
-    const unsigned grid = (unsigned)((p.T + tt - 1) / tt);
-    if (tt == 4)
-        rope_kernel<T, VEC, ADJ, 4><<<grid, threads, smem, st>>>(p);
-    else
-        rope_kernel<T, VEC, ADJ, 1><<<grid, threads, smem, st>>>(p);
+cudaError_t launch_warps(const RopeParams &p, cudaStream_t st) {
+    const size_t smem = (size_t)kRopeWarps * p.n_pairs * sizeof(float2);
+    const int64_t blocks = (p.T * p.split + kRopeWarps - 1) / kRopeWarps;
+    rope_kernel<T, VEC, ADJ><<<(unsigned)blocks, kRopeWarps * 32, smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -242,17 +243,15 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
-    const int trips = (p.total_heads * p.units + 639) / 640;
-    p.heads_per_block = std::max(1, (p.total_heads + trips - 1) / trips);
-    const int threads = std::min(1024, (p.units * p.heads_per_block + 31) / 32 * 32);
-    const int tt = p.T >= 1216 ? 4 : 1;
+    // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
+    const int groups = p.units > 32 ? p.total_heads : (p.total_heads + 32 / p.units - 1) / (32 / p.units);
+    p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));
     if (dtype == RA_FP32) {
-        if (!fast) return launch_tt<float, 1, false>(p, threads, tt, st);
-        return adj ? launch_tt<float, 4, true>(p, threads, tt, st) : launch_tt<float, 4, false>(p, threads, tt, st);
+        if (!fast) return launch_warps<float, 1, false>(p, st);
+        return adj ? launch_warps<float, 4, true>(p, st) : launch_warps<float, 4, false>(p, st);
     }
-    if (!fast) return launch_tt<__nv_bfloat16, 1, false>(p, threads, tt, st);
-    return adj ? launch_tt<__nv_bfloat16, 8, true>(p, threads, tt, st)
-               : launch_tt<__nv_bfloat16, 8, false>(p, threads, tt, st);
+    if (!fast) return launch_warps<__nv_bfloat16, 1, false>(p, st);
+    return adj ? launch_warps<__nv_bfloat16, 8, true>(p, st) : launch_warps<__nv_bfloat16, 8, false>(p, st);
 }
 
 }  // namespace ra
