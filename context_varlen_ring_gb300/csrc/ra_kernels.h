@@ -249,18 +249,20 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st);
 // evenly.  What CTA c computes of a unit whose rows start at partial row
 // `base` goes to partial rows base + rt * c on: along the line units and CTAs
 // only grow, and no unit has more than rt partial rows, so these never meet.
-struct PagedSeg {
+struct alignas(16) PagedSeg {
     int tok0, n, len, w;               // first query token, query tokens, keys, key tiles
+    long long W0, R0;                  // tiles and partial rows ahead of it
 };
-struct PagedHdr {
-    long long W[2], per[2];            // tiles in all, tiles a CTA
-    int err, pad[7];
+struct PagedHdr {                      // of each family
+    long long W, per;                  // tiles in all, tiles a CTA
+    int err, pad[3];
 };
 struct PagedFamily {
     int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
     int halves;                        // units of at most rt / 2 rows: two partials a row, of alternate key tiles
+    PagedHdr *hdr;
     PagedSeg *seg;                     // [S]
-    long long *cumW, *cumR;            // [S + 1] tiles, [S] partial rows ahead of each segment
+    int *start;                        // [n] the segment in which each CTA's run begins
     const int32_t *table;
     int64_t width;
     float *acc, *ml;                   // [partial rows][d], [partial rows][2]: sum p v; running maximum (log2), sum p
@@ -274,7 +276,6 @@ struct PagedArgs {
     int page_size, B, n_groups, causal;
     const int32_t *cu, *kv_lens, *prefix_lens, *groups;
     float scale_log2;
-    PagedHdr *hdr;
     PagedFamily f[2];
     void *out;
     int out_dtype;

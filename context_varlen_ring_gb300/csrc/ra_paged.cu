@@ -30,6 +30,7 @@ using namespace dev;
 
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 512;
+constexpr int kPlanHeld = 2048;  // segments whose places are searched in shared memory
 
 struct UW {
     long long u, w;  // partial rows, key tiles
@@ -64,64 +65,74 @@ __device__ __forceinline__ UW block_scan(UW v, UW *warp_sum, UW &total) {
     return UW{before.u + x.u - v.u, before.w + x.w - v.w};
 }
 
-// One block: checks the segment arrays, and writes each family's segments,
-// the running counts of partial rows and tiles, and the tiles a CTA.
+// A block per family: checks its segment arrays, and writes its segments with
+// the tiles and partial rows ahead of each, the tiles a CTA, and the segment
+// in which each CTA's run begins.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedArgs a) {
     __shared__ UW warp_sum[kPlanThreads / 32];
+    __shared__ long long ahead[kPlanHeld];
+    const int fi = blockIdx.x;
+    const PagedFamily &f = a.f[fi];
     pdl_launch();
     int bad = 0;
-    for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
-        const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.kv_lens[b];
-        bad |= c0 < 0 || c1 < c0 || c1 > a.T || len < 0 || len > a.f[0].width * a.page_size;
-    }
-    for (int g = threadIdx.x; g < a.n_groups; g += kPlanThreads) {
-        const int g0 = a.groups[g], g1 = a.groups[g + 1], len = a.prefix_lens[g];
-        bad |= g0 < 0 || g1 < g0 || g1 > a.B || len < 0 || len > a.f[1].width * a.page_size;
+    UW base{0, 0};
+    for (int s0 = 0; s0 < f.S; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        UW v{0, 0};
+        PagedSeg g{};
+        if (s < f.S) {
+            const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
+            const int len = fi ? a.prefix_lens[s] : a.kv_lens[s];
+            int c0 = 0, c1 = 0;
+            bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size;
+            if (fine) {
+                c0 = a.cu[b0];
+                c1 = a.cu[b1];
+                fine = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+            }
+            if (!fine) {
+                bad = 1;
+                c0 = c1 = 0;
+            }
+            g.tok0 = c0;
+            g.n = c1 - c0;
+            g.len = len;
+            g.w = g.n > 0 ? (len + f.kt - 1) / f.kt : 0;
+            const long long R = (long long)g.n * a.G, full = R / f.rt;
+            v.u = a.Hkv * (full * f.rt + paged_alloc(f, (int)(R - full * f.rt)));
+            v.w = (R + f.rt - 1) / f.rt * a.Hkv * g.w;
+        }
+        UW total;
+        const UW at = block_scan(v, warp_sum, total);
+        if (s < f.S) {
+            g.W0 = base.w + at.w;
+            g.R0 = base.u + at.u;
+            f.seg[s] = g;
+            if (s < kPlanHeld) ahead[s] = g.W0;
+        }
+        base.u += total.u;
+        base.w += total.w;
     }
     bad = __syncthreads_or(bad);
-    if (bad) {
-        if (threadIdx.x == 0) {
-            record_status(a.status, RA_ERR_DEVICE_BOUNDS);
-            a.hdr->W[0] = a.hdr->W[1] = 0;
-            a.hdr->per[0] = a.hdr->per[1] = 1;
-            a.hdr->err = 1;
-        }
-        return;
+    const long long W = bad ? 0 : base.w, per = max(1ll, (W + f.n - 1) / f.n);
+    if (threadIdx.x == 0) {
+        if (bad) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+        f.hdr->W = W;
+        f.hdr->per = per;
+        f.hdr->err = bad;
     }
-    for (int fi = 0; fi < 2; ++fi) {
-        const PagedFamily &f = a.f[fi];
-        UW base{0, 0};
-        for (int s0 = 0; s0 < f.S; s0 += kPlanThreads) {
-            const int s = s0 + threadIdx.x;
-            UW v{0, 0};
-            if (s < f.S) {
-                const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
-                PagedSeg g;
-                g.tok0 = a.cu[b0];
-                g.n = a.cu[b1] - g.tok0;
-                g.len = fi ? a.prefix_lens[s] : a.kv_lens[s];
-                g.w = g.n > 0 ? (g.len + f.kt - 1) / f.kt : 0;
-                f.seg[s] = g;
-                const long long R = (long long)g.n * a.G, full = R / f.rt;
-                v.u = a.Hkv * (full * f.rt + paged_alloc(f, (int)(R - full * f.rt)));
-                v.w = (R + f.rt - 1) / f.rt * a.Hkv * g.w;
-            }
-            UW total;
-            const UW at = block_scan(v, warp_sum, total);
-            if (s < f.S) {
-                f.cumR[s] = base.u + at.u;
-                f.cumW[s] = base.w + at.w;
-            }
-            base.u += total.u;
-            base.w += total.w;
+    // CTA c begins at place c * per: in the last segment that begins there or earlier and has tiles behind it
+    for (int c = threadIdx.x; c < f.n && c * per < W; c += kPlanThreads) {
+        int lo = 0, hi = f.S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((mid < kPlanHeld ? ahead[mid] : f.seg[mid].W0) <= c * per)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        if (threadIdx.x == 0) {
-            f.cumW[f.S] = base.w;
-            a.hdr->W[fi] = base.w;
-            a.hdr->per[fi] = max(1ll, (base.w + f.n - 1) / f.n);
-        }
+        f.start[c] = lo;  // (segments without tiles share their place with the one behind them: the last is it)
     }
-    if (threadIdx.x == 0) a.hdr->err = 0;
 }
 
 // ------------------------------------------------------------------ SIMT
@@ -159,16 +170,13 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
     const PagedFamily &f = a.f[fi];
     pdl_wait();
     pdl_launch();
-    const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
     const int cta = blockIdx.x;
-    long long x = cta * per;
-    const long long x1 = min(W, x + per);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x < x1 ? paged_find(f, x) : 0;
-    while (x < x1) {
-        while (f.cumW[s + 1] <= x) ++s;
-        const PagedSeg g = f.seg[s];
-        const PagedUnit u = paged_unit(a, f, g, s, x, x1);
+    PagedWalk walk = paged_begin(f);
+    while (walk.x < walk.x1) {
+        const PagedUnit u = paged_unit(a, f, walk);
+        const PagedSeg &g = walk.g;
+        const int s = walk.s;
         const int R = g.n * a.G, r0 = u.r0;
         __syncthreads();  // the last unit's readers are done with Q
         for (int i = threadIdx.x; i < RT * (D / 4); i += WARPS * 32) {
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
                 if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m[r], sum);
             }
         }
-        x += u.t1 - u.t0;
+        walk.x += u.t1 - u.t0;
     }
 }
 
@@ -304,30 +312,23 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t
 }
 
 // ------------------------------------------------------------------ join
-// The partials of a token and KV head in a family: cnt of them a row, the
-// i-th of query head g at partial row  at + g + (i >> two) * rt + (i & two) * second.
+// The partials of a token and query head in a family: cnt of them, the i-th at
+// partial row  at + (i >> two) * rt + (i & two) * second.
 struct Parts {
-    const float *acc, *ml;
     long long at;
-    int cnt, rt, two, second;
-    __device__ __forceinline__ long long row(int i, int g) const {
-        return at + g + (long long)(i >> two) * rt + (i & two) * second;
-    }
+    int cnt, two, second;
 };
 
-// G rows may straddle two units (rows a unit need not be a multiple of G), so
-// the place is found per query head g.
-__device__ __forceinline__ Parts find_parts(const PagedArgs &a, int fi, int s, int64_t t, int h, int g) {
-    const PagedFamily &f = a.f[fi];
-    Parts p{f.acc, f.ml, 0, 0, f.rt, 0, 0};
+__device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, int s, int64_t t, int h, int g) {
+    Parts p{0, 0, 0, 0};
     if (s < 0) return p;
-    const PagedSeg sg = f.seg[s];
+    const PagedSeg sg = paged_seg(f, s);
     if (sg.w == 0) return p;
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    const long long x = f.cumW[s] + (long long)(rtile * a.Hkv + h) * sg.w, per = a.hdr->per[fi];
+    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * sg.w, per = __ldcg(&f.hdr->per);
     const int c0 = (int)(x / per), c1 = (int)((x + sg.w - 1) / per);
-    p.at = f.cumR[s] + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt - g;
+    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
     p.two = alloc > rows ? 1 : 0;
     p.second = rows;
     p.cnt = (c1 - c0 + 1) << p.two;
@@ -339,31 +340,34 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, int fi, int s, i
 // maximum M, the weights 2^(m - M), the weighted sums.  Own keys come first,
 // then the prefix; warps' sums are added in order, so the result does not
 // depend on timing.  Latency bound (a chain of dependent loads: segment,
-// place, maxima, sums), so the segments are searched once a block, ahead of the
-// wait for the attention kernels, and few blocks get more warps.
-template <typename TOut, int WARPS>
+// place, maxima, sums): the segments are searched once a block, ahead of the
+// wait for the attention kernels; a lane finds one partial's place and weight
+// and hands it to its warp, which keeps the loop that all the bytes go
+// through short; few blocks get more warps.
+template <typename TOut, int WARPS, int NV>
 __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ float sum[WARPS][256];
+    __shared__ float4 sum[WARPS][32 * NV];
     __shared__ int seg[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x / a.Hkv;
     const int h = blockIdx.x % a.Hkv;
     if (warp == 0) {
-        const int b = segment_of(a.cu + 1, a.B, t);
-        const bool live = b < a.B && t >= a.cu[b];  // not behind the last sequence, nor ahead of the first
+        // one token a sequence, no sequence without: token t is sequence t's
+        int b = t < a.B && a.cu[t] <= t && t < a.cu[t + 1] ? (int)t : segment_of(a.cu + 1, a.B, t);
+        if (b >= a.B || t < a.cu[b]) b = -1;  // behind the last sequence, or ahead of the first
         int g = -1;
-        if (live && a.n_groups > 0) {
+        if (b >= 0 && a.n_groups > 0) {
             g = segment_of(a.groups + 1, a.n_groups, b);
             if (g >= a.n_groups || b < a.groups[g]) g = -1;  // a sequence outside every group
         }
         if (lane == 0) {
-            seg[0] = live ? b : -1;
+            seg[0] = b;
             seg[1] = g;
         }
     }
     __syncthreads();
     pdl_wait();
-    if (seg[0] < 0 || a.hdr->err) return;
+    if (seg[0] < 0 || __ldcg(&a.f[0].hdr->err) || (a.n_groups > 0 && __ldcg(&a.f[1].hdr->err))) return;
     int wpr = 1;  // warps a row: a power of two, heads in turn where there are more
     while (wpr * 2 * a.G <= WARPS) wpr *= 2;
     const int sub = warp % wpr, at_once = WARPS / wpr, d4 = a.d / 4;
@@ -371,64 +375,82 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
         const int g = g0 + warp / wpr;
         const bool live = g < a.G;
         float M = -INFINITY, L = 0.f;
-        float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        float4 o[NV];
+#pragma unroll
+        for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live) {
-            const Parts p0 = find_parts(a, 0, seg[0], t, h, g), p1 = find_parts(a, 1, seg[1], t, h, g);
+            const Parts p0 = find_parts(a, a.f[0], seg[0], t, h, g), p1 = find_parts(a, a.f[1], seg[1], t, h, g);
             const int cnt = p0.cnt + p1.cnt;
-            auto ml = [&](int i) {
-                const float *p = i < p0.cnt ? p0.ml + p0.row(i, g) * 2 : p1.ml + p1.row(i - p0.cnt, g) * 2;
-                return *reinterpret_cast<const float2 *>(p);
-            };
-            float2 mine = make_float2(-INFINITY, 0.f);
-            if (lane < cnt) mine = ml(lane);
-            M = mine.x;
-            for (int i = lane + 32; i < cnt; i += 32) M = fmaxf(M, ml(i).x);
+            // the maximum is carried along, as in the attention itself: 32 partials a trip
+#pragma unroll 1
+            for (int i0 = 0; i0 < cnt; i0 += 32) {
+                int i = i0 + lane;
+                const int fi = i < p0.cnt ? 0 : 1;
+                const Parts &p = fi ? p1 : p0;
+                if (fi) i -= p0.cnt;
+                const float *src = nullptr;
+                float2 v = make_float2(-INFINITY, 0.f);
+                if (i < p.cnt) {
+                    const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
+                    v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
+                    src = a.f[fi].acc + row * a.d;
+                }
+                float Mn = v.x;
 #pragma unroll
-            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-            if (M != -INFINITY) {
-                for (int i0 = 0; i0 < cnt; i0 += 32) {
-                    if (i0 > 0) mine = i0 + lane < cnt ? ml(i0 + lane) : make_float2(-INFINITY, 0.f);
-                    const float w = exp2f(mine.x - M);
-                    L += w * mine.y;
-                    const int most = min(32, cnt - i0);
+                for (int s = 16; s; s >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, s));
+                Mn = fmaxf(M, Mn);
+                if (Mn == -INFINITY) continue;
+                const float alpha = exp2f(M - Mn), w = exp2f(v.x - Mn);
+                M = Mn;
+                L = L * alpha + w * v.y;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    o[e].x *= alpha;
+                    o[e].y *= alpha;
+                    o[e].z *= alpha;
+                    o[e].w *= alpha;
+                }
+                const int most = min(32, cnt - i0);
 #pragma unroll 4
-                    for (int i = sub; i < most; i += wpr) {
-                        const float wi = __shfl_sync(0xffffffffu, w, i);
-                        const int k = i0 + i;
-                        const float4 *p = reinterpret_cast<const float4 *>(
-                            k < p0.cnt ? p0.acc + p0.row(k, g) * a.d : p1.acc + p1.row(k - p0.cnt, g) * a.d);
-                        // (a partial without weight may never have been written)
+                for (int k = sub; k < most; k += wpr) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k);
+                    const float4 *q = reinterpret_cast<const float4 *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+                    // (a partial without weight may never have been written)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (wi != 0.f && lane + 32 * e < d4) {
-                                const float4 v = p[lane + 32 * e];
-                                o[e].x = fmaf(wi, v.x, o[e].x);
-                                o[e].y = fmaf(wi, v.y, o[e].y);
-                                o[e].z = fmaf(wi, v.z, o[e].z);
-                                o[e].w = fmaf(wi, v.w, o[e].w);
-                            }
+                    for (int e = 0; e < NV; ++e) {
+                        if (wk != 0.f && lane + 32 * e < d4) {
+                            const float4 x = __ldcg(q + lane + 32 * e);
+                            o[e].x = fmaf(wk, x.x, o[e].x);
+                            o[e].y = fmaf(wk, x.y, o[e].y);
+                            o[e].z = fmaf(wk, x.z, o[e].z);
+                            o[e].w = fmaf(wk, x.w, o[e].w);
                         }
                     }
                 }
-#pragma unroll
-                for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
             }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
         }
         if (wpr > 1) {  // (then every head has its warps at once: one trip of the outer loop)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) *reinterpret_cast<float4 *>(&sum[warp][(lane + 32 * e) * 4]) = o[e];
+            for (int e = 0; e < NV; ++e) sum[warp][lane + 32 * e] = o[e];
             __syncthreads();
         }
         if (!live) continue;
         const float inv = L > 0.f ? 1.f / L : 0.f;
         const int head = h * a.G + g;
         TOut *out = static_cast<TOut *>(a.out) + (t * a.Hq + head) * a.d;
-        for (int c = (sub * 32 + lane) * 4; c < a.d; c += wpr * 128) {
-            float4 v = c < 128 ? o[0] : o[1];
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            const int c = lane + 32 * e;
+            if (c >= d4 || (wpr > 1 && sub != e)) continue;  // (of several warps, warp e of the row writes vector e)
+            float4 v = o[e];
             if (wpr > 1) {
                 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
                 for (int i = 0; i < wpr; ++i) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sum[warp - sub + i][c]);
+                    const float4 x = sum[warp - sub + i][c];
                     v.x += x.x;
                     v.y += x.y;
                     v.z += x.z;
@@ -436,12 +458,12 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
                 }
             }
             if constexpr (sizeof(TOut) == 4) {
-                *reinterpret_cast<float4 *>(out + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                *reinterpret_cast<float4 *>(out + c * 4) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             } else {
                 uint2 pk;
                 pk.x = pack_bf16x2(v.x * inv, v.y * inv);
                 pk.y = pack_bf16x2(v.z * inv, v.w * inv);
-                *reinterpret_cast<uint2 *>(out + c) = pk;
+                *reinterpret_cast<uint2 *>(out + c * 4) = pk;
             }
         }
         if (sub == 0 && lane == 0)
@@ -449,10 +471,19 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
     }
 }
 
+template <typename TOut>
+cudaError_t combine_as(const PagedArgs &a, cudaStream_t st) {
+    const int64_t blocks = a.T * a.Hkv;  // < 2^31
+    auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, (unsigned)blocks, warps * 32, 0, st, a); };
+    const bool few = blocks <= 2 * paged_sms();
+    if (a.d <= 128) return few ? go(paged_combine_kernel<TOut, 16, 1>, 16) : go(paged_combine_kernel<TOut, 8, 1>, 8);
+    return few ? go(paged_combine_kernel<TOut, 16, 2>, 16) : go(paged_combine_kernel<TOut, 8, 2>, 8);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st) {
-    paged_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    paged_plan_kernel<<<a.n_groups > 0 ? 2 : 1, kPlanThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -485,12 +516,7 @@ cudaError_t launch_paged_simt(const PagedArgs &a, int fi, cudaStream_t st) {
 }
 
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {
-    const int64_t blocks = a.T * a.Hkv;  // < 2^31
-    auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, (unsigned)blocks, warps * 32, 0, st, a); };
-    const bool few = blocks <= 2 * paged_sms();
-    if (a.out_dtype == RA_FP32)
-        return few ? go(paged_combine_kernel<float, 16>, 16) : go(paged_combine_kernel<float, 8>, 8);
-    return few ? go(paged_combine_kernel<__nv_bfloat16, 16>, 16) : go(paged_combine_kernel<__nv_bfloat16, 8>, 8);
+    return a.out_dtype == RA_FP32 ? combine_as<float>(a, st) : combine_as<__nv_bfloat16>(a, st);
 }
 
 }  // namespace ra

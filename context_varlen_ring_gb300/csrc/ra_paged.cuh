@@ -1,5 +1,5 @@
 // ra_paged.cuh -- what the paged-attention kernels share on the device: the
-// place of a CTA's run of key tiles, the keys a row sees, and the page table.
+// walk of a CTA along its run of key tiles, the keys a row sees, and the page table.
 #pragma once
 
 #include <utility>
@@ -9,19 +9,6 @@
 
 namespace ra {
 namespace dev {
-
-// The segment whose tiles hold place x of the line (x < cumW[S]).
-__device__ __forceinline__ int paged_find(const PagedFamily &f, long long x) {
-    int lo = 0, hi = f.S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (f.cumW[mid + 1] <= x)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
 
 // Partial rows of a tile of `rows` query rows.
 __device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
@@ -34,20 +21,53 @@ struct PagedUnit {
     long long base;      // first partial row (of CTA 0)
 };
 
-// The unit at place x of segment s, and the CTA's part of it up to place x1.
-// Row tiles are outermost, so CTAs an equal share of the line apart read the
-// same keys for different rows at about the same time (from L2).
-__device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g, int s,
-                                                long long x, long long x1) {
-    const long long rel = x - f.cumW[s];
-    const int lu = (int)(rel / g.w), rtile = lu / a.Hkv;
+// A CTA's run of the line, and its place in it: the segment and the unit.
+struct PagedWalk {
+    long long x, x1;
+    int s;
+    PagedSeg g;
+};
+
+// The run of this CTA (x == x1: none).  The plan's results are read past L1,
+// which may hold an earlier call's.
+__device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
+    const int4 *p = reinterpret_cast<const int4 *>(f.seg + s);
+    const int4 a = __ldcg(p), b = __ldcg(p + 1);
+    PagedSeg g;
+    g.tok0 = a.x;
+    g.n = a.y;
+    g.len = a.z;
+    g.w = a.w;
+    g.W0 = ((long long)b.y << 32) | (unsigned)b.x;
+    g.R0 = ((long long)b.w << 32) | (unsigned)b.z;
+    return g;
+}
+__device__ __forceinline__ PagedWalk paged_begin(const PagedFamily &f) {
+    const long long per = __ldcg(&f.hdr->per), W = __ldcg(&f.hdr->W);
+    PagedWalk k;
+    k.s = __ldcg(f.start + blockIdx.x);  // (not meant for a CTA without a run)
+    k.x = blockIdx.x * per;
+    k.x1 = min(W, k.x + per);
+    if (k.x < k.x1) k.g = paged_seg(f, k.s);
+    return k;
+}
+
+// The unit at the walk's place (in the next segment with tiles, where the last
+// one's are done), and the CTA's part of it.  Row tiles are outermost in a
+// segment, so CTAs an equal share of the line apart read the same keys for
+// different rows at about the same time (from L2).
+__device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedFamily &f, PagedWalk &k) {
+    auto tiles = [&]() { return (long long)((k.g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * k.g.w; };
+    while (k.g.W0 + tiles() <= k.x) k.g = paged_seg(f, ++k.s);
+    const long long rel = k.x - k.g.W0;
+    const int lu = (int)(rel / k.g.w), rtile = lu / a.Hkv;
     PagedUnit u;
-    u.t0 = (int)(rel - (long long)lu * g.w);
-    u.t1 = (int)min((long long)g.w, u.t0 + (x1 - x));
+    u.t0 = (int)(rel - (long long)lu * k.g.w);
+    u.t1 = (int)min((long long)k.g.w, u.t0 + (k.x1 - k.x));
     u.h = lu - rtile * a.Hkv;
     u.r0 = rtile * f.rt;
-    u.rows = min(f.rt, g.n * a.G - u.r0);
-    u.base = f.cumR[s] + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
+    u.rows = min(f.rt, k.g.n * a.G - u.r0);
+    u.base = k.g.R0 + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
     return u;
 }
 

@@ -176,15 +176,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
     const PagedFamily &f = a.f[fi];
     pdl_wait();
     pdl_launch();
-    const long long per = a.hdr->per[fi], W = a.hdr->W[fi];
-    long long x = blockIdx.x * per;
-    const long long x1 = min(W, x + per);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x < x1 ? paged_find(f, x) : 0;
-    while (x < x1) {
-        while (f.cumW[s + 1] <= x) ++s;
-        const PagedSeg g = f.seg[s];
-        const PagedUnit u = paged_unit(a, f, g, s, x, x1);
+    PagedWalk walk = paged_begin(f);
+    while (walk.x < walk.x1) {
+        const PagedUnit u = paged_unit(a, f, walk);
+        const PagedSeg &g = walk.g;
+        const int s = walk.s;
         const int R = g.n * a.G, r0 = u.r0 + (WIDE ? warp * 16 : 0);
         auto issue = [&](int t) {  // this warp's 16 keys of tile t
             const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage + warp * kBlk;
@@ -300,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
             }
             __syncthreads();  // the stages belong to the next unit
         }
-        x += u.t1 - u.t0;
+        walk.x += u.t1 - u.t0;
     }
 }
 

@@ -136,20 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     const WaitCtl wc{abort_flag, a.status, p.budget_ns};
     pdl_wait();
     pdl_launch();
-    const long long per = a.hdr->per[p.fi];
-    const long long x0 = blockIdx.x * per, x1 = min(a.hdr->W[p.fi], x0 + per);
 
     // The CTA's units in order, the same for every role.
-    auto first = [&]() { return x0 < x1 ? paged_find(f, x0) : 0; };
-    auto walk_at = [&](long long x, int s) {
+    auto next_unit = [&](PagedWalk &k) {
         Walk w;
-        while (f.cumW[s + 1] <= x) ++s;
-        w.s = s;
-        w.g = f.seg[s];
-        w.u = paged_unit(a, f, w.g, s, x, x1);
+        w.u = paged_unit(a, f, k);
+        w.g = k.g;
+        w.s = k.s;
         w.pair = w.u.rows > 128;
         const int sees = paged_limit(a, w.g, p.fi, w.u.r0 + w.u.rows - 1);
         w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
+        k.x += w.u.t1 - w.u.t0;
         return w;
     };
 
@@ -166,9 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tma_prefetch_desc(&p.tmV);
             }
             const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
-            for (long long x = x0, s = first(); x < x1 && ok;) {
-                const Walk w = walk_at(x, (int)s);
-                s = w.s;
+            for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
+                const Walk w = next_unit(walk);
                 const int tok = w.g.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
                 if (lane == 0) {
                     if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1u, wc);
@@ -224,7 +220,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     if (ok) load(&p.tmV, pa0, ra0);
                     if (two && ok) load(&p.tmV, pb0, rb0);
                 }
-                x += w.u.t1 - w.u.t0;
             }
             if (lane == 0) {
                 // the last copies must have landed before the CTA may exit
@@ -249,9 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 return kvs + (i % kSlots) * kTile;
             };
             auto empty = [&](uint32_t i) { tc_commit_w(kv_empty + i % kSlots); };
-            for (long long x = x0, s = first(); x < x1 && ok;) {
-                const Walk w = walk_at(x, (int)s);
-                s = w.s;
+            for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
+                const Walk w = next_unit(walk);
                 ok = mbar_wait_warp(q_full, nu & 1u, wc);
                 ++nu;
                 tc_fence_after();
@@ -271,8 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 };
                 if (w.u.t0 >= w.tend || !ok) {
                     tc_commit_w(q_empty);
-                    x += w.u.t1 - w.u.t0;
-                    continue;
+                        continue;
                 }
                 // S of the first step
                 {
@@ -343,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     }
                     n += two ? 4u : 2u;
                 }
-                x += w.u.t1 - w.u.t0;
             }
             // every MMA issued must have completed before TMEM is released
             tc_commit_w(mma_done);
@@ -361,9 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint32_t tO = tmem + lane_base + 256u + 128u * k;
         uint32_t nd_all = 0;  // S tiles of this group (all units)
         bool ok = true;
-        for (long long x = x0, s = first(); x < x1 && ok;) {
-            const Walk w = walk_at(x, (int)s);
-            s = w.s;
+        for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
+            const Walk w = next_unit(walk);
             const int by = w.pair ? 1 : 2;
             const int row = (w.pair ? 128 * k : 0) + m;  // of the unit
             const bool valid = row < w.u.rows;
@@ -458,18 +449,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     uint32_t v[32];
                     tmem_ld32(tO + 32u * ch, v);
                     if (valid) {
-                        float4 *dst = reinterpret_cast<float4 *>(f.acc + at * 128 + 32 * ch);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t o8[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o8[e] = v[8 * i + e];
+                            st_global_v8(f.acc + at * 128 + 32 * ch + 8 * i, o8);
+                        }
                     }
                 }
                 if (valid) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m_run, l_run);
             }
             // (O is next written by a later unit's first PV, which waits for this
             // thread's next P: the readout above comes first in program order)
-            x += w.u.t1 - w.u.t0;
         }
     }
     tc_fence_before();

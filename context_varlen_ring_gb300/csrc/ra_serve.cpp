@@ -94,7 +94,7 @@ ra_status check_cache(const ra_paged_kv *c) {
 // that a call of these shapes may choose (the choice also goes by the page
 // size and the scale, which the size query does not know).
 struct PagedLayout {
-    size_t o_hdr, o_seg[2], o_cumW[2], o_cumR[2], o_acc[2], o_ml[2], bytes;
+    size_t o_hdr[2], o_seg[2], o_start[2], o_acc[2], o_ml[2], bytes;
 };
 
 // A family whose units hold at most 16 rows is left to the warp-level kernel.
@@ -110,12 +110,11 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
         at = align_up(at + n, 256);
         return o;
     };
-    L.o_hdr = take(sizeof(PagedHdr));
     for (int f = 0; f < 2; ++f) {
         const int64_t S = f ? n_groups : B;
+        L.o_hdr[f] = take(sizeof(PagedHdr));
         L.o_seg[f] = take((size_t)S * sizeof(PagedSeg));
-        L.o_cumW[f] = take((size_t)(S + 1) * 8);
-        L.o_cumR[f] = take((size_t)(S + 1) * 8);
+        L.o_start[f] = take((size_t)kPagedMaxCtas * 4);
         // the rows themselves (twice where units are halved), and one unit more a CTA
         const bool few = paged_few(f, T, G, max_q_len), wide = !few && dtype == RA_BF16 && d == 128;
         int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (few ? 16 : 64) : 0;
@@ -270,7 +269,6 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.prefix_lens = prefix_lens;
     a.groups = prefix_groups;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr);
     enum { kSimt, kMma, kWide } kind[2];
     PagedMaps maps;
     const bool wide = (!paged_few(0, T, a.G, max_q_len) || (n_groups > 0 && !paged_few(1, T, a.G, max_q_len))) &&
@@ -289,8 +287,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
                   : kind[f] == kMma ? paged_mma_ctas(F.rt, d)
                                     : paged_simt_ctas(F.rt, d);
         F.seg = reinterpret_cast<PagedSeg *>(ws + L.o_seg[f]);
-        F.cumW = reinterpret_cast<long long *>(ws + L.o_cumW[f]);
-        F.cumR = reinterpret_cast<long long *>(ws + L.o_cumR[f]);
+        F.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr[f]);
+        F.start = reinterpret_cast<int *>(ws + L.o_start[f]);
         F.table = f ? prefix_table : page_table;
         F.width = f ? prefix_width : table_width;
         F.acc = reinterpret_cast<float *>(ws + L.o_acc[f]);
