@@ -290,7 +290,7 @@ cudaError_t launch_paged_simt(const PagedArgs &a, int family, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st);
 int paged_simt_ctas(int rt, int d);    // CTAs of the SIMT kernel that the current device holds at once
 bool paged_mma_supported(int dtype, int d);
-int paged_mma_ctas(int rt, int d);
+int paged_mma_ctas(int rt, int d, int page_size);
 cudaError_t launch_paged_mma(const PagedArgs &a, int family, cudaStream_t st);
 int paged_sms();                       // SMs of the current device
 struct PagedMaps {

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         base.w += total.w;
     }
     bad = __syncthreads_or(bad);
-    const long long W = bad ? 0 : base.w, per = max(1ll, (W + f.n - 1) / f.n);
+    const long long W = bad ? 0 : base.w, per = max(1ll, paged_div(W + f.n - 1, f.n));
     if (threadIdx.x == 0) {
         if (bad) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
         f.hdr->W = W;
@@ -327,7 +327,7 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
     const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * sg.w, per = __ldcg(&f.hdr->per);
-    const int c0 = (int)(x / per), c1 = (int)((x + sg.w - 1) / per);
+    const int c0 = (int)paged_div(x, per), c1 = (int)paged_div(x + sg.w - 1, per);
     p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
     p.two = alloc > rows ? 1 : 0;
     p.second = rows;
@@ -341,13 +341,16 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
 // then the prefix; warps' sums are added in order, so the result does not
 // depend on timing.  Latency bound (a chain of dependent loads: segment,
 // place, maxima, sums): the segments are searched once a block, ahead of the
-// wait for the attention kernels; a lane finds one partial's place and weight
-// and hands it to its warp, which keeps the loop that all the bytes go
-// through short; few blocks get more warps.
+// wait for the attention kernels; the place of each head's partials is found
+// by one lane (by every warp, it cost more instructions than the sums: 15
+// instead of FIG us for 64 tokens of 22 partials a row); a lane finds one
+// partial's weight and hands it to its warp, which keeps the loop that all the
+// bytes go through short; few blocks get more warps.
 template <typename TOut, int WARPS, int NV>
 __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
     __shared__ float4 sum[WARPS][32 * NV];
     __shared__ int seg[2];
+    __shared__ Parts parts[WARPS][2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x / a.Hkv;
     const int h = blockIdx.x % a.Hkv;
@@ -372,6 +375,11 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
     while (wpr * 2 * a.G <= WARPS) wpr *= 2;
     const int sub = warp % wpr, at_once = WARPS / wpr, d4 = a.d / 4;
     for (int g0 = 0; g0 < a.G; g0 += at_once) {
+        if (g0 > 0) __syncthreads();  // the last heads' places have been read
+        if ((int)threadIdx.x < 2 * at_once && g0 + (int)threadIdx.x / 2 < a.G)
+            parts[threadIdx.x / 2][threadIdx.x & 1] =
+                find_parts(a, a.f[threadIdx.x & 1], seg[threadIdx.x & 1], t, h, g0 + threadIdx.x / 2);
+        __syncthreads();
         const int g = g0 + warp / wpr;
         const bool live = g < a.G;
         float M = -INFINITY, L = 0.f;
@@ -379,15 +387,14 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live) {
-            const Parts p0 = find_parts(a, a.f[0], seg[0], t, h, g), p1 = find_parts(a, a.f[1], seg[1], t, h, g);
-            const int cnt = p0.cnt + p1.cnt;
+            const int own = parts[warp / wpr][0].cnt, cnt = own + parts[warp / wpr][1].cnt;
             // the maximum is carried along, as in the attention itself: 32 partials a trip
 #pragma unroll 1
             for (int i0 = 0; i0 < cnt; i0 += 32) {
                 int i = i0 + lane;
-                const int fi = i < p0.cnt ? 0 : 1;
-                const Parts &p = fi ? p1 : p0;
-                if (fi) i -= p0.cnt;
+                const int fi = i < own ? 0 : 1;
+                const Parts &p = parts[warp / wpr][fi];
+                if (fi) i -= own;
                 const float *src = nullptr;
                 float2 v = make_float2(-INFINITY, 0.f);
                 if (i < p.cnt) {

@@ -10,6 +10,12 @@
 namespace ra {
 namespace dev {
 
+// x / y of non-negative numbers, in 32 bits wherever they fit (a 64-bit
+// division is some hundred instructions).
+__device__ __forceinline__ long long paged_div(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // Partial rows of a tile of `rows` query rows.
 __device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
     return f.halves && 2 * rows <= f.rt ? 2 * rows : rows;
@@ -60,7 +66,7 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedF
     auto tiles = [&]() { return (long long)((k.g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * k.g.w; };
     while (k.g.W0 + tiles() <= k.x) k.g = paged_seg(f, ++k.s);
     const long long rel = k.x - k.g.W0;
-    const int lu = (int)(rel / k.g.w), rtile = lu / a.Hkv;
+    const int lu = (int)paged_div(rel, k.g.w), rtile = lu / a.Hkv;
     PagedUnit u;
     u.t0 = (int)(rel - (long long)lu * k.g.w);
     u.t1 = (int)min((long long)k.g.w, u.t0 + (k.x1 - k.x));

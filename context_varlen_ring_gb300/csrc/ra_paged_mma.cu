@@ -62,31 +62,51 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 // Shared address of 16-byte chunk c of row r: chunks are exchanged by the
 // row's low bits, so that eight rows of one chunk fall into eight bank groups.
+// (Row bases are multiples of the row's bytes, so chunk 2 k + b of a row is
+// its chunk b's address with bits 5 and up exchanged by k.)
 template <int D>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int r, int c) {
     return base + (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
 }
 
-// Starts the copies of 16 key rows (K and V) from logical index kb on; rows
-// that are not there are filled with zeros, so whatever the cache holds
-// behind a sequence's end never meets the products.
-template <int D>
-__device__ __forceinline__ void issue16(const PagedArgs &a, const PagedFamily &f, int s, int len, int h, int kb,
-                                        uint32_t ks, uint32_t vs) {
-    constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows a warp instruction
+// Where 16 keys from logical index kb on lie: with whole blocks in a page
+// (page_size % 16 == 0) the first one's row, the same in every lane; else lane
+// i < 16 holds row i's.  -1: none.  Looked up one tile ahead of its use.
+template <bool WHOLE>
+__device__ __forceinline__ long long find16(const PagedArgs &a, const PagedFamily &f, int s, int len, int kb) {
+    if (WHOLE) return paged_row(a, f, s, len, kb);
     const int lane = threadIdx.x & 31;
-    long long off = -1;
-    if (lane < 16) off = paged_row(a, f, s, len, kb + lane);
-    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + h * a.head_stride;
-    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + h * a.head_stride;
-    const int c = lane % CPR;
+    return lane < 16 ? paged_row(a, f, s, len, kb + lane) : -1;
+}
+
+// Starts the copies of those 16 rows (K and V); rows that are not there are
+// filled with zeros, so whatever the cache holds behind a sequence's end never
+// meets the products.
+template <int D, bool WHOLE>
+__device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int live, int h, uint32_t ks, uint32_t vs) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows a warp instruction
+    const int lane = threadIdx.x & 31, c = lane % CPR, r0 = lane / CPR;
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + h * a.head_stride + c * 8;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + h * a.head_stride + c * 8;
+    if (WHOLE) {
+        if (off < 0) live = 0;
+        long long at = (off < 0 ? 0 : off) + r0 * a.token_stride;
 #pragma unroll
-    for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = i * RPI + lane / CPR;
-        const long long o = __shfl_sync(0xffffffffu, off, r);
-        const long long at = (o < 0 ? 0 : o) + c * 8;
-        cp16(chunk_at<D>(ks, r, c), k + at, o >= 0);
-        cp16(chunk_at<D>(vs, r, c), v + at, o >= 0);
+        for (int i = 0; i < 16 / RPI; ++i) {
+            const bool there = i * RPI + r0 < live;
+            const long long o = there ? at : 0;
+            cp16(chunk_at<D>(ks, i * RPI + r0, c), k + o, there);
+            cp16(chunk_at<D>(vs, i * RPI + r0, c), v + o, there);
+            at += RPI * a.token_stride;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+            const int r = i * RPI + r0;
+            const long long o = __shfl_sync(0xffffffffu, off, r);
+            cp16(chunk_at<D>(ks, r, c), k + (o < 0 ? 0 : o), o >= 0);
+            cp16(chunk_at<D>(vs, r, c), v + (o < 0 ? 0 : o), o >= 0);
+        }
     }
 }
 
@@ -105,10 +125,11 @@ template <int D>
 __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, int kb, bool masked, float scale_log2) {
     const int lane = threadIdx.x & 31, id = lane >> 3, l8 = lane & 7;
     float s[2][4] = {};
+    const uint32_t ka = chunk_at<D>(ks, (id >> 1) * 8 + l8, id & 1);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
-        ldsm4(chunk_at<D>(ks, (id >> 1) * 8 + l8, 2 * k + (id & 1)), b);
+        ldsm4(ka ^ (k << 5), b);
         mma16816(s[0], w.q[k], b[0], b[1]);
         mma16816(s[1], w.q[k], b[2], b[3]);
     }
@@ -152,10 +173,11 @@ __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, in
             p[2 * n + r] = pack_bf16x2(p0, p1);
         }
     }
+    const uint32_t va = chunk_at<D>(vs, (id & 1) * 8 + l8, id >> 1);
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
         uint32_t b[4];
-        ldsm4t(chunk_at<D>(vs, (id & 1) * 8 + l8, 2 * n + (id >> 1)), b);
+        ldsm4t(va ^ (n << 5), b);
         mma16816(w.o[2 * n], p, b[0], b[1]);
         mma16816(w.o[2 * n + 1], p, b[2], b[3]);
     }
@@ -166,67 +188,89 @@ constexpr size_t mma_smem() {
     return (size_t)kWarps * kStages * 2 * 16 * D * 2 + (WIDE ? 0 : kWarps * 16 * 2 * sizeof(float));
 }
 
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_constant__ PagedArgs a, int fi) {
+template <int D, bool WIDE, bool WHOLE>
+__global__ void __launch_bounds__(kWarps * 32, 3) paged_mma_kernel(const __grid_constant__ PagedArgs a, int fi) {
     constexpr int RT = WIDE ? 16 * kWarps : 16;
     constexpr uint32_t kBlk = 16 * D * 2;          // bytes of 16 rows
     constexpr uint32_t kStage = kWarps * 2 * kBlk;  // K blocks of the warps, then V blocks
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const PagedFamily &f = a.f[fi];
     pdl_wait();
     pdl_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PagedWalk walk = paged_begin(f);
-    while (walk.x < walk.x1) {
-        const PagedUnit u = paged_unit(a, f, walk);
-        const PagedSeg &g = walk.g;
-        const int s = walk.s;
-        const int R = g.n * a.G, r0 = u.r0 + (WIDE ? warp * 16 : 0);
-        auto issue = [&](int t) {  // this warp's 16 keys of tile t
-            const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage + warp * kBlk;
-            if (t < u.t1) issue16<D>(a, f, s, g.len, u.h, t * kKT + warp * 16, st, st + kWarps * kBlk);
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(u.t0 + i);
+    if (walk.x >= walk.x1) return;
+    int it = 0;                      // key tiles so far: tile i lies in stage i % kStages
+    // this warp's 16 keys of tile t of the walk's segment
+    auto find = [&](int t) { return find16<WHOLE>(a, f, walk.s, walk.g.len, t * kKT + warp * 16); };
+    auto issue = [&](long long off, int h, int t, int i) {
+        const uint32_t st = base + (uint32_t)i % kStages * kStage + warp * kBlk;
+        issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk);
+    };
+    PagedUnit u = paged_unit(a, f, walk);
+    issue(find(u.t0), u.h, u.t0, 0);
+    cp_commit();
+    long long ahead = u.t0 + 1 < u.t1 ? find(u.t0 + 1) : -1;  // the next tile's place, when it is of this unit
+    for (bool more = true; more;) {
         Rows<D> w;
+        int lo, hi;  // the warp's rows: the fewest and the most keys any of them sees
+        {
+            const PagedSeg &g = walk.g;
+            const int R = g.n * a.G, r0 = u.r0 + (WIDE ? warp * 16 : 0);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = r0 + (lane >> 2) + 8 * r;
-            // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
-            w.lim[r] = row < R ? paged_limit(a, g, fi, row) : g.len;
-            w.m[r] = -INFINITY;
-            w.l[r] = 0.f;
-            const bool ok = row < R;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                     (ok ? (int64_t)(g.tok0 + row / a.G) * a.q_stride +
-                                               (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
+            for (int r = 0; r < 2; ++r) {
+                const int row = r0 + (lane >> 2) + 8 * r;
+                // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
+                w.lim[r] = row < R ? paged_limit(a, g, fi, row) : g.len;
+                w.m[r] = -INFINITY;
+                w.l[r] = 0.f;
+                const bool ok = row < R;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                         (ok ? (int64_t)(g.tok0 + row / a.G) * a.q_stride +
+                                                   (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                w.q[k][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;
-                w.q[k][2 + r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16 + 8) : 0u;
+                for (int k = 0; k < D / 16; ++k) {
+                    w.q[k][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;
+                    w.q[k][2 + r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16 + 8) : 0u;
+                }
             }
+            if (WIDE && r0 >= R) w.lim[0] = w.lim[1] = 0;  // a warp without rows only loads
         }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w.o[n][e] = 0.f;
-        // the warp's rows: the fewest and the most keys any of them sees
-        int lo = min(w.lim[0], w.lim[1]), hi = max(w.lim[0], w.lim[1]);
+        lo = min(w.lim[0], w.lim[1]);
+        hi = max(w.lim[0], w.lim[1]);
 #pragma unroll
         for (int o = 16; o >= 4; o >>= 1) {
             lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        for (int t = u.t0; t < u.t1; ++t) {
-            issue(t + kStages - 1);
-            cp_wait<kStages - 1>();
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[n][e] = 0.f;
+        const int64_t slot = u.base + (int64_t)blockIdx.x * RT;
+        const int rows = u.rows;
+        for (int t = u.t0, t1 = u.t1; t < t1; ++t, ++it) {
+            // the next tile is on its way while this one is used, the next unit's first one too
+            if (t + 1 < t1) {
+                issue(ahead, u.h, t + 1, it + 1);
+                if (t + 2 < t1) ahead = find(t + 2);
+            } else {
+                walk.x += t1 - u.t0;
+                more = walk.x < walk.x1;
+                if (more) {
+                    u = paged_unit(a, f, walk);
+                    issue(find(u.t0), u.h, u.t0, it + 1);
+                    if (u.t0 + 1 < u.t1) ahead = find(u.t0 + 1);
+                }
+            }
+            cp_commit();
+            cp_wait<1>();
             if (WIDE)
                 __syncthreads();
             else
                 __syncwarp();
-            const uint32_t st = base + (uint32_t)(t - u.t0) % kStages * kStage;
+            const uint32_t st = base + (uint32_t)it % kStages * kStage;
 #pragma unroll 1
             for (int b = WIDE ? 0 : warp; b < (WIDE ? kWarps : warp + 1); ++b) {
                 const int kb = t * kKT + b * 16;
@@ -239,8 +283,6 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
             else
                 __syncwarp();
         }
-        cp_wait<0>();
-        const int64_t slot = u.base + (int64_t)blockIdx.x * RT;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // the four lanes of a row hold different keys
             w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
@@ -249,9 +291,9 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
         if (WIDE) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = (lane >> 2) + 8 * r;
-                if (r0 + row >= R) continue;
-                const int64_t at = slot + warp * 16 + row;
+                const int row = warp * 16 + (lane >> 2) + 8 * r;
+                if (row >= rows) continue;
+                const int64_t at = slot + row;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     *reinterpret_cast<float2 *>(f.acc + at * D + n * 8 + (lane & 3) * 2) =
@@ -259,23 +301,23 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
                 if ((lane & 3) == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(w.m[r], w.l[r]);
             }
         } else {
-            // the warps' partials of the 16 rows, joined through shared memory
-            constexpr int OS = D + 8;  // floats a row; a warp's rows fit its two stages
-            float *wo = reinterpret_cast<float *>(smem) + (size_t)warp * 16 * OS;
+            // the warps' partials of the 16 rows, joined in the stage that was used last (the other one is
+            // being filled); float c of a row lies at c ^ 8 (row & 7), to spread the rows over the banks
+            float *all = reinterpret_cast<float *>(smem + (uint32_t)(it - 1) % kStages * kStage);
             float2 *ml = reinterpret_cast<float2 *>(smem + kStages * kStage);  // [kWarps][16]
-            __syncthreads();  // every warp is done with its stages
+            __syncthreads();  // every warp is done with the stage
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = (lane >> 2) + 8 * r;
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
-                    *reinterpret_cast<float2 *>(wo + row * OS + n * 8 + (lane & 3) * 2) =
+                    *reinterpret_cast<float2 *>(all + (warp * 16 + row) * D +
+                                                ((n * 8 + (lane & 3) * 2) ^ (8 * (row & 7)))) =
                         make_float2(w.o[n][2 * r], w.o[n][2 * r + 1]);
                 if ((lane & 3) == 0) ml[warp * 16 + row] = make_float2(w.m[r], w.l[r]);
             }
             __syncthreads();
-            const float *all = reinterpret_cast<const float *>(smem);
-            for (int row = warp; row < 16 && r0 + row < R; row += kWarps) {
+            for (int row = warp; row < rows; row += kWarps) {
                 float M = -INFINITY, L = 0.f, acc[D / 32];
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) M = fmaxf(M, ml[i * 16 + row].x);
@@ -288,24 +330,23 @@ __global__ void __launch_bounds__(kWarps * 32) paged_mma_kernel(const __grid_con
                     L += wt * v.y;
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e)
-                        acc[e] = fmaf(wt, all[(i * 16 + row) * OS + lane + 32 * e], acc[e]);
+                        acc[e] = fmaf(wt, all[(i * 16 + row) * D + ((lane + 32 * e) ^ (8 * (row & 7)))], acc[e]);
                 }
                 const int64_t at = slot + row;
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) f.acc[at * D + lane + 32 * e] = acc[e];
                 if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(M, L);
             }
-            __syncthreads();  // the stages belong to the next unit
+            __syncthreads();  // the stage may be filled again
         }
-        walk.x += u.t1 - u.t0;
     }
 }
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool WHOLE>
 cudaError_t mma_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
-    static_assert(WIDE || (size_t)kWarps * 16 * (D + 8) * 4 <= (size_t)kStages * kWarps * 2 * 16 * D * 2,
-                  "the joined rows lie over the stages");
-    auto kernel = paged_mma_kernel<D, WIDE>;
+    static_assert(kStages == 2 && (size_t)kWarps * 16 * D * 4 <= (size_t)kWarps * 2 * 16 * D * 2,
+                  "one tile ahead; the joined rows lie over one stage");
+    auto kernel = paged_mma_kernel<D, WIDE, WHOLE>;
     constexpr size_t smem = mma_smem<D, WIDE>();
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -313,10 +354,14 @@ cudaError_t mma_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
     return launch_pdl(kernel, a->f[fi].n, kWarps * 32, smem, st, *a, fi);
 }
 
-cudaError_t mma_by_shape(int rt, int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
-    if (d == 128)
-        return rt == 16 ? mma_launch<128, false>(a, fi, ctas, st) : mma_launch<128, true>(a, fi, ctas, st);
-    if (d == 64) return rt == 16 ? mma_launch<64, false>(a, fi, ctas, st) : mma_launch<64, true>(a, fi, ctas, st);
+template <int D, bool WIDE>
+cudaError_t mma_by_page(int page_size, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    return page_size % 16 == 0 ? mma_launch<D, WIDE, true>(a, fi, ctas, st) : mma_launch<D, WIDE, false>(a, fi, ctas, st);
+}
+
+cudaError_t mma_by_shape(int rt, int d, int page, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+    if (d == 128) return rt == 16 ? mma_by_page<128, false>(page, a, fi, ctas, st) : mma_by_page<128, true>(page, a, fi, ctas, st);
+    if (d == 64) return rt == 16 ? mma_by_page<64, false>(page, a, fi, ctas, st) : mma_by_page<64, true>(page, a, fi, ctas, st);
     return cudaErrorInvalidValue;
 }
 
@@ -324,14 +369,14 @@ cudaError_t mma_by_shape(int rt, int d, const PagedArgs *a, int fi, int *ctas, c
 
 bool paged_mma_supported(int dtype, int d) { return dtype == RA_BF16 && (d == 64 || d == 128); }
 
-int paged_mma_ctas(int rt, int d) {
+int paged_mma_ctas(int rt, int d, int page_size) {
     int n = 0;
-    if (mma_by_shape(rt, d, nullptr, 0, &n, nullptr) != cudaSuccess || n < 1) n = 1;
+    if (mma_by_shape(rt, d, page_size, nullptr, 0, &n, nullptr) != cudaSuccess || n < 1) n = 1;
     return std::min(kPagedMaxCtas, n * paged_sms());
 }
 
 cudaError_t launch_paged_mma(const PagedArgs &a, int fi, cudaStream_t st) {
-    return mma_by_shape(a.f[fi].rt, a.d, &a, fi, nullptr, st);
+    return mma_by_shape(a.f[fi].rt, a.d, a.page_size, &a, fi, nullptr, st);
 }
 
 }  // namespace ra

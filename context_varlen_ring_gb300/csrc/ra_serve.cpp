@@ -284,7 +284,7 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         F.halves = kind[f] == kWide;
         if (F.S)
             F.n = kind[f] == kWide  ? std::min(kPagedMaxWide, paged_sms())
-                  : kind[f] == kMma ? paged_mma_ctas(F.rt, d)
+                  : kind[f] == kMma ? paged_mma_ctas(F.rt, d, cache->page_size)
                                     : paged_simt_ctas(F.rt, d);
         F.seg = reinterpret_cast<PagedSeg *>(ws + L.o_seg[f]);
         F.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr[f]);
