@@ -286,19 +286,22 @@ constexpr int kPagedMaxCtas = 1024;     // of the warp-level and SIMT kernels
 constexpr int kPagedMaxWide = 256;      // of the tcgen05 kernel (one an SM)
 constexpr int kPagedWideRows = 256;     // its rows a unit
 cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st);
-cudaError_t launch_paged_simt(const PagedArgs &a, int family, cudaStream_t st);
+// `late`: launched behind the other family's kernel, which it need not wait for
+// (it reads the plan only); it then waits before it ends, so that the join,
+// which waits for it, finds both families' partials.
+cudaError_t launch_paged_simt(const PagedArgs &a, int family, int late, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st);
 int paged_simt_ctas(int rt, int d);    // CTAs of the SIMT kernel that the current device holds at once
 bool paged_mma_supported(int dtype, int d);
 int paged_mma_ctas(int rt, int d, int page_size);
-cudaError_t launch_paged_mma(const PagedArgs &a, int family, cudaStream_t st);
+cudaError_t launch_paged_mma(const PagedArgs &a, int family, int late, cudaStream_t st);
 int paged_sms();                       // SMs of the current device
 struct PagedMaps {
     CUtensorMap q, k, v;
     int rows_inner;                    // the cache's rows in a page lie closer than its heads
 };
 bool paged_tc_maps(const PagedArgs &a, PagedMaps &m);  // false: not a shape of the tcgen05 kernel
-cudaError_t launch_paged_tc(const PagedArgs &a, int family, const PagedMaps &m, cudaStream_t st);
+cudaError_t launch_paged_tc(const PagedArgs &a, int family, int late, const PagedMaps &m, cudaStream_t st);
 
 // Device-wait self-test (see ra_selftest_wait_timeout).
 cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t st);

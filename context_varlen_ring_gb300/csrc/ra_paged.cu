@@ -163,12 +163,13 @@ constexpr size_t simt_smem() {
 // wavefront: RPW * 8 / (8 + RPW) in the scores, so 8 rows a warp keep the FMA
 // pipe the limit; 4 rows a warp serve the few rows of single-token steps.
 template <typename T, int NV, int RPW, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_constant__ PagedArgs a, int fi) {
+__global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_constant__ PagedArgs a, int fi,
+                                                                int late) {
     constexpr int D = 32 * NV, RT = RPW * WARPS, KS = D + 4;
     extern __shared__ float4 smem4[];
     float *Ks = reinterpret_cast<float *>(smem4), *Vs = Ks + kKT * KS, *Qs = Vs + kKT * D, *Ps = Qs + RT * D;
     const PagedFamily &f = a.f[fi];
-    pdl_wait();
+    if (!late) pdl_wait();
     pdl_launch();
     const int cta = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -284,29 +285,30 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
         }
         walk.x += u.t1 - u.t0;
     }
+    if (late) pdl_wait();
 }
 
 template <typename T, int NV, int RPW, int WARPS>
-cudaError_t simt_launch(const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+cudaError_t simt_launch(const PagedArgs *a, int fi, int late, int *ctas, cudaStream_t st) {
     auto kernel = paged_simt_kernel<T, NV, RPW, WARPS>;
     constexpr size_t smem = simt_smem<NV, RPW, WARPS>();
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, WARPS * 32, smem);
-    return launch_pdl(kernel, a->f[fi].n, WARPS * 32, smem, st, *a, fi);
+    return launch_pdl(kernel, a->f[fi].n, WARPS * 32, smem, st, *a, fi, late);
 }
 
 template <typename T, int RPW, int WARPS>
-cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int *ctas, cudaStream_t st) {
+cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int late, int *ctas, cudaStream_t st) {
     switch (d / 32) {
-        case 1: return simt_launch<T, 1, RPW, WARPS>(a, fi, ctas, st);
-        case 2: return simt_launch<T, 2, RPW, WARPS>(a, fi, ctas, st);
-        case 3: return simt_launch<T, 3, RPW, WARPS>(a, fi, ctas, st);
-        case 4: return simt_launch<T, 4, RPW, WARPS>(a, fi, ctas, st);
-        case 5: return simt_launch<T, 5, RPW, WARPS>(a, fi, ctas, st);
-        case 6: return simt_launch<T, 6, RPW, WARPS>(a, fi, ctas, st);
-        case 7: return simt_launch<T, 7, RPW, WARPS>(a, fi, ctas, st);
-        case 8: return simt_launch<T, 8, RPW, WARPS>(a, fi, ctas, st);
+        case 1: return simt_launch<T, 1, RPW, WARPS>(a, fi, late, ctas, st);
+        case 2: return simt_launch<T, 2, RPW, WARPS>(a, fi, late, ctas, st);
+        case 3: return simt_launch<T, 3, RPW, WARPS>(a, fi, late, ctas, st);
+        case 4: return simt_launch<T, 4, RPW, WARPS>(a, fi, late, ctas, st);
+        case 5: return simt_launch<T, 5, RPW, WARPS>(a, fi, late, ctas, st);
+        case 6: return simt_launch<T, 6, RPW, WARPS>(a, fi, late, ctas, st);
+        case 7: return simt_launch<T, 7, RPW, WARPS>(a, fi, late, ctas, st);
+        case 8: return simt_launch<T, 8, RPW, WARPS>(a, fi, late, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -508,18 +510,19 @@ int paged_sms() {
 
 int paged_simt_ctas(int rt, int d) {
     int n = 0;
-    const cudaError_t e = rt == 16 ? simt_by_d<float, 4, 4>(d, nullptr, 0, &n, nullptr)
-                                   : simt_by_d<float, 8, 8>(d, nullptr, 0, &n, nullptr);
+    const cudaError_t e = rt == 16 ? simt_by_d<float, 4, 4>(d, nullptr, 0, 0, &n, nullptr)
+                                   : simt_by_d<float, 8, 8>(d, nullptr, 0, 0, &n, nullptr);
     if (e != cudaSuccess || n < 1) n = 1;
     return std::min(kPagedMaxCtas, n * paged_sms());
 }
 
-cudaError_t launch_paged_simt(const PagedArgs &a, int fi, cudaStream_t st) {
+cudaError_t launch_paged_simt(const PagedArgs &a, int fi, int late, cudaStream_t st) {
     const bool few = a.f[fi].rt == 16;
     if (a.dtype == RA_FP32)
-        return few ? simt_by_d<float, 4, 4>(a.d, &a, fi, nullptr, st) : simt_by_d<float, 8, 8>(a.d, &a, fi, nullptr, st);
-    return few ? simt_by_d<__nv_bfloat16, 4, 4>(a.d, &a, fi, nullptr, st)
-               : simt_by_d<__nv_bfloat16, 8, 8>(a.d, &a, fi, nullptr, st);
+        return few ? simt_by_d<float, 4, 4>(a.d, &a, fi, late, nullptr, st)
+                   : simt_by_d<float, 8, 8>(a.d, &a, fi, late, nullptr, st);
+    return few ? simt_by_d<__nv_bfloat16, 4, 4>(a.d, &a, fi, late, nullptr, st)
+               : simt_by_d<__nv_bfloat16, 8, 8>(a.d, &a, fi, late, nullptr, st);
 }
 
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {

@@ -53,7 +53,7 @@ constexpr uint32_t kSmem = kOffBar + 256 + 1024;  // + barriers + alignment slac
 struct TcParams {
     CUtensorMap tmQ, tmK, tmV;
     PagedArgs a;
-    int fi, box, log2G;  // family, rows a box
+    int fi, late, box, log2G;  // family, whether it waits last, rows a box
     int rows_inner;      // the maps' dimensions: (d, row in page, head, page) instead of (d, head, row in page, page)
     unsigned long long budget_ns;
 };
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, a.status, p.budget_ns};
-    pdl_wait();
+    if (!p.late) pdl_wait();
     pdl_launch();
 
     // The CTA's units in order, the same for every role.
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (p.late) pdl_wait();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -529,7 +530,7 @@ bool paged_tc_maps(const PagedArgs &a, PagedMaps &m) {
     return encode(&m.k, a.k, 4, kd, st, kb) && encode(&m.v, a.v, 4, kd, st, kb);
 }
 
-cudaError_t launch_paged_tc(const PagedArgs &a, int fi, const PagedMaps &m, cudaStream_t st) {
+cudaError_t launch_paged_tc(const PagedArgs &a, int fi, int late, const PagedMaps &m, cudaStream_t st) {
     TcParams p;
     memset(&p, 0, sizeof(p));
     p.tmQ = m.q;
@@ -538,6 +539,7 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int fi, const PagedMaps &m, cuda
     p.rows_inner = m.rows_inner;
     p.a = a;
     p.fi = fi;
+    p.late = late;
     p.box = std::min(a.page_size, 128);
     while ((1 << p.log2G) < a.G) ++p.log2G;
     p.budget_ns = wait_budget_ns();

@@ -97,9 +97,9 @@ struct PagedLayout {
     size_t o_hdr[2], o_seg[2], o_start[2], o_acc[2], o_ml[2], bytes;
 };
 
-// A family whose units hold at most 16 rows is left to the warp-level kernel.
-bool paged_few(int family, int64_t T, int G, int max_q_len) {
-    return (family || max_q_len <= 0 ? T : std::min<int64_t>(max_q_len, T)) * G <= 16;
+// The most query rows that a segment of the family has per KV head (as far as the hint goes).
+int64_t paged_rows(int family, int64_t T, int G, int max_q_len) {
+    return (family || max_q_len <= 0 ? T : std::min<int64_t>(max_q_len, T)) * G;
 }
 
 PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, int dtype, int max_q_len) {
@@ -116,8 +116,9 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
         L.o_seg[f] = take((size_t)S * sizeof(PagedSeg));
         L.o_start[f] = take((size_t)kPagedMaxCtas * 4);
         // the rows themselves (twice where units are halved), and one unit more a CTA
-        const bool few = paged_few(f, T, G, max_q_len), wide = !few && dtype == RA_BF16 && d == 128;
-        int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (few ? 16 : 64) : 0;
+        const int64_t most = paged_rows(f, T, G, max_q_len);
+        const bool wide = most > 32 && dtype == RA_BF16 && d == 128;
+        int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (most <= 16 ? 16 : 64) : 0;
         if (S && wide) rows = std::max(rows, 2 * T * G * Hkv + (int64_t)kPagedMaxWide * kPagedWideRows);
         L.o_acc[f] = take((size_t)rows * d * 4);
         L.o_ml[f] = take((size_t)rows * 8);
@@ -271,15 +272,16 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.scale_log2 = scale * 1.4426950408889634f;
     enum { kSimt, kMma, kWide } kind[2];
     PagedMaps maps;
-    const bool wide = (!paged_few(0, T, a.G, max_q_len) || (n_groups > 0 && !paged_few(1, T, a.G, max_q_len))) &&
-                      paged_tc_maps(a, maps);
+    const bool wide =
+        (paged_rows(0, T, a.G, max_q_len) > 32 || (n_groups > 0 && T * a.G > 32)) && paged_tc_maps(a, maps);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
-        const bool few = paged_few(f, T, a.G, max_q_len);
+        // rows a unit: what fits one warp-level pass over the keys, else the tcgen05 kernel's
+        const int64_t most = paged_rows(f, T, a.G, max_q_len);
         kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
-        if (!few && wide) kind[f] = kWide;
+        if (most > 32 && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
-        F.rt = kind[f] == kWide ? kPagedWideRows : few ? 16 : 64;
+        F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
         F.kt = kind[f] == kWide ? 128 : 64;
         F.halves = kind[f] == kWide;
         if (F.S)
@@ -306,8 +308,10 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     for (int f = 1; f >= 0; --f) {
         if (a.f[f].S == 0) continue;
         ProfScope ps(f ? "ra_paged_prefix" : "ra_paged_own", s);
-        e = kind[f] == kWide ? launch_paged_tc(a, f, maps, s) : kind[f] == kMma ? launch_paged_mma(a, f, s)
-                                                                          : launch_paged_simt(a, f, s);
+        const int late = f == 0 && n_groups > 0;  // behind the prefixes' kernel, and independent of it
+        e = kind[f] == kWide  ? launch_paged_tc(a, f, late, maps, s)
+            : kind[f] == kMma ? launch_paged_mma(a, f, late, s)
+                              : launch_paged_simt(a, f, late, s);
         if (e != cudaSuccess) return launch_failed(e, "paged attention launch");
     }
     ProfScope ps("ra_paged_combine", s);
