@@ -273,7 +273,8 @@ struct PagedArgs {
     int Hq, Hkv, G, d, dtype;
     const void *k, *v;
     int64_t n_pages, page_stride, token_stride, head_stride;
-    int page_size, B, n_groups, causal;
+    int page_size, page_shift;         // page_shift: its log2, or -1
+    int B, n_groups, causal;
     const int32_t *cu, *kv_lens, *prefix_lens, *groups;
     float scale_log2;
     PagedFamily f[2];

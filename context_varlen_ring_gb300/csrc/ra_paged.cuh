@@ -88,12 +88,13 @@ __device__ __forceinline__ int paged_limit(const PagedArgs &a, const PagedSeg &g
 // the length, or on a page outside the cache (recorded).
 __device__ __forceinline__ int64_t paged_row(const PagedArgs &a, const PagedFamily &f, int s, int len, int i) {
     if (i >= len) return -1;
-    const int pg = __ldg(f.table + (int64_t)s * f.width + i / a.page_size);
+    const int pi = a.page_shift >= 0 ? i >> a.page_shift : i / a.page_size;
+    const int pg = __ldg(f.table + (int64_t)s * f.width + pi);
     if (pg < 0 || pg >= a.n_pages) {
         record_status(a.status, RA_ERR_DEVICE_BOUNDS);
         return -1;
     }
-    return pg * a.page_stride + (int64_t)(i % a.page_size) * a.token_stride;
+    return pg * a.page_stride + (int64_t)(i - pi * a.page_size) * a.token_stride;
 }
 
 // Programmatic launches: a kernel's prologue runs beside its predecessor's

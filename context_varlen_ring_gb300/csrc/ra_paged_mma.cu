@@ -37,6 +37,9 @@ constexpr int kStages = 2;
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -89,25 +92,29 @@ __device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int l
     const int lane = threadIdx.x & 31, c = lane % CPR, r0 = lane / CPR;
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + h * a.head_stride + c * 8;
     const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + h * a.head_stride + c * 8;
-    if (WHOLE) {
-        if (off < 0) live = 0;
-        long long at = (off < 0 ? 0 : off) + r0 * a.token_stride;
+    // row i * RPI + r0 lies at (first row's address) ^ (its low bits << 4), + i * RPI rows
+    const uint32_t kd = chunk_at<D>(ks, r0, c), vd = chunk_at<D>(vs, r0, c);
+    if (WHOLE && off >= 0 && live >= 16) {
+        const __nv_bfloat16 *kp = k + off + r0 * a.token_stride, *vp = v + off + r0 * a.token_stride;
 #pragma unroll
         for (int i = 0; i < 16 / RPI; ++i) {
-            const bool there = i * RPI + r0 < live;
-            const long long o = there ? at : 0;
-            cp16(chunk_at<D>(ks, i * RPI + r0, c), k + o, there);
-            cp16(chunk_at<D>(vs, i * RPI + r0, c), v + o, there);
-            at += RPI * a.token_stride;
+            const uint32_t x = (uint32_t)((i * RPI & 7) << 4);
+            cp16((kd ^ x) + i * RPI * D * 2, kp);
+            cp16((vd ^ x) + i * RPI * D * 2, vp);
+            kp += RPI * a.token_stride;
+            vp += RPI * a.token_stride;
         }
-    } else {
+        return;
+    }
+    if (WHOLE && off < 0) live = 0;
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-            const int r = i * RPI + r0;
-            const long long o = __shfl_sync(0xffffffffu, off, r);
-            cp16(chunk_at<D>(ks, r, c), k + (o < 0 ? 0 : o), o >= 0);
-            cp16(chunk_at<D>(vs, r, c), v + (o < 0 ? 0 : o), o >= 0);
-        }
+    for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + r0;
+        const uint32_t x = (uint32_t)((i * RPI & 7) << 4);
+        const long long o = WHOLE ? off + r * a.token_stride : __shfl_sync(0xffffffffu, off, r);
+        const bool there = WHOLE ? r < live : o >= 0;
+        cp16((kd ^ x) + i * RPI * D * 2, k + (there ? o : 0), there);
+        cp16((vd ^ x) + i * RPI * D * 2, v + (there ? o : 0), there);
     }
 }
 

@@ -262,6 +262,9 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.token_stride = cache->token_stride;
     a.head_stride = cache->head_stride;
     a.page_size = cache->page_size;
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (cache->page_size == 1 << i) a.page_shift = i;
     a.B = B;
     a.n_groups = n_groups;
     a.causal = causal != 0;
