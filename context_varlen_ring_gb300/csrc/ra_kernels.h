@@ -277,12 +277,14 @@ struct PagedArgs {
     int B, n_groups, causal;
     const int32_t *cu, *kv_lens, *prefix_lens, *groups;
     float scale_log2;
+    int here;                          // no plan kernel: every block plans for itself
     PagedFamily f[2];
     void *out;
     int out_dtype;
     float *lse;
     int *status;
 };
+constexpr int kPagedHere = 256;         // most segments of a family that blocks plan for themselves
 constexpr int kPagedMaxCtas = 1024;     // of the warp-level and SIMT kernels
 constexpr int kPagedMaxWide = 256;      // of the tcgen05 kernel (one an SM)
 constexpr int kPagedWideRows = 256;     // its rows a unit

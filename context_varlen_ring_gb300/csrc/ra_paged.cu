@@ -81,26 +81,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         UW v{0, 0};
         PagedSeg g{};
         if (s < f.S) {
-            const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
-            const int len = fi ? a.prefix_lens[s] : a.kv_lens[s];
-            int c0 = 0, c1 = 0;
-            bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size;
-            if (fine) {
-                c0 = a.cu[b0];
-                c1 = a.cu[b1];
-                fine = c0 >= 0 && c1 >= c0 && c1 <= a.T;
-            }
-            if (!fine) {
-                bad = 1;
-                c0 = c1 = 0;
-            }
-            g.tok0 = c0;
-            g.n = c1 - c0;
-            g.len = len;
-            g.w = g.n > 0 ? (len + f.kt - 1) / f.kt : 0;
-            const long long R = (long long)g.n * a.G, full = R / f.rt;
-            v.u = a.Hkv * (full * f.rt + paged_alloc(f, (int)(R - full * f.rt)));
-            v.w = (R + f.rt - 1) / f.rt * a.Hkv * g.w;
+            bad |= !paged_record(a, f, fi, s, g);
+            v.u = paged_rows(a, f, g);
+            v.w = paged_tiles(a, f, g);
         }
         UW total;
         const UW at = block_scan(v, warp_sum, total);
@@ -173,9 +156,10 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
     pdl_launch();
     const int cta = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    PagedWalk walk = paged_begin(f);
+    __shared__ PlanShared plan;
+    PagedWalk walk = paged_begin<WARPS * 32>(a, f, fi, plan);
     while (walk.x < walk.x1) {
-        const PagedUnit u = paged_unit(a, f, walk);
+        const PagedUnit u = paged_unit(a, f, fi, walk);
         const PagedSeg &g = walk.g;
         const int s = walk.s;
         const int R = g.n * a.G, r0 = u.r0;
@@ -321,14 +305,13 @@ struct Parts {
     int cnt, two, second;
 };
 
-__device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, int s, int64_t t, int h, int g) {
+__device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, const PagedSeg &sg, long long per,
+                                            int64_t t, int h, int g) {
     Parts p{0, 0, 0, 0};
-    if (s < 0) return p;
-    const PagedSeg sg = paged_seg(f, s);
     if (sg.w == 0) return p;
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * sg.w, per = __ldcg(&f.hdr->per);
+    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * sg.w;
     const int c0 = (int)paged_div(x, per), c1 = (int)paged_div(x + sg.w - 1, per);
     p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
     p.two = alloc > rows ? 1 : 0;
@@ -353,6 +336,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
     __shared__ float4 sum[WARPS][32 * NV];
     __shared__ int seg[2];
     __shared__ Parts parts[WARPS][2];
+    __shared__ PlanShared plan[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x / a.Hkv;
     const int h = blockIdx.x % a.Hkv;
@@ -371,16 +355,31 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
         }
     }
     __syncthreads();
+    long long per[2] = {1, 1};
+    if (a.here) {
+        long long W;
+        per[0] = paged_plan_here<WARPS * 32>(a, a.f[0], 0, seg[0], plan[0], W);
+        if (a.n_groups > 0) per[1] = paged_plan_here<WARPS * 32>(a, a.f[1], 1, seg[1], plan[1], W);
+    }
     pdl_wait();
-    if (seg[0] < 0 || __ldcg(&a.f[0].hdr->err) || (a.n_groups > 0 && __ldcg(&a.f[1].hdr->err))) return;
+    if (seg[0] < 0) return;
+    if (!a.here) {
+        for (int i = 0; i < (a.n_groups > 0 ? 2 : 1); ++i) {
+            per[i] = __ldcg(&a.f[i].hdr->err) ? 0 : __ldcg(&a.f[i].hdr->per);
+            if ((int)threadIdx.x == i && seg[i] >= 0) plan[i].g = paged_seg(a.f[i], seg[i]);
+        }
+    }
+    if (!per[0] || !per[1]) return;  // an array that is not as it must be: nothing is written
     int wpr = 1;  // warps a row: a power of two, heads in turn where there are more
     while (wpr * 2 * a.G <= WARPS) wpr *= 2;
     const int sub = warp % wpr, at_once = WARPS / wpr, d4 = a.d / 4;
     for (int g0 = 0; g0 < a.G; g0 += at_once) {
-        if (g0 > 0) __syncthreads();  // the last heads' places have been read
+        __syncthreads();  // the segments are there; the last heads' places have been read
         if ((int)threadIdx.x < 2 * at_once && g0 + (int)threadIdx.x / 2 < a.G)
             parts[threadIdx.x / 2][threadIdx.x & 1] =
-                find_parts(a, a.f[threadIdx.x & 1], seg[threadIdx.x & 1], t, h, g0 + threadIdx.x / 2);
+                seg[threadIdx.x & 1] < 0 ? Parts{0, 0, 0, 0}
+                                         : find_parts(a, a.f[threadIdx.x & 1], plan[threadIdx.x & 1].g,
+                                                      per[threadIdx.x & 1], t, h, g0 + threadIdx.x / 2);
         __syncthreads();
         const int g = g0 + warp / wpr;
         const bool live = g < a.G;

@@ -27,6 +27,35 @@ struct PagedUnit {
     long long base;      // first partial row (of CTA 0)
 };
 
+// Segment s of a family from the call's arrays (W0 and R0 left to the plan);
+// false, and an empty one, where they are not as they must be.
+__device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFamily &f, int fi, int s, PagedSeg &g) {
+    const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
+    const int len = fi ? a.prefix_lens[s] : a.kv_lens[s];
+    int c0 = 0, c1 = 0;
+    bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size;
+    if (fine) {
+        c0 = a.cu[b0];
+        c1 = a.cu[b1];
+        fine = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+    }
+    if (!fine) c0 = c1 = 0;
+    g.tok0 = c0;
+    g.n = c1 - c0;
+    g.len = fine ? len : 0;
+    g.w = g.n > 0 ? (g.len + f.kt - 1) / f.kt : 0;
+    g.W0 = g.R0 = 0;
+    return fine;
+}
+// Its key tiles and partial rows over all units.  (n * G < 2^31.)
+__device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
+    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * g.w;
+}
+__device__ __forceinline__ long long paged_rows(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
+    const int R = g.n * a.G, full = R / f.rt * f.rt;
+    return (long long)a.Hkv * (full + paged_alloc(f, R - full));
+}
+
 // A CTA's run of the line, and its place in it: the segment and the unit.
 struct PagedWalk {
     long long x, x1;
@@ -34,8 +63,8 @@ struct PagedWalk {
     PagedSeg g;
 };
 
-// The run of this CTA (x == x1: none).  The plan's results are read past L1,
-// which may hold an earlier call's.
+// The plan kernel's record of a segment.  Its results are read past L1, which
+// may hold an earlier call's.
 __device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
     const int4 *p = reinterpret_cast<const int4 *>(f.seg + s);
     const int4 a = __ldcg(p), b = __ldcg(p + 1);
@@ -48,10 +77,99 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
     g.R0 = ((long long)b.w << 32) | (unsigned)b.z;
     return g;
 }
-__device__ __forceinline__ PagedWalk paged_begin(const PagedFamily &f) {
-    const long long per = __ldcg(&f.hdr->per), W = __ldcg(&f.hdr->W);
+
+// Up to kPagedHere segments are planned by every block for itself, from the
+// call's arrays: a scan over THREADS threads, which costs less than a launch
+// ahead of all others and the loads that depend on it (one request of 8192
+// keys: 19.6 us with the plan kernel, FIG without).  Finds the segment with
+// tiles at place blockIdx.x * per (want < 0), or segment `want`; per = 0 where
+// an array is not as it must be.
+struct PlanShared {
+    long long w[32], r[32];
+    PagedSeg g;
+    int s;
+};
+template <int THREADS>
+__device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const PagedFamily &f, int fi, int want,
+                                                     PlanShared &sh, long long &W) {
+    constexpr int K = (kPagedHere + THREADS - 1) / THREADS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    PagedSeg g[K];
+    long long w = 0, r = 0;
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int s = threadIdx.x * K + k;
+        g[k].n = g[k].w = 0;
+        if (s < f.S) {
+            bad |= !paged_record(a, f, fi, s, g[k]);
+            w += paged_tiles(a, f, g[k]);
+            r += paged_rows(a, f, g[k]);
+        }
+    }
+    long long wi = w, ri = r;  // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, wi, o), y = __shfl_up_sync(0xffffffffu, ri, o);
+        if (lane >= o) {
+            wi += x;
+            ri += y;
+        }
+    }
+    if (lane == 31) {
+        sh.w[warp] = wi;
+        sh.r[warp] = ri;
+    }
+    bad = __syncthreads_or(bad);
+    long long w0 = wi - w, r0 = ri - r;
+    W = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) {
+            w0 += sh.w[i];
+            r0 += sh.r[i];
+        }
+        W += sh.w[i];
+    }
+    const long long per = max(1ll, paged_div(W + f.n - 1, f.n));
+    if (bad) {
+        if (threadIdx.x == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+        W = 0;
+    }
+    const long long x = blockIdx.x * per;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int s = threadIdx.x * K + k;
+        if (s >= f.S) break;
+        const long long tiles = paged_tiles(a, f, g[k]);
+        if (want < 0 ? x >= w0 && x < w0 + tiles : s == want) {
+            g[k].W0 = w0;
+            g[k].R0 = r0;
+            sh.g = g[k];
+            sh.s = s;
+        }
+        w0 += tiles;
+        r0 += paged_rows(a, f, g[k]);
+    }
+    __syncthreads();
+    return bad ? 0 : per;
+}
+
+// The run of this CTA (x >= x1: none).
+template <int THREADS>
+__device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const PagedFamily &f, int fi, PlanShared &sh) {
     PagedWalk k;
-    k.s = __ldcg(f.start + blockIdx.x);  // (not meant for a CTA without a run)
+    if (a.here) {
+        long long W;
+        const long long per = paged_plan_here<THREADS>(a, f, fi, -1, sh, W);
+        k.x = blockIdx.x * per;
+        k.x1 = min(W, k.x + per);
+        k.s = sh.s;  // (not meant for a CTA without a run)
+        k.g = sh.g;
+        return k;
+    }
+    const long long per = __ldcg(&f.hdr->per), W = __ldcg(&f.hdr->W);
+    k.s = __ldcg(f.start + blockIdx.x);
     k.x = blockIdx.x * per;
     k.x1 = min(W, k.x + per);
     if (k.x < k.x1) k.g = paged_seg(f, k.s);
@@ -62,9 +180,18 @@ __device__ __forceinline__ PagedWalk paged_begin(const PagedFamily &f) {
 // one's are done), and the CTA's part of it.  Row tiles are outermost in a
 // segment, so CTAs an equal share of the line apart read the same keys for
 // different rows at about the same time (from L2).
-__device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedFamily &f, PagedWalk &k) {
-    auto tiles = [&]() { return (long long)((k.g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * k.g.w; };
-    while (k.g.W0 + tiles() <= k.x) k.g = paged_seg(f, ++k.s);
+__device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedFamily &f, int fi, PagedWalk &k) {
+    for (long long end; (end = k.g.W0 + paged_tiles(a, f, k.g)) <= k.x;) {
+        ++k.s;
+        if (a.here) {
+            const long long rows = k.g.R0 + paged_rows(a, f, k.g);
+            paged_record(a, f, fi, k.s, k.g);
+            k.g.W0 = end;
+            k.g.R0 = rows;
+        } else {
+            k.g = paged_seg(f, k.s);
+        }
+    }
     const long long rel = k.x - k.g.W0;
     const int lu = (int)paged_div(rel, k.g.w), rtile = lu / a.Hkv;
     PagedUnit u;

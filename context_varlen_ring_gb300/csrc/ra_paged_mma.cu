@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
     if (!late) pdl_wait();
     pdl_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    PagedWalk walk = paged_begin(f);
+    __shared__ PlanShared plan;
+    PagedWalk walk = paged_begin<kWarps * 32>(a, f, fi, plan);
     if (walk.x >= walk.x1) {
         if (late) pdl_wait();
         return;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
         const uint32_t st = base + (uint32_t)i % kStages * kStage + warp * kBlk;
         issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk);
     };
-    PagedUnit u = paged_unit(a, f, walk);
+    PagedUnit u = paged_unit(a, f, fi, walk);
     issue(find(u.t0), u.h, u.t0, 0);
     cp_commit();
     long long ahead = u.t0 + 1 < u.t1 ? find(u.t0 + 1) : -1;  // the next tile's place, when it is of this unit
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
                 walk.x += t1 - u.t0;
                 more = walk.x < walk.x1;
                 if (more) {
-                    u = paged_unit(a, f, walk);
+                    u = paged_unit(a, f, fi, walk);
                     issue(find(u.t0), u.h, u.t0, it + 1);
                     if (u.t0 + 1 < u.t1) ahead = find(u.t0 + 1);
                 }

@@ -137,16 +137,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     if (!p.late) pdl_wait();
     pdl_launch();
 
+    __shared__ PlanShared plan;
+    // Each warp's place in the CTA's run: in shared memory, so that it holds no
+    // registers in the loops over key tiles.
+    __shared__ PagedWalk place[kThreads / 32];
+    {
+        const PagedWalk begin = paged_begin<kThreads>(a, f, p.fi, plan);
+        if (lane == 0) place[warp] = begin;
+        __syncwarp();
+    }
     // The CTA's units in order, the same for every role.
-    auto next_unit = [&](PagedWalk &k) {
+    auto more = [&]() { return place[warp].x < place[warp].x1; };
+    auto next_unit = [&]() {
         Walk w;
-        w.u = paged_unit(a, f, k);
+        PagedWalk k = place[warp];
+        __syncwarp();
+        w.u = paged_unit(a, f, p.fi, k);
         w.g = k.g;
         w.s = k.s;
         w.pair = w.u.rows > 128;
         const int sees = paged_limit(a, w.g, p.fi, w.u.r0 + w.u.rows - 1);
         w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
         k.x += w.u.t1 - w.u.t0;
+        if (lane == 0) place[warp] = k;
+        __syncwarp();
         return w;
     };
 
@@ -163,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tma_prefetch_desc(&p.tmV);
             }
             const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
-            for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
-                const Walk w = next_unit(walk);
+            while (ok && more()) {
+                const Walk w = next_unit();
                 const int tok = w.g.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
                 if (lane == 0) {
                     if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1u, wc);
@@ -244,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 return kvs + (i % kSlots) * kTile;
             };
             auto empty = [&](uint32_t i) { tc_commit_w(kv_empty + i % kSlots); };
-            for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
-                const Walk w = next_unit(walk);
+            while (ok && more()) {
+                const Walk w = next_unit();
                 ok = mbar_wait_warp(q_full, nu & 1u, wc);
                 ++nu;
                 tc_fence_after();
@@ -353,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint32_t tO = tmem + lane_base + 256u + 128u * k;
         uint32_t nd_all = 0;  // S tiles of this group (all units)
         bool ok = true;
-        for (PagedWalk walk = paged_begin(f); walk.x < walk.x1 && ok;) {
-            const Walk w = next_unit(walk);
+        while (ok && more()) {
+            const Walk w = next_unit();
             const int by = w.pair ? 1 : 2;
             const int row = (w.pair ? 128 * k : 0) + m;  // of the unit
             const bool valid = row < w.u.rows;
