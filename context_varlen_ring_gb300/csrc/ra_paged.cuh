@@ -155,7 +155,16 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
     return bad ? 0 : per;
 }
 
-// The run of this CTA (x >= x1: none).
+// The run of this CTA (x >= x1: none), by the plan kernel's results or its own.
+__device__ __forceinline__ PagedWalk paged_planned(const PagedFamily &f) {
+    PagedWalk k;
+    const long long per = __ldcg(&f.hdr->per), W = __ldcg(&f.hdr->W);
+    k.s = __ldcg(f.start + blockIdx.x);  // (not meant for a CTA without a run)
+    k.x = blockIdx.x * per;
+    k.x1 = min(W, k.x + per);
+    if (k.x < k.x1) k.g = paged_seg(f, k.s);
+    return k;
+}
 template <int THREADS>
 __device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const PagedFamily &f, int fi, PlanShared &sh) {
     PagedWalk k;
@@ -168,12 +177,7 @@ __device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const Paged
         k.g = sh.g;
         return k;
     }
-    const long long per = __ldcg(&f.hdr->per), W = __ldcg(&f.hdr->W);
-    k.s = __ldcg(f.start + blockIdx.x);
-    k.x = blockIdx.x * per;
-    k.x1 = min(W, k.x + per);
-    if (k.x < k.x1) k.g = paged_seg(f, k.s);
-    return k;
+    return paged_planned(f);
 }
 
 // The unit at the walk's place (in the next segment with tiles, where the last

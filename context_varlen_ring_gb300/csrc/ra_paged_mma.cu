@@ -34,11 +34,14 @@ constexpr int kWarps = 4;
 constexpr int kKT = 64;      // keys a tile: 16 for each warp
 constexpr int kStages = 2;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0), "l"(policy)
+                 : "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -87,7 +90,8 @@ __device__ __forceinline__ long long find16(const PagedArgs &a, const PagedFamil
 // filled with zeros, so whatever the cache holds behind a sequence's end never
 // meets the products.
 template <int D, bool WHOLE>
-__device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int live, int h, uint32_t ks, uint32_t vs) {
+__device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int live, int h, uint32_t ks, uint32_t vs,
+                                        uint64_t policy) {
     constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks a row, rows a warp instruction
     const int lane = threadIdx.x & 31, c = lane % CPR, r0 = lane / CPR;
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + h * a.head_stride + c * 8;
@@ -99,8 +103,8 @@ __device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int l
 #pragma unroll
         for (int i = 0; i < 16 / RPI; ++i) {
             const uint32_t x = (uint32_t)((i * RPI & 7) << 4);
-            cp16((kd ^ x) + i * RPI * D * 2, kp);
-            cp16((vd ^ x) + i * RPI * D * 2, vp);
+            cp16((kd ^ x) + i * RPI * D * 2, kp, policy);
+            cp16((vd ^ x) + i * RPI * D * 2, vp, policy);
             kp += RPI * a.token_stride;
             vp += RPI * a.token_stride;
         }
@@ -113,8 +117,8 @@ __device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int l
         const uint32_t x = (uint32_t)((i * RPI & 7) << 4);
         const long long o = WHOLE ? off + r * a.token_stride : __shfl_sync(0xffffffffu, off, r);
         const bool there = WHOLE ? r < live : o >= 0;
-        cp16((kd ^ x) + i * RPI * D * 2, k + (there ? o : 0), there);
-        cp16((vd ^ x) + i * RPI * D * 2, v + (there ? o : 0), there);
+        cp16((kd ^ x) + i * RPI * D * 2, k + (there ? o : 0), there, policy);
+        cp16((vd ^ x) + i * RPI * D * 2, v + (there ? o : 0), there, policy);
     }
 }
 
@@ -235,12 +239,13 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
         if (late) pdl_wait();
         return;
     }
+    const uint64_t policy = l2_evict_first();
     int it = 0;                      // key tiles so far: tile i lies in stage i % kStages
     // this warp's 16 keys of tile t of the walk's segment
     auto find = [&](int t) { return find16<WHOLE>(a, f, walk.s, walk.g.len, t * kKT + warp * 16); };
     auto issue = [&](long long off, int h, int t, int i) {
         const uint32_t st = base + (uint32_t)i % kStages * kStage + warp * kBlk;
-        issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk);
+        issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk, policy);
     };
     PagedUnit u = paged_unit(a, f, fi, walk);
     issue(find(u.t0), u.h, u.t0, 0);

@@ -74,6 +74,23 @@ __device__ __forceinline__ uint32_t low_bits(int n, int base) {
     return k == 32 ? 0xffffffffu : (1u << k) - 1u;
 }
 
+// Columns of a tile that the softmax holds at once, in rolled loops: the
+// kernel's short runs wait for instructions as much as for anything (fully
+// unrolled, the first tile takes 10000 to 17000 cycles, a later one 1700).
+constexpr int kCols = 64, kChunks = 128 / kCols;
+__device__ __forceinline__ void load_cols(uint32_t t, uint32_t (&v)[32]) { tmem_ld32(t, v); }
+__device__ __forceinline__ void load_cols(uint32_t t, uint32_t (&v)[64]) { tmem_ld64(t, v); }
+__device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&v)[16]) { tmem_st16(t, v); }
+__device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&v)[32]) { tmem_st32(t, v); }
+__device__ __forceinline__ void mask_cols(uint32_t (&v)[kCols], int seen, int base) {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32) {
+        const uint32_t bits = low_bits(seen, base + c);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[c + i] = ((bits >> i) & 1u) ? v[c + i] : 0xff800000u;  // -inf
+    }
+}
+
 __device__ __forceinline__ void issue_s(uint32_t d_tmem, uint32_t q_s, uint32_t k_s, uint32_t idesc) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -141,11 +158,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     // Each warp's place in the CTA's run: in shared memory, so that it holds no
     // registers in the loops over key tiles.
     __shared__ PagedWalk place[kThreads / 32];
-    {
-        const PagedWalk begin = paged_begin<kThreads>(a, f, p.fi, plan);
-        if (lane == 0) place[warp] = begin;
+    auto begin = [&]() {
+        if (!p.late) pdl_wait();
+        pdl_launch();
+        const PagedWalk k = paged_planned(f);
+        if (lane == 0) place[warp] = k;
         __syncwarp();
-    }
+    };
     // The CTA's units in order, the same for every role.
     auto more = [&]() { return place[warp].x < place[warp].x1; };
     auto next_unit = [&]() {
@@ -171,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // -------------------------------------------- producer
             uint32_t n = 0;  // K and V tiles loaded
             int nq = 0, ok = 1;
+            const uint64_t policy = l2_evict_first();
+            begin();
             if (lane == 0) {
                 tma_prefetch_desc(&p.tmQ);
                 tma_prefetch_desc(&p.tmK);
@@ -214,9 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) return;
                     if (lane < boxes)
-                        tma_load_4d(base + kOffKV + slot * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128, m,
-                                    kv_full + slot, (lane & 1) * 64, p.rows_inner ? row : w.u.h,
-                                    p.rows_inner ? w.u.h : row, page);
+                        tma_load_4d_hint(base + kOffKV + slot * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128,
+                                         m, kv_full + slot, (lane & 1) * 64, p.rows_inner ? row : w.u.h,
+                                         p.rows_inner ? w.u.h : row, page, policy);
                     ++n;
                 };
                 const int by = w.pair ? 1 : 2;
@@ -249,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
             const uint32_t kvs = base_s + kOffKV;
             const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+            begin();
             uint32_t n = 0, np0 = 0, np1 = 0;  // tiles consumed; PVs issued per group (all units)
             int nu = 0;
             bool ok = true;
@@ -367,89 +389,115 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const uint32_t tO = tmem + lane_base + 256u + 128u * k;
         uint32_t nd_all = 0;  // S tiles of this group (all units)
         bool ok = true;
-        while (ok && more()) {
-            const Walk w = next_unit();
+        float m_run = -INFINITY, l_run = 0.f;
+        uint32_t nd = 0;
+        // One tile: `seen` of its columns count for this row.  `live` is false
+        // in the pass below that only warms the instruction cache.
+        auto tile = [&](int seen, bool live) {
+            const bool cut = __any_sync(0xffffffffu, seen < 128);
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint32_t v[kCols];
+                load_cols(tS + kCols * ch, v);
+                if (cut) mask_cols(v, seen, kCols * ch);
+                float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kCols; i += 8) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        m4[j] = max3f(m4[j], __uint_as_float(v[i + j]), __uint_as_float(v[i + 4 + j]));
+                }
+                mx = max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+            }
+            // the reference maximum moves only when it grew by more than 2^8: the final
+            // scaling uses the same one, so the result is exact
+            const float m_new = fmaxf(m_run, mx * a.scale_log2);
+            const bool need = m_new > m_run + 8.0f;
+            float alpha = 1.f;
+            if (need) {
+                alpha = ex2_approx(m_run - m_new);
+                m_run = m_new;
+                l_run *= alpha;
+            }
+            const float use = (m_run == -INFINITY) ? 0.f : m_run;
+            const float2 sl2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-use, -use);
+            float2 sum2 = make_float2(0.f, 0.f);
+            // P (bf16) replaces S column pair by column pair: P's columns of a chunk lie where S has been read
+#pragma unroll 1
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint32_t v[kCols], pk[kCols / 2];
+                load_cols(tS + kCols * ch, v);
+                if (cut) mask_cols(v, seen, kCols * ch);
+                float2 sum4[2] = {sum2, make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < kCols / 2; ++c) {
+                    const float2 e = fma2(make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sl2, nm2);
+                    const float2 e2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                    sum4[c & 1] = add2(sum4[c & 1], e2);
+                    pk[c] = pack_bf16x2(e2.x, e2.y);
+                }
+                sum2 = add2(sum4[0], sum4[1]);
+                if (live) store_cols(tS + kCols / 2 * ch, pk);
+            }
+            l_run += sum2.x + sum2.y;
+            if (live) {
+                // O is rescaled here: its last product finished before this S was computed
+                if (nd > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + 32u * ch, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+                        tmem_st32(tO + 32u * ch, v);
+                    }
+                }
+            }
+        };
+        // The unrolled tile is some 20 KB of instructions, which the first pass
+        // fetches from L2: 10000 cycles against 3700 of a warm one.  So one
+        // pass runs on whatever TMEM holds while the plan and the first keys
+        // are under way, without storing anything.
+#pragma unroll 1
+        for (int dry = p.budget_ns != 0; ok; dry = 0) {  // (always so: a value that the compiler does not unroll by)
+            Walk w;
+            if (dry) {
+                w.u.t0 = 0;
+                w.tend = 1;
+                w.pair = true;
+                w.u.rows = 0;
+            } else {
+                if (!more()) break;
+                w = next_unit();
+            }
             const int by = w.pair ? 1 : 2;
             const int row = (w.pair ? 128 * k : 0) + m;  // of the unit
             const bool valid = row < w.u.rows;
             // (padding rows hold other tokens' queries or zeros: computed without masks, dropped)
-            const int lim = valid ? paged_limit(a, w.g, p.fi, w.u.r0 + row) : w.g.len;
-            const bool busy = __any_sync(0xffffffffu, valid);  // a warp of padding rows only keeps the barriers going
-            float m_run = -INFINITY, l_run = 0.f;
-            uint32_t nd = 0;
-            for (int t = w.u.t0 + (w.pair ? 0 : k); t < w.tend; t += by) {
-                ok = mbar_wait_warp(s_full + k, nd_all & 1u, wc);
-                if (!ok) break;
-                tc_fence_after();
-                if (busy) {
-                    float sc[128];
-                    {
-                        uint32_t v[128];
-                        tmem_ld128(tS, v);
-#pragma unroll
-                        for (int i = 0; i < 128; ++i) sc[i] = __uint_as_float(v[i]);
-                    }
-                    const int seen = lim - t * 128;  // columns of this tile that the row sees
-                    if (__any_sync(0xffffffffu, seen < 128)) {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
-                            const uint32_t bits = low_bits(seen, 32 * ch);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                sc[32 * ch + i] = ((bits >> i) & 1u) ? sc[32 * ch + i] : -INFINITY;
-                        }
-                    }
-                    float mx8[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(sc[i], sc[8 + i]);
-#pragma unroll
-                    for (int c = 16; c < 128; c += 16) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) mx8[i] = max3f(mx8[i], sc[c + i], sc[c + 8 + i]);
-                    }
-                    const float mx =
-                        max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-                    // the reference maximum moves only when it grew by more than 2^8: the final
-                    // scaling uses the same one, so the result is exact
-                    const float m_new = fmaxf(m_run, mx * a.scale_log2);
-                    const bool need = m_new > m_run + 8.0f;
-                    float alpha = 1.f;
-                    if (need) {
-                        alpha = ex2_approx(m_run - m_new);
-                        m_run = m_new;
-                        l_run *= alpha;
-                    }
-                    const float use = (m_run == -INFINITY) ? 0.f : m_run;
-                    float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                      make_float2(0.f, 0.f)};
-                    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-use, -use);
-                    uint32_t pk[64];
-#pragma unroll
-                    for (int c2 = 0; c2 < 64; ++c2) {
-                        const float2 e = fma2(make_float2(sc[2 * c2], sc[2 * c2 + 1]), sl2, nm2);
-                        const float2 e2 = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                        sum4[c2 & 3] = add2(sum4[c2 & 3], e2);
-                        pk[c2] = pack_bf16x2(e2.x, e2.y);
-                    }
-                    const float2 sum2 = add2(add2(sum4[0], sum4[1]), add2(sum4[2], sum4[3]));
-                    l_run += sum2.x + sum2.y;
-                    tmem_st64(tS, pk);
-                    // O is rescaled here: its last product finished before this S was computed
-                    if (nd > 0 && __any_sync(0xffffffffu, need)) {
+            const int lim = dry ? 128 : valid ? paged_limit(a, w.g, p.fi, w.u.r0 + row) : w.g.len;
+            // a warp of padding rows only keeps the barriers going
+            const bool busy = dry || __any_sync(0xffffffffu, valid);
+            m_run = -INFINITY;
+            l_run = 0.f;
+            nd = 0;
 #pragma unroll 1
-                        for (int ch = 0; ch < 4; ++ch) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + 32u * ch, v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                            tmem_st32(tO + 32u * ch, v);
-                        }
-                    }
+            for (int t = w.u.t0 + (w.pair ? 0 : k); t < w.tend; t += by) {
+                if (!dry) {
+                    ok = mbar_wait_warp(s_full + k, nd_all & 1u, wc);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
+                if (busy) tile(lim - t * 128, !dry);
+                if (dry) break;
                 tc_fence_before();
                 mbar_arrive(p_ready + k);
                 ++nd;
                 ++nd_all;
+            }
+            if (dry) {
+                begin();
+                continue;
             }
             if (ok && nd > 0) {
                 ok = mbar_wait_warp(o_done + k, (nd_all - 1) & 1u, wc);
