@@ -87,9 +87,17 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
 struct PlanShared {
     long long w[32], r[32];
     PagedSeg g;
-    int s;
+    int s, bad[32];
 };
-template <int THREADS>
+// Barrier of the block's first THREADS threads (of all of them: 0).
+template <int THREADS, int BAR>
+__device__ __forceinline__ void plan_sync() {
+    if (BAR == 0)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(THREADS) : "memory");
+}
+template <int THREADS, int BAR = 0>
 __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const PagedFamily &f, int fi, int want,
                                                      PlanShared &sh, long long &W) {
     constexpr int K = (kPagedHere + THREADS - 1) / THREADS;
@@ -116,11 +124,13 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
             ri += y;
         }
     }
+    bad = __any_sync(0xffffffffu, bad);
     if (lane == 31) {
         sh.w[warp] = wi;
         sh.r[warp] = ri;
+        sh.bad[warp] = bad;
     }
-    bad = __syncthreads_or(bad);
+    plan_sync<THREADS, BAR>();
     long long w0 = wi - w, r0 = ri - r;
     W = 0;
 #pragma unroll
@@ -130,6 +140,7 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
             r0 += sh.r[i];
         }
         W += sh.w[i];
+        bad |= sh.bad[i];
     }
     const long long per = max(1ll, paged_div(W + f.n - 1, f.n));
     if (bad) {
@@ -151,7 +162,7 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
         w0 += tiles;
         r0 += paged_rows(a, f, g[k]);
     }
-    __syncthreads();
+    plan_sync<THREADS, BAR>();
     return bad ? 0 : per;
 }
 
@@ -165,12 +176,12 @@ __device__ __forceinline__ PagedWalk paged_planned(const PagedFamily &f) {
     if (k.x < k.x1) k.g = paged_seg(f, k.s);
     return k;
 }
-template <int THREADS>
+template <int THREADS, int BAR = 0>
 __device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const PagedFamily &f, int fi, PlanShared &sh) {
     PagedWalk k;
     if (a.here) {
         long long W;
-        const long long per = paged_plan_here<THREADS>(a, f, fi, -1, sh, W);
+        const long long per = paged_plan_here<THREADS, BAR>(a, f, fi, -1, sh, W);
         k.x = blockIdx.x * per;
         k.x1 = min(W, k.x + per);
         k.s = sh.s;  // (not meant for a CTA without a run)

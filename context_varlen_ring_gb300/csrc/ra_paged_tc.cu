@@ -151,20 +151,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, a.status, p.budget_ns};
-    if (!p.late) pdl_wait();
-    pdl_launch();
 
-    __shared__ PlanShared plan;
     // Each warp's place in the CTA's run: in shared memory, so that it holds no
     // registers in the loops over key tiles.
     __shared__ PagedWalk place[kThreads / 32];
-    auto begin = [&]() {
+    __shared__ PlanShared plan;
+    if (warp < 4) {
         if (!p.late) pdl_wait();
         pdl_launch();
-        const PagedWalk k = paged_planned(f);
-        if (lane == 0) place[warp] = k;
+        const PagedWalk k = paged_begin<128, 1>(a, f, p.fi, plan);
+        if (lane == 0) {
+            place[warp] = k;
+            place[warp + 4] = k;
+            place[warp + 8] = k;
+        }
         __syncwarp();
-    };
+        asm volatile("bar.arrive 2, 384;" ::: "memory");  // the softmax warps read theirs
+    }
     // The CTA's units in order, the same for every role.
     auto more = [&]() { return place[warp].x < place[warp].x1; };
     auto next_unit = [&]() {
@@ -191,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             uint32_t n = 0;  // K and V tiles loaded
             int nq = 0, ok = 1;
             const uint64_t policy = l2_evict_first();
-            begin();
             if (lane == 0) {
                 tma_prefetch_desc(&p.tmQ);
                 tma_prefetch_desc(&p.tmK);
@@ -270,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
             const uint32_t kvs = base_s + kOffKV;
             const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
-            begin();
             uint32_t n = 0, np0 = 0, np1 = 0;  // tiles consumed; PVs issued per group (all units)
             int nu = 0;
             bool ok = true;
@@ -457,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         };
         // The unrolled tile is some 20 KB of instructions, which the first pass
         // fetches from L2: 10000 cycles against 3700 of a warm one.  So one
-        // pass runs on whatever TMEM holds while the plan and the first keys
-        // are under way, without storing anything.
+        // pass runs on whatever TMEM holds while the run is planned and the
+        // first keys are under way, without storing anything.
 #pragma unroll 1
         for (int dry = p.budget_ns != 0; ok; dry = 0) {  // (always so: a value that the compiler does not unroll by)
             Walk w;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 ++nd_all;
             }
             if (dry) {
-                begin();
+                asm volatile("bar.sync 2, 384;" ::: "memory");  // the CTA's run is planned
                 continue;
             }
             if (ok && nd > 0) {

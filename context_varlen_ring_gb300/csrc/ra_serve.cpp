@@ -304,8 +304,7 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.lse = lse;
     a.status = device_status_ptr();
     cudaError_t e;
-    // (the tcgen05 kernel sets up beside the plan kernel, which then costs it nothing)
-    a.here = B <= kPagedHere && n_groups <= kPagedHere && kind[0] != kWide && (n_groups == 0 || kind[1] != kWide);
+    a.here = B <= kPagedHere && n_groups <= kPagedHere;
     if (!a.here) {
         ProfScope ps("ra_paged_plan", s);
         if ((e = launch_paged_plan(a, s)) != cudaSuccess) return launch_failed(e, "paged plan launch");
