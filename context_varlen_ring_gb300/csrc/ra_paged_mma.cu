@@ -11,9 +11,8 @@
 // time.  Scores, maximum, sum and products stay in registers; the warps'
 // partials are joined in shared memory when the CTA's run of the unit ends.
 //
-// With 17 to 32 rows a warp keeps two row tiles for each of its keys (Q then
-// comes from shared memory); with more, where the tcgen05 kernel does not take
-// the shape, the warps go over the rows and share the key tile (64 rows a CTA).
+// With more rows the key tile is shared: up to 32 rows a pair of warps has 16
+// rows and half of the keys each, up to 64 every warp has 16 rows and all keys.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -122,82 +121,67 @@ __device__ __forceinline__ void issue16(const PagedArgs &a, long long off, int l
     }
 }
 
-template <int D, int MT>
+template <int D>
 struct Rows {
-    uint32_t q[MT == 1 ? D / 16 : 1][4];  // A fragments of the 16 query rows (two row tiles read theirs from shared memory)
-    float o[MT][D / 8][4];                // sum p v of rows 16 i + lane / 4 and + 8
-    float m[MT][2], l[MT][2];             // running maximum (log2), sum p of the lane's own keys
-    int lim[MT][2];                       // keys the rows see
+    uint32_t q[D / 16][4];  // A fragments of the 16 query rows
+    float o[D / 8][4];      // sum p v of rows lane / 4 and lane / 4 + 8
+    float m[2], l[2];       // running maximum (log2), sum p of the lane's own keys
+    int lim[2];             // keys the rows see
 };
 
-// One block of 16 keys for MT tiles of 16 rows: S = Q K^T, the running
-// maximum, P in bf16 (rounded once: the products' inputs; the sums use the
-// unrounded values), O += P V.  Each key and value fragment serves every tile.
-template <int D, int MT>
-__device__ __forceinline__ void block16(Rows<D, MT> &w, uint32_t qs, uint32_t ks, uint32_t vs, int kb, bool masked,
-                                        float scale_log2) {
+// One block of 16 keys for 16 rows: S = Q K^T, the running maximum, P in
+// bf16 (rounded once: the products' inputs; the sums use the unrounded
+// values), O += P V.
+template <int D>
+__device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, int kb, bool masked, float scale_log2) {
     const int lane = threadIdx.x & 31, id = lane >> 3, l8 = lane & 7;
-    float s[MT][2][4] = {};
+    float s[2][4] = {};
     const uint32_t ka = chunk_at<D>(ks, (id >> 1) * 8 + l8, id & 1);
-    const uint32_t qa = chunk_at<D>(qs, (id & 1) * 8 + l8, id >> 1);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
         ldsm4(ka ^ (k << 5), b);
+        mma16816(s[0], w.q[k], b[0], b[1]);
+        mma16816(s[1], w.q[k], b[2], b[3]);
+    }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (MT == 1) {
-                mma16816(s[i][0], w.q[k % (MT == 1 ? D / 16 : 1)], b[0], b[1]);
-                mma16816(s[i][1], w.q[k % (MT == 1 ? D / 16 : 1)], b[2], b[3]);
-            } else {
-                uint32_t q[4];
-                ldsm4((qa ^ (k << 5)) + i * 16 * D * 2, q);
-                mma16816(s[i][0], q, b[0], b[1]);
-                mma16816(s[i][1], q, b[2], b[3]);
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[n][e] *= scale_log2;
+            if (masked && kb + n * 8 + (lane & 3) * 2 + (e & 1) >= w.lim[e >> 1]) s[n][e] = -INFINITY;
+        }
+    }
+    float mn[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        mn[r] = fmaxf(w.m[r], x);
+    }
+    if (__any_sync(0xffffffffu, mn[0] > w.m[0] || mn[1] > w.m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float alpha = mn[r] == -INFINITY ? 1.f : ex2_approx(w.m[r] - mn[r]);
+            w.m[r] = mn[r];
+            w.l[r] *= alpha;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                w.o[n][2 * r] *= alpha;
+                w.o[n][2 * r + 1] *= alpha;
             }
         }
     }
-    uint32_t p[MT][4];
+    uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int r = 0; r < 2; ++r) {
+        const float use = w.m[r] == -INFINITY ? 0.f : w.m[r];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[i][n][e] *= scale_log2;
-                if (masked && kb + n * 8 + (lane & 3) * 2 + (e & 1) >= w.lim[i][e >> 1]) s[i][n][e] = -INFINITY;
-            }
-        }
-        float mn[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float x = fmaxf(fmaxf(s[i][0][2 * r], s[i][0][2 * r + 1]), fmaxf(s[i][1][2 * r], s[i][1][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            mn[r] = fmaxf(w.m[i][r], x);
-        }
-        if (__any_sync(0xffffffffu, mn[0] > w.m[i][0] || mn[1] > w.m[i][1])) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float alpha = mn[r] == -INFINITY ? 1.f : ex2_approx(w.m[i][r] - mn[r]);
-                w.m[i][r] = mn[r];
-                w.l[i][r] *= alpha;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    w.o[i][n][2 * r] *= alpha;
-                    w.o[i][n][2 * r + 1] *= alpha;
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float use = w.m[i][r] == -INFINITY ? 0.f : w.m[i][r];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = ex2_approx(s[i][n][2 * r] - use), p1 = ex2_approx(s[i][n][2 * r + 1] - use);
-                w.l[i][r] += p0 + p1;
-                p[i][2 * n + r] = pack_bf16x2(p0, p1);
-            }
+            const float p0 = ex2_approx(s[n][2 * r] - use), p1 = ex2_approx(s[n][2 * r + 1] - use);
+            w.l[r] += p0 + p1;
+            p[2 * n + r] = pack_bf16x2(p0, p1);
         }
     }
     const uint32_t va = chunk_at<D>(vs, (id & 1) * 8 + l8, id >> 1);
@@ -205,26 +189,22 @@ __device__ __forceinline__ void block16(Rows<D, MT> &w, uint32_t qs, uint32_t ks
     for (int n = 0; n < D / 16; ++n) {
         uint32_t b[4];
         ldsm4t(va ^ (n << 5), b);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            mma16816(w.o[i][2 * n], p[i], b[0], b[1]);
-            mma16816(w.o[i][2 * n + 1], p[i], b[2], b[3]);
-        }
+        mma16816(w.o[2 * n], p, b[0], b[1]);
+        mma16816(w.o[2 * n + 1], p, b[2], b[3]);
     }
 }
 
-// Rows a unit: 16 or 32 with the warps over the keys (ROWS), 64 with the warps over the rows.
+// Rows a unit: 16, 32 or 64, in tiles of 16; KW = 64 / ROWS warps have a tile
+// of rows in common and the blocks of keys in turn.
 template <int D, int ROWS>
 constexpr size_t mma_smem() {
-    return (size_t)kWarps * kStages * 2 * 16 * D * 2 +
-           (ROWS == 64 ? 0 : kWarps * ROWS * sizeof(float2) + (ROWS == 32 ? 32 * D * 2 : 0));
+    return (size_t)kWarps * kStages * 2 * 16 * D * 2 + (ROWS == 64 ? 0 : kWarps * 16 * sizeof(float2));
 }
 
 template <int D, int ROWS, bool WHOLE>
-__global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     paged_mma_kernel(const __grid_constant__ PagedArgs a, int fi, int late) {
-    constexpr bool WIDE = ROWS == 64;
-    constexpr int MT = ROWS == 32 ? 2 : 1;
+    constexpr int KW = 64 / ROWS;
     constexpr uint32_t kBlk = 16 * D * 2;          // bytes of 16 rows
     constexpr uint32_t kStage = kWarps * 2 * kBlk;  // K blocks of the warps, then V blocks
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -247,72 +227,52 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
         const uint32_t st = base + (uint32_t)i % kStages * kStage + warp * kBlk;
         issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk, policy);
     };
+    auto sync_tile = [&]() {  // a warp alone with its keys waits for nobody
+        if (KW == kWarps)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
     PagedUnit u = paged_unit(a, f, fi, walk);
     issue(find(u.t0), u.h, u.t0, 0);
     cp_commit();
     long long ahead = u.t0 + 1 < u.t1 ? find(u.t0 + 1) : -1;  // the next tile's place, when it is of this unit
-    const uint32_t qs = base + kStages * kStage;               // two row tiles: Q [32][D], then the joins' statistics
     for (bool more = true; more;) {
-        Rows<D, MT> w;
+        Rows<D> w;
         int lo, hi;  // the warp's rows: the fewest and the most keys any of them sees
         {
             const PagedSeg &g = walk.g;
-            const int R = g.n * a.G, r0 = u.r0 + (WIDE ? warp * 16 : 0);
-            auto q_at = [&](int row) {
-                return static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(g.tok0 + row / a.G) * a.q_stride +
-                       (int64_t)(u.h * a.G + row % a.G) * D;
-            };
+            const int R = g.n * a.G, r0 = u.r0 + warp / KW * 16;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
+            for (int r = 0; r < 2; ++r) {
+                const int row = r0 + (lane >> 2) + 8 * r;
+                // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
+                w.lim[r] = row < R ? paged_limit(a, g, fi, row) : g.len;
+                w.m[r] = -INFINITY;
+                w.l[r] = 0.f;
+                const bool ok = row < R;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                         (ok ? (int64_t)(g.tok0 + row / a.G) * a.q_stride +
+                                                   (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = r0 + 16 * i + (lane >> 2) + 8 * r;
-                    // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
-                    w.lim[i][r] = row < R ? paged_limit(a, g, fi, row) : g.len;
-                    w.m[i][r] = -INFINITY;
-                    w.l[i][r] = 0.f;
-                    if (MT == 1) {
-                        const bool ok = row < R;
-                        const __nv_bfloat16 *q = (ok ? q_at(row) : static_cast<const __nv_bfloat16 *>(a.q)) + (lane & 3) * 2;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            w.q[k % (MT == 1 ? D / 16 : 1)][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;
-                            w.q[k % (MT == 1 ? D / 16 : 1)][2 + r] =
-                                ok ? *reinterpret_cast<const uint32_t *>(q + k * 16 + 8) : 0u;
-                        }
-                    }
+                for (int k = 0; k < D / 16; ++k) {
+                    w.q[k][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;
+                    w.q[k][2 + r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16 + 8) : 0u;
                 }
             }
-            if (MT > 1) {
-                for (int c = threadIdx.x; c < 16 * MT * (D / 8); c += kWarps * 32) {
-                    const int row = c / (D / 8), ch = c % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r0 + row < R) v = *reinterpret_cast<const uint4 *>(q_at(r0 + row) + ch * 8);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(chunk_at<D>(qs, row, ch)), "r"(v.x),
-                                 "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
-                }
-                __syncthreads();
-            }
-            if (WIDE && r0 >= R) w.lim[0][0] = w.lim[0][1] = 0;  // a warp without rows only loads
+            if (r0 >= R) w.lim[0] = w.lim[1] = 0;  // a warp without rows only loads
         }
-        lo = min(w.lim[0][0], w.lim[0][1]);
-        hi = max(w.lim[0][0], w.lim[0][1]);
-        if (MT > 1) {
-            lo = min(lo, min(w.lim[MT - 1][0], w.lim[MT - 1][1]));
-            hi = max(hi, max(w.lim[MT - 1][0], w.lim[MT - 1][1]));
-        }
+        lo = min(w.lim[0], w.lim[1]);
+        hi = max(w.lim[0], w.lim[1]);
 #pragma unroll
         for (int o = 16; o >= 4; o >>= 1) {
             lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w.o[i][n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) w.o[n][e] = 0.f;
         const int64_t slot = u.base + (int64_t)blockIdx.x * ROWS;
         const int rows = u.rows;
         for (int t = u.t0, t1 = u.t1; t < t1; ++t, ++it) {
@@ -331,32 +291,21 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
             }
             cp_commit();
             cp_wait<1>();
-            if (WIDE)
-                __syncthreads();
-            else
-                __syncwarp();
+            sync_tile();
             const uint32_t st = base + (uint32_t)it % kStages * kStage;
 #pragma unroll 1
-            for (int b = WIDE ? 0 : warp; b < (WIDE ? kWarps : warp + 1); ++b) {
+            for (int b = warp % KW * (kWarps / KW), e = b + kWarps / KW; b < e; ++b) {
                 const int kb = t * kKT + b * 16;
-                if (kb < hi)
-                    block16<D, MT>(w, qs, st + b * kBlk, st + (kWarps + b) * kBlk, kb, kb + 16 > lo, a.scale_log2);
+                if (kb < hi) block16<D>(w, st + b * kBlk, st + (kWarps + b) * kBlk, kb, kb + 16 > lo, a.scale_log2);
             }
-            // the stage may be filled again
-            if (WIDE)
-                __syncthreads();
-            else
-                __syncwarp();
+            sync_tile();  // the stage may be filled again
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {  // the four lanes of a row hold different keys
-                w.l[i][r] += __shfl_xor_sync(0xffffffffu, w.l[i][r], 1);
-                w.l[i][r] += __shfl_xor_sync(0xffffffffu, w.l[i][r], 2);
-            }
+        for (int r = 0; r < 2; ++r) {  // the four lanes of a row hold different keys
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 2);
         }
-        if (WIDE) {
+        if (KW == 1) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = warp * 16 + (lane >> 2) + 8 * r;
@@ -365,48 +314,47 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 32 ? 2 : 3)
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
                     *reinterpret_cast<float2 *>(f.acc + at * D + n * 8 + (lane & 3) * 2) =
-                        make_float2(w.o[0][n][2 * r], w.o[0][n][2 * r + 1]);
-                if ((lane & 3) == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(w.m[0][r], w.l[0][r]);
+                        make_float2(w.o[n][2 * r], w.o[n][2 * r + 1]);
+                if ((lane & 3) == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(w.m[r], w.l[r]);
             }
         } else {
-            // the warps' partials, 16 rows at a time, joined in the stage that was used last (the other one is
-            // being filled); float c of a row lies at c ^ 8 (row & 7), to spread the rows over the banks
+            // the warps' partials, joined in the stage that was used last (the other one is being filled);
+            // float c of a row lies at c ^ 8 (row & 7), to spread the rows over the banks
             float *all = reinterpret_cast<float *>(smem + (uint32_t)(it - 1) % kStages * kStage);
-            float2 *ml = reinterpret_cast<float2 *>(smem + kStages * kStage + (MT > 1 ? 32 * D * 2 : 0));  // [kWarps][16]
+            float2 *ml = reinterpret_cast<float2 *>(smem + kStages * kStage);  // [kWarps][16]
+            __syncthreads();  // every warp is done with the stage
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                __syncthreads();  // every warp is done with the stage
+            for (int r = 0; r < 2; ++r) {
+                const int row = (lane >> 2) + 8 * r;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = (lane >> 2) + 8 * r;
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2 *>(all + (warp * 16 + row) * D +
+                                                ((n * 8 + (lane & 3) * 2) ^ (8 * (row & 7)))) =
+                        make_float2(w.o[n][2 * r], w.o[n][2 * r + 1]);
+                if ((lane & 3) == 0) ml[warp * 16 + row] = make_float2(w.m[r], w.l[r]);
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int row = warp; row < rows; row += kWarps) {
+                const int j0 = row / 16 * KW * 16 + row % 16;  // its row in the first of its tile's warps
+                float M = -INFINITY, L = 0.f, acc[D / 32];
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        *reinterpret_cast<float2 *>(all + (warp * 16 + row) * D +
-                                                    ((n * 8 + (lane & 3) * 2) ^ (8 * (row & 7)))) =
-                            make_float2(w.o[i][n][2 * r], w.o[i][n][2 * r + 1]);
-                    if ((lane & 3) == 0) ml[warp * 16 + row] = make_float2(w.m[i][r], w.l[i][r]);
+                for (int j = 0; j < KW; ++j) M = fmaxf(M, ml[j0 + j * 16].x);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    const float2 v = ml[j0 + j * 16];
+                    const float wt = M == -INFINITY ? 0.f : ex2_approx(v.x - M);
+                    L += wt * v.y;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e)
+                        acc[e] = fmaf(wt, all[(j0 + j * 16) * D + ((lane + 32 * e) ^ (8 * (row & 7)))], acc[e]);
                 }
-                __syncthreads();
-                for (int row = warp; row < 16 && 16 * i + row < rows; row += kWarps) {
-                    float M = -INFINITY, L = 0.f, acc[D / 32];
+                const int64_t at = slot + row;
 #pragma unroll
-                    for (int j = 0; j < kWarps; ++j) M = fmaxf(M, ml[j * 16 + row].x);
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < kWarps; ++j) {
-                        const float2 v = ml[j * 16 + row];
-                        const float wt = M == -INFINITY ? 0.f : ex2_approx(v.x - M);
-                        L += wt * v.y;
-#pragma unroll
-                        for (int e = 0; e < D / 32; ++e)
-                            acc[e] = fmaf(wt, all[(j * 16 + row) * D + ((lane + 32 * e) ^ (8 * (row & 7)))], acc[e]);
-                    }
-                    const int64_t at = slot + 16 * i + row;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) f.acc[at * D + lane + 32 * e] = acc[e];
-                    if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(M, L);
-                }
+                for (int e = 0; e < D / 32; ++e) f.acc[at * D + lane + 32 * e] = acc[e];
+                if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(M, L);
             }
             __syncthreads();  // the stage may be filled again
         }

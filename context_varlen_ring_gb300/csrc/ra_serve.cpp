@@ -117,7 +117,7 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
         L.o_start[f] = take((size_t)kPagedMaxCtas * 4);
         // the rows themselves (twice where units are halved), and one unit more a CTA
         const int64_t most = paged_rows(f, T, G, max_q_len);
-        const bool wide = most > 32 && dtype == RA_BF16 && d == 128;
+        const bool wide = most > (f ? 16 : 64) && dtype == RA_BF16 && d == 128;
         int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (most <= 16 ? 16 : 64) : 0;
         if (S && wide) rows = std::max(rows, 2 * T * G * Hkv + (int64_t)kPagedMaxWide * kPagedWideRows);
         L.o_acc[f] = take((size_t)rows * d * 4);
@@ -276,13 +276,13 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     enum { kSimt, kMma, kWide } kind[2];
     PagedMaps maps;
     const bool wide =
-        (paged_rows(0, T, a.G, max_q_len) > 32 || (n_groups > 0 && T * a.G > 32)) && paged_tc_maps(a, maps);
+        (paged_rows(0, T, a.G, max_q_len) > 64 || (n_groups > 0 && T * a.G > 16)) && paged_tc_maps(a, maps);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
-        // rows a unit: what fits one warp-level pass over the keys, else the tcgen05 kernel's
+        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  RULEFIG
         const int64_t most = paged_rows(f, T, a.G, max_q_len);
         kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
-        if (most > 32 && wide) kind[f] = kWide;
+        if (most > (f ? 16 : 64) && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
         F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
         F.kt = kind[f] == kWide ? 128 : 64;
