@@ -245,21 +245,22 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st);
 // ------------------------------------------------------------ paged attention
 // Families of segments: 0 the sequences' own keys, 1 the groups' prefixes.
 // Each (segment, tile of `rt` query rows, KV head) is a unit of ceil(keys / kt)
-// key tiles; the units' tiles form one line that the family's `n` CTAs split
-// evenly.  What CTA c computes of a unit whose rows start at partial row
+// key tiles, each weighing what it costs; the units' tiles form one line that
+// the family's `n` CTAs split evenly.  What CTA c computes of a unit whose rows start at partial row
 // `base` goes to partial rows base + rt * c on: along the line units and CTAs
 // only grow, and no unit has more than rt partial rows, so these never meet.
 struct alignas(16) PagedSeg {
     int tok0, n, len, w;               // first query token, query tokens, keys, key tiles
-    long long W0, R0;                  // tiles and partial rows ahead of it
+    long long W0, R0;                  // weight of tiles and partial rows ahead of it
 };
 struct PagedHdr {                      // of each family
-    long long W, per;                  // tiles in all, tiles a CTA
+    long long W, per;                  // weight in all, weight a CTA
     int err, pad[3];
 };
 struct PagedFamily {
     int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
     int halves;                        // units of at most rt / 2 rows: two partials a row, of alternate key tiles
+    int least;                         // least tiles a CTA: fewer cost more in partials than they gain
     PagedHdr *hdr;
     PagedSeg *seg;                     // [S]
     int *start;                        // [n] the segment in which each CTA's run begins

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         base.w += total.w;
     }
     bad = __syncthreads_or(bad);
-    const long long W = bad ? 0 : base.w, per = max(1ll, paged_div(W + f.n - 1, f.n));
+    const long long W = bad ? 0 : base.w, per = paged_per(f, W);
     if (threadIdx.x == 0) {
         if (bad) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
         f.hdr->W = W;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
                 if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m[r], sum);
             }
         }
-        walk.x += u.t1 - u.t0;
+        walk.x += u.weight;
     }
     if (late) pdl_wait();
 }
@@ -311,8 +311,9 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
     if (sg.w == 0) return p;
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * sg.w;
-    const int c0 = (int)paged_div(x, per), c1 = (int)paged_div(x + sg.w - 1, per);
+    const int all = sg.w * paged_weight(a, f, sg);
+    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * all;
+    const int c0 = (int)paged_div(x, per), c1 = (int)paged_div(x + all - 1, per);
     p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
     p.two = alloc > rows ? 1 : 0;
     p.second = rows;
@@ -320,26 +321,28 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
     return p;
 }
 
-// A block per (token, KV head), its WARPS warps over the G query heads and,
-// where there are more warps than heads, over a head's partials: the largest
-// maximum M, the weights 2^(m - M), the weighted sums.  Own keys come first,
-// then the prefix; warps' sums are added in order, so the result does not
-// depend on timing.  Latency bound (a chain of dependent loads: segment,
-// place, maxima, sums): the segments are searched once a block, ahead of the
-// wait for the attention kernels; the place of each head's partials is found
-// by one lane (by every warp, it cost more instructions than the sums: 15
-// instead of FIG us for 64 tokens of 22 partials a row); a lane finds one
-// partial's weight and hands it to its warp, which keeps the loop that all the
-// bytes go through short; few blocks get more warps.
-template <typename TOut, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ float4 sum[WARPS][32 * NV];
+// A block per (token, KV head, up to 8 of its query heads), 8 / HB warps a head:
+// the largest maximum M, the weights 2^(m - M), the weighted sums.  Own keys
+// come first, then the prefix; warps' sums are added in order, so the result
+// does not depend on timing.  Latency bound (a chain of dependent loads:
+// segment, place, maxima, sums): the segments are searched once a block, ahead
+// of the wait for the attention kernels; the place of each head's partials is
+// found by one lane; a lane finds one partial's weight and hands it to its
+// warp, which keeps the loop that all the bytes go through short; where tokens
+// are few, a block has fewer heads and a head more warps.
+constexpr int kJoinWarps = 8;
+
+template <typename TOut, int HB, int NV>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+    constexpr int WPR = kJoinWarps / HB;  // warps a head
+    __shared__ float4 sum[kJoinWarps][32 * NV];
     __shared__ int seg[2];
-    __shared__ Parts parts[WARPS][2];
+    __shared__ Parts parts[HB][2];
     __shared__ PlanShared plan[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x / a.Hkv;
-    const int h = blockIdx.x % a.Hkv;
+    const int blocks = (a.G + HB - 1) / HB;  // of a token and KV head
+    const int64_t t = blockIdx.x / (blocks * a.Hkv);
+    const int hb = (int)(blockIdx.x - t * (blocks * a.Hkv)), h = hb / blocks, g0 = (hb - h * blocks) * HB;
     if (warp == 0) {
         // one token a sequence, no sequence without: token t is sequence t's
         int b = t < a.B && a.cu[t] <= t && t < a.cu[t + 1] ? (int)t : segment_of(a.cu + 1, a.B, t);
@@ -358,8 +361,8 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
     long long per[2] = {1, 1};
     if (a.here) {
         long long W;
-        per[0] = paged_plan_here<WARPS * 32>(a, a.f[0], 0, seg[0], plan[0], W);
-        if (a.n_groups > 0) per[1] = paged_plan_here<WARPS * 32>(a, a.f[1], 1, seg[1], plan[1], W);
+        per[0] = paged_plan_here<kJoinWarps * 32>(a, a.f[0], 0, seg[0], plan[0], W);
+        if (a.n_groups > 0) per[1] = paged_plan_here<kJoinWarps * 32>(a, a.f[1], 1, seg[1], plan[1], W);
     }
     pdl_wait();
     if (seg[0] < 0) return;
@@ -368,124 +371,124 @@ __global__ void __launch_bounds__(WARPS * 32) paged_combine_kernel(const __grid_
             per[i] = __ldcg(&a.f[i].hdr->err) ? 0 : __ldcg(&a.f[i].hdr->per);
             if ((int)threadIdx.x == i && seg[i] >= 0) plan[i].g = paged_seg(a.f[i], seg[i]);
         }
+        __syncthreads();
     }
     if (!per[0] || !per[1]) return;  // an array that is not as it must be: nothing is written
-    int wpr = 1;  // warps a row: a power of two, heads in turn where there are more
-    while (wpr * 2 * a.G <= WARPS) wpr *= 2;
-    const int sub = warp % wpr, at_once = WARPS / wpr, d4 = a.d / 4;
-    for (int g0 = 0; g0 < a.G; g0 += at_once) {
-        __syncthreads();  // the segments are there; the last heads' places have been read
-        if ((int)threadIdx.x < 2 * at_once && g0 + (int)threadIdx.x / 2 < a.G)
-            parts[threadIdx.x / 2][threadIdx.x & 1] =
-                seg[threadIdx.x & 1] < 0 ? Parts{0, 0, 0, 0}
-                                         : find_parts(a, a.f[threadIdx.x & 1], plan[threadIdx.x & 1].g,
-                                                      per[threadIdx.x & 1], t, h, g0 + threadIdx.x / 2);
-        __syncthreads();
-        const int g = g0 + warp / wpr;
-        const bool live = g < a.G;
-        float M = -INFINITY, L = 0.f;
-        float4 o[NV];
+    if (threadIdx.x < 2 * HB && g0 + (int)threadIdx.x / 2 < a.G) {
+        const int i = threadIdx.x & 1;
+        parts[threadIdx.x / 2][i] = seg[i] < 0 ? Parts{0, 0, 0, 0}
+                                               : find_parts(a, a.f[i], plan[i].g, i ? per[1] : per[0], t, h,
+                                                            g0 + threadIdx.x / 2);
+    }
+    __syncthreads();
+    const int sub = warp % WPR, g = g0 + warp / WPR, d4 = a.d / 4;
+    const bool live = g < a.G;
+    float M = -INFINITY, L = 0.f;
+    float4 o[NV];
 #pragma unroll
-        for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) {
-            const int own = parts[warp / wpr][0].cnt, cnt = own + parts[warp / wpr][1].cnt;
-            // the maximum is carried along, as in the attention itself: 32 partials a trip
+    for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+        const int own = parts[warp / WPR][0].cnt, cnt = own + parts[warp / WPR][1].cnt;
+        // the maximum is carried along, as in the attention itself: 32 partials a trip
 #pragma unroll 1
-            for (int i0 = 0; i0 < cnt; i0 += 32) {
-                int i = i0 + lane;
-                const int fi = i < own ? 0 : 1;
-                const Parts &p = parts[warp / wpr][fi];
-                if (fi) i -= own;
-                const float *src = nullptr;
-                float2 v = make_float2(-INFINITY, 0.f);
-                if (i < p.cnt) {
-                    const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
-                    v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
-                    src = a.f[fi].acc + row * a.d;
-                }
-                float Mn = v.x;
+        for (int i0 = 0; i0 < cnt; i0 += 32) {
+            int i = i0 + lane;
+            const int fi = i < own ? 0 : 1;
+            const Parts &p = parts[warp / WPR][fi];
+            if (fi) i -= own;
+            const float *src = nullptr;
+            float2 v = make_float2(-INFINITY, 0.f);
+            if (i < p.cnt) {
+                const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
+                v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
+                src = a.f[fi].acc + row * a.d;
+            }
+            float Mn = v.x;
 #pragma unroll
-                for (int s = 16; s; s >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, s));
-                Mn = fmaxf(M, Mn);
-                if (Mn == -INFINITY) continue;
-                const float alpha = exp2f(M - Mn), w = exp2f(v.x - Mn);
-                M = Mn;
-                L = L * alpha + w * v.y;
+            for (int s = 16; s; s >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, s));
+            Mn = fmaxf(M, Mn);
+            if (Mn == -INFINITY) continue;
+            const float alpha = exp2f(M - Mn), w = exp2f(v.x - Mn);
+            M = Mn;
+            L = L * alpha + w * v.y;
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                o[e].x *= alpha;
+                o[e].y *= alpha;
+                o[e].z *= alpha;
+                o[e].w *= alpha;
+            }
+            const int most = min(32, cnt - i0);
+#pragma unroll 4
+            for (int k = sub; k < most; k += WPR) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                const float4 *q = reinterpret_cast<const float4 *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+                // (a partial without weight may never have been written)
 #pragma unroll
                 for (int e = 0; e < NV; ++e) {
-                    o[e].x *= alpha;
-                    o[e].y *= alpha;
-                    o[e].z *= alpha;
-                    o[e].w *= alpha;
-                }
-                const int most = min(32, cnt - i0);
-#pragma unroll 4
-                for (int k = sub; k < most; k += wpr) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k);
-                    const float4 *q = reinterpret_cast<const float4 *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
-                    // (a partial without weight may never have been written)
-#pragma unroll
-                    for (int e = 0; e < NV; ++e) {
-                        if (wk != 0.f && lane + 32 * e < d4) {
-                            const float4 x = __ldcg(q + lane + 32 * e);
-                            o[e].x = fmaf(wk, x.x, o[e].x);
-                            o[e].y = fmaf(wk, x.y, o[e].y);
-                            o[e].z = fmaf(wk, x.z, o[e].z);
-                            o[e].w = fmaf(wk, x.w, o[e].w);
-                        }
+                    if (wk != 0.f && lane + 32 * e < d4) {
+                        const float4 x = __ldcg(q + lane + 32 * e);
+                        o[e].x = fmaf(wk, x.x, o[e].x);
+                        o[e].y = fmaf(wk, x.y, o[e].y);
+                        o[e].z = fmaf(wk, x.z, o[e].z);
+                        o[e].w = fmaf(wk, x.w, o[e].w);
                     }
                 }
             }
-#pragma unroll
-            for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
         }
-        if (wpr > 1) {  // (then every head has its warps at once: one trip of the outer loop)
 #pragma unroll
-            for (int e = 0; e < NV; ++e) sum[warp][lane + 32 * e] = o[e];
-            __syncthreads();
-        }
-        if (!live) continue;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int head = h * a.G + g;
-        TOut *out = static_cast<TOut *>(a.out) + (t * a.Hq + head) * a.d;
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            const int c = lane + 32 * e;
-            if (c >= d4 || (wpr > 1 && sub != e)) continue;  // (of several warps, warp e of the row writes vector e)
-            float4 v = o[e];
-            if (wpr > 1) {
-                v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-                for (int i = 0; i < wpr; ++i) {
-                    const float4 x = sum[warp - sub + i][c];
-                    v.x += x.x;
-                    v.y += x.y;
-                    v.z += x.z;
-                    v.w += x.w;
-                }
-            }
-            if constexpr (sizeof(TOut) == 4) {
-                *reinterpret_cast<float4 *>(out + c * 4) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            } else {
-                uint2 pk;
-                pk.x = pack_bf16x2(v.x * inv, v.y * inv);
-                pk.y = pack_bf16x2(v.z * inv, v.w * inv);
-                *reinterpret_cast<uint2 *>(out + c * 4) = pk;
-            }
-        }
-        if (sub == 0 && lane == 0)
-            a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
     }
+    if (WPR > 1) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) sum[warp][lane + 32 * e] = o[e];
+        __syncthreads();
+    }
+    if (!live) return;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int head = h * a.G + g;
+    TOut *out = static_cast<TOut *>(a.out) + (t * a.Hq + head) * a.d;
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+        const int c = lane + 32 * e;
+        if (c >= d4 || (WPR > 1 && sub != e)) continue;  // (of several warps, warp e of the head writes vector e)
+        float4 v = o[e];
+        if (WPR > 1) {
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) {
+                const float4 x = sum[warp - sub + i][c];
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+        }
+        if constexpr (sizeof(TOut) == 4) {
+            *reinterpret_cast<float4 *>(out + c * 4) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        } else {
+            uint2 pk;
+            pk.x = pack_bf16x2(v.x * inv, v.y * inv);
+            pk.y = pack_bf16x2(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2 *>(out + c * 4) = pk;
+        }
+    }
+    if (sub == 0 && lane == 0)
+        a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <typename TOut>
+template <typename TOut, int NV>
 cudaError_t combine_as(const PagedArgs &a, cudaStream_t st) {
-    const int64_t blocks = a.T * a.Hkv;  // < 2^31
-    auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, (unsigned)blocks, warps * 32, 0, st, a); };
-    const bool few = blocks <= 2 * paged_sms();
-    if (a.d <= 128) return few ? go(paged_combine_kernel<TOut, 16, 1>, 16) : go(paged_combine_kernel<TOut, 8, 1>, 8);
-    return few ? go(paged_combine_kernel<TOut, 16, 2>, 16) : go(paged_combine_kernel<TOut, 8, 2>, 8);
+    // heads a block: as many as it takes to leave every SM two blocks
+    auto blocks = [&](int hb) { return a.T * a.Hkv * ((a.G + hb - 1) / hb); };  // < 2^31
+    int hb = 1;
+    while (hb < 8 && hb < a.G && blocks(2 * hb) >= 2 * paged_sms()) hb *= 2;
+    auto go = [&](auto kernel) { return launch_pdl(kernel, (unsigned)blocks(hb), kJoinWarps * 32, 0, st, a); };
+    return hb == 1   ? go(paged_combine_kernel<TOut, 1, NV>)
+           : hb == 2 ? go(paged_combine_kernel<TOut, 2, NV>)
+           : hb == 4 ? go(paged_combine_kernel<TOut, 4, NV>)
+                     : go(paged_combine_kernel<TOut, 8, NV>);
 }
 
 }  // namespace
@@ -525,7 +528,8 @@ cudaError_t launch_paged_simt(const PagedArgs &a, int fi, int late, cudaStream_t
 }
 
 cudaError_t launch_paged_combine(const PagedArgs &a, cudaStream_t st) {
-    return a.out_dtype == RA_FP32 ? combine_as<float>(a, st) : combine_as<__nv_bfloat16>(a, st);
+    if (a.out_dtype == RA_FP32) return a.d <= 128 ? combine_as<float, 1>(a, st) : combine_as<float, 2>(a, st);
+    return a.d <= 128 ? combine_as<__nv_bfloat16, 1>(a, st) : combine_as<__nv_bfloat16, 2>(a, st);
 }
 
 }  // namespace ra

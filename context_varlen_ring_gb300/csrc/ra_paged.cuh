@@ -23,7 +23,7 @@ __device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
 
 struct PagedUnit {
     int r0, rows, h;     // first query row in the segment, query rows, KV head
-    int t0, t1;          // the CTA's key tiles in it
+    int t0, t1, weight;  // the CTA's key tiles in it (none, it may be), their part of the line
     long long base;      // first partial row (of CTA 0)
 };
 
@@ -47,9 +47,19 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     g.W0 = g.R0 = 0;
     return fine;
 }
-// Its key tiles and partial rows over all units.  (n * G < 2^31.)
+// What a key tile of the segment weighs.  Of the kernel with halved units, a
+// tile for two row tiles takes 2.0 us, one of alternating tiles for a single
+// row tile 1.0 to 1.4 (bound by its softmax, or by memory).
+__device__ __forceinline__ int paged_weight(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
+    return !f.halves ? 1 : g.n * a.G * 2 > f.rt ? 3 : 2;
+}
+// Its key tiles' weight and its partial rows over all units.  (n * G < 2^31.)
 __device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * g.w;
+    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * g.w * paged_weight(a, f, g);
+}
+// The weight of a CTA's run.
+__device__ __forceinline__ long long paged_per(const PagedFamily &f, long long W) {
+    return max((long long)f.least, paged_div(W + f.n - 1, f.n));
 }
 __device__ __forceinline__ long long paged_rows(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
     const int R = g.n * a.G, full = R / f.rt * f.rt;
@@ -142,7 +152,7 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
         W += sh.w[i];
         bad |= sh.bad[i];
     }
-    const long long per = max(1ll, paged_div(W + f.n - 1, f.n));
+    const long long per = paged_per(f, W);
     if (bad) {
         if (threadIdx.x == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
         W = 0;
@@ -208,10 +218,13 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedF
         }
     }
     const long long rel = k.x - k.g.W0;
-    const int lu = (int)paged_div(rel, k.g.w), rtile = lu / a.Hkv;
+    const int wt = paged_weight(a, f, k.g), all = k.g.w * wt;  // (w is below 2^26 keys' tiles)
+    const int lu = (int)paged_div(rel, all), rtile = lu / a.Hkv;
+    const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
     PagedUnit u;
-    u.t0 = (int)(rel - (long long)lu * k.g.w);
-    u.t1 = (int)min((long long)k.g.w, u.t0 + (k.x1 - k.x));
+    u.t0 = (from + wt - 1) / wt;  // a tile belongs to the run in which it begins
+    u.t1 = (to + wt - 1) / wt;
+    u.weight = to - from;
     u.h = lu - rtile * a.Hkv;
     u.r0 = rtile * f.rt;
     u.rows = min(f.rt, k.g.n * a.G - u.r0);

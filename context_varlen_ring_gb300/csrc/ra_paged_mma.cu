@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
                 issue(ahead, u.h, t + 1, it + 1);
                 if (t + 2 < t1) ahead = find(t + 2);
             } else {
-                walk.x += t1 - u.t0;
+                walk.x += u.weight;
                 more = walk.x < walk.x1;
                 if (more) {
                     u = paged_unit(a, f, fi, walk);

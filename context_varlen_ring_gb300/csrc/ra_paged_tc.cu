@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         w.pair = w.u.rows > 128;
         const int sees = paged_limit(a, w.g, p.fi, w.u.r0 + w.u.rows - 1);
         w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
-        k.x += w.u.t1 - w.u.t0;
+        k.x += w.u.weight;
         if (lane == 0) place[warp] = k;
         __syncwarp();
         return w;
