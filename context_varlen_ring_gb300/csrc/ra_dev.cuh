@@ -152,7 +152,7 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, uin
 // (code, tables, partial results) is not pushed out by it.
 __device__ __forceinline__ uint64_t l2_evict_first() {
     uint64_t p;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 __device__ __forceinline__ void tma_load_4d_hint(void *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1, int c2,

@@ -158,10 +158,9 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ PlanShared plan;
     PagedWalk walk = paged_begin<WARPS * 32>(a, f, fi, plan);
-    while (walk.x < walk.x1) {
-        const PagedUnit u = paged_unit(a, f, fi, walk);
-        const PagedSeg &g = walk.g;
-        const int s = walk.s;
+    for (PagedUnit u; paged_unit(a, f, fi, walk, u);) {
+        const PagedUnit &g = u;
+        const int s = u.s;
         const int R = g.n * a.G, r0 = u.r0;
         __syncthreads();  // the last unit's readers are done with Q
         for (int i = threadIdx.x; i < RT * (D / 4); i += WARPS * 32) {
@@ -267,7 +266,6 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
                 if (lane == 0) *reinterpret_cast<float2 *>(f.ml + at * 2) = make_float2(m[r], sum);
             }
         }
-        walk.x += u.weight;
     }
     if (late) pdl_wait();
 }
@@ -298,26 +296,28 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int late, int *ctas, cu
 }
 
 // ------------------------------------------------------------------ join
-// The partials of a token and query head in a family: cnt of them, the i-th at
-// partial row  at + (i >> two) * rt + (i & two) * second.
+// The partials of a token and query head in a family: cnt of them, the i-th
+// (of CTA c0 + (i >> two)) at partial row  at + (i >> two) * rt + (i & two) * second.
 struct Parts {
-    long long at;
-    int cnt, two, second;
+    long long at, x;  // x: the unit's place in the line
+    int cnt, two, second, c0, wt, all;
 };
 
 __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, const PagedSeg &sg, long long per,
                                             int64_t t, int h, int g) {
-    Parts p{0, 0, 0, 0};
+    Parts p{};
     if (sg.w == 0) return p;
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    const int all = sg.w * paged_weight(a, f, sg);
-    const long long x = sg.W0 + (long long)(rtile * a.Hkv + h) * all;
-    const int c0 = (int)paged_div(x, per), c1 = (int)paged_div(x + all - 1, per);
-    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)c0 * f.rt + r % f.rt;
+    p.wt = paged_weight(a, f, sg);
+    p.all = sg.w * p.wt;
+    p.x = sg.W0 + (long long)(rtile * a.Hkv + h) * p.all;
+    const int c1 = (int)paged_div(p.x + p.all - 1, per);
+    p.c0 = (int)paged_div(p.x, per);
+    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)p.c0 * f.rt + r % f.rt;
     p.two = alloc > rows ? 1 : 0;
     p.second = rows;
-    p.cnt = (c1 - c0 + 1) << p.two;
+    p.cnt = (c1 - p.c0 + 1) << p.two;
     return p;
 }
 
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
     if (!per[0] || !per[1]) return;  // an array that is not as it must be: nothing is written
     if (threadIdx.x < 2 * HB && g0 + (int)threadIdx.x / 2 < a.G) {
         const int i = threadIdx.x & 1;
-        parts[threadIdx.x / 2][i] = seg[i] < 0 ? Parts{0, 0, 0, 0}
+        parts[threadIdx.x / 2][i] = seg[i] < 0 ? Parts{}
                                                : find_parts(a, a.f[i], plan[i].g, i ? per[1] : per[0], t, h,
                                                             g0 + threadIdx.x / 2);
     }
@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
             if (fi) i -= own;
             const float *src = nullptr;
             float2 v = make_float2(-INFINITY, 0.f);
-            if (i < p.cnt) {
+            const long long run = (p.c0 + (i >> p.two)) * (fi ? per[1] : per[0]) - p.x;  // its CTA's place in the unit
+            const int from = (int)max(0ll, run), to = (int)min((long long)p.all, run + (fi ? per[1] : per[0]));
+            if (i < p.cnt && paged_tile(from, p.wt) < paged_tile(to, p.wt)) {  // (else it began no tile of the unit)
                 const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
                 v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
                 src = a.f[fi].acc + row * a.d;

@@ -22,8 +22,9 @@ __device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
 }
 
 struct PagedUnit {
+    int s, tok0, n, len; // its segment
     int r0, rows, h;     // first query row in the segment, query rows, KV head
-    int t0, t1, weight;  // the CTA's key tiles in it (none, it may be), their part of the line
+    int t0, t1;          // the CTA's key tiles in it
     long long base;      // first partial row (of CTA 0)
 };
 
@@ -47,12 +48,18 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     g.W0 = g.R0 = 0;
     return fine;
 }
-// What a key tile of the segment weighs.  Of the kernel with halved units, a
-// tile for two row tiles takes 2.0 us, one of alternating tiles for a single
-// row tile 1.0 to 1.4 (bound by its softmax, or by memory).
+// What a key tile of the segment weighs, in sixteenths of a warp-level tile:
+// its own cost and its share of a unit's (queries, join, partial), which is
+// about two tiles.  Of the tcgen05 kernel, a tile for two row tiles takes 2.0
+// us, one of alternating tiles for a single row tile 1.0 to 1.4 (bound by its
+// softmax, or by memory), a unit about 4.
 __device__ __forceinline__ int paged_weight(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return !f.halves ? 1 : g.n * a.G * 2 > f.rt ? 3 : 2;
+    const int tile = !f.halves ? 16 : g.n * a.G * 2 > f.rt ? 48 : 32, unit = f.halves ? 96 : 32;
+    return tile + (g.w ? unit / g.w : 0);
 }
+// The first tile of a unit that begins at or behind place `at` of it: a tile
+// belongs to the run in which it begins.
+__device__ __forceinline__ int paged_tile(int at, int weight) { return (at + weight - 1) / weight; }
 // Its key tiles' weight and its partial rows over all units.  (n * G < 2^31.)
 __device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
     return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * g.w * paged_weight(a, f, g);
@@ -201,40 +208,47 @@ __device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const Paged
     return paged_planned(f);
 }
 
-// The unit at the walk's place (in the next segment with tiles, where the last
-// one's are done), and the CTA's part of it.  Row tiles are outermost in a
-// segment, so CTAs an equal share of the line apart read the same keys for
-// different rows at about the same time (from L2).
-__device__ __forceinline__ PagedUnit paged_unit(const PagedArgs &a, const PagedFamily &f, int fi, PagedWalk &k) {
-    for (long long end; (end = k.g.W0 + paged_tiles(a, f, k.g)) <= k.x;) {
-        ++k.s;
-        if (a.here) {
-            const long long rows = k.g.R0 + paged_rows(a, f, k.g);
-            paged_record(a, f, fi, k.s, k.g);
-            k.g.W0 = end;
-            k.g.R0 = rows;
-        } else {
-            k.g = paged_seg(f, k.s);
+// The CTA's next unit and its tiles there; false where its run has no more.
+// Row tiles are outermost in a segment, so CTAs an equal share of the line
+// apart read the same keys for different rows at about the same time (from L2).
+__device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily &f, int fi, PagedWalk &k, PagedUnit &u) {
+    while (k.x < k.x1) {
+        for (long long end; (end = k.g.W0 + paged_tiles(a, f, k.g)) <= k.x;) {
+            ++k.s;
+            if (a.here) {
+                const long long rows = k.g.R0 + paged_rows(a, f, k.g);
+                paged_record(a, f, fi, k.s, k.g);
+                k.g.W0 = end;
+                k.g.R0 = rows;
+            } else {
+                k.g = paged_seg(f, k.s);
+            }
         }
+        const long long rel = k.x - k.g.W0;
+        const int wt = paged_weight(a, f, k.g), all = k.g.w * wt;  // (at most 2^25 tiles of 16 + 1, or 2^24 of 48 + 1)
+        const int lu = (int)paged_div(rel, all), rtile = lu / a.Hkv;
+        const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
+        k.x += to - from;
+        u.t0 = paged_tile(from, wt);
+        u.t1 = paged_tile(to, wt);
+        if (u.t0 >= u.t1) continue;  // the run ends inside a tile that another one began
+        u.s = k.s;
+        u.tok0 = k.g.tok0;
+        u.n = k.g.n;
+        u.len = k.g.len;
+        u.h = lu - rtile * a.Hkv;
+        u.r0 = rtile * f.rt;
+        u.rows = min(f.rt, k.g.n * a.G - u.r0);
+        u.base = k.g.R0 + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
+        return true;
     }
-    const long long rel = k.x - k.g.W0;
-    const int wt = paged_weight(a, f, k.g), all = k.g.w * wt;  // (w is below 2^26 keys' tiles)
-    const int lu = (int)paged_div(rel, all), rtile = lu / a.Hkv;
-    const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
-    PagedUnit u;
-    u.t0 = (from + wt - 1) / wt;  // a tile belongs to the run in which it begins
-    u.t1 = (to + wt - 1) / wt;
-    u.weight = to - from;
-    u.h = lu - rtile * a.Hkv;
-    u.r0 = rtile * f.rt;
-    u.rows = min(f.rt, k.g.n * a.G - u.r0);
-    u.base = k.g.R0 + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
-    return u;
+    return false;
 }
 
 // Keys that row `row` of the segment sees: all of a prefix, the causal part
 // of the own keys (a row behind the segment's last sees none).
-__device__ __forceinline__ int paged_limit(const PagedArgs &a, const PagedSeg &g, int family, int row) {
+template <typename Seg>
+__device__ __forceinline__ int paged_limit(const PagedArgs &a, const Seg &g, int family, int row) {
     if (row >= g.n * a.G) return 0;
     return family || !a.causal ? g.len : g.len - g.n + row / a.G + 1;
 }

@@ -214,18 +214,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     pdl_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ PlanShared plan;
-    PagedWalk walk = paged_begin<kWarps * 32>(a, f, fi, plan);
-    if (walk.x >= walk.x1) {
-        if (late) pdl_wait();
-        return;
+    // Each warp's place in the CTA's run, and its unit in hand and the next
+    // one: in shared memory, where they hold no registers in the loop over keys.
+    __shared__ PagedWalk place[kWarps];
+    __shared__ PagedUnit units[kWarps][2];
+    {
+        const PagedWalk k = paged_begin<kWarps * 32>(a, f, fi, plan);
+        if (lane == 0) place[warp] = k;
+        __syncwarp();
     }
     const uint64_t policy = l2_evict_first();
     int it = 0;                      // key tiles so far: tile i lies in stage i % kStages
-    // this warp's 16 keys of tile t of the walk's segment
-    auto find = [&](int t) { return find16<WHOLE>(a, f, walk.s, walk.g.len, t * kKT + warp * 16); };
-    auto issue = [&](long long off, int h, int t, int i) {
+    // this warp's 16 keys of tile t
+    auto find = [&](const PagedUnit &u, int t) { return find16<WHOLE>(a, f, u.s, u.len, t * kKT + warp * 16); };
+    auto issue = [&](const PagedUnit &u, long long off, int t, int i) {
         const uint32_t st = base + (uint32_t)i % kStages * kStage + warp * kBlk;
-        issue16<D, WHOLE>(a, off, walk.g.len - (t * kKT + warp * 16), h, st, st + kWarps * kBlk, policy);
+        issue16<D, WHOLE>(a, off, u.len - (t * kKT + warp * 16), u.h, st, st + kWarps * kBlk, policy);
     };
     auto sync_tile = [&]() {  // a warp alone with its keys waits for nobody
         if (KW == kWarps)
@@ -233,26 +237,43 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         else
             __syncthreads();
     };
-    PagedUnit u = paged_unit(a, f, fi, walk);
-    issue(find(u.t0), u.h, u.t0, 0);
-    cp_commit();
-    long long ahead = u.t0 + 1 < u.t1 ? find(u.t0 + 1) : -1;  // the next tile's place, when it is of this unit
-    for (bool more = true; more;) {
+    long long ahead = -1;  // the next tile's place, when it is of the unit in hand
+    for (int i = 0;; ++i) {
+        bool more;
+        {
+            PagedWalk k = place[warp];
+            PagedUnit next;
+            more = paged_unit(a, f, fi, k, next);
+            __syncwarp();
+            if (lane == 0) {
+                place[warp] = k;
+                if (more) units[warp][i & 1] = next;
+            }
+            __syncwarp();
+        }
+        const PagedUnit &nu = units[warp][i & 1];
+        if (i == 0) {
+            if (!more) break;
+            issue(nu, find(nu, nu.t0), nu.t0, 0);
+            cp_commit();
+            if (nu.t0 + 1 < nu.t1) ahead = find(nu, nu.t0 + 1);
+            continue;
+        }
+        const PagedUnit &u = units[warp][(i & 1) ^ 1];
         Rows<D> w;
         int lo, hi;  // the warp's rows: the fewest and the most keys any of them sees
         {
-            const PagedSeg &g = walk.g;
-            const int R = g.n * a.G, r0 = u.r0 + warp / KW * 16;
+            const int R = u.n * a.G, r0 = u.r0 + warp / KW * 16;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = r0 + (lane >> 2) + 8 * r;
                 // (padding rows pass for rows that see all keys: no masks for them, their results are dropped)
-                w.lim[r] = row < R ? paged_limit(a, g, fi, row) : g.len;
+                w.lim[r] = row < R ? paged_limit(a, u, fi, row) : u.len;
                 w.m[r] = -INFINITY;
                 w.l[r] = 0.f;
                 const bool ok = row < R;
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                         (ok ? (int64_t)(g.tok0 + row / a.G) * a.q_stride +
+                                         (ok ? (int64_t)(u.tok0 + row / a.G) * a.q_stride +
                                                    (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -278,16 +299,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         for (int t = u.t0, t1 = u.t1; t < t1; ++t, ++it) {
             // the next tile is on its way while this one is used, the next unit's first one too
             if (t + 1 < t1) {
-                issue(ahead, u.h, t + 1, it + 1);
-                if (t + 2 < t1) ahead = find(t + 2);
-            } else {
-                walk.x += u.weight;
-                more = walk.x < walk.x1;
-                if (more) {
-                    u = paged_unit(a, f, fi, walk);
-                    issue(find(u.t0), u.h, u.t0, it + 1);
-                    if (u.t0 + 1 < u.t1) ahead = find(u.t0 + 1);
-                }
+                issue(u, ahead, t + 1, it + 1);
+                if (t + 2 < t1) ahead = find(u, t + 2);
+            } else if (more) {
+                issue(nu, find(nu, nu.t0), nu.t0, it + 1);
+                if (nu.t0 + 1 < nu.t1) ahead = find(nu, nu.t0 + 1);
             }
             cp_commit();
             cp_wait<1>();
@@ -358,6 +374,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
             }
             __syncthreads();  // the stage may be filled again
         }
+        if (!more) break;
     }
     if (late) pdl_wait();  // the join waits for this kernel only: it must not end ahead of its predecessor
 }

@@ -61,9 +61,7 @@ struct TcParams {
 // What one CTA does of one unit: steps of one key tile (two row tiles) or of
 // two key tiles (one row tile).
 struct Walk {
-    PagedSeg g;
     PagedUnit u;
-    int s;
     bool pair;  // two row tiles
     int tend;   // key tiles [u.t0, tend): those that any row sees
 };
@@ -169,21 +167,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         asm volatile("bar.arrive 2, 384;" ::: "memory");  // the softmax warps read theirs
     }
     // The CTA's units in order, the same for every role.
-    auto more = [&]() { return place[warp].x < place[warp].x1; };
-    auto next_unit = [&]() {
-        Walk w;
+    auto next_unit = [&](Walk &w) {
         PagedWalk k = place[warp];
         __syncwarp();
-        w.u = paged_unit(a, f, p.fi, k);
-        w.g = k.g;
-        w.s = k.s;
-        w.pair = w.u.rows > 128;
-        const int sees = paged_limit(a, w.g, p.fi, w.u.r0 + w.u.rows - 1);
-        w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
-        k.x += w.u.weight;
+        if (!paged_unit(a, f, p.fi, k, w.u)) return false;
         if (lane == 0) place[warp] = k;
         __syncwarp();
-        return w;
+        w.pair = w.u.rows > 128;
+        const int sees = paged_limit(a, w.u, p.fi, w.u.r0 + w.u.rows - 1);
+        w.tend = min(w.u.t1, max(w.u.t0, (sees + 127) / 128));
+        return true;
     };
 
     // Registers: 128 x 80 + 256 x 200 = 61440, within the 384 x 168 = 64512 of the launch.
@@ -200,9 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tma_prefetch_desc(&p.tmV);
             }
             const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
-            while (ok && more()) {
-                const Walk w = next_unit();
-                const int tok = w.g.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
+            for (Walk w; ok && next_unit(w);) {
+                const int tok = w.u.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
                 if (lane == 0) {
                     if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1u, wc);
                     if (ok) {
@@ -220,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     const int key = t * 128 + (lane >> 1) * p.box;
                     page = (int)a.n_pages;  // outside the cache: filled with zeros
                     row = key % a.page_size;
-                    if (lane < boxes && key < w.g.len) {
-                        const int pg = __ldg(f.table + (int64_t)w.s * f.width + key / a.page_size);
+                    if (lane < boxes && key < w.u.len) {
+                        const int pg = __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size);
                         if (pg >= 0 && pg < a.n_pages)
                             page = pg;
                         else
@@ -281,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 return kvs + (i % kSlots) * kTile;
             };
             auto empty = [&](uint32_t i) { tc_commit_w(kv_empty + i % kSlots); };
-            while (ok && more()) {
-                const Walk w = next_unit();
+            for (Walk w; ok && next_unit(w);) {
                 ok = mbar_wait_warp(q_full, nu & 1u, wc);
                 ++nu;
                 tc_fence_after();
@@ -290,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int by = w.pair ? 1 : 2;
                 // V rows behind the length, up to the end of their page, may hold anything
                 auto clean = [&](int t, uint32_t i) {
-                    const int live = w.g.len - t * 128;
-                    if (live >= 128 || w.g.len % a.page_size == 0) return;
+                    const int live = w.u.len - t * 128;
+                    if (live >= 128 || w.u.len % a.page_size == 0) return;
                     uint8_t *v = base + kOffKV + (i % kSlots) * kTile;
                     for (int c = live * 8 + lane; c < 1024; c += 32) {
                         *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);
@@ -469,14 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 w.pair = true;
                 w.u.rows = 0;
             } else {
-                if (!more()) break;
-                w = next_unit();
+                if (!next_unit(w)) break;
             }
             const int by = w.pair ? 1 : 2;
             const int row = (w.pair ? 128 * k : 0) + m;  // of the unit
             const bool valid = row < w.u.rows;
             // (padding rows hold other tokens' queries or zeros: computed without masks, dropped)
-            const int lim = dry ? 128 : valid ? paged_limit(a, w.g, p.fi, w.u.r0 + row) : w.g.len;
+            const int lim = dry ? 128 : valid ? paged_limit(a, w.u, p.fi, w.u.r0 + row) : w.u.len;
             // a warp of padding rows only keeps the barriers going
             const bool busy = dry || __any_sync(0xffffffffu, valid);
             m_run = -INFINITY;

@@ -287,7 +287,7 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
         F.kt = kind[f] == kWide ? 128 : 64;
         F.halves = kind[f] == kWide;
-        F.least = kind[f] == kWide ? 4 : kind[f] == kMma && F.rt == 64 ? 2 : 1;  // MINFIG
+        F.least = kind[f] == kWide ? 64 : kind[f] == kMma && F.rt == 64 ? 32 : 16;  // MINFIG
         if (F.S)
             F.n = kind[f] == kWide  ? std::min(kPagedMaxWide, paged_sms())
                   : kind[f] == kMma ? paged_mma_ctas(F.rt, d, cache->page_size)
