@@ -26,6 +26,8 @@ namespace ra {
 namespace {
 
 constexpr int kRopeWarps = 4;
+constexpr int kBulkWarps = 8, kBulkStages = 4;
+constexpr int64_t kBulkTokens = 4096;
 
 template <typename T, int VEC>
 struct Pack;
@@ -59,6 +61,34 @@ __device__ __forceinline__ typename Pack<T, VEC>::V repack(const float (&f)[VEC]
 #pragma unroll
     for (int i = 0; i < VEC; ++i) e[i] = (T)f[i];  // round to nearest even: the one rounding of the result
     return v;
+}
+
+// The rotation of one unit, the same arithmetic in both kernels below: a
+// product, rounded, and a fused product and sum.  Half-split pairs: two
+// vectors; neighbouring pairs: one, with half as many angles.
+template <typename T, int VEC, bool ADJ, int NP>
+__device__ __forceinline__ void turn_unit(typename Pack<T, VEC>::V &a, typename Pack<T, VEC>::V &b,
+                                          const float (&c)[NP], const float (&s)[NP]) {
+    float fa[VEC], fb[VEC];
+    unpack<T, VEC>(a, fa);
+    if (VEC > 1 && ADJ) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const float x = fa[(2 * e) % VEC], y = fa[(2 * e + 1) % VEC];
+            fa[(2 * e) % VEC] = fmaf(x, c[e], -__fmul_rn(y, s[e]));
+            fa[(2 * e + 1) % VEC] = fmaf(x, s[e], __fmul_rn(y, c[e]));
+        }
+    } else {
+        unpack<T, VEC>(b, fb);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float x = fa[e], y = fb[e];
+            fa[e] = fmaf(x, c[e % NP], -__fmul_rn(y, s[e % NP]));
+            fb[e] = fmaf(x, s[e % NP], __fmul_rn(y, c[e % NP]));
+        }
+        b = repack<T, VEC>(fb);
+    }
+    a = repack<T, VEC>(fa);
 }
 
 // A warp owns a token, or where tokens are few every S-th group of its heads.
@@ -133,7 +163,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
             off1 = p.n_pairs + u * VEC;
             pb = u * VEC;
         }
-        float2 r[NP];
+        float rc[NP], rs[NP];
         bool loaded = false;
         int skip = sub;  // groups of heads ahead of this warp's first in the next job
         for (int j = 0; j < p.njobs; ++j) {
@@ -162,7 +192,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
                     loaded = true;
                     if (rot && mine) {
 #pragma unroll
-                        for (int e = 0; e < NP; ++e) r[e] = cs[pb + e];
+                        for (int e = 0; e < NP; ++e) {
+                            const float2 r = cs[pb + e];
+                            rc[e] = r.x;
+                            rs[e] = r.y;
+                        }
                     }
                 }
                 if (ok < (jb.paged ? 2 : 1) || (jb.x == jb.y && !turn)) continue;  // (in place and passed through)
@@ -171,28 +205,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < UN; ++i) {
                     if (h + i * step >= heads) continue;
-                    if (turn) {
-                        float fa[VEC], fb[VEC];
-                        unpack<T, VEC>(a[i], fa);
-                        if (VEC > 1 && ADJ) {
-#pragma unroll
-                            for (int e = 0; e < NP; ++e) {
-                                const float x0 = fa[(2 * e) % VEC], x1 = fa[(2 * e + 1) % VEC];
-                                fa[(2 * e) % VEC] = x0 * r[e].x - x1 * r[e].y;
-                                fa[(2 * e + 1) % VEC] = x0 * r[e].y + x1 * r[e].x;
-                            }
-                        } else {
-                            unpack<T, VEC>(b[i], fb);
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) {
-                                const float x0 = fa[e], x1 = fb[e];
-                                fa[e] = x0 * r[e % NP].x - x1 * r[e % NP].y;
-                                fb[e] = x0 * r[e % NP].y + x1 * r[e % NP].x;
-                            }
-                            b[i] = repack<T, VEC>(fb);
-                        }
-                        a[i] = repack<T, VEC>(fa);
-                    }
+                    if (turn) turn_unit<T, VEC, ADJ, NP>(a[i], b[i], rc, rs);
                     T *yh = y + (h + i * step + hh) * hs;
                     *reinterpret_cast<V *>(yh + off0) = a[i];
                     if (off1 >= 0) *reinterpret_cast<V *>(yh + off1) = b[i];
@@ -200,6 +213,180 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
             }
         }
     }
+}
+
+// The same for many tokens: each warp streams a run of consecutive tokens
+// through a ring in shared memory, copied in and out by the bulk-copy engine.
+// A token's queries, keys and values lie one behind the other in a stage; the
+// rotated units are read, turned and written back in place.  So the bytes in
+// flight are the rings' (some 100 KB an SM) and no thread's registers wait for
+// memory.  Consecutive tokens share their sequence and page, whose search is
+// repeated only at their ends.
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int VEC = 16 / (int)sizeof(T), NP = ADJ ? VEC / 2 : VEC;
+    using V = typename Pack<T, VEC>::V;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    uint8_t *ring = smem + (size_t)warp * p.stages * p.stage_bytes;
+    float2 *cs = reinterpret_cast<float2 *>(smem + (size_t)warps * p.stages * p.stage_bytes) + warp * p.n_pairs;
+    __shared__ uint64_t full[kBulkWarps][kBulkStages];
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < p.stages; ++i) dev::mbar_init(&full[warp][i], 1);
+        dev::fence_mbar_init();
+    }
+    __syncthreads();
+    const dev::WaitCtl wc{&abort_flag, p.status, p.budget_ns};
+
+    const int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * p.chunk, t1 = min(p.T, t0 + p.chunk);
+    const int hpi = 32 / p.rot_units, hh = lane / p.rot_units, u = lane % p.rot_units;
+    const int off0 = u * 16, off1 = p.n_pairs * (int)sizeof(T) + u * 16, pb = u * NP;
+    const int row = p.d * (int)sizeof(T);
+    int rotated = 0;  // heads, which come first
+    for (int j = 0; j < p.njobs; ++j) rotated += p.jobs[j].rotate ? p.jobs[j].heads : 0;
+    // this lane's pairs: angle a position, and where its positions are
+    unsigned long long turns[4];
+    const int32_t *pos_at[4];
+    int pos[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int w = min(lane + 32 * k, p.n_pairs - 1);
+        turns[k] = p.turns[w];
+        pos_at[k] = p.pos + (int64_t)p.axis[w] * p.T;
+        pos[k] = t0 < t1 ? __ldg(pos_at[k] + t0) : 0;
+    }
+    auto load = [&](int64_t t) {  // lane 0
+        const int st = (int)((t - t0) % p.stages);
+        uint8_t *dst = ring + (size_t)st * p.stage_bytes;
+        dev::mbar_arrive_expect_tx(&full[warp][st], p.token_bytes);
+        for (int j = 0; j < p.njobs; ++j) {
+            dev::bulk_load(dst, static_cast<const T *>(p.jobs[j].x) + t * p.jobs[j].x_stride, p.jobs[j].heads * row,
+                           &full[warp][st]);
+            dst += p.jobs[j].heads * row;
+        }
+    };
+    int64_t loaded = t0;
+    if (lane == 0)
+        for (; loaded < min(t1, t0 + p.stages - 2); ++loaded) load(loaded);
+    // the sequence of the token in hand, and its page
+    int seq = -1, page = -1, page_i = -1;
+    long long c0 = 0, c1 = -1, len = 0;
+    for (int64_t t = t0; t < t1; ++t) {
+        const int st = (int)((t - t0) % p.stages);
+        // the stores of the token before last have read their stage: it takes the next token but (stages - 3)
+        dev::bulk_wait_read<1>();
+        __syncwarp();
+        if (lane == 0 && loaded < t1) load(loaded++);
+        int ok = 1;
+        long long off = 0;
+        if (p.cu) {
+            if (t >= c1) {
+                seq = dev::segment_of(p.cu + 1, p.B, t);
+                page_i = -1;
+                if (seq < p.B) {
+                    c0 = p.cu[seq];
+                    c1 = p.cu[seq + 1];
+                    len = p.kv_lens[seq];
+                } else {
+                    c1 = p.T;  // behind the last sequence, to the end
+                }
+            }
+            ok = 0;
+            if (seq < p.B) {
+                const long long idx = len - (c1 - c0) + (t - c0);
+                bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
+                if (in) {
+                    const int pi = (int)idx / p.page_size;
+                    if (pi != page_i) {
+                        page_i = pi;
+                        page = p.page_table[(int64_t)seq * p.table_width + pi];
+                    }
+                    in = page >= 0 && page < p.n_pages;
+                    off = page * p.page_stride + ((int)idx - pi * p.page_size) * p.token_stride;
+                }
+                ok = in ? 2 : 1;
+                if (!in && lane == 0) dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int w = lane + 32 * k;
+            if (w < p.n_pairs) {
+                const unsigned long long turn = (unsigned long long)(long long)pos[k] * turns[k];
+                float s, c;
+                sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
+                cs[w] = make_float2(c, p.inverse ? -s : s);
+                if (t + 1 < t1) pos[k] = __ldg(pos_at[k] + t + 1);
+            }
+        }
+        __syncwarp();
+        float rc[NP], rs[NP];
+        if (hh < hpi) {
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float2 r = cs[pb + e];
+                rc[e] = r.x;
+                rs[e] = r.y;
+            }
+        }
+        if (!dev::mbar_wait_warp(&full[warp][st], (uint32_t)((t - t0) / p.stages) & 1u, wc)) break;
+        uint8_t *tok = ring + (size_t)st * p.stage_bytes;
+        if (hh < hpi) {
+#pragma unroll 4
+            for (int h = hh; h < rotated; h += hpi) {
+                V *pa = reinterpret_cast<V *>(tok + h * row + off0), *pb2 = reinterpret_cast<V *>(tok + h * row + off1);
+                V a = *pa, b;
+                if (!ADJ) b = *pb2;
+                turn_unit<T, VEC, ADJ, NP>(a, b, rc, rs);
+                *pa = a;
+                if (!ADJ) *pb2 = b;
+            }
+        }
+        dev::fence_proxy_async_smem();
+        __syncwarp();
+        const uint8_t *src = tok;
+        for (int j = 0; j < p.njobs; ++j) {
+            const RopeJob &jb = p.jobs[j];
+            T *y = static_cast<T *>(jb.y);
+            if (!jb.paged) {
+                if (ok >= 1 && lane == 0) dev::bulk_store(y + t * jb.y_stride, src, jb.heads * row);
+            } else if (ok == 2) {
+                if (p.head_stride == p.d || jb.heads == 1) {
+                    if (lane == 0) dev::bulk_store(y + off, src, jb.heads * row);
+                } else {
+                    for (int h = lane; h < jb.heads; h += 32) dev::bulk_store(y + off + h * p.head_stride, src + h * row, row);
+                }
+            }
+            src += jb.heads * row;
+        }
+        dev::bulk_commit();
+    }
+    // nothing may be under way when the CTA's shared memory goes
+    dev::bulk_wait_all();
+    if (lane == 0) {
+        volatile int local_abort = 0;
+        const dev::WaitCtl drain{&local_abort, p.status, p.budget_ns};
+        for (int64_t t = max(t0, loaded - p.stages); t < loaded; ++t)
+            (void)dev::mbar_wait(&full[warp][(t - t0) % p.stages], (uint32_t)((t - t0) / p.stages) & 1u, drain);
+    }
+}
+
+template <typename T>
+cudaError_t launch_bulk(RopeParams &p, int sms, cudaStream_t st) {
+    // as many warps as leave each three or four stages in some 200 KB
+    const int fit = 200 * 1024 / p.stage_bytes;
+    const int warps = std::min(kBulkWarps, std::max(1, fit / 3));
+    p.stages = std::min(kBulkStages, fit / warps);
+    const int64_t blocks = std::min<int64_t>(sms, (p.T + warps - 1) / warps);
+    p.chunk = (p.T + blocks * warps - 1) / (blocks * warps);
+    const size_t smem = (size_t)warps * p.stages * p.stage_bytes + (size_t)warps * p.n_pairs * sizeof(float2);
+    auto kernel = p.adjacent ? rope_bulk_kernel<T, true> : rope_bulk_kernel<T, false>;
+    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, warps * 32, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int VEC, bool ADJ>
@@ -226,6 +413,8 @@ void rope_table(RopeParams &p, const double *inv_freq, const uint8_t *axes, int 
 
 cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     if (p.T <= 0) return cudaSuccess;
+    p.status = device_status_ptr();
+    p.budget_ns = wait_budget_ns();
     const int es = dtype == RA_FP32 ? 4 : 2;
     int vec = 16 / es;
     // the 16-byte path: every row, head and unit starts on 16 bytes
@@ -243,6 +432,15 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
+    // Many tokens: the ring kernel, which needs whole vectors, at most 32 units a head, and its three stages of a token.
+    // RINGFIG
+    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens) {
+        p.token_bytes = p.total_heads * p.d * es;
+        p.stage_bytes = (p.token_bytes + 127) / 128 * 128;
+        if (p.stage_bytes * 3 <= 200 * 1024)
+            return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st)
+                                    : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
+    }
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
     const int groups = p.units > 32 ? p.total_heads : (p.total_heads + 32 / p.units - 1) / (32 / p.units);
     p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));

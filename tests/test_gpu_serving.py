@@ -40,6 +40,10 @@ ROPE = [  # T, hq, hk, d, pairs, adjacent, axes, packed, dtype
     (1216, 1, 1, 256, 128, False, 1, False, "bf16"), (5, 40, 8, 256, 1, True, 1, False, "fp32"),
     (130, 9, 3, 36, 17, False, 1, True, "fp32"), (65, 64, 8, 128, 32, False, 3, True, "bf16"),
     (3, 130, 4, 4, 2, True, 1, False, "bf16"),
+    # enough tokens for the ring kernel: rows of every kind, an odd count, heads of few units
+    (4096, 4, 2, 128, 64, False, 3, True, "bf16"), (5003, 3, 1, 64, 16, True, 2, False, "fp32"),
+    (4999, 1, 1, 64, 32, False, 1, True, "fp32"), (4500, 5, 2, 96, 48, True, 3, False, "bf16"),
+    (4097, 2, 1, 256, 128, False, 1, False, "bf16"), (4200, 2, 2, 64, 24, False, 1, True, "bf16"),
 ]
 
 
@@ -159,6 +163,9 @@ APPEND = [  # new, kv lens, page, hq, hkv, d, pairs, axes, layout, dtype, pad
     ([700, 613, 0, 1], [700, 800, 0, 64], 64, 8, 2, 128, 64, 3, "both", "bf16", 9),
     ([17, 5], [20, 5], 8, 2, 2, 36, 7, 1, "hnd", "bf16", 0),
     ([2] * 700, [2 + i % 9 for i in range(700)], 16, 2, 1, 64, 32, 1, "nhd", "fp32", 1),
+    ([3000, 0, 1, 1500, 33], [3000, 5, 1, 1700, 40], 16, 4, 2, 128, 64, 1, "nhd", "bf16", 20),
+    ([4000, 99], [4003, 99], 5, 3, 2, 64, 16, 3, "hnd", "fp32", 2),
+    ([3] * 1400, [3 + i % 50 for i in range(1400)], 32, 2, 1, 64, 32, 1, "both", "bf16", 0),
 ]
 
 
