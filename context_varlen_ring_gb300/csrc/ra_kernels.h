@@ -231,8 +231,7 @@ struct RopeParams {
     const int32_t *pos;                // DEVICE [axes][T]
     int n_pairs, adjacent, inverse;
     int units, rot_units, split;       // set by launch_rope
-    int stages, stage_bytes, token_bytes;
-    int64_t chunk;                     // tokens a warp
+    int stages, stage_bytes, parts, share;  // of the ring kernel: a token's shares, heads a share
     unsigned long long budget_ns;
     // cache rows (cu != NULL): logical index kv_lens[b] - n_b + j through the page table
     const int32_t *cu, *kv_lens, *page_table;

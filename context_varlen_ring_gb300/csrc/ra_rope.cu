@@ -26,7 +26,7 @@ namespace ra {
 namespace {
 
 constexpr int kRopeWarps = 4;
-constexpr int kBulkWarps = 8, kBulkStages = 4;
+constexpr int kBulkWarps = 16, kBulkStages = 8, kRingBytes = 212 * 1024;
 constexpr int64_t kBulkTokens = 4096;
 
 template <typename T, int VEC>
@@ -215,13 +215,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
     }
 }
 
-// The same for many tokens: each warp streams a run of consecutive tokens
-// through a ring in shared memory, copied in and out by the bulk-copy engine.
-// A token's queries, keys and values lie one behind the other in a stage; the
-// rotated units are read, turned and written back in place.  So the bytes in
-// flight are the rings' (some 100 KB an SM) and no thread's registers wait for
-// memory.  Consecutive tokens share their sequence and page, whose search is
-// repeated only at their ends.
+// The same for many tokens: each warp streams its tokens through a ring in
+// shared memory, copied in and out by the bulk-copy engine.  All warps go
+// through the tokens side by side (with a run of consecutive tokens each, their
+// rows lay at multiples of one distance and met in the same memory channels:
+// 112 to 130 us for 32768 tokens, 107 so).
+// A stage holds a token's heads (queries, keys, values, one behind the other),
+// or one of `parts` shares of them; the rotated units are read, turned and
+// written back in place.  So the bytes in flight are the rings' (some 100 KB
+// an SM) and no thread's registers wait for memory.
 template <typename T, bool ADJ>
 __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid_constant__ RopeParams p) {
     constexpr int VEC = 16 / (int)sizeof(T), NP = ADJ ? VEC / 2 : VEC;
@@ -240,7 +242,8 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
     __syncthreads();
     const dev::WaitCtl wc{&abort_flag, p.status, p.budget_ns};
 
-    const int64_t t0 = ((int64_t)blockIdx.x * warps + warp) * p.chunk, t1 = min(p.T, t0 + p.chunk);
+    const int64_t TS = (int64_t)gridDim.x * warps, t0 = min(p.T, (int64_t)blockIdx.x * warps + warp), t1 = p.T;
+    const int items = t0 < t1 ? (int)((t1 - t0 + TS - 1) / TS) * p.parts : 0;  // this warp's stages: token i / parts, share i % parts
     const int hpi = 32 / p.rot_units, hh = lane / p.rot_units, u = lane % p.rot_units;
     const int off0 = u * 16, off1 = p.n_pairs * (int)sizeof(T) + u * 16, pb = u * NP;
     const int row = p.d * (int)sizeof(T);
@@ -257,85 +260,123 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
         pos_at[k] = p.pos + (int64_t)p.axis[w] * p.T;
         pos[k] = t0 < t1 ? __ldg(pos_at[k] + t0) : 0;
     }
-    auto load = [&](int64_t t) {  // lane 0
-        const int st = (int)((t - t0) % p.stages);
-        uint8_t *dst = ring + (size_t)st * p.stage_bytes;
-        dev::mbar_arrive_expect_tx(&full[warp][st], p.token_bytes);
-        for (int j = 0; j < p.njobs; ++j) {
-            dev::bulk_load(dst, static_cast<const T *>(p.jobs[j].x) + t * p.jobs[j].x_stride, p.jobs[j].heads * row,
-                           &full[warp][st]);
-            dst += p.jobs[j].heads * row;
+    // the heads [from, to) of job j in a share of the heads [ha, hb), at `src` of the stage
+    struct Piece {
+        int from, to;
+        uint32_t src;
+    };
+    auto piece = [&](int j, int first, int ha, int hb) {
+        const int from = max(ha, first), to = min(hb, first + p.jobs[j].heads);
+        return Piece{from - first, to - first, (uint32_t)((from - ha) * row)};
+    };
+    auto share = [&](int part, int &ha, int &hb) {
+        ha = part * p.share;
+        hb = min(p.total_heads, ha + p.share);
+    };
+    // A walk over the items: stage, its use (odd or even), share and token, counted rather than divided.
+    struct Item {
+        int i, st, part;
+        uint32_t use;
+        int64_t t;
+    };
+    auto step = [&](Item &x) {
+        ++x.i;
+        if (++x.st == p.stages) {
+            x.st = 0;
+            x.use ^= 1u;
+        }
+        if (++x.part == p.parts) {
+            x.part = 0;
+            x.t += TS;
         }
     };
-    int64_t loaded = t0;
+    Item ld{0, 0, 0, 0, t0};
+    auto load = [&]() {  // lane 0: the next item
+        int ha, hb;
+        share(ld.part, ha, hb);
+        uint8_t *dst = ring + ld.st * p.stage_bytes;
+        uint64_t *bar = &full[warp][ld.st];
+        dev::mbar_arrive_expect_tx(bar, (uint32_t)((hb - ha) * row));
+        for (int j = 0, first = 0; j < p.njobs; first += p.jobs[j++].heads) {
+            const Piece q = piece(j, first, ha, hb);
+            if (q.from < q.to)
+                dev::bulk_load(dst + q.src,
+                               static_cast<const T *>(p.jobs[j].x) + ld.t * p.jobs[j].x_stride + (int64_t)q.from * p.d,
+                               (uint32_t)((q.to - q.from) * row), bar);
+        }
+        step(ld);
+    };
     if (lane == 0)
-        for (; loaded < min(t1, t0 + p.stages - 2); ++loaded) load(loaded);
-    // the sequence of the token in hand, and its page
-    int seq = -1, page = -1, page_i = -1;
-    long long c0 = 0, c1 = -1, len = 0;
-    for (int64_t t = t0; t < t1; ++t) {
-        const int st = (int)((t - t0) % p.stages);
-        // the stores of the token before last have read their stage: it takes the next token but (stages - 3)
+        while (ld.i < min(items, p.stages - 2)) load();
+    // the sequence of the token in hand, its page, and the angles of this lane's unit
+    int seq = -1, page = -1, page_i = -1, ok = 1;
+    long long c0 = 0, c1 = -1, len = 0, off = 0;
+    float rc[NP] = {}, rs[NP] = {};
+    for (Item it{0, 0, 0, 0, t0}; it.i < items; step(it)) {
+        const int64_t t = it.t;
+        // the stores of the item before last have read their stage: it takes the next item
         dev::bulk_wait_read<1>();
         __syncwarp();
-        if (lane == 0 && loaded < t1) load(loaded++);
-        int ok = 1;
-        long long off = 0;
-        if (p.cu) {
-            if (t >= c1) {
-                seq = dev::segment_of(p.cu + 1, p.B, t);
-                page_i = -1;
-                if (seq < p.B) {
-                    c0 = p.cu[seq];
-                    c1 = p.cu[seq + 1];
-                    len = p.kv_lens[seq];
-                } else {
-                    c1 = p.T;  // behind the last sequence, to the end
-                }
-            }
-            ok = 0;
-            if (seq < p.B) {
-                const long long idx = len - (c1 - c0) + (t - c0);
-                bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
-                if (in) {
-                    const int pi = (int)idx / p.page_size;
-                    if (pi != page_i) {
-                        page_i = pi;
-                        page = p.page_table[(int64_t)seq * p.table_width + pi];
+        if (lane == 0 && ld.i < items) load();
+        if (it.part == 0) {
+            if (p.cu) {
+                if (t >= c1) {
+                    seq = dev::segment_of(p.cu + 1, p.B, t);
+                    page_i = -1;
+                    if (seq < p.B) {
+                        c0 = p.cu[seq];
+                        c1 = p.cu[seq + 1];
+                        len = p.kv_lens[seq];
+                    } else {
+                        c1 = p.T;  // behind the last sequence, to the end
                     }
-                    in = page >= 0 && page < p.n_pages;
-                    off = page * p.page_stride + ((int)idx - pi * p.page_size) * p.token_stride;
                 }
-                ok = in ? 2 : 1;
-                if (!in && lane == 0) dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
+                ok = 0;
+                if (seq < p.B) {
+                    const long long idx = len - (c1 - c0) + (t - c0);
+                    bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
+                    if (in) {
+                        const int pi = (int)idx / p.page_size;
+                        if (pi != page_i) {
+                            page_i = pi;
+                            page = p.page_table[(int64_t)seq * p.table_width + pi];
+                        }
+                        in = page >= 0 && page < p.n_pages;
+                        off = page * p.page_stride + ((int)idx - pi * p.page_size) * p.token_stride;
+                    }
+                    ok = in ? 2 : 1;
+                    if (!in && lane == 0) dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int w = lane + 32 * k;
-            if (w < p.n_pairs) {
-                const unsigned long long turn = (unsigned long long)(long long)pos[k] * turns[k];
-                float s, c;
-                sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
-                cs[w] = make_float2(c, p.inverse ? -s : s);
-                if (t + 1 < t1) pos[k] = __ldg(pos_at[k] + t + 1);
+            for (int k = 0; k < 4; ++k) {
+                const int w = lane + 32 * k;
+                if (w < p.n_pairs) {
+                    const unsigned long long turn = (unsigned long long)(long long)pos[k] * turns[k];
+                    float s, c;
+                    sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
+                    cs[w] = make_float2(c, p.inverse ? -s : s);
+                    if (t + TS < t1) pos[k] = __ldg(pos_at[k] + t + TS);
+                }
             }
-        }
-        __syncwarp();
-        float rc[NP], rs[NP];
-        if (hh < hpi) {
+            __syncwarp();
+            if (hh < hpi) {
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const float2 r = cs[pb + e];
-                rc[e] = r.x;
-                rs[e] = r.y;
+                for (int e = 0; e < NP; ++e) {
+                    const float2 r = cs[pb + e];
+                    rc[e] = r.x;
+                    rs[e] = r.y;
+                }
             }
         }
-        if (!dev::mbar_wait_warp(&full[warp][st], (uint32_t)((t - t0) / p.stages) & 1u, wc)) break;
-        uint8_t *tok = ring + (size_t)st * p.stage_bytes;
+        if (!dev::mbar_wait_warp(&full[warp][it.st], it.use, wc)) break;
+        int ha, hb;
+        share(it.part, ha, hb);
+        uint8_t *tok = ring + it.st * p.stage_bytes;
         if (hh < hpi) {
+            const int most = min(hb, rotated) - ha;
 #pragma unroll 4
-            for (int h = hh; h < rotated; h += hpi) {
+            for (int h = hh; h < most; h += hpi) {
                 V *pa = reinterpret_cast<V *>(tok + h * row + off0), *pb2 = reinterpret_cast<V *>(tok + h * row + off1);
                 V a = *pa, b;
                 if (!ADJ) b = *pb2;
@@ -346,20 +387,17 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
         }
         dev::fence_proxy_async_smem();
         __syncwarp();
-        const uint8_t *src = tok;
-        for (int j = 0; j < p.njobs; ++j) {
+        for (int j = 0, first = 0; j < p.njobs; first += p.jobs[j++].heads) {
             const RopeJob &jb = p.jobs[j];
-            T *y = static_cast<T *>(jb.y);
-            if (!jb.paged) {
-                if (ok >= 1 && lane == 0) dev::bulk_store(y + t * jb.y_stride, src, jb.heads * row);
-            } else if (ok == 2) {
-                if (p.head_stride == p.d || jb.heads == 1) {
-                    if (lane == 0) dev::bulk_store(y + off, src, jb.heads * row);
-                } else {
-                    for (int h = lane; h < jb.heads; h += 32) dev::bulk_store(y + off + h * p.head_stride, src + h * row, row);
-                }
+            const Piece q = piece(j, first, ha, hb);
+            if (q.from >= q.to || ok < (jb.paged ? 2 : 1)) continue;
+            T *y = static_cast<T *>(jb.y) + (jb.paged ? off + q.from * p.head_stride : t * jb.y_stride + (int64_t)q.from * p.d);
+            if (!jb.paged || p.head_stride == p.d) {
+                if (lane == 0) dev::bulk_store(y, tok + q.src, (uint32_t)((q.to - q.from) * row));
+            } else {
+                for (int h = lane; h < q.to - q.from; h += 32)
+                    dev::bulk_store(y + h * p.head_stride, tok + q.src + h * row, (uint32_t)row);
             }
-            src += jb.heads * row;
         }
         dev::bulk_commit();
     }
@@ -368,19 +406,24 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
     if (lane == 0) {
         volatile int local_abort = 0;
         const dev::WaitCtl drain{&local_abort, p.status, p.budget_ns};
-        for (int64_t t = max(t0, loaded - p.stages); t < loaded; ++t)
-            (void)dev::mbar_wait(&full[warp][(t - t0) % p.stages], (uint32_t)((t - t0) / p.stages) & 1u, drain);
+        for (int i = max(0, ld.i - p.stages); i < ld.i; ++i)
+            (void)dev::mbar_wait(&full[warp][i % p.stages], (uint32_t)(i / p.stages) & 1u, drain);
     }
 }
 
 template <typename T>
 cudaError_t launch_bulk(RopeParams &p, int sms, cudaStream_t st) {
-    // as many warps as leave each three or four stages in some 200 KB
-    const int fit = 200 * 1024 / p.stage_bytes;
-    const int warps = std::min(kBulkWarps, std::max(1, fit / 3));
+    // four or more stages a warp, in kRingBytes
+    // (with cache rows to find a warp waits longer between stages: smaller ones and more warps.  BULKFIG)
+    const int row = p.d * (int)sizeof(T), part = p.cu ? 5120 : 8192;
+    p.parts = (p.total_heads * row + part - 1) / part;
+    p.share = (p.total_heads + p.parts - 1) / p.parts;
+    p.parts = (p.total_heads + p.share - 1) / p.share;
+    p.stage_bytes = (p.share * row + 127) / 128 * 128;
+    const int fit = kRingBytes / p.stage_bytes;
+    const int warps = std::min(kBulkWarps, fit / 4);
     p.stages = std::min(kBulkStages, fit / warps);
     const int64_t blocks = std::min<int64_t>(sms, (p.T + warps - 1) / warps);
-    p.chunk = (p.T + blocks * warps - 1) / (blocks * warps);
     const size_t smem = (size_t)warps * p.stages * p.stage_bytes + (size_t)warps * p.n_pairs * sizeof(float2);
     auto kernel = p.adjacent ? rope_bulk_kernel<T, true> : rope_bulk_kernel<T, false>;
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -432,15 +475,9 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
-    // Many tokens: the ring kernel, which needs whole vectors, at most 32 units a head, and its three stages of a token.
-    // RINGFIG
-    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens) {
-        p.token_bytes = p.total_heads * p.d * es;
-        p.stage_bytes = (p.token_bytes + 127) / 128 * 128;
-        if (p.stage_bytes * 3 <= 200 * 1024)
-            return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st)
-                                    : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
-    }
+    // Many tokens: the ring kernel, which needs whole vectors and at most 32 units a head.  RINGFIG
+    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens)
+        return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st) : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
     const int groups = p.units > 32 ? p.total_heads : (p.total_heads + 32 / p.units - 1) / (32 / p.units);
     p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));
