@@ -95,13 +95,12 @@ __device__ __forceinline__ void turn_unit(typename Pack<T, VEC>::V &a, typename 
 // Lane (hh, u) owns unit u (a vector, or the two vectors of a half-split pair)
 // of heads hh, hh + hpi, ...: its sines and cosines stay in registers for all
 // of them, so shared memory carries each angle once a token (with a read per
-// head the shared-memory pipe was the limit, at 81 %: 134 us for 32768 tokens
-// of 40 heads of 128 and 90 us for 8192 of 72; this form takes 128 and 64 us).
-// Two heads a lane are in flight, the first two before the angles are
-// computed; eight blocks an SM beat five with four heads in flight (131 us)
-// and ten that spill (164 us).
+// head the shared-memory pipe was the limit, at 81 %).  Two heads a lane are
+// in flight, the first two before the angles are computed.  A chain of loads
+// bounds the small calls this kernel is for (64 tokens appended to their
+// caches: 5.2 us): the token's sequence, its page, and beside them the positions.
 template <typename T, int VEC, bool ADJ>
-__global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Pack<T, VEC>::V;
     constexpr int UN = 2, NP = VEC > 1 && ADJ ? VEC / 2 : VEC;  // heads in flight, pairs a unit
     extern __shared__ float2 cs_all[];
@@ -116,30 +115,45 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 8) rope_kernel(const __grid_c
     int ok = 1;          // 0: leave the token alone, 1: its token rows only, 2: its cache row too
     long long off = 0;   // its cache row
     auto prepare = [&]() {
+        int pos[4];  // of this lane's pairs, in flight beside the search
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int w = lane + 32 * k;
+            if (w < p.n_pairs) pos[k] = __ldg(p.pos + (int64_t)p.axis[w] * p.T + t);
+        }
         if (p.cu) {
-            // the token's sequence: the number of segment ends <= t
-            const int s = dev::segment_of(p.cu + 1, p.B, t);
+            // the token's sequence: token t's is t in a decoding step, else the number of segment ends <= t
+            int s = p.B;
+            if (t < p.B && p.cu[t] <= t && t < p.cu[t + 1])
+                s = (int)t;
+            else
+                s = dev::segment_of(p.cu + 1, p.B, t);
             ok = 0;
             if (s < p.B) {
                 const long long c0 = p.cu[s], n = (long long)p.cu[s + 1] - c0;
                 const long long idx = (long long)p.kv_lens[s] - n + (t - c0);
                 bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
                 if (in) {
-                    const int pg = p.page_table[(int64_t)s * p.table_width + (int)idx / p.page_size];
+                    const int pi = (int)idx / p.page_size;
+                    const int pg = p.page_table[(int64_t)s * p.table_width + pi];
                     in = pg >= 0 && pg < p.n_pages;
-                    off = pg * p.page_stride + ((int)idx % p.page_size) * p.token_stride;
+                    off = pg * p.page_stride + ((int)idx - pi * p.page_size) * p.token_stride;
                 }
                 ok = in ? 2 : 1;
                 if (!in && lane == 0) dev::record_status(p.status, RA_ERR_DEVICE_BOUNDS);
             }
         }
-        for (int w = lane; w < p.n_pairs; w += 32) {
-            const long long pos = p.pos[(int64_t)p.axis[w] * p.T + t];
-            const unsigned long long turn = (unsigned long long)pos * p.turns[w];
-            // the upper half as a signed number of 2^-31 half turns
-            float s, c;
-            sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
-            cs[w] = make_float2(c, p.inverse ? -s : s);
+#pragma unroll 1
+        for (int k = 0; 32 * k < p.n_pairs; ++k) {
+            const int w = lane + 32 * k;
+            if (w < p.n_pairs) {
+                const int at = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
+                const unsigned long long turn = (unsigned long long)(long long)at * p.turns[w];
+                // the upper half as a signed number of 2^-31 half turns
+                float s, c;
+                sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
+                cs[w] = make_float2(c, p.inverse ? -s : s);
+            }
         }
         __syncwarp();
     };
