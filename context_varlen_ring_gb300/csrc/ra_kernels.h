@@ -287,6 +287,7 @@ struct PagedArgs {
     float *lse;
     int *status;
 };
+constexpr int kPagedMostKeys = 1 << 30;  // of a segment: places, tiles and their weights stay within 32 bits
 constexpr int kPagedHere = 256;         // most segments of a family that blocks plan for themselves
 constexpr int kPagedMaxCtas = 1024;     // of the warp-level and SIMT kernels
 constexpr int kPagedMaxWide = 256;      // of the tcgen05 kernel (one an SM)

@@ -189,16 +189,28 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
         for (int tile = u.t0; tile < u.t1; ++tile) {
             const int k0 = tile * kKT;
             __syncthreads();
-            for (int i = threadIdx.x; i < kKT * (D / 4); i += WARPS * 32) {
-                const int j = i / (D / 4), c = i % (D / 4) * 4;
-                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-                const int64_t off = paged_row(a, f, s, g.len, k0 + j);
-                if (off >= 0) {
-                    kv = load4(static_cast<const T *>(a.k) + off + u.h * a.head_stride + c);
-                    vv = load4(static_cast<const T *>(a.v) + off + u.h * a.head_stride + c);
+            // a batch of loads is on its way before the first of it is stored
+            constexpr int kBatch = 16 / WARPS;
+            for (int i0 = threadIdx.x; i0 < kKT * (D / 4); i0 += kBatch * WARPS * 32) {
+                int64_t off[kBatch];
+                float4 kv[kBatch], vv[kBatch];
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) off[n] = paged_row(a, f, s, g.len, k0 + (i0 + n * WARPS * 32) / (D / 4));
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) {
+                    const int c = (i0 + n * WARPS * 32) % (D / 4) * 4;
+                    kv[n] = vv[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (off[n] >= 0) {
+                        kv[n] = load4(static_cast<const T *>(a.k) + off[n] + u.h * a.head_stride + c);
+                        vv[n] = load4(static_cast<const T *>(a.v) + off[n] + u.h * a.head_stride + c);
+                    }
                 }
-                *reinterpret_cast<float4 *>(Ks + j * KS + c) = kv;
-                *reinterpret_cast<float4 *>(Vs + j * D + c) = vv;
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n) {
+                    const int i = i0 + n * WARPS * 32, j = i / (D / 4), c = i % (D / 4) * 4;
+                    *reinterpret_cast<float4 *>(Ks + j * KS + c) = kv[n];
+                    *reinterpret_cast<float4 *>(Vs + j * D + c) = vv[n];
+                }
             }
             __syncthreads();
             float s0[RPW], s1[RPW];
@@ -274,9 +286,9 @@ template <typename T, int NV, int RPW, int WARPS>
 cudaError_t simt_launch(const PagedArgs *a, int fi, int late, int *ctas, cudaStream_t st) {
     auto kernel = paged_simt_kernel<T, NV, RPW, WARPS>;
     constexpr size_t smem = simt_smem<NV, RPW, WARPS>();
-    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (ctas) return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, WARPS * 32, smem);
+    static PagedFit fit;
+    const cudaError_t e = fit.prepare((const void *)kernel, WARPS * 32, smem, ctas);
+    if (e != cudaSuccess || ctas) return e;
     return launch_pdl(kernel, a->f[fi].n, WARPS * 32, smem, st, *a, fi, late);
 }
 

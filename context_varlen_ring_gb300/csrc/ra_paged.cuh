@@ -2,6 +2,7 @@
 // walk of a CTA along its run of key tiles, the keys a row sees, and the page table.
 #pragma once
 
+#include <atomic>
 #include <utility>
 
 #include "ra_dev.cuh"
@@ -34,7 +35,7 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
     const int len = fi ? a.prefix_lens[s] : a.kv_lens[s];
     int c0 = 0, c1 = 0;
-    bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size;
+    bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size && len <= kPagedMostKeys;
     if (fine) {
         c0 = a.cu[b0];
         c1 = a.cu[b1];
@@ -273,6 +274,31 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace dev
+
+// A kernel's shared-memory opt-in and its CTAs an SM, asked once a device.
+class PagedFit {
+  public:
+    cudaError_t prepare(const void *kernel, int threads, size_t smem, int *ctas) {
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool held = dev >= 0 && dev < 128;
+        int n = held ? ctas_[dev].load(std::memory_order_acquire) : 0;
+        if (n == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+            if (e != cudaSuccess) return e;
+            n = n > 0 ? n : 1;
+            if (held) ctas_[dev].store(n, std::memory_order_release);
+        }
+        if (ctas) *ctas = n;
+        return cudaSuccess;
+    }
+
+  private:
+    std::atomic<int> ctas_[128] = {};
+};
 
 // Launches `kernel` on `st` as a programmatic successor of the kernel ahead of it.
 template <typename... P, typename... A>

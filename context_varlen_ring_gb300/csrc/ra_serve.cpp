@@ -133,7 +133,7 @@ ra_status check_paged_shape(int64_t T, int B, int n_groups, int Hq, int Hkv, int
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return fail(RA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hkv");
     if (d <= 0) return fail(RA_ERR_INVALID_ARG, "d must be positive");
     if (d % 32 != 0 || d > 256) return fail(RA_ERR_UNSUPPORTED, "d must be a multiple of 32 and <= 256");
-    if (T > INT32_MAX / Hq) return fail(RA_ERR_UNSUPPORTED, "T * Hq must be < 2^31");
+    if (T > (1 << 30) / Hq) return fail(RA_ERR_UNSUPPORTED, "T * Hq must be at most 2^30");
     if (B > (1 << 20) || n_groups > (1 << 20) || (int64_t)Hkv * ((int64_t)B + n_groups) > (1 << 28))
         return fail(RA_ERR_UNSUPPORTED, "too many sequences");
     return RA_OK;
@@ -285,6 +285,11 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         if (most > (f ? 16 : 64) && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
         F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
+        // the SIMT kernel with too few 64-row tiles for the SMs: four times as many of a quarter (2 x 24 tiles of
+        // fp32 keys of 64: SIMTFIG)
+        const int64_t tiles = (int64_t)Hkv * (f ? n_groups : B) * ((most + 63) / 64) *
+                              (((f ? prefix_width : table_width) * cache->page_size + 63) / 64);
+        if (kind[f] == kSimt && tiles <= paged_sms()) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
         F.halves = kind[f] == kWide;
         F.least = kind[f] == kWide ? 64 : kind[f] == kMma && F.rt == 64 ? 32 : 16;  // MINFIG

@@ -411,8 +411,9 @@ typedef struct ra_paged_kv {
  *   q, q_out DEVICE [T, Hq, d] or both NULL; q_out may be q
  *   pos, rope as in ra_rope_fwd (pos DEVICE int32 [n_axes, T]); rope NULL: nothing is rotated
  *      (q and q_out must then be NULL)
- * Tokens at or behind cu_seqlens[B] (a padded batch) are left alone: neither
- * their q_out rows nor any cache row is written for them.  A token whose
+ * cu_seqlens starts at 0 and does not decrease.  Tokens at or behind
+ * cu_seqlens[B] (a padded batch) are left alone: neither their q_out rows nor
+ * any cache row is written for them.  A token whose
  * logical index or page lies outside the table or the cache is not written
  * and RA_ERR_DEVICE_BOUNDS is recorded (its q_out row is still written).  Two tokens of
  * one call must not name the same cache row (distinct sequences' tables must
@@ -458,12 +459,12 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  * query tokens of a sequence see and others do not must be finite.
  * The device arrays are checked on the device: boundaries that decrease or
  * leave [0, T], groups that decrease or leave [0, B], and lengths outside
- * [0, width * page_size] are recorded as RA_ERR_DEVICE_BOUNDS and leave out
+ * [0, width * page_size] or above 2^30 are recorded as RA_ERR_DEVICE_BOUNDS and leave out
  * and lse unwritten; a page index outside [0, n_pages) is recorded too, reads
  * nothing, and leaves the rows that meet it unspecified.  Capturable; the
  * arrays' contents may change between replays.  Deterministic: the order of
  * all sums is fixed by the lengths.  d a multiple of 32, d <= 256; q and the cache 16-byte aligned
- * with strides of whole 16 bytes; T * Hq < 2^31.
+ * with strides of whole 16 bytes; T * Hq <= 2^30.
  * ------------------------------------------------------------------------ */
 size_t ra_paged_attn_workspace_bytes(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype,
                                      int max_q_len);
