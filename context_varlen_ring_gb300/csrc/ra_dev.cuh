@@ -6,6 +6,9 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
 #include <cstdint>
 
 #include "ra_kernels.h"
@@ -445,4 +448,29 @@ __device__ __forceinline__ float2 fma_mul2(float2 a, float2 b, float2 c, float2 
 }
 
 }  // namespace dev
+// A kernel's shared-memory opt-in and its CTAs an SM, asked once a device.
+class LaunchFit {
+  public:
+    cudaError_t prepare(const void *kernel, int threads, size_t smem, int *ctas) {
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool held = dev >= 0 && dev < 128;
+        int n = held ? ctas_[dev].load(std::memory_order_acquire) : 0;
+        if (n == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+            if (e != cudaSuccess) return e;
+            n = n > 0 ? n : 1;
+            if (held) ctas_[dev].store(n, std::memory_order_release);
+        }
+        if (ctas) *ctas = n;
+        return cudaSuccess;
+    }
+
+  private:
+    std::atomic<int> ctas_[128] = {};
+};
+
 }  // namespace ra

@@ -286,7 +286,7 @@ template <typename T, int NV, int RPW, int WARPS>
 cudaError_t simt_launch(const PagedArgs *a, int fi, int late, int *ctas, cudaStream_t st) {
     auto kernel = paged_simt_kernel<T, NV, RPW, WARPS>;
     constexpr size_t smem = simt_smem<NV, RPW, WARPS>();
-    static PagedFit fit;
+    static LaunchFit fit;
     const cudaError_t e = fit.prepare((const void *)kernel, WARPS * 32, smem, ctas);
     if (e != cudaSuccess || ctas) return e;
     return launch_pdl(kernel, a->f[fi].n, WARPS * 32, smem, st, *a, fi, late);
@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
                 const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
                 v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
                 src = a.f[fi].acc + row * a.d;
+                if (v.y != v.y) v.x = INFINITY;  // NaN scores leave no maximum: the row is to become NaN, not empty
             }
             float Mn = v.x;
 #pragma unroll
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
         __syncthreads();
     }
     if (!live) return;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (0: no visible key)
     const int head = h * a.G + g;
     TOut *out = static_cast<TOut *>(a.out) + (t * a.Hq + head) * a.d;
 #pragma unroll
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
         }
     }
     if (sub == 0 && lane == 0)
-        a.lse[(int64_t)head * a.T + t] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        a.lse[(int64_t)head * a.T + t] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 template <typename TOut, int NV>
@@ -513,15 +514,15 @@ cudaError_t launch_paged_plan(const PagedArgs &a, cudaStream_t st) {
 }
 
 int paged_sms() {
-    static int sms[128] = {};
+    static std::atomic<int> sms[128] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
-    if (!sms[dev]) {
-        int n = 0;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
-        sms[dev] = n;
+        sms[dev].store(n, std::memory_order_relaxed);
     }
-    return sms[dev];
+    return n;
 }
 
 int paged_simt_ctas(int rt, int d) {

@@ -2,7 +2,6 @@
 // walk of a CTA along its run of key tiles, the keys a row sees, and the page table.
 #pragma once
 
-#include <atomic>
 #include <utility>
 
 #include "ra_dev.cuh"
@@ -99,7 +98,7 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
 // Up to kPagedHere segments are planned by every block for itself, from the
 // call's arrays: a scan over THREADS threads, which costs less than a launch
 // ahead of all others and the loads that depend on it (one request of 8192
-// keys: 19.6 us with the plan kernel, FIG without).  Finds the segment with
+// keys: 19.6 us with the plan kernel, 15.7 without).  Finds the segment with
 // tiles at place blockIdx.x * per (want < 0), or segment `want`; per = 0 where
 // an array is not as it must be.
 struct PlanShared {
@@ -274,31 +273,6 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace dev
-
-// A kernel's shared-memory opt-in and its CTAs an SM, asked once a device.
-class PagedFit {
-  public:
-    cudaError_t prepare(const void *kernel, int threads, size_t smem, int *ctas) {
-        int dev = -1;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const bool held = dev >= 0 && dev < 128;
-        int n = held ? ctas_[dev].load(std::memory_order_acquire) : 0;
-        if (n == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
-            if (e != cudaSuccess) return e;
-            n = n > 0 ? n : 1;
-            if (held) ctas_[dev].store(n, std::memory_order_release);
-        }
-        if (ctas) *ctas = n;
-        return cudaSuccess;
-    }
-
-  private:
-    std::atomic<int> ctas_[128] = {};
-};
 
 // Launches `kernel` on `st` as a programmatic successor of the kernel ahead of it.
 template <typename... P, typename... A>

@@ -385,7 +385,7 @@ cudaError_t mma_launch(const PagedArgs *a, int fi, int late, int *ctas, cudaStre
                   "one tile ahead; the joined rows lie over one stage");
     auto kernel = paged_mma_kernel<D, ROWS, WHOLE>;
     constexpr size_t smem = mma_smem<D, ROWS>();
-    static PagedFit fit;
+    static LaunchFit fit;
     const cudaError_t e = fit.prepare((const void *)kernel, kWarps * 32, smem, ctas);
     if (e != cudaSuccess || ctas) return e;
     return launch_pdl(kernel, a->f[fi].n, kWarps * 32, smem, st, *a, fi, late);

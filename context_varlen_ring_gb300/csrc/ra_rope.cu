@@ -26,7 +26,7 @@ namespace ra {
 namespace {
 
 constexpr int kRopeWarps = 4;
-constexpr int kBulkWarps = 16, kBulkStages = 8, kRingBytes = 212 * 1024;
+constexpr int kBulkWarps = 16, kBulkStages = 8, kRingBytes = 212 * 1024, kBulkSmem = 224 * 1024;
 constexpr int64_t kBulkTokens = 4096;
 
 template <typename T, int VEC>
@@ -428,19 +428,22 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
 template <typename T>
 cudaError_t launch_bulk(RopeParams &p, int sms, cudaStream_t st) {
     // four or more stages a warp, in kRingBytes
-    // (with cache rows to find a warp waits longer between stages: smaller ones and more warps.  BULKFIG)
+    // (with cache rows to find a warp waits longer between stages: smaller ones and more warps.  Stages of 5 and of
+    // 8 KB: 32768 tokens appended 194 and 235 us, rotated 109 and 107; 8192 tokens of 72 heads 57 and 53)
     const int row = p.d * (int)sizeof(T), part = p.cu ? 5120 : 8192;
     p.parts = (p.total_heads * row + part - 1) / part;
     p.share = (p.total_heads + p.parts - 1) / p.parts;
     p.parts = (p.total_heads + p.share - 1) / p.share;
     p.stage_bytes = (p.share * row + 127) / 128 * 128;
-    const int fit = kRingBytes / p.stage_bytes;
+    // (the angles of 128 pairs take some of the ring's room)
+    const int fit = std::min(kRingBytes, kBulkSmem - kBulkWarps * p.n_pairs * (int)sizeof(float2)) / p.stage_bytes;
     const int warps = std::min(kBulkWarps, fit / 4);
     p.stages = std::min(kBulkStages, fit / warps);
     const int64_t blocks = std::min<int64_t>(sms, (p.T + warps - 1) / warps);
     const size_t smem = (size_t)warps * p.stages * p.stage_bytes + (size_t)warps * p.n_pairs * sizeof(float2);
     auto kernel = p.adjacent ? rope_bulk_kernel<T, true> : rope_bulk_kernel<T, false>;
-    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static LaunchFit half_split, adjacent;  // (the most that any call takes, so calls at once do not undo each other's)
+    const cudaError_t e = (p.adjacent ? adjacent : half_split).prepare((const void *)kernel, warps * 32, kBulkSmem, nullptr);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, warps * 32, smem, st>>>(p);
     return cudaGetLastError();
@@ -489,7 +492,8 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
-    // Many tokens: the ring kernel, which needs whole vectors and at most 32 units a head.  RINGFIG
+    // Many tokens: the ring kernel, which needs whole vectors and at most 32 units a head.  (40 heads of 128: at 4096
+    // tokens 19.0 us, the warp kernel 19.2; at 32768 109 and 128; a small call waits less for warps than for rings)
     if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens)
         return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st) : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads

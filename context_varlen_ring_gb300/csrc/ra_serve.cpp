@@ -225,7 +225,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     if ((st = check_paged_shape(T, B, n_groups, Hq, Hkv, d, dtype))) return st;
     if (out_dtype != RA_FP32 && out_dtype != dtype)
         return fail(RA_ERR_INVALID_ARG, "out_dtype must be RA_FP32 or the cache's dtype");
-    if (!std::isfinite(scale)) return fail(RA_ERR_INVALID_ARG, "scale must be finite");
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(scale_log2)) return fail(RA_ERR_INVALID_ARG, "scale must be finite, also times log2(e)");
     if (table_width < 0 || prefix_width < 0 || table_width > INT32_MAX || prefix_width > INT32_MAX)
         return fail(RA_ERR_INVALID_ARG, "table widths must be in [0, 2^31)");
     if (q_stride < (int64_t)Hq * d) return fail(RA_ERR_INVALID_ARG, "q_stride is smaller than the heads");
@@ -272,23 +273,26 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.kv_lens = kv_lens;
     a.prefix_lens = prefix_lens;
     a.groups = prefix_groups;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     enum { kSimt, kMma, kWide } kind[2];
     PagedMaps maps;
     const bool wide =
         (paged_rows(0, T, a.G, max_q_len) > 64 || (n_groups > 0 && T * a.G > 16)) && paged_tc_maps(a, maps);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
-        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  RULEFIG
+        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  Measured: own keys,
+        // 24 rows: 64-row tiles 53 us, two passes of 16 rows 62, tcgen05 68; 64 rows: 82, tcgen05 87.  A prefix of
+        // 30000 keys, 32 and 64 rows: tcgen05 41 and 42 us, warp-level 46 and 54.
         const int64_t most = paged_rows(f, T, a.G, max_q_len);
         kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
         if (most > (f ? 16 : 64) && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
         F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
-        // the SIMT kernel with too few 64-row tiles for the SMs: four times as many of a quarter (2 x 24 tiles of
-        // fp32 keys of 64: SIMTFIG)
-        const int64_t tiles = (int64_t)Hkv * (f ? n_groups : B) * ((most + 63) / 64) *
-                              (((f ? prefix_width : table_width) * cache->page_size + 63) / 64);
+        // (a cache without pages holds no keys: every length above 0 is out of range)
+        F.width = cache->n_pages == 0 ? 0 : f ? prefix_width : table_width;
+        // the SIMT kernel with too few 64-row tiles for the SMs: four times as many of a quarter (9 sequences of 5
+        // to 700 fp32 keys of 64 behind a prefix of 1500: 19.5 us, with 64-row tiles 22)
+        const double tiles = (double)Hkv * F.S * ((most + 63) / 64) * ((F.width * cache->page_size + 63) / 64);
         if (kind[f] == kSimt && tiles <= paged_sms()) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
         F.halves = kind[f] == kWide;
@@ -301,7 +305,6 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         F.hdr = reinterpret_cast<PagedHdr *>(ws + L.o_hdr[f]);
         F.start = reinterpret_cast<int *>(ws + L.o_start[f]);
         F.table = f ? prefix_table : page_table;
-        F.width = f ? prefix_width : table_width;
         F.acc = reinterpret_cast<float *>(ws + L.o_acc[f]);
         F.ml = reinterpret_cast<float *>(ws + L.o_ml[f]);
     }

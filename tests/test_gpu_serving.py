@@ -444,3 +444,231 @@ def test_prefill_with_the_ring_then_decode_from_the_cache(ra):
         R.check(R.f64(lse), wl, lb)
         R.check(R.f64(ring[sel]), wo, ob)
         R.check(R.f64(rlse[:, sel]), wl, lb)
+
+
+# ------------------------------------------------------------------ more shapes
+MORE = [  # as ATTN, and the hint
+    # more sequences or groups than a block plans for itself: every kernel, one, two and many scans, many segments
+    ([1] * 300, [1 + i % 90 for i in range(300)], [50], [0, 300], 16, 4, 1, 64, "nhd", "bf16", True, 1, 1),
+    ([1] * 600, [i % 150 for i in range(600)], [130, 77], [0, 500, 590], 16, 8, 2, 128, "nhd", "bf16", True, 0, 1),
+    ([1] * 2200, [i % 40 for i in range(2200)], [], [0], 8, 2, 1, 32, "nhd", "fp32", True, 0, 1),
+    ([0, 1, 2] * 1000, [2 + i % 33 for i in range(3000)], [], [0], 16, 2, 1, 64, "hnd", "bf16", True, 2, 2),
+    ([1] * 300, [i % 7 for i in range(300)], [i % 70 for i in range(300)], range(301), 16, 8, 1, 128, "nhd", "bf16", True,
+     0, 1),
+    ([3, 0] * 130, [3 + i % 200 for i in range(260)], [], [0], 32, 32, 1, 128, "nhd", "bf16", True, 0, 3),
+    ([1] * 256, [i % 60 for i in range(256)], [i % 50 for i in range(256)], range(257), 16, 4, 2, 128, "nhd", "bf16", True,
+     0, 1),
+    # 17 to 64 rows a KV head, whole blocks of 16 keys in a page and not
+    ([2, 1, 2], [300, 65, 2], [100], [0, 2], 24, 24, 2, 128, "nhd", "bf16", True, 0, 2),
+    ([2, 1, 2], [300, 65, 2], [100], [0, 2], 48, 24, 2, 64, "hnd", "bf16", True, 0, 2),
+    ([5, 3, 1, 8], [500, 3, 129, 1000], [], [0], 5, 16, 2, 64, "nhd", "bf16", True, 0, 8),
+    ([5, 3, 1, 8], [500, 3, 129, 1000], [], [0], 32, 16, 2, 128, "hnd", "bf16", False, 0, 8),
+    ([4] * 5, [4, 5, 63, 64, 65], [7], [2, 5], 1, 4, 1, 128, "nhd", "bf16", True, 0, 4),
+    # many query heads of one KV head, in one token and in several
+    ([1, 1], [777, 30], [], [0], 16, 32, 1, 128, "nhd", "bf16", True, 0, 1),
+    ([1, 1], [777, 30], [200], [0, 1], 16, 64, 1, 128, "nhd", "bf16", True, 0, 1),
+    ([1, 2, 1], [777, 30, 256], [300], [0, 3], 64, 128, 1, 128, "hnd", "bf16", True, 0, 2),
+    ([1, 1], [500, 30], [], [0], 16, 71, 1, 64, "nhd", "bf16", True, 0, 1),
+    ([1, 3], [500, 30], [40], [0, 2], 16, 256, 1, 128, "nhd", "bf16", True, 0, 3),      # more heads than a row tile takes
+    # chunks of prompts: boxes of 8 rows, of whole pages, heads that are no power of two, no causal mask
+    ([300, 1], [1000, 400], [], [0], 8, 8, 2, 128, "nhd", "bf16", True, 0, 300),
+    ([129, 64], [129, 1000], [513], [0, 2], 256, 4, 2, 128, "hnd", "bf16", True, 3, 129),
+    ([50, 7], [333, 7], [90], [0, 2], 16, 6, 2, 128, "both", "bf16", True, 0, 50),
+    ([200], [700], [128], [0, 1], 16, 4, 1, 128, "both", "bf16", False, 0, 200),
+    ([60, 3], [200, 90], [65], [0, 2], 16, 4, 2, 64, "nhd", "fp32", True, 0, 60),
+    ([260], [100], [], [0], 16, 2, 1, 128, "nhd", "bf16", True, 0, 260),                # more queries than keys
+    # a hint that is too small only chooses the kernels
+    ([40, 1, 90], [140, 200, 300], [150], [0, 3], 16, 8, 2, 128, "nhd", "bf16", True, 0, 1),
+    ([40, 1, 90], [140, 200, 300], [150], [0, 3], 16, 8, 2, 128, "nhd", "fp32", True, 0, 2),
+]
+
+
+@pytest.mark.parametrize("new,lens,plens,groups,page,hq,hkv,d,layout,dtype,causal,pad,most", MORE)
+def test_paged_attention_shapes(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, most):
+    c, cu, args, kw = _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad)
+    kw["max_q_len"] = most
+    q, S = args[0], len(lens)
+    out, lse = torch.full_like(q, 3.0), torch.full((hq, q.shape[0]), 3.0, device="cuda")
+    ra.paged_attn_fwd(*args, out=out, lse=lse, **kw)
+    torch.cuda.synchronize()
+    assert ra.device_status() == 0
+    wo, ob, wl, lb, written = R.paged_attn(R.f64(q), R.f64(c.k), R.f64(c.v), c.tables[:S], cu, lens, c.tables[S:],
+                                           plens, groups, causal, 1 / math.sqrt(d), dtype, dtype == "bf16")
+    R.check(R.f64(out)[written], wo[written], ob[written], "out")
+    R.check(R.f64(lse)[:, written], wl[:, written], lb[:, written], "lse")
+    assert (out[~torch.from_numpy(written)] == 3).all() and (lse[:, ~torch.from_numpy(written)] == 3).all()
+
+
+def test_many_sequences_are_checked(ra):
+    """The index arrays of more sequences than a block plans for itself."""
+    S = 700
+    c, cu, args, kw = _attn(ra, [1] * S, [1 + i % 30 for i in range(S)], [20], [0, S], 16, 4, 2, 64, "nhd", "bf16", True, 0)
+    q, kc, vc, own, cud, lens = args
+    for at, value in ((0, -1), (511, 33), (512, -2), (699, 2**31 - 1)):
+        bad = lens.clone()
+        bad[at] = value
+        out, lse = torch.full_like(q, 3.0), torch.full((4, S), 3.0, device="cuda")
+        ra.paged_attn_fwd(q, kc, vc, own, cud, bad, out=out, lse=lse, **kw)
+        assert ra.device_status() != 0 and ra.device_status() == 0
+        assert (out == 3).all() and (lse == 3).all()
+
+
+def test_cache_without_pages(ra):
+    """Lengths of 0 see nothing; a length above 0 is out of range whatever the table says."""
+    q = randn((2, 4, 64), 1, "bf16")
+    kc = torch.empty((0, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for lens in ([0, 0], [0, 3]):
+        out, lse = torch.full_like(q, 3.0), torch.full((4, 2), 3.0, device="cuda")
+        ra.paged_attn_fwd(q, kc, kc, dev(np.zeros((2, 1))), dev([0, 1, 2]), dev(lens), out=out, lse=lse)
+        assert (ra.device_status() != 0) == any(lens)
+        assert (out == (3 if any(lens) else 0)).all() and (lse == (3 if any(lens) else -math.inf)).all()
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,new", [("bf16", 8, 2, 1), ("bf16", 24, 2, 2), ("bf16", 16, 1, 4), ("bf16", 8, 2, 40),
+                                              ("fp32", 8, 2, 3)])
+def test_nan_reaches_the_rows_that_meet_it_and_no_others(ra, dtype, hq, hkv, new):
+    """A NaN query makes its own rows NaN (output and lse); a NaN key those that see it.  The rest keep their bits."""
+    S, d = 3, 128
+    c, cu, args, kw = _attn(ra, [new] * S, [200, 90, 130], [150], [0, S], 16, hq, hkv, d, "nhd", dtype, True, 0)
+    q, kc, vc, own, cud, lens = args
+    good, glse = ra.paged_attn_fwd(*args, **kw)
+    t, h, G = new, 1, hq // hkv                # the second sequence's first token
+    bad = q.clone()
+    bad[t, h, 5] = float("nan")
+    out, lse = ra.paged_attn_fwd(bad, *args[1:], **kw)
+    hit = torch.zeros((S * new, hq), dtype=torch.bool, device="cuda")
+    hit[t, h] = True
+    for _ in range(2):
+        assert out[hit].isnan().all() and lse.t()[hit].isnan().all()
+        assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse.t()[~hit], glse.t()[~hit])
+        # a key that the whole second sequence sees, of KV head 0
+        k2 = kc.clone()
+        k2[int(c.tables[1][0]), 3, 0, 7] = float("nan")
+        out, lse = ra.paged_attn_fwd(q, k2, *args[2:], **kw)
+        hit.zero_()
+        hit[new:2 * new, :G] = True
+    # all keys of a prefix
+    kc2 = kc.clone()
+    kc2[torch.from_numpy(c.tables[S][:10]).cuda(), :, 0] = float("nan")
+    out, lse = ra.paged_attn_fwd(q, kc2, *args[2:], **kw)
+    assert out[:, :G].isnan().all() and lse[:G].isnan().all()
+    assert torch.equal(out[:, G:], good[:, G:]) and torch.equal(lse[G:], glse[G:])
+
+
+def test_cache_behind_32_bits_of_elements(ra):
+    """Pages whose elements lie behind 2^31 (and 2^32): appended to and read, by every kernel."""
+    page, hkv, d, lens = 16, 8, 128, [40, 130, 1, 16]
+    pages = 2**32 // (page * hkv * d) + 64
+    small = Cache(lens + [300], page, hkv, d, "bf16", seed=4)
+    n = small.k.shape[0]
+    places = np.sort(np.random.default_rng(2).choice(np.arange(pages // 2 - 20, pages - 1), n - 2, replace=False))
+    places = np.concatenate([places, [pages - 1, 1]])
+    kc = torch.empty((pages, page, hkv, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    at = torch.from_numpy(places).cuda()
+    kc[at], vc[at] = small.k, small.v
+    far = np.where(small.tables < 0, -1, places[small.tables])
+    kw = dict(prefix_lens=dev([300]), prefix_groups=dev([0, 4]))
+    for new, hq in (([1] * 4, 16), ([5, 3, 1, 2], 32), ([40, 64, 1, 3], 16)):
+        cu = dev(np.concatenate([[0], np.cumsum(new)]))
+        q = randn((sum(new), hq, d), 9, "bf16")
+        k = randn((sum(new), hkv, d), 10, "bf16")
+        res = []
+        for K, V, t in ((small.k, small.v, small.tables), (kc, vc, far)):
+            ra.kv_cache_append(k, k, K, V, dev(t[:4]), cu, dev(lens))
+            res.append(ra.paged_attn_fwd(q, K, V, dev(t[:4]), cu, dev(lens), prefix_table=dev(t[4:]), max_q_len=max(new), **kw))
+        assert ra.device_status() == 0
+        assert torch.equal(kc[at].view(torch.int16), small.k.view(torch.int16))
+        assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+@pytest.mark.parametrize("T,stride", [(100, 2**31 // 90), (4200, 2**31 // 4000)])
+def test_rope_rows_behind_32_bits_of_elements(ra, T, stride):
+    stride = stride // 64 * 64
+    big = torch.empty((T, stride), dtype=torch.bfloat16, device="cuda")
+    x = big[:, 64:64 + 3 * 128].unflatten(1, (3, 128))
+    x.copy_(randn((T, 3, 128), 1, "bf16"))
+    pos, freq = dev(np.arange(T)), ra.rope_inv_freq(128)
+    want, _ = ra.rope_fwd(x.contiguous(), None, pos, freq)
+    got, _ = ra.rope_fwd(x, None, pos, freq, q_out=x)
+    assert got is x or torch.equal(got, x)
+    assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("T", [5, 4300])
+def test_rope_in_a_graph_and_on_another_stream(ra, T):
+    """Captured once and replayed after queries, keys and positions changed; beside calls on another stream."""
+    q, k = randn((T, 4, 128), 1, "bf16"), randn((T, 2, 128), 2, "bf16")
+    pos, freq = dev(np.arange(T)), ra.rope_inv_freq(128)
+    ra.rope_fwd(q, k, pos, freq)
+    qo, ko, dq = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ra.rope_fwd(q, k, pos, freq, q_out=qo, k_out=ko)
+        ra.rope_bwd(qo, None, pos, freq, dq_out=dq)
+    side = torch.cuda.Stream()
+    for seed in (3, 4):
+        q.copy_(randn((T, 4, 128), seed, "bf16"))
+        pos.copy_(dev(np.arange(T) * seed % 5000))
+        torch.cuda.synchronize()
+        g.replay()
+        with torch.cuda.stream(side):
+            other = ra.rope_fwd(q, k, pos, freq)
+        torch.cuda.synchronize()
+        assert torch.equal(qo, other[0]) and torch.equal(ko, other[1])
+        assert torch.equal(dq, ra.rope_bwd(qo, None, pos, freq)[0])
+    assert ra.device_status() == 0
+
+
+def test_rope_calls_of_different_sizes_from_several_threads(ra):
+    """Threads whose calls take different amounts of shared memory, at once."""
+    from concurrent.futures import ThreadPoolExecutor
+    pos = dev(np.arange(4500))
+    work = []
+    for i, (h, d) in enumerate(((1, 256), (9, 128), (40, 64), (3, 240))):
+        x = randn((4500, h, d), i, "bf16")
+        work.append((x, ra.rope_inv_freq(d), ra.rope_fwd(x, None, pos, ra.rope_inv_freq(d))[0]))
+    torch.cuda.synchronize()
+
+    def run(i):
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            x, freq, want = work[i % len(work)]
+            got = [ra.rope_fwd(x, None, pos, freq)[0] for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+            return all(torch.equal(y, want) for y in got)
+
+    with ThreadPoolExecutor(8) as pool:
+        assert all(pool.map(run, range(16)))
+
+
+def test_two_graphs_share_a_workspace_in_turn(ra):
+    """Two captured calls of different shapes over one workspace, replayed in turn on one stream."""
+    a = _attn(ra, [1] * 5, [90, 300, 1, 64, 700], [200], [0, 5], 16, 16, 2, 128, "nhd", "bf16", True, 0)
+    b = _attn(ra, [2, 9], [77, 500], [], [0], 16, 16, 2, 128, "nhd", "bf16", True, 0, seed=3)
+    want = [ra.paged_attn_fwd(*x[2], **x[3]) for x in (a, b)]
+    n = max(ra.paged_attn_workspace_bytes(5, 5, 1, 16, 2, 128, 0, 1), ra.paged_attn_workspace_bytes(11, 2, 0, 16, 2, 128, 0, 9))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for x in (a, b):
+        o, l = torch.empty_like(x[2][0]), torch.empty((16, x[2][0].shape[0]), device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ra.paged_attn_fwd(*x[2], out=o, lse=l, workspace=ws, **x[3])
+        graphs.append(g)
+        outs.append((o, l))
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, l), w in zip(outs, want):
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_output_over_the_queries(ra):
+    """out may be q: the queries are read before the join writes."""
+    c, cu, args, kw = _attn(ra, [1, 3], [300, 77], [90], [0, 2], 16, 8, 2, 128, "nhd", "bf16", True, 0)
+    want, _ = ra.paged_attn_fwd(*args, **kw)
+    q = args[0].clone()
+    ra.paged_attn_fwd(q, *args[1:], out=q, **kw)
+    assert torch.equal(q, want)

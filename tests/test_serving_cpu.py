@@ -145,3 +145,10 @@ def test_device_search_matches_numpy():
             assert segment_of(ends, t) == np.searchsorted(ends, t, side="right")
         mixed = rng.integers(0, 50, n)
         assert all(0 <= segment_of(mixed, t) <= n for t in range(50))
+
+
+def test_scale_is_finite_also_in_base_two(ra):
+    from context_varlen_ring_gb300 import _lib
+    kv = _kv(_lib)
+    assert ra.lib().ra_paged_attn_fwd(FAKE, 256, 8, 4, ctypes.byref(kv), FAKE, 4, FAKE, FAKE, 2, None, 0, None, None, 0, 1,
+                                      1, 3e38, FAKE, 0, FAKE, FAKE, 1 << 40, None) == _lib.RA_ERR_INVALID_ARG
