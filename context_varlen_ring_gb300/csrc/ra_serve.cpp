@@ -296,7 +296,11 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         if (kind[f] == kSimt && tiles <= paged_sms()) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
         F.halves = kind[f] == kWide;
-        F.least = kind[f] == kWide ? 64 : kind[f] == kMma && F.rt == 64 ? 32 : 16;  // MINFIG
+        // The shortest run, in sixteenths of a warp-level tile: two tiles where a partial has 32 rows or more, whose
+        // write and join cost about a tile.  8192 keys of one KV head: 64 rows with 1, 2 and 4 tiles at least 17.9,
+        // 15.9 and 17.9 us, 32 rows 16.6 with 1, 14.3 with 2; the tcgen05 kernel, 128 rows: 22.2 with 1, 20.0 with
+        // 2, 20.2 with 4.  With 16 rows one or two makes no difference.
+        F.least = kind[f] == kWide ? 64 : kind[f] == kMma && F.rt > 16 ? 32 : 16;
         if (F.S)
             F.n = kind[f] == kWide  ? std::min(kPagedMaxWide, paged_sms())
                   : kind[f] == kMma ? paged_mma_ctas(F.rt, d, cache->page_size)
