@@ -235,7 +235,7 @@ struct RopeParams {
     unsigned long long budget_ns;
     // cache rows (cu != NULL): logical index kv_lens[b] - n_b + j through the page table
     const int32_t *cu, *kv_lens, *page_table;
-    int64_t table_width, n_pages, page_stride, token_stride, head_stride;
+    int64_t table_width, table_keys, n_pages, page_stride, token_stride, head_stride;
     int B, page_size;
     int *status;
     uint64_t turns[128];               // inv_freq / (2 pi) modulo 1, in units of 2^-64

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
             if (s < p.B) {
                 const long long c0 = p.cu[s], n = (long long)p.cu[s + 1] - c0;
                 const long long idx = (long long)p.kv_lens[s] - n + (t - c0);
-                bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
+                bool in = t >= c0 && idx >= 0 && idx < p.table_keys;
                 if (in) {
                     const int pi = (int)idx / p.page_size;
                     const int pg = p.page_table[(int64_t)s * p.table_width + pi];
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
                 ok = 0;
                 if (seq < p.B) {
                     const long long idx = len - (c1 - c0) + (t - c0);
-                    bool in = t >= c0 && idx >= 0 && idx < p.table_width * p.page_size;
+                    bool in = t >= c0 && idx >= 0 && idx < p.table_keys;
                     if (in) {
                         const int pi = (int)idx / p.page_size;
                         if (pi != page_i) {

@@ -3,6 +3,7 @@
 // kernels.  Host code only.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <string>
@@ -195,6 +196,7 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
     p.kv_lens = kv_lens;
     p.page_table = page_table;
     p.table_width = table_width;
+    p.table_keys = std::min<int64_t>(table_width * cache->page_size, INT32_MAX);  // (places are 32-bit)
     p.n_pages = cache->n_pages;
     p.page_stride = cache->page_stride;
     p.token_stride = cache->token_stride;

@@ -413,13 +413,13 @@ typedef struct ra_paged_kv {
  *      (q and q_out must then be NULL)
  * cu_seqlens starts at 0 and does not decrease.  Tokens at or behind
  * cu_seqlens[B] (a padded batch) are left alone: neither their q_out rows nor
- * any cache row is written for them.  A token whose
- * logical index or page lies outside the table or the cache is not written
- * and RA_ERR_DEVICE_BOUNDS is recorded (its q_out row is still written).  Two tokens of
- * one call must not name the same cache row (distinct sequences' tables must
- * not share the pages that they append to); which of them a row then holds is
- * not defined, vector by vector.  Capturable; lengths and tables may change
- * between replays.  Limits on d, dtype and n_pairs as in ra_rope_fwd.
+ * any cache row is written for them.  A token whose logical index or page lies
+ * outside the table or the cache is not written and RA_ERR_DEVICE_BOUNDS is
+ * recorded (its q_out row is still written).  Two tokens of one call must not
+ * name the same cache row (distinct sequences' tables must not share the pages
+ * that they append to); which of them a row then holds is not defined, vector
+ * by vector.  Capturable; lengths and tables may change between replays.
+ * Limits on d, dtype and n_pairs as in ra_rope_fwd.
  * ------------------------------------------------------------------------ */
 ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t T,
                              const ra_paged_kv *cache, const int32_t *page_table, int64_t table_width,
@@ -459,12 +459,14 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  * query tokens of a sequence see and others do not must be finite.
  * The device arrays are checked on the device: boundaries that decrease or
  * leave [0, T], groups that decrease or leave [0, B], and lengths outside
- * [0, width * page_size] or above 2^30 are recorded as RA_ERR_DEVICE_BOUNDS and leave out
- * and lse unwritten; a page index outside [0, n_pages) is recorded too, reads
- * nothing, and leaves the rows that meet it unspecified.  Capturable; the
- * arrays' contents may change between replays.  Deterministic: the order of
- * all sums is fixed by the lengths.  d a multiple of 32, d <= 256; q and the cache 16-byte aligned
- * with strides of whole 16 bytes; T * Hq <= 2^30.
+ * [0, width * page_size] or above 2^30 are recorded as RA_ERR_DEVICE_BOUNDS
+ * and leave out and lse unwritten; a page index outside [0, n_pages) is
+ * recorded too, reads nothing, and leaves the rows that meet it unspecified.
+ * A NaN in a query or in a key makes the rows that it reaches NaN, lse too.
+ * Capturable; the arrays' contents may change between replays.  Deterministic:
+ * the order of all sums is fixed by the lengths and the device.  d a multiple
+ * of 32, d <= 256; q, out and the cache 16-byte aligned with strides of whole
+ * 16 bytes; T * Hq <= 2^30.  out may be q.
  * ------------------------------------------------------------------------ */
 size_t ra_paged_attn_workspace_bytes(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype,
                                      int max_q_len);

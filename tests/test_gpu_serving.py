@@ -672,3 +672,17 @@ def test_output_over_the_queries(ra):
     q = args[0].clone()
     ra.paged_attn_fwd(q, *args[1:], out=q, **kw)
     assert torch.equal(q, want)
+
+
+def test_append_places_stay_within_32_bits(ra):
+    """Boundaries that decrease by 2^31 in a table of more places than that: recorded, nothing is written."""
+    B, d = 40, 64
+    ends = np.full(B, 5)
+    ends[2], ends[3] = 0, -2**31
+    kc = torch.zeros((1, 1, 1, d), dtype=torch.bfloat16, device="cuda")
+    vc, k = torch.zeros_like(kc), randn((1, 1, d), 1, "bf16")
+    one = (1, 2**30, 1, d)  # every row of the page is the same one
+    ra.kv_cache_append(k, k, kc.expand(one), vc.expand(one), dev(np.zeros((B, 3))), dev(np.concatenate([[1], ends])),
+                       dev(np.full(B, 100)))
+    assert ra.device_status() != 0 and ra.device_status() == 0
+    assert (kc == 0).all() and (vc == 0).all()
