@@ -22,7 +22,8 @@
 // behind the length is masked in S, and its V rows are zeroed in shared
 // memory before the product, so it may be anything.
 // Measured: a prefix of 65536 keys for 128 requests of 64 heads (8 of keys) in
-// 0.70 of the measured bf16 rate, where the products wait for the softmax.
+// 0.74 of the measured bf16 rate: a step of 128 keys takes 3130 cycles for 2048
+// of products, of which a row tile's softmax 1720, its P V and next S the rest.
 // Every wait is bounded as in the rest of the library.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -91,18 +92,21 @@ __device__ __forceinline__ void mask_cols(uint32_t (&v)[kCols], int seen, int ba
     }
 }
 
-__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint32_t q_s, uint32_t k_s, uint32_t idesc) {
+// A descriptor `bytes` further on: its address field is the low word's, and
+// no address of shared memory leaves it.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint64_t q, uint64_t k, uint32_t idesc) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
         const uint32_t off = (uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u;
-        tc_mma_ss_w(d_tmem, sdesc_sw128(q_s + off, 16, 1024), sdesc_sw128(k_s + off, 16, 1024), idesc, ks > 0);
+        tc_mma_ss_w(d_tmem, desc_at(q, off), desc_at(k, off), idesc, ks > 0);
     }
 }
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_s, uint32_t idesc,
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v, uint32_t idesc,
                                          uint32_t accumulate) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
-        tc_mma_ts_w(d_tmem, p_tmem + 8u * ks, sdesc_sw128(v_s + (uint32_t)ks * 2048u, kHalf, 1024), idesc,
+        tc_mma_ts_w(d_tmem, p_tmem + 8u * ks, desc_at(v, (uint32_t)ks * 2048u), idesc,
                     (accumulate || ks > 0) ? 1u : 0u);
 }
 
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     uint64_t *kv_empty = bars + 7;   // [kSlots]
     uint64_t *s_full = bars + 12;    // [2] S of a group computed
     uint64_t *p_ready = bars + 14;   // [2] P of a group written to TMEM (128 arrivals)
-    uint64_t *o_done = bars + 16;    // [2] PV of a group done
+    uint64_t *o_done = bars + 16;    // [2] a group's PVs of a unit done
     uint64_t *mma_done = bars + 18;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 20);
@@ -141,6 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
         mbar_init(mma_done, 1);
         fence_mbar_init();
+        tma_prefetch_desc(&p.tmQ);
+        tma_prefetch_desc(&p.tmK);
+        tma_prefetch_desc(&p.tmV);
     }
     if (warp == 2) {
         tmem_alloc(tmem_slot, 512);
@@ -189,11 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             uint32_t n = 0;  // K and V tiles loaded
             int nq = 0, ok = 1;
             const uint64_t policy = l2_evict_first();
-            if (lane == 0) {
-                tma_prefetch_desc(&p.tmQ);
-                tma_prefetch_desc(&p.tmK);
-                tma_prefetch_desc(&p.tmV);
-            }
             const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
             for (Walk w; ok && next_unit(w);) {
                 const int tok = w.u.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
@@ -209,47 +211,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                // page and row of this lane's box of a tile
-                auto look_up = [&](int t, int &page, int &row) {
+                // the page of this lane's box of a tile, as the table has it (n_pages: outside the cache, filled with zeros)
+                auto look_up = [&](int t) {
                     const int key = t * 128 + (lane >> 1) * p.box;
-                    page = (int)a.n_pages;  // outside the cache: filled with zeros
-                    row = key % a.page_size;
-                    if (lane < boxes && key < w.u.len) {
-                        const int pg = __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size);
-                        if (pg >= 0 && pg < a.n_pages)
-                            page = pg;
-                        else
-                            record_status(a.status, RA_ERR_DEVICE_BOUNDS);
-                    }
+                    return lane < boxes && key < w.u.len ? __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size)
+                                                         : (int)a.n_pages;
                 };
-                auto load = [&](const CUtensorMap *m, int page, int row) {
+                auto load = [&](const CUtensorMap *m, int t, int page) {
                     const uint32_t slot = n % kSlots;
-                    if (lane == 0) {
-                        ok = mbar_wait(kv_empty + slot, ((n / kSlots) & 1u) ^ 1u, wc);
-                        if (ok) mbar_arrive_expect_tx(kv_full + slot, kTile);
+                    // (all that can be done ahead of the wait is: a free slot is to be filled at once)
+                    const int key = t * 128 + (lane >> 1) * p.box, row = key % a.page_size;
+                    if (page < 0 || page >= a.n_pages) {
+                        if (lane < boxes && key < w.u.len) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+                        page = (int)a.n_pages;
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    const int c1 = p.rows_inner ? row : w.u.h, c2 = p.rows_inner ? w.u.h : row;
+                    uint8_t *dst = base + kOffKV + slot * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128;
+                    ok = mbar_wait_warp(kv_empty + slot, ((n / kSlots) & 1u) ^ 1u, wc);
                     if (!ok) return;
-                    if (lane < boxes)
-                        tma_load_4d_hint(base + kOffKV + slot * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128,
-                                         m, kv_full + slot, (lane & 1) * 64, p.rows_inner ? row : w.u.h,
-                                         p.rows_inner ? w.u.h : row, page, policy);
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full + slot, kTile);
+                    __syncwarp();
+                    if (lane < boxes) tma_load_4d_hint(dst, m, kv_full + slot, (lane & 1) * 64, c1, c2, page, policy);
                     ++n;
                 };
                 const int by = w.pair ? 1 : 2;
-                int pa = 0, ra = 0, pb = 0, rb = 0;
-                if (w.u.t0 < w.tend) look_up(w.u.t0, pa, ra);
-                if (!w.pair && w.u.t0 + 1 < w.tend) look_up(w.u.t0 + 1, pb, rb);
+                // the next step's pages are looked up ahead of this step's waits
+                int pa = look_up(w.u.t0), pb = look_up(w.u.t0 + 1);
+#pragma unroll 1
                 for (int t = w.u.t0; t < w.tend && ok; t += by) {
-                    const bool two = !w.pair && t + 1 < w.tend;
-                    const int pa0 = pa, ra0 = ra, pb0 = pb, rb0 = rb;
-                    // the next step's pages are looked up ahead of this step's waits
-                    if (t + by < w.tend) look_up(t + by, pa, ra);
-                    if (!w.pair && t + 3 < w.tend) look_up(t + 3, pb, rb);
-                    load(&p.tmK, pa0, ra0);
-                    if (two && ok) load(&p.tmK, pb0, rb0);
-                    if (ok) load(&p.tmV, pa0, ra0);
-                    if (two && ok) load(&p.tmV, pb0, rb0);
+                    const int cnt = !w.pair && t + 1 < w.tend ? 2 : 1;
+                    const int pa0 = pa, pb0 = pb;
+                    pa = w.pair ? pb : look_up(t + 2);
+                    pb = look_up(t + by + 1);
+#pragma unroll 1
+                    for (int i = 0; i < 2 * cnt && ok; ++i) {
+                        const bool v = i >= cnt;
+                        const int j = v ? i - cnt : i;
+                        load(v ? &p.tmV : &p.tmK, t + j, j ? pb0 : pa0);
+                    }
                 }
             }
             if (lane == 0) {
@@ -264,22 +263,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // -------------------------------------------- MMA issuer
             const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
             const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
-            const uint32_t kvs = base_s + kOffKV;
-            const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+            // Q; the ring's first slot as K (rows of d) and as V (columns of d)
+            const uint64_t dq = sdesc_sw128(base_s, 16, 1024), dk = sdesc_sw128(base_s + kOffKV, 16, 1024),
+                           dv = sdesc_sw128(base_s + kOffKV, kHalf, 1024);
             uint32_t n = 0, np0 = 0, np1 = 0;  // tiles consumed; PVs issued per group (all units)
             int nu = 0;
             bool ok = true;
             auto full = [&](uint32_t i) {
                 ok = ok && mbar_wait_warp(kv_full + i % kSlots, (i / kSlots) & 1u, wc);
                 tc_fence_after();
-                return kvs + (i % kSlots) * kTile;
+                return (i % kSlots) * kTile;
             };
             auto empty = [&](uint32_t i) { tc_commit_w(kv_empty + i % kSlots); };
             for (Walk w; ok && next_unit(w);) {
                 ok = mbar_wait_warp(q_full, nu & 1u, wc);
                 ++nu;
                 tc_fence_after();
-                const uint32_t q0 = base_s, q1 = base_s + (w.pair ? kTile : 0u);
                 const int by = w.pair ? 1 : 2;
                 // V rows behind the length, up to the end of their page, may hold anything
                 auto clean = [&](int t, uint32_t i) {
@@ -297,74 +296,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     tc_commit_w(q_empty);
                     continue;
                 }
-                // S of the first step
-                {
-                    const bool two = !w.pair && w.u.t0 + 1 < w.tend;
-                    const uint32_t k0 = full(n);
-                    if (!ok) break;
-                    issue_s(tS[0], q0, k0, idesc_s);
-                    tc_commit_w(s_full + 0);
-                    if (w.pair) {
-                        issue_s(tS[1], q1, k0, idesc_s);
-                        tc_commit_w(s_full + 1);
-                        empty(n);
-                    } else {
-                        empty(n);
-                        if (two) {
-                            const uint32_t k1 = full(n + 1);
+                // Step t: P V of the tiles t (group 0) and t + 1 (group 1; of t too where both have the same keys), and
+                // S of the next step's, group by group.  The first step has no products, only its next step's S, so
+                // that there is no second copy of that code: a run may be a dozen steps, and code that is met for the
+                // first time costs more than it does (with a copy for the first S, the second one came 3500 ns after
+                // it, now 2000).  Rolled over the groups too, that start is faster still, but every step slower: a
+                // prefix of 65536 keys for 128 requests 256 us, 249 so.
+#pragma unroll 1
+                for (int t = w.u.t0 - by; t < w.tend && ok; t += by) {
+                    const bool head = t < w.u.t0;
+                    // the step's K tiles, then its V tiles, in the order of their loads
+                    const uint32_t cnt = head ? 0u : !w.pair && t + 1 < w.tend ? 2u : 1u, next = n + 2 * cnt;
+                    if (t + by >= w.tend) tc_commit_w(q_empty);  // every S of this unit is issued
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (!ok) break;
+                        const int off = w.pair ? 0 : k;
+                        const uint32_t tSk = tmem + 128u * k;
+                        const bool last = k == 1 || !w.pair;  // reader of the tile
+                        if (!head && t + off < w.tend) {
+                            const uint32_t vi = n + cnt + off, v = full(vi);
                             if (!ok) break;
-                            issue_s(tS[1], q0, k1, idesc_s);
-                            tc_commit_w(s_full + 1);
-                            empty(n + 1);
+                            if (k == off) clean(t + off, vi);
+                            ok = mbar_wait_warp(p_ready + k, (k ? np1 : np0) & 1u, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_pv(tmem + 256u + 128u * k, tSk, desc_at(dv, v), idesc_o, t > w.u.t0);
+                            if (t + by + off >= w.tend) tc_commit_w(o_done + k);  // the group's last of the unit
+                            if (k)
+                                ++np1;
+                            else
+                                ++np0;
+                            if (last) empty(vi);
+                        }
+                        if (t + by + off < w.tend) {
+                            const uint32_t ki = next + off, kt = full(ki);
+                            if (!ok) break;
+                            issue_s(tSk, desc_at(dq, w.pair && k ? kTile : 0u), desc_at(dk, kt), idesc_s);
+                            tc_commit_w(s_full + k);
+                            if (last) empty(ki);
                         }
                     }
-                }
-                uint32_t pv0 = 0, pv1 = 0;  // this unit's
-                for (int t = w.u.t0; t < w.tend; t += by) {
-                    const bool two = !w.pair && t + 1 < w.tend, one1 = w.pair || two;
-                    const bool next = t + by < w.tend, next1 = w.pair ? next : t + 3 < w.tend;
-                    const uint32_t va = n + (two ? 2u : 1u), vb = w.pair ? va : va + 1;
-                    const uint32_t ka = n + (two ? 4u : 2u), kb = w.pair ? ka : ka + 1;
-                    if (!next) tc_commit_w(q_empty);  // every S of this unit is issued
-                    const uint32_t v0 = full(va);
-                    if (!ok) break;
-                    clean(t, va);
-                    ok = mbar_wait_warp(p_ready + 0, np0 & 1u, wc);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(tO[0], tS[0], v0, idesc_o, pv0 > 0);
-                    tc_commit_w(o_done + 0);
-                    ++np0;
-                    ++pv0;
-                    if (!w.pair) empty(va);
-                    if (next) {
-                        const uint32_t k0 = full(ka);
-                        if (!ok) break;
-                        issue_s(tS[0], q0, k0, idesc_s);
-                        tc_commit_w(s_full + 0);
-                        if (!w.pair) empty(ka);
-                    }
-                    if (one1) {
-                        const uint32_t v1 = full(vb);
-                        if (!ok) break;
-                        if (!w.pair) clean(t + 1, vb);
-                        ok = mbar_wait_warp(p_ready + 1, np1 & 1u, wc);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(tO[1], tS[1], v1, idesc_o, pv1 > 0);
-                        tc_commit_w(o_done + 1);
-                        ++np1;
-                        ++pv1;
-                        empty(vb);
-                    }
-                    if (next1) {
-                        const uint32_t k1 = full(kb);
-                        if (!ok) break;
-                        issue_s(tS[1], q1, k1, idesc_s);
-                        tc_commit_w(s_full + 1);
-                        empty(kb);
-                    }
-                    n += two ? 4u : 2u;
+                    n = next;
                 }
             }
             // every MMA issued must have completed before TMEM is released
@@ -384,15 +357,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         uint32_t nd_all = 0;  // S tiles of this group (all units)
         bool ok = true;
         float m_run = -INFINITY, l_run = 0.f;
-        uint32_t nd = 0;
+        uint32_t nd = 0, no = 0;  // S tiles of this group in the unit; units with any
         // One tile: `seen` of its columns count for this row.  `live` is false
         // in the pass below that only warms the instruction cache.
         auto tile = [&](int seen, bool live) {
             const bool cut = __any_sync(0xffffffffu, seen < 128);
             float mx = -INFINITY;
+            uint32_t v[kCols];
 #pragma unroll 1
-            for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t v[kCols];
+            for (int ch = kChunks - 1; ch >= 0; --ch) {  // (the first columns last: they stay for the exponentials)
                 load_cols(tS + kCols * ch, v);
                 if (cut) mask_cols(v, seen, kCols * ch);
                 float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
@@ -420,9 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // P (bf16) replaces S column pair by column pair: P's columns of a chunk lie where S has been read
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t v[kCols], pk[kCols / 2];
-                load_cols(tS + kCols * ch, v);
-                if (cut) mask_cols(v, seen, kCols * ch);
+                uint32_t pk[kCols / 2];
+                if (ch) {
+                    load_cols(tS + kCols * ch, v);
+                    if (cut) mask_cols(v, seen, kCols * ch);
+                }
                 float2 sum4[2] = {sum2, make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kCols / 2; ++c) {
@@ -440,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 if (nd > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t v[32];
-                        tmem_ld32(tO + 32u * ch, v);
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * ch, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                        tmem_st32(tO + 32u * ch, v);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tO + 32u * ch, o);
                     }
                 }
             }
@@ -494,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 continue;
             }
             if (ok && nd > 0) {
-                ok = mbar_wait_warp(o_done + k, (nd_all - 1) & 1u, wc);
+                ok = mbar_wait_warp(o_done + k, no++ & 1u, wc);
                 tc_fence_after();
             }
             // the partial: rows of group 1 lie behind group 0's when both have the same rows
