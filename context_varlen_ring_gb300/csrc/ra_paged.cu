@@ -336,16 +336,19 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
 // A block per (token, KV head, up to 8 of its query heads), 8 / HB warps a head:
 // the largest maximum M, the weights 2^(m - M), the weighted sums.  Own keys
 // come first, then the prefix; warps' sums are added in order, so the result
-// does not depend on timing.  Latency bound (a chain of dependent loads:
-// segment, place, maxima, sums): the segments are searched once a block, ahead
-// of the wait for the attention kernels; the place of each head's partials is
-// found by one lane; a lane finds one partial's weight and hands it to its
-// warp, which keeps the loop that all the bytes go through short; where tokens
-// are few, a block has fewer heads and a head more warps.
+// does not depend on timing.  Latency bound, so as much as can be is done ahead
+// of the wait for the attention kernels (segments, plan, the places of the
+// first 64 partials), and each warp's first sums are loaded beside the weights
+// rather than behind them (one request of 8192 keys, 57 partials a head: 17.0
+// -> 15.3 us).  A lane finds the weights of two partials and hands them to its
+// warp.  Where tokens are few, a block has fewer heads and a head more warps,
+// and registers for loads count; else blocks an SM do (64 registers: a prefix
+// of 32768 keys for 64 requests 78.5 us, 96 registers 83.4).
 constexpr int kJoinWarps = 8;
 
 template <typename TOut, int HB, int NV>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, HB == 1 ? 2 : 4)
+    paged_combine_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int WPR = kJoinWarps / HB;  // warps a head
     __shared__ float4 sum[kJoinWarps][32 * NV];
     __shared__ int seg[2];
@@ -371,22 +374,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
     }
     __syncthreads();
     long long per[2] = {1, 1};
-    if (a.here) {
+    if (a.here) {  // all places are found ahead of the wait for the attention kernels
         long long W;
         per[0] = paged_plan_here<kJoinWarps * 32>(a, a.f[0], 0, seg[0], plan[0], W);
         if (a.n_groups > 0) per[1] = paged_plan_here<kJoinWarps * 32>(a, a.f[1], 1, seg[1], plan[1], W);
-    }
-    pdl_wait();
-    if (seg[0] < 0) return;
-    if (!a.here) {
+    } else {
+        pdl_wait();
         for (int i = 0; i < (a.n_groups > 0 ? 2 : 1); ++i) {
             per[i] = __ldcg(&a.f[i].hdr->err) ? 0 : __ldcg(&a.f[i].hdr->per);
             if ((int)threadIdx.x == i && seg[i] >= 0) plan[i].g = paged_seg(a.f[i], seg[i]);
         }
         __syncthreads();
     }
-    if (!per[0] || !per[1]) return;  // an array that is not as it must be: nothing is written
-    if (threadIdx.x < 2 * HB && g0 + (int)threadIdx.x / 2 < a.G) {
+    const bool fine = seg[0] >= 0 && per[0] && per[1];  // (an array that is not as it must be: nothing is written)
+    if (fine && threadIdx.x < 2 * HB && g0 + (int)threadIdx.x / 2 < a.G) {
         const int i = threadIdx.x & 1;
         parts[threadIdx.x / 2][i] = seg[i] < 0 ? Parts{}
                                                : find_parts(a, a.f[i], plan[i].g, i ? per[1] : per[0], t, h,
@@ -394,67 +395,110 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_combine_kernel(const __
     }
     __syncthreads();
     const int sub = warp % WPR, g = g0 + warp / WPR, d4 = a.d / 4;
-    const bool live = g < a.G;
-    float M = -INFINITY, L = 0.f;
-    float4 o[NV];
+    const bool live = fine && g < a.G;
+    const int own = live ? parts[warp / WPR][0].cnt : 0, cnt = live ? own + parts[warp / WPR][1].cnt : 0;
+    // lane's partials i0 + lane and i0 + lane + 32: their (m, l) and sums
+    const float2 *ml[2];
+    const float *src[2];
+    auto place = [&](int i0) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-        const int own = parts[warp / WPR][0].cnt, cnt = own + parts[warp / WPR][1].cnt;
-        // the maximum is carried along, as in the attention itself: 32 partials a trip
-#pragma unroll 1
-        for (int i0 = 0; i0 < cnt; i0 += 32) {
-            int i = i0 + lane;
+        for (int u = 0; u < 2; ++u) {
+            int i = i0 + 32 * u + lane;
             const int fi = i < own ? 0 : 1;
             const Parts &p = parts[warp / WPR][fi];
             if (fi) i -= own;
-            const float *src = nullptr;
-            float2 v = make_float2(-INFINITY, 0.f);
+            ml[u] = nullptr;
+            src[u] = nullptr;
             const long long run = (p.c0 + (i >> p.two)) * (fi ? per[1] : per[0]) - p.x;  // its CTA's place in the unit
             const int from = (int)max(0ll, run), to = (int)min((long long)p.all, run + (fi ? per[1] : per[0]));
             if (i < p.cnt && paged_tile(from, p.wt) < paged_tile(to, p.wt)) {  // (else it began no tile of the unit)
                 const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
-                v = __ldcg(reinterpret_cast<const float2 *>(a.f[fi].ml) + row);
-                src = a.f[fi].acc + row * a.d;
-                if (v.y != v.y) v.x = INFINITY;  // NaN scores leave no maximum: the row is to become NaN, not empty
-            }
-            float Mn = v.x;
-#pragma unroll
-            for (int s = 16; s; s >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, s));
-            Mn = fmaxf(M, Mn);
-            if (Mn == -INFINITY) continue;
-            const float alpha = exp2f(M - Mn), w = exp2f(v.x - Mn);
-            M = Mn;
-            L = L * alpha + w * v.y;
-#pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                o[e].x *= alpha;
-                o[e].y *= alpha;
-                o[e].z *= alpha;
-                o[e].w *= alpha;
-            }
-            const int most = min(32, cnt - i0);
-#pragma unroll 4
-            for (int k = sub; k < most; k += WPR) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                const float4 *q = reinterpret_cast<const float4 *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
-                // (a partial without weight may never have been written)
-#pragma unroll
-                for (int e = 0; e < NV; ++e) {
-                    if (wk != 0.f && lane + 32 * e < d4) {
-                        const float4 x = __ldcg(q + lane + 32 * e);
-                        o[e].x = fmaf(wk, x.x, o[e].x);
-                        o[e].y = fmaf(wk, x.y, o[e].y);
-                        o[e].z = fmaf(wk, x.z, o[e].z);
-                        o[e].w = fmaf(wk, x.w, o[e].w);
-                    }
-                }
+                ml[u] = reinterpret_cast<const float2 *>(a.f[fi].ml) + row;
+                src[u] = a.f[fi].acc + row * a.d;
             }
         }
+    };
+    auto at_lane = [&](const float *p, int k) {
+        return reinterpret_cast<const float4 *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), k));
+    };
+    if (cnt > 0) place(0);
+    if (a.here) pdl_wait();
+    if (!fine) return;
+    float M = -INFINITY, L = 0.f;
+    float4 o[NV];
 #pragma unroll
-        for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+    for (int e = 0; e < NV; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int PRE = 4 / NV;  // sums of a warp that are loaded beside the weights, not behind them
+    // the maximum is carried along, as in the attention itself: 64 partials a trip
+#pragma unroll 1
+    for (int i0 = 0; i0 < cnt; i0 += 64) {
+        if (i0) place(i0);
+        const int most = min(64, cnt - i0);
+        float2 v[2];
+        float4 x[PRE][NV];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) v[u] = ml[u] ? __ldcg(ml[u]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int j = 0; j < PRE; ++j) {
+            const int u = j * WPR / 32, k = sub + j * WPR;  // (u: a constant, sub < WPR)
+            const float4 *q = at_lane(src[u], k & 31);
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+                if (u < 2 && k < most && q && lane + 32 * e < d4) x[j][e] = __ldcg(q + lane + 32 * e);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (v[u].y != v[u].y) v[u].x = INFINITY;  // NaN scores leave no maximum: the row is to become NaN, not empty
+            Mn = fmaxf(Mn, v[u].x);
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, s));
+        if (Mn == -INFINITY) continue;
+        const float alpha = exp2f(M - Mn);
+        float w[2];
+        M = Mn;
+        L *= alpha;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w[u] = exp2f(v[u].x - Mn);
+            L += w[u] * v[u].y;
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            o[e].x *= alpha;
+            o[e].y *= alpha;
+            o[e].z *= alpha;
+            o[e].w *= alpha;
+        }
+        // (a partial without weight may never have been written)
+        auto add = [&](float wk, const float4 &y, float4 &z) {
+            z.x = fmaf(wk, y.x, z.x);
+            z.y = fmaf(wk, y.y, z.y);
+            z.z = fmaf(wk, y.z, z.z);
+            z.w = fmaf(wk, y.w, z.w);
+        };
+#pragma unroll
+        for (int j = 0; j < PRE; ++j) {
+            const int u = j * WPR / 32, k = sub + j * WPR;
+            const float wk = __shfl_sync(0xffffffffu, w[u], k & 31);
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+                if (u < 2 && k < most && wk != 0.f && lane + 32 * e < d4) add(wk, x[j][e], o[e]);
+        }
+#pragma unroll 4
+        for (int k = sub + PRE * WPR; k < most; k += WPR) {
+            const float w0 = __shfl_sync(0xffffffffu, w[0], k & 31), w1 = __shfl_sync(0xffffffffu, w[1], k & 31);
+            const float4 *q0 = at_lane(src[0], k & 31), *q1 = at_lane(src[1], k & 31);
+            const float wk = k < 32 ? w0 : w1;
+            const float4 *q = k < 32 ? q0 : q1;
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+                if (wk != 0.f && lane + 32 * e < d4) add(wk, __ldcg(q + lane + 32 * e), o[e]);
+        }
     }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
     if (WPR > 1) {
 #pragma unroll
         for (int e = 0; e < NV; ++e) sum[warp][lane + 32 * e] = o[e];

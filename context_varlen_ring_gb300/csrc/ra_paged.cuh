@@ -31,15 +31,12 @@ struct PagedUnit {
 // Segment s of a family from the call's arrays (W0 and R0 left to the plan);
 // false, and an empty one, where they are not as they must be.
 __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFamily &f, int fi, int s, PagedSeg &g) {
-    const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
     const int len = fi ? a.prefix_lens[s] : a.kv_lens[s];
-    int c0 = 0, c1 = 0;
-    bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size && len <= kPagedMostKeys;
-    if (fine) {
-        c0 = a.cu[b0];
-        c1 = a.cu[b1];
-        fine = c0 >= 0 && c1 >= c0 && c1 <= a.T;
-    }
+    const int b0 = fi ? a.groups[s] : s, b1 = fi ? a.groups[s + 1] : s + 1;
+    // (loaded whatever the others say, so that no load waits for another's check)
+    int c0 = a.cu[min(max(b0, 0), a.B)], c1 = a.cu[min(max(b1, 0), a.B)];
+    const bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= f.width * a.page_size &&
+                      len <= kPagedMostKeys && c0 >= 0 && c1 >= c0 && c1 <= a.T;
     if (!fine) c0 = c1 = 0;
     g.tok0 = c0;
     g.n = c1 - c0;
