@@ -312,7 +312,8 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int late, int *ctas, cu
 // (of CTA c0 + (i >> two)) at partial row  at + (i >> two) * rt + (i & two) * second.
 struct Parts {
     long long at, x;  // x: the unit's place in the line
-    int cnt, two, second, c0, wt, all;
+    int cnt, two, second, c0, all;
+    PagedCost cost;
 };
 
 __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, const PagedSeg &sg, long long per,
@@ -321,8 +322,8 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
     if (sg.w == 0) return p;
     const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    p.wt = paged_weight(a, f, sg);
-    p.all = sg.w * p.wt;
+    p.cost = paged_cost(a, f, sg);
+    p.all = paged_all(sg, p.cost);
     p.x = sg.W0 + (long long)(rtile * a.Hkv + h) * p.all;
     const int c1 = (int)paged_div(p.x + p.all - 1, per);
     p.c0 = (int)paged_div(p.x, per);
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, HB == 1 ? 2 : 4)
             src[u] = nullptr;
             const long long run = (p.c0 + (i >> p.two)) * (fi ? per[1] : per[0]) - p.x;  // its CTA's place in the unit
             const int from = (int)max(0ll, run), to = (int)min((long long)p.all, run + (fi ? per[1] : per[0]));
-            if (i < p.cnt && paged_tile(from, p.wt) < paged_tile(to, p.wt)) {  // (else it began no tile of the unit)
+            if (i < p.cnt && paged_tile(from, p.cost) < paged_tile(to, p.cost)) {  // (else it began no tile of the unit)
                 const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
                 ml[u] = reinterpret_cast<const float2 *>(a.f[fi].ml) + row;
                 src[u] = a.f[fi].acc + row * a.d;

@@ -45,21 +45,28 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     g.W0 = g.R0 = 0;
     return fine;
 }
-// What a key tile of the segment weighs, in sixteenths of a warp-level tile:
-// its own cost and its share of a unit's (queries, join, partial), which is
-// about two tiles.  Of the tcgen05 kernel, a tile for two row tiles takes 2.0
-// us, one of alternating tiles for a single row tile 1.0 to 1.4 (bound by its
-// softmax, or by memory), a unit about 4.
-__device__ __forceinline__ int paged_weight(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    const int tile = !f.halves ? 16 : g.n * a.G * 2 > f.rt ? 48 : 32, unit = f.halves ? 96 : 32;
-    return tile + (g.w ? unit / g.w : 0);
+// What a unit and its key tiles weigh, in sixteenths of a warp-level tile: a
+// unit takes its own cost (queries, join, partial) and then its tiles, so a run
+// that goes on into another unit has fewer tiles for it.  Of the tcgen05 kernel,
+// a tile for two row tiles takes 1.75 us, one of alternating tiles for a single
+// row tile 1.0 to 1.4 (bound by its softmax, or by memory), a unit about 4.
+struct PagedCost {
+    int tile, unit;
+};
+__device__ __forceinline__ PagedCost paged_cost(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
+    return PagedCost{!f.halves ? 16 : g.n * a.G * 2 > f.rt ? 48 : 32, f.halves ? 96 : 32};
+}
+__device__ __forceinline__ int paged_all(const PagedSeg &g, const PagedCost &c) {  // (at most 2^24 tiles)
+    return g.w ? g.w * c.tile + c.unit : 0;
 }
 // The first tile of a unit that begins at or behind place `at` of it: a tile
 // belongs to the run in which it begins.
-__device__ __forceinline__ int paged_tile(int at, int weight) { return (at + weight - 1) / weight; }
-// Its key tiles' weight and its partial rows over all units.  (n * G < 2^31.)
+__device__ __forceinline__ int paged_tile(int at, const PagedCost &c) {
+    return at <= c.unit ? 0 : (at - c.unit + c.tile - 1) / c.tile;
+}
+// The weight of all its units, and its partial rows.  (n * G < 2^31.)
 __device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * g.w * paged_weight(a, f, g);
+    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * paged_all(g, paged_cost(a, f, g));
 }
 // The weight of a CTA's run.
 __device__ __forceinline__ long long paged_per(const PagedFamily &f, long long W) {
@@ -222,12 +229,13 @@ __device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily
             }
         }
         const long long rel = k.x - k.g.W0;
-        const int wt = paged_weight(a, f, k.g), all = k.g.w * wt;  // (at most 2^25 tiles of 16 + 1, or 2^24 of 48 + 1)
+        const PagedCost cost = paged_cost(a, f, k.g);
+        const int all = paged_all(k.g, cost);
         const int lu = (int)paged_div(rel, all), rtile = lu / a.Hkv;
         const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
         k.x += to - from;
-        u.t0 = paged_tile(from, wt);
-        u.t1 = paged_tile(to, wt);
+        u.t0 = paged_tile(from, cost);
+        u.t1 = paged_tile(to, cost);
         if (u.t0 >= u.t1) continue;  // the run ends inside a tile that another one began
         u.s = k.s;
         u.tok0 = k.g.tok0;
