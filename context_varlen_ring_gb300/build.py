@@ -47,7 +47,7 @@ def _module_job(extra=()):
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     cmd += [x for i in inc for x in ("-isystem", i)] + list(extra) + ["-c", MODULE_SRC, "-o", obj]
     lib = os.path.join(root, "lib")
-    link = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libra.so",
+    link = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libra.so",
             "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
     return obj, cmd, ["g++", "-shared", obj, "-o"], link
 

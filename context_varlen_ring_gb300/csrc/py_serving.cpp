@@ -8,7 +8,7 @@
 // used; the work is in the library's C entries.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -136,8 +136,13 @@ struct On {  // the tensors' device is current, and their stream
           stream(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream()) {}
 };
 
+// A new tensor straight from the allocator (the dispatcher's way there takes 0.5 us more).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) {
+    return at::Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
+}
+
 at::Tensor output(PyObject *o, const at::Tensor &like, const char *name) {
-    if (o == Py_None) return at::empty(like.sizes(), like.options().requires_grad(false));
+    if (o == Py_None) return fresh(like.sizes(), like.scalar_type(), like);
     const at::Tensor &x = tensor(o, name);
     if (x.sizes() != like.sizes()) value_error(std::string(name) + " must have the shape of its input");
     return x;
@@ -314,7 +319,7 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
     On on(dev);
     at::Tensor out, lse, ws;
     if (a[12] == Py_None) {
-        out = at::empty(q.sizes(), q.options().dtype(ot).requires_grad(false));
+        out = fresh(q.sizes(), ot, q);
     } else {
         out = tensor(a[12], "out");
         if (out.sizes() != q.sizes() || !out.is_contiguous() || !out.is_cuda() || out.get_device() != dev)
@@ -322,7 +327,7 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
         if (has_type && out.scalar_type() != ot) value_error("out does not have out_dtype");
     }
     if (a[13] == Py_None) {
-        lse = at::empty({hq, T}, q.options().dtype(at::kFloat).requires_grad(false));
+        lse = fresh({hq, T}, at::kFloat, q);
     } else {
         lse = tensor(a[13], "lse");
         if (lse.dim() != 2 || lse.size(0) != hq || lse.size(1) != T || !lse.is_contiguous() || !lse.is_cuda() ||
@@ -332,7 +337,7 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
     const int groups = pre ? pre->B : 0;
     if (a[15] == Py_None) {
         const size_t need = ra_paged_attn_workspace_bytes(T, s.B, groups, hq, cache.Hkv, (int)d, cache.dtype, (int)most);
-        ws = at::empty({(int64_t)std::max<size_t>(need, 256)}, q.options().dtype(at::kByte).requires_grad(false));
+        ws = fresh({(int64_t)std::max<size_t>(need, 256)}, at::kByte, q);
     } else {
         ws = tensor(a[15], "workspace");
         if (!ws.is_contiguous() || !ws.is_cuda() || ws.get_device() != dev)

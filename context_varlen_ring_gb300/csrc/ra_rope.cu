@@ -466,7 +466,7 @@ void rope_table(RopeParams &p, const double *inv_freq, const uint8_t *axes, int 
     for (int i = 0; i < n_pairs; ++i) {
         const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
         const double frac = turns - std::floor(turns);              // in [0, 1]
-        p.turns[i] = frac >= 1.0 ? 0ull : (uint64_t)std::ldexp(frac, 64);
+        p.turns[i] = frac >= 1.0 ? 0ull : (uint64_t)(frac * 18446744073709551616.0);  // (exact: times 2^64)
         p.axis[i] = axes ? axes[i] : 0;
     }
 }
