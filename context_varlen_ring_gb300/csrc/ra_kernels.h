@@ -261,6 +261,7 @@ struct PagedHdr {                      // of each family
 };
 struct PagedFamily {
     int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
+    int rt_log, kt_log;                // (rows and keys are powers of two)
     int halves;                        // units of at most rt / 2 rows: two partials a row, of alternate key tiles
     int least;                         // least tiles a CTA: fewer cost more in partials than they gain
     PagedHdr *hdr;

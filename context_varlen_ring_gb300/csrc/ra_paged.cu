@@ -320,14 +320,14 @@ __device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamil
                                             int64_t t, int h, int g) {
     Parts p{};
     if (sg.w == 0) return p;
-    const int r = (int)(t - sg.tok0) * a.G + g, rtile = r / f.rt;
+    const int r = (int)(t - sg.tok0) * a.G + g, rtile = r >> f.rt_log;
     const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
     p.cost = paged_cost(a, f, sg);
     p.all = paged_all(sg, p.cost);
     p.x = sg.W0 + (long long)(rtile * a.Hkv + h) * p.all;
     const int c1 = (int)paged_div(p.x + p.all - 1, per);
     p.c0 = (int)paged_div(p.x, per);
-    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)p.c0 * f.rt + r % f.rt;
+    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)p.c0 * f.rt + (r & (f.rt - 1));
     p.two = alloc > rows ? 1 : 0;
     p.second = rows;
     p.cnt = (c1 - p.c0 + 1) << p.two;

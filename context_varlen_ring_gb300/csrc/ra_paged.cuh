@@ -41,7 +41,7 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     g.tok0 = c0;
     g.n = c1 - c0;
     g.len = fine ? len : 0;
-    g.w = g.n > 0 ? (g.len + f.kt - 1) / f.kt : 0;
+    g.w = g.n > 0 ? (g.len + f.kt - 1) >> f.kt_log : 0;
     g.W0 = g.R0 = 0;
     return fine;
 }
@@ -62,18 +62,19 @@ __device__ __forceinline__ int paged_all(const PagedSeg &g, const PagedCost &c) 
 // The first tile of a unit that begins at or behind place `at` of it: a tile
 // belongs to the run in which it begins.
 __device__ __forceinline__ int paged_tile(int at, const PagedCost &c) {
-    return at <= c.unit ? 0 : (at - c.unit + c.tile - 1) / c.tile;
+    const unsigned x = (unsigned)max(at - c.unit + c.tile - 1, 0) >> 4;
+    return (int)(c.tile == 48 ? x / 3 : c.tile == 32 ? x >> 1 : x);
 }
 // The weight of all its units, and its partial rows.  (n * G < 2^31.)
 __device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return (long long)((g.n * a.G + f.rt - 1) / f.rt) * a.Hkv * paged_all(g, paged_cost(a, f, g));
+    return (long long)((g.n * a.G + f.rt - 1) >> f.rt_log) * a.Hkv * paged_all(g, paged_cost(a, f, g));
 }
 // The weight of a CTA's run.
 __device__ __forceinline__ long long paged_per(const PagedFamily &f, long long W) {
     return max((long long)f.least, paged_div(W + f.n - 1, f.n));
 }
 __device__ __forceinline__ long long paged_rows(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    const int R = g.n * a.G, full = R / f.rt * f.rt;
+    const int R = g.n * a.G, full = R & -f.rt;
     return (long long)a.Hkv * (full + paged_alloc(f, R - full));
 }
 
@@ -124,17 +125,19 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
     constexpr int K = (kPagedHere + THREADS - 1) / THREADS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PagedSeg g[K];
-    long long w = 0, r = 0;
+    long long gw[K], gr[K], w = 0, r = 0;  // of each segment, and of the thread's
     int bad = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int s = threadIdx.x * K + k;
-        g[k].n = g[k].w = 0;
+        gw[k] = gr[k] = 0;
         if (s < f.S) {
             bad |= !paged_record(a, f, fi, s, g[k]);
-            w += paged_tiles(a, f, g[k]);
-            r += paged_rows(a, f, g[k]);
+            gw[k] = paged_tiles(a, f, g[k]);
+            gr[k] = paged_rows(a, f, g[k]);
         }
+        w += gw[k];
+        r += gr[k];
     }
     long long wi = w, ri = r;  // inclusive over the warp
 #pragma unroll
@@ -173,15 +176,14 @@ __device__ __forceinline__ long long paged_plan_here(const PagedArgs &a, const P
     for (int k = 0; k < K; ++k) {
         const int s = threadIdx.x * K + k;
         if (s >= f.S) break;
-        const long long tiles = paged_tiles(a, f, g[k]);
-        if (want < 0 ? x >= w0 && x < w0 + tiles : s == want) {
+        if (want < 0 ? x >= w0 && x < w0 + gw[k] : s == want) {
             g[k].W0 = w0;
             g[k].R0 = r0;
             sh.g = g[k];
             sh.s = s;
         }
-        w0 += tiles;
-        r0 += paged_rows(a, f, g[k]);
+        w0 += gw[k];
+        r0 += gr[k];
     }
     plan_sync<THREADS, BAR>();
     return bad ? 0 : per;
@@ -231,7 +233,7 @@ __device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily
         const long long rel = k.x - k.g.W0;
         const PagedCost cost = paged_cost(a, f, k.g);
         const int all = paged_all(k.g, cost);
-        const int lu = (int)paged_div(rel, all), rtile = lu / a.Hkv;
+        const int lu = (int)paged_div(rel, all), rtile = lu < a.Hkv ? 0 : lu / a.Hkv;
         const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
         k.x += to - from;
         u.t0 = paged_tile(from, cost);
@@ -242,7 +244,7 @@ __device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily
         u.n = k.g.n;
         u.len = k.g.len;
         u.h = lu - rtile * a.Hkv;
-        u.r0 = rtile * f.rt;
+        u.r0 = rtile << f.rt_log;
         u.rows = min(f.rt, k.g.n * a.G - u.r0);
         u.base = k.g.R0 + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
         return true;

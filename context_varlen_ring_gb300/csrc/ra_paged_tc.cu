@@ -199,6 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
             for (Walk w; ok && next_unit(w);) {
                 const int tok = w.u.tok0 + (w.u.r0 >> p.log2G), hq = w.u.h << p.log2G;
+                // the page of this lane's box of a tile, as the table has it (n_pages: outside the cache, filled with zeros)
+                auto look_up = [&](int t) {
+                    const int key = t * 128 + (lane >> 1) * p.box;
+                    return lane < boxes && key < w.u.len ? __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size)
+                                                         : (int)a.n_pages;
+                };
+                int pa = look_up(w.u.t0), pb = look_up(w.u.t0 + 1);
                 if (lane == 0) {
                     if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1u, wc);
                     if (ok) {
@@ -211,12 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                // the page of this lane's box of a tile, as the table has it (n_pages: outside the cache, filled with zeros)
-                auto look_up = [&](int t) {
-                    const int key = t * 128 + (lane >> 1) * p.box;
-                    return lane < boxes && key < w.u.len ? __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size)
-                                                         : (int)a.n_pages;
-                };
                 auto load = [&](const CUtensorMap *m, int t, int page) {
                     const uint32_t slot = n % kSlots;
                     // (all that can be done ahead of the wait is: a free slot is to be filled at once)
@@ -235,8 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     ++n;
                 };
                 const int by = w.pair ? 1 : 2;
-                // the next step's pages are looked up ahead of this step's waits
-                int pa = look_up(w.u.t0), pb = look_up(w.u.t0 + 1);
+                // (the next step's pages are looked up ahead of this step's waits)
 #pragma unroll 1
                 for (int t = w.u.t0; t < w.tend && ok; t += by) {
                     const int cnt = !w.pair && t + 1 < w.tend ? 2 : 1;

@@ -297,6 +297,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         const double tiles = (double)Hkv * F.S * ((most + 63) / 64) * ((F.width * cache->page_size + 63) / 64);
         if (kind[f] == kSimt && tiles <= paged_sms()) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
+        while (1 << F.rt_log < F.rt) ++F.rt_log;
+        while (1 << F.kt_log < F.kt) ++F.kt_log;
         F.halves = kind[f] == kWide;
         // The shortest run, in sixteenths of a warp-level tile: two tiles where a partial has 32 rows or more, whose
         // write and join cost about a tile.  8192 keys of one KV head: 64 rows with 1, 2 and 4 tiles at least 17.9,
