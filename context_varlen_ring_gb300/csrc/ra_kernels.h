@@ -222,6 +222,7 @@ struct RopeJob {
     int heads;
     int rotate;                        // 0: copied
     int paged;                         // written to the token's cache row instead of its token row
+    int groups;                        // of hpi heads (set by launch_rope)
 };
 // Travels with the launch (a kernel parameter), so a captured graph keeps it.
 struct RopeParams {
@@ -231,12 +232,13 @@ struct RopeParams {
     const int32_t *pos;                // DEVICE [axes][T]
     int n_pairs, adjacent, inverse;
     int units, rot_units, split;       // set by launch_rope
+    int hpi, unit_inv;                 // heads a warp takes at once; 2^16 / units, rounded up
     int stages, stage_bytes, parts, share;  // of the ring kernel: a token's shares, heads a share
     unsigned long long budget_ns;
     // cache rows (cu != NULL): logical index kv_lens[b] - n_b + j through the page table
     const int32_t *cu, *kv_lens, *page_table;
     int64_t table_width, table_keys, n_pages, page_stride, token_stride, head_stride;
-    int B, page_size;
+    int B, page_size, page_shift;      // page_shift: its log2, or -1
     int *status;
     uint64_t turns[128];               // inv_freq / (2 pi) modulo 1, in units of 2^-64
     uint8_t axis[128];
@@ -247,9 +249,9 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st);
 // ------------------------------------------------------------ paged attention
 // Families of segments: 0 the sequences' own keys, 1 the groups' prefixes.
 // Each (segment, tile of `rt` query rows, KV head) is a unit of ceil(keys / kt)
-// key tiles, each weighing what it costs; the units' tiles form one line that
-// the family's `n` CTAs split evenly.  What CTA c computes of a unit whose rows start at partial row
-// `base` goes to partial rows base + rt * c on: along the line units and CTAs
+// key tiles; a unit and its tiles weigh what they cost, and the units form one
+// line that the family's `n` CTAs split evenly.  What CTA c computes of a unit
+// whose rows start at partial row `base` goes to partial rows base + rt * c on: along the line units and CTAs
 // only grow, and no unit has more than rt partial rows, so these never meet.
 struct alignas(16) PagedSeg {
     int tok0, n, len, w;               // first query token, query tokens, keys, key tiles
@@ -278,6 +280,7 @@ struct PagedArgs {
     const void *k, *v;
     int64_t n_pages, page_stride, token_stride, head_stride;
     int page_size, page_shift;         // page_shift: its log2, or -1
+    unsigned long long G_inv;          // 2^64 / G, rounded up (G > 1)
     int B, n_groups, causal;
     const int32_t *cu, *kv_lens, *prefix_lens, *groups;
     float scale_log2;

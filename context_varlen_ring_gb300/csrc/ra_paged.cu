@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
             const int r = i / (D / 4), c = i % (D / 4) * 4, row = r0 + r;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (row < R) {
-                const int64_t t = g.tok0 + row / a.G;
-                v = load4(static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)(u.h * a.G + row % a.G) * D + c);
+                const int t = paged_token(a, row);
+                v = load4(static_cast<const T *>(a.q) + (int64_t)(g.tok0 + t) * a.q_stride +
+                          (int64_t)(u.h * a.G + row - t * a.G) * D + c);
                 v.x *= a.scale_log2;
                 v.y *= a.scale_log2;
                 v.z *= a.scale_log2;

@@ -16,6 +16,15 @@ __device__ __forceinline__ long long paged_div(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
+// Query token of a row, row / G: exact for rows of 32 bits, by one product.
+__device__ __forceinline__ int paged_token(const PagedArgs &a, int row) {
+    return a.G == 1 ? row : (int)__umul64hi((unsigned)row, a.G_inv);
+}
+// Page of a key, and its row in it.
+__device__ __forceinline__ int paged_page(const PagedArgs &a, int key) {
+    return a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+}
+
 // Partial rows of a tile of `rows` query rows.
 __device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
     return f.halves && 2 * rows <= f.rt ? 2 * rows : rows;
@@ -257,14 +266,14 @@ __device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily
 template <typename Seg>
 __device__ __forceinline__ int paged_limit(const PagedArgs &a, const Seg &g, int family, int row) {
     if (row >= g.n * a.G) return 0;
-    return family || !a.causal ? g.len : g.len - g.n + row / a.G + 1;
+    return family || !a.causal ? g.len : g.len - g.n + paged_token(a, row) + 1;
 }
 
 // Element offset of key `i`'s row (head 0), or -1 where there is none: behind
 // the length, or on a page outside the cache (recorded).
 __device__ __forceinline__ int64_t paged_row(const PagedArgs &a, const PagedFamily &f, int s, int len, int i) {
     if (i >= len) return -1;
-    const int pi = a.page_shift >= 0 ? i >> a.page_shift : i / a.page_size;
+    const int pi = paged_page(a, i);
     const int pg = __ldg(f.table + (int64_t)s * f.width + pi);
     if (pg < 0 || pg >= a.n_pages) {
         record_status(a.status, RA_ERR_DEVICE_BOUNDS);

@@ -272,9 +272,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
                 w.m[r] = -INFINITY;
                 w.l[r] = 0.f;
                 const bool ok = row < R;
+                const int tok = paged_token(a, row);
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                         (ok ? (int64_t)(u.tok0 + row / a.G) * a.q_stride +
-                                                   (int64_t)(u.h * a.G + row % a.G) * D : 0) + (lane & 3) * 2;
+                                         (ok ? (int64_t)(u.tok0 + tok) * a.q_stride +
+                                                   (int64_t)(u.h * a.G + row - tok * a.G) * D : 0) + (lane & 3) * 2;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     w.q[k][r] = ok ? *reinterpret_cast<const uint32_t *>(q + k * 16) : 0u;

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 // the page of this lane's box of a tile, as the table has it (n_pages: outside the cache, filled with zeros)
                 auto look_up = [&](int t) {
                     const int key = t * 128 + (lane >> 1) * p.box;
-                    return lane < boxes && key < w.u.len ? __ldg(f.table + (int64_t)w.u.s * f.width + key / a.page_size)
+                    return lane < boxes && key < w.u.len ? __ldg(f.table + (int64_t)w.u.s * f.width + paged_page(a, key))
                                                          : (int)a.n_pages;
                 };
                 int pa = look_up(w.u.t0), pb = look_up(w.u.t0 + 1);
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 auto load = [&](const CUtensorMap *m, int t, int page) {
                     const uint32_t slot = n % kSlots;
                     // (all that can be done ahead of the wait is: a free slot is to be filled at once)
-                    const int key = t * 128 + (lane >> 1) * p.box, row = key % a.page_size;
+                    const int key = t * 128 + (lane >> 1) * p.box, row = key - paged_page(a, key) * a.page_size;
                     if (page < 0 || page >= a.n_pages) {
                         if (lane < boxes && key < w.u.len) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
                         page = (int)a.n_pages;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 // V rows behind the length, up to the end of their page, may hold anything
                 auto clean = [&](int t, uint32_t i) {
                     const int live = w.u.len - t * 128;
-                    if (live >= 128 || w.u.len % a.page_size == 0) return;
+                    if (live >= 128 || w.u.len == paged_page(a, w.u.len) * a.page_size) return;
                     uint8_t *v = base + kOffKV + (i % kSlots) * kTile;
                     for (int c = live * 8 + lane; c < 1024; c += 32) {
                         *reinterpret_cast<uint4 *>(v + c * 16) = make_uint4(0, 0, 0, 0);

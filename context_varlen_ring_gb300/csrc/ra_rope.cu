@@ -91,6 +91,10 @@ __device__ __forceinline__ void turn_unit(typename Pack<T, VEC>::V &a, typename 
     a = repack<T, VEC>(fa);
 }
 
+__device__ __forceinline__ int page_of(const RopeParams &p, int key) {
+    return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+}
+
 // A warp owns a token, or where tokens are few every S-th group of its heads.
 // Lane (hh, u) owns unit u (a vector, or the two vectors of a half-split pair)
 // of heads hh, hh + hpi, ...: its sines and cosines stay in registers for all
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float2 *cs = cs_all + warp * p.n_pairs;
     const int64_t gw = (int64_t)blockIdx.x * kRopeWarps + warp;
-    const int64_t t = gw / p.split;
+    const int64_t t = p.split == 1 ? gw : (int64_t)((unsigned)gw / (unsigned)p.split);  // (split only when tokens are few)
     if (t >= p.T) return;
     const int sub = (int)(gw - t * p.split);
 
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
                 const long long idx = (long long)p.kv_lens[s] - n + (t - c0);
                 bool in = t >= c0 && idx >= 0 && idx < p.table_keys;
                 if (in) {
-                    const int pi = (int)idx / p.page_size;
+                    const int pi = page_of(p, (int)idx);
                     const int pg = p.page_table[(int64_t)s * p.table_width + pi];
                     in = pg >= 0 && pg < p.n_pages;
                     off = pg * p.page_stride + ((int)idx - pi * p.page_size) * p.token_stride;
@@ -158,8 +162,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
         __syncwarp();
     };
     for (int u0 = 0; u0 < p.units; u0 += 32) {  // (one trip unless a head has more than 32 units)
-        const int hpi = p.units > 32 ? 1 : 32 / p.units;
-        const int hh = p.units > 32 ? 0 : lane / p.units, u = p.units > 32 ? u0 + lane : lane % p.units;
+        const int hpi = p.hpi;
+        const int hh = p.units > 32 ? 0 : lane * p.unit_inv >> 16, u = u0 + lane - hh * p.units;
         const bool mine = hh < hpi && u < p.units;
         const bool rot = u < p.rot_units;
         int off0, off1 = -1, pb = 0;
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
             const int heads = mine ? jb.heads - hh : 0, step = p.split * hpi;  // heads from this lane's on
             const T *x = static_cast<const T *>(jb.x) + t * jb.x_stride + hh * p.d;
             const bool turn = rot && jb.rotate;
-            const int groups = (jb.heads + hpi - 1) / hpi;
+            const int groups = jb.groups;
             int h = skip * hpi;
             while (skip < groups) skip += p.split;
             skip -= groups;
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
                     const long long idx = len - (c1 - c0) + (t - c0);
                     bool in = t >= c0 && idx >= 0 && idx < p.table_keys;
                     if (in) {
-                        const int pi = (int)idx / p.page_size;
+                        const int pi = page_of(p, (int)idx);
                         if (pi != page_i) {
                             page_i = pi;
                             page = p.page_table[(int64_t)seq * p.table_width + pi];
@@ -497,7 +501,10 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens)
         return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st) : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
-    const int groups = p.units > 32 ? p.total_heads : (p.total_heads + 32 / p.units - 1) / (32 / p.units);
+    p.hpi = p.units > 32 ? 1 : 32 / p.units;
+    p.unit_inv = (65535 + p.units) / p.units;
+    for (int j = 0; j < p.njobs; ++j) p.jobs[j].groups = (p.jobs[j].heads + p.hpi - 1) / p.hpi;
+    const int groups = (p.total_heads + p.hpi - 1) / p.hpi;
     p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));
     if (dtype == RA_FP32) {
         if (!fast) return launch_warps<float, 1, false>(p, st);

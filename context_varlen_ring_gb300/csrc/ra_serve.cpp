@@ -22,6 +22,12 @@ bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int elem(int dtype) { return dtype == RA_FP32 ? 4 : 2; }
 bool on_elem(const void *p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem(dtype) == 0; }
 
+int log2_or_none(int x) {
+    for (int i = 0; i < 31; ++i)
+        if (x == 1 << i) return i;
+    return -1;
+}
+
 ra_status check_rope(const ra_rope *r, const int32_t *pos, int d) {
     if (!r->inv_freq || !pos) return fail(RA_ERR_INVALID_ARG, "inv_freq or pos is NULL");
     if (r->n_axes < 1 || r->n_axes > 8) return fail(RA_ERR_INVALID_ARG, "n_axes must be in [1, 8]");
@@ -203,6 +209,7 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
     p.head_stride = cache->head_stride;
     p.B = B;
     p.page_size = cache->page_size;
+    p.page_shift = log2_or_none(cache->page_size);
     p.status = device_status_ptr();
     ProfScope ps("ra_kv_cache_append", static_cast<cudaStream_t>(stream));
     const cudaError_t e = launch_rope(p, dt, static_cast<cudaStream_t>(stream));
@@ -265,9 +272,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.token_stride = cache->token_stride;
     a.head_stride = cache->head_stride;
     a.page_size = cache->page_size;
-    a.page_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (cache->page_size == 1 << i) a.page_shift = i;
+    a.page_shift = log2_or_none(cache->page_size);
+    if (a.G > 1) a.G_inv = ~0ull / (unsigned)a.G + 1;
     a.B = B;
     a.n_groups = n_groups;
     a.causal = causal != 0;
