@@ -261,23 +261,8 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
     const dev::WaitCtl wc{&abort_flag, p.status, p.budget_ns};
 
     const int64_t TS = (int64_t)gridDim.x * warps, t0 = min(p.T, (int64_t)blockIdx.x * warps + warp), t1 = p.T;
-    const int items = t0 < t1 ? (int)((t1 - t0 + TS - 1) / TS) * p.parts : 0;  // this warp's stages: token i / parts, share i % parts
-    const int hpi = 32 / p.rot_units, hh = lane / p.rot_units, u = lane % p.rot_units;
-    const int off0 = u * 16, off1 = p.n_pairs * (int)sizeof(T) + u * 16, pb = u * NP;
+    const int items = t0 < t1 ? (int)((unsigned)(t1 - t0 + TS - 1) / (unsigned)TS) * p.parts : 0;  // this warp's stages: token i / parts, share i % parts
     const int row = p.d * (int)sizeof(T);
-    int rotated = 0;  // heads, which come first
-    for (int j = 0; j < p.njobs; ++j) rotated += p.jobs[j].rotate ? p.jobs[j].heads : 0;
-    // this lane's pairs: angle a position, and where its positions are
-    unsigned long long turns[4];
-    const int32_t *pos_at[4];
-    int pos[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int w = min(lane + 32 * k, p.n_pairs - 1);
-        turns[k] = p.turns[w];
-        pos_at[k] = p.pos + (int64_t)p.axis[w] * p.T;
-        pos[k] = t0 < t1 ? __ldg(pos_at[k] + t0) : 0;
-    }
     // the heads [from, to) of job j in a share of the heads [ha, hb), at `src` of the stage
     struct Piece {
         int from, to;
@@ -326,6 +311,21 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
     };
     if (lane == 0)
         while (ld.i < min(items, p.stages - 2)) load();
+    const int hpi = 32 / p.rot_units, hh = lane / p.rot_units, u = lane % p.rot_units;
+    const int off0 = u * 16, off1 = p.n_pairs * (int)sizeof(T) + u * 16, pb = u * NP;
+    int rotated = 0;  // heads, which come first
+    for (int j = 0; j < p.njobs; ++j) rotated += p.jobs[j].rotate ? p.jobs[j].heads : 0;
+    // this lane's pairs: angle a position, and where its positions are
+    unsigned long long turns[4];
+    const int32_t *pos_at[4];
+    int pos[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int w = min(lane + 32 * k, p.n_pairs - 1);
+        turns[k] = p.turns[w];
+        pos_at[k] = p.pos + (int64_t)p.axis[w] * p.T;
+        pos[k] = t0 < t1 ? __ldg(pos_at[k] + t0) : 0;
+    }
     // the sequence of the token in hand, its page, and the angles of this lane's unit
     int seq = -1, page = -1, page_i = -1, ok = 1;
     long long c0 = 0, c1 = -1, len = 0, off = 0;
