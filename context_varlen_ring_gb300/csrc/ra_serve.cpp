@@ -124,7 +124,7 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
         L.o_start[f] = take((size_t)kPagedMaxCtas * 4);
         // the rows themselves (twice where units are halved), and one unit more a CTA
         const int64_t most = paged_rows(f, T, G, max_q_len);
-        const bool wide = most > (f ? 16 : 64) && dtype == RA_BF16 && d == 128;
+        const bool wide = most > (f ? 16 : 32) && dtype == RA_BF16 && d == 128;
         int64_t rows = S ? T * G * Hkv + (int64_t)kPagedMaxCtas * (most <= 16 ? 16 : 64) : 0;
         if (S && wide) rows = std::max(rows, 2 * T * G * Hkv + (int64_t)kPagedMaxWide * kPagedWideRows);
         L.o_acc[f] = take((size_t)rows * d * 4);
@@ -285,15 +285,16 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     enum { kSimt, kMma, kWide } kind[2];
     PagedMaps maps;
     const bool wide =
-        (paged_rows(0, T, a.G, max_q_len) > 64 || (n_groups > 0 && T * a.G > 16)) && paged_tc_maps(a, maps);
+        (paged_rows(0, T, a.G, max_q_len) > 32 || (n_groups > 0 && T * a.G > 16)) && paged_tc_maps(a, maps);
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
-        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  Measured: own keys,
-        // 24 rows: 64-row tiles 53 us, two passes of 16 rows 62, tcgen05 68; 64 rows: 82, tcgen05 87.  A prefix of
-        // 30000 keys, 32 and 64 rows: tcgen05 41 and 42 us, warp-level 46 and 54.
+        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  Measured, own keys of
+        // 24 sequences, 24 rows: warp-level 44 us, tcgen05 50; 48 rows: 61 and 59; 64 rows: 74 and 70, 64 sequences of
+        // one KV head 27.6 and 22.4 (but 8 short ones, 48 rows, 14.5 and 16.6).  A prefix of 30000 keys, 32 rows: 36.5
+        // and 35.5; 64 rows: 54.5 and 42.
         const int64_t most = paged_rows(f, T, a.G, max_q_len);
         kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
-        if (most > (f ? 16 : 64) && wide) kind[f] = kWide;
+        if (most > (f ? 16 : 32) && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
         F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
         // (a cache without pages holds no keys: every length above 0 is out of range)
