@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 constexpr int kBulkWarps = 16, kBulkStages = 8, kRingBytes = 212 * 1024, kBulkSmem = 224 * 1024;
-constexpr int64_t kBulkTokens = 4096;
+constexpr int kHeldWarps = 20;
 
 template <typename T, int VEC>
 struct Pack;
@@ -102,7 +102,7 @@ __device__ __forceinline__ int page_of(const RopeParams &p, int key) {
 // head the shared-memory pipe was the limit, at 81 %).  Two heads a lane are
 // in flight, the first two before the angles are computed.  A chain of loads
 // bounds the small calls this kernel is for (64 tokens appended to their
-// caches: 5.2 us): the token's sequence, its page, and beside them the positions.
+// caches: 5.1 us): the token's sequence, its page, and beside them the positions.
 template <typename T, int VEC, bool ADJ>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_constant__ RopeParams p) {
     using V = typename Pack<T, VEC>::V;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
 // shared memory, copied in and out by the bulk-copy engine.  All warps go
 // through the tokens side by side (with a run of consecutive tokens each, their
 // rows lay at multiples of one distance and met in the same memory channels:
-// 112 to 130 us for 32768 tokens, 107 so).
+// 112 to 130 us for 32768 tokens, 104 to 107 so).
 // A stage holds a token's heads (queries, keys, values, one behind the other),
 // or one of `parts` shares of them; the rotated units are read, turned and
 // written back in place.  So the bytes in flight are the rings' (some 100 KB
@@ -433,7 +433,7 @@ template <typename T>
 cudaError_t launch_bulk(RopeParams &p, int sms, cudaStream_t st) {
     // four or more stages a warp, in kRingBytes
     // (with cache rows to find a warp waits longer between stages: smaller ones and more warps.  Stages of 5 and of
-    // 8 KB: 32768 tokens appended 194 and 235 us, rotated 109 and 107; 8192 tokens of 72 heads 57 and 53)
+    // 8 KB: 32768 tokens appended 192 and 231 us, rotated 104 and 104; 8192 tokens of 72 heads 54 and 52)
     const int row = p.d * (int)sizeof(T), part = p.cu ? 5120 : 8192;
     p.parts = (p.total_heads * row + part - 1) / part;
     p.share = (p.total_heads + p.parts - 1) / p.parts;
@@ -496,9 +496,10 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
-    // Many tokens: the ring kernel, which needs whole vectors and at most 32 units a head.  (40 heads of 128: at 4096
-    // tokens 19.0 us, the warp kernel 19.2; at 32768 109 and 128; a small call waits less for warps than for rings)
-    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T >= kBulkTokens)
+    // More tokens than the warp kernel holds at once (20 warps an SM): the ring kernel, which needs whole vectors and
+    // at most 32 units a head.  (40 heads of 128, warp kernel and ring: 3000 tokens 14.4 and 13.8 us, 3100 21.9 and
+    // 17.0, 32768 140 and 104; 9 heads: 3000 tokens 7.2 and 9.5, 3500 10.8 and 9.5)
+    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T > (int64_t)kHeldWarps * paged_sms())
         return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st) : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
     p.hpi = p.units > 32 ? 1 : 32 / p.units;

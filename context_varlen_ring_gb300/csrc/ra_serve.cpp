@@ -300,7 +300,7 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         // (a cache without pages holds no keys: every length above 0 is out of range)
         F.width = cache->n_pages == 0 ? 0 : f ? prefix_width : table_width;
         // the SIMT kernel with too few 64-row tiles for the SMs: four times as many of a quarter (9 sequences of 5
-        // to 700 fp32 keys of 64 behind a prefix of 1500: 19.5 us, with 64-row tiles 22)
+        // to 700 fp32 keys of 64 behind a prefix of 1500: 17 us, with 64-row tiles 20)
         const double tiles = (double)Hkv * F.S * ((most + 63) / 64) * ((F.width * cache->page_size + 63) / 64);
         if (kind[f] == kSimt && tiles <= paged_sms()) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
@@ -308,9 +308,9 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         while (1 << F.kt_log < F.kt) ++F.kt_log;
         F.halves = kind[f] == kWide;
         // The shortest run, in sixteenths of a warp-level tile: two tiles where a partial has 32 rows or more, whose
-        // write and join cost about a tile.  8192 keys of one KV head: 64 rows with 1, 2 and 4 tiles at least 17.9,
-        // 15.9 and 17.9 us, 32 rows 16.6 with 1, 14.3 with 2; the tcgen05 kernel, 128 rows: 22.2 with 1, 20.0 with
-        // 2, 20.2 with 4.  With 16 rows one or two makes no difference.
+        // write and join cost about a tile.  8192 keys of one KV head, 32 rows with 1 and 2 tiles at least: 14.8 and
+        // 12.4 us; the tcgen05 kernel, 128 rows: 17.3 with 1, 15.9 with 2, 15.6 with 4 (1024 keys: 9.8, 10.6, 12.7).
+        // With 16 rows one or two makes no difference.
         F.least = kind[f] == kWide ? 64 : kind[f] == kMma && F.rt > 16 ? 32 : 16;
         if (F.S)
             F.n = kind[f] == kWide  ? std::min(kPagedMaxWide, paged_sms())
