@@ -22,7 +22,7 @@
 // behind the length is masked in S, and its V rows are zeroed in shared
 // memory before the product, so it may be anything.
 // Measured: a prefix of 65536 keys for 128 requests of 64 heads (8 of keys) in
-// 0.74 of the measured bf16 rate: a step of 128 keys takes 3130 cycles for 2048
+// 0.76 of the measured bf16 rate: a step of 128 keys takes 3130 cycles for 2048
 // of products, of which a row tile's softmax 1720, its P V and next S the rest.
 // Every wait is bounded as in the rest of the library.
 #include <cuda.h>
