@@ -477,6 +477,12 @@ MORE = [  # as ATTN, and the hint
     ([200], [700], [128], [0, 1], 16, 4, 1, 128, "both", "bf16", False, 0, 200),
     ([60, 3], [200, 90], [65], [0, 2], 16, 4, 2, 64, "nhd", "fp32", True, 0, 60),
     ([260], [100], [], [0], 16, 2, 1, 128, "nhd", "bf16", True, 0, 260),                # more queries than keys
+    # one KV head and many keys: hundreds of partials a row in the join, from every kernel
+    ([1, 1], [30000, 5], [], [0], 16, 4, 1, 128, "nhd", "bf16", True, 0, 1),
+    ([1], [25000], [], [0], 7, 20, 1, 64, "hnd", "bf16", True, 0, 1),
+    ([2, 1], [9000, 100], [12000], [0, 2], 16, 3, 1, 64, "nhd", "fp32", True, 0, 2),
+    ([3, 1], [700, 30], [40000], [0, 2], 64, 16, 1, 128, "nhd", "bf16", True, 0, 3),
+    ([1, 1], [64, 128], [20000], [0, 2], 128, 128, 1, 128, "hnd", "bf16", False, 0, 1),
     # a hint that is too small only chooses the kernels
     ([40, 1, 90], [140, 200, 300], [150], [0, 3], 16, 8, 2, 128, "nhd", "bf16", True, 0, 1),
     ([40, 1, 90], [140, 200, 300], [150], [0, 3], 16, 8, 2, 128, "nhd", "fp32", True, 0, 2),

@@ -152,3 +152,42 @@ def test_scale_is_finite_also_in_base_two(ra):
     kv = _kv(_lib)
     assert ra.lib().ra_paged_attn_fwd(FAKE, 256, 8, 4, ctypes.byref(kv), FAKE, 4, FAKE, FAKE, 2, None, 0, None, None, 0, 1,
                                       1, 3e38, FAKE, 0, FAKE, FAKE, 1 << 40, None) == _lib.RA_ERR_INVALID_ARG
+
+
+def test_split_covers_every_tile_once():
+    """The split of the attention's units over CTAs, restated: each unit stands on a line with its own cost and then
+    its key tiles; a tile belongs to the run in which it begins.  Every tile is computed once, and the partial rows of
+    different (unit, CTA) pairs do not meet nor leave the workspace."""
+    rng = np.random.default_rng(5)
+    for case in range(60):
+        rt, unit, tile = [(16, 32, 16), (64, 32, 16), (256, 96, 48), (256, 96, 32)][case % 4]
+        halves, heads, n, least = rt == 256, int(rng.integers(1, 5)), int(rng.integers(1, 200)), 16
+        S = int(rng.integers(1, 30))
+        rows = rng.integers(0, 3 * rt, S)
+        tiles = rng.integers(0, 40, S) * (rows > 0)
+        units, W, R = [], 0, 0   # place, tiles, first partial row, its rows there
+        for s in range(S):
+            for r0 in range(0, int(rows[s]), rt):
+                r = min(rt, int(rows[s]) - r0)
+                alloc = 2 * r if halves and 2 * r <= rt else r
+                for h in range(heads):
+                    if tiles[s]:
+                        units.append((W, int(tiles[s]), R, alloc))
+                        W += unit + int(tiles[s]) * tile
+                    R += alloc
+        per = max(least, -(-W // n))
+        first = lambda at: 0 if at <= unit else -(-(at - unit) // tile)  # noqa: E731
+        spans = []
+        for place, w, row, alloc in units:
+            all_ = unit + w * tile
+            seen = []
+            for c in range(place // per, (place + all_ - 1) // per + 1):
+                assert c < n
+                t0, t1 = first(max(0, c * per - place)), first(min(all_, (c + 1) * per - place))
+                if t0 < t1:
+                    seen += range(t0, t1)
+                    spans.append((row + c * rt, row + c * rt + alloc))
+            assert seen == list(range(w))
+        spans.sort()
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        assert not spans or spans[-1][1] <= R + n * rt
