@@ -163,17 +163,17 @@ def test_split_covers_every_tile_once():
         rt, unit, tile = [(16, 32, 16), (64, 32, 16), (256, 96, 48), (256, 96, 32)][case % 4]
         halves, heads, n, least = rt == 256, int(rng.integers(1, 5)), int(rng.integers(1, 200)), 16
         S = int(rng.integers(1, 30))
-        rows = rng.integers(0, 3 * rt, S)
-        tiles = rng.integers(0, 40, S) * (rows > 0)
+        rows = rng.integers(0, 3 * rt, S).tolist()
+        tiles = rng.integers(0, 40, S).tolist()
         units, W, R = [], 0, 0   # place, tiles, first partial row, its rows there
         for s in range(S):
-            for r0 in range(0, int(rows[s]), rt):
-                r = min(rt, int(rows[s]) - r0)
+            for r0 in range(0, rows[s], rt):
+                r = min(rt, rows[s] - r0)
                 alloc = 2 * r if halves and 2 * r <= rt else r
                 for h in range(heads):
                     if tiles[s]:
-                        units.append((W, int(tiles[s]), R, alloc))
-                        W += unit + int(tiles[s]) * tile
+                        units.append((W, tiles[s], R, alloc))
+                        W += unit + tiles[s] * tile
                     R += alloc
         per = max(least, -(-W // n))
         first = lambda at: 0 if at <= unit else -(-(at - unit) // tile)  # noqa: E731
