@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_simt_kernel(const __grid_con
             const int k0 = tile * kKT;
             __syncthreads();
             // a batch of loads is on its way before the first of it is stored
-            constexpr int kBatch = 16 / WARPS;
+            constexpr int kEach = kKT * (D / 4) / (WARPS * 32), kBatch = kEach % 8 == 0 ? 8 : kEach % 4 == 0 ? 4 : 2;
             for (int i0 = threadIdx.x; i0 < kKT * (D / 4); i0 += kBatch * WARPS * 32) {
                 int64_t off[kBatch];
                 float4 kv[kBatch], vv[kBatch];

@@ -300,8 +300,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
         // (a cache without pages holds no keys: every length above 0 is out of range)
         F.width = cache->n_pages == 0 ? 0 : f ? prefix_width : table_width;
         // The SIMT kernel with few 64-row tiles: four times as many of a quarter, while an SM has one of them at d > 64
-        // and four below.  fp32, 64 and 16 rows a tile: 1000 keys of 2 heads of 128, 32 rows, 17.5 and 14.6 us; 4
-        // sequences of 500, 64 rows, 22.3 and 28.2; 4000 keys of 64, 64 rows, 19.4 and 17.5.
+        // and four below.  fp32, 64 and 16 rows a tile: 1000 keys of 2 heads of 128, 32 rows, 17.5 and 15.0 us; 4
+        // sequences of 500, 64 rows, 21.8 and 28; 4000 keys of 64, 64 rows, 19.4 and 16.4.
         const double tiles = (double)Hkv * F.S * ((most + 63) / 64) * ((F.width * cache->page_size + 63) / 64);
         if (kind[f] == kSimt && 4 * tiles <= paged_sms() * (d <= 64 ? 4 : 1)) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
