@@ -4,8 +4,8 @@
 
 #include <utility>
 
-#include "ra_dev.cuh"
 #include "ra_kernels.h"
+#include "ra_serve.cuh"
 
 namespace ra {
 namespace dev {

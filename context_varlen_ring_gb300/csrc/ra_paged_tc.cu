@@ -17,10 +17,10 @@
 //    other's products although there is only one tile of rows.
 // Pages: a 4-D tensor map (d, head, row in page, page; head and row in the
 // order of their strides) with a box of min(page, 128) rows; the lanes of the
-// producer warp look up a page each and issue the boxes of a tile side by side.  Keys behind the length come from a
-// page outside the cache, which TMA fills with zeros; what a last page holds
-// behind the length is masked in S, and its V rows are zeroed in shared
-// memory before the product, so it may be anything.
+// producer warp look up a page each and issue the boxes of a tile side by side.
+// Keys behind the length come from a page outside the cache, which TMA fills
+// with zeros; what a last page holds behind the length is masked in S, and its V
+// rows are zeroed in shared memory before the product, so it may be anything.
 // Measured: a prefix of 65536 keys for 128 requests of 64 heads (8 of keys) in
 // 0.76 of the measured bf16 rate: a step of 128 keys takes 3130 cycles for 2048
 // of products, of which a row tile's softmax 1720, its P V and next S the rest.

@@ -19,8 +19,8 @@
 #include <cmath>
 #include <cstdint>
 
-#include "ra_dev.cuh"
 #include "ra_kernels.h"
+#include "ra_serve.cuh"
 
 namespace ra {
 namespace {
