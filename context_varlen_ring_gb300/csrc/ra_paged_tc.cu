@@ -78,11 +78,7 @@ __device__ __forceinline__ uint32_t low_bits(int n, int base) {
 // Columns of a tile that the softmax holds at once, in rolled loops: the
 // kernel's short runs wait for instructions as much as for anything (with the
 // tile unrolled the first one took 10000 to 17000 cycles, a later one 3400).
-constexpr int kCols = 64, kChunks = 128 / kCols;
-__device__ __forceinline__ void load_cols(uint32_t t, uint32_t (&v)[32]) { tmem_ld32(t, v); }
-__device__ __forceinline__ void load_cols(uint32_t t, uint32_t (&v)[64]) { tmem_ld64(t, v); }
-__device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&v)[16]) { tmem_st16(t, v); }
-__device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&v)[32]) { tmem_st32(t, v); }
+constexpr int kCols = 64, kChunks = 128 / kCols;  // (the loads and stores below are of 64 and 32 columns)
 __device__ __forceinline__ void mask_cols(uint32_t (&v)[kCols], int seen, int base) {
 #pragma unroll
     for (int c = 0; c < kCols; c += 32) {
@@ -366,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             uint32_t v[kCols];
 #pragma unroll 1
             for (int ch = kChunks - 1; ch >= 0; --ch) {  // (the first columns last: they stay for the exponentials)
-                load_cols(tS + kCols * ch, v);
+                tmem_ld64(tS + kCols * ch, v);
                 if (cut) mask_cols(v, seen, kCols * ch);
                 float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -395,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t pk[kCols / 2];
                 if (ch) {
-                    load_cols(tS + kCols * ch, v);
+                    tmem_ld64(tS + kCols * ch, v);
                     if (cut) mask_cols(v, seen, kCols * ch);
                 }
                 float2 sum4[2] = {sum2, make_float2(0.f, 0.f)};
@@ -407,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     pk[c] = pack_bf16x2(e2.x, e2.y);
                 }
                 sum2 = add2(sum4[0], sum4[1]);
-                if (live) store_cols(tS + kCols / 2 * ch, pk);
+                if (live) tmem_st32(tS + kCols / 2 * ch, pk);
             }
             l_run += sum2.x + sum2.y;
             if (live) {
