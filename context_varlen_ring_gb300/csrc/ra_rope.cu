@@ -496,16 +496,21 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
     const bool adj = fast && p.adjacent;
     p.rot_units = adj ? 2 * p.n_pairs / vec : p.n_pairs / vec;
     p.units = p.rot_units + (p.d - 2 * p.n_pairs) / vec;
-    // More tokens than the warp kernel holds at once (20 warps an SM): the ring kernel, which needs whole vectors and
-    // at most 32 units a head.  (40 heads of 128, warp kernel and ring: 3000 tokens 14.4 and 13.8 us, 3100 21.9 and
-    // 17.0, 32768 140 and 104; 9 heads: 3000 tokens 7.2 and 9.5, 3500 10.8 and 9.5)
-    if (fast && p.n_pairs > 0 && p.rot_units <= 32 && p.T > (int64_t)kHeldWarps * paged_sms())
-        return dtype == RA_FP32 ? launch_bulk<float>(p, paged_sms(), st) : launch_bulk<__nv_bfloat16>(p, paged_sms(), st);
-    // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
     p.hpi = p.units > 32 ? 1 : 32 / p.units;
     p.unit_inv = (65535 + p.units) / p.units;
     for (int j = 0; j < p.njobs; ++j) p.jobs[j].groups = (p.jobs[j].heads + p.hpi - 1) / p.hpi;
     const int groups = (p.total_heads + p.hpi - 1) / p.hpi;
+    // The ring kernel, which needs whole vectors and at most 32 units a head: for more tokens than the warp kernel
+    // holds at once (20 warps an SM), and, rotating alone, for tokens of so many heads that the warps' loops over them
+    // are longer.  (Heads of 128, warp kernel and ring.  40 heads: 3000 tokens 14.4 and 13.8 us, 3100 21.9 and 17.0,
+    // 32768 140 and 104; 9 heads: 3000 tokens 7.2 and 9.5, 3500 10.8 and 9.5; 72 heads: 1000 tokens 9.9 and 9.3, 1400
+    // 17.3 and 15.4, half of them rotated 29.6 and 12.6; 136 heads: 400 tokens 8.3 and 12.9, 1000 18.7 and 13.6.
+    // Appended, 48 heads: 3000 tokens 17.8 and 19.3.)
+    const int64_t sms = paged_sms();
+    if (fast && p.n_pairs > 0 && p.rot_units <= 32 &&
+        (p.T > kHeldWarps * sms || (!p.cu && p.T >= 4 * sms && p.T * groups > 144 * sms)))
+        return dtype == RA_FP32 ? launch_bulk<float>(p, (int)sms, st) : launch_bulk<__nv_bfloat16>(p, (int)sms, st);
+    // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
     p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));
     if (dtype == RA_FP32) {
         if (!fast) return launch_warps<float, 1, false>(p, st);

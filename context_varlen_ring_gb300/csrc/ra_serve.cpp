@@ -283,27 +283,37 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
     a.groups = prefix_groups;
     a.scale_log2 = scale_log2;
     enum { kSimt, kMma, kWide } kind[2];
-    PagedMaps maps;
-    const bool wide =
-        (paged_rows(0, T, a.G, max_q_len) > 32 || (n_groups > 0 && T * a.G > 16)) && paged_tc_maps(a, maps);
+    int64_t most[2];   // query rows of a segment per KV head
+    double passes[2];  // of 64 rows over tiles of 64 keys, at most: what the warp-level kernel would make
+    bool want = false;
     for (int f = 0; f < 2; ++f) {
         PagedFamily &F = a.f[f];
-        // Rows a unit: what one warp-level pass over the keys holds, else the tcgen05 kernel's.  Measured, own keys of
-        // 24 sequences, 24 rows: warp-level 44 us, tcgen05 50; 48 rows: 61 and 59; 64 rows: 74 and 70, 64 sequences of
-        // one KV head 27.6 and 22.4 (but 8 short ones, 48 rows, 14.5 and 16.6).  A prefix of 30000 keys, 32 rows: 36.5
-        // and 35.5; 64 rows: 54.5 and 42.
-        const int64_t most = paged_rows(f, T, a.G, max_q_len);
-        kind[f] = paged_mma_supported(dtype, d) ? kMma : kSimt;
-        if (most > (f ? 16 : 32) && wide) kind[f] = kWide;
         F.S = f ? n_groups : B;
-        F.rt = kind[f] == kWide ? kPagedWideRows : most <= 16 ? 16 : kind[f] == kMma && most <= 32 ? 32 : 64;
         // (a cache without pages holds no keys: every length above 0 is out of range)
         F.width = cache->n_pages == 0 ? 0 : f ? prefix_width : table_width;
+        most[f] = paged_rows(f, T, a.G, max_q_len);
+        const int64_t tiles = (most[f] + 63) / 64;  // (a family's prefixes share its rows)
+        passes[f] = (double)Hkv * (f ? std::max<int64_t>(F.S, tiles) : F.S * tiles) * ((F.width * cache->page_size + 63) / 64);
+        // The kernel: what one warp-level pass over the keys holds, else the tcgen05 kernel's where there is enough to
+        // do (it starts 4 us later).  Measured, own keys of 24 sequences, 24 rows: warp-level 44 us, tcgen05 50; 48
+        // rows: 61 and 59; 64 rows: 74 and 70, 64 sequences of one KV head 27.6 and 22.4.  A prefix for 8 KV heads, 32
+        // rows: 8000 keys 22.8 and 23.6, 30000 keys 36.5 and 35.5; 64 rows: 2000 keys 22.5 and 23.9, 4000 26.6 and
+        // 26.0, 8000 34.3 and 30.2; 256 rows: 1000 keys 24.5 and 25.5, 2000 30.7 and 28.2.
+        kind[f] = !paged_mma_supported(dtype, d) ? kSimt
+                  : F.S && most[f] > (f ? 16 : 32) && passes[f] > (most[f] <= 32 ? 12 : 3) * (double)paged_sms() ? kWide
+                                                                                                                  : kMma;
+        want = want || kind[f] == kWide;
+    }
+    PagedMaps maps;
+    const bool wide = want && paged_tc_maps(a, maps);
+    for (int f = 0; f < 2; ++f) {
+        PagedFamily &F = a.f[f];
+        if (kind[f] == kWide && !wide) kind[f] = kMma;
+        F.rt = kind[f] == kWide ? kPagedWideRows : most[f] <= 16 ? 16 : kind[f] == kMma && most[f] <= 32 ? 32 : 64;
         // The SIMT kernel with few 64-row tiles: four times as many of a quarter, while an SM has one of them at d > 64
         // and four below.  fp32, 64 and 16 rows a tile: 1000 keys of 2 heads of 128, 32 rows, 17.5 and 15.0 us; 4
         // sequences of 500, 64 rows, 21.8 and 28; 4000 keys of 64, 64 rows, 19.4 and 16.4.
-        const double tiles = (double)Hkv * F.S * ((most + 63) / 64) * ((F.width * cache->page_size + 63) / 64);
-        if (kind[f] == kSimt && 4 * tiles <= paged_sms() * (d <= 64 ? 4 : 1)) F.rt = 16;
+        if (kind[f] == kSimt && 4 * passes[f] <= paged_sms() * (d <= 64 ? 4 : 1)) F.rt = 16;
         F.kt = kind[f] == kWide ? 128 : 64;
         while (1 << F.rt_log < F.rt) ++F.rt_log;
         while (1 << F.kt_log < F.kt) ++F.kt_log;

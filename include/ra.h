@@ -447,8 +447,9 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  *   page_table [B, table_width], prefix_table [n_groups, prefix_width],
  *   cu_seqlens_q [B+1], kv_lens [B], prefix_lens [n_groups],
  *   prefix_groups [n_groups+1]: DEVICE int32
- *   max_q_len: the most query tokens a sequence is expected to have; it only
- *      chooses the kernels (<= 0: not known), results hold for any n_b
+ *   max_q_len: the most query tokens a sequence is expected to have; it and
+ *      the tables' widths only choose the kernels (<= 0: not known), results
+ *      hold for any n_b
  *   workspace DEVICE, 256-byte aligned, >= ra_paged_attn_workspace_bytes(...);
  *      every byte read from it is written by the same call first.  Calls in
  *      flight at the same time, and captured graphs that may run so, need

@@ -248,13 +248,21 @@ ATTN = [  # new, kv lens, prefix lens, groups, page, hq, hkv, d, layout, dtype, 
 ]
 
 
-def _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint=True, seed=0, **kw):
+def roomy_table(t, page):
+    """Columns for far more keys than there are, as a table of the longest context has: the kernels are chosen by the
+    keys that a table has room for, and with many the tcgen05 kernel is."""
+    return np.concatenate([t, np.full((len(t), 130000 // (page * max(len(t), 1)) + 1), -1)], 1)
+
+
+def _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint=True, seed=0, roomy=True,
+          **kw):
     S = len(lens)
+    room = (lambda t: roomy_table(t, page)) if roomy else (lambda t: t)
     c = Cache(list(lens) + list(plens), page, hkv, d, dtype, layout, seed=seed)
     cu = np.concatenate([[0], np.cumsum(new)])
     q = randn((int(cu[-1]) + pad, hq, d), 7 + seed, dtype)
-    own = dev(c.tables[:S])
-    pre = dict(prefix_table=dev(c.tables[S:]), prefix_lens=dev(plens), prefix_groups=dev(groups)) if plens else {}
+    own = dev(room(c.tables[:S]))
+    pre = dict(prefix_table=dev(room(c.tables[S:])), prefix_lens=dev(plens), prefix_groups=dev(groups)) if plens else {}
     args = (q, c.k, c.v, own, dev(cu), dev(lens))
     kw = dict(pre, causal=causal, max_q_len=max(new) if hint else None, **kw)
     return c, cu, args, kw
@@ -262,9 +270,9 @@ def _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal,
 
 @pytest.mark.parametrize("new,lens,plens,groups,page,hq,hkv,d,layout,dtype,causal,pad", ATTN)
 @pytest.mark.parametrize("hint", [True, False])
-@pytest.mark.parametrize("out32", [False, True])
-def test_paged_attention(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint, out32):
-    c, cu, args, kw = _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint)
+@pytest.mark.parametrize("out32,roomy", [(False, True), (True, True), (False, False)])
+def test_paged_attention(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint, out32, roomy):
+    c, cu, args, kw = _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, hint, roomy=roomy)
     q, S = args[0], len(lens)
     out = torch.full(q.shape, 3.0, dtype=torch.float32 if out32 else q.dtype, device="cuda")
     lse = torch.full((hq, q.shape[0]), 3.0, device="cuda")
@@ -323,7 +331,7 @@ def test_paged_attention_partials_merge(ra):
 def test_paged_attention_checks_its_index_arrays(ra):
     """Boundaries, groups and lengths outside their ranges are recorded and leave the results unwritten;
     a page outside the cache is recorded and never read."""
-    c, cu, args, kw = _attn(ra, [1, 2], [30, 40], [20], [0, 2], 16, 4, 2, 128, "nhd", "bf16", True, 0)
+    c, cu, args, kw = _attn(ra, [1, 2], [30, 40], [20], [0, 2], 16, 4, 2, 128, "nhd", "bf16", True, 0, roomy=False)
     q, kc, vc, own, cud, lens = args
     bad = [dict(cu=[0, 5, 3]), dict(cu=[0, 1, 4]), dict(cu=[-1, 1, 3]), dict(lens=[30, 49]), dict(lens=[-1, 40]),
            dict(plens=[49]), dict(plens=[-1]), dict(groups=[0, 3]), dict(groups=[2, 0]), dict(groups=[-1, 2])]
@@ -421,7 +429,7 @@ def test_prefill_with_the_ring_then_decode_from_the_cache(ra):
     ring, rlse = ra.ring_attn_fwd(qr, kr, v.contiguous(), cu, 4, ra.RA_ZZ_PER_DOC)
 
     c = Cache(tails + [common], page, hkv, d, "bf16", fill=False)
-    own, pre = dev(c.tables[:-1]), dev(c.tables[-1:])
+    own, pre = dev(roomy_table(c.tables[:-1], page)), dev(roomy_table(c.tables[-1:], page))
     ra.kv_cache_append(k[:common], v[:common], c.k, c.v, pre, dev([0, common]), dev([common]), pos=dev(pos[:common]),
                        inv_freq=freq)
     rows = np.concatenate([np.arange(cu[b] + common, cu[b + 1]) for b in range(len(docs))])
@@ -490,8 +498,9 @@ MORE = [  # as ATTN, and the hint
 
 
 @pytest.mark.parametrize("new,lens,plens,groups,page,hq,hkv,d,layout,dtype,causal,pad,most", MORE)
-def test_paged_attention_shapes(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, most):
-    c, cu, args, kw = _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad)
+@pytest.mark.parametrize("roomy", [True, False])
+def test_paged_attention_shapes(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, most, roomy):
+    c, cu, args, kw = _attn(ra, new, lens, plens, groups, page, hq, hkv, d, layout, dtype, causal, pad, roomy=roomy)
     kw["max_q_len"] = most
     q, S = args[0], len(lens)
     out, lse = torch.full_like(q, 3.0), torch.full((hq, q.shape[0]), 3.0, device="cuda")
@@ -508,7 +517,8 @@ def test_paged_attention_shapes(ra, new, lens, plens, groups, page, hq, hkv, d, 
 def test_many_sequences_are_checked(ra):
     """The index arrays of more sequences than a block plans for itself."""
     S = 700
-    c, cu, args, kw = _attn(ra, [1] * S, [1 + i % 30 for i in range(S)], [20], [0, S], 16, 4, 2, 64, "nhd", "bf16", True, 0)
+    c, cu, args, kw = _attn(ra, [1] * S, [1 + i % 30 for i in range(S)], [20], [0, S], 16, 4, 2, 64, "nhd", "bf16", True,
+                            0, roomy=False)
     q, kc, vc, own, cud, lens = args
     for at, value in ((0, -1), (511, 33), (512, -2), (699, 2**31 - 1)):
         bad = lens.clone()
@@ -532,10 +542,11 @@ def test_cache_without_pages(ra):
 
 @pytest.mark.parametrize("dtype,hq,hkv,new", [("bf16", 8, 2, 1), ("bf16", 24, 2, 2), ("bf16", 16, 1, 4), ("bf16", 8, 2, 40),
                                               ("fp32", 8, 2, 3)])
-def test_nan_reaches_the_rows_that_meet_it_and_no_others(ra, dtype, hq, hkv, new):
+@pytest.mark.parametrize("roomy", [True, False])
+def test_nan_reaches_the_rows_that_meet_it_and_no_others(ra, dtype, hq, hkv, new, roomy):
     """A NaN query makes its own rows NaN (output and lse); a NaN key those that see it.  The rest keep their bits."""
     S, d = 3, 128
-    c, cu, args, kw = _attn(ra, [new] * S, [200, 90, 130], [150], [0, S], 16, hq, hkv, d, "nhd", dtype, True, 0)
+    c, cu, args, kw = _attn(ra, [new] * S, [200, 90, 130], [150], [0, S], 16, hq, hkv, d, "nhd", dtype, True, 0, roomy=roomy)
     q, kc, vc, own, cud, lens = args
     good, glse = ra.paged_attn_fwd(*args, **kw)
     t, h, G = new, 1, hq // hkv                # the second sequence's first token
@@ -581,8 +592,9 @@ def test_cache_behind_32_bits_of_elements(ra):
         k = randn((sum(new), hkv, d), 10, "bf16")
         res = []
         for K, V, t in ((small.k, small.v, small.tables), (kc, vc, far)):
-            ra.kv_cache_append(k, k, K, V, dev(t[:4]), cu, dev(lens))
-            res.append(ra.paged_attn_fwd(q, K, V, dev(t[:4]), cu, dev(lens), prefix_table=dev(t[4:]), max_q_len=max(new), **kw))
+            own, pre = dev(roomy_table(t[:4], page)), dev(roomy_table(t[4:], page))
+            ra.kv_cache_append(k, k, K, V, own, cu, dev(lens))
+            res.append(ra.paged_attn_fwd(q, K, V, own, cu, dev(lens), prefix_table=pre, max_q_len=max(new), **kw))
         assert ra.device_status() == 0
         assert torch.equal(kc[at].view(torch.int16), small.k.view(torch.int16))
         assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
