@@ -6,8 +6,8 @@
 // Mathematics: pair i of token t turns by phi = pos[axis_i][t] * f_i.  The
 // table holds f_i / (2 pi) as a 64-bit fraction of a turn, so pos * turns
 // modulo 2^64 is the angle modulo a full turn, without any rounding that grows with the
-// position, in one 64-bit integer product; its upper 32 bits, as a signed
-// fraction of half a turn, go through sincospif.
+// position, in one 64-bit integer product; its distance to the nearest quarter
+// turn goes through sincospif.
 //
 // Bound: memory.  Per token (Hq + Hk) * d elements are read and written; the
 // n_pairs sines and cosines are computed once per token into shared memory
@@ -91,6 +91,22 @@ __device__ __forceinline__ void turn_unit(typename Pack<T, VEC>::V &a, typename 
     a = repack<T, VEC>(fa);
 }
 
+// Cosine and sine of pos * turns / 2^64 of a turn.  The upper two bits of the
+// angle, rounded, are its quarter; what is left of it, an eighth of a turn at
+// most either way, becomes a float of 2^-33 half turns (that of a whole angle
+// would be off by 2^-25 half turns, four times as much).
+__device__ __forceinline__ float2 angle(int pos, unsigned long long turns, int inverse) {
+    const unsigned long long turn = (unsigned long long)(long long)pos * turns;
+    const unsigned hi = (unsigned)(turn >> 32), quarter = (hi + 0x20000000u) >> 30;
+    const int rest = (int)__funnelshift_l((unsigned)turn, hi, 2);
+    float s, c;
+    sincospif((float)rest * 1.1641532182693481e-10f, &s, &c);
+    const bool odd = quarter & 1;
+    // (quarters 1 and 2 negate the cosine, 2 and 3 the sine, the gradient the sine once more)
+    return make_float2(__uint_as_float(__float_as_uint(odd ? s : c) ^ ((quarter + 1) & 2) << 30),
+                       __uint_as_float(__float_as_uint(odd ? c : s) ^ ((quarter ^ (unsigned)inverse << 1) & 2) << 30));
+}
+
 __device__ __forceinline__ int page_of(const RopeParams &p, int key) {
     return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
 }
@@ -152,11 +168,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
             const int w = lane + 32 * k;
             if (w < p.n_pairs) {
                 const int at = k == 0 ? pos[0] : k == 1 ? pos[1] : k == 2 ? pos[2] : pos[3];
-                const unsigned long long turn = (unsigned long long)(long long)at * p.turns[w];
-                // the upper half as a signed number of 2^-31 half turns
-                float s, c;
-                sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
-                cs[w] = make_float2(c, p.inverse ? -s : s);
+                cs[w] = angle(at, p.turns[w], p.inverse);
             }
         }
         __syncwarp();
@@ -336,6 +348,9 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
         dev::bulk_wait_read<1>();
         __syncwarp();
         if (lane == 0 && ld.i < items) load();
+        // (the wait ahead of the angles, which paces the warps: 32768 tokens of 40 heads 105.4 us, behind them 109.6; 8192
+        // of 72 heads 53.9 and 53.4, packed prefill appended 194.4 and 193.1)
+        if (!dev::mbar_wait_warp(&full[warp][it.st], it.use, wc)) break;
         if (it.part == 0) {
             if (p.cu) {
                 if (t >= c1) {
@@ -370,10 +385,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
             for (int k = 0; k < 4; ++k) {
                 const int w = lane + 32 * k;
                 if (w < p.n_pairs) {
-                    const unsigned long long turn = (unsigned long long)(long long)pos[k] * turns[k];
-                    float s, c;
-                    sincospif((float)(int)(turn >> 32) * 4.6566128730773926e-10f, &s, &c);
-                    cs[w] = make_float2(c, p.inverse ? -s : s);
+                    cs[w] = angle(pos[k], turns[k], p.inverse);
                     if (t + TS < t1) pos[k] = __ldg(pos_at[k] + t + TS);
                 }
             }
@@ -387,7 +399,6 @@ __global__ void __launch_bounds__(kBulkWarps * 32) rope_bulk_kernel(const __grid
                 }
             }
         }
-        if (!dev::mbar_wait_warp(&full[warp][it.st], it.use, wc)) break;
         int ha, hb;
         share(it.part, ha, hb);
         uint8_t *tok = ring + it.st * p.stage_bytes;

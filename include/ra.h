@@ -361,7 +361,9 @@ ra_status ra_ring_attn_bwd_masked(const void *q, const void *k, const void *v, i
  * Several axes (time, height, width) give each pair the coordinate that
  * axes[i] names.  The angle is reduced exactly: inv_freq / (2 pi) is kept as
  * a 64-bit binary fraction of a turn, so positions over the whole int32 range
- * keep an angle as exact as a 64-bit product.
+ * keep an angle as exact as a 64-bit product.  Its distance to the nearest
+ * quarter turn is rounded to fp32 (2.4e-8 rad at most) ahead of the sine and
+ * cosine, which are exact to one unit in the last place.
  *   q  DEVICE [T, Hq, d], k DEVICE [T, Hk, d] (k and k_out NULL: queries only);
  *      rows of H*d contiguous elements, q_stride / k_stride elements apart
  *      (a slice of a packed QKV projection); the same for the outputs.  An
