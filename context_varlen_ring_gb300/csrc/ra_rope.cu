@@ -479,9 +479,11 @@ void rope_table(RopeParams &p, const double *inv_freq, const uint8_t *axes, int 
     p.adjacent = adjacent ? 1 : 0;
     p.inverse = inverse;
     for (int i = 0; i < n_pairs; ++i) {
-        const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-        const double frac = turns - std::floor(turns);              // in [0, 1]
-        p.turns[i] = frac >= 1.0 ? 0ull : (uint64_t)(frac * 18446744073709551616.0);  // (exact: times 2^64)
+        // (of the magnitude, negated at the end: what a negative one lacks to a whole turn would lose its low bits)
+        const double turns = std::fabs(inv_freq[i]) * 0.15915494309189533577;            // 1 / (2 pi)
+        const double frac = turns - std::floor(turns);                                   // in [0, 1), exact
+        const uint64_t part = (uint64_t)(frac * 18446744073709551616.0);                 // (exact: times 2^64)
+        p.turns[i] = inv_freq[i] < 0 ? 0 - part : part;
         p.axis[i] = axes ? axes[i] : 0;
     }
 }
