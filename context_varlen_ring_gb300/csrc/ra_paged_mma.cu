@@ -130,9 +130,15 @@ struct Rows {
 };
 
 // One block of 16 keys for 16 rows: S = Q K^T, the running maximum, P in
-// bf16 (rounded once: the products' inputs; the sums use the unrounded
-// values), O += P V.
-template <int D>
+// bf16, O += P V.  The sums use the unrounded values.  With WHOLE_P P is two
+// bf16 parts, a product each (2^-15 of P is lost, not 2^-8): single tokens are
+// bound by memory and the results lose nothing beside their own rounding (64
+// ragged requests: error against 64 bits 0.0021 -> 0.0017, 77.8 -> 78.3 us;
+// one request of 8192 keys 14.0 -> 14.6 us).  With shared key tiles (17 rows
+// and more) P is rounded, as in the tcgen05 kernel and the packed ring: there
+// the products show (drafts' own keys, 43.9 -> 46.4 us).
+constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+template <int D, bool WHOLE_P>
 __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, int kb, bool masked, float scale_log2) {
     const int lane = threadIdx.x & 31, id = lane >> 3, l8 = lane & 7;
     float s[2][4] = {};
@@ -173,7 +179,7 @@ __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, in
             }
         }
     }
-    uint32_t p[4];
+    uint32_t p[4], rest[4] = {};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const float use = w.m[r] == -INFINITY ? 0.f : w.m[r];
@@ -181,7 +187,15 @@ __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, in
         for (int n = 0; n < 2; ++n) {
             const float p0 = ex2_approx(s[n][2 * r] - use), p1 = ex2_approx(s[n][2 * r + 1] - use);
             w.l[r] += p0 + p1;
-            p[2 * n + r] = pack_bf16x2(p0, p1);
+            if (!WHOLE_P) {
+                p[2 * n + r] = pack_bf16x2(p0, p1);
+            } else {
+                // the upper halves, and what they cut off: never below zero, so that an infinite value stays one
+                const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                p[2 * n + r] = __byte_perm(u0, u1, 0x7632);
+                rest[2 * n + r] = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kLeast),
+                                              fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kLeast));
+            }
         }
     }
     const uint32_t va = chunk_at<D>(vs, (id & 1) * 8 + l8, id >> 1);
@@ -191,6 +205,10 @@ __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, in
         ldsm4t(va ^ (n << 5), b);
         mma16816(w.o[2 * n], p, b[0], b[1]);
         mma16816(w.o[2 * n + 1], p, b[2], b[3]);
+        if (WHOLE_P) {
+            mma16816(w.o[2 * n], rest, b[0], b[1]);
+            mma16816(w.o[2 * n + 1], rest, b[2], b[3]);
+        }
     }
 }
 
@@ -313,7 +331,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 #pragma unroll 1
             for (int b = warp % KW * (kWarps / KW), e = b + kWarps / KW; b < e; ++b) {
                 const int kb = t * kKT + b * 16;
-                if (kb < hi) block16<D>(w, st + b * kBlk, st + (kWarps + b) * kBlk, kb, kb + 16 > lo, a.scale_log2);
+                if (kb < hi)
+                    block16<D, ROWS == 16>(w, st + b * kBlk, st + (kWarps + b) * kBlk, kb, kb + 16 > lo, a.scale_log2);
             }
             sync_tile();  // the stage may be filled again
         }

@@ -456,6 +456,10 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  *      every byte read from it is written by the same call first.  Calls in
  *      flight at the same time, and captured graphs that may run so, need
  *      workspaces of their own.
+ * Scores, softmax statistics and sums are fp32.  In bf16 with d 64 or 128 and
+ * more than 16 query rows a KV head (max_q_len, or T where it is not known and
+ * for prefixes, times Hq / Hkv) the weights are rounded to bf16 ahead of their
+ * product with V, as in ra_ring_attn_fwd; else they keep 15 bits or more.
  * A row without any visible key has output 0 and lse -inf.  Rows at or behind
  * cu_seqlens_q[B] (a padded batch) are not written.  Cache rows at or behind
  * a sequence's length may hold anything (NaN included); a key that some

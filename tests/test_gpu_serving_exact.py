@@ -1,9 +1,12 @@
-"""How exact the positions' sines and cosines are, seen by themselves."""
+"""How exact the positions' sines and cosines are, seen by themselves, and the weights of paged attention."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_serving import dev, ra  # noqa: F401  (ra: the module's fixture)
+import serving_ref as R
+from test_gpu_serving import _attn, dev, ra  # noqa: F401  (ra: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +48,39 @@ def test_angles_of_negative_frequencies(ra):  # noqa: F811
         c, s = sines(ra, pos, freq, fn)
         close(c, np.cos(angle), angle)
         close(s, sign * np.sin(angle), angle)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,layout,plens,groups", [
+    (8, 2, 128, 16, "nhd", [], [0]), (16, 1, 64, 32, "hnd", [], [0]), (14, 2, 64, 5, "both", [], [0]),
+    # (a prefix counts the rows of all tokens: 7 and 14)
+    (5, 5, 128, 7, "nhd", [3, 90], [0, 1, 3]), (4, 2, 64, 16, "hnd", [3, 90], [0, 4, 6])])
+def test_single_tokens_keep_the_weights(ra, hq, hkv, d, page, layout, plens, groups):  # noqa: F811
+    """Up to 16 query rows a KV head the weights reach their product with V in two bf16 parts: the first is cut off, by
+    2^-7 of the weight at most, and the second rounded, by 2^-8 of that.  Few keys, so that a rounded weight would show."""
+    lens = [2, 5, 300, 3, 17, 0, 33]
+    c, cu, args, kw = _attn(ra, [1] * 7, lens, plens, groups, page, hq, hkv, d, layout, "bf16", True, 0)
+    out, lse = ra.paged_attn_fwd(*args, out_dtype=torch.float32, **kw)
+    q, kc, vc = (R.f64(t) for t in args[:3])
+    ref = (c.tables[:7], cu, lens, c.tables[7:], plens, groups, True, 1 / math.sqrt(d), "bf16", False, False)
+    want, bound, wl, lb, _ = R.paged_attn(q, kc, vc, *ref)
+    size = R.paged_attn(q, kc, np.abs(vc), *ref)[0]  # sum of weights times |v|
+    R.check(R.f64(out), want, bound + size * 2.0 ** -15)
+    R.check(R.f64(lse), wl, lb)
+
+
+@pytest.mark.parametrize("hq", [8, 40])  # 4 and 20 rows: weights in two parts, and rounded
+def test_infinite_values_stay_infinite(ra, hq):  # noqa: F811
+    """Infinities in V, each in a column of its own, reach the outputs that see them with their sign; the rest keeps its
+    bits.  (Every weight is far from zero.)"""
+    lens = [1, 40, 300]
+    c, cu, args, kw = _attn(ra, [1] * 3, lens, [], [0], 16, hq, 2, 128, "nhd", "bf16", True, 0)
+    args = (args[0] * 0.1,) + args[1:]
+    good, _ = ra.paged_attn_fwd(*args, **kw)
+    for b, n in enumerate(lens):
+        for h, (col, value) in enumerate(((5, math.inf), (77, -math.inf))):
+            args[2][int(c.tables[b][(n - 1) // 16]), (n - 1) % 16, h, col] = value
+    out, _ = ra.paged_attn_fwd(*args, **kw)
+    G = hq // 2
+    assert (out[:, :G, 5] == math.inf).all() and (out[:, G:, 77] == -math.inf).all()
+    out[:, :G, 5], out[:, G:, 77] = good[:, :G, 5], good[:, G:, 77]
+    assert torch.equal(out, good)
