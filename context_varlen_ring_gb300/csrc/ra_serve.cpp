@@ -136,7 +136,8 @@ PagedLayout paged_layout(int64_t T, int B, int n_groups, int G, int Hkv, int d, 
 
 ra_status check_paged_shape(int64_t T, int B, int n_groups, int Hq, int Hkv, int d, int dtype) {
     if (dtype != RA_BF16 && dtype != RA_FP32) return fail(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
-    if (T < 0 || B < 1 || n_groups < 0) return fail(RA_ERR_INVALID_ARG, "T and n_groups must be >= 0, B >= 1");
+    if (T < 0 || n_groups < 0 || B < 0 || (B == 0 && T > 0))
+        return fail(RA_ERR_INVALID_ARG, "T and n_groups must be >= 0, B >= 1 (0 with T = 0: an empty batch)");
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return fail(RA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hkv");
     if (d <= 0) return fail(RA_ERR_INVALID_ARG, "d must be positive");
     if (d % 32 != 0 || d > 256) return fail(RA_ERR_UNSUPPORTED, "d must be a multiple of 32 and <= 256");
@@ -175,8 +176,8 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
     ra_status st = check_cache(cache);
     if (st) return st;
     if ((st = check_rows(cache->dtype, T, cache->d))) return st;
-    if (B < 1 || table_width < 0 || table_width > INT32_MAX)
-        return fail(RA_ERR_INVALID_ARG, "B must be >= 1 and table_width in [0, 2^31)");
+    if (B < 0 || (B == 0 && T > 0) || table_width < 0 || table_width > INT32_MAX)
+        return fail(RA_ERR_INVALID_ARG, "B must be >= 1 (0 with T = 0: an empty batch) and table_width in [0, 2^31)");
     if ((q == nullptr) != (q_out == nullptr)) return fail(RA_ERR_INVALID_ARG, "q and q_out go together");
     if (q && !rope) return fail(RA_ERR_INVALID_ARG, "queries are taken along to be rotated: q without rope");
     if (T == 0) return RA_OK;

@@ -421,6 +421,7 @@ typedef struct ra_paged_kv {
  * name the same cache row (distinct sequences' tables must not share the pages
  * that they append to); which of them a row then holds is not defined, vector
  * by vector.  Capturable; lengths and tables may change between replays.
+ * An empty batch (T = 0, also with B = 0) does nothing.
  * Limits on d, dtype and n_pairs as in ra_rope_fwd.
  * ------------------------------------------------------------------------ */
 ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int64_t T,
@@ -460,6 +461,7 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  * more than 16 query rows a KV head (max_q_len, or T where it is not known and
  * for prefixes, times Hq / Hkv) the weights are rounded to bf16 ahead of their
  * product with V, as in ra_ring_attn_fwd; else they keep 15 bits or more.
+ * An empty batch (T = 0, also with B = 0) does nothing.
  * A row without any visible key has output 0 and lse -inf.  Rows at or behind
  * cu_seqlens_q[B] (a padded batch) are not written.  Cache rows at or behind
  * a sequence's length may hold anything (NaN included); a key that some

@@ -84,3 +84,14 @@ def test_infinite_values_stay_infinite(ra, hq):  # noqa: F811
     assert (out[:, :G, 5] == math.inf).all() and (out[:, G:, 77] == -math.inf).all()
     out[:, :G, 5], out[:, G:, 77] = good[:, :G, 5], good[:, G:, 77]
     assert torch.equal(out, good)
+
+
+def test_an_empty_batch(ra):  # noqa: F811
+    """No sequences and no tokens: empty results, the cache untouched."""
+    kc = torch.ones((3, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    vc, e = kc.clone(), torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    none, cu, table = dev(np.zeros(0)), dev([0]), dev(np.zeros((0, 4)))
+    got = ra.kv_cache_append(e, e, kc, vc, table, cu, none, q=e, pos=none, inv_freq=ra.rope_inv_freq(64))
+    out, lse = ra.paged_attn_fwd(e, kc, vc, table, cu, none, max_q_len=1)
+    assert got.shape == e.shape and out.shape == e.shape and lse.shape == (2, 0)
+    assert (kc == 1).all() and (vc == 1).all() and ra.device_status() == 0
