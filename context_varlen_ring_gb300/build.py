@@ -35,8 +35,9 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _module_job(extra=()):
-    """(object file, compile command, link command) of the Python module, for the installed torch."""
+def _module_job():
+    """(object file, compile command, link command, libraries) of the Python module, for the installed torch; each
+    command wants its output's name next."""
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
@@ -45,11 +46,27 @@ def _module_job(extra=()):
            sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
-    cmd += [x for i in inc for x in ("-isystem", i)] + list(extra) + ["-c", MODULE_SRC, "-o", obj]
+    cmd += [x for i in inc for x in ("-isystem", i)] + ["-c", MODULE_SRC, "-o"]
     lib = os.path.join(root, "lib")
     link = ["-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libra.so",
             "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
     return obj, cmd, ["g++", "-shared", obj, "-o"], link
+
+
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+
+
+def _compile_module(force, headers):
+    """Compiles the binding where it is stale; its object file, and the link command with its libraries."""
+    obj, cmd, link, libs = _module_job()
+    if force or _stale(obj, [MODULE_SRC, __file__] + headers):
+        tmp = obj + f".tmp{os.getpid()}"
+        _run(cmd + [tmp])
+        os.replace(tmp, obj)
+    return obj, link, libs
 
 
 def _stale(out: str, deps) -> bool:
@@ -60,6 +77,8 @@ def _stale(out: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Builds the library, which needs nvcc alone, and the torch binding.  A binding that cannot be built is reported
+    and left out: the serving calls of Python then raise, all else works."""
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(HERE, "..", "include", "ra.h"))
@@ -75,16 +94,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             if s.endswith(".cpp"):
                 cmd = [nvcc(), "-x", "c++"] + COMMON + list(extra) + ["-c", src, "-o", obj]
             jobs.append(cmd)
-    mod_obj, mod_cmd, mod_link, mod_libs = _module_job()
-    if force or _stale(mod_obj, [MODULE_SRC, __file__] + headers):
-        jobs.insert(0, mod_cmd)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
     failed = []
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        module = ex.submit(_compile_module, force, headers)
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
@@ -100,14 +117,16 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
-    if force or _stale(MODULE, [mod_obj, LIB]):
-        tmp = MODULE + f".tmp{os.getpid()}"
-        cmd = mod_link + [tmp] + mod_libs
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            raise RuntimeError("link failed")
-        os.replace(tmp, MODULE)
+    try:
+        obj, link, libs = module.result()
+        if force or _stale(MODULE, [obj, LIB]):
+            tmp = MODULE + f".tmp{os.getpid()}"
+            _run(link + [tmp] + libs)
+            os.replace(tmp, MODULE)
+    except Exception as e:  # (torch missing, its headers, g++, or a torch that the binding does not fit)
+        if os.path.exists(MODULE):
+            os.remove(MODULE)  # it is older than the library
+        sys.stderr.write(f"{LIB} is built; the torch binding of the serving calls is not: {e}\n")
     return LIB
 
 

@@ -21,7 +21,7 @@ _mod = None
 
 
 def _native():
-    """The compiled binding; raises if it was not built."""
+    """The compiled binding; raises if it was not built (where its build failed, the library stands without it)."""
     global _mod
     if _mod is None:
         lib()  # libra.so first: the binding calls into it
