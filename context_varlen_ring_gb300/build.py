@@ -1,5 +1,6 @@
 """Builds libra.so (the C-ABI library) in-tree for sm_103a with nvcc, and
-the Python module _serving (the torch binding of the serving calls) with g++.
+the Python module _serving (the torch binding of the serving calls, a file for
+each torch and Python ABI) with g++.
 
 Each translation unit compiles in parallel into _build/, then one link
 step writes context_varlen_ring_gb300/libra.so, and one the module, which
@@ -21,11 +22,21 @@ LIB = os.path.join(HERE, "libra.so")
 SOURCES = ["ra_api.cpp", "ra_plan.cpp", "ra_stats.cpp", "ra_misc.cu", "ra_simt.cu", "ra_tc_fwd.cu", "ra_tc_bwd.cu",
            "ra_tc_dq.cu", "ra_noalloc.cu", "ra_tile_build.cu", "ra_rope.cu", "ra_paged.cu", "ra_paged_mma.cu",
            "ra_paged_tc.cu", "ra_serve.cpp"]
-MODULE = os.path.join(HERE, "_serving.so")
 MODULE_SRC = os.path.join(CSRC, "py_serving.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I" + os.path.join(HERE, "..", "include")]
+
+
+def environment() -> str:
+    """The installed torch and Python ABI, which the binding is compiled for."""
+    import torch
+    return f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}"
+
+
+def module_path() -> str:
+    """The binding of this environment: a file for each, so that none loads (or takes for new) another's."""
+    return os.path.join(HERE, f"_serving-{environment()}.so")
 
 
 def nvcc() -> str:
@@ -41,7 +52,7 @@ def _module_job():
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    obj = os.path.join(BUILD, f"py_serving-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.o")
+    obj = os.path.join(BUILD, f"py_serving-{environment()}.o")
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
            sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
@@ -117,15 +128,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    out = None
     try:
+        out = module_path()
         obj, link, libs = module.result()
-        if force or _stale(MODULE, [obj, LIB]):
-            tmp = MODULE + f".tmp{os.getpid()}"
+        if force or _stale(out, [obj, LIB]):
+            tmp = out + f".tmp{os.getpid()}"
             _run(link + [tmp] + libs)
-            os.replace(tmp, MODULE)
+            os.replace(tmp, out)
     except Exception as e:  # (torch missing, its headers, g++, or a torch that the binding does not fit)
-        if os.path.exists(MODULE):
-            os.remove(MODULE)  # it is older than the library
+        if out and os.path.exists(out):
+            os.remove(out)  # it is older than the library
         sys.stderr.write(f"{LIB} is built; the torch binding of the serving calls is not: {e}\n")
     return LIB
 

@@ -9,6 +9,9 @@ the calls into include/ra.h are in csrc/py_serving.cpp.
 """
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import numpy as np
 import torch
 
@@ -25,8 +28,14 @@ def _native():
     global _mod
     if _mod is None:
         lib()  # libra.so first: the binding calls into it
-        from . import _serving
-        _mod = _serving
+        from .build import module_path
+        path = module_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built: python -m context_varlen_ring_gb300.build")
+        spec = importlib.util.spec_from_file_location(__package__ + "._serving", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _mod = mod
     return _mod
 
 
