@@ -454,7 +454,8 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  *      the tables' widths only choose the kernels (<= 0: not known), results
  *      hold for any n_b
  *   workspace DEVICE, 256-byte aligned, >= ra_paged_attn_workspace_bytes(...);
- *      every byte read from it is written by the same call first.  Calls in
+ *      what it holds ahead of the call does not change the results (bytes that
+ *      the call has not written may be read, and are dropped).  Calls in
  *      flight at the same time, and captured graphs that may run so, need
  *      workspaces of their own.
  * Scores, softmax statistics and sums are fp32.  In bf16 with d 64 or 128 and
@@ -473,7 +474,10 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  * recorded too, reads nothing, and leaves the rows that meet it unspecified.
  * A NaN in a query or in a key makes the rows that it reaches NaN, lse too.
  * Capturable; the arrays' contents may change between replays.  Deterministic:
- * the order of all sums is fixed by the lengths and the device.  d a multiple
+ * the same arguments on the same kind of device give the same bits.  Other
+ * lengths, table widths, max_q_len, page sizes, strides or signs of the scale
+ * may be other kernels and another order of the sums, so the same keys behind a
+ * wider table can differ by rounding.  d a multiple
  * of 32, d <= 256; q, out and the cache 16-byte aligned with strides of whole
  * 16 bytes; T * Hq <= 2^30.  out may be q.
  * ------------------------------------------------------------------------ */
