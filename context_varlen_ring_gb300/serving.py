@@ -4,8 +4,8 @@ What stands before and after the packed attention in a model: `rope_fwd` /
 `rope_bwd` turn queries and keys (and their gradients) ahead of and behind
 `ring_attn_fwd` / `ring_attn_bwd`; `kv_cache_append` writes new keys and values
 into a paged cache, rotated on the way; `paged_attn_fwd` attends over that
-cache, reading a prefix that a batch shares once for all of it.  The checks and
-the calls into include/ra.h are in csrc/py_serving.cpp.
+cache, reading a prefix that a batch shares for all of it together.  The checks
+and the calls into include/ra.h are in csrc/py_serving.cpp.
 """
 from __future__ import annotations
 
@@ -101,8 +101,9 @@ def paged_attn_fwd(q, k_cache, v_cache, page_table, cu_seqlens_q, kv_lens, prefi
     of its kv_lens[b] cached ones; each sees its sequence's keys up to itself
     (all of them when not causal) and the whole prefix of its group: sequences
     prefix_groups[g] .. prefix_groups[g+1] - 1 share prefix_lens[g] tokens in
-    the pages prefix_table[g], whose keys are read once for all of them.  All
-    index arrays int32 on the device; capturable.  max_q_len: the most query
+    the pages prefix_table[g], whose keys are read once for every 256 query rows
+    of a KV head, or 64 (include/ra.h says which shapes).  All index arrays
+    int32 on the device; capturable.  max_q_len: the most query
     tokens a sequence is expected to have (a hint that chooses the kernels).
     scale: 1 / sqrt(d) unless given.  out_dtype torch.float32 makes (out, lse)
     a partial for lse_merge.  Rows behind cu_seqlens_q[-1] are not written."""

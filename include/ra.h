@@ -434,7 +434,12 @@ ra_status ra_kv_cache_append(const void *k, const void *v, int64_t k_stride, int
  * ra_paged_attn_fwd  (DEVICE tensors and DEVICE segment arrays)
  *
  * Attention of a batch's new tokens over a paged cache, where sequences may
- * share a prefix whose keys are read once for all of them.  Sequence b has
+ * share a prefix whose keys are read for all of them together: once for every
+ * 256 query rows (tokens of the group times Hq / Hkv) in bf16 with d 128,
+ * Hq / Hkv a power of two up to 128, pages of 8, 16, 32, 64 or a multiple of 128
+ * tokens, a positive scale and keys enough (see max_q_len); once for every 64
+ * rows in other shapes of bf16 with d 64 or 128; once for every 64, of few keys
+ * 16, in fp32 and with other d, in fp32 arithmetic.  Sequence b has
  * n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] query tokens, the last n_b of its
  * kv_lens[b] cached tokens.  Token j sees
  *   - the whole prefix of its sequence's group, and
