@@ -309,32 +309,6 @@ cudaError_t simt_by_d(int d, const PagedArgs *a, int fi, int late, int *ctas, cu
 }
 
 // ------------------------------------------------------------------ join
-// The partials of a token and query head in a family: cnt of them, the i-th
-// (of CTA c0 + (i >> two)) at partial row  at + (i >> two) * rt + (i & two) * second.
-struct Parts {
-    long long at, x;  // x: the unit's place in the line
-    int cnt, two, second, c0, all;
-    PagedCost cost;
-};
-
-__device__ __forceinline__ Parts find_parts(const PagedArgs &a, const PagedFamily &f, const PagedSeg &sg, long long per,
-                                            int64_t t, int h, int g) {
-    Parts p{};
-    if (sg.w == 0) return p;
-    const int r = (int)(t - sg.tok0) * a.G + g, rtile = r >> f.rt_log;
-    const int rows = min(f.rt, sg.n * a.G - rtile * f.rt), alloc = paged_alloc(f, rows);
-    p.cost = paged_cost(a, f, sg);
-    p.all = paged_all(sg, p.cost);
-    p.x = sg.W0 + (long long)(rtile * a.Hkv + h) * p.all;
-    const int c1 = (int)paged_div(p.x + p.all - 1, per);
-    p.c0 = (int)paged_div(p.x, per);
-    p.at = sg.R0 + (long long)rtile * f.rt * a.Hkv + (long long)h * alloc + (long long)p.c0 * f.rt + (r & (f.rt - 1));
-    p.two = alloc > rows ? 1 : 0;
-    p.second = rows;
-    p.cnt = (c1 - p.c0 + 1) << p.two;
-    return p;
-}
-
 // A block per (token, KV head, up to 8 of its query heads), 8 / HB warps a head:
 // the largest maximum M, the weights 2^(m - M), the weighted sums.  Own keys
 // come first, then the prefix; warps' sums are added in order, so the result
@@ -354,7 +328,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, HB == 1 ? 2 : 4)
     constexpr int WPR = kJoinWarps / HB;  // warps a head
     __shared__ float4 sum[kJoinWarps][32 * NV];
     __shared__ int seg[2];
-    __shared__ Parts parts[HB][2];
+    __shared__ PagedParts parts[HB][2];
     __shared__ PlanShared plan[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = (a.G + HB - 1) / HB;  // of a token and KV head
@@ -391,9 +365,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, HB == 1 ? 2 : 4)
     const bool fine = seg[0] >= 0 && per[0] && per[1];  // (an array that is not as it must be: nothing is written)
     if (fine && threadIdx.x < 2 * HB && g0 + (int)threadIdx.x / 2 < a.G) {
         const int i = threadIdx.x & 1;
-        parts[threadIdx.x / 2][i] = seg[i] < 0 ? Parts{}
-                                               : find_parts(a, a.f[i], plan[i].g, i ? per[1] : per[0], t, h,
-                                                            g0 + threadIdx.x / 2);
+        const PagedSeg &sg = plan[i].g;
+        parts[threadIdx.x / 2][i] = seg[i] < 0 ? PagedParts{}
+                                               : paged_parts(a, a.f[i], sg, i ? per[1] : per[0],
+                                                             (int)(t - sg.tok0) * a.G + g0 + (int)threadIdx.x / 2, h);
     }
     __syncthreads();
     const int sub = warp % WPR, g = g0 + warp / WPR, d4 = a.d / 4;
@@ -407,14 +382,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, HB == 1 ? 2 : 4)
         for (int u = 0; u < 2; ++u) {
             int i = i0 + 32 * u + lane;
             const int fi = i < own ? 0 : 1;
-            const Parts &p = parts[warp / WPR][fi];
-            if (fi) i -= own;
             ml[u] = nullptr;
             src[u] = nullptr;
-            const long long run = (p.c0 + (i >> p.two)) * (fi ? per[1] : per[0]) - p.x;  // its CTA's place in the unit
-            const int from = (int)max(0ll, run), to = (int)min((long long)p.all, run + (fi ? per[1] : per[0]));
-            if (i < p.cnt && paged_tile(from, p.cost) < paged_tile(to, p.cost)) {  // (else it began no tile of the unit)
-                const long long row = p.at + (long long)(i >> p.two) * a.f[fi].rt + (i & p.two) * p.second;
+            if (fi) i -= own;
+            const long long row = paged_part(a.f[fi], parts[warp / WPR][fi], fi ? per[1] : per[0], i);
+            if (row >= 0) {
                 ml[u] = reinterpret_cast<const float2 *>(a.f[fi].ml) + row;
                 src[u] = a.f[fi].acc + row * a.d;
             }

@@ -5,16 +5,11 @@
 #include <utility>
 
 #include "ra_kernels.h"
+#include "ra_paged_split.h"
 #include "ra_serve.cuh"
 
 namespace ra {
 namespace dev {
-
-// x / y of non-negative numbers, in 32 bits wherever they fit (a 64-bit
-// division is some hundred instructions).
-__device__ __forceinline__ long long paged_div(long long x, long long y) {
-    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
 
 // Query token of a row, row / G: exact for rows of 32 bits, by one product.
 __device__ __forceinline__ int paged_token(const PagedArgs &a, int row) {
@@ -24,18 +19,6 @@ __device__ __forceinline__ int paged_token(const PagedArgs &a, int row) {
 __device__ __forceinline__ int paged_page(const PagedArgs &a, int key) {
     return a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
 }
-
-// Partial rows of a tile of `rows` query rows.
-__device__ __forceinline__ int paged_alloc(const PagedFamily &f, int rows) {
-    return f.halves && 2 * rows <= f.rt ? 2 * rows : rows;
-}
-
-struct PagedUnit {
-    int s, tok0, n, len; // its segment
-    int r0, rows, h;     // first query row in the segment, query rows, KV head
-    int t0, t1;          // the CTA's key tiles in it
-    long long base;      // first partial row (of CTA 0)
-};
 
 // Segment s of a family from the call's arrays (W0 and R0 left to the plan);
 // false, and an empty one, where they are not as they must be.
@@ -54,46 +37,6 @@ __device__ __forceinline__ bool paged_record(const PagedArgs &a, const PagedFami
     g.W0 = g.R0 = 0;
     return fine;
 }
-// What a unit and its key tiles weigh, in sixteenths of a warp-level tile: a
-// unit takes its own cost (queries, join, partial) and then its tiles, so a run
-// that goes on into another unit has fewer tiles for it.  Of the tcgen05 kernel,
-// a tile for two row tiles takes 1.75 us, one of alternating tiles for a single
-// row tile 1.0 to 1.4 (bound by its softmax, or by memory), a unit about 4.
-struct PagedCost {
-    int tile, unit;
-};
-__device__ __forceinline__ PagedCost paged_cost(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return PagedCost{!f.halves ? 16 : g.n * a.G * 2 > f.rt ? 48 : 32, f.halves ? 96 : 32};
-}
-__device__ __forceinline__ int paged_all(const PagedSeg &g, const PagedCost &c) {  // (at most 2^24 tiles)
-    return g.w ? g.w * c.tile + c.unit : 0;
-}
-// The first tile of a unit that begins at or behind place `at` of it: a tile
-// belongs to the run in which it begins.
-__device__ __forceinline__ int paged_tile(int at, const PagedCost &c) {
-    const unsigned x = (unsigned)max(at - c.unit + c.tile - 1, 0) >> 4;
-    return (int)(c.tile == 48 ? x / 3 : c.tile == 32 ? x >> 1 : x);
-}
-// The weight of all its units, and its partial rows.  (n * G < 2^31.)
-__device__ __forceinline__ long long paged_tiles(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    return (long long)((g.n * a.G + f.rt - 1) >> f.rt_log) * a.Hkv * paged_all(g, paged_cost(a, f, g));
-}
-// The weight of a CTA's run.
-__device__ __forceinline__ long long paged_per(const PagedFamily &f, long long W) {
-    return max((long long)f.least, paged_div(W + f.n - 1, f.n));
-}
-__device__ __forceinline__ long long paged_rows(const PagedArgs &a, const PagedFamily &f, const PagedSeg &g) {
-    const int R = g.n * a.G, full = R & -f.rt;
-    return (long long)a.Hkv * (full + paged_alloc(f, R - full));
-}
-
-// A CTA's run of the line, and its place in it: the segment and the unit.
-struct PagedWalk {
-    long long x, x1;
-    int s;
-    PagedSeg g;
-};
-
 // The plan kernel's record of a segment.  Its results are read past L1, which
 // may hold an earlier call's.
 __device__ __forceinline__ PagedSeg paged_seg(const PagedFamily &f, int s) {
@@ -224,41 +167,18 @@ __device__ __forceinline__ PagedWalk paged_begin(const PagedArgs &a, const Paged
 }
 
 // The CTA's next unit and its tiles there; false where its run has no more.
-// Row tiles are outermost in a segment, so CTAs an equal share of the line
-// apart read the same keys for different rows at about the same time (from L2).
 __device__ __forceinline__ bool paged_unit(const PagedArgs &a, const PagedFamily &f, int fi, PagedWalk &k, PagedUnit &u) {
-    while (k.x < k.x1) {
-        for (long long end; (end = k.g.W0 + paged_tiles(a, f, k.g)) <= k.x;) {
-            ++k.s;
-            if (a.here) {
-                const long long rows = k.g.R0 + paged_rows(a, f, k.g);
-                paged_record(a, f, fi, k.s, k.g);
-                k.g.W0 = end;
-                k.g.R0 = rows;
-            } else {
-                k.g = paged_seg(f, k.s);
-            }
+    return paged_walk(a, f, k, u, [&](PagedWalk &w, long long end) {
+        ++w.s;
+        if (a.here) {
+            const long long rows = w.g.R0 + paged_rows(a, f, w.g);
+            paged_record(a, f, fi, w.s, w.g);
+            w.g.W0 = end;
+            w.g.R0 = rows;
+        } else {
+            w.g = paged_seg(f, w.s);
         }
-        const long long rel = k.x - k.g.W0;
-        const PagedCost cost = paged_cost(a, f, k.g);
-        const int all = paged_all(k.g, cost);
-        const int lu = (int)paged_div(rel, all), rtile = lu < a.Hkv ? 0 : lu / a.Hkv;
-        const int from = (int)(rel - (long long)lu * all), to = (int)min((long long)all, from + (k.x1 - k.x));
-        k.x += to - from;
-        u.t0 = paged_tile(from, cost);
-        u.t1 = paged_tile(to, cost);
-        if (u.t0 >= u.t1) continue;  // the run ends inside a tile that another one began
-        u.s = k.s;
-        u.tok0 = k.g.tok0;
-        u.n = k.g.n;
-        u.len = k.g.len;
-        u.h = lu - rtile * a.Hkv;
-        u.r0 = rtile << f.rt_log;
-        u.rows = min(f.rt, k.g.n * a.G - u.r0);
-        u.base = k.g.R0 + (long long)u.r0 * a.Hkv + (long long)u.h * paged_alloc(f, u.rows);
-        return true;
-    }
-    return false;
+    });
 }
 
 // Keys that row `row` of the segment sees: all of a prefix, the causal part

@@ -8,25 +8,20 @@
 #include <atomic>
 
 #include "ra_dev.cuh"
+#include "ra_paged_split.h"
 
 namespace ra {
 namespace dev {
 
 // How many of the n non-decreasing ends are <= t: the segment that holds t.
-// The whole warp searches, 32 probes a round (n <= 1024 in two rounds).  With
-// ends that decrease the result is still in [0, n].
+// The whole warp searches, 32 probes a round (n <= 1024 in two rounds).
 __device__ __forceinline__ int segment_of(const int32_t *ends, int n, int64_t t) {
     const int lane = threadIdx.x & 31;
-    int lo = 0;
-    while (n > 0) {
-        const int step = (n + 31) / 32;
+    return search32(n, [&](int lo, int step, int left) {
         const int q = (lane + 1) * step - 1;
-        const bool le = q < n && (int64_t)__ldg(ends + lo + q) <= t;
-        const int c = __popc(__ballot_sync(0xffffffffu, le));
-        lo += c * step;
-        n = min(step - 1, n - c * step);
-    }
-    return lo;
+        const bool le = q < left && (int64_t)__ldg(ends + lo + q) <= t;
+        return __popc(__ballot_sync(0xffffffffu, le));
+    });
 }
 
 // The L2 policy of data that is read once: it leaves first, so that what stays
