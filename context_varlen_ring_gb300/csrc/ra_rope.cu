@@ -10,8 +10,8 @@
 // turn goes through sincospif.
 //
 // Bound: memory.  Per token (Hq + Hk) * d elements are read and written; the
-// n_pairs sines and cosines are computed once per token into shared memory
-// and used by every head.
+// n_pairs sines and cosines are computed once per token, meet in shared memory,
+// and stay in registers for all heads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -524,7 +524,7 @@ cudaError_t launch_rope(RopeParams &p, int dtype, cudaStream_t st) {
         (p.T > kHeldWarps * sms || (!p.cu && p.T >= 4 * sms && p.T * groups > 144 * sms)))
         return dtype == RA_FP32 ? launch_bulk<float>(p, (int)sms, st) : launch_bulk<__nv_bfloat16>(p, (int)sms, st);
     // warps a token: enough to fill the GPU (16 warps an SM) when tokens are few, at most one per group of heads
-    p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, 152 * 16 / p.T));
+    p.split = (int)std::min<int64_t>(groups, std::max<int64_t>(1, sms * 16 / p.T));
     if (dtype == RA_FP32) {
         if (!fast) return launch_warps<float, 1, false>(p, st);
         return adj ? launch_warps<float, 4, true>(p, st) : launch_warps<float, 4, false>(p, st);
