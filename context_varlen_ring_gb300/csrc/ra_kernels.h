@@ -265,7 +265,7 @@ struct PagedFamily {
     int S, rt, kt, n;                  // segments, rows a unit, keys a tile, CTAs
     int rt_log, kt_log;                // (rows and keys are powers of two)
     int halves;                        // units of at most rt / 2 rows: two partials a row, of alternate key tiles
-    int least;                         // least weight a CTA (sixteenths of a tile): less costs more in partials than it gains
+    int least;                         // least weight a CTA (16ths of a tile): less costs more partials than it gains
     PagedHdr *hdr;
     PagedSeg *seg;                     // [S]
     int *start;                        // [n] the segment in which each CTA's run begins
