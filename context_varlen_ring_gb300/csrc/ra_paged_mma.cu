@@ -137,7 +137,7 @@ struct Rows {
 // one request of 8192 keys 14.0 -> 14.6 us).  With shared key tiles (17 rows
 // and more) P is rounded, as in the tcgen05 kernel and the packed ring: there
 // the products show (drafts' own keys, 43.9 -> 46.4 us).
-constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+constexpr float kLeast = 9.5367431640625e-7f;  // 2^-20
 template <int D, bool WHOLE_P>
 __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, int kb, bool masked, float scale_log2) {
     const int lane = threadIdx.x & 31, id = lane >> 3, l8 = lane & 7;
@@ -190,11 +190,12 @@ __device__ __forceinline__ void block16(Rows<D> &w, uint32_t ks, uint32_t vs, in
             if (!WHOLE_P) {
                 p[2 * n + r] = pack_bf16x2(p0, p1);
             } else {
-                // the upper halves, and what they cut off: never below zero, so that an infinite value stays one
+                // the upper halves, and what they cut off: 2^-20 of the weight at least, so that an infinite value stays
+                // one, and nothing of a weight of zero, so that the largest value behind a mask adds nothing
                 const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                 p[2 * n + r] = __byte_perm(u0, u1, 0x7632);
-                rest[2 * n + r] = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kLeast),
-                                              fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kLeast));
+                rest[2 * n + r] = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), p0 * kLeast),
+                                              fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), p1 * kLeast));
             }
         }
     }

@@ -86,6 +86,20 @@ def test_infinite_values_stay_infinite(ra, hq):  # noqa: F811
     assert torch.equal(out, good)
 
 
+@pytest.mark.parametrize("hq", [8, 24])  # 8 and 24 rows: weights in two parts, and rounded
+@pytest.mark.parametrize("value", [3e38, -3e38])
+def test_masked_values_add_nothing(ra, hq, value):  # noqa: F811
+    """The largest finite values of the keys that a token does not see leave its results as they are, bit for bit."""
+    lens = [2, 40, 300]
+    c, cu, args, kw = _attn(ra, [2] * 3, lens, [], [0], 16, hq, 2, 128, "nhd", "bf16", True, 0)
+    good, glse = ra.paged_attn_fwd(*args, **kw)
+    for b, n in enumerate(lens):
+        args[2][int(c.tables[b][(n - 1) // 16]), (n - 1) % 16] = value
+    out, lse = ra.paged_attn_fwd(*args, **kw)
+    first = [0, 2, 4]  # each sequence's last key is seen by its second token only
+    assert torch.equal(out[first], good[first]) and torch.equal(lse, glse)
+
+
 def test_an_empty_batch(ra):  # noqa: F811
     """No sequences and no tokens: empty results, the cache untouched."""
     kc = torch.ones((3, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
