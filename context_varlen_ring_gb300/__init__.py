@@ -22,6 +22,7 @@ __all__ = [
     "ring_attn_fwd", "ring_attn_bwd", "ring_rank_pairs", "ring_plan_stats", "device_status", "selftest_wait_timeout",
     "rope_inv_freq", "rope_axes", "rope_fwd", "rope_bwd", "kv_cache_append", "paged_attn_fwd",
     "paged_attn_workspace_bytes",
+    "delta_rule_fwd", "delta_rule_bwd", "delta_rule_step", "delta_rule_workspace_bytes",
     "RA_ZZ_GLOBAL", "RA_ZZ_PER_DOC", "RA_SCHED_FUSED", "RA_SCHED_STEPWISE", "RA_SCHED_ALLGATHER", "RaError",
 ]
 
@@ -335,5 +336,7 @@ def selftest_wait_timeout(budget_us: int = 1000):
           "ra_selftest_wait_timeout")
 
 
+from .delta import (delta_rule_bwd, delta_rule_fwd, delta_rule_step,  # noqa: E402
+                    delta_rule_workspace_bytes)
 from .serving import (kv_cache_append, paged_attn_fwd, paged_attn_workspace_bytes, rope_axes, rope_bwd,  # noqa: E402
                       rope_fwd, rope_inv_freq)

@@ -40,6 +40,7 @@ EXPORTS = (
     "ra_ring_workspace_bytes_masked", "ra_ring_attn_fwd_masked", "ra_ring_attn_bwd_masked",
     "ra_ring_plan_stats_masked", "ra_varlen_attn_partial_dev",
     "ra_rope_fwd", "ra_rope_bwd", "ra_kv_cache_append", "ra_paged_attn_workspace_bytes", "ra_paged_attn_fwd",
+    "ra_delta_rule_workspace_bytes", "ra_delta_rule_fwd", "ra_delta_rule_bwd", "ra_delta_rule_step",
 )
 
 
@@ -55,6 +56,16 @@ class PagedKV(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class Delta(ctypes.Structure):
+    """ra_delta of include/ra.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("T", ctypes.c_int64), ("N", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("Hv", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("n_slots", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -100,6 +111,10 @@ def _declare(L):
         "ra_paged_attn_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32]),
         "ra_paged_attn_fwd": (i32, [P, i64, i64, i32, P, P, i64, P, P, i32, P, i64, P, P, i32, i32, i32, f32,
                                     P, i32, P, P, sz, P]),
+        "ra_delta_rule_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32]),
+        "ra_delta_rule_fwd": (i32, [P, P, P, P, sz, P]),
+        "ra_delta_rule_bwd": (i32, [P, P, i64, P, P, P, P, P, P, P, P, sz, P]),
+        "ra_delta_rule_step": (i32, [P, P, P, P]),
         "ra_get_device_status": (i32, [P]),
         "ra_selftest_wait_timeout": (i32, [i64, P]),
         "ra_status_string": (ctypes.c_char_p, [i32]),

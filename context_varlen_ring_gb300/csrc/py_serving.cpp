@@ -1,6 +1,6 @@
 // py_serving.cpp -- the Python module `_serving`: argument checks, output
 // allocation and the calls into libra.so for rotary positions, the cache
-// append and paged attention.
+// append, paged attention and the gated delta rule.
 //
 // These calls are made once a layer and decoding step, where the kernels take
 // a few microseconds: the same checks in Python took 40 to 50 us a call on a
@@ -352,6 +352,195 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
     return pair(std::move(out), std::move(lse));
 }
 
+// The gated delta rule's inputs: q, k [T, Hk, dk], v [T, Hv, dv], g, beta fp32 [T, Hv].
+struct DeltaArg {
+    ra_delta c{};
+    int64_t dev;
+    const at::Tensor &q, &k, &v;
+    DeltaArg(PyObject *q_o, PyObject *k_o, PyObject *v_o, PyObject *g_o, PyObject *b_o, PyObject *scale_o)
+        : q(tensor(q_o, "q")), k(tensor(k_o, "k")), v(tensor(v_o, "v")) {
+        c.q_stride = rows(q, "q");
+        dev = q.get_device();
+        c.k_stride = rows(k, "k", &q);
+        c.v_stride = rows(v, "v", &q);
+        if (k.sizes() != q.sizes() || v.size(0) != q.size(0))
+            value_error("q and k must be [T, Hk, dk] and v [T, Hv, dv] of the same tokens");
+        c.T = q.size(0);
+        c.Hk = int_of(q.size(1), "q");
+        c.Hv = int_of(v.size(1), "v");
+        c.dk = int_of(q.size(2), "q");
+        c.dv = int_of(v.size(2), "v");
+        c.dtype = dtype_code(q);
+        c.q = q.data_ptr();
+        c.k = k.data_ptr();
+        c.v = v.data_ptr();
+        c.g = gate(g_o, "g");
+        c.beta = gate(b_o, "beta");
+        double scale = 1.0 / std::sqrt((double)c.dk);
+        if (scale_o != Py_None) {
+            scale = PyFloat_AsDouble(scale_o);
+            if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+        }
+        c.scale = (float)scale;
+    }
+    const float *gate(PyObject *o, const char *name) {
+        const at::Tensor &x = tensor(o, name);
+        if (x.scalar_type() != at::kFloat) raise(PyExc_TypeError, std::string(name) + " must be float32");
+        if (x.dim() != 2 || x.size(0) != c.T || x.size(1) != c.Hv || !x.is_contiguous() || !x.is_cuda() ||
+            x.get_device() != dev)
+            value_error(std::string(name) + " must be a contiguous [T, Hv] tensor on the device of q");
+        return static_cast<const float *>(x.data_ptr());
+    }
+    // fp32 [n, Hv, dk, dv] (n < 0: any number)
+    float *states(const at::Tensor &x, const char *name, int64_t n) {
+        if (x.scalar_type() != at::kFloat) raise(PyExc_TypeError, std::string(name) + " must be float32");
+        if (x.dim() != 4 || (n >= 0 && x.size(0) != n) || x.size(1) != c.Hv || x.size(2) != c.dk || x.size(3) != c.dv ||
+            !x.is_contiguous() || !x.is_cuda() || x.get_device() != dev)
+            value_error(std::string(name) + " must be a contiguous [states, Hv, dk, dv] tensor on the device of q");
+        return static_cast<float *>(x.data_ptr());
+    }
+    void segments(PyObject *cu_o) {
+        const at::Tensor &cu = tensor(cu_o, "cu_seqlens");
+        c.cu_seqlens = index(cu, "cu_seqlens", dev);
+        if (cu.dim() != 1 || cu.numel() < 1 || cu.numel() > INT32_MAX) value_error("cu_seqlens must be [N + 1]");
+        c.N = (int)cu.numel() - 1;
+    }
+    // slots [N], into a pool of n states
+    void places(PyObject *slots_o, int64_t n) {
+        c.n_slots = n;
+        if (slots_o == Py_None) {
+            if (n != c.N) value_error("without slots there must be one state for each sequence");
+            return;
+        }
+        const at::Tensor &s = tensor(slots_o, "slots");
+        c.slots = index(s, "slots", dev);
+        if (s.dim() != 1 || s.numel() != c.N) value_error("slots must be [N], one for each sequence");
+    }
+};
+
+at::Tensor scratch(PyObject *o, const DeltaArg &d, int bwd) {
+    if (o == Py_None) {
+        const size_t need = ra_delta_rule_workspace_bytes(d.c.T, d.c.N, d.c.Hk, d.c.Hv, d.c.dk, d.c.dv, d.c.dtype, bwd);
+        return fresh({(int64_t)std::max<size_t>(need, 256)}, at::kByte, d.q);
+    }
+    const at::Tensor &ws = tensor(o, "workspace");
+    if (!ws.is_contiguous() || !ws.is_cuda() || ws.get_device() != d.dev)
+        value_error("workspace must be a contiguous tensor on q's device");
+    return ws;
+}
+
+// (q, k, v, g, beta, cu_seqlens, state, slots, state_out, final_state, scale, out, workspace)
+PyObject *delta_fwd(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 13);
+    DeltaArg d(a[0], a[1], a[2], a[3], a[4], a[10]);
+    d.segments(a[5]);
+    const int want = PyObject_IsTrue(a[9]);
+    if (want < 0) throw Raised{};
+    On on(d.dev);
+    at::Tensor out, last;
+    int64_t pool = -1;
+    if (a[6] != Py_None) {
+        const at::Tensor &s = tensor(a[6], "state");
+        d.c.state = d.states(s, "state", -1);
+        pool = s.size(0);
+    }
+    if (a[8] != Py_None) {
+        last = tensor(a[8], "state_out");
+        d.states(last, "state_out", pool);
+        pool = last.size(0);
+    } else if (want) {
+        if (a[7] != Py_None) value_error("final states at slots need state_out (it may be state)");
+        if (pool >= 0 && pool != d.c.N) value_error("without slots there must be one state for each sequence");
+        last = fresh({d.c.N, d.c.Hv, d.c.dk, d.c.dv}, at::kFloat, d.q);
+        pool = d.c.N;
+    }
+    if (pool >= 0)
+        d.places(a[7], pool);
+    else if (a[7] != Py_None)
+        value_error("slots without state or state_out");
+    if (a[11] == Py_None) {
+        out = fresh(d.v.sizes(), d.q.scalar_type(), d.q);
+    } else {
+        out = tensor(a[11], "out");
+        if (out.sizes() != d.v.sizes() || !out.is_contiguous() || !out.is_cuda() || out.get_device() != d.dev ||
+            out.scalar_type() != d.q.scalar_type())
+            value_error("out must be a contiguous [T, Hv, dv] tensor of q's dtype and device");
+    }
+    const at::Tensor ws = scratch(a[12], d, 0);
+    check(ra_delta_rule_fwd(&d.c, out.data_ptr(), last.defined() ? static_cast<float *>(last.data_ptr()) : nullptr,
+                            ws.data_ptr(), ws.nbytes(), on.stream),
+          "ra_delta_rule_fwd");
+    return pair(std::move(out), std::move(last));
+}
+
+// (dout, q, k, v, g, beta, cu_seqlens, state, slots, dstate, scale, workspace)
+PyObject *delta_bwd(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 12);
+    DeltaArg d(a[1], a[2], a[3], a[4], a[5], a[10]);
+    d.segments(a[6]);
+    const at::Tensor &dout = tensor(a[0], "dout");
+    const int64_t stride = rows(dout, "dout", &d.q);
+    if (dout.sizes() != d.v.sizes()) value_error("dout must be [T, Hv, dv]");
+    On on(d.dev);
+    at::Tensor g[6];
+    float *last = nullptr;
+    if (a[7] != Py_None) {
+        const at::Tensor &s = tensor(a[7], "state");
+        d.c.state = d.states(s, "state", -1);
+        d.places(a[8], s.size(0));
+        g[5] = fresh({d.c.N, d.c.Hv, d.c.dk, d.c.dv}, at::kFloat, d.q);
+    } else if (a[8] != Py_None) {
+        value_error("slots without state");
+    }
+    if (a[9] != Py_None) last = d.states(tensor(a[9], "dstate"), "dstate", d.c.N);
+    const auto type = d.q.scalar_type();
+    g[0] = fresh(d.q.sizes(), type, d.q);
+    g[1] = fresh(d.q.sizes(), type, d.q);
+    g[2] = fresh(d.v.sizes(), type, d.q);
+    g[3] = fresh({d.c.T, d.c.Hv}, at::kFloat, d.q);
+    g[4] = fresh({d.c.T, d.c.Hv}, at::kFloat, d.q);
+    const at::Tensor ws = scratch(a[11], d, 1);
+    check(ra_delta_rule_bwd(&d.c, dout.data_ptr(), stride, last, g[0].data_ptr(), g[1].data_ptr(), g[2].data_ptr(),
+                            static_cast<float *>(g[3].data_ptr()), static_cast<float *>(g[4].data_ptr()),
+                            g[5].defined() ? static_cast<float *>(g[5].data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(),
+                            on.stream),
+          "ra_delta_rule_bwd");
+    PyObject *t = PyTuple_New(6);
+    if (!t) throw Raised{};
+    for (int i = 0; i < 6; ++i) {
+        PyObject *x = g[i].defined() ? THPVariable_Wrap(std::move(g[i])) : Py_NewRef(Py_None);
+        if (!x) {
+            Py_DECREF(t);
+            throw Raised{};
+        }
+        PyTuple_SET_ITEM(t, i, x);
+    }
+    return t;
+}
+
+// (q, k, v, g, beta, state, slots, scale, out)
+PyObject *delta_step(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 9);
+    DeltaArg d(a[0], a[1], a[2], a[3], a[4], a[7]);
+    if (d.c.T > INT32_MAX) value_error("too many sequences");
+    d.c.N = (int)d.c.T;
+    const at::Tensor &s = tensor(a[5], "state");
+    float *state = d.states(s, "state", -1);
+    d.places(a[6], s.size(0));
+    On on(d.dev);
+    at::Tensor out;
+    if (a[8] == Py_None) {
+        out = fresh(d.v.sizes(), d.q.scalar_type(), d.q);
+    } else {
+        out = tensor(a[8], "out");
+        if (out.sizes() != d.v.sizes() || !out.is_contiguous() || !out.is_cuda() || out.get_device() != d.dev ||
+            out.scalar_type() != d.q.scalar_type())
+            value_error("out must be a contiguous [B, Hv, dv] tensor of q's dtype and device");
+    }
+    check(ra_delta_rule_step(&d.c, state, out.data_ptr(), on.stream), "ra_delta_rule_step");
+    return THPVariable_Wrap(std::move(out));
+}
+
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -367,6 +556,9 @@ PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void *)entry<rope>, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void *)entry<append>, METH_FASTCALL, nullptr},
     {"attn", (PyCFunction)(void *)entry<attn>, METH_FASTCALL, nullptr},
+    {"delta_fwd", (PyCFunction)(void *)entry<delta_fwd>, METH_FASTCALL, nullptr},
+    {"delta_bwd", (PyCFunction)(void *)entry<delta_bwd>, METH_FASTCALL, nullptr},
+    {"delta_step", (PyCFunction)(void *)entry<delta_step>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

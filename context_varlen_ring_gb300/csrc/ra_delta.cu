@@ -1,0 +1,533 @@
+// ra_delta.cu -- the gated delta rule forward: packed sequences chunk by
+// chunk, and one token of each sequence against its state.
+//
+// A head's state S [dk, dv] takes up one token after another:
+//   S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  o = scale S^T q.
+// Over a chunk of 64 tokens with the state S0 ahead of it, and G the running
+// sums of g in the chunk, D_ij = exp(G_i - G_j) for j <= i:
+//   A_ij = beta_i D_ij k_i.k_j (j < i),   T = (I + A)^-1
+//   r = v - e^G (K S0),   u = T (beta r)
+//   o = scale e^G (Q S0) + P u,   P_ij = scale D_ij q_i.k_j (j <= i)
+//   S1 = e^(G_63) S0 + K^T (e^(G_63 - G) u)
+// T and P need no state: one kernel makes them for all chunks at once.  A
+// second one walks each sequence's chunks, a CTA for each head and slice of
+// the state's columns (columns never meet), the state in registers.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ra_delta.cuh"
+#include "ra_serve.cuh"
+
+namespace ra {
+namespace {
+
+using namespace delta;
+
+// ------------------------------------------------------------ plan
+// The chunks of all sequences, and the sequences by their number of chunks
+// (the longest walk begins first).  One block.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSort = 4096;  // more sequences stay in their order
+
+__global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArgs a) {
+    __shared__ int warp_sum[32], carry, bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) carry = bad = 0;
+    __syncthreads();
+    for (int s0 = 0; s0 < a.N; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int c0 = 0, n = 0;
+        if (s < a.N) {
+            c0 = a.cu[s];
+            const int c1 = a.cu[s + 1];
+            if (c0 < 0 || c1 < c0 || c1 > a.T)
+                bad = 1;
+            else
+                n = (c1 - c0 + C - 1) / C;
+        }
+        __syncthreads();
+        if (bad) n = 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int at = carry + sum - n;
+        for (int i = 0; i < warp; ++i) at += warp_sum[i];
+        if (s < a.N) a.first[s] = at;
+        __syncthreads();
+        if (tid == kPlanThreads - 1) carry = at + n;
+        __syncthreads();
+    }
+    // (boundaries that start above 0 leave the tokens ahead of them alone)
+    const int total = min(carry, a.max_chunks);
+    if (tid == 0) {
+        a.first[a.N] = total;
+        a.hdr->chunks = bad ? 0 : total;
+        a.hdr->bad = bad;
+        if (bad) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+    }
+    __syncthreads();
+    if (bad) return;
+    for (int i = tid; i < total; i += kPlanThreads) {
+        int lo = 0, hi = a.N;  // the last sequence that begins at or ahead of chunk i
+        while (hi - lo > 1) {
+            const int m = (lo + hi) / 2;
+            if (a.first[m] <= i)
+                lo = m;
+            else
+                hi = m;
+        }
+        const int t = a.cu[lo] + (i - a.first[lo]) * C;
+        a.chunk[i] = DeltaChunk{t, min(C, a.cu[lo + 1] - t)};
+    }
+    for (int s = tid; s < a.N; s += kPlanThreads) {
+        int rank = s;
+        if (a.N <= kPlanSort) {
+            const int n = a.first[s + 1] - a.first[s];
+            rank = 0;
+            for (int i = 0; i < a.N; ++i) {
+                const int m = a.first[i + 1] - a.first[i];
+                rank += m > n || (m == n && i < s);
+            }
+        }
+        a.order[rank] = s;
+    }
+}
+
+// ------------------------------------------------------------ T and P
+constexpr int kLocalThreads = 128;
+constexpr int kLdf = C + 1;
+
+template <typename E, int NP, int DK>
+struct LocalSmem {
+    static constexpr int NPI = std::is_same<E, float>::value ? 3 : 1, LD = DK + 8;
+    bf16 k[NPI][C][LD], q[NPI][C][LD];
+    float A[C][kLdf], T[C][kLdf], Y[32][33];
+    Gates g;
+};
+
+template <typename E, int NP, int DK>
+__global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaArgs a) {
+    using Smem = LocalSmem<E, NP, DK>;
+    constexpr int NPI = Smem::NPI, LD = Smem::LD, PL = C * LD * 2;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5;
+    if (c >= a.hdr->chunks) return;
+    const DeltaChunk ch = a.chunk[c];
+    const int hk = h / (a.Hv / a.Hk);
+    const E *k = static_cast<const E *>(a.k) + ch.tok0 * a.k_stride + hk * DK;
+    const E *q = static_cast<const E *>(a.q) + ch.tok0 * a.q_stride + hk * DK;
+    load_rows<E, DK, kLocalThreads>(&sm.k[0][0][0], LD, C * LD, k, a.k_stride, ch.n);
+    load_rows<E, DK, kLocalThreads>(&sm.q[0][0][0], LD, C * LD, q, a.q_stride, ch.n);
+    cp_commit();
+    if (warp == 0) {
+        float g[2], b[2];
+        gates_load(a, ch, h, g, b);
+        gates_put(sm.g, g, b);
+    }
+    cp_wait<0>();
+    __syncthreads();
+    // rows 16 warp .. of K K^T and Q K^T, up to the diagonal
+    const uint32_t kb = smem_u32(sm.k), row = 16 * warp * LD * 2;
+    uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
+    for (int which = 0; which < 2; ++which) {
+        float acc[8][4];
+        zero(acc);
+        mm<8, NPI, NPI, 3, false, false>(acc, (which ? smem_u32(sm.q) : kb) + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
+        bf16 *P = reinterpret_cast<bf16 *>(tp + NP * C * C);
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = 16 * warp + acc_row(hf), j = acc_col(n);
+                float x = 0.f, y = 0.f;
+                if (j <= i) x = acc[n][2 * hf] * decay(sm.g, i, j);
+                if (j + 1 <= i) y = acc[n][2 * hf + 1] * decay(sm.g, i, j + 1);
+                if (which) {
+                    put2<NP>(P + i * C + j, C * C, x * a.scale, y * a.scale);
+                } else {
+                    sm.A[i][j] = j < i ? x * sm.g.beta[i] : 0.f;
+                    sm.A[i][j + 1] = j + 1 < i ? y * sm.g.beta[i] : 0.f;
+                }
+            }
+    }
+    __syncthreads();
+    // T = (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a
+    // thread a column, then [T11, 0; -T22 A21 T11, T22] for blocks of 32 and 64
+    if (tid < C) {
+        const int b = tid & ~15, j = tid & 15;
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float x = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m) x -= sm.A[b + i][b + m] * t[m];
+            t[i] = x;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sm.T[b + i][b + j] = i >= j ? t[i] : 0.f;
+    }
+    // (the blocks above the diagonal)
+    for (int i = tid; i < C * C; i += kLocalThreads)
+        if ((i >> 6) / 16 < (i & 63) / 16) sm.T[i >> 6][i & 63] = 0.f;
+    __syncthreads();
+    for (int w = 16; w < C; w *= 2) {  // two blocks of 16, one of 32
+        const int blocks = C / (2 * w);
+        for (int i = tid; i < blocks * w * w; i += kLocalThreads) {
+            const int b = i / (w * w) * 2 * w, x = i / w % w, y = i % w;
+            float s = 0.f;
+            for (int m = y; m < w; ++m) s += sm.A[b + w + x][b + m] * sm.T[b + m][b + y];
+            sm.Y[(b / (2 * w)) * 16 + x][y] = s;
+        }
+        __syncthreads();
+        for (int i = tid; i < blocks * w * w; i += kLocalThreads) {
+            const int b = i / (w * w) * 2 * w, x = i / w % w, y = i % w;
+            float s = 0.f;
+            for (int m = 0; m <= x; ++m) s += sm.T[b + w + x][b + w + m] * sm.Y[(b / (2 * w)) * 16 + m][y];
+            sm.T[b + w + x][b + y] = -s;
+        }
+        __syncthreads();
+    }
+    bf16 *T = reinterpret_cast<bf16 *>(tp);
+    for (int i = tid; i < C * C / 2; i += kLocalThreads) {
+        const int x = i / (C / 2), y = i % (C / 2) * 2;
+        put2<NP>(T + x * C + y, C * C, sm.T[x][y], sm.T[x][y + 1]);
+    }
+}
+
+// ------------------------------------------------------------ the walk
+constexpr int kScanThreads = 256;
+
+template <typename E, int NP, int DK, int DVS>
+struct ScanSmem {
+    static constexpr bool F = std::is_same<E, float>::value;
+    static constexpr int NPI = F ? 3 : 1, KB = F ? 1 : 2, LD = DK + 8, LV = DVS + 8;
+    bf16 k[KB][NPI][C][LD], q[NPI][C][LD];
+    bf16 T[NP][C][kLdc], P[NP][C][kLdc];
+    bf16 S[NP][DK][LV], R[NP][C][LV], U[NP][C][LV];
+    Gates g[2];
+};
+
+template <typename E, int NP, int DK, int DVS>
+__global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const DeltaArgs a, int keep) {
+    using Smem = ScanSmem<E, NP, DK, DVS>;
+    constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
+    constexpr int MW = DK / 16, NS = DVS / 8 / (8 / MW), NX = DVS / 16;  // n-tiles of a warp: of S, of rows of the chunk
+    constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    if (a.hdr->bad) return;
+    const int slices = a.dv / DVS, per = a.Hv * slices;
+    const int seq = a.order[blockIdx.x / per], h = blockIdx.x % per / slices, v0 = blockIdx.x % slices * DVS;
+    const int hk = h / (a.Hv / a.Hk), dv = a.dv;
+    const int c0 = a.first[seq], c1 = a.first[seq + 1];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int srow = 16 * (warp % MW), scol = warp / MW * 8 * NS;  // this warp's part of S
+    const int xrow = 16 * (warp & 3), xcol = (warp >> 2) * 8 * NX;  // and of the chunk's rows
+    const int64_t slot = a.state || a.state_out ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
+    const int64_t splace = ((slot * a.Hv + h) * DK) * dv + v0;
+
+    float S[NS][4];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            float2 x = make_float2(0.f, 0.f);
+            if (a.state && slot >= 0)
+                x = *reinterpret_cast<const float2 *>(a.state + splace + (int64_t)(srow + acc_row(hf)) * dv + scol + acc_col(n));
+            S[n][2 * hf] = x.x;
+            S[n][2 * hf + 1] = x.y;
+        }
+
+    auto load_k = [&](int c, int buf) {
+        const DeltaChunk ch = a.chunk[c];
+        load_rows<E, DK, kScanThreads>(&sm.k[buf][0][0][0], LD, C * LD, static_cast<const E *>(a.k) + ch.tok0 * a.k_stride + hk * DK,
+                                       a.k_stride, ch.n);
+    };
+    auto load_q = [&](int c) {
+        const DeltaChunk ch = a.chunk[c];
+        load_rows<E, DK, kScanThreads>(&sm.q[0][0][0], LD, C * LD, static_cast<const E *>(a.q) + ch.tok0 * a.q_stride + hk * DK,
+                                       a.q_stride, ch.n);
+    };
+    auto load_tp = [&](int c, int which) {
+        load_square<NP, kScanThreads>(which ? &sm.P[0][0][0] : &sm.T[0][0][0],
+                                      a.tp + (((int64_t)c * a.Hv + h) * 2 + which) * NP * C * C);
+    };
+    const bool want = a.out != nullptr;
+    float gg[2], gb[2];
+    if (c0 < c1) {
+        if (KB == 2) load_k(c0, 0);
+        cp_commit();
+        if (KB == 2 && want) load_q(c0);
+        cp_commit();
+        load_tp(c0, 0);
+        cp_commit();
+        if (want) load_tp(c0, 1);
+        cp_commit();
+        if (warp == 0) gates_load(a, a.chunk[c0], h, gg, gb);
+    }
+    for (int c = c0; c < c1; ++c) {
+        const int buf = KB == 2 ? (c - c0) & 1 : 0;
+        const DeltaChunk ch = a.chunk[c];
+        Gates &g = sm.g[(c - c0) & 1];
+        const int64_t cell = (int64_t)c * a.Hv + h;
+        if (KB == 1) {
+            __syncthreads();  // (the last chunk's products with K)
+            load_k(c, 0);
+            if (want) load_q(c);
+        }
+        if (warp == 0) {
+            gates_put(g, gg, gb);
+            if (c + 1 < c1) gates_load(a, a.chunk[c + 1], h, gg, gb);
+        }
+        // the values of this thread's places
+        float2 v[NX][2];
+#pragma unroll
+        for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = xrow + acc_row(hf);
+                v[n][hf] = make_float2(0.f, 0.f);
+                if (i < ch.n)
+                    v[n][hf] = load2(static_cast<const E *>(a.v) + (ch.tok0 + i) * a.v_stride + h * dv + v0 + xcol + acc_col(n));
+            }
+        // the state's parts
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = srow + acc_row(hf), j = scol + acc_col(n);
+                put2<NP>(&sm.S[0][i][j], DK * LV, S[n][2 * hf], S[n][2 * hf + 1]);
+                if (keep)
+                    *reinterpret_cast<float2 *>(a.s0 + (cell * DK + i) * dv + v0 + j) =
+                        make_float2(S[n][2 * hf], S[n][2 * hf + 1]);
+            }
+        cp_wait<2>();  // K and Q
+        __syncthreads();
+        if (KB == 2 && c + 1 < c1) load_k(c + 1, buf ^ 1);
+        cp_commit();
+        float x[NX][4], o[NX][4];
+        zero(x);
+        mm<NX, NPI, NP, NP, false, true>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+                                         DK);
+        if (want) {
+            zero(o);
+            mm<NX, NPI, NP, NP, false, true>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+                                             DK);
+        }
+#pragma unroll
+        for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
+                const float e = g.eG[i], b = g.beta[i];
+                const float r0 = v[n][hf].x - e * x[n][2 * hf], r1 = v[n][hf].y - e * x[n][2 * hf + 1];
+                put2<NP>(&sm.R[0][i][j], C * LV, b * r0, b * r1);
+                if (keep) *reinterpret_cast<float2 *>(a.r + (cell * C + i) * dv + v0 + j) = make_float2(r0, r1);
+                if (want) {
+                    o[n][2 * hf] *= e * a.scale;
+                    o[n][2 * hf + 1] *= e * a.scale;
+                }
+            }
+        cp_wait<2>();  // T
+        __syncthreads();
+        if (KB == 2 && want && c + 1 < c1) load_q(c + 1);
+        cp_commit();
+        zero(x);
+        mm<NX, NP, NP, NP, false, true>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR, 0,
+                                        xrow + 16);
+#pragma unroll
+        for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
+                if (want) put2<NP>(&sm.U[0][i][j], C * LV, x[n][2 * hf], x[n][2 * hf + 1]);
+                if (keep)
+                    *reinterpret_cast<float2 *>(a.u + (cell * C + i) * dv + v0 + j) =
+                        make_float2(x[n][2 * hf], x[n][2 * hf + 1]);
+            }
+        cp_wait<2>();  // P
+        __syncthreads();
+        if (c + 1 < c1) load_tp(c + 1, 0);
+        cp_commit();
+#pragma unroll
+        for (int n = 0; n < NX; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
+                put2<NP>(&sm.R[0][i][j], C * LV, g.eL[i] * x[n][2 * hf], g.eL[i] * x[n][2 * hf + 1]);
+            }
+        if (want) {
+            mm<NX, NP, NP, NP, false, true>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
+                                            0, xrow + 16);
+#pragma unroll
+            for (int n = 0; n < NX; ++n)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int i = xrow + acc_row(hf);
+                    if (i < ch.n)
+                        store2(static_cast<E *>(a.out) + ((int64_t)(ch.tok0 + i) * a.Hv + h) * dv + v0 + xcol + acc_col(n),
+                               o[n][2 * hf], o[n][2 * hf + 1]);
+                }
+        }
+        __syncthreads();
+        if (want && c + 1 < c1) load_tp(c + 1, 1);
+        cp_commit();
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
+        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
+    }
+    cp_wait<0>();
+    if (a.state_out && slot >= 0) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                *reinterpret_cast<float2 *>(a.state_out + splace + (int64_t)(srow + acc_row(hf)) * dv + scol + acc_col(n)) =
+                    make_float2(S[n][2 * hf], S[n][2 * hf + 1]);
+    }
+}
+
+// ------------------------------------------------------------ one token
+// Bound: memory, the state read and written once.  A CTA takes 32 columns of
+// one head's state (128 bytes a row), a thread four columns of DK / 16 rows,
+// all of them loaded before any is used.  S^T k and S^T q are summed together
+// and the output is S^T q + (k.q) u, so the rows meet once.
+constexpr int kStepThreads = 128;
+
+template <typename E, int DK>
+__global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaStepArgs a) {
+    constexpr int ROWS = DK / 16;
+    __shared__ float sk[DK], sq[DK], kq[4];
+    __shared__ float4 red[2][4][8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int parts = a.dv / 32, b = blockIdx.x / (a.Hv * parts), h = blockIdx.x / parts % a.Hv, v0 = blockIdx.x % parts * 32;
+    const int hk = h / (a.Hv / a.Hk);
+    const int64_t slot = slot_of(a.slots, a.n_slots, b, a.status);
+    const int rg = tid >> 3, c4 = (tid & 7) * 4;
+    E *out = static_cast<E *>(a.out) + ((int64_t)b * a.Hv + h) * a.dv + v0;
+    if (slot < 0) {  // a padded batch: no state, no output
+        if (tid < 16) store2(out + 2 * tid, 0.f, 0.f);
+        return;
+    }
+    float *S = a.state + ((slot * a.Hv + h) * DK + rg) * a.dv + v0 + c4;
+    float4 s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) s[i] = *reinterpret_cast<const float4 *>(S + (int64_t)i * 16 * a.dv);
+    const E *k = static_cast<const E *>(a.k) + b * a.k_stride + hk * DK, *q = static_cast<const E *>(a.q) + b * a.q_stride + hk * DK;
+    float dot = 0.f;
+    for (int i = tid; i < DK; i += kStepThreads) {
+        sk[i] = (float)k[i];
+        sq[i] = (float)q[i];
+        dot += sk[i] * sq[i];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) kq[warp] = dot;
+    const E *vp = static_cast<const E *>(a.v) + b * a.v_stride + h * a.dv + v0 + c4;
+    const float2 va = load2(vp), vb = load2(vp + 2);
+    const float decay = expf(__ldg(a.g + (int64_t)b * a.Hv + h)), beta = __ldg(a.beta + (int64_t)b * a.Hv + h);
+    __syncthreads();
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const float kk = sk[rg + 16 * i], qq = sq[rg + 16 * i];
+        s[i].x *= decay, s[i].y *= decay, s[i].z *= decay, s[i].w *= decay;
+        x.x += s[i].x * kk, x.y += s[i].y * kk, x.z += s[i].z * kk, x.w += s[i].w * kk;
+        y.x += s[i].x * qq, y.y += s[i].y * qq, y.z += s[i].z * qq, y.w += s[i].w * qq;
+    }
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o), x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, o), x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+        y.x += __shfl_xor_sync(0xffffffffu, y.x, o), y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+        y.z += __shfl_xor_sync(0xffffffffu, y.z, o), y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+    }
+    if (lane < 8) {
+        red[0][warp][lane] = x;
+        red[1][warp][lane] = y;
+    }
+    __syncthreads();
+    x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    dot = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float4 p = red[0][w][tid & 7], r = red[1][w][tid & 7];
+        x.x += p.x, x.y += p.y, x.z += p.z, x.w += p.w;
+        y.x += r.x, y.y += r.y, y.z += r.z, y.w += r.w;
+        dot += kq[w];
+    }
+    const float4 u = make_float4(beta * (va.x - x.x), beta * (va.y - x.y), beta * (vb.x - x.z), beta * (vb.y - x.w));
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const float kk = sk[rg + 16 * i];
+        s[i].x += kk * u.x, s[i].y += kk * u.y, s[i].z += kk * u.z, s[i].w += kk * u.w;
+        *reinterpret_cast<float4 *>(S + (int64_t)i * 16 * a.dv) = s[i];
+    }
+    if (tid < 8) {
+        store2(out + c4, a.scale * (y.x + dot * u.x), a.scale * (y.y + dot * u.y));
+        store2(out + c4 + 2, a.scale * (y.z + dot * u.z), a.scale * (y.w + dot * u.w));
+    }
+}
+
+template <typename E, int NP, int DK>
+cudaError_t local(const DeltaArgs &a, cudaStream_t st) {
+    static LaunchFit fit;
+    auto kernel = delta_local_kernel<E, NP, DK>;
+    const size_t smem = sizeof(LocalSmem<E, NP, DK>);
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kLocalThreads, smem, nullptr);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(a.max_chunks, a.Hv), kLocalThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename E, int NP, int DK, int DVS>
+cudaError_t scan(const DeltaArgs &a, int keep, cudaStream_t st) {
+    static LaunchFit fit;
+    auto kernel = delta_scan_kernel<E, NP, DK, DVS>;
+    const size_t smem = sizeof(ScanSmem<E, NP, DK, DVS>);
+    static_assert(sizeof(ScanSmem<E, NP, DK, DVS>) <= 232448, "shared memory of one CTA");
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kScanThreads, smem, nullptr);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kScanThreads, smem, st>>>(a, keep);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_plan(const DeltaArgs &a, cudaStream_t st) {
+    delta_plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+cudaError_t launch_delta_local(const DeltaArgs &a, cudaStream_t st) {
+    if (a.dtype == RA_FP32) return a.dk == 64 ? local<float, 3, 64>(a, st) : local<float, 3, 128>(a, st);
+    if (a.parts == 2) return a.dk == 64 ? local<bf16, 2, 64>(a, st) : local<bf16, 2, 128>(a, st);
+    return a.dk == 64 ? local<bf16, 3, 64>(a, st) : local<bf16, 3, 128>(a, st);
+}
+cudaError_t launch_delta_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
+    if (a.dtype == RA_FP32) return a.dk == 64 ? scan<float, 3, 64, 32>(a, keep, st) : scan<float, 3, 128, 32>(a, keep, st);
+    if (a.parts == 2) return a.dk == 64 ? scan<bf16, 2, 64, 64>(a, keep, st) : scan<bf16, 2, 128, 64>(a, keep, st);
+    return a.dk == 64 ? scan<bf16, 3, 64, 64>(a, keep, st) : scan<bf16, 3, 128, 64>(a, keep, st);
+}
+cudaError_t launch_delta_step(const DeltaStepArgs &a, cudaStream_t st) {
+    const unsigned grid = (unsigned)((int64_t)a.B * a.Hv * (a.dv / 32));
+    if (a.dtype == RA_FP32) {
+        if (a.dk == 64)
+            delta_step_kernel<float, 64><<<grid, kStepThreads, 0, st>>>(a);
+        else
+            delta_step_kernel<float, 128><<<grid, kStepThreads, 0, st>>>(a);
+    } else if (a.dk == 64) {
+        delta_step_kernel<bf16, 64><<<grid, kStepThreads, 0, st>>>(a);
+    } else {
+        delta_step_kernel<bf16, 128><<<grid, kStepThreads, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace ra

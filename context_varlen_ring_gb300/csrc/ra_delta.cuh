@@ -1,0 +1,238 @@
+// ra_delta.cuh -- what the gated delta rule's kernels share: products of tiles
+// held as bf16 parts, a chunk's gates, and the loads of its rows.
+//
+// Arithmetic.  The states, their gradients and the gates' gradients are fp32
+// results, so the products' operands have to carry more than bf16's 8 bits: an
+// operand that is not bf16 itself is held as the sum of 2 or 3 bf16 parts (16
+// or 24 bits), and a product adds the parts' products up to the order that the
+// parts have, in fp32.  q, k, v and dout of a bf16 call are one part, exactly.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "ra_delta.h"
+#include "ra_dev.cuh"
+
+namespace ra {
+namespace delta {
+
+using namespace dev;
+using bf16 = __nv_bfloat16;
+constexpr int C = kDeltaChunk;
+constexpr int kLdc = C + 8;  // pitch of a [64][64] tile: rows of 9 x 16 bytes, so that eight rows meet eight bank groups
+
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// acc[16 x 8 NT] += A[16 x K] B[K x 8 NT] over K = k0 .. k1 - 1 (multiples of
+// 16), operands of PA and PB parts, products of parts i, j with i + j < NP.
+// a, b: shared addresses of A's and B's first element; lda, ldb: pitches in
+// elements; pa, pb: bytes between parts.  TA: A is stored [K][M]; BKN: B is
+// stored [K][N], else [N][K].
+template <int NT, int PA, int PB, int NP, bool TA, bool BKN>
+__device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int pa, uint32_t b, int ldb, int pb, int k0,
+                                   int k1, int pairs = NT / 2) {
+    const int l = threadIdx.x & 31, r = l & 7, s = (l >> 3) & 1, h = l >> 4;
+    a += 2 * (TA ? (h * 8 + r) * lda + s * 8 : (s * 8 + r) * lda + h * 8);
+    b += 2 * (BKN ? (s * 8 + r) * ldb + h * 8 : (h * 8 + r) * ldb + s * 8);
+    const int as = TA ? 2 * lda : 2, bs = BKN ? 2 * ldb : 2, bn = BKN ? 32 : 32 * ldb;
+#pragma unroll 2
+    for (int k = k0; k < k1; k += 16) {
+        uint32_t fa[PA][4];
+#pragma unroll
+        for (int i = 0; i < PA; ++i) ldsm4<TA>(a + i * pa + k * as, fa[i]);
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) {
+            if (n >= pairs) break;
+            uint32_t fb[PB][4];
+#pragma unroll
+            for (int j = 0; j < PB; ++j) ldsm4<BKN>(b + j * pb + k * bs + n * bn, fb[j]);
+            // (the small products first)
+#pragma unroll
+            for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i < PA; ++i) {
+                    const int j = o - i;
+                    if (j < 0 || j >= PB) continue;
+                    mma(acc[2 * n], fa[i], fb[j][0], fb[j][1]);
+                    mma(acc[2 * n + 1], fa[i], fb[j][2], fb[j][3]);
+                }
+        }
+    }
+}
+template <int NT>
+__device__ __forceinline__ void zero(float (&acc)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+}
+
+// Two neighbouring elements into NP bf16 parts, `plane` elements apart.
+template <int NP>
+__device__ __forceinline__ void put2(bf16 *p, int plane, float x, float y) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        *reinterpret_cast<__nv_bfloat162 *>(p + i * plane) = h;
+        x -= __low2float(h);
+        y -= __high2float(h);
+    }
+}
+template <int NP>
+__device__ __forceinline__ float2 get2(const bf16 *p, int plane) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = NP - 1; i >= 0; --i) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + i * plane));
+        s.x += x.x;
+        s.y += x.y;
+    }
+    return s;
+}
+// Row and first column of an accumulator's pair: acc[n][2 half], acc[n][2 half + 1].
+__device__ __forceinline__ int acc_row(int half) { return ((threadIdx.x & 31) >> 2) + 8 * half; }
+__device__ __forceinline__ int acc_col(int n) { return n * 8 + 2 * (threadIdx.x & 3); }
+
+template <typename E>
+__device__ __forceinline__ float2 load2(const E *p) {
+    if (std::is_same<E, float>::value) return *reinterpret_cast<const float2 *>(p);
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+}
+template <typename E>
+__device__ __forceinline__ void store2(E *p, float x, float y) {
+    if (std::is_same<E, float>::value)
+        *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+    else
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
+
+// Rows 0 .. n - 1 of [64][W] elements, `stride` apart, into parts of pitch ld
+// (rows behind them zero).  bf16: asynchronous copies, not committed.
+template <typename E, int W, int THREADS>
+__device__ __forceinline__ void load_rows(bf16 *dst, int ld, int plane, const E *src, int64_t stride, int n) {
+    if (std::is_same<E, float>::value) {
+        for (int i = threadIdx.x; i < C * (W / 4); i += THREADS) {
+            const int row = i / (W / 4), c = i % (W / 4) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < n) x = *reinterpret_cast<const float4 *>(src + row * stride + c);
+            put2<3>(dst + row * ld + c, plane, x.x, x.y);
+            put2<3>(dst + row * ld + c + 2, plane, x.z, x.w);
+        }
+    } else {
+        for (int i = threadIdx.x; i < C * (W / 8); i += THREADS) {
+            const int row = i / (W / 8), c = i % (W / 8) * 8;
+            cp16z(smem_u32(dst + row * ld + c), src + (row < n ? row * stride : 0) + c, row < n);
+        }
+    }
+}
+// T or P (parts of [64][64], one behind another) into parts of pitch kLdc; not committed.
+template <int NP, int THREADS>
+__device__ __forceinline__ void load_square(bf16 *dst, const uint16_t *src) {
+    for (int i = threadIdx.x; i < NP * C * 8; i += THREADS) {
+        const int row = i >> 3, c = (i & 7) * 8;  // (parts one behind another on both sides)
+        cp16z(smem_u32(dst + row * kLdc + c), src + row * C + c, true);
+    }
+}
+__device__ __forceinline__ const uint16_t *square_of(const DeltaArgs &a, int64_t ch, int which, int parts) {
+    return a.tp + (ch * 2 + which) * parts * C * C;
+}
+
+// A chunk's gates.  G_i is the sum of its first i + 1 log decays; kept as the
+// sum of two floats, because the products use exp(G_i - G_j), whose exponent
+// would otherwise lose the bits that a strong decay ahead of both pushes out.
+// Decays below -1e4 are e^-1e4 = 0 all the same, and keep the sums finite.
+struct Gates {
+    float hi[C], lo[C];
+    float beta[C];
+    float eG[C];     // exp(G_i): the state ahead of the chunk as token i sees it
+    float eL[C];     // exp(G_63 - G_i): what token i writes as the chunk's end sees it
+    float eC;        // exp(G_63)
+};
+__device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
+    const float s = a.x + b.x, t = s - a.x;
+    const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+    const float h = s + e;
+    return make_float2(h, e - (h - s));
+}
+__device__ __forceinline__ float gate_exp(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
+// The exponential of the gates between tokens j < i (1 at j = i).
+__device__ __forceinline__ float decay(const Gates &s, int i, int j) {
+    return gate_exp(make_float2(s.hi[i], s.lo[i]), make_float2(s.hi[j], s.lo[j]));
+}
+// Lane l's log decays and betas of tokens 2 l and 2 l + 1 (0 behind the chunk's n).
+__device__ __forceinline__ void gates_load(const DeltaArgs &a, const DeltaChunk &ch, int h, float (&g)[2], float (&b)[2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const int64_t at = (int64_t)(ch.tok0 + t) * a.Hv + h;
+        g[i] = t < ch.n ? __ldg(a.g + at) : 0.f;
+        b[i] = t < ch.n ? __ldg(a.beta + at) : 0.f;
+        if (g[i] < -1e4f) g[i] = -1e4f;
+    }
+}
+// One warp.
+__device__ __forceinline__ void gates_put(Gates &s, const float (&g)[2], const float (&b)[2]) {
+    const int lane = threadIdx.x & 31;
+    const float2 first = make_float2(g[0], 0.f);
+    float2 sum = two_sum(first, make_float2(g[1], 0.f));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float2 x = make_float2(__shfl_up_sync(0xffffffffu, sum.x, o), __shfl_up_sync(0xffffffffu, sum.y, o));
+        if (lane >= o) sum = two_sum(x, sum);
+    }
+    float2 before = make_float2(__shfl_up_sync(0xffffffffu, sum.x, 1), __shfl_up_sync(0xffffffffu, sum.y, 1));
+    if (lane == 0) before = make_float2(0.f, 0.f);
+    const float2 last = make_float2(__shfl_sync(0xffffffffu, sum.x, 31), __shfl_sync(0xffffffffu, sum.y, 31));
+    const float2 none = make_float2(0.f, 0.f), at[2] = {two_sum(before, first), sum};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        s.hi[t] = at[i].x;
+        s.lo[t] = at[i].y;
+        s.beta[t] = b[i];
+        s.eG[t] = gate_exp(at[i], none);
+        s.eL[t] = gate_exp(last, at[i]);
+    }
+    if (lane == 0) s.eC = gate_exp(last, none);
+}
+
+// The state's place of a sequence in the pool; -1: it has none (a negative slot), or one outside the pool (recorded).
+__device__ __forceinline__ int64_t slot_of(const int32_t *slots, int64_t n_slots, int seq, int *status) {
+    const int64_t s = slots ? __ldg(slots + seq) : seq;
+    if (s >= 0 && s < n_slots) return s;
+    if (s >= n_slots) record_status(status, RA_ERR_DEVICE_BOUNDS);
+    return -1;
+}
+
+}  // namespace delta
+}  // namespace ra

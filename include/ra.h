@@ -496,6 +496,75 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
                             void *workspace, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * ra_delta_rule_fwd / ra_delta_rule_bwd / ra_delta_rule_step  (DEVICE tensors
+ * and DEVICE segment arrays)
+ *
+ * The gated delta rule over packed sequences: the mixer of tokens whose memory
+ * is a state of fixed size, S [dk, dv] for each value head.  Token t, with
+ * a = exp(g[t]) and b = beta[t]:
+ *   S <- a S;   u = b (v - S^T k);   S <- S + k u^T;   out = scale S^T q
+ * Value head h reads query and key head h / (Hv / Hk).
+ *   q, k DEVICE [T, Hk, dk], v DEVICE [T, Hv, dv] of dtype (rows q_stride,
+ *      k_stride, v_stride elements apart); g, beta DEVICE fp32 [T, Hv]
+ *      contiguous: the logarithm of the decay (usually <= 0; -inf forgets all,
+ *      as does anything below -1e4), and the writing strength
+ *   cu_seqlens DEVICE int32 [N+1], non-decreasing, from 0 on; tokens at or
+ *      behind cu_seqlens[N] (a padded batch) are left alone: no output and no
+ *      gradient is written for them
+ *   state DEVICE fp32 [n_slots, Hv, dk, dv] or NULL (zeros): the states ahead
+ *      of the sequences; slots DEVICE int32 [N] or NULL (0, 1, ...): sequence
+ *      b's place.  A negative slot: the sequence begins at zero and its last
+ *      state is dropped.  A slot at or above n_slots is treated so too, and
+ *      RA_ERR_DEVICE_BOUNDS is recorded.
+ * Forward: out DEVICE [T, Hv, dv] contiguous, of dtype; state_out NULL or
+ *   DEVICE fp32 [n_slots, Hv, dk, dv], the states behind the sequences at the
+ *   same slots (it may be `state`; two sequences of one call must not name one
+ *   slot).
+ * Backward: dout DEVICE [T, Hv, dv] of dtype (rows dout_stride apart), dstate
+ *   DEVICE fp32 [N, Hv, dk, dv] or NULL (zeros): the gradients of out and of
+ *   the last states, by sequence; dq, dk [T, Hk, dk], dv [T, Hv, dv]
+ *   contiguous of dtype, dg, dbeta fp32 [T, Hv], dstate0 NULL or fp32
+ *   [N, Hv, dk, dv], by sequence.  Nothing of the forward is needed: the
+ *   states are computed again.
+ * Step: one token of each sequence (T = N, cu_seqlens and state of d unused):
+ *   `state` is read and written in place at the slots; a sequence without a
+ *   slot gets output 0.
+ * States, sums and gates are fp32, and the products carry 24 bits (16 in the
+ * forward of bf16 tensors without state_out, whose only result is rounded to
+ * bf16).  One rounding of each bf16 result; deterministic.  A NaN or an
+ * infinity reaches every token of its chunk (64 tokens of a sequence) and all
+ * behind it.  Chunks of a sequence with nothing to forget are exact in the
+ * same sense at any length.
+ * dk and dv 64 or 128; q, k, v, dout and all outputs 16-byte aligned with
+ * strides of whole 16 bytes; T <= 2^30, N <= 2^20, N * Hv <= 2^26.
+ * workspace DEVICE, 256-byte aligned, >= ra_delta_rule_workspace_bytes(...)
+ * (0 for invalid arguments); calls in flight at the same time, and captured
+ * graphs that may run so, need workspaces of their own.  Capturable; the
+ * arrays' contents may change between replays.  Boundaries that decrease or
+ * leave [0, T] are recorded as RA_ERR_DEVICE_BOUNDS and leave all outputs
+ * unwritten.
+ * ------------------------------------------------------------------------ */
+typedef struct ra_delta {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta;
+    int64_t T;
+    int32_t N, Hk, Hv, dk, dv, dtype;
+    const int32_t *cu_seqlens;
+    const float *state;
+    const int32_t *slots;
+    int64_t n_slots;
+    float scale;
+} ra_delta;
+size_t ra_delta_rule_workspace_bytes(int64_t T, int N, int Hk, int Hv, int dk, int dv, int dtype, int bwd);
+ra_status ra_delta_rule_fwd(const ra_delta *d, void *out, float *state_out, void *workspace, size_t ws_bytes,
+                            void *stream);
+ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_stride, const float *dstate, void *dq,
+                            void *dk, void *dv, float *dg, float *dbeta, float *dstate0, void *workspace,
+                            size_t ws_bytes, void *stream);
+ra_status ra_delta_rule_step(const ra_delta *d, float *state, void *out, void *stream);
+
+/* ------------------------------------------------------------------------
  * ra_ring_rank_pairs  (HOST, synchronous)
  *
  * Allowed (query, key) pairs each simulated rank computes over the whole
