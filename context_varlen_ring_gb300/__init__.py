@@ -21,7 +21,7 @@ __all__ = [
     "lse_merge",
     "ring_attn_fwd", "ring_attn_bwd", "ring_rank_pairs", "ring_plan_stats", "device_status", "selftest_wait_timeout",
     "rope_inv_freq", "rope_axes", "rope_fwd", "rope_bwd", "kv_cache_append", "paged_attn_fwd",
-    "paged_attn_workspace_bytes",
+    "paged_attn_workspace_bytes", "paged_attn_key_weights", "kv_cache_evict",
     "delta_rule_fwd", "delta_rule_bwd", "delta_rule_step", "delta_rule_workspace_bytes",
     "RA_ZZ_GLOBAL", "RA_ZZ_PER_DOC", "RA_SCHED_FUSED", "RA_SCHED_STEPWISE", "RA_SCHED_ALLGATHER", "RaError",
 ]
@@ -338,5 +338,5 @@ def selftest_wait_timeout(budget_us: int = 1000):
 
 from .delta import (delta_rule_bwd, delta_rule_fwd, delta_rule_step,  # noqa: E402
                     delta_rule_workspace_bytes)
-from .serving import (kv_cache_append, paged_attn_fwd, paged_attn_workspace_bytes, rope_axes, rope_bwd,  # noqa: E402
-                      rope_fwd, rope_inv_freq)
+from .serving import (kv_cache_append, kv_cache_evict, paged_attn_fwd, paged_attn_key_weights,  # noqa: E402
+                      paged_attn_workspace_bytes, rope_axes, rope_bwd, rope_fwd, rope_inv_freq)

@@ -40,6 +40,7 @@ EXPORTS = (
     "ra_ring_workspace_bytes_masked", "ra_ring_attn_fwd_masked", "ra_ring_attn_bwd_masked",
     "ra_ring_plan_stats_masked", "ra_varlen_attn_partial_dev",
     "ra_rope_fwd", "ra_rope_bwd", "ra_kv_cache_append", "ra_paged_attn_workspace_bytes", "ra_paged_attn_fwd",
+    "ra_paged_attn_key_weights", "ra_kv_cache_evict",
     "ra_delta_rule_workspace_bytes", "ra_delta_rule_fwd", "ra_delta_rule_bwd", "ra_delta_rule_step",
 )
 
@@ -56,6 +57,12 @@ class PagedKV(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class PagedWeights(ctypes.Structure):
+    """ra_paged_weights of include/ra.h."""
+    _fields_ = [("w", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 class Delta(ctypes.Structure):
@@ -111,6 +118,9 @@ def _declare(L):
         "ra_paged_attn_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32]),
         "ra_paged_attn_fwd": (i32, [P, i64, i64, i32, P, P, i64, P, P, i32, P, i64, P, P, i32, i32, i32, f32,
                                     P, i32, P, P, sz, P]),
+        "ra_paged_attn_key_weights": (i32, [P, i64, i64, i32, P, P, P, i64, P, P, i32, P, i64, P, P, i32, i32, i32,
+                                            f32, P, P]),
+        "ra_kv_cache_evict": (i32, [P, P, P, i64, P, i32, i32, P, i32, i32, i32, P, i64, P, P, P]),
         "ra_delta_rule_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i32, i32]),
         "ra_delta_rule_fwd": (i32, [P, P, P, P, sz, P]),
         "ra_delta_rule_bwd": (i32, [P, P, i64, P, P, P, P, P, P, P, P, sz, P]),

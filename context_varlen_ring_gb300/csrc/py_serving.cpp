@@ -1,6 +1,6 @@
 // py_serving.cpp -- the Python module `_serving`: argument checks, output
 // allocation and the calls into libra.so for rotary positions, the cache
-// append, paged attention and the gated delta rule.
+// append, paged attention, its keys' weights, eviction and the gated delta rule.
 //
 // These calls are made once a layer and decoding step, where the kernels take
 // a few microseconds: the same checks in Python took 40 to 50 us a call on a
@@ -352,6 +352,121 @@ PyObject *attn(PyObject *const *a, Py_ssize_t n) {
     return pair(std::move(out), std::move(lse));
 }
 
+// Weights [pages, page_size, Hkv] of a cache's keys.
+ra_paged_weights paged_weights(const at::Tensor &w, const ra_paged_kv &cache, int64_t dev) {
+    if (w.scalar_type() != at::kFloat) raise(PyExc_TypeError, "weights must be float32");
+    if (w.dim() != 3 || w.size(0) != cache.n_pages || w.size(1) != cache.page_size || w.size(2) != cache.Hkv)
+        value_error("weights must be [pages, page_size, Hkv] of the cache");
+    if (!w.is_cuda() || w.get_device() != dev) value_error("weights must be on the device of the cache");
+    return ra_paged_weights{static_cast<float *>(w.data_ptr()), w.stride(0), w.stride(1), w.stride(2)};
+}
+
+// (q, k_cache, page_table, cu_seqlens_q, kv_lens, lse, weights, prefix_table, prefix_lens, prefix_groups, causal, scale,
+//  max_q_len)
+PyObject *key_weights(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 13);
+    const at::Tensor &q = tensor(a[0], "q");
+    const int64_t qs = rows(q, "q"), T = q.size(0), d = q.size(2), dev = q.get_device();
+    const int hq = int_of(q.size(1), "q");
+    const at::Tensor &kc = tensor(a[1], "k_cache"), &lse = tensor(a[5], "lse"), &w = tensor(a[6], "weights");
+    const ra_paged_kv cache = paged(kc, kc);
+    if (kc.get_device() != dev || kc.scalar_type() != q.scalar_type() || cache.d != d)
+        value_error("the cache must have the device, dtype and head size of q");
+    const ra_paged_weights pw = paged_weights(w, cache, dev);
+    if (lse.dim() != 2 || lse.size(0) != hq || lse.size(1) != T || !lse.is_contiguous() || !lse.is_cuda() ||
+        lse.get_device() != dev || lse.scalar_type() != at::kFloat)
+        value_error("lse must be a contiguous fp32 [Hq, T] tensor on q's device");
+    const Segments s(a[2], a[3], a[4], dev);
+    const bool some = a[7] != Py_None || a[8] != Py_None || a[9] != Py_None;
+    if (some && (a[7] == Py_None || a[8] == Py_None || a[9] == Py_None))
+        value_error("prefix_table, prefix_lens and prefix_groups go together");
+    const Segments *pre = nullptr;
+    alignas(Segments) char room[sizeof(Segments)];
+    if (some) pre = new (room) Segments(a[7], a[9], a[8], dev);
+    const int causal = PyObject_IsTrue(a[10]);
+    if (causal < 0) throw Raised{};
+    double scale = 1.0 / std::sqrt((double)d);
+    if (a[11] != Py_None) {
+        scale = PyFloat_AsDouble(a[11]);
+        if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    }
+    long long most = 0;
+    if (a[12] != Py_None) {
+        most = PyLong_AsLongLong(a[12]);
+        if (most == -1 && PyErr_Occurred()) throw Raised{};
+        most = std::min<long long>(std::max<long long>(most, 0), INT32_MAX);
+    }
+    On on(dev);
+    check(ra_paged_attn_key_weights(q.data_ptr(), qs, T, hq, &cache, &pw, s.table, s.width, s.cu, s.lens, s.B,
+                                    pre ? pre->table : nullptr, pre ? pre->width : 0, pre ? pre->lens : nullptr,
+                                    pre ? pre->cu : nullptr, pre ? pre->B : 0, causal, (int)most, (float)scale,
+                                    static_cast<const float *>(lse.data_ptr()), on.stream),
+          "ra_paged_attn_key_weights");
+    return Py_NewRef(a[6]);
+}
+
+// (k_cache, v_cache, weights, page_table, kv_lens, keep, keep_lens, sinks, recent, per_head, out_table, new_lens, kept)
+PyObject *evict(PyObject *const *a, Py_ssize_t n) {
+    arity(n, 13);
+    const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache");
+    const ra_paged_kv cache = paged(kc, vc);
+    const int64_t dev = kc.get_device();
+    const ra_paged_weights pw = paged_weights(tensor(a[2], "weights"), cache, dev);
+    const at::Tensor &table = tensor(a[3], "page_table"), &lens = tensor(a[4], "kv_lens");
+    const int32_t *tp = index(table, "page_table", dev), *lp = index(lens, "kv_lens", dev);
+    if (table.dim() != 2 || lens.dim() != 1 || table.size(0) != lens.numel() || lens.numel() > INT32_MAX)
+        value_error("page_table [B, width] and kv_lens [B] must agree");
+    const int B = (int)lens.numel();
+    long long num[3];
+    const char *names[3] = {"keep", "sinks", "recent"};
+    PyObject *const given[3] = {a[5], a[7], a[8]};
+    for (int i = 0; i < 3; ++i) {
+        num[i] = PyLong_AsLongLong(given[i]);
+        if (num[i] == -1 && PyErr_Occurred()) throw Raised{};
+        if (num[i] < 0 || num[i] > INT32_MAX) value_error(std::string(names[i]) + " must be in [0, 2^31)");
+    }
+    const int32_t *each = nullptr, *op = nullptr;
+    int64_t ow = 0;
+    if (a[6] != Py_None) {
+        const at::Tensor &x = tensor(a[6], "keep_lens");
+        each = index(x, "keep_lens", dev);
+        if (x.dim() != 1 || x.numel() != B) value_error("keep_lens must be [B]");
+    }
+    const int per_head = PyObject_IsTrue(a[9]);
+    if (per_head < 0) throw Raised{};
+    if (a[10] != Py_None) {
+        const at::Tensor &x = tensor(a[10], "out_table");
+        op = index(x, "out_table", dev);
+        if (x.dim() != 2 || x.size(0) != B) value_error("out_table must be [B, width]");
+        ow = x.size(1);
+        static const int32_t none = 0;
+        if (!op) op = &none;  // (no entries: nothing is read, nothing is kept)
+    }
+    On on(dev);
+    at::Tensor left, kept;
+    const int64_t H = per_head ? cache.Hkv : 1;
+    if (a[11] == Py_None) {
+        left = fresh({B}, at::kInt, kc);
+    } else {
+        left = tensor(a[11], "new_lens");
+        index(left, "new_lens", dev);
+        if (left.dim() != 1 || left.numel() != B) value_error("new_lens must be [B]");
+    }
+    if (a[12] == Py_None) {
+        kept = fresh({B, H, num[0]}, at::kInt, kc);
+    } else {
+        kept = tensor(a[12], "kept");
+        index(kept, "kept", dev);
+        if (kept.dim() != 3 || kept.size(0) != B || kept.size(1) != H || kept.size(2) != num[0])
+            value_error("kept must be [B, Hkv (1 without per_head), keep]");
+    }
+    check(ra_kv_cache_evict(&cache, &pw, tp, table.size(1), lp, B, (int)num[0], each, (int)num[1], (int)num[2], per_head, op,
+                            ow, static_cast<int32_t *>(left.data_ptr()), static_cast<int32_t *>(kept.data_ptr()),
+                            on.stream),
+          "ra_kv_cache_evict");
+    return pair(std::move(left), std::move(kept));
+}
+
 // The gated delta rule's inputs: q, k [T, Hk, dk], v [T, Hv, dv], g, beta fp32 [T, Hv].
 struct DeltaArg {
     ra_delta c{};
@@ -556,6 +671,8 @@ PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void *)entry<rope>, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void *)entry<append>, METH_FASTCALL, nullptr},
     {"attn", (PyCFunction)(void *)entry<attn>, METH_FASTCALL, nullptr},
+    {"key_weights", (PyCFunction)(void *)entry<key_weights>, METH_FASTCALL, nullptr},
+    {"evict", (PyCFunction)(void *)entry<evict>, METH_FASTCALL, nullptr},
     {"delta_fwd", (PyCFunction)(void *)entry<delta_fwd>, METH_FASTCALL, nullptr},
     {"delta_bwd", (PyCFunction)(void *)entry<delta_bwd>, METH_FASTCALL, nullptr},
     {"delta_step", (PyCFunction)(void *)entry<delta_step>, METH_FASTCALL, nullptr},

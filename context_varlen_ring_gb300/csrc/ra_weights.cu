@@ -1,0 +1,437 @@
+// ra_weights.cu -- the attention weight that each cached key gathers from a
+// batch's new tokens: w[key, KV head] += sum over the query rows that see the
+// key of exp(scale q.k - lse), what eviction from the cache goes by.
+//
+// A unit is a tile of keys of one KV head: its CTA loads the keys once, walks
+// the query rows that see them and owns their sums, so nothing is added by two
+// CTAs and the order of the sums is fixed.  Scores have keys as rows and query
+// rows as columns: a key's sum is then a sum over columns, which stays in the
+// thread that has the key until the tile ends.  The units of all sequences and
+// prefixes form one line, which the CTAs take in strides.
+//
+// Bound: with the few rows of a decoding step, memory (each key read once);
+// with a chunk of hundreds of tokens, the products and exponentials.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "ra_dev.cuh"
+#include "ra_keep.h"
+#include "ra_kernels.h"
+#include "ra_serve.cuh"
+
+namespace ra {
+namespace {
+
+using namespace dev;
+using bf16 = __nv_bfloat16;
+
+constexpr int kThreads = 128;
+constexpr int kSegs = 1024;  // segments that a CTA lines up at a time
+
+__device__ __forceinline__ int token_of(const WeightArgs &a, int row) {
+    return a.G == 1 ? row : (int)__umul64hi((unsigned)row, a.G_inv);
+}
+
+// A segment: own keys of a sequence, or the keys of a prefix (behind the B sequences).
+struct Segment {
+    int tok0, n, len;
+};
+__device__ __forceinline__ bool segment(const WeightArgs &a, int s, Segment &g) {
+    const int f = s >= a.B, i = s - (f ? a.B : 0);
+    const int len = f ? a.prefix_lens[i] : a.kv_lens[i];
+    const int b0 = f ? a.groups[i] : i, b1 = f ? a.groups[i + 1] : i + 1;
+    const int c0 = a.cu[min(max(b0, 0), a.B)], c1 = a.cu[min(max(b1, 0), a.B)];
+    const bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= a.width[f] * a.page_size &&
+                      len <= kPagedMostKeys && c0 >= 0 && c1 >= c0 && c1 <= a.T;
+    g.tok0 = c0;
+    g.n = fine ? c1 - c0 : 0;
+    g.len = fine ? len : 0;
+    return fine;
+}
+
+struct Line {
+    int at[kSegs + 1];  // tiles ahead of each segment
+    long long warp[kThreads / 32];
+};
+// Lines up the segments from s0 on; their tiles of 2^k keys, or -1 where any segment is not as it must be (or the
+// tiles are more than any memory holds).
+__device__ __forceinline__ int line_up(const WeightArgs &a, int s0, int k, Line &sh) {
+    constexpr int PER = kSegs / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, S = a.B + a.n_groups;
+    int n[PER], bad = 0;
+    long long sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int s = s0 + tid * PER + i;
+        Segment g;
+        n[i] = 0;
+        if (s < S) {
+            bad |= !segment(a, s, g);
+            n[i] = g.n > 0 ? (g.len + (1 << k) - 1) >> k : 0;
+        }
+        sum += n[i];
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp[tid >> 5] = inc;
+    bad = __syncthreads_or(bad);
+    long long at = inc - sum, all = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < (tid >> 5)) at += sh.warp[i];
+        all += sh.warp[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        sh.at[tid * PER + i] = (int)at;
+        at += n[i];
+    }
+    if (tid == kThreads - 1) sh.at[kSegs] = (int)all;
+    __syncthreads();
+    return bad || all > INT32_MAX ? -1 : (int)all;
+}
+// The segment of a tile on the line.
+__device__ __forceinline__ int find(const Line &sh, int tile) {
+    int lo = 0, hi = kSegs;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (sh.at[m] <= tile)
+            lo = m;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+// Page and row of a key of segment s; false: on no page of the cache (recorded).
+__device__ __forceinline__ bool place(const WeightArgs &a, int s, int key, int64_t &page, int &row) {
+    const int f = s >= a.B, i = s - (f ? a.B : 0);
+    const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+    const int p = __ldg(a.table[f] + (int64_t)i * a.width[f] + pi);
+    page = p;
+    row = key - pi * a.page_size;
+    if (p >= 0 && p < a.n_pages) return true;
+    record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+    return false;
+}
+
+// A row's offset in the exponent, -lse in base 2; -inf (nothing is added) behind the segment's rows and where the row
+// saw no key.
+__device__ __forceinline__ float row_lse(const WeightArgs &a, const Segment &g, int h, int row) {
+    if (row >= g.n * a.G) return -INFINITY;
+    const int t = token_of(a, row);
+    const float x = __ldg(a.lse + (int64_t)(h * a.G + row - t * a.G) * a.T + g.tok0 + t);
+    return x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
+}
+
+// Keys of the segment that a row sees.
+__device__ __forceinline__ int limit_of(const WeightArgs &a, const Segment &g, bool own, int row) {
+    return own && a.causal ? g.len - g.n + token_of(a, row) + 1 : g.len;
+}
+
+// ------------------------------------------------------------ bf16, warp-level products
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int KEYS>
+struct MmaSmem {
+    static constexpr int WK = KEYS / 16, WR = 4 / WK;  // warps along the keys, along the rows
+    static constexpr int RB = 16 * WR < 32 ? 32 : 16 * WR;  // query rows a step
+    static constexpr int LD = D + 8;
+    bf16 k[KEYS][LD];
+    bf16 q[2][RB][LD];
+    float lse[2][RB];
+    float sum[WR][KEYS];
+    Line line;
+};
+
+template <int D, int KEYS>
+__global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs a) {
+    using Smem = MmaSmem<D, KEYS>;
+    constexpr int WK = Smem::WK, WR = Smem::WR, RB = Smem::RB, RW = RB / WR;  // rows a step and warp
+    constexpr int LOG = KEYS == 16 ? 4 : KEYS == 32 ? 5 : 6;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wk = warp % WK, wr = warp / WK;
+    const int S = a.B + a.n_groups;
+    for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)  // (nothing is added where any segment is bad)
+        if (line_up(a, s0, LOG, sm.line) < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+    for (int s0 = 0; s0 < S; s0 += kSegs) {
+        const int tiles = line_up(a, s0, LOG, sm.line);
+        if (tiles < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+        for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.Hkv; u += gridDim.x) {
+            const int tile = (int)(u / a.Hkv), h = (int)(u - (int64_t)tile * a.Hkv);
+            const int i = find(sm.line, tile), s = s0 + i, k0 = (tile - sm.line.at[i]) * KEYS;
+            Segment g;
+            segment(a, s, g);
+            const bool own = s < a.B;
+            const int rows = g.n * a.G;
+            // the first row that sees a key of the tile
+            const int first = own && a.causal ? max(0, k0 - (g.len - g.n)) * a.G : 0;
+            __syncthreads();  // (the last unit's reads)
+            for (int x = tid; x < KEYS * (D / 8); x += kThreads) {
+                const int r = x / (D / 8), c = x % (D / 8) * 8;
+                int64_t page = 0;
+                int row = 0;
+                const bool there = k0 + r < g.len && place(a, s, k0 + r, page, row);
+                cp16(smem_u32(&sm.k[r][c]),
+                     static_cast<const bf16 *>(a.k) + (there ? page * a.page_stride + row * a.token_stride + h * a.head_stride : 0) + c,
+                     there);
+            }
+            auto load_q = [&](int r0, int buf) {
+                for (int x = tid; x < RB * (D / 8); x += kThreads) {
+                    const int r = r0 + x / (D / 8), c = x % (D / 8) * 8;
+                    const bool there = r < rows;
+                    const int t = token_of(a, there ? r : 0);
+                    cp16(smem_u32(&sm.q[buf][x / (D / 8)][c]),
+                         static_cast<const bf16 *>(a.q) + (g.tok0 + t) * a.q_stride + (h * a.G + (there ? r : 0) - t * a.G) * D + c,
+                         there);
+                }
+                for (int x = tid; x < RB; x += kThreads) sm.lse[buf][x] = row_lse(a, g, h, r0 + x);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            load_q(first, 0);
+            float sum[2] = {0.f, 0.f};
+            const int key = k0 + wk * 16 + (lane >> 2);  // and key + 8
+            uint32_t fa[D / 16][4];
+            for (int r0 = first, buf = 0; r0 < rows; r0 += RB, buf ^= 1) {
+                if (r0 + RB < rows) {
+                    load_q(r0 + RB, buf ^ 1);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                } else {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                }
+                __syncthreads();
+                if (r0 == first) {
+                    const uint32_t ka = smem_u32(&sm.k[wk * 16 + (lane & 15)][(lane >> 4) * 8]);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) ldsm4(ka + k * 32, fa[k]);
+                }
+                const bool masked = own && a.causal && g.len - g.n + token_of(a, r0) + 1 < k0 + KEYS;
+#pragma unroll
+                for (int n = 0; n < RW / 16; ++n) {
+                    const int rw = wr * RW + n * 16;
+                    float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint32_t qa = smem_u32(&sm.q[buf][rw + (lane >> 4) * 8 + (lane & 7)][(lane >> 3 & 1) * 8]);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t fb[4];
+                        ldsm4(qa + k * 32, fb);
+                        mma16816(c0, fa[k], fb[0], fb[1]);
+                        mma16816(c1, fa[k], fb[2], fb[3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // columns rw + 2 (lane % 4) + {0, 1, 8, 9}
+                        const int col = rw + 2 * (lane & 3) + (e & 1) + (e >> 1) * 8;
+                        const float off = sm.lse[buf][col];
+                        const float *c = e >> 1 ? c1 : c0;
+                        float p0 = ex2_approx(fmaf(c[e & 1], a.scale_log2, off));
+                        float p1 = ex2_approx(fmaf(c[2 + (e & 1)], a.scale_log2, off));
+                        if (off == -INFINITY) p0 = p1 = 0.f;  // (a padded or empty row adds nothing, whatever the key)
+                        if (masked) {
+                            const int limit = limit_of(a, g, true, r0 + col);
+                            if (key >= limit) p0 = 0.f;
+                            if (key + 8 >= limit) p1 = 0.f;
+                        }
+                        sum[0] += p0;
+                        sum[1] += p1;
+                    }
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+                if ((lane & 3) == 0) sm.sum[wr][wk * 16 + (lane >> 2) + 8 * e] = sum[e];
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+            for (int r = tid; r < KEYS; r += kThreads) {
+                int64_t page;
+                int row;
+                if (k0 + r >= g.len || !place(a, s, k0 + r, page, row)) continue;
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < WR; ++w) x += sm.sum[w][r];
+                a.w[page * a.w_page + row * a.w_token + h * a.w_head] += x;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ fp32 arithmetic: fp32, and bf16 of other head sizes
+constexpr int kSimtKeys = 32, kSimtRows = 32;
+
+struct SimtSmem {
+    float lse[kSimtRows];
+    float sum[8][kSimtKeys];
+    Line line;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs a) {
+    extern __shared__ __align__(128) uint8_t raw[];
+    SimtSmem &sm = *reinterpret_cast<SimtSmem *>(raw);
+    const int ld = a.d + 4;
+    float *sk = reinterpret_cast<float *>(raw + (sizeof(SimtSmem) + 127) / 128 * 128), *sq = sk + kSimtKeys * ld;
+    const int tid = threadIdx.x, kx = tid & 15, ry = tid >> 4;
+    const int S = a.B + a.n_groups;
+    for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)
+        if (line_up(a, s0, 5, sm.line) < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+    auto put4 = [&](float *dst, const E *src, bool there) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) {
+            if (sizeof(E) == 4) {
+                x = *reinterpret_cast<const float4 *>(src);
+            } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(src);
+                const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&y.x));
+                const float2 r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&y.y));
+                x = make_float4(p.x, p.y, r.x, r.y);
+            }
+        }
+        *reinterpret_cast<float4 *>(dst) = x;
+    };
+    const int vec = a.d / 4;
+    for (int s0 = 0; s0 < S; s0 += kSegs) {
+        const int tiles = line_up(a, s0, 5, sm.line);
+        if (tiles < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+        for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.Hkv; u += gridDim.x) {
+            const int tile = (int)(u / a.Hkv), h = (int)(u - (int64_t)tile * a.Hkv);
+            const int i = find(sm.line, tile), s = s0 + i, k0 = (tile - sm.line.at[i]) * kSimtKeys;
+            Segment g;
+            segment(a, s, g);
+            const bool own = s < a.B;
+            const int rows = g.n * a.G;
+            const int first = own && a.causal ? max(0, k0 - (g.len - g.n)) * a.G : 0;
+            __syncthreads();
+            for (int x = tid; x < kSimtKeys * vec; x += kThreads) {
+                const int r = x / vec, c = x % vec * 4;
+                int64_t page = 0;
+                int row = 0;
+                const bool there = k0 + r < g.len && place(a, s, k0 + r, page, row);
+                put4(sk + r * ld + c, static_cast<const E *>(a.k) + page * a.page_stride + row * a.token_stride + h * a.head_stride + c, there);
+            }
+            float sum[2] = {0.f, 0.f};
+            for (int r0 = first; r0 < rows; r0 += kSimtRows) {
+                __syncthreads();
+                for (int x = tid; x < kSimtRows * vec; x += kThreads) {
+                    const int r = r0 + x / vec, c = x % vec * 4, t = token_of(a, min(r, rows - 1));
+                    put4(sq + x / vec * ld + c,
+                         static_cast<const E *>(a.q) + (g.tok0 + t) * a.q_stride + (int64_t)(h * a.G + min(r, rows - 1) - t * a.G) * a.d + c,
+                         r < rows);
+                }
+                if (tid < kSimtRows) sm.lse[tid] = row_lse(a, g, h, r0 + tid);
+                __syncthreads();
+                float acc[2][4] = {};
+                for (int c = 0; c < a.d; c += 4) {
+                    float4 k[2], q[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) k[e] = *reinterpret_cast<const float4 *>(sk + (kx + 16 * e) * ld + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q[e] = *reinterpret_cast<const float4 *>(sq + (ry + 8 * e) * ld + c);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            acc[e][f] += k[e].x * q[f].x + k[e].y * q[f].y + k[e].z * q[f].z + k[e].w * q[f].w;
+                }
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int row = ry + 8 * f;
+                    const float off = sm.lse[row];
+                    if (off == -INFINITY) continue;
+                    const int limit = limit_of(a, g, own, r0 + row);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (k0 + kx + 16 * e < limit) sum[e] += exp2f(fmaf(acc[e][f], a.scale_log2, off));
+                }
+            }
+            sm.sum[ry][kx] = sum[0];
+            sm.sum[ry][kx + 16] = sum[1];
+            __syncthreads();
+            if (tid < kSimtKeys) {
+                int64_t page;
+                int row;
+                if (k0 + tid < g.len && place(a, s, k0 + tid, page, row)) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) x += sm.sum[w][tid];
+                    a.w[page * a.w_page + row * a.w_token + h * a.w_head] += x;
+                }
+            }
+        }
+    }
+}
+
+template <int D, int KEYS>
+cudaError_t mma_launch(const WeightArgs &a, cudaStream_t st) {
+    static LaunchFit fit;
+    auto kernel = weights_mma_kernel<D, KEYS>;
+    int ctas = 0;
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, sizeof(MmaSmem<D, KEYS>), &ctas);
+    if (e != cudaSuccess) return e;
+    kernel<<<paged_sms() * ctas, kThreads, sizeof(MmaSmem<D, KEYS>), st>>>(a);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t mma_keys(const WeightArgs &a, int keys, cudaStream_t st) {
+    return keys == 16 ? mma_launch<D, 16>(a, st) : keys == 32 ? mma_launch<D, 32>(a, st) : mma_launch<D, 64>(a, st);
+}
+
+}  // namespace
+
+bool weights_mma_supported(int dtype, int d) { return dtype == RA_BF16 && (d == 64 || d == 128); }
+cudaError_t launch_weights_mma(const WeightArgs &a, int keys, cudaStream_t st) {
+    return a.d == 64 ? mma_keys<64>(a, keys, st) : mma_keys<128>(a, keys, st);
+}
+cudaError_t launch_weights_simt(const WeightArgs &a, cudaStream_t st) {
+    static LaunchFit fit[2];
+    const bool f = a.dtype == RA_FP32;
+    const void *kernel = f ? reinterpret_cast<const void *>(weights_simt_kernel<float>) : reinterpret_cast<const void *>(weights_simt_kernel<bf16>);
+    const size_t fixed = (sizeof(SimtSmem) + 127) / 128 * 128;
+    int ctas = 0;  // (of the largest heads)
+    const cudaError_t e = fit[f].prepare(kernel, kThreads, fixed + (kSimtKeys + kSimtRows) * (256 + 4) * 4, &ctas);
+    if (e != cudaSuccess) return e;
+    const size_t smem = fixed + (size_t)(kSimtKeys + kSimtRows) * (a.d + 4) * 4;
+    if (f)
+        weights_simt_kernel<float><<<paged_sms() * ctas, kThreads, smem, st>>>(a);
+    else
+        weights_simt_kernel<bf16><<<paged_sms() * ctas, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

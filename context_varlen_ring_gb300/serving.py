@@ -4,7 +4,9 @@ What stands before and after the packed attention in a model: `rope_fwd` /
 `rope_bwd` turn queries and keys (and their gradients) ahead of and behind
 `ring_attn_fwd` / `ring_attn_bwd`; `kv_cache_append` writes new keys and values
 into a paged cache, rotated on the way; `paged_attn_fwd` attends over that
-cache, reading a prefix that a batch shares for all of it together.  The checks
+cache, reading a prefix that a batch shares for all of it together;
+`paged_attn_key_weights` adds up the attention weight that each cached key
+gathers, and `kv_cache_evict` holds the cache to a budget by it.  The checks
 and the calls into include/ra.h are in csrc/py_serving.cpp.
 """
 from __future__ import annotations
@@ -18,7 +20,7 @@ import torch
 from ._lib import lib
 
 __all__ = ["rope_inv_freq", "rope_axes", "rope_fwd", "rope_bwd", "kv_cache_append", "paged_attn_fwd",
-           "paged_attn_workspace_bytes"]
+           "paged_attn_workspace_bytes", "paged_attn_key_weights", "kv_cache_evict"]
 
 _mod = None
 
@@ -109,3 +111,31 @@ def paged_attn_fwd(q, k_cache, v_cache, page_table, cu_seqlens_q, kv_lens, prefi
     a partial for lse_merge.  Rows behind cu_seqlens_q[-1] are not written."""
     return _native().attn(q, k_cache, v_cache, page_table, cu_seqlens_q, kv_lens, prefix_table, prefix_lens,
                           prefix_groups, causal, scale, max_q_len, out, lse, out_dtype, workspace)
+
+
+def paged_attn_key_weights(q, k_cache, page_table, cu_seqlens_q, kv_lens, lse, weights, prefix_table=None,
+                           prefix_lens=None, prefix_groups=None, causal: bool = True, scale: float | None = None,
+                           max_q_len: int | None = None):
+    """Adds to weights (fp32 [pages, page_size, Hkv], any strides; heads outside
+    the rows are the fastest to read) the attention weight that each cached key
+    gathers from the new tokens: the sum of exp(scale q.k - lse) over the tokens
+    that see it and the query heads of its KV head.  Arguments as in the
+    paged_attn_fwd call that gave lse (fp32 [Hq, T]); with a part of its rows,
+    the weights that those give.  Two sequences must not share a page but through
+    a prefix.  Returns weights.  Capturable."""
+    return _native().key_weights(q, k_cache, page_table, cu_seqlens_q, kv_lens, lse, weights, prefix_table,
+                                 prefix_lens, prefix_groups, causal, scale, max_q_len)
+
+
+def kv_cache_evict(k_cache, v_cache, weights, page_table, kv_lens, keep: int, keep_lens=None, sinks: int = 0,
+                   recent: int = 0, per_head: bool = True, out_table=None, new_lens=None, kept=None):
+    """Holds each cached sequence to keep keys (keep_lens int32 [B] on the
+    device: fewer for some): the first sinks, the last recent, and the heaviest of
+    the rest by weights, in their order (ties: the first).  per_head: every KV
+    head by its own weights, else all by the heads' sum.  The kept rows of K, V
+    and weights move to the front of the sequence's pages, or are copied into
+    those of out_table [B, width], which the call's page_table must not use.
+    Returns (new_lens int32 [B], kept int32 [B, Hkv or 1, keep]: the indexes that
+    stayed, then -1).  Capturable."""
+    return _native().evict(k_cache, v_cache, weights, page_table, kv_lens, keep, keep_lens, sinks, recent, per_head,
+                           out_table, new_lens, kept)

@@ -495,6 +495,84 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
                             int max_q_len, float scale, void *out, int out_dtype, float *lse,
                             void *workspace, size_t ws_bytes, void *stream);
 
+/* Weights of the cache's keys (DEVICE, fp32): page p, row r, head h at w +
+ * p * page_stride + r * token_stride + h * head_stride, for the pages, rows
+ * and heads of a ra_paged_kv. */
+typedef struct ra_paged_weights {
+    float *w;
+    int64_t page_stride, token_stride, head_stride;
+} ra_paged_weights;
+
+/* ------------------------------------------------------------------------
+ * ra_paged_attn_key_weights  (DEVICE tensors and DEVICE segment arrays)
+ *
+ * The attention weight that each cached key gathers from a batch's new tokens,
+ * added to `weights`: what ra_kv_cache_evict goes by.  With q, cache, tables,
+ * lengths, groups, causal and scale of a ra_paged_attn_fwd call and the lse
+ * that it wrote, for every key of KV head h that sequence b's tokens see,
+ *   w += sum over the tokens t that see it and the query heads of h
+ *        of exp(scale q.k - lse[head][t]),
+ * its own keys and the prefix of its group (for all of the group's sequences
+ * together).  Query rows that are left out (a later call with a part of the
+ * rows: cu_seqlens_q, q and lse of those) add nothing, so the weights of the
+ * last tokens alone can be gathered as well.  cache->v is not used.
+ *   lse DEVICE fp32 [Hq, T]; a row with lse = -inf saw nothing and adds nothing
+ * Each weight is added to once, by one thread, and in a fixed order: the same
+ * call gives the same bits.  Two sequences (or groups) of one call must not
+ * name the same page; keys that sequences share belong into a prefix.
+ * Sums are fp32; the products are fp32 in fp32, exact products summed in fp32
+ * in bf16.  Cache rows at or behind a sequence's length may hold anything, and
+ * their weights are not touched; a NaN in a key makes its own weight NaN, one in
+ * a query the weights of all keys that it sees.  Device arrays are checked as
+ * in ra_paged_attn_fwd: a bad boundary or length is recorded as
+ * RA_ERR_DEVICE_BOUNDS and nothing is added; keys on a page outside the cache
+ * are recorded and add nothing.  max_q_len is a hint, as there.  Limits on
+ * shapes, alignment and strides as there.  Capturable; no workspace.  An empty
+ * batch (T = 0) does nothing.
+ * ------------------------------------------------------------------------ */
+ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, int Hq, const ra_paged_kv *cache,
+                                    const ra_paged_weights *weights, const int32_t *page_table, int64_t table_width,
+                                    const int32_t *cu_seqlens_q, const int32_t *kv_lens, int B,
+                                    const int32_t *prefix_table, int64_t prefix_width, const int32_t *prefix_lens,
+                                    const int32_t *prefix_groups, int n_groups, int causal, int max_q_len, float scale,
+                                    const float *lse, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ra_kv_cache_evict  (DEVICE tensors and DEVICE segment arrays)
+ *
+ * Holds B cached sequences to a budget.  Of the n = kv_lens[b] keys of a
+ * sequence with more than keep_b stay the first `sinks`, the last `recent` and,
+ * of those between, the ones of the largest weight (ties: the lowest index;
+ * NaN below all else), keep_b in all and in their order; a sequence of at most
+ * keep_b keys keeps them.  With per_head every KV head chooses by its own
+ * weights (row r of the cache then holds the r-th kept key of each head, of
+ * other tokens perhaps: keys carry their positions, so attention over the cache
+ * goes on as before); without it all heads keep the same tokens, by the sum of
+ * the heads' weights (fp32, in the heads' order).
+ *   keep: the most keys that a sequence may keep, >= 1; keep_lens DEVICE int32
+ *      [B] or NULL: keep_b, taken into [0, keep] (NULL: keep).  A keep_b below
+ *      sinks + recent keeps the sinks first.
+ *   kept DEVICE int32 [B, Hkv or 1, keep] out: the logical indexes that stay,
+ *      increasing, then -1;  new_lens DEVICE int32 [B] out: min(n, keep_b)
+ *      (not kv_lens itself)
+ *   out_table NULL: the kept rows of K, V and the weights move to the front of
+ *      their own sequence's pages; what lies behind new_lens[b] is what was
+ *      there before.  Else DEVICE int32 [B, out_width]: they are copied to the
+ *      front of the sequence in those pages, which no page_table of the call
+ *      may use, and page_table's pages stay as they are.
+ * Two sequences must not name the same page when rows move in place, nor two
+ * sequences' out_tables.  A length outside [0, width * page_size] or above 2^30
+ * is recorded as RA_ERR_DEVICE_BOUNDS and taken as 0 keys; a key on a page
+ * outside the cache is recorded, weighs least, and its row is not moved.
+ * A copy: the rows' bits do not change.  d of whole 16 bytes, d <= 256; the
+ * cache 16-byte aligned with strides of whole 16 bytes.  Capturable; no
+ * workspace.  B = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *weights, const int32_t *page_table,
+                            int64_t table_width, const int32_t *kv_lens, int B, int keep, const int32_t *keep_lens,
+                            int sinks, int recent, int per_head, const int32_t *out_table, int64_t out_width,
+                            int32_t *new_lens, int32_t *kept, void *stream);
+
 /* ------------------------------------------------------------------------
  * ra_delta_rule_fwd / ra_delta_rule_bwd / ra_delta_rule_step  (DEVICE tensors
  * and DEVICE segment arrays)
