@@ -268,6 +268,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictAr
         }
         __syncthreads();
     }
+    // keys that are appended behind the kept ones begin without a weight
+    const int n = a.kv_lens[b];
+    if (which || col || n > a.most) return;
+    for (int i = left + tid; i < n; i += kMoveThreads) {
+        int64_t page;
+        int row;
+        if (place(a, a.table, a.width, b, i, page, row)) a.w[page * a.w_page + row * a.w_token + h * a.w_head] = 0.f;
+    }
 }
 
 }  // namespace

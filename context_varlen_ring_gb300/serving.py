@@ -121,8 +121,8 @@ def paged_attn_key_weights(q, k_cache, page_table, cu_seqlens_q, kv_lens, lse, w
     gathers from the new tokens: the sum of exp(scale q.k - lse) over the tokens
     that see it and the query heads of its KV head.  Arguments as in the
     paged_attn_fwd call that gave lse (fp32 [Hq, T]); with a part of its rows,
-    the weights that those give.  Two sequences must not share a page but through
-    a prefix.  Returns weights.  Capturable."""
+    the weights that those give.  Weights begin at 0.  Two sequences must not
+    share a page but through a prefix.  Returns weights.  Capturable."""
     return _native().key_weights(q, k_cache, page_table, cu_seqlens_q, kv_lens, lse, weights, prefix_table,
                                  prefix_lens, prefix_groups, causal, scale, max_q_len)
 
@@ -133,8 +133,9 @@ def kv_cache_evict(k_cache, v_cache, weights, page_table, kv_lens, keep: int, ke
     device: fewer for some): the first sinks, the last recent, and the heaviest of
     the rest by weights, in their order (ties: the first).  per_head: every KV
     head by its own weights, else all by the heads' sum.  The kept rows of K, V
-    and weights move to the front of the sequence's pages, or are copied into
-    those of out_table [B, width], which the call's page_table must not use.
+    and weights move to the front of the sequence's pages (the weights behind
+    them become 0, for keys appended there), or are copied into the pages of
+    out_table [B, width], which the call's page_table must not use.
     Returns (new_lens int32 [B], kept int32 [B, Hkv or 1, keep]: the indexes that
     stayed, then -1).  Capturable."""
     return _native().evict(k_cache, v_cache, weights, page_table, kv_lens, keep, keep_lens, sinks, recent, per_head,

@@ -513,9 +513,11 @@ typedef struct ra_paged_weights {
  *   w += sum over the tokens t that see it and the query heads of h
  *        of exp(scale q.k - lse[head][t]),
  * its own keys and the prefix of its group (for all of the group's sequences
- * together).  Query rows that are left out (a later call with a part of the
- * rows: cu_seqlens_q, q and lse of those) add nothing, so the weights of the
- * last tokens alone can be gathered as well.  cache->v is not used.
+ * together).  A new key's weight is to be 0 ahead of its first call: pages
+ * begin with 0, and ra_kv_cache_evict leaves 0 behind what it keeps in place.
+ * Query rows that are left out (a call with a part of the rows: cu_seqlens_q,
+ * q and lse of those) add nothing, so the weights of the last tokens alone can
+ * be gathered as well.  cache->v is not used.
  *   lse DEVICE fp32 [Hq, T]; a row with lse = -inf saw nothing and adds nothing
  * Each weight is added to once, by one thread, and in a fixed order: the same
  * call gives the same bits.  Two sequences (or groups) of one call must not
@@ -556,10 +558,13 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
  *      increasing, then -1;  new_lens DEVICE int32 [B] out: min(n, keep_b)
  *      (not kv_lens itself)
  *   out_table NULL: the kept rows of K, V and the weights move to the front of
- *      their own sequence's pages; what lies behind new_lens[b] is what was
- *      there before.  Else DEVICE int32 [B, out_width]: they are copied to the
- *      front of the sequence in those pages, which no page_table of the call
- *      may use, and page_table's pages stay as they are.
+ *      their own sequence's pages; behind new_lens[b] K and V are what they
+ *      were, and the weights up to n become 0, so that keys appended there
+ *      begin without any.  Else DEVICE int32 [B, out_width]: they are copied to
+ *      the front of the sequence in those pages, which no page_table of the
+ *      call may use; nothing else of those pages, and nothing of page_table's,
+ *      is written (a page that a sequence is given is to be handed out with
+ *      weights of 0).
  * Two sequences must not name the same page when rows move in place, nor two
  * sequences' out_tables.  A length outside [0, width * page_size] or above 2^30
  * is recorded as RA_ERR_DEVICE_BOUNDS and taken as 0 keys; a key on a page
