@@ -99,31 +99,42 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArg
 }
 
 // ------------------------------------------------------------ T and P
+// Bound: what it writes, 16 KB a chunk and head for each part.  Measured (8192 chunks of 64, 16 heads' worth, two
+// parts): see launch_delta_local.  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a lane a column;
+// then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
 constexpr int kLocalThreads = 128;
-constexpr int kLdf = C + 1;
+constexpr int kLdy = 40;
 
 template <typename E, int NP, int DK>
 struct LocalSmem {
     static constexpr int NPI = std::is_same<E, float>::value ? 3 : 1, LD = DK + 8;
-    bf16 k[NPI][C][LD], q[NPI][C][LD];
-    float A[C][kLdf], T[C][kLdf], Y[32][33];
+    struct Rows {
+        bf16 k[NPI][C][LD], q[NPI][C][LD];
+    };
+    union {
+        Rows in;
+        bf16 P[NP][C][kLdc];  // (when the products are done)
+    };
+    bf16 A[NP][C][kLdc], T[NP][C][kLdc];
+    bf16 Y[NP][32][kLdy];
+    float diag[4][16][17];
     Gates g;
 };
 
 template <typename E, int NP, int DK>
 __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaArgs a) {
     using Smem = LocalSmem<E, NP, DK>;
-    constexpr int NPI = Smem::NPI, LD = Smem::LD, PL = C * LD * 2;
+    constexpr int NPI = Smem::NPI, LD = Smem::LD, PL = C * LD * 2, PT = C * kLdc * 2, PY = 32 * kLdy * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
-    const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5;
+    const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (c >= a.hdr->chunks) return;
     const DeltaChunk ch = a.chunk[c];
     const int hk = h / (a.Hv / a.Hk);
     const E *k = static_cast<const E *>(a.k) + ch.tok0 * a.k_stride + hk * DK;
     const E *q = static_cast<const E *>(a.q) + ch.tok0 * a.q_stride + hk * DK;
-    load_rows<E, DK, kLocalThreads>(&sm.k[0][0][0], LD, C * LD, k, a.k_stride, ch.n);
-    load_rows<E, DK, kLocalThreads>(&sm.q[0][0][0], LD, C * LD, q, a.q_stride, ch.n);
+    load_rows<E, DK, kLocalThreads>(&sm.in.k[0][0][0], LD, C * LD, k, a.k_stride, ch.n);
+    load_rows<E, DK, kLocalThreads>(&sm.in.q[0][0][0], LD, C * LD, q, a.q_stride, ch.n);
     cp_commit();
     if (warp == 0) {
         float g[2], b[2];
@@ -133,71 +144,95 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     cp_wait<0>();
     __syncthreads();
     // rows 16 warp .. of K K^T and Q K^T, up to the diagonal
-    const uint32_t kb = smem_u32(sm.k), row = 16 * warp * LD * 2;
-    uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
-    for (int which = 0; which < 2; ++which) {
-        float acc[8][4];
-        zero(acc);
-        mm<8, NPI, NPI, 3, false, false>(acc, (which ? smem_u32(sm.q) : kb) + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
-        bf16 *P = reinterpret_cast<bf16 *>(tp + NP * C * C);
+    const int row0 = 16 * warp;
+    const uint32_t kb = smem_u32(sm.in.k), row = row0 * LD * 2;
+    float kk[8][4], qk[8][4];
+    zero(kk);
+    zero(qk);
+    mm<8, NPI, NPI, 3, false, false>(kk, kb + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
+    mm<8, NPI, NPI, 3, false, false>(qk, smem_u32(sm.in.q) + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
+    __syncthreads();  // (P takes the place of K and Q)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int i = 16 * warp + acc_row(hf), j = acc_col(n);
-                float x = 0.f, y = 0.f;
-                if (j <= i) x = acc[n][2 * hf] * decay(sm.g, i, j);
-                if (j + 1 <= i) y = acc[n][2 * hf + 1] * decay(sm.g, i, j + 1);
-                if (which) {
-                    put2<NP>(P + i * C + j, C * C, x * a.scale, y * a.scale);
-                } else {
-                    sm.A[i][j] = j < i ? x * sm.g.beta[i] : 0.f;
-                    sm.A[i][j + 1] = j + 1 < i ? y * sm.g.beta[i] : 0.f;
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = row0 + acc_row(hf), j = acc_col(n);
+            float x[2] = {0.f, 0.f}, p[2] = {0.f, 0.f};
+            if (n / 2 <= warp) {
+                const float b = sm.g.beta[i];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (j + e <= i) {
+                        const float D = decay(sm.g, i, j + e);
+                        p[e] = a.scale * D * qk[n][2 * hf + e];
+                        if (j + e < i) x[e] = b * D * kk[n][2 * hf + e];
+                    }
+                put2<NP>(&sm.A[0][i][j], C * kLdc, x[0], x[1]);
+                if (n / 2 == warp) {
+                    sm.diag[warp][i & 15][j & 15] = x[0];
+                    sm.diag[warp][i & 15][(j & 15) + 1] = x[1];
                 }
+            } else {
+                put2<NP>(&sm.T[0][i][j], C * kLdc, 0.f, 0.f);
             }
-    }
-    __syncthreads();
-    // T = (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a
-    // thread a column, then [T11, 0; -T22 A21 T11, T22] for blocks of 32 and 64
-    if (tid < C) {
-        const int b = tid & ~15, j = tid & 15;
+            put2<NP>(&sm.P[0][i][j], C * kLdc, p[0], p[1]);
+        }
+    __syncwarp();
+    if (lane < 16) {
         float t[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float x = i == j ? 1.f : 0.f;
+            float x = i == lane ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) x -= sm.A[b + i][b + m] * t[m];
+            for (int m = 0; m < i; ++m) x -= sm.diag[warp][i][m] * t[m];
             t[i] = x;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sm.T[b + i][b + j] = i >= j ? t[i] : 0.f;
+        for (int i = 0; i < 16; ++i) {
+            float x = t[i];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const bf16 b = __float2bfloat16_rn(x);
+                sm.T[p][row0 + i][row0 + lane] = b;
+                x -= __bfloat162float(b);
+            }
+        }
     }
-    // (the blocks above the diagonal)
-    for (int i = tid; i < C * C; i += kLocalThreads)
-        if ((i >> 6) / 16 < (i & 63) / 16) sm.T[i >> 6][i & 63] = 0.f;
     __syncthreads();
-    for (int w = 16; w < C; w *= 2) {  // two blocks of 16, one of 32
-        const int blocks = C / (2 * w);
-        for (int i = tid; i < blocks * w * w; i += kLocalThreads) {
-            const int b = i / (w * w) * 2 * w, x = i / w % w, y = i % w;
-            float s = 0.f;
-            for (int m = y; m < w; ++m) s += sm.A[b + w + x][b + m] * sm.T[b + m][b + y];
-            sm.Y[(b / (2 * w)) * 16 + x][y] = s;
-        }
-        __syncthreads();
-        for (int i = tid; i < blocks * w * w; i += kLocalThreads) {
-            const int b = i / (w * w) * 2 * w, x = i / w % w, y = i % w;
-            float s = 0.f;
-            for (int m = 0; m <= x; ++m) s += sm.T[b + w + x][b + w + m] * sm.Y[(b / (2 * w)) * 16 + m][y];
-            sm.T[b + w + x][b + y] = -s;
-        }
-        __syncthreads();
+    uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
+    const uint32_t Ab = smem_u32(sm.A), Tb = smem_u32(sm.T), Yb = smem_u32(sm.Y);
+    auto tile = [&](uint32_t b, int r, int col) { return b + (r * kLdc + col) * 2; };
+    auto put = [&](bf16 *dst, int ld, int plane, const float (&x)[2][4], float sign) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                put2<NP>(dst + acc_row(hf) * ld + acc_col(n), plane, sign * x[n][2 * hf], sign * x[n][2 * hf + 1]);
+    };
+    float y[2][4];
+    if (warp & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
+        zero(y);
+        mm<2, NP, NP, NP, false, true>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
+        put(&sm.Y[0][(warp >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
+        __syncwarp();
+        zero(y);
+        mm<2, NP, NP, NP, false, true>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (warp >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
+        put(&sm.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
     }
-    bf16 *T = reinterpret_cast<bf16 *>(tp);
-    for (int i = tid; i < C * C / 2; i += kLocalThreads) {
-        const int x = i / (C / 2), y = i % (C / 2) * 2;
-        put2<NP>(T + x * C + y, C * C, sm.T[x][y], sm.T[x][y + 1]);
+    __syncthreads();
+    {  // rows 32 .. 63 by columns 0 .. 31: a block of 16 x 16 each warp
+        const int r = (warp >> 1) * 16, col = (warp & 1) * 16;
+        zero(y);
+        mm<2, NP, NP, NP, false, true>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
+        put(&sm.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
+        store_square<NP, kLocalThreads>(tp + NP * C * C, &sm.P[0][0][0]);
+        __syncthreads();
+        zero(y);
+        mm<2, NP, NP, NP, false, true>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
+        put(&sm.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
     }
+    __syncthreads();
+    store_square<NP, kLocalThreads>(tp, &sm.T[0][0][0]);
 }
 
 // ------------------------------------------------------------ the walk

@@ -154,18 +154,25 @@ __device__ __forceinline__ void load_rows(bf16 *dst, int ld, int plane, const E 
         }
     }
 }
-// T or P (parts of [64][64], one behind another) into parts of pitch kLdc; not committed.
+// T and P lie in the workspace as tiles that a bulk copy can take to shared memory: a part after another, rows of 128
+// bytes whose 16-byte pieces are exchanged by the row's low bits (the 128-byte swizzle of the tensor cores' operands).
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * C + ((piece ^ (row & 7)) << 3); }
+// Such a tile into parts of pitch kLdc; not committed.
 template <int NP, int THREADS>
 __device__ __forceinline__ void load_square(bf16 *dst, const uint16_t *src) {
     for (int i = threadIdx.x; i < NP * C * 8; i += THREADS) {
-        const int row = i >> 3, c = (i & 7) * 8;  // (parts one behind another on both sides)
-        cp16z(smem_u32(dst + row * kLdc + c), src + row * C + c, true);
+        const int row = i >> 3, c = i & 7;  // (parts one behind another on both sides: whole groups of 8 rows)
+        cp16z(smem_u32(dst + row * kLdc + c * 8), src + swizzled(row, c), true);
     }
 }
-__device__ __forceinline__ const uint16_t *square_of(const DeltaArgs &a, int64_t ch, int which, int parts) {
-    return a.tp + (ch * 2 + which) * parts * C * C;
+// And back, from parts of pitch kLdc.
+template <int NP, int THREADS>
+__device__ __forceinline__ void store_square(uint16_t *dst, const bf16 *src) {
+    for (int i = threadIdx.x; i < NP * C * 8; i += THREADS) {
+        const int row = i >> 3, c = i & 7;
+        *reinterpret_cast<uint4 *>(dst + swizzled(row, c)) = *reinterpret_cast<const uint4 *>(src + row * kLdc + c * 8);
+    }
 }
-
 // A chunk's gates.  G_i is the sum of its first i + 1 log decays; kept as the
 // sum of two floats, because the products use exp(G_i - G_j), whose exponent
 // would otherwise lose the bits that a strong decay ahead of both pushes out.
