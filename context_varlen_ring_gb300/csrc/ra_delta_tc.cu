@@ -1,0 +1,472 @@
+// ra_delta_tc.cu -- the gated delta rule's walk along a sequence's chunks on
+// the 5th-generation tensor cores (bf16, heads of 128): the formulas are in
+// ra_delta.cu, T and P come from its first kernel.
+//
+// Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
+// the output Q S0 and P u) follow one another, and the next chunk needs their
+// result; a batch's longest sequence is a chain of hundreds of them.  So a CTA
+// has one head of one sequence, with the whole state, and everything is held
+// the other way round (a column of v to a TMEM lane): the state is the A operand
+// of the first product straight from TMEM, its tokens' values the A operand of
+// the next, K, Q, T and P the B operands from shared memory as they come by TMA
+// and bulk copies, and no result is transposed or passes through shared memory.
+//  * warp 0 loads, warp 1 issues products, warp 3 makes the gates; two
+//    warpgroups, a thread a lane and half of the columns each, hold the state
+//    in registers (fp32), make bf16 parts of what the next product reads and
+//    put them into TMEM.
+//  * the output's products run behind those that the chain needs, and are read
+//    while the next chunk's first ones run.
+// TMEM columns: 0 the state's growth (and, ahead of it, R's parts); 128 K S0,
+// then u; 192 Q S0; 256 the state's parts, then e^(G_63 - G) u's; 448 P u; u's
+// parts behind the state's, or (of three) in their place.
+// Every wait is bounded as in the rest of the library.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cstring>
+#include <mutex>
+
+#include "ra_delta.cuh"
+#include "ra_internal.h"
+#include "ra_serve.cuh"
+
+namespace ra {
+namespace {
+
+using namespace delta;
+
+constexpr int kThreads = 384;
+constexpr int kD = 128;                   // dk = dv
+constexpr int kStages = 2;
+constexpr uint32_t kHalf = 16384;         // 64 rows of K, 64 of Q, 128 bytes each (half of dk)
+constexpr uint32_t kSquare = 8192;        // a part of T or P
+constexpr uint32_t kValues = C * kD * 2;  // [64][128] of v
+
+template <int NP>
+struct Shape {
+    static constexpr uint32_t oTP = 2 * kHalf, oV = oTP + 2 * NP * kSquare, stage = oV + kValues;
+    static constexpr uint32_t oBar = kStages * stage, smem = oBar + 256 + 1024;
+};
+constexpr int kColD = 0, kColX = 128, kColQ = 192, kColS = 256, kColP = 448;
+// u's parts: with two there is room for them; with three they follow e^(G_63 - G) u's over the state's, which are
+// written again only when the output's products are done.
+template <int NP>
+constexpr int kColU = NP == 2 ? kColS + 64 * NP : kColS + 32 * NP;
+
+struct ScanParams {
+    CUtensorMap tmQ, tmK, tmV;
+    DeltaArgs a;
+    int keep;
+    unsigned long long budget_ns;
+};
+
+// 2 n floats into bf16 pairs, and what that leaves of them.
+template <int N>
+__device__ __forceinline__ void part(float (&x)[2 * N], uint32_t (&h)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        x[2 * i] -= __uint_as_float(h[i] << 16);
+        x[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+    }
+}
+// 32 values as NP parts of 16 columns, `apart` columns from each other.
+template <int NP>
+__device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float (&x)[32]) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        uint32_t h[16];
+        part<16>(x, h);
+        tmem_st16(tmem + p * apart, h);
+    }
+}
+
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
+    using Sh = Shape<NP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Gates gates[2];
+    const DeltaArgs &a = p.a;
+    if (a.hdr->bad) return;
+    const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
+    uint64_t *full = bars + 0;      // [2] a chunk's rows landed
+    uint64_t *empty = bars + 2;     // [2] its products are done, its values read
+    uint64_t *g_full = bars + 4;    // [2] its gates
+    uint64_t *g_empty = bars + 6;   // [2]
+    uint64_t *s_ready = bars + 8;   // the state's parts are in TMEM
+    uint64_t *x_full = bars + 9;    // K S0 is there
+    uint64_t *r_ready = bars + 10;  // R's parts
+    uint64_t *u_full = bars + 11;   // u is there
+    uint64_t *u_ready = bars + 12;  // u's parts
+    uint64_t *d_full = bars + 13;   // the state's growth is there
+    uint64_t *o_full = bars + 14;   // the output is there
+    uint64_t *o_empty = bars + 15;  // and read
+    uint64_t *mma_done = bars + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 18);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = a.order[blockIdx.x / a.Hv], h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0;
+    const bool want = a.out != nullptr, keep = p.keep != 0;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1 + 8);
+            mbar_init(g_full + i, 1);
+            mbar_init(g_empty + i, 8);
+        }
+        mbar_init(s_ready, 256);
+        mbar_init(x_full, 1);
+        mbar_init(r_ready, 256);
+        mbar_init(u_full, 1);
+        mbar_init(u_ready, 256);
+        mbar_init(d_full, 1);
+        mbar_init(o_full, 1);
+        mbar_init(o_empty, 256);
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tmQ);
+        tma_prefetch_desc(&p.tmK);
+        tma_prefetch_desc(&p.tmV);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl wc{abort_flag, a.status, p.budget_ns};
+
+    // Registers: 128 x 80 + 256 x 200 = 61440, within the 384 x 168 = 64512 of the launch.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+        if (warp == 0) {
+            // -------------------------------------------- loads
+            if (lane == 0) {
+                int i = 0;
+                for (bool ok = true; i < n_chunks; ++i) {
+                    const int s = i & 1;
+                    const int64_t c = c0 + i;
+                    const int tok = a.chunk[c].tok0;
+                    uint8_t *st = base + s * Sh::stage;
+                    ok = mbar_wait(empty + s, ((i >> 1) & 1u) ^ 1u, wc);
+                    if (!ok) break;
+                    const uint32_t squares = (want ? 2 : 1) * NP * kSquare;
+                    mbar_arrive_expect_tx(full + s, (want ? 4 : 2) * (kHalf / 2) + squares + kValues);
+                    for (int d = 0; d < 2; ++d) tma_load_3d(st + d * kHalf, &p.tmK, full + s, d * 64, hk, tok);
+                    tma_load_3d(st + Sh::oV, &p.tmV, full + s, 0, h, tok);
+                    bulk_load(st + Sh::oTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, squares, full + s);
+                    if (want)
+                        for (int d = 0; d < 2; ++d)
+                            tma_load_3d(st + d * kHalf + kHalf / 2, &p.tmQ, full + s, d * 64, hk, tok);
+                }
+                // the last copies must have landed before the CTA may exit
+                volatile int local_abort = 0;
+                const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) (void)mbar_wait(full + (j & 1), (j >> 1) & 1u, drain);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------- products
+            const uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0), id128 = idesc_bf16_f32(128, 128, 0, 1);
+            bool ok = true;
+            for (int i = 0; i < n_chunks && ok; ++i) {
+                const int s = i & 1;
+                const uint32_t st = base_s + s * Sh::stage, ph = i & 1u;
+                const uint64_t dK = sdesc_sw128(st, 16, 1024), dQ = sdesc_sw128(st + kHalf / 2, 16, 1024);
+                const uint64_t dKn = sdesc_sw128(st, kHalf, 1024);  // columns of dk
+                const uint64_t dT = sdesc_sw128(st + Sh::oTP, 16, 1024), dP = sdesc_sw128(st + Sh::oTP + NP * kSquare, 16, 1024);
+                ok = mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
+                if (!ok) break;
+                const int n = a.chunk[c0 + i].n;
+                if (n < C) {  // rows of K behind the sequence's end are another's, or none
+                    uint8_t *k = base + s * Sh::stage;
+                    for (int x = n * 8 + lane; x < C * 8; x += 32) {
+                        *reinterpret_cast<uint4 *>(k + x * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(k + kHalf + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                // S0 by 64 rows of K or of Q: D [v, token]
+                auto by_state = [&](uint32_t d, uint64_t b) {
+#pragma unroll
+                    for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc_mma_ts_w(tmem + d, tmem + kColS + 64 * q + 8 * ks,
+                                        b + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), id64,
+                                        !(q == NP - 1 && ks == 0));
+                };
+                // parts [v, token] by parts of T or P
+                auto by_square = [&](uint32_t d, uint32_t x, uint64_t b, bool more) {
+#pragma unroll
+                    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                        for (int q = 0; q <= o; ++q)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) {
+                                tc_mma_ts_w(tmem + d, tmem + x + 32 * q + 8 * ks, b + (((o - q) * kSquare + ks * 32u) >> 4), id64,
+                                            more);
+                                more = true;
+                            }
+                };
+                ok = mbar_wait_warp(s_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+                by_state(kColX, dK);
+                tc_commit_w(x_full);
+                if (want) {
+                    if (i > 0) {
+                        ok = mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    by_state(kColQ, dQ);
+                }
+                ok = mbar_wait_warp(r_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+                by_square(kColX, kColD, dT, false);
+                tc_commit_w(u_full);
+                ok = mbar_wait_warp(u_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc_mma_ts_w(tmem + kColD, tmem + kColS + 32 * q + 8 * ks, dKn + ((uint32_t)ks * 2048u >> 4), id128,
+                                    !(q == NP - 1 && ks == 0));
+                tc_commit_w(d_full);
+                if (want) {
+                    by_square(kColP, kColU<NP>, dP, false);
+                    tc_commit_w(o_full);
+                }
+                tc_commit_w(empty + s);
+            }
+            // every product issued must have completed before TMEM is released
+            tc_commit_w(mma_done);
+            volatile int local_abort = 0;
+            const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+            (void)mbar_wait_warp(mma_done, 0, drain);
+        } else if (warp == 3) {
+            // -------------------------------------------- gates
+            float g[2], b[2];
+            if (n_chunks > 0) gates_load(a, a.chunk[c0], h, g, b);
+            for (int i = 0; i < n_chunks; ++i) {
+                if (!mbar_wait_warp(g_empty + (i & 1), ((i >> 1) & 1u) ^ 1u, wc)) break;
+                gates_put(gates[i & 1], g, b);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_full + (i & 1));
+                if (i + 1 < n_chunks) gates_load(a, a.chunk[c0 + i + 1], h, g, b);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+        // ------------------------------------------------ the state, and what the products read
+        const int half = warp >= 8 ? 1 : 0, m = (warp & 3) * 32 + lane;  // TMEM lane: the column of v
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int64_t slot = a.state || a.state_out ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
+        const int64_t place = ((slot * a.Hv + h) * kD + 64 * half) * kD + m;
+        float S[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) S[j] = a.state && slot >= 0 ? a.state[place + j * kD] : 0.f;
+        bool ok = true;
+        // the output of chunk i: scale e^G (Q S0) + P u
+        auto output = [&](int i, const DeltaChunk &ch) {
+            ok = mbar_wait_warp(o_full, i & 1u, wc);
+            if (!ok) return;
+            tc_fence_after();
+            uint32_t x[32], y[32];
+            tmem_ld32(at + kColQ + 32 * half, x);
+            tmem_ld32(at + kColP + 32 * half, y);
+            tc_fence_before();
+            mbar_arrive(o_empty);
+            const Gates &g = gates[i & 1];
+            bf16 *o = static_cast<bf16 *>(a.out) + ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (32 * half + j < ch.n)
+                    o[(int64_t)j * a.Hv * kD] = __float2bfloat16_rn(
+                        fmaf(a.scale * g.eG[32 * half + j], __uint_as_float(x[j]), __uint_as_float(y[j])));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g_empty + (i & 1));
+        };
+        DeltaChunk ch{0, 0}, last;
+#pragma unroll 1
+        for (int i = 0; i < n_chunks && ok; ++i) {
+            const int s = i & 1;
+            const uint32_t ph = i & 1u;
+            const int64_t cell = (int64_t)(c0 + i) * a.Hv + h;
+            last = ch;
+            ch = a.chunk[c0 + i];
+            if (NP == 3 && want && i > 0) {
+                output(i - 1, last);
+                if (!ok) break;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float x[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = S[32 * q + j];
+                put_parts<NP>(at + kColS + 32 * half + 16 * q, 64, x);
+            }
+            tc_fence_before();
+            mbar_arrive(s_ready);
+            if (keep) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) a.s0[(cell * kD + 64 * half + j) * kD + m] = S[j];
+            }
+            if (NP == 2 && want && i > 0) {
+                output(i - 1, last);
+                if (!ok) break;
+            }
+            ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc) && mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
+            if (!ok) break;
+            const Gates &g = gates[s];
+            float v[32];
+            const bf16 *vp = reinterpret_cast<const bf16 *>(base + s * Sh::stage + Sh::oV) + 32 * half * kD + m;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __bfloat162float(vp[j * kD]);
+            ok = mbar_wait_warp(x_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                uint32_t x[32];
+                tmem_ld32(at + kColX + 32 * half, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int t = 32 * half + j;
+                    const float r = fmaf(-g.eG[t], __uint_as_float(x[j]), v[j]);
+                    // (rows of v behind the sequence's end are another's, or none)
+                    v[j] = t < ch.n ? g.beta[t] * r : 0.f;
+                    if (keep) a.r[(cell * C + t) * kD + m] = t < ch.n ? r : 0.f;
+                }
+            }
+            put_parts<NP>(at + kColD + 16 * half, 32, v);
+            tc_fence_before();
+            mbar_arrive(r_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + s);
+            ok = mbar_wait_warp(u_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                uint32_t x[32];
+                float y[32];
+                tmem_ld32(at + kColX + 32 * half, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[j] = __uint_as_float(x[j]);
+                    y[j] = g.eL[32 * half + j] * v[j];
+                    if (keep) a.u[(cell * C + 32 * half + j) * kD + m] = v[j];
+                }
+                put_parts<NP>(at + kColS + 16 * half, 32, y);
+                if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
+            }
+            tc_fence_before();
+            mbar_arrive(u_ready);
+            const float eC = g.eC;
+            if (!want) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_empty + s);
+            }
+            ok = mbar_wait_warp(d_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t x[32];
+                tmem_ld32(at + kColD + 64 * half + 32 * q, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[32 * q + j] = fmaf(eC, S[32 * q + j], __uint_as_float(x[j]));
+            }
+        }
+        if (ok && want && n_chunks > 0) output(n_chunks - 1, ch);
+        if (ok && a.state_out && slot >= 0) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) a.state_out[place + j * kD] = S[j];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// Rows [T][H][128] of bf16, `stride` elements apart, in boxes of 64 tokens of one head: 64 columns wide with the
+// tensor cores' swizzle, or 128 without.
+bool rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t stride, bool swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    if (T == 1) stride = (int64_t)H * kD;  // (a single row has no stride)
+    const cuuint64_t dims[3] = {kD, (cuuint64_t)H, (cuuint64_t)T}, strides[2] = {kD * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {swizzle ? 64u : 128u, 1, C}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NP>
+cudaError_t scan(const ScanParams &p, cudaStream_t st) {
+    static std::atomic<bool> ready[128] = {};
+    auto kernel = delta_tc_scan_kernel<NP>;
+    static_assert(Shape<NP>::smem <= 232448 - 2 * sizeof(Gates), "shared memory of one CTA");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128 || !ready[dev]) {
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NP>::smem);
+        if (e != cudaSuccess) return e;
+        // The register split draws on the 384 x 168 of the launch: with fewer, the increase could never be granted.
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, (const void *)kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 128) ready[dev] = true;
+    }
+    kernel<<<dim3((unsigned)(p.a.N * p.a.Hv)), kThreads, Shape<NP>::smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool delta_tc_supported(const DeltaArgs &a) { return a.dtype == RA_BF16 && a.dk == kD && a.dv == kD && a.T > 0; }
+
+cudaError_t launch_delta_tc_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
+    ScanParams p;
+    memset(&p, 0, sizeof(p));
+    if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
+        !rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false))
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.keep = keep;
+    p.budget_ns = wait_budget_ns();
+    return a.parts == 2 ? scan<2>(p, st) : scan<3>(p, st);
+}
+
+}  // namespace ra
