@@ -177,7 +177,7 @@ __device__ __forceinline__ void store_square(uint16_t *dst, const bf16 *src) {
 // sum of two floats, because the products use exp(G_i - G_j), whose exponent
 // would otherwise lose the bits that a strong decay ahead of both pushes out.
 // Decays below -1e4 are e^-1e4 = 0 all the same, and keep the sums finite.
-struct Gates {
+struct alignas(16) Gates {
     float hi[C], lo[C];
     float beta[C];
     float eG[C];     // exp(G_i): the state ahead of the chunk as token i sees it

@@ -63,26 +63,52 @@ struct ScanParams {
     unsigned long long budget_ns;
 };
 
-// 2 n floats into bf16 pairs, and what that leaves of them.
+// registers -> TMEM: 32 lanes x 16 columns; complete behind tmem_put_wait.
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 columns at each of two places, one wait.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t a0, uint32_t a1, uint32_t (&x)[32], uint32_t (&y)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31]),
+          "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15]), "=r"(y[16]), "=r"(y[17]), "=r"(y[18]), "=r"(y[19]), "=r"(y[20]), "=r"(y[21]), "=r"(y[22]), "=r"(y[23]), "=r"(y[24]), "=r"(y[25]), "=r"(y[26]), "=r"(y[27]), "=r"(y[28]), "=r"(y[29]), "=r"(y[30]), "=r"(y[31])
+        : "r"(a0), "r"(a1)
+        : "memory");
+}
+// 2 N floats into bf16 pairs, and what that leaves of them.
 template <int N>
-__device__ __forceinline__ void part(float (&x)[2 * N], uint32_t (&h)[N]) {
+__device__ __forceinline__ void part(float2 (&x)[N], uint32_t (&h)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        x[2 * i] -= __uint_as_float(h[i] << 16);
-        x[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
+        h[i] = pack_bf16x2(x[i].x, x[i].y);
+        x[i] = add2(x[i], make_float2(__uint_as_float((h[i] << 16) ^ 0x80000000u), __uint_as_float((h[i] & 0xffff0000u) ^ 0x80000000u)));
     }
 }
-// 32 values as NP parts of 16 columns, `apart` columns from each other.
+// 32 values as NP parts of 16 columns, `apart` columns from each other (to be waited for).
 template <int NP>
-__device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float (&x)[32]) {
+__device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float2 (&x)[16]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         uint32_t h[16];
-        part<16>(x, h);
-        tmem_st16(tmem + p * apart, h);
+        if (p + 1 < NP) {
+            part<16>(x, h);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(x[i].x, x[i].y);
+        }
+        tmem_put16(tmem + p * apart, h);
     }
 }
+__device__ __forceinline__ float2 f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 
 template <int NP>
 __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
@@ -277,27 +303,40 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const int64_t slot = a.state || a.state_out ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
         const int64_t place = ((slot * a.Hv + h) * kD + 64 * half) * kD + m;
-        float S[64];
+        float2 S[32];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = a.state && slot >= 0 ? a.state[place + j * kD] : 0.f;
+        for (int j = 0; j < 32; ++j) {
+            const bool there = a.state && slot >= 0;
+            S[j] = make_float2(there ? a.state[place + 2 * j * kD] : 0.f, there ? a.state[place + (2 * j + 1) * kD] : 0.f);
+        }
         bool ok = true;
+        // four of the gates of this thread's tokens
+        auto four = [&](const float (&x)[C], int j) { return *reinterpret_cast<const float4 *>(x + 32 * half + 4 * j); };
         // the output of chunk i: scale e^G (Q S0) + P u
         auto output = [&](int i, const DeltaChunk &ch) {
             ok = mbar_wait_warp(o_full, i & 1u, wc);
             if (!ok) return;
             tc_fence_after();
             uint32_t x[32], y[32];
-            tmem_ld32(at + kColQ + 32 * half, x);
-            tmem_ld32(at + kColP + 32 * half, y);
+            tmem_ld32x2(at + kColQ + 32 * half, at + kColP + 32 * half, x, y);
             tc_fence_before();
             mbar_arrive(o_empty);
             const Gates &g = gates[i & 1];
+            const int64_t stride = (int64_t)a.Hv * kD;
             bf16 *o = static_cast<bf16 *>(a.out) + ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
+            const int rows = ch.n - 32 * half;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (32 * half + j < ch.n)
-                    o[(int64_t)j * a.Hv * kD] = __float2bfloat16_rn(
-                        fmaf(a.scale * g.eG[32 * half + j], __uint_as_float(x[j]), __uint_as_float(y[j])));
+            for (int j = 0; j < 8; ++j) {
+                const float4 e = four(g.eG, j);
+                const float2 s = make_float2(a.scale, a.scale);
+                const float2 p0 = fma2(mul2(s, make_float2(e.x, e.y)), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
+                const float2 p1 = fma2(mul2(s, make_float2(e.z, e.w)), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
+                if (4 * j < rows) o[0] = __float2bfloat16_rn(p0.x);
+                if (4 * j + 1 < rows) o[stride] = __float2bfloat16_rn(p0.y);
+                if (4 * j + 2 < rows) o[2 * stride] = __float2bfloat16_rn(p1.x);
+                if (4 * j + 3 < rows) o[3 * stride] = __float2bfloat16_rn(p1.y);
+                o += 4 * stride;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(g_empty + (i & 1));
         };
@@ -315,16 +354,21 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float x[32];
+                float2 x[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = S[32 * q + j];
+                for (int j = 0; j < 16; ++j) x[j] = S[16 * q + j];
                 put_parts<NP>(at + kColS + 32 * half + 16 * q, 64, x);
             }
+            tmem_put_wait();
             tc_fence_before();
             mbar_arrive(s_ready);
             if (keep) {
+                float *p = a.s0 + (cell * kD + 64 * half) * kD + m;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) a.s0[(cell * kD + 64 * half + j) * kD + m] = S[j];
+                for (int j = 0; j < 32; ++j) {
+                    p[2 * j * kD] = S[j].x;
+                    p[(2 * j + 1) * kD] = S[j].y;
+                }
             }
             if (NP == 2 && want && i > 0) {
                 output(i - 1, last);
@@ -333,49 +377,73 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
             ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc) && mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
             if (!ok) break;
             const Gates &g = gates[s];
-            float v[32];
+            float2 v[16];
             const bf16 *vp = reinterpret_cast<const bf16 *>(base + s * Sh::stage + Sh::oV) + 32 * half * kD + m;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __bfloat162float(vp[j * kD]);
+            for (int j = 0; j < 16; ++j)
+                v[j] = make_float2(__bfloat162float(vp[2 * j * kD]), __bfloat162float(vp[(2 * j + 1) * kD]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + s);
             ok = mbar_wait_warp(x_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
             {
                 uint32_t x[32];
                 tmem_ld32(at + kColX + 32 * half, x);
+                float *p = a.r + (cell * C + 32 * half) * kD + m;
+                const int rows = ch.n - 32 * half;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int t = 32 * half + j;
-                    const float r = fmaf(-g.eG[t], __uint_as_float(x[j]), v[j]);
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eG, j), b = four(g.beta, j);
+                    float2 r0 = fma2(make_float2(-e.x, -e.y), f2(x[4 * j], x[4 * j + 1]), v[2 * j]);
+                    float2 r1 = fma2(make_float2(-e.z, -e.w), f2(x[4 * j + 2], x[4 * j + 3]), v[2 * j + 1]);
                     // (rows of v behind the sequence's end are another's, or none)
-                    v[j] = t < ch.n ? g.beta[t] * r : 0.f;
-                    if (keep) a.r[(cell * C + t) * kD + m] = t < ch.n ? r : 0.f;
+                    r0 = make_float2(4 * j < rows ? r0.x : 0.f, 4 * j + 1 < rows ? r0.y : 0.f);
+                    r1 = make_float2(4 * j + 2 < rows ? r1.x : 0.f, 4 * j + 3 < rows ? r1.y : 0.f);
+                    if (keep) {
+                        p[4 * j * kD] = r0.x;
+                        p[(4 * j + 1) * kD] = r0.y;
+                        p[(4 * j + 2) * kD] = r1.x;
+                        p[(4 * j + 3) * kD] = r1.y;
+                    }
+                    v[2 * j] = mul2(make_float2(b.x, b.y), r0);
+                    v[2 * j + 1] = mul2(make_float2(b.z, b.w), r1);
                 }
             }
             put_parts<NP>(at + kColD + 16 * half, 32, v);
+            tmem_put_wait();
             tc_fence_before();
             mbar_arrive(r_ready);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + s);
             ok = mbar_wait_warp(u_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
             {
                 uint32_t x[32];
-                float y[32];
+                float2 y[16];
                 tmem_ld32(at + kColX + 32 * half, x);
+                float *p = a.u + (cell * C + 32 * half) * kD + m;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] = __uint_as_float(x[j]);
-                    y[j] = g.eL[32 * half + j] * v[j];
-                    if (keep) a.u[(cell * C + 32 * half + j) * kD + m] = v[j];
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eL, j);
+                    v[2 * j] = f2(x[4 * j], x[4 * j + 1]);
+                    v[2 * j + 1] = f2(x[4 * j + 2], x[4 * j + 3]);
+                    y[2 * j] = mul2(make_float2(e.x, e.y), v[2 * j]);
+                    y[2 * j + 1] = mul2(make_float2(e.z, e.w), v[2 * j + 1]);
                 }
                 put_parts<NP>(at + kColS + 16 * half, 32, y);
+                if (keep) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        p[2 * j * kD] = v[j].x;
+                        p[(2 * j + 1) * kD] = v[j].y;
+                    }
+                }
                 if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
+                tmem_put_wait();
             }
             tc_fence_before();
             mbar_arrive(u_ready);
-            const float eC = g.eC;
+            const float2 eC = make_float2(g.eC, g.eC);
             if (!want) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(g_empty + s);
@@ -383,18 +451,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
             ok = mbar_wait_warp(d_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
+            {
+                uint32_t x[64];
+                tmem_ld64(at + kColD + 64 * half, x);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t x[32];
-                tmem_ld32(at + kColD + 64 * half + 32 * q, x);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) S[32 * q + j] = fmaf(eC, S[32 * q + j], __uint_as_float(x[j]));
+                for (int j = 0; j < 32; ++j) S[j] = fma2(eC, S[j], f2(x[2 * j], x[2 * j + 1]));
             }
         }
         if (ok && want && n_chunks > 0) output(n_chunks - 1, ch);
         if (ok && a.state_out && slot >= 0) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) a.state_out[place + j * kD] = S[j];
+            for (int j = 0; j < 32; ++j) {
+                a.state_out[place + 2 * j * kD] = S[j].x;
+                a.state_out[place + (2 * j + 1) * kD] = S[j].y;
+            }
         }
     }
     tc_fence_before();
