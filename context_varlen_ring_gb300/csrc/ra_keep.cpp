@@ -114,8 +114,8 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
     ProfScope ps("ra_paged_attn_key_weights", s);
     cudaError_t e;
     if (weights_mma_supported(a.dtype, d)) {
-        (void)max_q_len;
-        e = launch_weights_mma(a, 64, s);
+        const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * a.G;
+        e = rows <= 16 && n_groups == 0 ? launch_weights_stream(a, s) : launch_weights_mma(a, 64, s);
     } else {
         e = launch_weights_simt(a, s);
     }

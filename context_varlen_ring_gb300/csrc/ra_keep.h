@@ -29,6 +29,7 @@ struct WeightArgs {
 };
 bool weights_mma_supported(int dtype, int d);
 cudaError_t launch_weights_mma(const WeightArgs &a, int keys, cudaStream_t st);   // keys a unit: 16, 32 or 64
+cudaError_t launch_weights_stream(const WeightArgs &a, cudaStream_t st);  // few query rows (as weights_mma_supported)
 cudaError_t launch_weights_simt(const WeightArgs &a, cudaStream_t st);
 
 struct EvictArgs {

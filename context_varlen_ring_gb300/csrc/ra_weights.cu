@@ -53,12 +53,13 @@ __device__ __forceinline__ bool segment(const WeightArgs &a, int s, Segment &g) 
 
 struct Line {
     int at[kSegs + 1];  // tiles ahead of each segment
-    long long warp[kThreads / 32];
+    long long warp[32];
 };
 // Lines up the segments from s0 on; their tiles of 2^k keys, or -1 where any segment is not as it must be (or the
 // tiles are more than any memory holds).
+template <int THREADS>
 __device__ __forceinline__ int line_up(const WeightArgs &a, int s0, int k, Line &sh) {
-    constexpr int PER = kSegs / kThreads;
+    constexpr int PER = kSegs / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, S = a.B + a.n_groups;
     int n[PER], bad = 0;
     long long sum = 0;
@@ -84,7 +85,7 @@ __device__ __forceinline__ int line_up(const WeightArgs &a, int s0, int k, Line 
     bad = __syncthreads_or(bad);
     long long at = inc - sum, all = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         if (i < (tid >> 5)) at += sh.warp[i];
         all += sh.warp[i];
     }
@@ -93,7 +94,7 @@ __device__ __forceinline__ int line_up(const WeightArgs &a, int s0, int k, Line 
         sh.at[tid * PER + i] = (int)at;
         at += n[i];
     }
-    if (tid == kThreads - 1) sh.at[kSegs] = (int)all;
+    if (tid == THREADS - 1) sh.at[kSegs] = (int)all;
     __syncthreads();
     return bad || all > INT32_MAX ? -1 : (int)all;
 }
@@ -175,12 +176,12 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wk = warp % WK, wr = warp / WK;
     const int S = a.B + a.n_groups;
     for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)  // (nothing is added where any segment is bad)
-        if (line_up(a, s0, LOG, sm.line) < 0) {
+        if (line_up<kThreads>(a, s0, LOG, sm.line) < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
     for (int s0 = 0; s0 < S; s0 += kSegs) {
-        const int tiles = line_up(a, s0, LOG, sm.line);
+        const int tiles = line_up<kThreads>(a, s0, LOG, sm.line);
         if (tiles < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
@@ -286,6 +287,185 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs 
     }
 }
 
+// ------------------------------------------------------------ bf16, few query rows: a stream of keys a warp
+// A decoding step has G rows a KV head, one 16-row block of products for each 16 keys, and reads 2 D bytes a key.  Every
+// warp streams its own runs of kRun keys through a private ring of kRing blocks of 16, its next run's keys under way
+// while the last one's are used; the rows stay in registers.  More rows are taken block by block against each 16 keys.
+constexpr int kRun = 64, kRing = 6, kStreamWarps = 8, kStreamThreads = 32 * kStreamWarps;
+
+template <int D>
+struct StreamSmem {
+    uint8_t k[kStreamWarps][kRing][16 * D * 2];
+    Line line;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const WeightArgs a) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte pieces a row, rows a warp instruction
+    extern __shared__ __align__(128) uint8_t raw[];
+    StreamSmem<D> &sm = *reinterpret_cast<StreamSmem<D> *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = a.B + a.n_groups;
+    for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)
+        if (line_up<kStreamThreads>(a, s0, 6, sm.line) < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+    const uint32_t ring = smem_u32(sm.k[warp]);
+    for (int s0 = 0; s0 < S; s0 += kSegs) {
+        const int tiles = line_up<kStreamThreads>(a, s0, 6, sm.line);
+        if (tiles < 0) {
+            if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+            return;
+        }
+        // this warp's blocks of 16 keys, in the order of its runs
+        struct Place {
+            int64_t u;      // run
+            int s, h, k0, len, b;
+        };
+        const int64_t units = (int64_t)tiles * a.Hkv, step = (int64_t)gridDim.x * kStreamWarps;
+        auto enter = [&](Place &p) {  // the run's segment; false behind the last
+            if (p.u >= units) return false;
+            const int tile = (int)(p.u / a.Hkv), i = find(sm.line, tile);
+            Segment g;
+            p.h = (int)(p.u - (int64_t)tile * a.Hkv);
+            p.s = s0 + i;
+            p.k0 = (tile - sm.line.at[i]) * kRun;
+            segment(a, p.s, g);
+            p.len = g.len;
+            p.b = 0;
+            return true;
+        };
+        auto advance = [&](Place &p) {
+            if (++p.b < kRun / 16 && p.k0 + 16 * p.b < p.len) return true;
+            p.u += step;
+            return enter(p);
+        };
+        int head = 0, tail = 0;
+        auto load = [&](const Place &p) {
+            const int key = p.k0 + 16 * p.b + (lane & 15);
+            int64_t page = 0;
+            int row = 0;
+            const bool there = lane < 16 && key < p.len && place(a, p.s, key, page, row);
+            const int64_t off = there ? page * a.page_stride + row * a.token_stride + p.h * a.head_stride : -1;
+            const int c = lane % CPR, r0 = lane / CPR;
+            const uint32_t dst = ring + head * (16 * D * 2);
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int r = i * RPI + r0;
+                const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                cp16(dst + r * (D * 2) + ((c ^ (r & 7)) << 4), static_cast<const bf16 *>(a.k) + (o < 0 ? 0 : o) + c * 8, o >= 0);
+            }
+            head = head + 1 == kRing ? 0 : head + 1;
+        };
+        Place in, at;
+        in.u = at.u = blockIdx.x + (int64_t)gridDim.x * warp;
+        bool more = enter(in);
+        at = in;
+        bool left = more;
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) {
+            if (more) {
+                load(in);
+                more = advance(in);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int64_t held = -1;  // the segment and head whose rows are in registers
+        uint32_t fb[D / 16][4];
+        float off[4];
+        Segment g{};
+        int rows = 0;
+        // rows r0 .. r0 + 15 as the products' columns, straight from the tensor: 4 bytes a place
+        auto rows_of = [&](int h, int r0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * e + (lane >> 2);
+                const bool there = r < rows;
+                const int t = token_of(a, there ? r : 0);
+                const bf16 *q = static_cast<const bf16 *>(a.q) + (g.tok0 + t) * a.q_stride + (h * a.G + (there ? r : 0) - t * a.G) * D + 2 * (lane & 3);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    fb[k][2 * e] = there ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * k)) : 0u;
+                    fb[k][2 * e + 1] = there ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * k + 8)) : 0u;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) off[e] = row_lse(a, g, h, r0 + 2 * (lane & 3) + (e & 1) + (e >> 1) * 8);
+        };
+        while (left) {
+            const int k0 = at.k0 + 16 * at.b;
+            const bool own = at.s < a.B;
+            // the weights' old values, on their way while the keys are waited for
+            float *w = nullptr, old = 0.f;
+            if ((lane & 3) < 2) {
+                const int key = k0 + (lane >> 2) + 8 * (lane & 3);
+                int64_t page;
+                int row;
+                if (key < at.len && place(a, at.s, key, page, row)) {
+                    w = a.w + page * a.w_page + row * a.w_token + at.h * a.w_head;
+                    old = *w;
+                }
+            }
+            const int64_t want = (int64_t)at.s * a.Hkv + at.h;
+            if (want != held) {
+                segment(a, at.s, g);
+                rows = g.n * a.G;
+            }
+            const int first = own && a.causal ? max(0, k0 - (g.len - g.n)) * a.G & ~15 : 0;
+            if (want != held && rows <= 16) rows_of(at.h, 0);
+            held = want;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            __syncwarp();
+            uint32_t fa[D / 16][4];
+            const uint32_t ka = ring + tail * (16 * D * 2) + (lane & 15) * (D * 2);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) ldsm4(ka + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), fa[k]);
+            tail = tail + 1 == kRing ? 0 : tail + 1;
+            __syncwarp();  // (the block can be loaded over)
+            if (more) {
+                load(in);
+                more = advance(in);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            float sum[2] = {0.f, 0.f};
+            const int key = k0 + (lane >> 2);
+            for (int r0 = first; r0 < rows; r0 += 16) {
+                if (rows > 16) rows_of(at.h, r0);
+                float c[2][4] = {};
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    mma16816(c[0], fa[k], fb[k][0], fb[k][1]);
+                    mma16816(c[1], fa[k], fb[k][2], fb[k][3]);
+                }
+                const bool masked = own && a.causal && g.len - g.n + token_of(a, r0) + 1 < k0 + 16;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *x = c[e >> 1];
+                    float p0 = ex2_approx(fmaf(x[e & 1], a.scale_log2, off[e]));
+                    float p1 = ex2_approx(fmaf(x[2 + (e & 1)], a.scale_log2, off[e]));
+                    if (off[e] == -INFINITY) p0 = p1 = 0.f;
+                    if (masked) {
+                        const int limit = limit_of(a, g, true, r0 + 2 * (lane & 3) + (e & 1) + (e >> 1) * 8);
+                        if (key >= limit) p0 = 0.f;
+                        if (key + 8 >= limit) p1 = 0.f;
+                    }
+                    sum[0] += p0;
+                    sum[1] += p1;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+            }
+            if (w) *w = old + sum[lane & 1];
+            left = advance(at);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+}
+
 // ------------------------------------------------------------ fp32 arithmetic: fp32, and bf16 of other head sizes
 constexpr int kSimtKeys = 32, kSimtRows = 32;
 
@@ -304,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
     const int tid = threadIdx.x, kx = tid & 15, ry = tid >> 4;
     const int S = a.B + a.n_groups;
     for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)
-        if (line_up(a, s0, 5, sm.line) < 0) {
+        if (line_up<kThreads>(a, s0, 5, sm.line) < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
@@ -324,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
     };
     const int vec = a.d / 4;
     for (int s0 = 0; s0 < S; s0 += kSegs) {
-        const int tiles = line_up(a, s0, 5, sm.line);
+        const int tiles = line_up<kThreads>(a, s0, 5, sm.line);
         if (tiles < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
@@ -412,8 +592,22 @@ cudaError_t mma_keys(const WeightArgs &a, int keys, cudaStream_t st) {
     return keys == 16 ? mma_launch<D, 16>(a, st) : keys == 32 ? mma_launch<D, 32>(a, st) : mma_launch<D, 64>(a, st);
 }
 
+template <int D>
+cudaError_t stream_launch(const WeightArgs &a, cudaStream_t st) {
+    static LaunchFit fit;
+    auto kernel = weights_stream_kernel<D>;
+    int ctas = 0;
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kStreamThreads, sizeof(StreamSmem<D>), &ctas);
+    if (e != cudaSuccess) return e;
+    kernel<<<paged_sms() * ctas, kStreamThreads, sizeof(StreamSmem<D>), st>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
+cudaError_t launch_weights_stream(const WeightArgs &a, cudaStream_t st) {
+    return a.d == 64 ? stream_launch<64>(a, st) : stream_launch<128>(a, st);
+}
 bool weights_mma_supported(int dtype, int d) { return dtype == RA_BF16 && (d == 64 || d == 128); }
 cudaError_t launch_weights_mma(const WeightArgs &a, int keys, cudaStream_t st) {
     return a.d == 64 ? mma_keys<64>(a, keys, st) : mma_keys<128>(a, keys, st);
