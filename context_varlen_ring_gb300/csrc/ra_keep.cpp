@@ -114,8 +114,12 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
     ProfScope ps("ra_paged_attn_key_weights", s);
     cudaError_t e;
     if (weights_mma_supported(a.dtype, d)) {
-        const int64_t rows = (max_q_len > 0 ? std::min<int64_t>(max_q_len, T) : T) * a.G;
-        e = rows <= 16 && n_groups == 0 ? launch_weights_stream(a, s) : launch_weights_mma(a, 64, s);
+        const int64_t rows = (max_q_len > 0 && n_groups == 0 ? std::min<int64_t>(max_q_len, T) : T) * a.G;
+        const int64_t units = Hkv * (B * ((a.width[0] * a.page_size + 255) / 256) + n_groups * ((a.width[1] * a.page_size + 255) / 256));
+        PagedMaps maps;
+        e = rows <= 16                                                                ? launch_weights_stream(a, s)
+            : rows >= 256 && units >= paged_sms() / 2 && weights_tc_maps(a, maps) ? launch_weights_tc(a, maps, s)
+                                                                                  : launch_weights_mma(a, 64, s);
     } else {
         e = launch_weights_simt(a, s);
     }

@@ -32,6 +32,10 @@ cudaError_t launch_weights_mma(const WeightArgs &a, int keys, cudaStream_t st); 
 cudaError_t launch_weights_stream(const WeightArgs &a, cudaStream_t st);  // few query rows (as weights_mma_supported)
 cudaError_t launch_weights_simt(const WeightArgs &a, cudaStream_t st);
 
+struct PagedMaps;
+bool weights_tc_maps(const WeightArgs &a, PagedMaps &m);  // false: not a shape of the tcgen05 kernel
+cudaError_t launch_weights_tc(const WeightArgs &a, const PagedMaps &m, cudaStream_t st);
+
 struct EvictArgs {
     void *k, *v;
     int64_t n_pages, page_stride, token_stride, head_stride;

@@ -20,123 +20,16 @@
 #include "ra_keep.h"
 #include "ra_kernels.h"
 #include "ra_serve.cuh"
+#include "ra_weights.cuh"
 
 namespace ra {
 namespace {
 
 using namespace dev;
+using namespace weights;
 using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 128;
-constexpr int kSegs = 1024;  // segments that a CTA lines up at a time
-
-__device__ __forceinline__ int token_of(const WeightArgs &a, int row) {
-    return a.G == 1 ? row : (int)__umul64hi((unsigned)row, a.G_inv);
-}
-
-// A segment: own keys of a sequence, or the keys of a prefix (behind the B sequences).
-struct Segment {
-    int tok0, n, len;
-};
-__device__ __forceinline__ bool segment(const WeightArgs &a, int s, Segment &g) {
-    const int f = s >= a.B, i = s - (f ? a.B : 0);
-    const int len = f ? a.prefix_lens[i] : a.kv_lens[i];
-    const int b0 = f ? a.groups[i] : i, b1 = f ? a.groups[i + 1] : i + 1;
-    const int c0 = a.cu[min(max(b0, 0), a.B)], c1 = a.cu[min(max(b1, 0), a.B)];
-    const bool fine = b0 >= 0 && b1 >= b0 && b1 <= a.B && len >= 0 && len <= a.width[f] * a.page_size &&
-                      len <= kPagedMostKeys && c0 >= 0 && c1 >= c0 && c1 <= a.T;
-    g.tok0 = c0;
-    g.n = fine ? c1 - c0 : 0;
-    g.len = fine ? len : 0;
-    return fine;
-}
-
-struct Line {
-    int at[kSegs + 1];  // tiles ahead of each segment
-    long long warp[32];
-};
-// Lines up the segments from s0 on; their tiles of 2^k keys, or -1 where any segment is not as it must be (or the
-// tiles are more than any memory holds).
-template <int THREADS>
-__device__ __forceinline__ int line_up(const WeightArgs &a, int s0, int k, Line &sh) {
-    constexpr int PER = kSegs / THREADS;
-    const int tid = threadIdx.x, lane = tid & 31, S = a.B + a.n_groups;
-    int n[PER], bad = 0;
-    long long sum = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int s = s0 + tid * PER + i;
-        Segment g;
-        n[i] = 0;
-        if (s < S) {
-            bad |= !segment(a, s, g);
-            n[i] = g.n > 0 ? (g.len + (1 << k) - 1) >> k : 0;
-        }
-        sum += n[i];
-    }
-    long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    __syncthreads();
-    if (lane == 31) sh.warp[tid >> 5] = inc;
-    bad = __syncthreads_or(bad);
-    long long at = inc - sum, all = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i < (tid >> 5)) at += sh.warp[i];
-        all += sh.warp[i];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        sh.at[tid * PER + i] = (int)at;
-        at += n[i];
-    }
-    if (tid == THREADS - 1) sh.at[kSegs] = (int)all;
-    __syncthreads();
-    return bad || all > INT32_MAX ? -1 : (int)all;
-}
-// The segment of a tile on the line.
-__device__ __forceinline__ int find(const Line &sh, int tile) {
-    int lo = 0, hi = kSegs;
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (sh.at[m] <= tile)
-            lo = m;
-        else
-            hi = m;
-    }
-    return lo;
-}
-
-// Page and row of a key of segment s; false: on no page of the cache (recorded).
-__device__ __forceinline__ bool place(const WeightArgs &a, int s, int key, int64_t &page, int &row) {
-    const int f = s >= a.B, i = s - (f ? a.B : 0);
-    const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
-    const int p = __ldg(a.table[f] + (int64_t)i * a.width[f] + pi);
-    page = p;
-    row = key - pi * a.page_size;
-    if (p >= 0 && p < a.n_pages) return true;
-    record_status(a.status, RA_ERR_DEVICE_BOUNDS);
-    return false;
-}
-
-// A row's offset in the exponent, -lse in base 2; -inf (nothing is added) behind the segment's rows and where the row
-// saw no key.
-__device__ __forceinline__ float row_lse(const WeightArgs &a, const Segment &g, int h, int row) {
-    if (row >= g.n * a.G) return -INFINITY;
-    const int t = token_of(a, row);
-    const float x = __ldg(a.lse + (int64_t)(h * a.G + row - t * a.G) * a.T + g.tok0 + t);
-    return x == -INFINITY ? -INFINITY : -x * 1.4426950408889634f;
-}
-
-// Keys of the segment that a row sees.
-__device__ __forceinline__ int limit_of(const WeightArgs &a, const Segment &g, bool own, int row) {
-    return own && a.causal ? g.len - g.n + token_of(a, row) + 1 : g.len;
-}
-
 // ------------------------------------------------------------ bf16, warp-level products
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -289,13 +182,17 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs 
 
 // ------------------------------------------------------------ bf16, few query rows: a stream of keys a warp
 // A decoding step has G rows a KV head, one 16-row block of products for each 16 keys, and reads 2 D bytes a key.  Every
-// warp streams its own runs of kRun keys through a private ring of kRing blocks of 16, its next run's keys under way
-// while the last one's are used; the rows stay in registers.  More rows are taken block by block against each 16 keys.
-constexpr int kRun = 64, kRing = 6, kStreamWarps = 8, kStreamThreads = 32 * kStreamWarps;
+// warp streams its own runs of keys through a private ring of kRing blocks of 16; a block's keys and old weights come by
+// asynchronous copies, its page is looked up a block ahead of them, and the rows stay in registers.  More rows are taken
+// block by block against each 16 keys.  Runs are 64 keys, or 256 where every warp has 8 of them all the same (a run
+// begins with a search for its segment).
+constexpr int kRing = 6, kStreamWarps = 8, kStreamThreads = 32 * kStreamWarps;
 
 template <int D>
 struct StreamSmem {
     uint8_t k[kStreamWarps][kRing][16 * D * 2];
+    float old[kStreamWarps][kRing][16];
+    int64_t w[kStreamWarps][kRing][16];  // where the weights are; -1: none
     Line line;
 };
 
@@ -311,43 +208,62 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
-    const uint32_t ring = smem_u32(sm.k[warp]);
+    const uint32_t ring = smem_u32(sm.k[warp]), olds = smem_u32(sm.old[warp]);
+    const int64_t step = (int64_t)gridDim.x * kStreamWarps;
     for (int s0 = 0; s0 < S; s0 += kSegs) {
-        const int tiles = line_up<kStreamThreads>(a, s0, 6, sm.line);
+        int log = 6, tiles = line_up<kStreamThreads>(a, s0, log, sm.line);
         if (tiles < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
+        if ((int64_t)tiles * a.Hkv >= 32 * step) {
+            log = 8;
+            tiles = line_up<kStreamThreads>(a, s0, log, sm.line);
+        }
         // this warp's blocks of 16 keys, in the order of its runs
         struct Place {
-            int64_t u;      // run
-            int s, h, k0, len, b;
+            int64_t u;  // run
+            int s, h, k, end, len;
         };
-        const int64_t units = (int64_t)tiles * a.Hkv, step = (int64_t)gridDim.x * kStreamWarps;
+        const int64_t units = (int64_t)tiles * a.Hkv;
         auto enter = [&](Place &p) {  // the run's segment; false behind the last
             if (p.u >= units) return false;
             const int tile = (int)(p.u / a.Hkv), i = find(sm.line, tile);
             Segment g;
             p.h = (int)(p.u - (int64_t)tile * a.Hkv);
             p.s = s0 + i;
-            p.k0 = (tile - sm.line.at[i]) * kRun;
+            p.k = (tile - sm.line.at[i]) << log;
             segment(a, p.s, g);
             p.len = g.len;
-            p.b = 0;
+            p.end = min(g.len, p.k + (1 << log));
             return true;
         };
         auto advance = [&](Place &p) {
-            if (++p.b < kRun / 16 && p.k0 + 16 * p.b < p.len) return true;
+            p.k += 16;
+            if (p.k < p.end) return true;
             p.u += step;
             return enter(p);
         };
+        // the page of this lane's key of a block (lanes 0 .. 15), as the table has it
+        auto look_up = [&](const Place &p) {
+            const int f = p.s >= a.B, i = p.s - (f ? a.B : 0), key = p.k + (lane & 15);
+            const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+            return key < p.len ? __ldg(a.table[f] + (int64_t)i * a.width[f] + pi) : -1;
+        };
         int head = 0, tail = 0;
-        auto load = [&](const Place &p) {
-            const int key = p.k0 + 16 * p.b + (lane & 15);
-            int64_t page = 0;
-            int row = 0;
-            const bool there = lane < 16 && key < p.len && place(a, p.s, key, page, row);
+        auto load = [&](const Place &p, int page) {
+            const int key = p.k + (lane & 15), pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+            const int row = key - pi * a.page_size;
+            const bool there = key < p.len && page >= 0 && page < a.n_pages;
+            if (key < p.len && !there) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             const int64_t off = there ? page * a.page_stride + row * a.token_stride + p.h * a.head_stride : -1;
+            const int64_t w = there ? page * a.w_page + row * a.w_token + p.h * a.w_head : -1;
+            if (lane < 16) {
+                sm.w[warp][head][lane] = w;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(olds + (head * 16 + lane) * 4),
+                             "l"(a.w + (there ? w : 0)), "r"(there ? 4 : 0)
+                             : "memory");
+            }
             const int c = lane % CPR, r0 = lane / CPR;
             const uint32_t dst = ring + head * (16 * D * 2);
 #pragma unroll
@@ -363,11 +279,15 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
         bool more = enter(in);
         at = in;
         bool left = more;
-#pragma unroll
+        int page = more ? look_up(in) : -1;
+#pragma unroll 1
         for (int i = 0; i < kRing - 1; ++i) {
             if (more) {
-                load(in);
+                const Place now = in;
+                const int p = page;
                 more = advance(in);
+                if (more) page = look_up(in);
+                load(now, p);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -394,19 +314,8 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             for (int e = 0; e < 4; ++e) off[e] = row_lse(a, g, h, r0 + 2 * (lane & 3) + (e & 1) + (e >> 1) * 8);
         };
         while (left) {
-            const int k0 = at.k0 + 16 * at.b;
+            const int k0 = at.k;
             const bool own = at.s < a.B;
-            // the weights' old values, on their way while the keys are waited for
-            float *w = nullptr, old = 0.f;
-            if ((lane & 3) < 2) {
-                const int key = k0 + (lane >> 2) + 8 * (lane & 3);
-                int64_t page;
-                int row;
-                if (key < at.len && place(a, at.s, key, page, row)) {
-                    w = a.w + page * a.w_page + row * a.w_token + at.h * a.w_head;
-                    old = *w;
-                }
-            }
             const int64_t want = (int64_t)at.s * a.Hkv + at.h;
             if (want != held) {
                 segment(a, at.s, g);
@@ -421,11 +330,17 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             const uint32_t ka = ring + tail * (16 * D * 2) + (lane & 15) * (D * 2);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) ldsm4(ka + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), fa[k]);
+            const int mine = (lane >> 2) + 8 * (lane & 1);  // the key that this lane writes (lanes 0 and 1 of each four)
+            const float old = sm.old[warp][tail][mine];
+            const int64_t w = sm.w[warp][tail][mine];
             tail = tail + 1 == kRing ? 0 : tail + 1;
             __syncwarp();  // (the block can be loaded over)
             if (more) {
-                load(in);
+                const Place now = in;
+                const int p = page;
                 more = advance(in);
+                if (more) page = look_up(in);
+                load(now, p);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             float sum[2] = {0.f, 0.f};
@@ -433,14 +348,16 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             for (int r0 = first; r0 < rows; r0 += 16) {
                 if (rows > 16) rows_of(at.h, r0);
                 float c[2][4] = {};
+                const bool both = r0 + 8 < rows;  // rows in the second half of the block
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     mma16816(c[0], fa[k], fb[k][0], fb[k][1]);
-                    mma16816(c[1], fa[k], fb[k][2], fb[k][3]);
+                    if (both) mma16816(c[1], fa[k], fb[k][2], fb[k][3]);
                 }
                 const bool masked = own && a.causal && g.len - g.n + token_of(a, r0) + 1 < k0 + 16;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    if (e >= 2 && !both) break;
                     const float *x = c[e >> 1];
                     float p0 = ex2_approx(fmaf(x[e & 1], a.scale_log2, off[e]));
                     float p1 = ex2_approx(fmaf(x[2 + (e & 1)], a.scale_log2, off[e]));
@@ -459,10 +376,11 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
             }
-            if (w) *w = old + sum[lane & 1];
+            if ((lane & 3) < 2 && w >= 0) a.w[w] = old + sum[lane & 1];
             left = advance(at);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
     }
 }
 

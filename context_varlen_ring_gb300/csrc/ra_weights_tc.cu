@@ -1,0 +1,335 @@
+// ra_weights_tc.cu -- key weights of many query rows (bf16, d = 128) on the
+// 5th-generation tensor cores: chunks of a prompt, and prefixes of a batch.
+//
+// Bound: 2 d flops and one exponential for each (row, key) pair; the tensor
+// pipe and the special-function unit take 512 cycles each for 128 x 128 of them.
+// Keys are the rows of S (A operand, a key a TMEM lane) and query rows its
+// columns, so a key's weight is summed in one thread's registers and no sum
+// passes between threads.  A unit is 256 keys of one KV head: two tiles in
+// shared memory that meet every tile of 128 query rows, which come by TMA through
+// a ring; two warpgroups have a tile of keys each, with two buffers of S, so that
+// the next product runs beside the exponentials.  The next unit's keys are
+// loaded beside this unit's rows.  Every wait is bounded as in the rest of the
+// library.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "ra_internal.h"
+#include "ra_serve.cuh"
+#include "ra_weights.cuh"
+
+namespace ra {
+namespace {
+
+using namespace weights;
+
+constexpr int kThreads = 384;
+constexpr int kKeys = 256;             // of a unit
+constexpr uint32_t kHalf = 16384;      // 128 rows x 128 B (64 bf16), 128-byte swizzle
+constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
+constexpr uint32_t kOffQ = 4 * kTile;  // behind two units' keys
+constexpr uint32_t kOffBar = kOffQ + 2 * kTile;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+
+struct TcParams {
+    CUtensorMap tmQ, tmK;
+    WeightArgs a;
+    int box, log2G, rows_inner;  // as in the paged attention's tensor maps
+    unsigned long long budget_ns;
+};
+
+struct Shared {
+    Line line;
+    alignas(16) float off[8][2][128];  // (read as float4) of each warp's two tiles of rows: -lse in base 2
+};
+
+struct Unit {
+    Segment g;
+    int s, h, k0, first, tiles, parts;  // first row; tiles of 128 rows; tiles of 128 keys
+    bool own;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_constant__ TcParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    const WeightArgs &a = p.a;
+    const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
+    uint64_t *k_full = bars + 0;    // [2] a unit's keys landed
+    uint64_t *k_empty = bars + 2;   // [2]
+    uint64_t *q_full = bars + 4;    // [2] a tile of rows
+    uint64_t *q_empty = bars + 6;   // [2]
+    uint64_t *s_full = bars + 8;    // [2][2] S of a warpgroup's buffer
+    uint64_t *s_empty = bars + 12;  // [2][2] (128 arrivals)
+    uint64_t *mma_done = bars + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 18);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 1);
+            mbar_init(q_full + i, 1);
+            mbar_init(q_empty + i, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(s_empty + i, 128);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tmQ);
+        tma_prefetch_desc(&p.tmK);
+    }
+    // (256 of the 384 threads line the segments up: kSegs is a multiple of 256)
+    const int tiles = line_up<256, kThreads>(a, 0, 8, sh.line);
+    if (tiles < 0) {
+        if (threadIdx.x == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl wc{abort_flag, a.status, p.budget_ns};
+    const int64_t units = (int64_t)tiles * a.Hkv;
+    auto unit = [&](int64_t u, Unit &w) {
+        const int tile = (int)(u / a.Hkv);
+        w.h = (int)(u - (int64_t)tile * a.Hkv);
+        w.s = find(sh.line, tile);
+        w.k0 = (tile - sh.line.at[w.s]) * kKeys;
+        segment(a, w.s, w.g);
+        w.own = w.s < a.B;
+        const int rows = w.g.n << p.log2G;
+        w.first = w.own && a.causal ? (max(0, w.k0 - (w.g.len - w.g.n)) << p.log2G) & ~127 : 0;
+        w.tiles = (rows - w.first + 127) / 128;
+        w.parts = w.g.len - w.k0 > 128 ? 2 : 1;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        uint32_t nk = 0, nq = 0;
+        bool ok = true;
+        const uint64_t policy = l2_evict_first();
+        const int boxes = 256 / p.box;  // of a tile: 128 / box row ranges x 2 halves of d
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            Unit w;
+            unit(u, w);
+            const uint32_t kb = nk & 1;
+            ok = mbar_wait_warp(k_empty + kb, ((nk >> 1) & 1u) ^ 1u, wc);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(k_full + kb, w.parts * kTile);
+            __syncwarp();
+            ++nk;
+            for (int t = 0; t < w.parts; ++t) {
+                if (lane < boxes) {
+                    const int key = w.k0 + t * 128 + (lane >> 1) * p.box;
+                    const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size, row = key - pi * a.page_size;
+                    int page = (int)a.n_pages;  // (outside the cache: filled with zeros)
+                    if (key < w.g.len) {
+                        const int f = w.s >= a.B;
+                        page = __ldg(a.table[f] + (int64_t)(w.s - (f ? a.B : 0)) * a.width[f] + pi);
+                        if (page < 0 || page >= a.n_pages) {
+                            record_status(a.status, RA_ERR_DEVICE_BOUNDS);
+                            page = (int)a.n_pages;
+                        }
+                    }
+                    const int c1 = p.rows_inner ? row : w.h, c2 = p.rows_inner ? w.h : row;
+                    tma_load_4d_hint(base + (kb * 2 + t) * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128, &p.tmK,
+                                     k_full + kb, (lane & 1) * 64, c1, c2, page, policy);
+                }
+                __syncwarp();
+            }
+            for (int j = 0; j < w.tiles && ok; ++j, ++nq) {
+                const uint32_t s = nq & 1;
+                ok = mbar_wait_warp(q_empty + s, ((nq >> 1) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tok = w.g.tok0 + ((w.first + j * 128) >> p.log2G), hq = w.h << p.log2G;
+                    mbar_arrive_expect_tx(q_full + s, kTile);
+                    tma_load_3d(base + kOffQ + s * kTile, &p.tmQ, q_full + s, 0, hq, tok);
+                    tma_load_3d(base + kOffQ + s * kTile + kHalf, &p.tmQ, q_full + s, 64, hq, tok);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {
+            // the last copies must have landed before the CTA may exit
+            volatile int local_abort = 0;
+            const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+            for (uint32_t i = nk > 2 ? nk - 2 : 0; i < nk; ++i) (void)mbar_wait(k_full + (i & 1), (i >> 1) & 1u, drain);
+            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) (void)mbar_wait(q_full + (i & 1), (i >> 1) & 1u, drain);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ products
+        const uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+        uint32_t nk = 0, nq = 0, ns[2] = {0, 0};
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            Unit w;
+            unit(u, w);
+            const uint32_t kb = nk & 1;
+            ok = mbar_wait_warp(k_full + kb, (nk >> 1) & 1u, wc);
+            ++nk;
+            for (int j = 0; j < w.tiles && ok; ++j, ++nq) {
+                const uint32_t s = nq & 1;
+                ok = mbar_wait_warp(q_full + s, (nq >> 1) & 1u, wc);
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= w.parts) break;
+                    const uint32_t b = ns[t] & 1;
+                    ok = mbar_wait_warp(s_empty + 2 * t + b, ((ns[t] >> 1) & 1u) ^ 1u, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dk = sdesc_sw128(base_s + (kb * 2 + t) * kTile, 16, 1024);
+                    const uint64_t dq = sdesc_sw128(base_s + kOffQ + s * kTile, 16, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t o = ((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4;
+                        tc_mma_ss_w(tmem + 256u * t + 128u * b, dk + o, dq + o, idesc, ks > 0);
+                    }
+                    tc_commit_w(s_full + 2 * t + b);
+                    ++ns[t];
+                }
+                tc_commit_w(q_empty + s);
+            }
+            tc_commit_w(k_empty + kb);
+        }
+        // every product issued must have completed before TMEM is released
+        tc_commit_w(mma_done);
+        volatile int local_abort = 0;
+        const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+        (void)mbar_wait_warp(mma_done, 0, drain);
+    } else if (warp >= 4) {
+        // ------------------------------------------------ exponentials and sums
+        const int k = warp >= 8 ? 1 : 0, m = threadIdx.x - 128 - 128 * k;  // TMEM lane: the key
+        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k;
+        uint32_t ns = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            Unit w;
+            unit(u, w);
+            if (k >= w.parts) continue;
+            const int key = w.k0 + 128 * k + m;
+            // the first row that sees the key
+            const int from = w.own && a.causal ? (key - (w.g.len - w.g.n)) * a.G : 0;
+            // a tile's offsets: four rows a lane, and whether any of the 128 adds nothing
+            float4 next;
+            auto look = [&](int r0) {
+                next = make_float4(row_lse(a, w.g, w.h, r0 + 4 * lane), row_lse(a, w.g, w.h, r0 + 4 * lane + 1),
+                                   row_lse(a, w.g, w.h, r0 + 4 * lane + 2), row_lse(a, w.g, w.h, r0 + 4 * lane + 3));
+            };
+            auto put = [&](uint32_t b) {
+                reinterpret_cast<float4 *>(sh.off[warp - 4][b])[lane] = next;
+                const bool any = fminf(fminf(next.x, next.y), fminf(next.z, next.w)) == -INFINITY;
+                return __any_sync(0xffffffffu, any);
+            };
+            look(w.first);
+            bool odd = put(ns & 1);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll 1
+            for (int j = 0; j < w.tiles; ++j, ++ns) {
+                const uint32_t b = ns & 1;
+                const int r0 = w.first + 128 * j;
+                if (j + 1 < w.tiles) look(r0 + 128);
+                const bool cut = odd || __any_sync(0xffffffffu, from > r0);
+                __syncwarp();  // (the offsets that the other lanes put)
+                ok = mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t v[64];
+                    tmem_ld64(tS + 128u * b + c, v);
+                    const float4 *off = reinterpret_cast<const float4 *>(sh.off[warp - 4][b] + c);
+                    if (!cut) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 f = off[i];
+                            const float2 x = fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sl2, make_float2(f.x, f.y));
+                            const float2 y = fma2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sl2, make_float2(f.z, f.w));
+                            sum[0] = add2(sum[0], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                            sum[1] = add2(sum[1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+                        }
+                    } else {  // rows that do not see the key, or add nothing (their scores may be anything)
+                        const int seen = from - r0 - c;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) {
+                            const float f = sh.off[warp - 4][b][c + i];
+                            const float x = ex2_approx(fmaf(__uint_as_float(v[i]), a.scale_log2, f));
+                            sum[0].x += i >= seen && f != -INFINITY ? x : 0.f;
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(s_empty + 2 * k + b);
+                if (j + 1 < w.tiles) odd = put(b ^ 1);
+            }
+            __syncwarp();  // (the last tile's offsets are read before the next unit's first take their place)
+            int64_t page;
+            int row;
+            if (ok && key < w.g.len && place(a, w.s, key, page, row))
+                a.w[page * a.w_page + row * a.w_token + w.h * a.w_head] += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+bool weights_tc_maps(const WeightArgs &a, PagedMaps &m) {
+    PagedArgs p{};  // (the paged attention's maps of q and of the cache)
+    p.q = a.q;
+    p.q_stride = a.q_stride;
+    p.T = a.T;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.G;
+    p.d = a.d;
+    p.dtype = a.dtype;
+    p.k = p.v = a.k;
+    p.n_pages = a.n_pages;
+    p.page_stride = a.page_stride;
+    p.token_stride = a.token_stride;
+    p.head_stride = a.head_stride;
+    p.page_size = a.page_size;
+    p.scale_log2 = 1.f;
+    return a.B + a.n_groups <= kSegs && paged_tc_maps(p, m);
+}
+
+cudaError_t launch_weights_tc(const WeightArgs &a, const PagedMaps &m, cudaStream_t st) {
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    p.tmQ = m.q;
+    p.tmK = m.k;
+    p.rows_inner = m.rows_inner;
+    p.a = a;
+    p.box = a.page_size < 128 ? a.page_size : 128;
+    while ((1 << p.log2G) < a.G) ++p.log2G;
+    p.budget_ns = wait_budget_ns();
+    static LaunchFit fit;
+    static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory of one CTA");
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(weights_tc_kernel), kThreads, kSmem, nullptr);
+    if (e != cudaSuccess) return e;
+    weights_tc_kernel<<<paged_sms(), kThreads, kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

@@ -60,13 +60,24 @@ WEIGHTS = [  # new, lens, prefix lens, groups, page, hq, hkv, d, dtype, causal, 
     ([1, 6], [64, 32], (5, 9), (0, 1, 2), 16, 2, 1, 256, "fp32", True, False, True, 0),
     ([5], [3], (), (0,), 16, 2, 1, 128, "bf16", True, False, True, 0),       # more new tokens than keys: the first see none
     ([33, 1], [33, 500], (100,), (0, 2), 64, 32, 1, 128, "bf16", True, False, True, 0),
+    ([4, 4], [300, 20], (), (0,), 16, 8, 2, 64, "bf16", True, False, True, 0),         # rows of a stream, its longest block
+    ([3, 1, 2], [90, 33, 2], (), (0,), 8, 14, 2, 128, "bf16", True, True, False, 1),
+    # rows and tables enough for tiles of 128 rows by 256 keys: heads, groups and pages of every kind
+    ([100, 300], [700, 300], (), (0,), 64, 16, 8, 128, "bf16", True, False, True, 3),
+    ([70, 1, 65], [70, 513, 900], (300,), (0, 3), 16, 32, 8, 128, "bf16", True, True, True, 0),
+    ([260], [1000], (), (0,), 256, 8, 8, 128, "bf16", False, False, False, 0),
+    ([3, 2], [400, 257], (129, 0), (0, 1, 2), 8, 128, 1, 128, "bf16", True, False, True, 0),
+    ([129], [129], (), (0,), 128, 16, 8, 128, "bf16", True, True, True, 0),
+    ([40], [30], (), (0,), 32, 64, 8, 128, "bf16", True, False, True, 0),
 ]
 
 
 def weights_case(rng, new, lens, plens, groups, page, hq, hkv, d, dtype, hnd, outer, tail):
     pages = sum(-(-n // page) for n in list(lens) + list(plens)) + 3
     kc = cache(pages, page, hkv, d, dtype, hnd, d + pages)
-    table, free = tables(rng, lens, page, pages, -(-max(lens) // page) + 1)
+    # (many rows: room in the tables for as many keys as choose the kernel for them)
+    width = -(-20000 // page) if sum(new) * hq // hkv >= 256 and d == 128 else -(-max(lens) // page) + 1
+    table, free = tables(rng, lens, page, pages, width)
     ptable, _ = tables(rng, plens, page, pages, -(-max(plens or (0,)) // page), set(table.ravel().tolist()))
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     T = int(cu[-1]) + tail
