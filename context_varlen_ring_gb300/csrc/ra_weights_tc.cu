@@ -31,8 +31,9 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 256;             // of a unit
 constexpr uint32_t kHalf = 16384;      // 128 rows x 128 B (64 bf16), 128-byte swizzle
 constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
-constexpr uint32_t kOffQ = 4 * kTile;  // behind two units' keys
-constexpr uint32_t kOffBar = kOffQ + 2 * kTile;
+constexpr int kRing = 4;               // tiles of rows
+constexpr uint32_t kOffQ = 2 * kTile;  // behind the keys
+constexpr uint32_t kOffBar = kOffQ + kRing * kTile;
 constexpr uint32_t kSmem = kOffBar + 256 + 1024;
 
 struct TcParams {
@@ -60,21 +61,21 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - raw_s);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
-    uint64_t *k_full = bars + 0;    // [2] a unit's keys landed
-    uint64_t *k_empty = bars + 2;   // [2]
-    uint64_t *q_full = bars + 4;    // [2] a tile of rows
-    uint64_t *q_empty = bars + 6;   // [2]
-    uint64_t *s_full = bars + 8;    // [2][2] S of a warpgroup's buffer
-    uint64_t *s_empty = bars + 12;  // [2][2] (128 arrivals)
-    uint64_t *mma_done = bars + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 18);
+    uint64_t *k_full = bars + 0;    // a unit's keys landed
+    uint64_t *k_empty = bars + 1;
+    uint64_t *q_full = bars + 2;    // [kRing] a tile of rows
+    uint64_t *q_empty = bars + 6;   // [kRing]
+    uint64_t *s_full = bars + 10;   // [2][2] S of a warpgroup's buffer
+    uint64_t *s_empty = bars + 14;  // [2][2] (128 arrivals)
+    uint64_t *mma_done = bars + 18;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 20);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(k_full + i, 1);
-            mbar_init(k_empty + i, 1);
+        mbar_init(k_full, 1);
+        mbar_init(k_empty, 1);
+        for (int i = 0; i < kRing; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
         }
@@ -125,10 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             Unit w;
             unit(u, w);
-            const uint32_t kb = nk & 1;
-            ok = mbar_wait_warp(k_empty + kb, ((nk >> 1) & 1u) ^ 1u, wc);
+            ok = mbar_wait_warp(k_empty, (nk & 1u) ^ 1u, wc);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(k_full + kb, w.parts * kTile);
+            if (lane == 0) mbar_arrive_expect_tx(k_full, w.parts * kTile);
             __syncwarp();
             ++nk;
             for (int t = 0; t < w.parts; ++t) {
@@ -145,14 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         }
                     }
                     const int c1 = p.rows_inner ? row : w.h, c2 = p.rows_inner ? w.h : row;
-                    tma_load_4d_hint(base + (kb * 2 + t) * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128, &p.tmK,
-                                     k_full + kb, (lane & 1) * 64, c1, c2, page, policy);
+                    tma_load_4d_hint(base + t * kTile + (lane & 1) * kHalf + (lane >> 1) * p.box * 128, &p.tmK,
+                                     k_full, (lane & 1) * 64, c1, c2, page, policy);
                 }
                 __syncwarp();
             }
             for (int j = 0; j < w.tiles && ok; ++j, ++nq) {
-                const uint32_t s = nq & 1;
-                ok = mbar_wait_warp(q_empty + s, ((nq >> 1) & 1u) ^ 1u, wc);
+                const uint32_t s = nq % kRing;
+                ok = mbar_wait_warp(q_empty + s, ((nq / kRing) & 1u) ^ 1u, wc);
                 if (!ok) break;
                 if (lane == 0) {
                     const int tok = w.g.tok0 + ((w.first + j * 128) >> p.log2G), hq = w.h << p.log2G;
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             // the last copies must have landed before the CTA may exit
             volatile int local_abort = 0;
             const WaitCtl drain{&local_abort, a.status, p.budget_ns};
-            for (uint32_t i = nk > 2 ? nk - 2 : 0; i < nk; ++i) (void)mbar_wait(k_full + (i & 1), (i >> 1) & 1u, drain);
-            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) (void)mbar_wait(q_full + (i & 1), (i >> 1) & 1u, drain);
+            if (nk > 0) (void)mbar_wait(k_full, (nk - 1) & 1u, drain);
+            for (uint32_t i = nq > kRing ? nq - kRing : 0; i < nq; ++i) (void)mbar_wait(q_full + i % kRing, (i / kRing) & 1u, drain);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ products
@@ -178,12 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             Unit w;
             unit(u, w);
-            const uint32_t kb = nk & 1;
-            ok = mbar_wait_warp(k_full + kb, (nk >> 1) & 1u, wc);
+            ok = mbar_wait_warp(k_full, nk & 1u, wc);
             ++nk;
             for (int j = 0; j < w.tiles && ok; ++j, ++nq) {
-                const uint32_t s = nq & 1;
-                ok = mbar_wait_warp(q_full + s, (nq >> 1) & 1u, wc);
+                const uint32_t s = nq % kRing;
+                ok = mbar_wait_warp(q_full + s, (nq / kRing) & 1u, wc);
                 if (!ok) break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                     ok = mbar_wait_warp(s_empty + 2 * t + b, ((ns[t] >> 1) & 1u) ^ 1u, wc);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t dk = sdesc_sw128(base_s + (kb * 2 + t) * kTile, 16, 1024);
+                    const uint64_t dk = sdesc_sw128(base_s + t * kTile, 16, 1024);
                     const uint64_t dq = sdesc_sw128(base_s + kOffQ + s * kTile, 16, 1024);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 }
                 tc_commit_w(q_empty + s);
             }
-            tc_commit_w(k_empty + kb);
+            tc_commit_w(k_empty);
         }
         // every product issued must have completed before TMEM is released
         tc_commit_w(mma_done);
@@ -224,15 +223,27 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             const int key = w.k0 + 128 * k + m;
             // the first row that sees the key
             const int from = w.own && a.causal ? (key - (w.g.len - w.g.n)) * a.G : 0;
-            // a tile's offsets: four rows a lane, and whether any of the 128 adds nothing
-            float4 next;
+            // a tile's offsets: four rows a lane, loaded a tile ahead and made of what was loaded when it is due; and
+            // whether any of the 128 adds nothing
+            float next[4];
+            int left = 0;  // rows from the lane's first on
             auto look = [&](int r0) {
-                next = make_float4(row_lse(a, w.g, w.h, r0 + 4 * lane), row_lse(a, w.g, w.h, r0 + 4 * lane + 1),
-                                   row_lse(a, w.g, w.h, r0 + 4 * lane + 2), row_lse(a, w.g, w.h, r0 + 4 * lane + 3));
+                left = (w.g.n << p.log2G) - r0 - 4 * lane;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = r0 + 4 * lane + min(e, max(left - 1, 0)), t = (left > 0 ? r : 0) >> p.log2G;
+                    next[e] = __ldg(a.lse + (int64_t)(w.h * a.G + (r & (a.G - 1))) * a.T + w.g.tok0 + t);
+                }
             };
             auto put = [&](uint32_t b) {
-                reinterpret_cast<float4 *>(sh.off[warp - 4][b])[lane] = next;
-                const bool any = fminf(fminf(next.x, next.y), fminf(next.z, next.w)) == -INFINITY;
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool none = e >= left || next[e] == -INFINITY;
+                    next[e] = none ? -INFINITY : -next[e] * 1.4426950408889634f;
+                    any |= none || next[e] == -INFINITY;
+                }
+                reinterpret_cast<float4 *>(sh.off[warp - 4][b])[lane] = make_float4(next[0], next[1], next[2], next[3]);
                 return __any_sync(0xffffffffu, any);
             };
             look(w.first);
