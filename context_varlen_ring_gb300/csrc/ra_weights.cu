@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs 
 // asynchronous copies, its page is looked up a block ahead of them, and the rows stay in registers.  More rows are taken
 // block by block against each 16 keys.  Runs are 64 keys, or 256 where every warp has 8 of them all the same (a run
 // begins with a search for its segment).
-constexpr int kRing = 6, kStreamWarps = 8, kStreamThreads = 32 * kStreamWarps;
+constexpr int kRing = 3, kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
 
 template <int D>
 struct StreamSmem {
@@ -347,12 +347,18 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             const int key = k0 + (lane >> 2);
             for (int r0 = first; r0 < rows; r0 += 16) {
                 if (rows > 16) rows_of(at.h, r0);
-                float c[2][4] = {};
+                float c[2][4] = {}, c2[4] = {};
                 const bool both = r0 + 8 < rows;  // rows in the second half of the block
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
+                for (int k = 0; k < D / 16; k += 2) {  // (two chains of products)
                     mma16816(c[0], fa[k], fb[k][0], fb[k][1]);
-                    if (both) mma16816(c[1], fa[k], fb[k][2], fb[k][3]);
+                    mma16816(c2, fa[k + 1], fb[k + 1][0], fb[k + 1][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[0][e] += c2[e];
+                if (both) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) mma16816(c[1], fa[k], fb[k][2], fb[k][3]);
                 }
                 const bool masked = own && a.causal && g.len - g.n + token_of(a, r0) + 1 < k0 + 16;
 #pragma unroll

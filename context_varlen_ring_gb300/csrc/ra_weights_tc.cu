@@ -27,7 +27,7 @@ namespace {
 
 using namespace weights;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kKeys = 256;             // of a unit
 constexpr uint32_t kHalf = 16384;      // 128 rows x 128 B (64 bf16), 128-byte swizzle
 constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
@@ -45,7 +45,8 @@ struct TcParams {
 
 struct Shared {
     Line line;
-    alignas(16) float off[8][2][128];  // (read as float4) of each warp's two tiles of rows: -lse in base 2
+    alignas(16) float off[16][2][64];  // (read as float4) of each warp's columns of two tiles of rows: -lse in base 2
+    float sum[2][4][128];              // of the second half of the columns, a unit after another
 };
 
 struct Unit {
@@ -66,10 +67,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     uint64_t *q_full = bars + 2;    // [kRing] a tile of rows
     uint64_t *q_empty = bars + 6;   // [kRing]
     uint64_t *s_full = bars + 10;   // [2][2] S of a warpgroup's buffer
-    uint64_t *s_empty = bars + 14;  // [2][2] (128 arrivals)
-    uint64_t *mma_done = bars + 18;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 19);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 20);
+    uint64_t *s_empty = bars + 14;  // [2][2] (256 arrivals)
+    uint64_t *part = bars + 18;     // [2][4] a unit's second halves are summed (128 arrivals)
+    uint64_t *mma_done = bars + 26;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 27);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 28);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -81,8 +83,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(s_empty + i, 128);
+            mbar_init(s_empty + i, 256);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(part + i, 128);
         mbar_init(mma_done, 1);
         fence_mbar_init();
         tma_prefetch_desc(&p.tmQ);
@@ -212,9 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         (void)mbar_wait_warp(mma_done, 0, drain);
     } else if (warp >= 4) {
         // ------------------------------------------------ exponentials and sums
-        const int k = warp >= 8 ? 1 : 0, m = threadIdx.x - 128 - 128 * k;  // TMEM lane: the key
-        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k;
-        uint32_t ns = 0;
+        const int k = warp >= 12 ? 1 : 0, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4 .. 7 and 12 .. 15: the first half
+        const int m = (warp & 3) * 32 + lane;                                // TMEM lane: the key
+        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k + 64u * half;
+        uint32_t ns = 0, nu = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             Unit w;
@@ -223,27 +227,28 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             const int key = w.k0 + 128 * k + m;
             // the first row that sees the key
             const int from = w.own && a.causal ? (key - (w.g.len - w.g.n)) * a.G : 0;
-            // a tile's offsets: four rows a lane, loaded a tile ahead and made of what was loaded when it is due; and
-            // whether any of the 128 adds nothing
-            float next[4];
+            // a tile's offsets: two rows a lane, loaded a tile ahead and made of what was loaded when it is due; and
+            // whether any of the warp's 64 adds nothing
+            float next[2];
             int left = 0;  // rows from the lane's first on
             auto look = [&](int r0) {
-                left = (w.g.n << p.log2G) - r0 - 4 * lane;
+                r0 += 64 * half + 2 * lane;
+                left = (w.g.n << p.log2G) - r0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = r0 + 4 * lane + min(e, max(left - 1, 0)), t = (left > 0 ? r : 0) >> p.log2G;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = left > e ? r0 + e : 0, t = r >> p.log2G;
                     next[e] = __ldg(a.lse + (int64_t)(w.h * a.G + (r & (a.G - 1))) * a.T + w.g.tok0 + t);
                 }
             };
             auto put = [&](uint32_t b) {
                 bool any = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     const bool none = e >= left || next[e] == -INFINITY;
                     next[e] = none ? -INFINITY : -next[e] * 1.4426950408889634f;
                     any |= none || next[e] == -INFINITY;
                 }
-                reinterpret_cast<float4 *>(sh.off[warp - 4][b])[lane] = make_float4(next[0], next[1], next[2], next[3]);
+                reinterpret_cast<float2 *>(sh.off[warp - 4][b])[lane] = make_float2(next[0], next[1]);
                 return __any_sync(0xffffffffu, any);
             };
             look(w.first);
@@ -253,21 +258,25 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
 #pragma unroll 1
             for (int j = 0; j < w.tiles; ++j, ++ns) {
                 const uint32_t b = ns & 1;
-                const int r0 = w.first + 128 * j;
-                if (j + 1 < w.tiles) look(r0 + 128);
+                const int r0 = w.first + 128 * j + 64 * half;
+                if (j + 1 < w.tiles) look(w.first + 128 * (j + 1));
                 const bool cut = odd || __any_sync(0xffffffffu, from > r0);
                 __syncwarp();  // (the offsets that the other lanes put)
                 ok = mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t v[64];
-                    tmem_ld64(tS + 128u * b + c, v);
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tS + 128u * b + c, v);
+                    if (c) {  // (all columns are read)
+                        tc_fence_before();
+                        mbar_arrive(s_empty + 2 * k + b);
+                    }
                     const float4 *off = reinterpret_cast<const float4 *>(sh.off[warp - 4][b] + c);
                     if (!cut) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const float4 f = off[i];
                             const float2 x = fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), sl2, make_float2(f.x, f.y));
                             const float2 y = fma2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), sl2, make_float2(f.z, f.w));
@@ -277,22 +286,31 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                     } else {  // rows that do not see the key, or add nothing (their scores may be anything)
                         const int seen = from - r0 - c;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) {
+                        for (int i = 0; i < 32; ++i) {
                             const float f = sh.off[warp - 4][b][c + i];
                             const float x = ex2_approx(fmaf(__uint_as_float(v[i]), a.scale_log2, f));
                             sum[0].x += i >= seen && f != -INFINITY ? x : 0.f;
                         }
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(s_empty + 2 * k + b);
                 if (j + 1 < w.tiles) odd = put(b ^ 1);
             }
             __syncwarp();  // (the last tile's offsets are read before the next unit's first take their place)
-            int64_t page;
-            int row;
-            if (ok && key < w.g.len && place(a, w.s, key, page, row))
-                a.w[page * a.w_page + row * a.w_token + w.h * a.w_head] += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            // the second half of the columns goes to the threads of the first, which are two tiles behind at most and so
+            // two units: of the four places none is written before it was read
+            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            const uint32_t at = nu & 3;
+            if (half) {
+                sh.sum[k][at][m] = all;
+                mbar_arrive(part + 4 * k + at);
+            } else {
+                ok = ok && mbar_wait_warp(part + 4 * k + at, (nu >> 2) & 1u, wc);
+                int64_t page;
+                int row;
+                if (ok && key < w.g.len && place(a, w.s, key, page, row))
+                    a.w[page * a.w_page + row * a.w_token + w.h * a.w_head] += all + sh.sum[k][at][m];
+            }
+            ++nu;
         }
     }
     tc_fence_before();
