@@ -475,6 +475,340 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
     }
 }
 
+// ------------------------------------------------------------ the walk from the end
+// The gradient's walk (formulas in ra_delta_bwd.cu), held the same way: dS^T as A
+// operand against K, its tokens' gradients against T and P with their rows as
+// the products' depth, and then against K and Q.  What needs no state (P^T do,
+// Q^T do) runs beside the conversions of the chain.
+// TMEM columns: 0 the growth of dS; 128 K dS; 192 P^T do; 256 dS's parts, then
+// du's and, behind them, scale e^G do's; in du's place -beta e^G dR's; 448 do.
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid_constant__ ScanParams p) {
+    using Sh = Shape<NP>;
+    constexpr int kColY = 192, kColZ = kColS, kColW = kColS + 32 * NP, kColDO = 448;
+    static_assert(kColS + 64 * NP <= kColDO, "columns");
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Gates gates[2];
+    const DeltaArgs &a = p.a;
+    if (a.hdr->bad) return;
+    const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
+    uint64_t *full = bars + 0;      // [2] a chunk's rows landed
+    uint64_t *empty = bars + 2;     // [2] its products are done, its do read
+    uint64_t *g_full = bars + 4;    // [2] its gates
+    uint64_t *g_empty = bars + 6;   // [2]
+    uint64_t *y_ready = bars + 8;   // do is in TMEM
+    uint64_t *s_ready = bars + 9;   // dS's parts
+    uint64_t *x_full = bars + 10;   // K dS and P^T do are there
+    uint64_t *r_ready = bars + 11;  // du's parts, and scale e^G do's
+    uint64_t *u_full = bars + 12;   // dR is there
+    uint64_t *z_ready = bars + 13;  // -beta e^G dR's parts
+    uint64_t *d_full = bars + 14;   // the growth of dS is there
+    uint64_t *mma_done = bars + 15;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 17);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = a.order[blockIdx.x / a.Hv], h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0, c1 = c0 + n_chunks - 1;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1 + 8);
+            mbar_init(g_full + i, 1);
+            mbar_init(g_empty + i, 8);
+        }
+        mbar_init(y_ready, 256);
+        mbar_init(s_ready, 256);
+        mbar_init(x_full, 1);
+        mbar_init(r_ready, 256);
+        mbar_init(u_full, 1);
+        mbar_init(z_ready, 256);
+        mbar_init(d_full, 1);
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tmQ);
+        tma_prefetch_desc(&p.tmK);
+        tma_prefetch_desc(&p.tmV);
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl wc{abort_flag, a.status, p.budget_ns};
+
+    // Registers: 128 x 80 + 256 x 200 = 61440, within the 384 x 168 = 64512 of the launch.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+        if (warp == 0) {
+            // -------------------------------------------- loads
+            if (lane == 0) {
+                int i = 0;
+                for (bool ok = true; i < n_chunks; ++i) {
+                    const int s = i & 1;
+                    const int64_t c = c1 - i;
+                    const int tok = a.chunk[c].tok0;
+                    uint8_t *st = base + s * Sh::stage;
+                    ok = mbar_wait(empty + s, ((i >> 1) & 1u) ^ 1u, wc);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(full + s, 2 * kHalf + 2 * NP * kSquare + kValues);
+                    for (int d = 0; d < 2; ++d) {
+                        tma_load_3d(st + d * kHalf, &p.tmK, full + s, d * 64, hk, tok);
+                        tma_load_3d(st + d * kHalf + kHalf / 2, &p.tmQ, full + s, d * 64, hk, tok);
+                    }
+                    tma_load_3d(st + Sh::oV, &p.tmV, full + s, 0, h, tok);
+                    bulk_load(st + Sh::oTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, 2 * NP * kSquare, full + s);
+                }
+                // the last copies must have landed before the CTA may exit
+                volatile int local_abort = 0;
+                const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) (void)mbar_wait(full + (j & 1), (j >> 1) & 1u, drain);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------- products
+            const uint32_t id64 = idesc_bf16_f32(128, 64, 0, 0), id64n = idesc_bf16_f32(128, 64, 0, 1),
+                           id128n = idesc_bf16_f32(128, 128, 0, 1);
+            bool ok = true;
+            for (int i = 0; i < n_chunks && ok; ++i) {
+                const int s = i & 1;
+                const uint32_t st = base_s + s * Sh::stage, ph = i & 1u;
+                const uint64_t dK = sdesc_sw128(st, 16, 1024);
+                const uint64_t dKn = sdesc_sw128(st, kHalf, 1024), dQn = sdesc_sw128(st + kHalf / 2, kHalf, 1024);  // columns of dk
+                const uint64_t dT = sdesc_sw128(st + Sh::oTP, kHalf, 1024), dP = sdesc_sw128(st + Sh::oTP + NP * kSquare, kHalf, 1024);
+                ok = mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
+                if (!ok) break;
+                const int n = a.chunk[c1 - i].n;
+                if (n < C) {  // rows of K and Q behind the sequence's end are another's, or none
+                    uint8_t *k = base + s * Sh::stage;
+                    for (int x = n * 8 + lane; x < C * 8; x += 32)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(k + e * (kHalf / 2) + x * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                // parts [v, token] by 64 rows of K or Q: D [v, dk]
+                auto by_rows = [&](uint32_t x, uint64_t b, bool more) {
+#pragma unroll
+                    for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc_mma_ts_w(tmem + kColD, tmem + x + 32 * q + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id128n, more);
+                            more = true;
+                        }
+                };
+                ok = mbar_wait_warp(y_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = NP - 1; q >= 0; --q)  // do by P's rows
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc_mma_ts_w(tmem + kColY, tmem + kColDO + 8 * ks, dP + ((q * kSquare + (uint32_t)ks * 2048u) >> 4), id64n,
+                                    !(q == NP - 1 && ks == 0));
+                ok = mbar_wait_warp(s_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_ts_w(tmem + kColX, tmem + kColS + 64 * q + 8 * ks,
+                                    dK + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), id64,
+                                    !(q == NP - 1 && ks == 0));
+                tc_commit_w(x_full);
+                ok = mbar_wait_warp(r_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+                bool more = false;
+#pragma unroll
+                for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                    for (int q = 0; q <= o; ++q)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            tc_mma_ts_w(tmem + kColX, tmem + kColZ + 32 * q + 8 * ks,
+                                        dT + (((o - q) * kSquare + (uint32_t)ks * 2048u) >> 4), id64n, more);
+                            more = true;
+                        }
+                tc_commit_w(u_full);
+                by_rows(kColW, dQn, false);
+                ok = mbar_wait_warp(z_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
+                by_rows(kColZ, dKn, true);
+                tc_commit_w(d_full);
+                tc_commit_w(empty + s);
+            }
+            // every product issued must have completed before TMEM is released
+            tc_commit_w(mma_done);
+            volatile int local_abort = 0;
+            const WaitCtl drain{&local_abort, a.status, p.budget_ns};
+            (void)mbar_wait_warp(mma_done, 0, drain);
+        } else if (warp == 3) {
+            // -------------------------------------------- gates
+            float g[2], b[2];
+            if (n_chunks > 0) gates_load(a, a.chunk[c1], h, g, b);
+            for (int i = 0; i < n_chunks; ++i) {
+                if (!mbar_wait_warp(g_empty + (i & 1), ((i >> 1) & 1u) ^ 1u, wc)) break;
+                gates_put(gates[i & 1], g, b);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_full + (i & 1));
+                if (i + 1 < n_chunks) gates_load(a, a.chunk[c1 - i - 1], h, g, b);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+        // ------------------------------------------------ dS, and what the products read
+        const int half = warp >= 8 ? 1 : 0, m = (warp & 3) * 32 + lane;  // TMEM lane: the column of v
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int64_t place = (((int64_t)seq * a.Hv + h) * kD + 64 * half) * kD + m;
+        float2 S[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            S[j] = make_float2(a.dstate ? a.dstate[place + 2 * j * kD] : 0.f, a.dstate ? a.dstate[place + (2 * j + 1) * kD] : 0.f);
+        bool ok = true;
+        auto four = [&](const float (&x)[C], int j) { return *reinterpret_cast<const float4 *>(x + 32 * half + 4 * j); };
+        // chunk i's do: pairs of tokens, as they are (one part), into registers and TMEM
+        uint32_t d[16];
+        auto take = [&](int i) {
+            ok = mbar_wait_warp(full + (i & 1), (i >> 1) & 1u, wc);
+            if (!ok) return;
+            const int rows = a.chunk[c1 - i].n - 32 * half;
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * Sh::stage + Sh::oV) + 32 * half * kD + m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)  // (rows behind the sequence's end are another's, or none)
+                d[j] = (2 * j < rows ? x[2 * j * kD] : 0u) | (2 * j + 1 < rows ? (uint32_t)x[(2 * j + 1) * kD] << 16 : 0u);
+            tmem_put16(at + kColDO + 16 * half, d);
+            tmem_put_wait();
+            tc_fence_before();
+            mbar_arrive(y_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + (i & 1));
+        };
+        if (n_chunks > 0) take(0);
+#pragma unroll 1
+        for (int i = 0; i < n_chunks && ok; ++i) {
+            const int s = i & 1;
+            const uint32_t ph = i & 1u;
+            const int64_t cell = (int64_t)(c1 - i) * a.Hv + h;
+            const DeltaChunk ch = a.chunk[c1 - i];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float2 x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = S[16 * q + j];
+                put_parts<NP>(at + kColS + 32 * half + 16 * q, 64, x);
+            }
+            tmem_put_wait();
+            tc_fence_before();
+            mbar_arrive(s_ready);
+            {
+                float *o = a.ds + (cell * kD + 64 * half) * kD + m;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    o[2 * j * kD] = S[j].x;
+                    o[(2 * j + 1) * kD] = S[j].y;
+                }
+            }
+            ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc) && mbar_wait_warp(x_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const Gates &g = gates[s];
+            {
+                uint32_t x[32], y[32];
+                float2 v[16];
+                tmem_ld32x2(at + kColX + 32 * half, at + kColY + 32 * half, x, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eL, j);
+                    v[2 * j] = fma2(make_float2(e.x, e.y), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
+                    v[2 * j + 1] = fma2(make_float2(e.z, e.w), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
+                }
+                put_parts<NP>(at + kColZ + 16 * half, 32, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eG, j);
+                    v[2 * j] = mul2(make_float2(a.scale * e.x, a.scale * e.y), f2(d[2 * j] << 16, d[2 * j] & 0xffff0000u));
+                    v[2 * j + 1] = mul2(make_float2(a.scale * e.z, a.scale * e.w), f2(d[2 * j + 1] << 16, d[2 * j + 1] & 0xffff0000u));
+                }
+                put_parts<NP>(at + kColW + 16 * half, 32, v);
+            }
+            tmem_put_wait();
+            tc_fence_before();
+            mbar_arrive(r_ready);
+            ok = mbar_wait_warp(u_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                uint32_t x[32];
+                float2 v[16];
+                tmem_ld32(at + kColX + 32 * half, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eG, j), b = four(g.beta, j);
+                    v[2 * j] = mul2(make_float2(-b.x * e.x, -b.y * e.y), f2(x[4 * j], x[4 * j + 1]));
+                    v[2 * j + 1] = mul2(make_float2(-b.z * e.z, -b.w * e.w), f2(x[4 * j + 2], x[4 * j + 3]));
+                }
+                put_parts<NP>(at + kColZ + 16 * half, 32, v);
+                tmem_put_wait();
+                tc_fence_before();
+                mbar_arrive(z_ready);
+                const int rows = ch.n - 32 * half;
+                const int64_t stride = (int64_t)a.Hv * kD;
+                bf16 *o = static_cast<bf16 *>(a.dv_) + ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
+                float *r = a.dr + (cell * C + 32 * half) * kD + m;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 b = four(g.beta, j);
+                    const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = __uint_as_float(x[4 * j + e]);
+                        r[(4 * j + e) * kD] = y;
+                        if (4 * j + e < rows) o[e * stride] = __float2bfloat16_rn(bb[e] * y);
+                    }
+                    o += 4 * stride;
+                }
+            }
+            const float2 eC = make_float2(g.eC, g.eC);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g_empty + s);
+            if (i + 1 < n_chunks) {
+                take(i + 1);
+                if (!ok) break;
+            }
+            ok = mbar_wait_warp(d_full, ph, wc);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                uint32_t x[64];
+                tmem_ld64(at + kColD + 64 * half, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[j] = fma2(eC, S[j], f2(x[2 * j], x[2 * j + 1]));
+            }
+        }
+        if (ok && a.dstate0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                a.dstate0[place + 2 * j * kD] = S[j].x;
+                a.dstate0[place + (2 * j + 1) * kD] = S[j].y;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -501,10 +835,10 @@ bool rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t stride, b
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NP>
-cudaError_t scan(const ScanParams &p, cudaStream_t st) {
+// kernel: one of the walks, of NP parts.
+template <int NP, void (*kernel)(const ScanParams)>
+cudaError_t walk(const ScanParams &p, cudaStream_t st) {
     static std::atomic<bool> ready[128] = {};
-    auto kernel = delta_tc_scan_kernel<NP>;
     static_assert(Shape<NP>::smem <= 232448 - 2 * sizeof(Gates), "shared memory of one CTA");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -536,7 +870,18 @@ cudaError_t launch_delta_tc_scan(const DeltaArgs &a, int keep, cudaStream_t st) 
     p.a = a;
     p.keep = keep;
     p.budget_ns = wait_budget_ns();
-    return a.parts == 2 ? scan<2>(p, st) : scan<3>(p, st);
+    return a.parts == 2 ? walk<2, delta_tc_scan_kernel<2>>(p, st) : walk<3, delta_tc_scan_kernel<3>>(p, st);
+}
+
+cudaError_t launch_delta_tc_back(const DeltaArgs &a, cudaStream_t st) {
+    ScanParams p;
+    memset(&p, 0, sizeof(p));
+    if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
+        !rows_map(&p.tmV, a.dout, a.T, a.Hv, a.dout_stride, false))
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.budget_ns = wait_budget_ns();
+    return walk<3, delta_tc_back_kernel<3>>(p, st);
 }
 
 }  // namespace ra
