@@ -129,10 +129,6 @@ ra_status launched(cudaError_t e, const char *what) {
     return e == cudaSuccess ? RA_OK : fail(RA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
 }
 
-cudaError_t scan(const DeltaArgs &a, int keep, cudaStream_t s) {
-    return delta_tc_supported(a) ? launch_delta_tc_scan(a, keep, s) : launch_delta_scan(a, keep, s);
-}
-
 template <typename F>
 ra_status step(const char *name, cudaStream_t s, F &&f) {
     ProfScope ps(name, s);
@@ -171,7 +167,7 @@ ra_status ra_delta_rule_fwd(const ra_delta *d, void *out, float *state_out, void
     a.parts = d->dtype == RA_BF16 && !state_out ? 2 : 3;
     if ((st = step("ra_delta_plan", s, [&] { return launch_delta_plan(a, s); }))) return st;
     if (a.max_chunks > 0 && (st = step("ra_delta_local", s, [&] { return launch_delta_local(a, s); }))) return st;
-    return step("ra_delta_scan", s, [&] { return scan(a, 0, s); });
+    return step("ra_delta_scan", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_scan(a, s) : launch_delta_scan(a, 0, s); });
 }
 
 ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_stride, const float *dstate, void *dq,
@@ -202,11 +198,13 @@ ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_st
     a.dg = dg;
     a.dbeta = dbeta;
     if ((st = step("ra_delta_plan", s, [&] { return launch_delta_plan(a, s); }))) return st;
-    if (a.max_chunks > 0) {
-        if ((st = step("ra_delta_local", s, [&] { return launch_delta_local(a, s); }))) return st;
-        if ((st = step("ra_delta_scan", s, [&] { return scan(a, 1, s); }))) return st;
+    if (a.max_chunks > 0 && (st = step("ra_delta_local", s, [&] { return launch_delta_local(a, s); }))) return st;
+    if (delta_tc_supported(a)) {
+        if ((st = step("ra_delta_walks", s, [&] { return launch_delta_tc_walks(a, s); }))) return st;
+    } else {
+        if (a.max_chunks > 0 && (st = step("ra_delta_scan", s, [&] { return launch_delta_scan(a, 1, s); }))) return st;
+        if ((st = step("ra_delta_back", s, [&] { return launch_delta_back(a, s); })) || a.max_chunks == 0) return st;
     }
-    if ((st = step("ra_delta_back", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_back(a, s) : launch_delta_back(a, s); })) || a.max_chunks == 0) return st;
     if ((st = step("ra_delta_grads", s, [&] { return launch_delta_grads(a, s); })) || !a.part) return st;
     return step("ra_delta_sum", s, [&] { return launch_delta_sum(a, s); });
 }

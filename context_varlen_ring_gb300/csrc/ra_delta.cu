@@ -99,10 +99,11 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArg
 }
 
 // ------------------------------------------------------------ T and P
-// Bound: what it writes, 16 KB a chunk and head for each part.  Measured (8192 chunks of 64, 16 heads' worth, two
-// parts): see launch_delta_local.  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a lane a column;
-// then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
-constexpr int kLocalThreads = 128;
+// Bound: what it writes, 16 KB a chunk and head for each part; but each chunk is a chain of small steps, and the SMs
+// hold few at once.  So half of the warps make A and its inverse, the other half P (8192 chunks, two parts: 264 us with
+// all of it in four warps, 208 so).  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a lane a
+// column; then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
+constexpr int kLocalThreads = 256;
 constexpr int kLdy = 40;
 
 template <typename E, int NP, int DK>
@@ -143,63 +144,67 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     }
     cp_wait<0>();
     __syncthreads();
-    // rows 16 warp .. of K K^T and Q K^T, up to the diagonal
-    const int row0 = 16 * warp;
+    // rows 16 (warp % 4) .. of K K^T (warps 0 to 3) or Q K^T (4 to 7), up to the diagonal
+    const int w = warp & 3, row0 = 16 * w;
+    const bool own = warp < 4;
     const uint32_t kb = smem_u32(sm.in.k), row = row0 * LD * 2;
-    float kk[8][4], qk[8][4];
-    zero(kk);
-    zero(qk);
-    mm<8, NPI, NPI, 3, false, false>(kk, kb + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
-    mm<8, NPI, NPI, 3, false, false>(qk, smem_u32(sm.in.q) + row, LD, PL, kb, LD, PL, 0, DK, warp + 1);
+    float x[8][4];
+    zero(x);
+    mm<8, NPI, NPI, 3, false, false>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
     __syncthreads();  // (P takes the place of K and Q)
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int i = row0 + acc_row(hf), j = acc_col(n);
-            float x[2] = {0.f, 0.f}, p[2] = {0.f, 0.f};
-            if (n / 2 <= warp) {
-                const float b = sm.g.beta[i];
+            float y[2] = {0.f, 0.f};
+            const float f = own ? sm.g.beta[i] : a.scale;
+            if (n / 2 <= w) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (j + e <= i) {
-                        const float D = decay(sm.g, i, j + e);
-                        p[e] = a.scale * D * qk[n][2 * hf + e];
-                        if (j + e < i) x[e] = b * D * kk[n][2 * hf + e];
-                    }
-                put2<NP>(&sm.A[0][i][j], C * kLdc, x[0], x[1]);
-                if (n / 2 == warp) {
-                    sm.diag[warp][i & 15][j & 15] = x[0];
-                    sm.diag[warp][i & 15][(j & 15) + 1] = x[1];
+                    if (j + e + own <= i) y[e] = f * decay(sm.g, i, j + e) * x[n][2 * hf + e];
+            }
+            if (!own) {
+                put2<NP>(&sm.P[0][i][j], C * kLdc, y[0], y[1]);
+            } else if (n / 2 <= w) {
+                put2<NP>(&sm.A[0][i][j], C * kLdc, y[0], y[1]);
+                if (n / 2 == w) {
+                    sm.diag[w][i & 15][j & 15] = y[0];
+                    sm.diag[w][i & 15][(j & 15) + 1] = y[1];
                 }
             } else {
                 put2<NP>(&sm.T[0][i][j], C * kLdc, 0.f, 0.f);
             }
-            put2<NP>(&sm.P[0][i][j], C * kLdc, p[0], p[1]);
         }
+    uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
+    if (!own) {
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        store_square<NP, 128>(tp + NP * C * C, &sm.P[0][0][0]);
+        return;
+    }
+    auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };  // (of the four that go on)
     __syncwarp();
     if (lane < 16) {
         float t[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float x = i == lane ? 1.f : 0.f;
+            float s = i == lane ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) x -= sm.diag[warp][i][m] * t[m];
-            t[i] = x;
+            for (int m = 0; m < i; ++m) s -= sm.diag[w][i][m] * t[m];
+            t[i] = s;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float x = t[i];
+            float s = t[i];
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const bf16 b = __float2bfloat16_rn(x);
+                const bf16 b = __float2bfloat16_rn(s);
                 sm.T[p][row0 + i][row0 + lane] = b;
-                x -= __bfloat162float(b);
+                s -= __bfloat162float(b);
             }
         }
     }
-    __syncthreads();
-    uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
+    sync();
     const uint32_t Ab = smem_u32(sm.A), Tb = smem_u32(sm.T), Yb = smem_u32(sm.Y);
     auto tile = [&](uint32_t b, int r, int col) { return b + (r * kLdc + col) * 2; };
     auto put = [&](bf16 *dst, int ld, int plane, const float (&x)[2][4], float sign) {
@@ -210,29 +215,28 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
                 put2<NP>(dst + acc_row(hf) * ld + acc_col(n), plane, sign * x[n][2 * hf], sign * x[n][2 * hf + 1]);
     };
     float y[2][4];
-    if (warp & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
+    if (w & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
         zero(y);
         mm<2, NP, NP, NP, false, true>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
-        put(&sm.Y[0][(warp >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
+        put(&sm.Y[0][(w >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
         __syncwarp();
         zero(y);
-        mm<2, NP, NP, NP, false, true>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (warp >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
+        mm<2, NP, NP, NP, false, true>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
         put(&sm.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
     }
-    __syncthreads();
+    sync();
     {  // rows 32 .. 63 by columns 0 .. 31: a block of 16 x 16 each warp
-        const int r = (warp >> 1) * 16, col = (warp & 1) * 16;
+        const int r = (w >> 1) * 16, col = (w & 1) * 16;
         zero(y);
         mm<2, NP, NP, NP, false, true>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
         put(&sm.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
-        store_square<NP, kLocalThreads>(tp + NP * C * C, &sm.P[0][0][0]);
-        __syncthreads();
+        sync();
         zero(y);
         mm<2, NP, NP, NP, false, true>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
         put(&sm.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
     }
-    __syncthreads();
-    store_square<NP, kLocalThreads>(tp, &sm.T[0][0][0]);
+    sync();
+    store_square<NP, 128>(tp, &sm.T[0][0][0]);
 }
 
 // ------------------------------------------------------------ the walk

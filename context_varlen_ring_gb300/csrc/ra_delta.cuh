@@ -165,18 +165,18 @@ __device__ __forceinline__ void load_square(bf16 *dst, const uint16_t *src) {
         cp16z(smem_u32(dst + row * kLdc + c * 8), src + swizzled(row, c), true);
     }
 }
-// And back, from parts of pitch kLdc.
+// And back, from parts of pitch kLdc, by a group of THREADS threads.
 template <int NP, int THREADS>
 __device__ __forceinline__ void store_square(uint16_t *dst, const bf16 *src) {
-    for (int i = threadIdx.x; i < NP * C * 8; i += THREADS) {
+    for (int i = threadIdx.x % THREADS; i < NP * C * 8; i += THREADS) {
         const int row = i >> 3, c = i & 7;
         *reinterpret_cast<uint4 *>(dst + swizzled(row, c)) = *reinterpret_cast<const uint4 *>(src + row * kLdc + c * 8);
     }
 }
-// A chunk's gates.  G_i is the sum of its first i + 1 log decays; kept as the
-// sum of two floats, because the products use exp(G_i - G_j), whose exponent
-// would otherwise lose the bits that a strong decay ahead of both pushes out.
-// Decays below -1e4 are e^-1e4 = 0 all the same, and keep the sums finite.
+// A chunk's gates.  G_i is the sum of its first i + 1 log decays; kept in base 2
+// and as the sum of two floats, because the products use exp(G_i - G_j), whose
+// exponent would otherwise lose the bits that a strong decay ahead of both pushes
+// out.  Decays below -1e4 are e^-1e4 = 0 all the same, and keep the sums finite.
 struct alignas(16) Gates {
     float hi[C], lo[C];
     float beta[C];
@@ -190,7 +190,12 @@ __device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
     const float h = s + e;
     return make_float2(h, e - (h - s));
 }
-__device__ __forceinline__ float gate_exp(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
+__device__ __forceinline__ float gate_exp(float2 a, float2 b) { return ex2_approx((a.x - b.x) + (a.y - b.y)); }
+// g log2(e), log2(e) = 1.44269502 + 1.92596e-8.
+__device__ __forceinline__ float2 in_base_2(float g) {
+    const float p = g * 1.44269502f;
+    return make_float2(p, fmaf(g, 1.44269502f, -p) + g * 1.92596299e-8f);
+}
 // The exponential of the gates between tokens j < i (1 at j = i).
 __device__ __forceinline__ float decay(const Gates &s, int i, int j) {
     return gate_exp(make_float2(s.hi[i], s.lo[i]), make_float2(s.hi[j], s.lo[j]));
@@ -210,8 +215,8 @@ __device__ __forceinline__ void gates_load(const DeltaArgs &a, const DeltaChunk 
 // One warp.
 __device__ __forceinline__ void gates_put(Gates &s, const float (&g)[2], const float (&b)[2]) {
     const int lane = threadIdx.x & 31;
-    const float2 first = make_float2(g[0], 0.f);
-    float2 sum = two_sum(first, make_float2(g[1], 0.f));
+    const float2 first = in_base_2(g[0]);
+    float2 sum = two_sum(first, in_base_2(g[1]));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float2 x = make_float2(__shfl_up_sync(0xffffffffu, sum.x, o), __shfl_up_sync(0xffffffffu, sum.y, o));

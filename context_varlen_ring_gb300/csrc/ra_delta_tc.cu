@@ -57,7 +57,7 @@ template <int NP>
 constexpr int kColU = NP == 2 ? kColS + 64 * NP : kColS + 32 * NP;
 
 struct ScanParams {
-    CUtensorMap tmQ, tmK, tmV;
+    CUtensorMap tmQ, tmK, tmV, tmO;  // tmO: dout
     DeltaArgs a;
     int keep;
     unsigned long long budget_ns;
@@ -110,8 +110,49 @@ __device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float2 (&x)[
 __device__ __forceinline__ float2 f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 
+// The products, issued by unrolled code (rolled, an issue takes longer than a product of 64 columns: 32768 tokens 390
+// -> 527 us; rolled over the parts alone, the backward's walks 330 -> 346).
+// D [v, token] = A's NP parts [v, dk] (64 columns a part) by 64 rows of K or Q (descriptor b).
 template <int NP>
-__global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
+    bool more = false;
+#pragma unroll
+    for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            tc_mma_ts_w(d, x + 64 * q + 8 * ks, b + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), idesc, more);
+            more = true;
+        }
+}
+// D [v, token] = A's NP parts [v, token] (32 columns a part) by T's or P's parts, `step` bytes apart from 16 tokens to
+// the next; products of parts i, j with i + j < NP, the small ones first.
+template <int NP>
+__device__ __forceinline__ void mma_square(uint32_t d, uint32_t x, uint64_t b, uint32_t step, uint32_t idesc) {
+    bool more = false;
+#pragma unroll
+    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+        for (int q = 0; q <= o; ++q)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                tc_mma_ts_w(d, x + 32 * q + 8 * ks, b + (((uint32_t)(o - q) * kSquare + (uint32_t)ks * step) >> 4), idesc, more);
+                more = true;
+            }
+}
+// D [v, dk] (+)= A's NP parts [v, token] by 64 rows of K or Q, their dk as columns.
+template <int NP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc, bool more) {
+#pragma unroll
+    for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            tc_mma_ts_w(d, x + 32 * q + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), idesc, more);
+            more = true;
+        }
+}
+
+template <int NP>
+__device__ __forceinline__ void scan_body(const ScanParams &p, const int block) {
     using Sh = Shape<NP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Gates gates[2];
@@ -136,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 18);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int seq = a.order[blockIdx.x / a.Hv], h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int seq = a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
     const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0;
     const bool want = a.out != nullptr, keep = p.keep != 0;
 
@@ -222,33 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // S0 by 64 rows of K or of Q: D [v, token]
-                auto by_state = [&](uint32_t d, uint64_t b) {
-#pragma unroll
-                    for (int q = NP - 1; q >= 0; --q)
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ts_w(tmem + d, tmem + kColS + 64 * q + 8 * ks,
-                                        b + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), id64,
-                                        !(q == NP - 1 && ks == 0));
-                };
-                // parts [v, token] by parts of T or P
-                auto by_square = [&](uint32_t d, uint32_t x, uint64_t b, bool more) {
-#pragma unroll
-                    for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                        for (int q = 0; q <= o; ++q)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                tc_mma_ts_w(tmem + d, tmem + x + 32 * q + 8 * ks, b + (((o - q) * kSquare + ks * 32u) >> 4), id64,
-                                            more);
-                                more = true;
-                            }
-                };
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                by_state(kColX, dK);
+                mma_state<NP>(tmem + kColX, tmem + kColS, dK, id64);
                 tc_commit_w(x_full);
                 if (want) {
                     if (i > 0) {
@@ -256,25 +274,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    by_state(kColQ, dQ);
+                    mma_state<NP>(tmem + kColQ, tmem + kColS, dQ, id64);
                 }
                 ok = mbar_wait_warp(r_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                by_square(kColX, kColD, dT, false);
+                mma_square<NP>(tmem + kColX, tmem + kColD, dT, 32, id64);
                 tc_commit_w(u_full);
                 ok = mbar_wait_warp(u_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int q = NP - 1; q >= 0; --q)
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc_mma_ts_w(tmem + kColD, tmem + kColS + 32 * q + 8 * ks, dKn + ((uint32_t)ks * 2048u >> 4), id128,
-                                    !(q == NP - 1 && ks == 0));
+                mma_rows<NP>(tmem + kColD, tmem + kColS, dKn, id128, false);
                 tc_commit_w(d_full);
                 if (want) {
-                    by_square(kColP, kColU<NP>, dP, false);
+                    mma_square<NP>(tmem + kColP, tmem + kColU<NP>, dP, 32, id64);
                     tc_commit_w(o_full);
                 }
                 tc_commit_w(empty + s);
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
 // TMEM columns: 0 the growth of dS; 128 K dS; 192 P^T do; 256 dS's parts, then
 // du's and, behind them, scale e^G do's; in du's place -beta e^G dR's; 448 do.
 template <int NP>
-__global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid_constant__ ScanParams p) {
+__device__ __forceinline__ void back_body(const ScanParams &p, const int block) {
     using Sh = Shape<NP>;
     constexpr int kColY = 192, kColZ = kColS, kColW = kColS + 32 * NP, kColDO = 448;
     static_assert(kColS + 64 * NP <= kColDO, "columns");
@@ -509,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 17);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int seq = a.order[blockIdx.x / a.Hv], h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int seq = a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
     const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0, c1 = c0 + n_chunks - 1;
 
     if (threadIdx.x == 0) {
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid
         fence_mbar_init();
         tma_prefetch_desc(&p.tmQ);
         tma_prefetch_desc(&p.tmK);
-        tma_prefetch_desc(&p.tmV);
+        tma_prefetch_desc(&p.tmO);
     }
     if (warp == 2) {
         tmem_alloc(tmem_slot, 512);
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid
                         tma_load_3d(st + d * kHalf, &p.tmK, full + s, d * 64, hk, tok);
                         tma_load_3d(st + d * kHalf + kHalf / 2, &p.tmQ, full + s, d * 64, hk, tok);
                     }
-                    tma_load_3d(st + Sh::oV, &p.tmV, full + s, 0, h, tok);
+                    tma_load_3d(st + Sh::oV, &p.tmO, full + s, 0, h, tok);
                     bulk_load(st + Sh::oTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, 2 * NP * kSquare, full + s);
                 }
                 // the last copies must have landed before the CTA may exit
@@ -592,56 +605,29 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // parts [v, token] by 64 rows of K or Q: D [v, dk]
-                auto by_rows = [&](uint32_t x, uint64_t b, bool more) {
-#pragma unroll
-                    for (int q = NP - 1; q >= 0; --q)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc_mma_ts_w(tmem + kColD, tmem + x + 32 * q + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id128n, more);
-                            more = true;
-                        }
-                };
                 ok = mbar_wait_warp(y_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int q = NP - 1; q >= 0; --q)  // do by P's rows
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc_mma_ts_w(tmem + kColY, tmem + kColDO + 8 * ks, dP + ((q * kSquare + (uint32_t)ks * 2048u) >> 4), id64n,
-                                    !(q == NP - 1 && ks == 0));
+#pragma unroll 1
+                for (int x = 0; x < 4 * NP; ++x) {  // do by P's rows, the small parts first
+                    const uint32_t q = NP - 1 - x / 4, ks = x % 4;
+                    tc_mma_ts_w(tmem + kColY, tmem + kColDO + 8 * ks, dP + ((q * kSquare + ks * 2048u) >> 4), id64n, x > 0);
+                }
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int q = NP - 1; q >= 0; --q)
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc_mma_ts_w(tmem + kColX, tmem + kColS + 64 * q + 8 * ks,
-                                    dK + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), id64,
-                                    !(q == NP - 1 && ks == 0));
+                mma_state<NP>(tmem + kColX, tmem + kColS, dK, id64);
                 tc_commit_w(x_full);
                 ok = mbar_wait_warp(r_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                bool more = false;
-#pragma unroll
-                for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                    for (int q = 0; q <= o; ++q)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            tc_mma_ts_w(tmem + kColX, tmem + kColZ + 32 * q + 8 * ks,
-                                        dT + (((o - q) * kSquare + (uint32_t)ks * 2048u) >> 4), id64n, more);
-                            more = true;
-                        }
+                mma_square<NP>(tmem + kColX, tmem + kColZ, dT, 2048, id64n);
                 tc_commit_w(u_full);
-                by_rows(kColW, dQn, false);
+                mma_rows<NP>(tmem + kColD, tmem + kColW, dQn, id128n, false);
                 ok = mbar_wait_warp(z_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                by_rows(kColZ, dKn, true);
+                mma_rows<NP>(tmem + kColD, tmem + kColZ, dKn, id128n, true);
                 tc_commit_w(d_full);
                 tc_commit_w(empty + s);
             }
@@ -809,6 +795,24 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_back_kernel(const __grid
     }
 }
 
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
+    scan_body<NP>(p, blockIdx.x);
+}
+// The backward's two walks need nothing of each other, and each is bound by its longest chain, which leaves SMs idle: one
+// launch of both (8192 tokens of 16 heads in 7 documents: 305 and 324 us one behind the other, 333 so).  Blocks of one
+// walk come 16 in a row, the longest first: neighbouring SMs share an instruction cache that does not hold both walks
+// (blocks in turn: 502 us).
+constexpr int kTurn = 16;
+__global__ void __launch_bounds__(kThreads, 1) delta_tc_walks_kernel(const __grid_constant__ ScanParams p) {
+    const int turn = blockIdx.x / kTurn, i = turn / 2 * kTurn + blockIdx.x % kTurn;
+    if (i >= p.a.N * p.a.Hv) return;
+    if (turn & 1)
+        scan_body<3>(p, i);
+    else
+        back_body<3>(p, i);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -837,7 +841,7 @@ bool rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t stride, b
 
 // kernel: one of the walks, of NP parts.
 template <int NP, void (*kernel)(const ScanParams)>
-cudaError_t walk(const ScanParams &p, cudaStream_t st) {
+cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
     static std::atomic<bool> ready[128] = {};
     static_assert(Shape<NP>::smem <= 232448 - 2 * sizeof(Gates), "shared memory of one CTA");
     int dev = 0;
@@ -853,7 +857,7 @@ cudaError_t walk(const ScanParams &p, cudaStream_t st) {
         if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 128) ready[dev] = true;
     }
-    kernel<<<dim3((unsigned)(p.a.N * p.a.Hv)), kThreads, Shape<NP>::smem, st>>>(p);
+    kernel<<<dim3((unsigned)blocks), kThreads, Shape<NP>::smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -861,27 +865,27 @@ cudaError_t walk(const ScanParams &p, cudaStream_t st) {
 
 bool delta_tc_supported(const DeltaArgs &a) { return a.dtype == RA_BF16 && a.dk == kD && a.dv == kD && a.T > 0; }
 
-cudaError_t launch_delta_tc_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
+cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st) {
     ScanParams p;
     memset(&p, 0, sizeof(p));
     if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
         !rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false))
         return cudaErrorInvalidValue;
     p.a = a;
-    p.keep = keep;
     p.budget_ns = wait_budget_ns();
-    return a.parts == 2 ? walk<2, delta_tc_scan_kernel<2>>(p, st) : walk<3, delta_tc_scan_kernel<3>>(p, st);
+    return a.parts == 2 ? walk<2, delta_tc_scan_kernel<2>>(p, a.N * a.Hv, st) : walk<3, delta_tc_scan_kernel<3>>(p, a.N * a.Hv, st);
 }
 
-cudaError_t launch_delta_tc_back(const DeltaArgs &a, cudaStream_t st) {
+cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st) {
     ScanParams p;
     memset(&p, 0, sizeof(p));
     if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
-        !rows_map(&p.tmV, a.dout, a.T, a.Hv, a.dout_stride, false))
+        !rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false) || !rows_map(&p.tmO, a.dout, a.T, a.Hv, a.dout_stride, false))
         return cudaErrorInvalidValue;
     p.a = a;
+    p.keep = 1;
     p.budget_ns = wait_budget_ns();
-    return walk<3, delta_tc_back_kernel<3>>(p, st);
+    return walk<3, delta_tc_walks_kernel>(p, (a.N * a.Hv + kTurn - 1) / kTurn * 2 * kTurn, st);
 }
 
 }  // namespace ra
