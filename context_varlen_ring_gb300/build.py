@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libra.so")
 SOURCES = ["ra_api.cpp", "ra_plan.cpp", "ra_stats.cpp", "ra_misc.cu", "ra_simt.cu", "ra_tc_fwd.cu", "ra_tc_bwd.cu",
            "ra_tc_dq.cu", "ra_noalloc.cu", "ra_tile_build.cu", "ra_rope.cu", "ra_paged.cu", "ra_paged_mma.cu",
-           "ra_paged_tc.cu", "ra_serve.cpp", "ra_delta.cu", "ra_delta_tc.cu", "ra_delta_bwd.cu", "ra_delta.cpp",
+           "ra_paged_tc.cu", "ra_serve.cpp", "ra_delta.cu", "ra_delta_tc.cu", "ra_delta_tc_grads.cu", "ra_delta_bwd.cu", "ra_delta.cpp",
            "ra_weights.cu", "ra_weights_tc.cu", "ra_evict.cu", "ra_keep.cpp"]
 MODULE_SRC = os.path.join(CSRC, "py_serving.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -205,7 +205,7 @@ ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_st
         if (a.max_chunks > 0 && (st = step("ra_delta_scan", s, [&] { return launch_delta_scan(a, 1, s); }))) return st;
         if ((st = step("ra_delta_back", s, [&] { return launch_delta_back(a, s); })) || a.max_chunks == 0) return st;
     }
-    if ((st = step("ra_delta_grads", s, [&] { return launch_delta_grads(a, s); })) || !a.part) return st;
+    if ((st = step("ra_delta_grads", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_grads(a, s) : launch_delta_grads(a, s); })) || !a.part) return st;
     return step("ra_delta_sum", s, [&] { return launch_delta_sum(a, s); });
 }
 

@@ -57,6 +57,7 @@ cudaError_t launch_delta_scan(const DeltaArgs &a, int keep, cudaStream_t st);  /
 bool delta_tc_supported(const DeltaArgs &a);  // the walks on tcgen05 (ra_delta_tc.cu)
 cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st);   // launch_delta_scan that keeps nothing
 cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st);  // launch_delta_scan that keeps, and launch_delta_back
+cudaError_t launch_delta_tc_grads(const DeltaArgs &a, cudaStream_t st);  // launch_delta_grads
 cudaError_t launch_delta_back(const DeltaArgs &a, cudaStream_t st);    // ds, dr and dv, chunk by chunk from the end
 cudaError_t launch_delta_grads(const DeltaArgs &a, cudaStream_t st);   // dq, dk, dg, dbeta of every chunk
 cudaError_t launch_delta_sum(const DeltaArgs &a, cudaStream_t st);     // dq and dk over a key head's value heads

@@ -30,6 +30,7 @@
 #include <mutex>
 
 #include "ra_delta.cuh"
+#include "ra_delta_maps.h"
 #include "ra_internal.h"
 #include "ra_serve.cuh"
 
@@ -72,17 +73,6 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 columns at each of two places, one wait.
-__device__ __forceinline__ void tmem_ld32x2(uint32_t a0, uint32_t a1, uint32_t (&x)[32], uint32_t (&y)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31]),
-          "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15]), "=r"(y[16]), "=r"(y[17]), "=r"(y[18]), "=r"(y[19]), "=r"(y[20]), "=r"(y[21]), "=r"(y[22]), "=r"(y[23]), "=r"(y[24]), "=r"(y[25]), "=r"(y[26]), "=r"(y[27]), "=r"(y[28]), "=r"(y[29]), "=r"(y[30]), "=r"(y[31])
-        : "r"(a0), "r"(a1)
-        : "memory");
-}
 // 2 N floats into bf16 pairs, and what that leaves of them.
 template <int N>
 __device__ __forceinline__ void part(float2 (&x)[N], uint32_t (&h)[N]) {
@@ -826,19 +816,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Rows [T][H][128] of bf16, `stride` elements apart, in boxes of 64 tokens of one head: 64 columns wide with the
-// tensor cores' swizzle, or 128 without.
-bool rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t stride, bool swizzle) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    if (T == 1) stride = (int64_t)H * kD;  // (a single row has no stride)
-    const cuuint64_t dims[3] = {kD, (cuuint64_t)H, (cuuint64_t)T}, strides[2] = {kD * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {swizzle ? 64u : 128u, 1, C}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // kernel: one of the walks, of NP parts.
 template <int NP, void (*kernel)(const ScanParams)>
 cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
@@ -863,13 +840,26 @@ cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
 
 }  // namespace
 
+// Rows [T][H][128] of bf16, `stride` elements apart, in boxes of 64 tokens of one head: 64 columns wide with the
+// tensor cores' swizzle, or 128 without.
+bool delta_rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t stride, bool swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    if (T == 1) stride = (int64_t)H * kD;  // (a single row has no stride)
+    const cuuint64_t dims[3] = {kD, (cuuint64_t)H, (cuuint64_t)T}, strides[2] = {kD * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {swizzle ? 64u : 128u, 1, C}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool delta_tc_supported(const DeltaArgs &a) { return a.dtype == RA_BF16 && a.dk == kD && a.dv == kD && a.T > 0; }
 
 cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st) {
     ScanParams p;
     memset(&p, 0, sizeof(p));
-    if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
-        !rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false))
+    if (!delta_rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !delta_rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
+        !delta_rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false))
         return cudaErrorInvalidValue;
     p.a = a;
     p.budget_ns = wait_budget_ns();
@@ -879,8 +869,8 @@ cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st) {
 cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st) {
     ScanParams p;
     memset(&p, 0, sizeof(p));
-    if (!rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
-        !rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false) || !rows_map(&p.tmO, a.dout, a.T, a.Hv, a.dout_stride, false))
+    if (!delta_rows_map(&p.tmQ, a.q, a.T, a.Hk, a.q_stride, true) || !delta_rows_map(&p.tmK, a.k, a.T, a.Hk, a.k_stride, true) ||
+        !delta_rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false) || !delta_rows_map(&p.tmO, a.dout, a.T, a.Hv, a.dout_stride, false))
         return cudaErrorInvalidValue;
     p.a = a;
     p.keep = 1;
