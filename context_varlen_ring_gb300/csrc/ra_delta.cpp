@@ -46,7 +46,7 @@ int64_t most_chunks(int64_t T, int64_t N) { return T / kDeltaChunk + std::min(T,
 struct Layout {
     size_t hdr, chunk, first, order, tp, s0, ds, u, r, dr, part, bytes;
 };
-Layout layout(int64_t T, int64_t N, int Hk, int Hv, int dk, int dv, int bwd) {
+Layout layout(int64_t T, int64_t N, int Hk, int Hv, int dk, int dv, int dtype, int bwd) {
     Layout L{};
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -66,7 +66,8 @@ Layout layout(int64_t T, int64_t N, int Hk, int Hv, int dk, int dv, int bwd) {
         L.u = take(cells * kDeltaChunk * dv * 4);
         L.r = take(cells * kDeltaChunk * dv * 4);
         L.dr = take(cells * kDeltaChunk * dv * 4);
-        if (Hv != Hk) L.part = take((size_t)T * Hv * dk * 4 * 2);
+        // (the tcgen05 kernel sums a key head's gradients by itself)
+        if (Hv != Hk && !(dtype == RA_BF16 && dk == 128 && dv == 128)) L.part = take((size_t)T * Hv * dk * 4 * 2);
     }
     L.bytes = at;
     return L;
@@ -107,7 +108,7 @@ DeltaArgs arguments(const ra_delta *d, uint8_t *ws, const Layout &L, int bwd) {
         a.u = reinterpret_cast<float *>(ws + L.u);
         a.r = reinterpret_cast<float *>(ws + L.r);
         a.dr = reinterpret_cast<float *>(ws + L.dr);
-        if (d->Hv != d->Hk) a.part = reinterpret_cast<float *>(ws + L.part);
+        if (L.part) a.part = reinterpret_cast<float *>(ws + L.part);
     }
     a.status = device_status_ptr();
     return a;
@@ -144,7 +145,7 @@ extern "C" {
 
 size_t ra_delta_rule_workspace_bytes(int64_t T, int N, int Hk, int Hv, int dk, int dv, int dtype, int bwd) {
     if (check_shape(T, N, Hk, Hv, dk, dv, dtype)) return 0;
-    return layout(T, N, Hk, Hv, dk, dv, bwd).bytes;
+    return layout(T, N, Hk, Hv, dk, dv, dtype, bwd).bytes;
 }
 
 ra_status ra_delta_rule_fwd(const ra_delta *d, void *out, float *state_out, void *workspace, size_t ws_bytes,
@@ -157,7 +158,7 @@ ra_status ra_delta_rule_fwd(const ra_delta *d, void *out, float *state_out, void
     if (!on16(out) || !on16(state_out)) return fail(RA_ERR_UNSUPPORTED, "out and state_out must be 16-byte aligned");
     if (state_out && (d->n_slots < 0 || (!d->slots && d->n_slots < d->N)))
         return fail(RA_ERR_INVALID_ARG, "without slots there must be a state for each sequence");
-    const Layout L = layout(d->T, d->N, d->Hk, d->Hv, d->dk, d->dv, 0);
+    const Layout L = layout(d->T, d->N, d->Hk, d->Hv, d->dk, d->dv, d->dtype, 0);
     if ((st = check_call(d, L, workspace, ws_bytes))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeltaArgs a = arguments(d, static_cast<uint8_t *>(workspace), L, 0);
@@ -184,7 +185,7 @@ ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_st
     if (!on16(dout) || !on16(dq) || !on16(dk) || !on16(dv) || !on16(dstate) || !on16(dstate0) ||
         (d->T > 1 && dout_stride * e % 16))
         return fail(RA_ERR_UNSUPPORTED, "dout, the gradients and the states must be 16-byte aligned, with strides of whole 16 bytes");
-    const Layout L = layout(d->T, d->N, d->Hk, d->Hv, d->dk, d->dv, 1);
+    const Layout L = layout(d->T, d->N, d->Hk, d->Hv, d->dk, d->dv, d->dtype, 1);
     if ((st = check_call(d, L, workspace, ws_bytes))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeltaArgs a = arguments(d, static_cast<uint8_t *>(workspace), L, 1);
@@ -205,7 +206,8 @@ ra_status ra_delta_rule_bwd(const ra_delta *d, const void *dout, int64_t dout_st
         if (a.max_chunks > 0 && (st = step("ra_delta_scan", s, [&] { return launch_delta_scan(a, 1, s); }))) return st;
         if ((st = step("ra_delta_back", s, [&] { return launch_delta_back(a, s); })) || a.max_chunks == 0) return st;
     }
-    if ((st = step("ra_delta_grads", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_grads(a, s) : launch_delta_grads(a, s); })) || !a.part) return st;
+    if ((st = step("ra_delta_grads", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_grads(a, s) : launch_delta_grads(a, s); })) || !a.part)
+        return st;
     return step("ra_delta_sum", s, [&] { return launch_delta_sum(a, s); });
 }
 

@@ -14,7 +14,8 @@
 // A token's sums over dk then are sums over lanes: dG_i = q_i.dq_i
 // - k_i.(dP^T Q + M^T K + F)_i + k_i.(M K + B)_i needs no sums of P's rows and
 // columns, and dbeta_i = dR_i.r_i + k_i.(W K)_i.
-// Persistent CTAs, one a SM.  Every wait is bounded, and what a thread finds of
+// Persistent CTAs, one a SM, take a chunk's value heads of one key head one behind
+// the other and sum their dq and dk in TMEM.  Every wait is bounded, and what a thread finds of
 // one is agreed on by all before the next barrier.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -32,7 +33,7 @@ namespace {
 
 using namespace delta;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kD = 128, kNP = 3;
 constexpr uint32_t kHalf = 16384, kQuarter = 8192;  // 128, 64 rows of 128 bytes
 constexpr uint32_t kOffKQ = 0;                      // [2 halves of dk][K's 64 rows, Q's 64 rows]
@@ -43,7 +44,8 @@ constexpr uint32_t kOffS = kOffU + 3 * kQuarter;    // [S0, dS1][3 parts], of on
 constexpr uint32_t kOffSq = kOffS;                  // [dP, W, M][3 parts], when the products above are done
 constexpr uint32_t kOffBar = kOffS + 6 * kHalf;
 constexpr uint32_t kSmem = kOffBar + 64 + 1024;
-constexpr int kColB = 0, kColQ = 64, kColF = 128, kColP = 192, kColQ2 = 256, kColA2 = 320, kColB2 = 384;
+constexpr int kColB = 0, kColQ = 64, kColF = 128, kColP = 192, kColQ2 = 192, kColA2 = 320, kColB2 = 384;  // (P' is read when Q2 is made)
+constexpr int kColSumQ = 256, kColSumK = 448;  // dq and dk of a key head's value heads so far
 
 struct GradParams {
     CUtensorMap tmQ, tmK, tmO;
@@ -54,7 +56,7 @@ struct GradParams {
 struct Shared {
     Gates g;
     float red[2][4][C];  // of dG and of dbeta: a token's sums over a warp's lanes
-    float rr[C], far[8], ss[8];
+    float rr[C], far[16], ss[16];
 };
 
 __device__ __forceinline__ uint32_t swz(int row, int byte) { return row * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15); }
@@ -69,35 +71,54 @@ __device__ __forceinline__ void put4(uint8_t *tile, int row, int col, float4 x, 
         x.z -= __uint_as_float(b << 16), x.w -= __uint_as_float(b & 0xffff0000u);
     }
 }
-// 32 neighbouring floats of a square's row into its parts.
-__device__ __forceinline__ void put32(uint8_t *square, int row, int half, float (&x)[32]) {
+// 16 neighbouring floats of a square's row, from column 16 c on, into its parts.
+__device__ __forceinline__ void put16(uint8_t *square, int row, int c, float (&x)[16]) {
 #pragma unroll
     for (int p = 0; p < kNP; ++p) {
-        uint32_t h[16];
+        uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
             x[2 * i] -= __uint_as_float(h[i] << 16);
             x[2 * i + 1] -= __uint_as_float(h[i] & 0xffff0000u);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(square + p * kQuarter + swz(row, 64 * half + 16 * i)) =
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4 *>(square + p * kQuarter + swz(row, 32 * c + 16 * i)) =
                 make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
     }
 }
-// The sum over the warp's lanes of x[i], in lane i.
-__device__ __forceinline__ float lane_sums(float (&x)[32]) {
+// The sum over the warp's lanes of x[i], in lanes i and i + 16.
+__device__ __forceinline__ float lane_sums(float (&x)[16]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
+    for (int o = 8; o; o >>= 1)
 #pragma unroll
         for (int i = 0; i < o; ++i) {
             const bool up = lane & o;
             const float send = up ? x[i] : x[i + o], stay = up ? x[i + o] : x[i];
             x[i] = stay + __shfl_xor_sync(0xffffffffu, send, o);
         }
-    return x[0];
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
+}
+// TMEM -> registers: 16 columns, and 16 columns at each of two places; one wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a0, uint32_t a1, uint32_t (&x)[16], uint32_t (&y)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+          "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]), "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15])
+        : "r"(a0), "r"(a1)
+        : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __grid_constant__ GradParams p) {
@@ -135,11 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
                    id64a = idesc_bf16_f32(128, 64, 1, 0), id64ab = idesc_bf16_f32(128, 64, 1, 1);
     uint32_t n_done = 0, n_full = 0;
     bool ok = true;
-    const int64_t cells = (int64_t)a.hdr->chunks * a.Hv;
-    const int quad = warp & 3, half = warp >> 2;
+    const int share = a.Hv / a.Hk;
+    const int64_t units = (int64_t)a.hdr->chunks * a.Hk;
+    const int quad = warp & 3, part = warp >> 2;  // 32 lanes, 16 tokens
     const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
-    for (int64_t cell = blockIdx.x; cell < cells; cell += gridDim.x) {
-        const int c = (int)(cell / a.Hv), h = (int)(cell - (int64_t)c * a.Hv), hk = h / (a.Hv / a.Hk);
+    int turn = 0;  // of the key head's value heads
+    for (int64_t unit = blockIdx.x; unit < units; turn = turn + 1 == share ? 0 : turn + 1, unit += turn ? 0 : gridDim.x) {
+        const int c = (int)(unit / a.Hk), hk = (int)(unit - (int64_t)c * a.Hk), h = hk * share + turn;
+        const int64_t cell = (int64_t)c * a.Hv + h;
         const DeltaChunk ch = a.chunk[c];
         if (tid == 0) {
             mbar_arrive_expect_tx(full, 6 * kQuarter);
@@ -149,26 +173,26 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
                 tma_load_3d(base + kOffRD + d * kHalf + kQuarter, &p.tmO, full, d * 64, h, ch.tok0);
             }
         }
-        if (warp == 7) {
+        if (warp == 15) {
             float g[2], b[2];
             gates_load(a, ch, h, g, b);
             gates_put(sh.g, g, b);
         }
-        float ss = 0.f, rr[4] = {0.f, 0.f, 0.f, 0.f};
+        float ss = 0.f, rr[2] = {0.f, 0.f};
         const uint32_t parts_s[kNP] = {0, kHalf, 2 * kHalf}, parts_u[kNP] = {0, kQuarter, 2 * kQuarter};
 #pragma unroll 1
         for (int v = 0; v < 2 && ok; ++v) {
             // this half's rows, all on their way at once (and beside the last half's products)
-            float4 s0[8], ds[8], u[4], dr[4], r[4];
+            float4 s0[4], ds[4], u[2], dr[2], r[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t x = (cell * kD + (tid >> 4) + 16 * e) * kD + 64 * v + (tid & 15) * 4;
+            for (int e = 0; e < 4; ++e) {
+                const int64_t x = (cell * kD + (tid >> 4) + 32 * e) * kD + 64 * v + (tid & 15) * 4;
                 s0[e] = __ldcs(reinterpret_cast<const float4 *>(a.s0 + x));
                 ds[e] = __ldcs(reinterpret_cast<const float4 *>(a.ds + x));
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t x = (cell * C + (tid >> 4) + 16 * e) * kD + 64 * v + (tid & 15) * 4;
+            for (int e = 0; e < 2; ++e) {
+                const int64_t x = (cell * C + (tid >> 4) + 32 * e) * kD + 64 * v + (tid & 15) * 4;
                 u[e] = __ldcs(reinterpret_cast<const float4 *>(a.u + x));
                 dr[e] = __ldcs(reinterpret_cast<const float4 *>(a.dr + x));
                 r[e] = __ldcs(reinterpret_cast<const float4 *>(a.r + x));
@@ -181,16 +205,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
             }
             const uint32_t parts_r[kNP] = {kOffRD + v * kHalf, kOffR, kOffR + kHalf};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
                 ss += s0[e].x * ds[e].x + s0[e].y * ds[e].y + s0[e].z * ds[e].z + s0[e].w * ds[e].w;
-                put4(base + kOffS, (tid >> 4) + 16 * e, (tid & 15) * 4, s0[e], parts_s);
-                put4(base + kOffS + 3 * kHalf, (tid >> 4) + 16 * e, (tid & 15) * 4, ds[e], parts_s);
+                put4(base + kOffS, (tid >> 4) + 32 * e, (tid & 15) * 4, s0[e], parts_s);
+                put4(base + kOffS + 3 * kHalf, (tid >> 4) + 32 * e, (tid & 15) * 4, ds[e], parts_s);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
                 rr[e] += dr[e].x * r[e].x + dr[e].y * r[e].y + dr[e].z * r[e].z + dr[e].w * r[e].w;
-                put4(base + kOffU, (tid >> 4) + 16 * e, (tid & 15) * 4, u[e], parts_u);
-                put4(base, (tid >> 4) + 16 * e, (tid & 15) * 4, dr[e], parts_r);
+                put4(base + kOffU, (tid >> 4) + 32 * e, (tid & 15) * 4, u[e], parts_u);
+                put4(base, (tid >> 4) + 32 * e, (tid & 15) * 4, dr[e], parts_r);
             }
             if (v == 0) {
                 ok = mbar_wait(full, n_full++ & 1u, wc);
@@ -241,27 +265,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
         {
             const int row = quad * 32 + lane, i = row & 63;  // lanes 0 to 63: dR u^T, 64 to 127: do u^T
             const bool w = quad < 2;
-            uint32_t x[32];
-            float y[32];
-            tmem_ld32(at + kColP + 32 * half, x);
+            uint32_t x[16];
+            float y[16];
+            tmem_ld16(at + kColP + 16 * part, x);
             const float f = w ? -1.f : a.scale;
             const float2 me = make_float2(sh.g.hi[i], sh.g.lo[i]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int t = 32 * half + j;
+            for (int j = 0; j < 16; ++j) {
+                const int t = 16 * part + j;
                 const float D = gate_exp(me, make_float2(sh.g.hi[t], sh.g.lo[t]));
                 y[j] = t + (w ? 1 : 0) <= i ? f * D * __uint_as_float(x[j]) : 0.f;
             }
             uint8_t *sq = base + kOffSq;
             if (w) {
-                float z[32];
+                float z[16];
                 const float b = sh.g.beta[i];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = b * y[j];
-                put32(sq + 3 * kQuarter, i, half, y);
-                put32(sq + 6 * kQuarter, i, half, z);
+                for (int j = 0; j < 16; ++j) z[j] = b * y[j];
+                put16(sq + 3 * kQuarter, i, part, y);
+                put16(sq + 6 * kQuarter, i, part, z);
             } else {
-                put32(sq, i, half, y);
+                put16(sq, i, part, y);
             }
         }
         tc_fence_before();
@@ -286,12 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
             by(kColB2, K, 1, 16, 32, id64a, true);
             tc_commit_w(done);
         }
-        // (beside them: sums of what was loaded)
+        // beside them: the next cell's way to L2, a line of 128 bytes a thread and turn; and sums of what was loaded
+        const int64_t next_unit = turn + 1 < share ? unit : unit + gridDim.x;
+        if (next_unit < units) {
+            const int64_t next = next_unit * share + (turn + 1 < share ? turn + 1 : 0);  // (units and cells are in one order)
+            auto fetch = [&](const float *x, int floats) {
+                for (int i = tid * 32; i < floats; i += kThreads * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + next * floats + i));
+            };
+            fetch(a.s0, kD * kD);
+            fetch(a.ds, kD * kD);
+            fetch(a.u, C * kD);
+            fetch(a.dr, C * kD);
+            fetch(a.r, C * kD);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) rr[e] += __shfl_xor_sync(0xffffffffu, rr[e], o);
-            if ((tid & 15) == 0) sh.rr[(tid >> 4) + 16 * e] = rr[e];
+            if ((tid & 15) == 0) sh.rr[(tid >> 4) + 32 * e] = rr[e];
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -302,55 +338,69 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
         tc_fence_after();
         {
             const int m = quad * 32 + lane;  // dk
-            float far = 0.f, sum[32], db[32];
+            float far = 0.f, sum[16], db[16];
             const uint8_t *kq = base + kOffKQ + (m >> 6) * kHalf;
-            const int64_t stride = (int64_t)a.Hv * kD, o0 = ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
-            const int rows = ch.n - 32 * half;
+            const int64_t stride = (int64_t)a.Hk * kD, o0 = ((int64_t)(ch.tok0 + 16 * part) * a.Hk + hk) * kD + m;
+            const int rows = ch.n - 16 * part;
+            // a gradient of this head: to the sums, or with them to the tensor
+            auto put = [&](uint32_t col, float (&x)[16], void *to) {
+                if (turn > 0) {
+                    uint32_t s[16];
+                    tmem_ld16(at + col + 16 * part, s);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(s[j]);
+                }
+                if (turn + 1 < share) {
+                    uint32_t s[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(x[j]);
+                    tmem_st16(at + col + 16 * part, s);
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < rows) static_cast<bf16 *>(to)[o0 + j * stride] = __float2bfloat16_rn(x[j]);
+            };
             auto value = [&](int row) {
                 return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(kq + swz(row, (m & 63) * 2)) << 16);
             };
-            uint32_t x[32], y[32];
-            tmem_ld32x2(at + kColQ + 32 * half, at + kColQ2 + 32 * half, x, y);
+            uint32_t x[16], y[16];
+            tmem_ld16x2(at + kColQ + 16 * part, at + kColQ2 + 16 * part, x, y);
+            float dq[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int t = 32 * half + j;
-                const float dq = fmaf(a.scale * sh.g.eG[t], __uint_as_float(x[j]), __uint_as_float(y[j]));
-                sum[j] = value(C + t) * dq;
-                if (j < rows) {
-                    if (a.part)
-                        a.part[o0 + j * stride] = dq;
-                    else
-                        static_cast<bf16 *>(a.dq)[o0 + j * stride] = __float2bfloat16_rn(dq);
-                }
+            for (int j = 0; j < 16; ++j) {
+                const int t = 16 * part + j;
+                dq[j] = fmaf(a.scale * sh.g.eG[t], __uint_as_float(x[j]), __uint_as_float(y[j]));
+                sum[j] = value(C + t) * dq[j];
             }
-            tmem_ld32x2(at + kColF + 32 * half, at + kColA2 + 32 * half, x, y);
-            float dk[32];
+            put(kColSumQ, dq, a.dq);
+            tmem_ld16x2(at + kColF + 16 * part, at + kColA2 + 16 * part, x, y);
+            float dk[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int t = 32 * half + j;
+            for (int j = 0; j < 16; ++j) {
+                const int t = 16 * part + j;
                 const float k = value(t), F = sh.g.eL[t] * __uint_as_float(x[j]);
                 far += F * k;
                 dk[j] = F + __uint_as_float(y[j]);
                 sum[j] -= k * dk[j];
             }
-            tmem_ld32x2(at + kColB + 32 * half, at + kColB2 + 32 * half, x, y);
+            tmem_ld16x2(at + kColB + 16 * part, at + kColB2 + 16 * part, x, y);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int t = 32 * half + j;
+            for (int j = 0; j < 16; ++j) {
+                const int t = 16 * part + j;
                 const float k = value(t), W = __uint_as_float(y[j]);
                 const float b = sh.g.beta[t] * fmaf(-sh.g.eG[t], __uint_as_float(x[j]), W);
                 db[j] = k * W;
                 sum[j] += k * b;
-                if (j < rows) {
-                    if (a.part)
-                        a.part[a.T * stride + o0 + j * stride] = dk[j] + b;
-                    else
-                        static_cast<bf16 *>(a.dk_)[o0 + j * stride] = __float2bfloat16_rn(dk[j] + b);
-                }
+                dk[j] += b;
             }
+            put(kColSumK, dk, a.dk_);
             tc_fence_before();
-            sh.red[0][quad][32 * half + lane] = lane_sums(sum);
-            sh.red[1][quad][32 * half + lane] = lane_sums(db);
+            const float r0 = lane_sums(sum), r1 = lane_sums(db);
+            if (lane < 16) {
+                sh.red[0][quad][16 * part + lane] = r0;
+                sh.red[1][quad][16 * part + lane] = r1;
+            }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) far += __shfl_xor_sync(0xffffffffu, far, o);
             if (lane == 0) sh.far[warp] = far;
@@ -359,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
         if (warp == 0) {  // the gates: sums from each token to the chunk's end
             float end = 0.f, s = 0.f, x[2];
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < 16; ++w) {
                 end += sh.far[w];
                 s += sh.ss[w];
             }
