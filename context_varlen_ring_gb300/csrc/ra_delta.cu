@@ -125,10 +125,12 @@ struct LocalSmem {
 template <typename E, int NP, int DK>
 __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaArgs a) {
     using Smem = LocalSmem<E, NP, DK>;
+    constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, LD = Smem::LD, PL = C * LD * 2, PT = C * kLdc * 2, PY = 32 * kLdy * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_ahead();
     if (c >= a.hdr->chunks) return;
     const DeltaChunk ch = a.chunk[c];
     const int hk = h / (a.Hv / a.Hk);
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     const uint32_t kb = smem_u32(sm.in.k), row = row0 * LD * 2;
     float x[8][4];
     zero(x);
-    mm<8, NPI, NPI, 3, false, false>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
+    mm<8, NPI, NPI, 3, false, false, EX>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
     __syncthreads();  // (P takes the place of K and Q)
 #pragma unroll
     for (int n = 0; n < 8; ++n)
@@ -217,22 +219,22 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     float y[2][4];
     if (w & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
         zero(y);
-        mm<2, NP, NP, NP, false, true>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
+        mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
         put(&sm.Y[0][(w >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
         __syncwarp();
         zero(y);
-        mm<2, NP, NP, NP, false, true>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
+        mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
         put(&sm.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
     }
     sync();
     {  // rows 32 .. 63 by columns 0 .. 31: a block of 16 x 16 each warp
         const int r = (w >> 1) * 16, col = (w & 1) * 16;
         zero(y);
-        mm<2, NP, NP, NP, false, true>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
+        mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
         put(&sm.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
         sync();
         zero(y);
-        mm<2, NP, NP, NP, false, true>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
+        mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
         put(&sm.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
     }
     sync();
@@ -255,11 +257,13 @@ struct ScanSmem {
 template <typename E, int NP, int DK, int DVS>
 __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const DeltaArgs a, int keep) {
     using Smem = ScanSmem<E, NP, DK, DVS>;
+    constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
     constexpr int MW = DK / 16, NS = DVS / 8 / (8 / MW), NX = DVS / 16;  // n-tiles of a warp: of S, of rows of the chunk
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
+    wait_ahead();
     if (a.hdr->bad) return;
     const int slices = a.dv / DVS, per = a.Hv * slices;
     const int seq = a.order[blockIdx.x / per], h = blockIdx.x % per / slices, v0 = blockIdx.x % slices * DVS;
@@ -352,11 +356,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         cp_commit();
         float x[NX][4], o[NX][4];
         zero(x);
-        mm<NX, NPI, NP, NP, false, true>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+        mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                          DK);
         if (want) {
             zero(o);
-            mm<NX, NPI, NP, NP, false, true>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+            mm<NX, NPI, NP, NP, false, true, EX>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                              DK);
         }
 #pragma unroll
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         if (KB == 2 && want && c + 1 < c1) load_q(c + 1);
         cp_commit();
         zero(x);
-        mm<NX, NP, NP, NP, false, true>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR, 0,
+        mm<NX, NP, NP, NP, false, true, EX>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR, 0,
                                         xrow + 16);
 #pragma unroll
         for (int n = 0; n < NX; ++n)
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
                 put2<NP>(&sm.R[0][i][j], C * LV, g.eL[i] * x[n][2 * hf], g.eL[i] * x[n][2 * hf + 1]);
             }
         if (want) {
-            mm<NX, NP, NP, NP, false, true>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
+            mm<NX, NP, NP, NP, false, true, EX>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
                                             0, xrow + 16);
 #pragma unroll
             for (int n = 0; n < NX; ++n)
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
-        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
+        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
     }
     cp_wait<0>();
     if (a.state_out && slot >= 0) {
@@ -523,8 +527,7 @@ cudaError_t local(const DeltaArgs &a, cudaStream_t st) {
     const size_t smem = sizeof(LocalSmem<E, NP, DK>);
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kLocalThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(a.max_chunks, a.Hv), kLocalThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_next(kernel, dim3(a.max_chunks, a.Hv), kLocalThreads, smem, st, a);
 }
 template <typename E, int NP, int DK, int DVS>
 cudaError_t scan(const DeltaArgs &a, int keep, cudaStream_t st) {
@@ -534,8 +537,7 @@ cudaError_t scan(const DeltaArgs &a, int keep, cudaStream_t st) {
     static_assert(sizeof(ScanSmem<E, NP, DK, DVS>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kScanThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kScanThreads, smem, st>>>(a, keep);
-    return cudaGetLastError();
+    return launch_next(kernel, dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kScanThreads, smem, st, a, keep);
 }
 
 }  // namespace

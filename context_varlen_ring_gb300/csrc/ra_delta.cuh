@@ -56,8 +56,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // 16), operands of PA and PB parts, products of parts i, j with i + j < NP.
 // a, b: shared addresses of A's and B's first element; lda, ldb: pitches in
 // elements; pa, pb: bytes between parts.  TA: A is stored [K][M]; BKN: B is
-// stored [K][N], else [N][K].
-template <int NT, int PA, int PB, int NP, bool TA, bool BKN>
+// stored [K][N], else [N][K].  EX: every 16 of K are summed by themselves and
+// added to acc in fp32, because the tensor cores cut what they add to an
+// accumulator, always towards 0 (fp32 gradients off by 1.5e-6 of their norm
+// without, 1.6e-7 with).
+template <int NT, int PA, int PB, int NP, bool TA, bool BKN, bool EX = false>
 __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int pa, uint32_t b, int ldb, int pb, int k0,
                                    int k1, int pairs = NT / 2) {
     const int l = threadIdx.x & 31, r = l & 7, s = (l >> 3) & 1, h = l >> 4;
@@ -75,6 +78,8 @@ __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int
             uint32_t fb[PB][4];
 #pragma unroll
             for (int j = 0; j < PB; ++j) ldsm4<BKN>(b + j * pb + k * bs + n * bn, fb[j]);
+            float own[2][4] = {};
+            float(&c0)[4] = EX ? own[0] : acc[2 * n], (&c1)[4] = EX ? own[1] : acc[2 * n + 1];
             // (the small products first)
 #pragma unroll
             for (int o = NP - 1; o >= 0; --o)
@@ -82,9 +87,16 @@ __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int
                 for (int i = 0; i < PA; ++i) {
                     const int j = o - i;
                     if (j < 0 || j >= PB) continue;
-                    mma(acc[2 * n], fa[i], fb[j][0], fb[j][1]);
-                    mma(acc[2 * n + 1], fa[i], fb[j][2], fb[j][3]);
+                    mma(c0, fa[i], fb[j][0], fb[j][1]);
+                    mma(c1, fa[i], fb[j][2], fb[j][3]);
                 }
+            if (EX) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[2 * n][i] += own[0][i];
+                    acc[2 * n + 1][i] += own[1][i];
+                }
+            }
         }
     }
 }
@@ -256,6 +268,24 @@ __device__ __forceinline__ int64_t slot_of(const int32_t *slots, int64_t n_slots
     if (s >= 0 && s < n_slots) return s;
     if (s >= n_slots) record_status(status, RA_ERR_DEVICE_BOUNDS);
     return -1;
+}
+
+// The kernels of a call but the first are launched as programmatic successors: their blocks are set up while the
+// kernel ahead ends, and wait for it before they read what it wrote.
+__device__ __forceinline__ void wait_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 }  // namespace delta

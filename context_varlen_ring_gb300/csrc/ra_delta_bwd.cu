@@ -45,11 +45,13 @@ struct BackSmem {
 template <typename E, int NP, int DK, int DVS>
 __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs a) {
     using Smem = BackSmem<E, NP, DK, DVS>;
+    constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
     constexpr int MW = DK / 16, NS = DVS / 8 / (8 / MW), NX = DVS / 16;
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
+    wait_ahead();
     if (a.hdr->bad) return;
     const int slices = a.dv / DVS, per = a.Hv * slices;
     const int seq = a.order[blockIdx.x / per], h = blockIdx.x % per / slices, v0 = blockIdx.x % slices * DVS;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         if (KB == 2 && c > c0) load_k(c - 1, buf ^ 1);
         float x[NX][4];
         zero(x);
-        mm<NX, NPI, NP, NP, false, true>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+        mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                          DK);
 #pragma unroll
         for (int n = 0; n < NX; ++n)
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
                 x[n][2 * hf] *= e;
                 x[n][2 * hf + 1] *= e;
             }
-        mm<NX, NP, NPI, NP, true, true>(x, smem_u32(sm.P) + xrow * 2, kLdc, PT, smem_u32(sm.Y) + xcol * 2, LV, PR, xrow, C);
+        mm<NX, NP, NPI, NP, true, true, EX>(x, smem_u32(sm.P) + xrow * 2, kLdc, PT, smem_u32(sm.Y) + xcol * 2, LV, PR, xrow, C);
 #pragma unroll
         for (int n = 0; n < NX; ++n)
 #pragma unroll
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         if (c > c0) load_tp(c - 1, 1);
         cp_commit();  // (with the next K)
         zero(x);
-        mm<NX, NP, NP, NP, true, true>(x, smem_u32(sm.T) + xrow * 2, kLdc, PT, smem_u32(sm.X) + xcol * 2, LV, PR, xrow, C);
+        mm<NX, NP, NP, NP, true, true, EX>(x, smem_u32(sm.T) + xrow * 2, kLdc, PT, smem_u32(sm.X) + xcol * 2, LV, PR, xrow, C);
         cp_wait<1>();  // Q (behind it the next K and P)
         __syncthreads();
         if (c > c0) load_tp(c - 1, 0);
@@ -181,8 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
-        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.q) + srow * 2, LD, PK, smem_u32(sm.X) + scol * 2, LV, PR, 0, C);
-        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.Y) + scol * 2, LV, PR, 0, C);
+        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.q) + srow * 2, LD, PK, smem_u32(sm.X) + scol * 2, LV, PR, 0, C);
+        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.Y) + scol * 2, LV, PR, 0, C);
     }
     cp_wait<0>();
     if (a.dstate0) {
@@ -221,12 +223,14 @@ struct GradSmem {
 template <typename E, int NP, int DK>
 __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArgs a) {
     using Smem = GradSmem<E, NP, DK>;
+    constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, LD = Smem::LD, LV = Smem::LV;
     constexpr int NK = DK / 16;  // n-tiles of a warp along dk
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_ahead();
     if (c >= a.hdr->chunks) return;
     const DeltaChunk ch = a.chunk[c];
     const int hk = h / (a.Hv / a.Hk), dv = a.dv;
@@ -281,11 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         __syncthreads();
         const uint32_t d = smem_u32(sm.v.d) + row0 * LV * 2, u = smem_u32(sm.v.u), dr = smem_u32(sm.v.dr) + row0 * LV * 2;
         const uint32_t s0 = smem_u32(sm.v.s0) + kcol * LV * 2, ds = smem_u32(sm.v.ds) + kcol * LV * 2;
-        mm<NK, NPI, NP, NP, false, false>(dq, d, LV, PR, s0, LV, PS, 0, kVS);
-        mm<NK, NP, NP, NP, false, false>(F, u + row0 * LV * 2, LV, PR, ds, LV, PS, 0, kVS);
-        mm<NK, NP, NP, NP, false, false>(B, dr, LV, PR, s0, LV, PS, 0, kVS);
-        mm<4, NPI, NP, NP, false, false>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
-        mm<4, NP, NP, NP, false, false>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<NK, NPI, NP, NP, false, false, EX>(dq, d, LV, PR, s0, LV, PS, 0, kVS);
+        mm<NK, NP, NP, NP, false, false, EX>(F, u + row0 * LV * 2, LV, PR, ds, LV, PS, 0, kVS);
+        mm<NK, NP, NP, NP, false, false, EX>(B, dr, LV, PR, s0, LV, PS, 0, kVS);
+        mm<4, NPI, NP, NP, false, false, EX>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<4, NP, NP, NP, false, false, EX>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
     }
     // sums of rows over the four threads that hold them
     rr += __shfl_xor_sync(0xffffffffu, rr, 1);
@@ -297,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         float kk[4][4], qk[4][4];
         zero(kk);
         zero(qk);
-        mm<4, NPI, NPI, 3, false, false>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
-        mm<4, NPI, NPI, 3, false, false>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        mm<4, NPI, NPI, 3, false, false, EX>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        mm<4, NPI, NPI, 3, false, false, EX>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
         __syncthreads();  // (the slices' products: dP and M take their place)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -401,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         if (2 * lane + 1 < ch.n) a.dg[at + a.Hv] = x[1] + after + end;
     }
     const uint32_t Pb = smem_u32(sm.c.dP), Mb = smem_u32(sm.c.M);
-    mm<NK, NP, NPI, NP, false, true>(dq, Pb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
-    mm<NK, NP, NPI, NP, true, true>(F, Pb + row0 * 2, kLdc, PT, qb + kcol * 2, LD, PK, row0, C);
-    mm<NK, NP, NPI, NP, false, true>(F, Mb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
-    mm<NK, NP, NPI, NP, true, true>(F, Mb + row0 * 2, kLdc, PT, kb + kcol * 2, LD, PK, row0, C);
+    mm<NK, NP, NPI, NP, false, true, EX>(dq, Pb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
+    mm<NK, NP, NPI, NP, true, true, EX>(F, Pb + row0 * 2, kLdc, PT, qb + kcol * 2, LD, PK, row0, C);
+    mm<NK, NP, NPI, NP, false, true, EX>(F, Mb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
+    mm<NK, NP, NPI, NP, true, true, EX>(F, Mb + row0 * 2, kLdc, PT, kb + kcol * 2, LD, PK, row0, C);
 #pragma unroll
     for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -426,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
 // dq and dk of a key head: the sum over its value heads, in their order, rounded once.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) delta_sum_kernel(const DeltaArgs a) {
+    wait_ahead();
     if (a.hdr->bad) return;
     const int share = a.Hv / a.Hk, vec = a.dk / 4;
     const int64_t t0 = a.cu[0], t1 = a.cu[a.N], n = (t1 - t0) * a.Hk * vec;
@@ -452,8 +457,7 @@ cudaError_t back(const DeltaArgs &a, cudaStream_t st) {
     static_assert(sizeof(BackSmem<E, NP, DK, DVS>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_next(kernel, dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kThreads, smem, st, a);
 }
 template <typename E, int NP, int DK>
 cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
@@ -463,8 +467,7 @@ cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
     static_assert(sizeof(GradSmem<E, NP, DK>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(a.max_chunks, a.Hv), kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_next(kernel, dim3(a.max_chunks, a.Hv), kThreads, smem, st, a);
 }
 
 }  // namespace
@@ -480,11 +483,7 @@ cudaError_t launch_delta_grads(const DeltaArgs &a, cudaStream_t st) {
 cudaError_t launch_delta_sum(const DeltaArgs &a, cudaStream_t st) {
     const int64_t n = 2 * a.T * a.Hk * (a.dk / 4);
     const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads < 8192 ? (n + kThreads - 1) / kThreads : 8192);
-    if (a.dtype == RA_FP32)
-        delta_sum_kernel<float><<<grid, kThreads, 0, st>>>(a);
-    else
-        delta_sum_kernel<bf16><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_next(a.dtype == RA_FP32 ? delta_sum_kernel<float> : delta_sum_kernel<bf16>, dim3(grid), kThreads, 0, st, a);
 }
 
 }  // namespace ra

@@ -147,7 +147,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
     extern __shared__ uint8_t smem_raw[];
     __shared__ Gates gates[2];
     const DeltaArgs &a = p.a;
-    if (a.hdr->bad) return;
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - raw_s);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
@@ -167,9 +166,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 18);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int seq = a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
-    const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0;
-    const bool want = a.out != nullptr, keep = p.keep != 0;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -200,6 +196,11 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_ahead();
+    const bool want = a.out != nullptr, keep = p.keep != 0;
+    const bool bad = a.hdr->bad != 0;  // (boundaries without a plan: nothing is written)
+    const int seq = bad ? 0 : a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int c0 = bad ? 0 : a.first[seq], n_chunks = bad ? 0 : a.first[seq + 1] - c0;
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, a.status, p.budget_ns};
 
@@ -304,7 +305,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
         // ------------------------------------------------ the state, and what the products read
         const int half = warp >= 8 ? 1 : 0, m = (warp & 3) * 32 + lane;  // TMEM lane: the column of v
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int64_t slot = a.state || a.state_out ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
+        const int64_t slot = !bad && (a.state || a.state_out) ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
         const int64_t place = ((slot * a.Hv + h) * kD + 64 * half) * kD + m;
         float2 S[32];
 #pragma unroll
@@ -462,7 +463,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             }
         }
         if (ok && want && n_chunks > 0) output(n_chunks - 1, ch);
-        if (ok && a.state_out && slot >= 0) {
+        if (ok && !bad && a.state_out && slot >= 0) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 a.state_out[place + 2 * j * kD] = S[j].x;
@@ -493,7 +494,6 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     extern __shared__ uint8_t smem_raw[];
     __shared__ Gates gates[2];
     const DeltaArgs &a = p.a;
-    if (a.hdr->bad) return;
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - raw_s);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
@@ -512,8 +512,6 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 17);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int seq = a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
-    const int c0 = a.first[seq], n_chunks = a.first[seq + 1] - c0, c1 = c0 + n_chunks - 1;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -543,6 +541,10 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_ahead();
+    const bool bad = a.hdr->bad != 0;
+    const int seq = bad ? 0 : a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int c0 = bad ? 0 : a.first[seq], n_chunks = bad ? 0 : a.first[seq + 1] - c0, c1 = c0 + n_chunks - 1;
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{abort_flag, a.status, p.budget_ns};
 
@@ -769,7 +771,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                 for (int j = 0; j < 32; ++j) S[j] = fma2(eC, S[j], f2(x[2 * j], x[2 * j + 1]));
             }
         }
-        if (ok && a.dstate0) {
+        if (ok && !bad && a.dstate0) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 a.dstate0[place + 2 * j * kD] = S[j].x;
@@ -834,8 +836,7 @@ cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
         if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 128) ready[dev] = true;
     }
-    kernel<<<dim3((unsigned)blocks), kThreads, Shape<NP>::smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_next(kernel, dim3((unsigned)blocks), kThreads, Shape<NP>::smem, st, p);
 }
 
 }  // namespace

@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
                    id64a = idesc_bf16_f32(128, 64, 1, 0), id64ab = idesc_bf16_f32(128, 64, 1, 1);
     uint32_t n_done = 0, n_full = 0;
     bool ok = true;
+    wait_ahead();
     const int share = a.Hv / a.Hk;
     const int64_t units = (int64_t)a.hdr->chunks * a.Hk;
     const int quad = warp & 3, part = warp >> 2;  // 32 lanes, 16 tokens
@@ -466,8 +467,7 @@ cudaError_t launch_delta_tc_grads(const DeltaArgs &a, cudaStream_t st) {
     static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(delta_tc_grads_kernel), kThreads, kSmem, nullptr);
     if (e != cudaSuccess) return e;
-    delta_tc_grads_kernel<<<paged_sms(), kThreads, kSmem, st>>>(p);
-    return cudaGetLastError();
+    return launch_next(delta_tc_grads_kernel, dim3(paged_sms()), kThreads, kSmem, st, p);
 }
 
 }  // namespace ra
