@@ -79,7 +79,7 @@ __device__ __forceinline__ void part(float2 (&x)[N], uint32_t (&h)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         h[i] = pack_bf16x2(x[i].x, x[i].y);
-        x[i] = add2(x[i], make_float2(__uint_as_float((h[i] << 16) ^ 0x80000000u), __uint_as_float((h[i] & 0xffff0000u) ^ 0x80000000u)));
+        x[i] = fma2(make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)), make_float2(-1.f, -1.f), x[i]);
     }
 }
 // 32 values as NP parts of 16 columns, `apart` columns from each other (to be waited for).
@@ -329,21 +329,44 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             const int64_t stride = (int64_t)a.Hv * kD;
             bf16 *o = static_cast<bf16 *>(a.out) + ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
             const int rows = ch.n - 32 * half;
+            auto put = [&](bool all) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 e = four(g.eG, j);
-                const float2 s = make_float2(a.scale, a.scale);
-                const float2 p0 = fma2(mul2(s, make_float2(e.x, e.y)), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
-                const float2 p1 = fma2(mul2(s, make_float2(e.z, e.w)), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
-                if (4 * j < rows) o[0] = __float2bfloat16_rn(p0.x);
-                if (4 * j + 1 < rows) o[stride] = __float2bfloat16_rn(p0.y);
-                if (4 * j + 2 < rows) o[2 * stride] = __float2bfloat16_rn(p1.x);
-                if (4 * j + 3 < rows) o[3 * stride] = __float2bfloat16_rn(p1.y);
-                o += 4 * stride;
-            }
+                for (int j = 0; j < 8; ++j) {
+                    const float4 e = four(g.eG, j);
+                    const float2 s = make_float2(a.scale, a.scale);
+                    const float2 p0 = fma2(mul2(s, make_float2(e.x, e.y)), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
+                    const float2 p1 = fma2(mul2(s, make_float2(e.z, e.w)), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
+                    if (all || 4 * j < rows) o[0] = __float2bfloat16_rn(p0.x);
+                    if (all || 4 * j + 1 < rows) o[stride] = __float2bfloat16_rn(p0.y);
+                    if (all || 4 * j + 2 < rows) o[2 * stride] = __float2bfloat16_rn(p1.x);
+                    if (all || 4 * j + 3 < rows) o[3 * stride] = __float2bfloat16_rn(p1.y);
+                    o += 4 * stride;
+                }
+            };
+            if (rows >= 32)
+                put(true);
+            else
+                put(false);
             __syncwarp();
             if (lane == 0) mbar_arrive(g_empty + (i & 1));
         };
+        // chunk i's values, pairs of tokens as they are: taken while the chunk ahead waits for its products
+        uint32_t d[16];
+        auto take = [&](int i) {
+            ok = mbar_wait_warp(full + (i & 1), (i >> 1) & 1u, wc);
+            if (!ok) return;
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * Sh::stage + Sh::oV) + 32 * half * kD + m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) d[j] = x[2 * j * kD] | (uint32_t)x[(2 * j + 1) * kD] << 16;
+            const int rows = a.chunk[c0 + i].n - 32 * half;
+            if (rows < 32) {  // (rows behind the sequence's end are another's, or none)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) d[j] = 2 * j + 1 < rows ? d[j] : 2 * j < rows ? d[j] & 0xffffu : 0u;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + (i & 1));
+        };
+        if (n_chunks > 0) take(0);
         DeltaChunk ch{0, 0}, last;
 #pragma unroll 1
         for (int i = 0; i < n_chunks && ok; ++i) {
@@ -378,32 +401,22 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 output(i - 1, last);
                 if (!ok) break;
             }
-            ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc) && mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
+            ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc);
             if (!ok) break;
             const Gates &g = gates[s];
-            float2 v[16];
-            const bf16 *vp = reinterpret_cast<const bf16 *>(base + s * Sh::stage + Sh::oV) + 32 * half * kD + m;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v[j] = make_float2(__bfloat162float(vp[2 * j * kD]), __bfloat162float(vp[(2 * j + 1) * kD]));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + s);
             ok = mbar_wait_warp(x_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
+            float2 v[16];
             {
                 uint32_t x[32];
                 tmem_ld32(at + kColX + 32 * half, x);
                 float *p = a.r + (cell * C + 32 * half) * kD + m;
-                const int rows = ch.n - 32 * half;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float4 e = four(g.eG, j), b = four(g.beta, j);
-                    float2 r0 = fma2(make_float2(-e.x, -e.y), f2(x[4 * j], x[4 * j + 1]), v[2 * j]);
-                    float2 r1 = fma2(make_float2(-e.z, -e.w), f2(x[4 * j + 2], x[4 * j + 3]), v[2 * j + 1]);
-                    // (rows of v behind the sequence's end are another's, or none)
-                    r0 = make_float2(4 * j < rows ? r0.x : 0.f, 4 * j + 1 < rows ? r0.y : 0.f);
-                    r1 = make_float2(4 * j + 2 < rows ? r1.x : 0.f, 4 * j + 3 < rows ? r1.y : 0.f);
+                    const float2 r0 = fma2(make_float2(-e.x, -e.y), f2(x[4 * j], x[4 * j + 1]), f2(d[2 * j] << 16, d[2 * j] & 0xffff0000u));
+                    const float2 r1 = fma2(make_float2(-e.z, -e.w), f2(x[4 * j + 2], x[4 * j + 3]), f2(d[2 * j + 1] << 16, d[2 * j + 1] & 0xffff0000u));
                     if (keep) {
                         p[4 * j * kD] = r0.x;
                         p[(4 * j + 1) * kD] = r0.y;
@@ -451,6 +464,10 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             if (!want) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(g_empty + s);
+            }
+            if (i + 1 < n_chunks) {
+                take(i + 1);
+                if (!ok) break;
             }
             ok = mbar_wait_warp(d_full, ph, wc);
             if (!ok) break;
