@@ -112,13 +112,15 @@ struct LocalSmem {
     struct Rows {
         bf16 k[NPI][C][LD], q[NPI][C][LD];
     };
+    struct Made {
+        bf16 P[NP][C][kLdc], Y[NP][32][kLdy];
+        float diag[4][16][17];
+    };
     union {
         Rows in;
-        bf16 P[NP][C][kLdc];  // (when the products are done)
+        Made made;  // when the products with K and Q are done
     };
     bf16 A[NP][C][kLdc], T[NP][C][kLdc];
-    bf16 Y[NP][32][kLdy];
-    float diag[4][16][17];
     Gates g;
 };
 
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     float x[8][4];
     zero(x);
     mm<8, NPI, NPI, 3, false, false, EX>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
-    __syncthreads();  // (P takes the place of K and Q)
+    __syncthreads();  // (what is made of them takes the place of K and Q)
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -167,12 +169,12 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
                     if (j + e + own <= i) y[e] = f * decay(sm.g, i, j + e) * x[n][2 * hf + e];
             }
             if (!own) {
-                put2<NP>(&sm.P[0][i][j], C * kLdc, y[0], y[1]);
+                put2<NP>(&sm.made.P[0][i][j], C * kLdc, y[0], y[1]);
             } else if (n / 2 <= w) {
                 put2<NP>(&sm.A[0][i][j], C * kLdc, y[0], y[1]);
                 if (n / 2 == w) {
-                    sm.diag[w][i & 15][j & 15] = y[0];
-                    sm.diag[w][i & 15][(j & 15) + 1] = y[1];
+                    sm.made.diag[w][i & 15][j & 15] = y[0];
+                    sm.made.diag[w][i & 15][(j & 15) + 1] = y[1];
                 }
             } else {
                 put2<NP>(&sm.T[0][i][j], C * kLdc, 0.f, 0.f);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
     if (!own) {
         asm volatile("bar.sync 2, 128;" ::: "memory");
-        store_square<NP, 128>(tp + NP * C * C, &sm.P[0][0][0]);
+        store_square<NP, 128>(tp + NP * C * C, &sm.made.P[0][0][0]);
         return;
     }
     auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };  // (of the four that go on)
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         for (int i = 0; i < 16; ++i) {
             float s = i == lane ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s -= sm.diag[w][i][m] * t[m];
+            for (int m = 0; m < i; ++m) s -= sm.made.diag[w][i][m] * t[m];
             t[i] = s;
         }
 #pragma unroll
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         }
     }
     sync();
-    const uint32_t Ab = smem_u32(sm.A), Tb = smem_u32(sm.T), Yb = smem_u32(sm.Y);
+    const uint32_t Ab = smem_u32(sm.A), Tb = smem_u32(sm.T), Yb = smem_u32(sm.made.Y);
     auto tile = [&](uint32_t b, int r, int col) { return b + (r * kLdc + col) * 2; };
     auto put = [&](bf16 *dst, int ld, int plane, const float (&x)[2][4], float sign) {
 #pragma unroll
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     if (w & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
-        put(&sm.Y[0][(w >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
+        put(&sm.made.Y[0][(w >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
         __syncwarp();
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         const int r = (w >> 1) * 16, col = (w & 1) * 16;
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
-        put(&sm.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
+        put(&sm.made.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
         sync();
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
