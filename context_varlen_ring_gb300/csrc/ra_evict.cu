@@ -88,7 +88,7 @@ struct ChooseSmem {
 };
 
 template <bool CLUSTER>
-__global__ void __launch_bounds__(CLUSTER ? 1024 : 512) evict_choose_kernel(const EvictArgs a, int room) {
+__global__ void __launch_bounds__(CLUSTER ? 1024 : 512, CLUSTER ? 1 : 2) evict_choose_kernel(const EvictArgs a, int room) {
     constexpr int T = CLUSTER ? 1024 : 512, W = T / 32, PER = kBins / T;
     extern __shared__ __align__(16) uint8_t raw[];
     ChooseSmem &sm = *reinterpret_cast<ChooseSmem *>(raw);
@@ -136,11 +136,11 @@ __global__ void __launch_bounds__(CLUSTER ? 1024 : 512) evict_choose_kernel(cons
     };
     for (int i = tid; i < 3 * kBins / 4; i += T) reinterpret_cast<int4 *>(sm.bins)[i] = make_int4(0, 0, 0, 0);
     if (held)
-        for (int i = tid; i < cnt; i += 8 * T) {
-            uint32_t x[8];
-            weight_keys<8, T>(a, b, wh, at0 + i, at0 + cnt, x);
+        for (int i = tid; i < cnt; i += 4 * T) {
+            uint32_t x[4];
+            weight_keys<4, T>(a, b, wh, at0 + i, at0 + cnt, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
                 if (i + e * T < cnt) sm.held[i + e * T] = x[e];
         }
     __syncthreads();
@@ -261,10 +261,11 @@ cudaError_t launch_next(void (*kernel)(P...), dim3 grid, cudaStream_t st, A... a
 }
 
 // To other pages: a warp takes ROWS rows of one head, looks up a row's places in each lane, and then copies them 16 bytes
-// a lane, kCopies pieces a lane on their way at once.
-constexpr int kCopies = 8;
+// a lane, kCopies pieces a lane on their way at once (8 of them, in 78 registers: 121 us for 64 sequences of 8 heads and 1024 keys
+// kept; five blocks an SM with 4: 90).
+constexpr int kCopies = 4;
 template <int ROWS>
-__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 5) evict_copy_kernel(const EvictArgs a) {
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     pdl_wait();
     const int left = a.new_lens[b], vecs = a.row_bytes / 16, pieces = 2 * vecs;  // of a row: K, then V
