@@ -114,12 +114,23 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
     ProfScope ps("ra_paged_attn_key_weights", s);
     cudaError_t e;
     if (weights_mma_supported(a.dtype, d)) {
+        // The kernel, by the query rows that a KV head may have and the keys that the tables have room for.  Few rows:
+        // the stream (up to 32 rows of 8 sequences of 2000 keys the tiles are faster, 22.6 us to its 28.3).  From 64 rows
+        // on tcgen05, where there are a few tiles of 256 keys (15 sequences of 5 tokens behind a prefix 12.3 us, by tiles of
+        // 64 keys 26.7; 4 of 200 tokens and 1000 keys of 2 heads 18.6 and 38.9).  Else tiles of 64 keys, or of fewer where
+        // those would leave SMs without one: 500 keys of 8 heads by tiles of 64, 32 and 16 keys 12.3, 10.3 and 8.2 us, 3000
+        // of 2 heads (groups of 7) 82, 68 and 52; 2000 of 8 in 8 sequences 22.6, 26.7 and 45.
         const int64_t rows = (max_q_len > 0 && n_groups == 0 ? std::min<int64_t>(max_q_len, T) : T) * a.G;
-        const int64_t units = Hkv * (B * ((a.width[0] * a.page_size + 255) / 256) + n_groups * ((a.width[1] * a.page_size + 255) / 256));
+        auto tiles = [&](int keys) {
+            return Hkv * (B * ((a.width[0] * a.page_size + keys - 1) / keys) + n_groups * ((a.width[1] * a.page_size + keys - 1) / keys));
+        };
         PagedMaps maps;
-        e = rows <= 16                                                                ? launch_weights_stream(a, s)
-            : rows >= 256 && units >= paged_sms() / 2 && weights_tc_maps(a, maps) ? launch_weights_tc(a, maps, s)
-                                                                                  : launch_weights_mma(a, 64, s);
+        if (rows <= 16)
+            e = launch_weights_stream(a, s);
+        else if (rows >= 64 && tiles(256) >= 8 && weights_tc_maps(a, maps))
+            e = launch_weights_tc(a, maps, s);
+        else
+            e = launch_weights_mma(a, tiles(64) < paged_sms() ? 16 : tiles(64) < 2 * paged_sms() ? 32 : 64, s);
     } else {
         e = launch_weights_simt(a, s);
     }

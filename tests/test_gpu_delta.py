@@ -228,22 +228,24 @@ def test_steps_continue_a_packed_call(ra):
     assert (s - last).norm() <= 4.6e-5 * last.norm()
 
 
-def test_long_chains_stay_exact(ra):
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_long_chains_stay_exact(ra, dk, dv):
     """2200 tokens that forget nothing: the state keeps its 24 bits through 35 chunks."""
-    q, k, v, g, beta, cu, cud = make([2200], 1, 1, 64, 64, "bf16", "none", 8)
+    q, k, v, g, beta, cu, cud = make([2200], 1, 1, dk, dv, "bf16", "none", 8)
     out, last = ra.delta_rule_fwd(q, k, v, g, beta, cud, final_state=True)
-    want, wl = ref(q, k, v, g, beta, cu, None, 1 / 8)
+    want, wl = ref(q, k, v, g, beta, cu, None, dk ** -0.5)
     R.delta_check(out, want, "out")
     R.delta_check(last, wl, "state")
 
 
-def test_many_sequences(ra):
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_many_sequences(ra, dk, dv):
     """More sequences than the plan lines up at a time, and than it sorts."""
     rng = np.random.default_rng(0)
     lens = rng.integers(0, 4, 4500).tolist()
-    q, k, v, g, beta, cu, cud = make(lens, 1, 1, 64, 64, "bf16", "usual", 9)
+    q, k, v, g, beta, cu, cud = make(lens, 1, 1, dk, dv, "bf16", "usual", 9)
     out, last = ra.delta_rule_fwd(q, k, v, g, beta, cud, final_state=True)
-    want, wl = ref(q, k, v, g, beta, cu, None, 1 / 8)
+    want, wl = ref(q, k, v, g, beta, cu, None, dk ** -0.5)
     R.delta_check(out, want, "out")
     R.delta_check(last, wl, "state")
 
@@ -267,38 +269,48 @@ def test_empty_calls(ra, dtype):
     assert (keep == 5.0).all() and ra.device_status() == 0
 
 
-def test_nan_stays_in_its_sequence(ra):
-    """A NaN or an infinity reaches its own sequence's tokens of its chunk and behind, and nothing else."""
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_nan_stays_in_its_sequence(ra, dk, dv):
+    """A NaN or an infinity reaches its own sequence's tokens of its chunk and behind, and nothing else: not the sequence
+    ahead either, whose last chunk ends where it begins."""
     lens = [130, 70, 64]
-    for bad, dtype in ((math.nan, "bf16"), (math.inf, "fp32")):
-        q, k, v, g, beta, cu, cud = make(lens, 1, 2, 64, 64, dtype, "usual", 2)
+    for bad, dtype, seq in ((math.nan, "bf16", 0), (math.inf, "fp32", 0), (math.nan, "bf16", 1), (math.inf, "bf16", 1)):
+        q, k, v, g, beta, cu, cud = make(lens, 1, 2, dk, dv, dtype, "usual", 2)
         clean, last = ra.delta_rule_fwd(q, k, v, g, beta, cud, final_state=True)
-        for x in (q, k, v):
+        alone = ra.delta_rule_fwd(q, k, v, g, beta, cud)[0]
+        dout = torch.randn_like(v)
+        at = cu[seq] + (70 if seq == 0 else 2)
+        others = [t for t in range(cu[-1]) if not cu[seq] <= t < cu[seq + 1] or (seq == 0 and t < 64)]
+        rest = [t for t in range(cu[-1]) if not cu[seq] <= t < cu[seq + 1]]
+        seqs = [b for b in range(3) if b != seq]
+        for x in (q, k, v, dout):
             y = x.clone()
-            y[cu[0] + 70, 0, 3] = bad
+            y[at, 0, 3] = bad
             args = [y if z is x else z for z in (q, k, v)]
-            out, s = ra.delta_rule_fwd(*args, g, beta, cud, final_state=True)
-            assert torch.equal(out[cu[1]:], clean[cu[1]:]) and torch.equal(out[:64], clean[:64])
-            assert torch.equal(s[1:], last[1:])
-            assert not torch.isfinite(out[cu[0] + 70]).all()
-            dout = torch.ones_like(v)
-            got, want = (ra.delta_rule_bwd(dout, *z, g, beta, cud) for z in (args, (q, k, v)))
-            assert all(torch.equal(a[cu[1]:], b[cu[1]:]) for a, b in zip(got[:5], want[:5]))
+            if x is not dout:
+                out, s = ra.delta_rule_fwd(*args, g, beta, cud, final_state=True)
+                assert torch.equal(out[others], clean[others]) and torch.equal(s[seqs], last[seqs])
+                assert not torch.isfinite(out[at]).all()
+                assert torch.equal(ra.delta_rule_fwd(*args, g, beta, cud)[0][others], alone[others])
+            got = ra.delta_rule_bwd(y if x is dout else dout, *args, g, beta, cud)
+            want = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud)
+            assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got[:5], want[:5]))
     assert ra.device_status() == 0
 
 
-def test_bad_arrays_are_recorded(ra):
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_bad_arrays_are_recorded(ra, dk, dv):
     """Boundaries that decrease or leave the tokens: recorded, nothing written.  A slot outside the pool: recorded, the
     sequence begins at zero and its state is dropped."""
-    q, k, v, g, beta, cu, cud = make([40, 50], 1, 1, 64, 64, "bf16", "usual", 1)
+    q, k, v, g, beta, cu, cud = make([40, 50], 1, 1, dk, dv, "bf16", "usual", 1)
     for bad in ([0, 60, 50], [0, 40, 91], [-1, 40, 90]):
         out = torch.full_like(v, 2.0)
-        s = torch.full((2, 1, 64, 64), 2.0, device="cuda")
+        s = torch.full((2, 1, dk, dv), 2.0, device="cuda")
         ra.delta_rule_fwd(q, k, v, g, beta, ints(bad), state_out=s, out=out)
         assert ra.device_status() == 6 and (out == 2.0).all() and (s == 2.0).all()
         grads = ra.delta_rule_bwd(v, q, k, v, g, beta, ints(bad))
         assert ra.device_status() == 6 and len(grads) == 6
-    pool = states(2, 1, 64, 64, 1)
+    pool = states(2, 1, dk, dv, 1)
     keep = pool.clone()
     out, _ = ra.delta_rule_fwd(q, k, v, g, beta, cud, state=pool, slots=ints([1, 2]), state_out=pool)
     assert ra.device_status() == 6 and torch.equal(pool[0], keep[0]) and not torch.equal(pool[1], keep[1])
@@ -358,12 +370,13 @@ def test_same_bits_from_any_workspace(ra):
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
-def test_in_a_graph_and_on_another_stream(ra):
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_in_a_graph_and_on_another_stream(ra, dk, dv):
     """Captured calls follow their arrays' contents; a call on a side stream runs there."""
     lens = [70, 64, 10]
-    q, k, v, g, beta, cu, cud = make(lens, 1, 2, 64, 64, "bf16", "usual", 6, tail=20)
+    q, k, v, g, beta, cu, cud = make(lens, 1, 2, dk, dv, "bf16", "usual", 6, tail=20)
     dout = torch.randn_like(v)
-    pool = states(4, 2, 64, 64, 1)
+    pool = states(4, 2, dk, dv, 1)
     slots = ints([2, 0, 3])
     start = pool.clone()
     side = torch.cuda.Stream()
@@ -398,8 +411,9 @@ def test_in_a_graph_and_on_another_stream(ra):
     assert ra.device_status() == 0
 
 
-def test_calls_from_several_threads(ra):
-    ins = [make([30 + 50 * i, 5], 1, 1 + i % 2, 64, 64, "bf16", "usual", i) for i in range(4)]
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_calls_from_several_threads(ra, dk, dv):
+    ins = [make([30 + 50 * i, 5], 1, 1 + i % 2, dk, dv, "bf16", "usual", i) for i in range(4)]
     want = [ra.delta_rule_fwd(*x[:5], x[6], final_state=True) for x in ins]
     torch.cuda.synchronize()
     got, errors = [None] * 4, []

@@ -69,6 +69,10 @@ WEIGHTS = [  # new, lens, prefix lens, groups, page, hq, hkv, d, dtype, causal, 
     ([3, 2], [400, 257], (129, 0), (0, 1, 2), 8, 128, 1, 128, "bf16", True, False, True, 0),
     ([129], [129], (), (0,), 128, 16, 8, 128, "bf16", True, True, True, 0),
     ([40], [30], (), (0,), 32, 64, 8, 128, "bf16", True, False, True, 0),
+    # tiles of 64, 32 and 16 keys (groups that are no power of two)
+    ([12, 30], [900, 800], (), (0,), 16, 42, 14, 64, "bf16", True, False, True, 0),
+    ([25], [800], (), (0,), 16, 42, 14, 128, "bf16", True, True, True, 0),
+    ([31], [700], (), (0,), 24, 10, 2, 128, "bf16", True, False, False, 0),
 ]
 
 
@@ -88,7 +92,7 @@ def weights_case(rng, new, lens, plens, groups, page, hq, hkv, d, dtype, hnd, ou
 
 
 @pytest.mark.parametrize("new,lens,plens,groups,page,hq,hkv,d,dtype,causal,hnd,outer,tail", WEIGHTS)
-@pytest.mark.parametrize("hint", [True, False])
+@pytest.mark.parametrize("hint", [True, False, "wrong"])
 def test_key_weights(ra, new, lens, plens, groups, page, hq, hkv, d, dtype, causal, hnd, outer, tail, hint):
     rng = np.random.default_rng(sum(lens))
     q, kc, w, table, ptable, cu = weights_case(rng, new, lens, plens, groups, page, hq, hkv, d, dtype, hnd, outer, tail)
@@ -106,12 +110,12 @@ def test_key_weights(ra, new, lens, plens, groups, page, hq, hkv, d, dtype, caus
                                 scale)
     before = w.clone()
     got = ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, w, causal=causal, scale=scale,
-                                    max_q_len=max(new) if hint else None, **pre)
+                                    max_q_len=1 if hint == "wrong" else max(new) if hint else None, **pre)
     assert got is w and ra.device_status() == 0
     SR.check(R.f64(w), want, bound)
     again = before.clone()  # (other strides: contiguous)
     ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, again, causal=causal, scale=scale,
-                              max_q_len=max(new) if hint else None, **pre)
+                              max_q_len=1 if hint == "wrong" else max(new) if hint else None, **pre)
     assert torch.equal(again, w)
 
 
@@ -138,6 +142,34 @@ def test_key_weights_of_the_last_rows(ra):
     want, bound = R.key_weights(R.f64(q[-8:]), R.f64(kc), table, [0, 8], [300], R.f64(lse[:, -8:]), R.f64(w) * 0,
                                 scale=1 / 8)
     SR.check(R.f64(w), want, bound)
+
+
+def test_key_weights_nan_in_tiles_of_many_rows(ra):
+    """A NaN in one sequence's query or key reaches that sequence's weights only: its rows come with its neighbours' in one
+    tile of 128, whose rows are not all one sequence's."""
+    rng = np.random.default_rng(14)
+    new, lens = [40, 70, 20], [300, 70, 500]
+    q, kc, w, table, ptable, cu = weights_case(rng, new, lens, (), (0,), 16, 32, 8, 128, "bf16", False, True, 0)
+    w.zero_()
+    lse = ra.paged_attn_fwd(q, kc, kc, dev(table), dev(cu), dev(lens))[1]
+    a = ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, w.clone())
+    q2 = q.clone()
+    q2[45, 6, 9] = math.nan  # the second sequence's sixth token, KV head 1: sees 6 keys
+    b = ra.paged_attn_key_weights(q2, kc, dev(table), dev(cu), dev(lens), lse, w.clone())
+    hit = torch.isnan(b)
+    assert hit.sum() == 6 and all(hit[int(table[1][0]), i, 1] for i in range(6)) and torch.equal(b[~hit], a[~hit])
+    k2 = kc.clone()
+    k2[int(table[0][3]), 5, 2, 100] = math.inf  # key 53 of the first sequence, KV head 2
+    b = ra.paged_attn_key_weights(q, k2, dev(table), dev(cu), dev(lens), lse, w.clone())
+    b[int(table[0][3]), 5, 2] = a[int(table[0][3]), 5, 2]
+    assert torch.equal(a, b)
+    lse2 = lse.clone()
+    lse2[:, 40:110] = -math.inf  # the second sequence's rows left out
+    b = ra.paged_attn_key_weights(q2, kc, dev(table), dev(cu), dev(lens), lse2, w.clone())
+    for i in range(5):
+        assert (b[int(table[1][i])] == 0).all()
+        b[int(table[1][i])] = a[int(table[1][i])]
+    assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp32", 64)])
