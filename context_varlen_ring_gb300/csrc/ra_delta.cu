@@ -299,6 +299,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         load_rows<E, DK, kScanThreads>(&sm.q[0][0][0], LD, C * LD, static_cast<const E *>(a.q) + ch.tok0 * a.q_stride + hk * DK,
                                        a.q_stride, ch.n);
     };
+    RowsAhead<DK, kScanThreads> k_ahead, q_ahead;  // (fp32: K and Q of the next chunk)
+    auto fetch = [&](int c, bool with_q) {
+        const DeltaChunk ch = a.chunk[c];
+        k_ahead.fetch(static_cast<const float *>(a.k) + ch.tok0 * a.k_stride + hk * DK, a.k_stride, ch.n);
+        if (with_q) q_ahead.fetch(static_cast<const float *>(a.q) + ch.tok0 * a.q_stride + hk * DK, a.q_stride, ch.n);
+    };
     auto load_tp = [&](int c, int which) {
         load_square<NP, kScanThreads>(which ? &sm.P[0][0][0] : &sm.T[0][0][0],
                                       a.tp + (((int64_t)c * a.Hv + h) * 2 + which) * NP * C * C);
@@ -315,6 +321,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         if (want) load_tp(c0, 1);
         cp_commit();
         if (warp == 0) gates_load(a, a.chunk[c0], h, gg, gb);
+        if (KB == 1) fetch(c0, want);
     }
     for (int c = c0; c < c1; ++c) {
         const int buf = KB == 2 ? (c - c0) & 1 : 0;
@@ -323,8 +330,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         const int64_t cell = (int64_t)c * a.Hv + h;
         if (KB == 1) {
             __syncthreads();  // (the last chunk's products with K)
-            load_k(c, 0);
-            if (want) load_q(c);
+            k_ahead.put(&sm.k[0][0][0][0], LD, C * LD);
+            if (want) q_ahead.put(&sm.q[0][0][0], LD, C * LD);
+            if (c + 1 < c1) fetch(c + 1, want);
         }
         if (warp == 0) {
             gates_put(g, gg, gb);

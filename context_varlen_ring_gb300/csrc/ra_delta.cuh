@@ -166,6 +166,26 @@ __device__ __forceinline__ void load_rows(bf16 *dst, int ld, int plane, const E 
         }
     }
 }
+// fp32 rows [64][W] by way of registers, so that they can be under way while the tile is in use.
+template <int W, int THREADS>
+struct RowsAhead {
+    float4 x[C * (W / 4) / THREADS];
+    __device__ __forceinline__ void fetch(const float *src, int64_t stride, int n) {
+#pragma unroll
+        for (int e = 0; e < C * (W / 4) / THREADS; ++e) {
+            const int i = threadIdx.x + e * THREADS, row = i / (W / 4), c = i % (W / 4) * 4;
+            x[e] = row < n ? *reinterpret_cast<const float4 *>(src + row * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void put(bf16 *dst, int ld, int plane) const {
+#pragma unroll
+        for (int e = 0; e < C * (W / 4) / THREADS; ++e) {
+            const int i = threadIdx.x + e * THREADS, row = i / (W / 4), c = i % (W / 4) * 4;
+            put2<3>(dst + row * ld + c, plane, x[e].x, x[e].y);
+            put2<3>(dst + row * ld + c + 2, plane, x[e].z, x[e].w);
+        }
+    }
+};
 // T and P lie in the workspace as tiles that a bulk copy can take to shared memory: a part after another, rows of 128
 // bytes whose 16-byte pieces are exchanged by the row's low bits (the 128-byte swizzle of the tensor cores' operands).
 __device__ __forceinline__ int swizzled(int row, int piece) { return row * C + ((piece ^ (row & 7)) << 3); }

@@ -391,16 +391,19 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
 }
 
 // ------------------------------------------------------------ fp32 arithmetic: fp32, and bf16 of other head sizes
-constexpr int kSimtKeys = 32, kSimtRows = 32;
+// 32 keys by 64 rows a step; the next step's rows are on their way to registers beside it (9 sequences of a few tokens
+// behind prefixes of 1500 keys, heads of 64: 31 us with 32 rows a step, loaded when due, 17 so).
+constexpr int kSimtKeys = 32, kSimtRows = 64, kSimtThreads = 256;
 
 struct SimtSmem {
     float lse[kSimtRows];
-    float sum[8][kSimtKeys];
+    float sum[16][kSimtKeys];
     Line line;
 };
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs a) {
+// P: pieces of 4 elements that a thread loads of a row, four threads a row (d <= 16 P).
+template <typename E, int P>
+__global__ void __launch_bounds__(kSimtThreads) weights_simt_kernel(const WeightArgs a) {
     extern __shared__ __align__(128) uint8_t raw[];
     SimtSmem &sm = *reinterpret_cast<SimtSmem *>(raw);
     const int ld = a.d + 4;
@@ -408,11 +411,11 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
     const int tid = threadIdx.x, kx = tid & 15, ry = tid >> 4;
     const int S = a.B + a.n_groups;
     for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)
-        if (line_up<kThreads>(a, s0, 5, sm.line) < 0) {
+        if (line_up<kSimtThreads>(a, s0, 5, sm.line) < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
-    auto put4 = [&](float *dst, const E *src, bool there) {
+    auto get4 = [&](const E *src, bool there) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (there) {
             if (sizeof(E) == 4) {
@@ -424,11 +427,11 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
                 x = make_float4(p.x, p.y, r.x, r.y);
             }
         }
-        *reinterpret_cast<float4 *>(dst) = x;
+        return x;
     };
     const int vec = a.d / 4;
     for (int s0 = 0; s0 < S; s0 += kSegs) {
-        const int tiles = line_up<kThreads>(a, s0, 5, sm.line);
+        const int tiles = line_up<kSimtThreads>(a, s0, 5, sm.line);
         if (tiles < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
@@ -441,32 +444,50 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
             const bool own = s < a.B;
             const int rows = g.n * a.G;
             const int first = own && a.causal ? max(0, k0 - (g.len - g.n)) * a.G : 0;
-            __syncthreads();
-            for (int x = tid; x < kSimtKeys * vec; x += kThreads) {
-                const int r = x / vec, c = x % vec * 4;
+            // rows r0 .. of q: this thread's row and pieces, and the row's offset
+            float4 next[P];
+            float next_lse = 0.f;
+            auto look = [&](int r0) {
+                const int r = r0 + (tid >> 2);
+                const bool there = r < rows;
+                const int t = token_of(a, there ? r : 0);
+                const E *q = static_cast<const E *>(a.q) + (g.tok0 + t) * a.q_stride + (int64_t)(h * a.G + (there ? r : 0) - t * a.G) * a.d;
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int c = (tid & 3) + 4 * e;
+                    next[e] = get4(q + c * 4, there && c < vec);
+                }
+                if (tid < kSimtRows) next_lse = row_lse(a, g, h, r0 + tid);
+            };
+            look(first);
+            __syncthreads();  // (the last unit's reads)
+            {
+                const int r = tid >> 3;
                 int64_t page = 0;
                 int row = 0;
                 const bool there = k0 + r < g.len && place(a, s, k0 + r, page, row);
-                put4(sk + r * ld + c, static_cast<const E *>(a.k) + page * a.page_stride + row * a.token_stride + h * a.head_stride + c, there);
+                const E *k = static_cast<const E *>(a.k) + (there ? page * a.page_stride + row * a.token_stride + h * a.head_stride : 0);
+                for (int c = tid & 7; c < vec; c += 8) *reinterpret_cast<float4 *>(sk + r * ld + c * 4) = get4(k + c * 4, there);
             }
             float sum[2] = {0.f, 0.f};
             for (int r0 = first; r0 < rows; r0 += kSimtRows) {
                 __syncthreads();
-                for (int x = tid; x < kSimtRows * vec; x += kThreads) {
-                    const int r = r0 + x / vec, c = x % vec * 4, t = token_of(a, min(r, rows - 1));
-                    put4(sq + x / vec * ld + c,
-                         static_cast<const E *>(a.q) + (g.tok0 + t) * a.q_stride + (int64_t)(h * a.G + min(r, rows - 1) - t * a.G) * a.d + c,
-                         r < rows);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int c = (tid & 3) + 4 * e;
+                    if (c < vec) *reinterpret_cast<float4 *>(sq + (tid >> 2) * ld + c * 4) = next[e];
                 }
-                if (tid < kSimtRows) sm.lse[tid] = row_lse(a, g, h, r0 + tid);
+                if (tid < kSimtRows) sm.lse[tid] = next_lse;
                 __syncthreads();
+                if (r0 + kSimtRows < rows) look(r0 + kSimtRows);
                 float acc[2][4] = {};
+#pragma unroll 4
                 for (int c = 0; c < a.d; c += 4) {
                     float4 k[2], q[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) k[e] = *reinterpret_cast<const float4 *>(sk + (kx + 16 * e) * ld + c);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) q[e] = *reinterpret_cast<const float4 *>(sq + (ry + 8 * e) * ld + c);
+                    for (int e = 0; e < 4; ++e) q[e] = *reinterpret_cast<const float4 *>(sq + (ry + 16 * e) * ld + c);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -475,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
                 }
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int row = ry + 8 * f;
+                    const int row = ry + 16 * f;
                     const float off = sm.lse[row];
                     if (off == -INFINITY) continue;
                     const int limit = limit_of(a, g, own, r0 + row);
@@ -493,12 +514,25 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightArgs
                 if (k0 + tid < g.len && place(a, s, k0 + tid, page, row)) {
                     float x = 0.f;
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) x += sm.sum[w][tid];
+                    for (int w = 0; w < 16; ++w) x += sm.sum[w][tid];
                     a.w[page * a.w_page + row * a.w_token + h * a.w_head] += x;
                 }
             }
         }
     }
+}
+
+template <typename E, int P>
+cudaError_t simt_launch(const WeightArgs &a, cudaStream_t st) {
+    static LaunchFit fit;
+    auto kernel = weights_simt_kernel<E, P>;
+    const size_t fixed = (sizeof(SimtSmem) + 127) / 128 * 128;
+    int ctas = 0;  // (of the largest heads)
+    const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kSimtThreads,
+                                      fixed + (kSimtKeys + kSimtRows) * (16 * P + 4) * 4, &ctas);
+    if (e != cudaSuccess) return e;
+    kernel<<<paged_sms() * ctas, kSimtThreads, fixed + (size_t)(kSimtKeys + kSimtRows) * (a.d + 4) * 4, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <int D, int KEYS>
@@ -537,19 +571,9 @@ cudaError_t launch_weights_mma(const WeightArgs &a, int keys, cudaStream_t st) {
     return a.d == 64 ? mma_keys<64>(a, keys, st) : mma_keys<128>(a, keys, st);
 }
 cudaError_t launch_weights_simt(const WeightArgs &a, cudaStream_t st) {
-    static LaunchFit fit[2];
-    const bool f = a.dtype == RA_FP32;
-    const void *kernel = f ? reinterpret_cast<const void *>(weights_simt_kernel<float>) : reinterpret_cast<const void *>(weights_simt_kernel<bf16>);
-    const size_t fixed = (sizeof(SimtSmem) + 127) / 128 * 128;
-    int ctas = 0;  // (of the largest heads)
-    const cudaError_t e = fit[f].prepare(kernel, kThreads, fixed + (kSimtKeys + kSimtRows) * (256 + 4) * 4, &ctas);
-    if (e != cudaSuccess) return e;
-    const size_t smem = fixed + (size_t)(kSimtKeys + kSimtRows) * (a.d + 4) * 4;
-    if (f)
-        weights_simt_kernel<float><<<paged_sms() * ctas, kThreads, smem, st>>>(a);
-    else
-        weights_simt_kernel<bf16><<<paged_sms() * ctas, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    if (a.dtype == RA_FP32)
+        return a.d <= 64 ? simt_launch<float, 4>(a, st) : a.d <= 128 ? simt_launch<float, 8>(a, st) : simt_launch<float, 16>(a, st);
+    return a.d <= 64 ? simt_launch<bf16, 4>(a, st) : a.d <= 128 ? simt_launch<bf16, 8>(a, st) : simt_launch<bf16, 16>(a, st);
 }
 
 }  // namespace ra
