@@ -261,7 +261,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
     using Smem = ScanSmem<E, NP, DK, DVS>;
     constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
-    constexpr int MW = DK / 16, NS = DVS / 8 / (8 / MW), NX = DVS / 16;  // n-tiles of a warp: of S, of rows of the chunk
+    // Slices of 32 or 64 columns: every warp has 16 rows and half of the columns.  Of 16: warps 0 .. 3 have the chain (K S0, T R
+    // and, with dk 64, the state), and warps 4 .. 7 the output.
+    constexpr bool kRoles = DVS == 16;
+    constexpr int MW = DK / 16, MS = kRoles && MW == 4 ? 4 : 8;  // warps along dk, and those with rows of S
+    constexpr int NS = DVS / 8 / (MS / MW), NX = kRoles ? 2 : DVS / 16;  // n-tiles of a warp: of S, of rows of the chunk
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
@@ -273,7 +277,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
     const int c0 = a.first[seq], c1 = a.first[seq + 1];
     const int tid = threadIdx.x, warp = tid >> 5;
     const int srow = 16 * (warp % MW), scol = warp / MW * 8 * NS;  // this warp's part of S
-    const int xrow = 16 * (warp & 3), xcol = (warp >> 2) * 8 * NX;  // and of the chunk's rows
+    const int xrow = 16 * (warp & 3), xcol = kRoles ? 0 : (warp >> 2) * 8 * NX;  // and of the chunk's rows
+    const bool chain = !kRoles || warp < 4, state = warp < MS;
     const int64_t slot = a.state || a.state_out ? slot_of(a.slots, a.n_slots, seq, a.status) : -1;
     const int64_t splace = ((slot * a.Hv + h) * DK) * dv + v0;
 
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             float2 x = make_float2(0.f, 0.f);
-            if (a.state && slot >= 0)
+            if (a.state && slot >= 0 && state)
                 x = *reinterpret_cast<const float2 *>(a.state + splace + (int64_t)(srow + acc_row(hf)) * dv + scol + acc_col(n));
             S[n][2 * hf] = x.x;
             S[n][2 * hf + 1] = x.y;
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         load_square<NP, kScanThreads>(which ? &sm.P[0][0][0] : &sm.T[0][0][0],
                                       a.tp + (((int64_t)c * a.Hv + h) * 2 + which) * NP * C * C);
     };
-    const bool want = a.out != nullptr;
+    const bool want = a.out != nullptr, output = want && (!kRoles || warp >= 4);
     float gg[2], gb[2];
     if (c0 < c1) {
         if (KB == 2) load_k(c0, 0);
@@ -346,12 +351,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
             for (int hf = 0; hf < 2; ++hf) {
                 const int i = xrow + acc_row(hf);
                 v[n][hf] = make_float2(0.f, 0.f);
-                if (i < ch.n)
+                if (i < ch.n && chain)
                     v[n][hf] = load2(static_cast<const E *>(a.v) + (ch.tok0 + i) * a.v_stride + h * dv + v0 + xcol + acc_col(n));
             }
         // the state's parts
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int n = 0; n < NS && state; ++n)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int i = srow + acc_row(hf), j = scol + acc_col(n);
@@ -366,9 +371,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         cp_commit();
         float x[NX][4], o[NX][4];
         zero(x);
-        mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
-                                         DK);
-        if (want) {
+        if (chain)
+            mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS,
+                                                 0, DK);
+        if (output) {
             zero(o);
             mm<NX, NPI, NP, NP, false, true, EX>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                              DK);
@@ -380,9 +386,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
                 const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
                 const float e = g.eG[i], b = g.beta[i];
                 const float r0 = v[n][hf].x - e * x[n][2 * hf], r1 = v[n][hf].y - e * x[n][2 * hf + 1];
-                put2<NP>(&sm.R[0][i][j], C * LV, b * r0, b * r1);
-                if (keep) *reinterpret_cast<float2 *>(a.r + (cell * C + i) * dv + v0 + j) = make_float2(r0, r1);
-                if (want) {
+                if (chain) {
+                    put2<NP>(&sm.R[0][i][j], C * LV, b * r0, b * r1);
+                    if (keep) *reinterpret_cast<float2 *>(a.r + (cell * C + i) * dv + v0 + j) = make_float2(r0, r1);
+                }
+                if (output) {
                     o[n][2 * hf] *= e * a.scale;
                     o[n][2 * hf + 1] *= e * a.scale;
                 }
@@ -392,10 +400,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         if (KB == 2 && want && c + 1 < c1) load_q(c + 1);
         cp_commit();
         zero(x);
-        mm<NX, NP, NP, NP, false, true, EX>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR, 0,
-                                        xrow + 16);
+        if (chain)
+            mm<NX, NP, NP, NP, false, true, EX>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR,
+                                                0, xrow + 16);
 #pragma unroll
-        for (int n = 0; n < NX; ++n)
+        for (int n = 0; n < NX && chain; ++n)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
@@ -409,13 +418,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         if (c + 1 < c1) load_tp(c + 1, 0);
         cp_commit();
 #pragma unroll
-        for (int n = 0; n < NX; ++n)
+        for (int n = 0; n < NX && chain; ++n)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int i = xrow + acc_row(hf), j = xcol + acc_col(n);
                 put2<NP>(&sm.R[0][i][j], C * LV, g.eL[i] * x[n][2 * hf], g.eL[i] * x[n][2 * hf + 1]);
             }
-        if (want) {
+        if (output) {
             mm<NX, NP, NP, NP, false, true, EX>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
                                             0, xrow + 16);
 #pragma unroll
@@ -435,10 +444,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
-        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
+        if (state)
+            mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
     }
     cp_wait<0>();
-    if (a.state_out && slot >= 0) {
+    if (a.state_out && slot >= 0 && state) {
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -561,9 +571,23 @@ cudaError_t launch_delta_local(const DeltaArgs &a, cudaStream_t st) {
     if (a.parts == 2) return a.dk == 64 ? local<bf16, 2, 64>(a, st) : local<bf16, 2, 128>(a, st);
     return a.dk == 64 ? local<bf16, 3, 64>(a, st) : local<bf16, 3, 128>(a, st);
 }
+// Slices of the state's columns: a step of the chain is bound by its warp-level products (fp32, dk 64, 32 columns: 5700 of
+// 11,400 cycles), so they are as narrow as leaves every CTA an SM (fp32, 5 sequences of up to 292 tokens, 4 heads of 64:
+// slices of 32 columns 35.0 us, of 16 28.4; bf16, up to 1408 tokens, one head of 64 by 128: of 64 the call takes 33.6, of
+// 32 27.2).  With more CTAs than SMs, narrow slices only read K and Q more often.
 cudaError_t launch_delta_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
-    if (a.dtype == RA_FP32) return a.dk == 64 ? scan<float, 3, 64, 32>(a, keep, st) : scan<float, 3, 128, 32>(a, keep, st);
-    if (a.parts == 2) return a.dk == 64 ? scan<bf16, 2, 64, 64>(a, keep, st) : scan<bf16, 2, 128, 64>(a, keep, st);
+    const int64_t heads = (int64_t)a.N * a.Hv;
+    if (a.dtype == RA_FP32) {
+        if (heads * (a.dv / 16) <= paged_sms())
+            return a.dk == 64 ? scan<float, 3, 64, 16>(a, keep, st) : scan<float, 3, 128, 16>(a, keep, st);
+        return a.dk == 64 ? scan<float, 3, 64, 32>(a, keep, st) : scan<float, 3, 128, 32>(a, keep, st);
+    }
+    const bool few = heads * (a.dv / 32) <= paged_sms();
+    if (a.parts == 2) {
+        if (few) return a.dk == 64 ? scan<bf16, 2, 64, 32>(a, keep, st) : scan<bf16, 2, 128, 32>(a, keep, st);
+        return a.dk == 64 ? scan<bf16, 2, 64, 64>(a, keep, st) : scan<bf16, 2, 128, 64>(a, keep, st);
+    }
+    if (few) return a.dk == 64 ? scan<bf16, 3, 64, 32>(a, keep, st) : scan<bf16, 3, 128, 32>(a, keep, st);
     return a.dk == 64 ? scan<bf16, 3, 64, 64>(a, keep, st) : scan<bf16, 3, 128, 64>(a, keep, st);
 }
 cudaError_t launch_delta_step(const DeltaStepArgs &a, cudaStream_t st) {

@@ -474,6 +474,9 @@ cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
 
 cudaError_t launch_delta_back(const DeltaArgs &a, cudaStream_t st) {
     if (a.dtype == RA_FP32) return a.dk == 64 ? back<float, 3, 64, 32>(a, st) : back<float, 3, 128, 32>(a, st);
+    // (slices as narrow as leaves every CTA an SM: 12 sequences of up to 39 tokens, 2 heads of 64, both walks 41.9 -> 38.0 us)
+    if ((int64_t)a.N * a.Hv * (a.dv / 32) <= paged_sms())
+        return a.dk == 64 ? back<bf16, 3, 64, 32>(a, st) : back<bf16, 3, 128, 32>(a, st);
     return a.dk == 64 ? back<bf16, 3, 64, 64>(a, st) : back<bf16, 3, 128, 64>(a, st);
 }
 cudaError_t launch_delta_grads(const DeltaArgs &a, cudaStream_t st) {
