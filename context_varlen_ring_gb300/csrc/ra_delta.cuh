@@ -293,18 +293,21 @@ __device__ __forceinline__ int64_t slot_of(const int32_t *slots, int64_t n_slots
 // The kernels of a call but the first are launched as programmatic successors: their blocks are set up while the
 // kernel ahead ends, and wait for it before they read what it wrote.
 __device__ __forceinline__ void wait_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <typename... P, typename... A>
+template <int CLUSTER = 1, typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, const A &...args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CLUSTER;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(block);
     c.dynamicSmemBytes = smem;
     c.stream = st;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    c.attrs = at;
+    c.numAttrs = CLUSTER > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
 

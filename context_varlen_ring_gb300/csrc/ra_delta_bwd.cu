@@ -17,6 +17,7 @@
 //        E = dP (q.k) + M (k.k)
 //   dg_t = sum over i >= t of dG_i, + sum F.k + e^(G_63) <S0, dS1>
 #include <cuda_bf16.h>
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "ra_delta.cuh"
@@ -24,6 +25,8 @@
 
 namespace ra {
 namespace {
+
+namespace cg = cooperative_groups;
 
 using namespace delta;
 
@@ -216,26 +219,37 @@ struct GradSmem {
         Square c;
     };
     Gates g;
-    float row[2][C], db[2][C], col[4][C];  // of each half of the columns, of each warp's rows
-    float rr[C], far[8], ss[8];
+    float row[4][C], db[4][C], col[4][C];  // of each group of columns, of each 16 rows
+    float rr[C], far[16], ss[8];
 };
 
-template <typename E, int NP, int DK>
+// R CTAs (a cluster) a cell, 64 / R rows each.  Of two, the second gives the first what its rows have of the first
+// one's columns (dP, M) and its sums for the gates; nothing goes the other way, as dP and M are triangular.
+template <typename E, int NP, int DK, int R>
 __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArgs a) {
     using Smem = GradSmem<E, NP, DK>;
     constexpr bool EX = NP == 3;
     constexpr int NPI = Smem::NPI, LD = Smem::LD, LV = Smem::LV;
-    constexpr int NK = DK / 16;  // n-tiles of a warp along dk
+    constexpr int RT = C / R / 16, CG = 8 / RT;                 // 16 rows a warp, and a CGth of the columns:
+    constexpr int NK = DK / 8 / CG, NC = C / 8 / CG;            // n-tiles along dk, along the chunk
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
-    const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x / R, rank = blockIdx.x % R, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     wait_ahead();
     if (c >= a.hdr->chunks) return;
     const DeltaChunk ch = a.chunk[c];
     const int hk = h / (a.Hv / a.Hk), dv = a.dv;
     const int64_t cell = (int64_t)c * a.Hv + h;
-    const int row0 = 16 * (warp & 3), half = warp >> 2, kcol = half * 8 * NK, ccol = half * 32;
+    const int row0 = 16 * (rank * RT + warp % RT), group = warp / RT, kcol = group * 8 * NK, ccol = group * 8 * NC;
+    auto own = [&](int r) { return R == 1 || r / (C / R) == rank; };
+    Smem &first = R == 1 ? sm : *cg::this_cluster().map_shared_rank(&sm, 0);
+    auto sync = [&]() {
+        if constexpr (R == 1)
+            __syncthreads();
+        else
+            cg::this_cluster().sync();
+    };
     load_rows<E, DK, kThreads>(&sm.k[0][0][0], LD, C * LD, static_cast<const E *>(a.k) + ch.tok0 * a.k_stride + hk * DK,
                                a.k_stride, ch.n);
     load_rows<E, DK, kThreads>(&sm.q[0][0][0], LD, C * LD, static_cast<const E *>(a.q) + ch.tok0 * a.q_stride + hk * DK,
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         gates_load(a, ch, h, g, b);
         gates_put(sm.g, g, b);
     }
-    float dq[NK][4], F[NK][4], B[NK][4], dP[4][4], dA[4][4];
+    float dq[NK][4], F[NK][4], B[NK][4], dP[NC][4], dA[NC][4];
     zero(dq);
     zero(F);
     zero(B);
@@ -273,11 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
             const int r = tid >> 2, j = (tid & 3) * 4 + i * 16;
             const int64_t at = (cell * C + r) * dv + v0 + j;
             const float4 x = *reinterpret_cast<const float4 *>(a.u + at);
+            put2<NP>(&sm.v.u[0][r][j], C * LV, x.x, x.y);
+            put2<NP>(&sm.v.u[0][r][j + 2], C * LV, x.z, x.w);
+            if (!own(r)) continue;
             const float4 y = *reinterpret_cast<const float4 *>(a.dr + at);
             const float4 z = *reinterpret_cast<const float4 *>(a.r + at);
             rr += y.x * z.x + y.y * z.y + y.z * z.z + y.w * z.w;
-            put2<NP>(&sm.v.u[0][r][j], C * LV, x.x, x.y);
-            put2<NP>(&sm.v.u[0][r][j + 2], C * LV, x.z, x.w);
             put2<NP>(&sm.v.dr[0][r][j], C * LV, y.x, y.y);
             put2<NP>(&sm.v.dr[0][r][j + 2], C * LV, y.z, y.w);
         }
@@ -288,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         mm<NK, NPI, NP, NP, false, false, EX>(dq, d, LV, PR, s0, LV, PS, 0, kVS);
         mm<NK, NP, NP, NP, false, false, EX>(F, u + row0 * LV * 2, LV, PR, ds, LV, PS, 0, kVS);
         mm<NK, NP, NP, NP, false, false, EX>(B, dr, LV, PR, s0, LV, PS, 0, kVS);
-        mm<4, NPI, NP, NP, false, false, EX>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
-        mm<4, NP, NP, NP, false, false, EX>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<NC, NPI, NP, NP, false, false, EX>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<NC, NP, NP, NP, false, false, EX>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
     }
     // sums of rows over the four threads that hold them
     rr += __shfl_xor_sync(0xffffffffu, rr, 1);
@@ -298,14 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
     float row[2] = {0.f, 0.f}, db[2] = {0.f, 0.f}, far = 0.f;
     const uint32_t kb = smem_u32(sm.k), qb = smem_u32(sm.q);
     {
-        float kk[4][4], qk[4][4];
+        float kk[NC][4], qk[NC][4];
         zero(kk);
         zero(qk);
-        mm<4, NPI, NPI, 3, false, false, EX>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
-        mm<4, NPI, NPI, 3, false, false, EX>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
-        __syncthreads();  // (the slices' products: dP and M take their place)
+        mm<NC, NPI, NPI, 3, false, false, EX>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        mm<NC, NPI, NPI, 3, false, false, EX>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        sync();  // (the slices' products: dP and M take their place)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < NC; ++n) {
             float col[2] = {0.f, 0.f};
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -324,12 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
                 }
                 put2<NP>(&sm.c.dP[0][i][j], C * kLdc, p[0], p[1]);
                 put2<NP>(&sm.c.M[0][i][j], C * kLdc, m[0], m[1]);
+                if (R > 1 && rank && own(j + C / R)) {
+                    put2<NP>(&first.c.dP[0][i][j], C * kLdc, p[0], p[1]);
+                    put2<NP>(&first.c.M[0][i][j], C * kLdc, m[0], m[1]);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) col[e] += __shfl_xor_sync(0xffffffffu, col[e], o);
-                if (lane < 4) sm.col[warp & 3][ccol + n * 8 + 2 * lane + e] = col[e];
+                if (lane < 4) first.col[row0 / 16][ccol + n * 8 + 2 * lane + e] = col[e];
             }
         }
     }
@@ -361,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
             db[hf] += __shfl_xor_sync(0xffffffffu, db[hf], o);
         }
         if ((lane & 3) == 0) {
-            sm.row[half][row0 + acc_row(hf)] = row[hf];
-            sm.db[half][row0 + acc_row(hf)] = db[hf];
+            first.row[group][row0 + acc_row(hf)] = row[hf];
+            sm.db[group][row0 + acc_row(hf)] = db[hf];
         }
     }
 #pragma unroll
@@ -371,26 +390,32 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
     if (lane == 0) {
-        sm.far[warp] = far;
+        first.far[rank * 8 + warp] = far;
         sm.ss[warp] = ss;
     }
-    __syncthreads();
-    if (warp == 0) {  // the gates: sums from each token to the chunk's end
+    sync();
+    if (tid < C && tid < ch.n && own(tid)) {
+        float x = sm.rr[tid];
+#pragma unroll
+        for (int i = 0; i < CG; ++i) x += sm.db[i][tid];
+        a.dbeta[(int64_t)(ch.tok0 + tid) * a.Hv + h] = x;
+    }
+    if (warp == 0 && rank == 0) {  // the gates: sums from each token to the chunk's end
         float end = 0.f, s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            end += sm.far[w];
-            s += sm.ss[w];
-        }
+        for (int w = 0; w < 8 * R; ++w) end += sm.far[w];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += sm.ss[w];
         end += s * sm.g.eC;
         float x[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = 2 * lane + e;
-            x[e] = sm.row[0][t] + sm.row[1][t];
+            x[e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < CG; ++i) x[e] += sm.row[i][t];
 #pragma unroll
             for (int w = 0; w < 4; ++w) x[e] -= sm.col[w][t];
-            if (t < ch.n) a.dbeta[(int64_t)(ch.tok0 + t) * a.Hv + h] = sm.rr[t] + sm.db[0][t] + sm.db[1][t];
         }
         float sum = x[0] + x[1];  // of this lane's tokens and all behind
 #pragma unroll
@@ -459,15 +484,21 @@ cudaError_t back(const DeltaArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_next(kernel, dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kThreads, smem, st, a);
 }
-template <typename E, int NP, int DK>
+template <typename E, int NP, int DK, int R>
 cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
     static LaunchFit fit;
-    auto kernel = delta_grads_kernel<E, NP, DK>;
+    auto kernel = delta_grads_kernel<E, NP, DK, R>;
     const size_t smem = sizeof(GradSmem<E, NP, DK>);
     static_assert(sizeof(GradSmem<E, NP, DK>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
-    return launch_next(kernel, dim3(a.max_chunks, a.Hv), kThreads, smem, st, a);
+    return launch_next<R>(kernel, dim3(a.max_chunks * R, a.Hv), kThreads, smem, st, a);
+}
+// Two CTAs a cell while every CTA has an SM: a cell's time is its warp-level products' (fp32, 5 chunks of 2 heads of 64 by
+// 128: 31.2 -> 26.5 us).
+template <typename E, int NP, int DK>
+cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
+    return (int64_t)a.max_chunks * a.Hv * 2 <= paged_sms() ? grads<E, NP, DK, 2>(a, st) : grads<E, NP, DK, 1>(a, st);
 }
 
 }  // namespace
