@@ -184,8 +184,9 @@ __global__ void __launch_bounds__(kThreads) weights_mma_kernel(const WeightArgs 
 // A decoding step has G rows a KV head, one 16-row block of products for each 16 keys, and reads 2 D bytes a key.  Every
 // warp streams its own runs of keys through a private ring of kRing blocks of 16; a block's keys and old weights come by
 // asynchronous copies, its page is looked up a block ahead of them, and the rows stay in registers.  More rows are taken
-// block by block against each 16 keys.  Runs are 64 keys, or 256 where every warp has 8 of them all the same (a run
-// begins with a search for its segment).
+// block by block against each 16 keys.  A warp's blocks are one piece of the line of all segments' heads, so that it
+// searches for a segment, and loads its rows, once or twice (64 sequences of up to 8192 keys, in runs of 64 or 256 keys
+// dealt out to the warps in turn: 67 us, so 52).
 constexpr int kRing = 3, kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
 
 template <int D>
@@ -204,45 +205,44 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = a.B + a.n_groups;
     for (int s0 = S > kSegs ? 0 : -1; s0 >= 0 && s0 < S; s0 += kSegs)
-        if (line_up<kStreamThreads>(a, s0, 6, sm.line) < 0) {
+        if (line_up<kStreamThreads>(a, s0, 4, sm.line) < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
     const uint32_t ring = smem_u32(sm.k[warp]), olds = smem_u32(sm.old[warp]);
-    const int64_t step = (int64_t)gridDim.x * kStreamWarps;
+    const int64_t warps = (int64_t)gridDim.x * kStreamWarps, self = (int64_t)blockIdx.x * kStreamWarps + warp;
     for (int s0 = 0; s0 < S; s0 += kSegs) {
-        int log = 6, tiles = line_up<kStreamThreads>(a, s0, log, sm.line);
+        const int tiles = line_up<kStreamThreads>(a, s0, 4, sm.line);
         if (tiles < 0) {
             if (tid == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);
             return;
         }
-        if ((int64_t)tiles * a.Hkv >= 32 * step) {
-            log = 8;
-            tiles = line_up<kStreamThreads>(a, s0, log, sm.line);
-        }
-        // this warp's blocks of 16 keys, in the order of its runs
+        // this warp's blocks of 16 keys: an equal share of all (segment, head, block), one behind the other
         struct Place {
-            int64_t u;  // run
-            int s, h, k, end, len;
+            int64_t u;  // the block
+            int s, h, k, len;
         };
-        const int64_t units = (int64_t)tiles * a.Hkv;
-        auto enter = [&](Place &p) {  // the run's segment; false behind the last
-            if (p.u >= units) return false;
-            const int tile = (int)(p.u / a.Hkv), i = find(sm.line, tile);
+        const int64_t blocks = (int64_t)tiles * a.Hkv, share = blocks / warps, rest = blocks % warps;
+        const int64_t u0 = self * share + min(self, rest), u1 = u0 + share + (self < rest);
+        auto enter = [&](Place &p) {  // the block's segment; false behind the last
+            if (p.u >= u1) return false;
+            const int i = find(sm.line, (int)(p.u / a.Hkv));
+            const int64_t off = p.u - (int64_t)sm.line.at[i] * a.Hkv;
+            const int n = sm.line.at[i + 1] - sm.line.at[i];
             Segment g;
-            p.h = (int)(p.u - (int64_t)tile * a.Hkv);
+            p.h = (int)(off / n);
             p.s = s0 + i;
-            p.k = (tile - sm.line.at[i]) << log;
+            p.k = (int)(off - (int64_t)p.h * n) * 16;
             segment(a, p.s, g);
             p.len = g.len;
-            p.end = min(g.len, p.k + (1 << log));
             return true;
         };
         auto advance = [&](Place &p) {
+            if (++p.u >= u1) return false;
             p.k += 16;
-            if (p.k < p.end) return true;
-            p.u += step;
-            return enter(p);
+            if (p.k < p.len) return true;
+            p.k = 0;
+            return ++p.h < a.Hkv || enter(p);
         };
         // the page of this lane's key of a block (lanes 0 .. 15), as the table has it
         auto look_up = [&](const Place &p) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kStreamThreads) weights_stream_kernel(const We
             head = head + 1 == kRing ? 0 : head + 1;
         };
         Place in, at;
-        in.u = at.u = blockIdx.x + (int64_t)gridDim.x * warp;
+        in.u = u0;
         bool more = enter(in);
         at = in;
         bool left = more;
