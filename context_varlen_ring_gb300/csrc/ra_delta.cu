@@ -113,14 +113,16 @@ struct LocalSmem {
         bf16 k[NPI][C][LD], q[NPI][C][LD];
     };
     struct Made {
-        bf16 P[NP][C][kLdc], Y[NP][32][kLdy];
-        float diag[4][16][17];
+        bf16 P[C][kLdc], A[NP][C][kLdc], T[NP][C][kLdc];
+        union {
+            float diag[4][16][17];
+            bf16 Y[NP][32][kLdy];  // when the diagonal's blocks are inverted
+        };
     };
     union {
         Rows in;
         Made made;  // when the products with K and Q are done
     };
-    bf16 A[NP][C][kLdc], T[NP][C][kLdc];
     Gates g;
 };
 
@@ -169,21 +171,36 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
                     if (j + e + own <= i) y[e] = f * decay(sm.g, i, j + e) * x[n][2 * hf + e];
             }
             if (!own) {
-                put2<NP>(&sm.made.P[0][i][j], C * kLdc, y[0], y[1]);
+                x[n][2 * hf] = y[0];
+                x[n][2 * hf + 1] = y[1];
             } else if (n / 2 <= w) {
-                put2<NP>(&sm.A[0][i][j], C * kLdc, y[0], y[1]);
+                put2<NP>(&sm.made.A[0][i][j], C * kLdc, y[0], y[1]);
                 if (n / 2 == w) {
                     sm.made.diag[w][i & 15][j & 15] = y[0];
                     sm.made.diag[w][i & 15][(j & 15) + 1] = y[1];
                 }
             } else {
-                put2<NP>(&sm.T[0][i][j], C * kLdc, 0.f, 0.f);
+                put2<NP>(&sm.made.T[0][i][j], C * kLdc, 0.f, 0.f);
             }
         }
     uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
     if (!own) {
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        store_square<NP, 128>(tp + NP * C * C, &sm.made.P[0][0][0]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {  // (a part at a time: four CTAs an SM)
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float *y = x[n] + 2 * hf;
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(y[0], y[1]);
+                    *reinterpret_cast<__nv_bfloat162 *>(&sm.made.P[row0 + acc_row(hf)][acc_col(n)]) = b;
+                    y[0] -= __low2float(b);
+                    y[1] -= __high2float(b);
+                }
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+            store_square<1, 128>(tp + (NP + p) * C * C, &sm.made.P[0][0]);
+            asm volatile("bar.sync 2, 128;" ::: "memory");
+        }
         return;
     }
     auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };  // (of the four that go on)
@@ -203,13 +220,13 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 const bf16 b = __float2bfloat16_rn(s);
-                sm.T[p][row0 + i][row0 + lane] = b;
+                sm.made.T[p][row0 + i][row0 + lane] = b;
                 s -= __bfloat162float(b);
             }
         }
     }
     sync();
-    const uint32_t Ab = smem_u32(sm.A), Tb = smem_u32(sm.T), Yb = smem_u32(sm.made.Y);
+    const uint32_t Ab = smem_u32(sm.made.A), Tb = smem_u32(sm.made.T), Yb = smem_u32(sm.made.Y);
     auto tile = [&](uint32_t b, int r, int col) { return b + (r * kLdc + col) * 2; };
     auto put = [&](bf16 *dst, int ld, int plane, const float (&x)[2][4], float sign) {
 #pragma unroll
@@ -226,7 +243,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         __syncwarp();
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
-        put(&sm.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
+        put(&sm.made.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
     }
     sync();
     {  // rows 32 .. 63 by columns 0 .. 31: a block of 16 x 16 each warp
@@ -237,10 +254,10 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         sync();
         zero(y);
         mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
-        put(&sm.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
+        put(&sm.made.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
     }
     sync();
-    store_square<NP, 128>(tp, &sm.T[0][0][0]);
+    store_square<NP, 128>(tp, &sm.made.T[0][0][0]);
 }
 
 // ------------------------------------------------------------ the walk
