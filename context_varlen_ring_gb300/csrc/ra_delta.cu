@@ -99,10 +99,12 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArg
 }
 
 // ------------------------------------------------------------ T and P
-// Bound: what it writes, 16 KB a chunk and head for each part; but each chunk is a chain of small steps, and the SMs
-// hold few at once.  So half of the warps make A and its inverse, the other half P (8192 chunks, two parts: 264 us with
-// all of it in four warps, 208 so).  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a lane a
-// column; then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
+// Floor: what it writes, 16 KB a chunk and head for each part.  Bound: each chunk is a chain of small steps, an SM holds
+// four, and shared memory's port is busy for 64 % of the time (its K, Q, A, T and P, all read and written in pieces of 16
+// bytes).  So half of the warps make A and its inverse, the other half P (8576 chunks, two parts: 264 us with all of it in
+// four warps, 208 so), what is made takes the place of K and Q, P a part at a time (160), and the gates and the diagonal's
+// blocks are read 8 and 16 bytes at a time (160 -> 135).  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a
+// lane a column; then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
 constexpr int kLocalThreads = 256;
 constexpr int kLdy = 40;
 
@@ -115,7 +117,7 @@ struct LocalSmem {
     struct Made {
         bf16 P[C][kLdc], A[NP][C][kLdc], T[NP][C][kLdc];
         union {
-            float diag[4][16][17];
+            alignas(16) float diag[4][16][20];
             bf16 Y[NP][32][kLdy];  // when the diagonal's blocks are inverted
         };
     };
@@ -158,17 +160,25 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     zero(x);
     mm<8, NPI, NPI, 3, false, false, EX>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
     __syncthreads();  // (what is made of them takes the place of K and Q)
+    float2 Gi[2];
+    float f[2];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int hf = 0; hf < 2; ++hf) {
+        const int i = row0 + acc_row(hf);
+        Gi[hf] = make_float2(sm.g.hi[i], sm.g.lo[i]);
+        f[hf] = own ? sm.g.beta[i] : a.scale;
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int j = acc_col(n);
+        const float2 hi = *reinterpret_cast<const float2 *>(sm.g.hi + j), lo = *reinterpret_cast<const float2 *>(sm.g.lo + j);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const int i = row0 + acc_row(hf), j = acc_col(n);
+            const int i = row0 + acc_row(hf);
             float y[2] = {0.f, 0.f};
-            const float f = own ? sm.g.beta[i] : a.scale;
             if (n / 2 <= w) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (j + e + own <= i) y[e] = f * decay(sm.g, i, j + e) * x[n][2 * hf + e];
+                if (j + own <= i) y[0] = f[hf] * gate_exp(Gi[hf], make_float2(hi.x, lo.x)) * x[n][2 * hf];
+                if (j + 1 + own <= i) y[1] = f[hf] * gate_exp(Gi[hf], make_float2(hi.y, lo.y)) * x[n][2 * hf + 1];
             }
             if (!own) {
                 x[n][2 * hf] = y[0];
@@ -176,13 +186,13 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
             } else if (n / 2 <= w) {
                 put2<NP>(&sm.made.A[0][i][j], C * kLdc, y[0], y[1]);
                 if (n / 2 == w) {
-                    sm.made.diag[w][i & 15][j & 15] = y[0];
-                    sm.made.diag[w][i & 15][(j & 15) + 1] = y[1];
+                    *reinterpret_cast<float2 *>(&sm.made.diag[w][i & 15][j & 15]) = make_float2(y[0], y[1]);
                 }
             } else {
                 put2<NP>(&sm.made.T[0][i][j], C * kLdc, 0.f, 0.f);
             }
         }
+    }
     uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
     if (!own) {
 #pragma unroll
@@ -211,7 +221,13 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
         for (int i = 0; i < 16; ++i) {
             float s = i == lane ? 1.f : 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) s -= sm.made.diag[w][i][m] * t[m];
+            for (int m = 0; m < i; m += 4) {
+                const float4 d = *reinterpret_cast<const float4 *>(&sm.made.diag[w][i][m]);
+                s -= d.x * t[m];
+                if (m + 1 < i) s -= d.y * t[m + 1];
+                if (m + 2 < i) s -= d.z * t[m + 2];
+                if (m + 3 < i) s -= d.w * t[m + 3];
+            }
             t[i] = s;
         }
 #pragma unroll
