@@ -238,6 +238,30 @@ def test_long_chains_stay_exact(ra, dk, dv):
     R.delta_check(last, wl, "state")
 
 
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, "fp32"), (128, 64, "fp32"), (64, 128, "fp32"), (128, 128, "fp32"),
+                                         (64, 64, "bf16"), (128, 64, "bf16"), (64, 128, "bf16")])
+@pytest.mark.parametrize("hk,hv", [(1, 2), (4, 16)])
+def test_few_and_many_heads(ra, hk, hv, dk, dv, dtype):
+    """Few heads: narrow slices of the state, two CTAs a chunk's gradients.  Many: wide slices, one."""
+    lens = [70, 3, 64, 130, 0, 1]
+    q, k, v, g, beta, cu, cud = make(lens, hk, hv, dk, dv, dtype, "usual", 11, tail=1)
+    s0, ds = states(6, hv, dk, dv, 1), states(6, hv, dk, dv, 2)
+    want, last = ref(q, k, v, g, beta, cu, s0, 0.3)
+    got, s1 = ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0, final_state=True, scale=0.3)
+    R.delta_check(got[:cu[-1]], want, "out")
+    R.delta_check(s1, last, "state")
+    R.delta_check(ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0, scale=0.3)[0][:cu[-1]], want, "out")
+    dout = torch.randn(v.shape, generator=torch.Generator().manual_seed(9)).to(v.dtype).cuda()
+    want = ref(q, k, v, g, beta, cu, s0, 0.3, dout, ds)
+    got = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds, scale=0.3)
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+        R.delta_check(x[:cu[-1]], y[:cu[-1]], name)
+    R.delta_check(got[5], want[5], "dstate0")
+    again = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds, scale=0.3)
+    assert all(torch.equal(x[:cu[-1]] if i < 5 else x, y[:cu[-1]] if i < 5 else y) for i, (x, y) in enumerate(zip(got, again)))
+    assert ra.device_status() == 0
+
+
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
 def test_many_sequences(ra, dk, dv):
     """More sequences than the plan lines up at a time, and than it sorts."""
