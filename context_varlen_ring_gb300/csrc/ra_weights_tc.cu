@@ -2,7 +2,8 @@
 // 5th-generation tensor cores: chunks of a prompt, and prefixes of a batch.
 //
 // Bound: 2 d flops and one exponential for each (row, key) pair; the tensor
-// pipe and the special-function unit take 512 cycles each for 128 x 128 of them.
+// pipe and the special-function unit take 512 cycles each for 128 x 128 of them
+// (2048 tokens of 32 heads behind 30720 keys of 8: 488 us, 1.09 PFLOP/s).
 // Keys are the rows of S (A operand, a key a TMEM lane) and query rows its
 // columns, so a key's weight is summed in one thread's registers and no sum
 // passes between threads.  A unit is 256 keys of one KV head: two tiles in
