@@ -35,7 +35,7 @@ constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
 constexpr int kRing = 4;               // tiles of rows
 constexpr uint32_t kOffQ = 2 * kTile;  // behind the keys
 constexpr uint32_t kOffBar = kOffQ + kRing * kTile;
-constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+constexpr uint32_t kSmem = kOffBar + 320 + 1024;
 
 struct TcParams {
     CUtensorMap tmQ, tmK;
@@ -46,8 +46,9 @@ struct TcParams {
 
 struct Shared {
     Line line;
-    alignas(16) float off[16][2][64];  // (read as float4) of each warp's columns of two tiles of rows: -lse in base 2
-    float sum[2][4][128];              // of the second half of the columns, a unit after another
+    alignas(16) float off[kRing][128];  // (read as float4) of the rows of a tile: -lse in base 2
+    int none[kRing][2];                 // whether any of a tile's first, or last, 64 rows adds nothing
+    float sum[2][4][128];               // of the second half of the columns, a unit after another
 };
 
 struct Unit {
@@ -73,6 +74,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     uint64_t *mma_done = bars + 26;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 27);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 28);
+    uint64_t *o_full = bars + 29;   // [kRing] a tile's offsets
+    uint64_t *o_empty = bars + 33;  // [kRing] (16 warps)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -81,6 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         for (int i = 0; i < kRing; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, 16);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
@@ -214,55 +219,69 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         volatile int local_abort = 0;
         const WaitCtl drain{&local_abort, a.status, p.budget_ns};
         (void)mbar_wait_warp(mma_done, 0, drain);
+    } else if (warp == 3) {
+        // ------------------------------------------------ the rows' offsets, four a lane, for all of the warps below
+        // (each for itself, 488 us: XX so)
+        uint32_t no = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            Unit w;
+            unit(u, w);
+            const int rows = w.g.n << p.log2G;
+            for (int j = 0; j < w.tiles; ++j, ++no) {
+                const int r0 = w.first + 128 * j + 4 * lane;
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = r0 + e < rows ? r0 + e : 0;
+                    x[e] = __ldg(a.lse + (int64_t)(w.h * a.G + (r & (a.G - 1))) * a.T + w.g.tok0 + (r >> p.log2G));
+                }
+                ok = mbar_wait_warp(o_empty + no % kRing, ((no / kRing) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool none = r0 + e >= rows || x[e] == -INFINITY;
+                    x[e] = none ? -INFINITY : -x[e] * 1.4426950408889634f;
+                    any |= x[e] == -INFINITY;
+                }
+                const uint32_t vote = __ballot_sync(0xffffffffu, any);
+                *reinterpret_cast<float4 *>(sh.off[no % kRing] + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+                if (lane < 2) sh.none[no % kRing][lane] = (vote >> (16 * lane) & 0xffffu) != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_full + no % kRing);
+            }
+        }
     } else if (warp >= 4) {
         // ------------------------------------------------ exponentials and sums
         const int k = warp >= 12 ? 1 : 0, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4 .. 7 and 12 .. 15: the first half
         const int m = (warp & 3) * 32 + lane;                                // TMEM lane: the key
         const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k + 64u * half;
-        uint32_t ns = 0, nu = 0;
+        uint32_t ns = 0, nu = 0, no = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             Unit w;
             unit(u, w);
-            if (k >= w.parts) continue;
+            if (k >= w.parts) {
+                for (int j = 0; j < w.tiles && ok; ++j, ++no) {
+                    ok = mbar_wait_warp(o_full + no % kRing, (no / kRing) & 1u, wc);
+                    if (ok && lane == 0) mbar_arrive(o_empty + no % kRing);
+                }
+                continue;
+            }
             const int key = w.k0 + 128 * k + m;
-            // the first row that sees the key
-            const int from = w.own && a.causal ? (key - (w.g.len - w.g.n)) * a.G : 0;
-            // a tile's offsets: two rows a lane, loaded a tile ahead and made of what was loaded when it is due; and
-            // whether any of the warp's 64 adds nothing
-            float next[2];
-            int left = 0;  // rows from the lane's first on
-            auto look = [&](int r0) {
-                r0 += 64 * half + 2 * lane;
-                left = (w.g.n << p.log2G) - r0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = left > e ? r0 + e : 0, t = r >> p.log2G;
-                    next[e] = __ldg(a.lse + (int64_t)(w.h * a.G + (r & (a.G - 1))) * a.T + w.g.tok0 + t);
-                }
-            };
-            auto put = [&](uint32_t b) {
-                bool any = false;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool none = e >= left || next[e] == -INFINITY;
-                    next[e] = none ? -INFINITY : -next[e] * 1.4426950408889634f;
-                    any |= none || next[e] == -INFINITY;
-                }
-                reinterpret_cast<float2 *>(sh.off[warp - 4][b])[lane] = make_float2(next[0], next[1]);
-                return __any_sync(0xffffffffu, any);
-            };
-            look(w.first);
-            bool odd = put(ns & 1);
+            // the first row that sees the key, and the first that all of the warp's keys are seen by
+            const bool causal = w.own && a.causal;
+            const int from = causal ? (key - (w.g.len - w.g.n)) * a.G : 0, all_from = causal ? from + (31 - lane) * a.G : 0;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll 1
-            for (int j = 0; j < w.tiles; ++j, ++ns) {
-                const uint32_t b = ns & 1;
+            for (int j = 0; j < w.tiles; ++j, ++ns, ++no) {
+                const uint32_t b = ns & 1, slot = no % kRing;
                 const int r0 = w.first + 128 * j + 64 * half;
-                if (j + 1 < w.tiles) look(w.first + 128 * (j + 1));
-                const bool cut = odd || __any_sync(0xffffffffu, from > r0);
-                __syncwarp();  // (the offsets that the other lanes put)
+                ok = mbar_wait_warp(o_full + slot, (no / kRing) & 1u, wc);
+                if (!ok) break;
+                const bool cut = sh.none[slot][half] || all_from > r0;
                 ok = mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
@@ -274,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         tc_fence_before();
                         mbar_arrive(s_empty + 2 * k + b);
                     }
-                    const float4 *off = reinterpret_cast<const float4 *>(sh.off[warp - 4][b] + c);
+                    const float4 *off = reinterpret_cast<const float4 *>(sh.off[slot] + 64 * half + c);
                     if (!cut) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -288,15 +307,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         const int seen = from - r0 - c;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float f = sh.off[warp - 4][b][c + i];
+                            const float f = sh.off[slot][64 * half + c + i];
                             const float x = ex2_approx(fmaf(__uint_as_float(v[i]), a.scale_log2, f));
                             sum[0].x += i >= seen && f != -INFINITY ? x : 0.f;
                         }
                     }
                 }
-                if (j + 1 < w.tiles) odd = put(b ^ 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_empty + slot);
             }
-            __syncwarp();  // (the last tile's offsets are read before the next unit's first take their place)
             // the second half of the columns goes to the threads of the first, which are two tiles behind at most and so
             // two units: of the four places none is written before it was read
             const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
