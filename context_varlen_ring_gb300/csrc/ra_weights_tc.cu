@@ -279,12 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             for (int j = 0; j < w.tiles; ++j, ++ns, ++no) {
                 const uint32_t b = ns & 1, slot = no % kRing;
                 const int r0 = w.first + 128 * j + 64 * half;
-                ok = mbar_wait_warp(o_full + slot, (no / kRing) & 1u, wc);
-                if (!ok) break;
-                const bool cut = sh.none[slot][half] || all_from > r0;
-                ok = mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
-                if (!ok) break;
+                // (both looked at in one go: they are there as a rule)
+                const bool o = mbar_try_wait(o_full + slot, (no / kRing) & 1u), s = mbar_try_wait(s_full + 2 * k + b, (ns >> 1) & 1u);
+                if (!__all_sync(0xffffffffu, o && s)) {
+                    ok = mbar_wait_warp(o_full + slot, (no / kRing) & 1u, wc) && mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
+                    if (!ok) break;
+                }
                 tc_fence_after();
+                const bool cut = sh.none[slot][half] || all_from > r0;
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     uint32_t v[32];
