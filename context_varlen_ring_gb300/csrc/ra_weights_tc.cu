@@ -35,7 +35,9 @@ constexpr uint32_t kTile = 2 * kHalf;  // 128 rows x 128 bf16
 constexpr int kRing = 4;               // tiles of rows
 constexpr uint32_t kOffQ = 2 * kTile;  // behind the keys
 constexpr uint32_t kOffBar = kOffQ + kRing * kTile;
-constexpr uint32_t kSmem = kOffBar + 320 + 1024;
+constexpr uint32_t kSmem = kOffBar + 384 + 1024;
+
+constexpr int kPlaces = 8;
 
 struct TcParams {
     CUtensorMap tmQ, tmK;
@@ -47,8 +49,8 @@ struct TcParams {
 struct Shared {
     Line line;
     alignas(16) float off[kRing][128];  // (read as float4) of the rows of a tile: -lse in base 2
-    int none[kRing][2];                 // whether any of a tile's first, or last, 64 rows adds nothing
-    float sum[2][4][128];               // of the second half of the columns, a unit after another
+    int none[kRing];                    // whether any of a tile's rows adds nothing
+    float sum[2][kPlaces][128];         // of the odd tiles of rows, a unit after another
 };
 
 struct Unit {
@@ -69,13 +71,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     uint64_t *q_full = bars + 2;    // [kRing] a tile of rows
     uint64_t *q_empty = bars + 6;   // [kRing]
     uint64_t *s_full = bars + 10;   // [2][2] S of a warpgroup's buffer
-    uint64_t *s_empty = bars + 14;  // [2][2] (256 arrivals)
-    uint64_t *part = bars + 18;     // [2][4] a unit's second halves are summed (128 arrivals)
-    uint64_t *mma_done = bars + 26;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 27);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 28);
-    uint64_t *o_full = bars + 29;   // [kRing] a tile's offsets
-    uint64_t *o_empty = bars + 33;  // [kRing] (16 warps)
+    uint64_t *s_empty = bars + 14;  // [2][2] (128 arrivals)
+    uint64_t *part = bars + 18;     // [2][kPlaces] a unit's odd tiles are summed (128 arrivals)
+    uint64_t *mma_done = bars + 34;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 36);
+    uint64_t *o_full = bars + 37;   // [kRing] a tile's offsets
+    uint64_t *o_empty = bars + 41;  // [kRing] (8 warps)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -85,13 +87,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
             mbar_init(o_full + i, 1);
-            mbar_init(o_empty + i, 16);
+            mbar_init(o_empty + i, 8);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(s_empty + i, 256);
+            mbar_init(s_empty + i, 128);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(part + i, 128);
+        for (int i = 0; i < 2 * kPlaces; ++i) mbar_init(part + i, 128);
         mbar_init(mma_done, 1);
         fence_mbar_init();
         tma_prefetch_desc(&p.tmQ);
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     } else if (warp == 1) {
         // ------------------------------------------------ products
         const uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
-        uint32_t nk = 0, nq = 0, ns[2] = {0, 0};
+        uint32_t nk = 0, nq = 0, ns[2][2] = {};  // (uses of each buffer)
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
             Unit w;
@@ -190,14 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             ok = mbar_wait_warp(k_full, nk & 1u, wc);
             ++nk;
             for (int j = 0; j < w.tiles && ok; ++j, ++nq) {
-                const uint32_t s = nq % kRing;
+                const uint32_t s = nq % kRing, b = nq & 1;
                 ok = mbar_wait_warp(q_full + s, (nq / kRing) & 1u, wc);
                 if (!ok) break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (t >= w.parts) break;
-                    const uint32_t b = ns[t] & 1;
-                    ok = mbar_wait_warp(s_empty + 2 * t + b, ((ns[t] >> 1) & 1u) ^ 1u, wc);
+                    ok = mbar_wait_warp(s_empty + 2 * t + b, ((b ? ns[t][1] : ns[t][0]) & 1u) ^ 1u, wc);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t dk = sdesc_sw128(base_s + t * kTile, 16, 1024);
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         tc_mma_ss_w(tmem + 256u * t + 128u * b, dk + o, dq + o, idesc, ks > 0);
                     }
                     tc_commit_w(s_full + 2 * t + b);
-                    ++ns[t];
+                    ns[t][0] += b == 0;
+                    ns[t][1] += b;
                 }
                 tc_commit_w(q_empty + s);
             }
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         (void)mbar_wait_warp(mma_done, 0, drain);
     } else if (warp == 3) {
         // ------------------------------------------------ the rows' offsets, four a lane, for all of the warps below
-        // (each for itself, 488 us: XX so)
+        // (2048 tokens at 32768 keys; each for itself, 488 us: 452 so)
         uint32_t no = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -247,16 +249,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 }
                 const uint32_t vote = __ballot_sync(0xffffffffu, any);
                 *reinterpret_cast<float4 *>(sh.off[no % kRing] + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
-                if (lane < 2) sh.none[no % kRing][lane] = (vote >> (16 * lane) & 0xffffu) != 0;
+                if (lane == 0) sh.none[no % kRing] = vote != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_full + no % kRing);
             }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------ exponentials and sums
-        const int k = warp >= 12 ? 1 : 0, half = (warp >> 2) & 1 ? 0 : 1;  // warps 4 .. 7 and 12 .. 15: the first half
-        const int m = (warp & 3) * 32 + lane;                                // TMEM lane: the key
-        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k + 64u * half;
+        // two warpgroups a tile of keys, which take its tiles of rows in turn
+        const int k = warp >= 12 ? 1 : 0;
+        const uint32_t b = (warp >> 2) & 1 ? 0 : 1;  // its buffer: warps 4 .. 7 and 12 .. 15 have the even tiles
+        const int m = (warp & 3) * 32 + lane;        // TMEM lane: the key
+        const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * k + 128u * b;
         uint32_t ns = 0, nu = 0, no = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -264,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             unit(u, w);
             if (k >= w.parts) {
                 for (int j = 0; j < w.tiles && ok; ++j, ++no) {
+                    if ((no & 1) != b) continue;
                     ok = mbar_wait_warp(o_full + no % kRing, (no / kRing) & 1u, wc);
                     if (ok && lane == 0) mbar_arrive(o_empty + no % kRing);
                 }
@@ -276,26 +281,27 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll 1
-            for (int j = 0; j < w.tiles; ++j, ++ns, ++no) {
-                const uint32_t b = ns & 1, slot = no % kRing;
-                const int r0 = w.first + 128 * j + 64 * half;
+            for (int j = 0; j < w.tiles; ++j, ++no) {
+                if ((no & 1) != b) continue;
+                const uint32_t slot = no % kRing, ph = ns++ & 1;
+                const int r0 = w.first + 128 * j;
                 // (both looked at in one go: they are there as a rule)
-                const bool o = mbar_try_wait(o_full + slot, (no / kRing) & 1u), s = mbar_try_wait(s_full + 2 * k + b, (ns >> 1) & 1u);
+                const bool o = mbar_try_wait(o_full + slot, (no / kRing) & 1u), s = mbar_try_wait(s_full + 2 * k + b, ph);
                 if (!__all_sync(0xffffffffu, o && s)) {
-                    ok = mbar_wait_warp(o_full + slot, (no / kRing) & 1u, wc) && mbar_wait_warp(s_full + 2 * k + b, (ns >> 1) & 1u, wc);
+                    ok = mbar_wait_warp(o_full + slot, (no / kRing) & 1u, wc) && mbar_wait_warp(s_full + 2 * k + b, ph, wc);
                     if (!ok) break;
                 }
                 tc_fence_after();
-                const bool cut = sh.none[slot][half] || all_from > r0;
+                const bool cut = sh.none[slot] || all_from > r0;
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
+                for (int c = 0; c < 128; c += 32) {
                     uint32_t v[32];
-                    tmem_ld32(tS + 128u * b + c, v);
-                    if (c) {  // (all columns are read)
+                    tmem_ld32(tS + c, v);
+                    if (c == 96) {  // (all columns are read)
                         tc_fence_before();
                         mbar_arrive(s_empty + 2 * k + b);
                     }
-                    const float4 *off = reinterpret_cast<const float4 *>(sh.off[slot] + 64 * half + c);
+                    const float4 *off = reinterpret_cast<const float4 *>(sh.off[slot] + c);
                     if (!cut) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         const int seen = from - r0 - c;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float f = sh.off[slot][64 * half + c + i];
+                            const float f = sh.off[slot][c + i];
                             const float x = ex2_approx(fmaf(__uint_as_float(v[i]), a.scale_log2, f));
                             sum[0].x += i >= seen && f != -INFINITY ? x : 0.f;
                         }
@@ -318,15 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_empty + slot);
             }
-            // the second half of the columns goes to the threads of the first, which are two tiles behind at most and so
-            // two units: of the four places none is written before it was read
+            // the odd tiles' sums go to the threads of the even ones.  Products are issued tile after tile, and a tile's
+            // only when its buffer was read: so the odd ones are two tiles ahead at most, and, with units of one tile,
+            // where every other one is nothing to them, four units: of the eight places none is written before it was read
             const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            const uint32_t at = nu & 3;
-            if (half) {
+            const uint32_t at = nu % kPlaces;
+            if (b) {
                 sh.sum[k][at][m] = all;
-                mbar_arrive(part + 4 * k + at);
+                mbar_arrive(part + kPlaces * k + at);
             } else {
-                ok = ok && mbar_wait_warp(part + 4 * k + at, (nu >> 2) & 1u, wc);
+                ok = ok && mbar_wait_warp(part + kPlaces * k + at, (nu / kPlaces) & 1u, wc);
                 int64_t page;
                 int row;
                 if (ok && key < w.g.len && place(a, w.s, key, page, row))
