@@ -3,13 +3,15 @@
 //
 // Bound: 2 d flops and one exponential for each (row, key) pair; the tensor
 // pipe and the special-function unit take 512 cycles each for 128 x 128 of them
-// (2048 tokens of 32 heads behind 30720 keys of 8: 488 us, 1.09 PFLOP/s).
+// (2048 tokens of 32 heads behind 30720 keys of 8: 420 us, 1.27 PFLOP/s).
 // Keys are the rows of S (A operand, a key a TMEM lane) and query rows its
 // columns, so a key's weight is summed in one thread's registers and no sum
-// passes between threads.  A unit is 256 keys of one KV head: two tiles in
-// shared memory that meet every tile of 128 query rows, which come by TMA through
-// a ring; two warpgroups have a tile of keys each, with two buffers of S, so that
-// the next product runs beside the exponentials.  The next unit's keys are
+// passes between threads but one of each unit.  A unit is 256 keys of one KV head:
+// two tiles in shared memory that meet every tile of 128 query rows, which come by
+// TMA through a ring.  Each tile of keys has two buffers of S and two warpgroups,
+// which take its tiles of rows in turn, so that the next product runs beside the
+// exponentials (a warpgroup with half of every tile's columns waits twice as
+// often: 439 us).  One more warp makes the rows' offsets.  The next unit's keys are
 // loaded beside this unit's rows.  Every wait is bounded as in the rest of the
 // library.
 #include <cuda.h>
