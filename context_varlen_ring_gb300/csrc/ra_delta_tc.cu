@@ -143,6 +143,19 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint64_t b, uin
         }
 }
 
+// The same with the two parts of 32 tokens side by side.
+template <int NP>
+__device__ __forceinline__ void mma_rows_in(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
+    bool more = false;
+#pragma unroll
+    for (int q = NP - 1; q >= 0; --q)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            tc_mma_ts_w(d, x + 32 * (ks >> 1) + 16 * q + 8 * (ks & 1), b + ((uint32_t)ks * 2048u >> 4), idesc, more);
+            more = true;
+        }
+}
+
 template <int NP>
 __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) {
     using Sh = Shape<NP>;
@@ -259,23 +272,32 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                if (want && i > 0) {
-                    ok = mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
-                    if (!ok) break;
+                // of two parts: Q's rows behind the chain's next product; of three: with K's
+                const bool both = want && NP == 3;
+                auto out_read = [&]() {
+                    ok = i == 0 || mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
                     tc_fence_after();
-                }
-                // (K's rows, and with them Q's: half as many products to issue, 394 -> 386 us)
-                mma_state<NP>(tmem + kColX, tmem + kColS, dK, want ? id128k : id64);
+                    return ok;
+                };
+                if (both && !out_read()) break;
+                mma_state<NP>(tmem + kColX, tmem + kColS, dK, both ? id128k : id64);
                 tc_commit_w(x_full);
                 ok = mbar_wait_warp(r_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
                 mma_square<NP>(tmem + kColX, tmem + kColD, dT, 32, id64);
                 tc_commit_w(u_full);
+                if (want && !both) {
+                    if (!out_read()) break;
+                    mma_state<NP>(tmem + kColQ, tmem + kColS, dK + (kHalf / 2 >> 4), id64);
+                }
                 ok = mbar_wait_warp(u_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_rows<NP>(tmem + kColD, tmem + kColS, dKn, id128, false);
+                if (NP == 2)
+                    mma_rows_in<NP>(tmem + kColD, tmem + kColX, dKn, id128);
+                else
+                    mma_rows<NP>(tmem + kColD, tmem + kColS, dKn, id128, false);
                 tc_commit_w(d_full);
                 if (want) {
                     mma_square<NP>(tmem + kColP, tmem + kColU<NP>, dP, 32, id64);
@@ -316,26 +338,30 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
         bool ok = true;
         // four of the gates of this thread's tokens
         auto four = [&](const float (&x)[C], int j) { return *reinterpret_cast<const float4 *>(x + 32 * half + 4 * j); };
-        // the output of chunk i: scale e^G (Q S0) + P u
-        auto output = [&](int i, const DeltaChunk &ch) {
-            ok = mbar_wait_warp(o_full, i & 1u, wc);
-            if (!ok) return;
-            tc_fence_after();
-            uint32_t x[32], y[32];
-            tmem_ld32x2(at + kColQ + 32 * half, at + kColP + 32 * half, x, y);
-            tc_fence_before();
-            mbar_arrive(o_empty);
+        // the output of chunk i, scale e^G (Q S0) + P u: 16 of this thread's 32 tokens
+        auto output = [&](int i, const DeltaChunk &ch, int e) {
+            if (e == 0) {
+                ok = mbar_wait_warp(o_full, i & 1u, wc);
+                if (!ok) return;
+                tc_fence_after();
+            }
+            uint32_t x[16], y[16];
+            tmem_ld16x2(at + kColQ + 32 * half + 16 * e, at + kColP + 32 * half + 16 * e, x, y);
+            if (e) {
+                tc_fence_before();
+                mbar_arrive(o_empty);
+            }
             const Gates &g = gates[i & 1];
             const int64_t stride = (int64_t)a.Hv * kD;
-            bf16 *o = static_cast<bf16 *>(a.out) + ((int64_t)(ch.tok0 + 32 * half) * a.Hv + h) * kD + m;
-            const int rows = ch.n - 32 * half;
+            const int first = 32 * half + 16 * e, rows = ch.n - first;
+            bf16 *o = static_cast<bf16 *>(a.out) + ((int64_t)(ch.tok0 + first) * a.Hv + h) * kD + m;
             auto put = [&](bool all) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 e = four(g.eG, j);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 d = four(g.eG, 4 * e + j);
                     const float2 s = make_float2(a.scale, a.scale);
-                    const float2 p0 = fma2(mul2(s, make_float2(e.x, e.y)), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
-                    const float2 p1 = fma2(mul2(s, make_float2(e.z, e.w)), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
+                    const float2 p0 = fma2(mul2(s, make_float2(d.x, d.y)), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
+                    const float2 p1 = fma2(mul2(s, make_float2(d.z, d.w)), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
                     if (all || 4 * j < rows) o[0] = __float2bfloat16_rn(p0.x);
                     if (all || 4 * j + 1 < rows) o[stride] = __float2bfloat16_rn(p0.y);
                     if (all || 4 * j + 2 < rows) o[2 * stride] = __float2bfloat16_rn(p1.x);
@@ -343,12 +369,14 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     o += 4 * stride;
                 }
             };
-            if (rows >= 32)
+            if (rows >= 16)
                 put(true);
             else
                 put(false);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(g_empty + (i & 1));
+            if (e) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(g_empty + (i & 1));
+            }
         };
         // chunk i's values, pairs of tokens as they are: taken while the chunk ahead waits for its products
         uint32_t d[16];
@@ -376,8 +404,9 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             last = ch;
             ch = a.chunk[c0 + i];
             if (NP == 3 && want && i > 0) {
-                output(i - 1, last);
+                output(i - 1, last, 0);
                 if (!ok) break;
+                output(i - 1, last, 1);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -397,8 +426,8 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     p[(2 * j + 1) * kD] = S[j].y;
                 }
             }
-            if (NP == 2 && want && i > 0) {
-                output(i - 1, last);
+            if (NP == 2 && want && i > 0) {  // (half of it beside K S0, and half beside T R)
+                output(i - 1, last, 0);
                 if (!ok) break;
             }
             ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc);
@@ -431,6 +460,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             tmem_put_wait();
             tc_fence_before();
             mbar_arrive(r_ready);
+            if (NP == 2 && want && i > 0) output(i - 1, last, 1);
             ok = mbar_wait_warp(u_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
@@ -447,7 +477,10 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     y[2 * j] = mul2(make_float2(e.x, e.y), v[2 * j]);
                     y[2 * j + 1] = mul2(make_float2(e.z, e.w), v[2 * j + 1]);
                 }
-                put_parts<NP>(at + kColS + 16 * half, 32, y);
+                if (NP == 2)
+                    put_parts<NP>(at + kColX + 32 * half, 16, y);
+                else
+                    put_parts<NP>(at + kColS + 16 * half, 32, y);
                 if (keep) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -479,7 +512,10 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 for (int j = 0; j < 32; ++j) S[j] = fma2(eC, S[j], f2(x[2 * j], x[2 * j + 1]));
             }
         }
-        if (ok && want && n_chunks > 0) output(n_chunks - 1, ch);
+        if (ok && want && n_chunks > 0) {
+            output(n_chunks - 1, ch, 0);
+            if (ok) output(n_chunks - 1, ch, 1);
+        }
         if (ok && !bad && a.state_out && slot >= 0) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
