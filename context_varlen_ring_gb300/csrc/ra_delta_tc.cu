@@ -5,7 +5,7 @@
 // Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
 // the output Q S0 and P u) follow one another, and the next chunk needs their
 // result; a batch's longest sequence is a chain of hundreds of them (24 sequences
-// of 32768 tokens, 16 heads, the longest 7422: 380 us, 6300 cycles a chunk, of
+// of 32768 tokens, 16 heads, the longest 7422: 365 us, 6300 cycles a chunk, of
 // which the products take 1900 and what they wait for the rest).  So a CTA
 // has one head of one sequence, with the whole state, and everything is held
 // the other way round (a column of v to a TMEM lane): the state is the A operand
@@ -16,11 +16,12 @@
 //    warpgroups, a thread a lane and half of the columns each, hold the state
 //    in registers (fp32), make bf16 parts of what the next product reads and
 //    put them into TMEM.
-//  * the output's products run behind those that the chain needs, and are read
-//    while the next chunk's first ones run.
+//  * the output's products (with two parts) run behind those that the chain
+//    needs, and are read, half at a time, while the next chunk's products run.
 // TMEM columns: 0 the state's growth (and, ahead of it, R's parts); 128 K S0,
-// then u; 192 Q S0; 256 the state's parts, then e^(G_63 - G) u's; 448 P u; u's
-// parts behind the state's, or (of three) in their place.
+// then u, with two parts then e^(G_63 - G) u's; 192 Q S0; 256 the state's parts
+// (with three, e^(G_63 - G) u's in their place); 448 P u; u's parts behind the
+// state's, or (of three) in their place.
 // Every wait is bounded as in the rest of the library.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -272,7 +273,8 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                // of two parts: Q's rows behind the chain's next product; of three: with K's
+                // of two parts: Q's rows behind the chain's next product, so that the last output may be read late (380 -> 365
+                // us); of three, whose other operands take the state's columns: with K's
                 const bool both = want && NP == 3;
                 auto out_read = [&]() {
                     ok = i == 0 || mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
