@@ -5,7 +5,7 @@
 // Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
 // the output Q S0 and P u) follow one another, and the next chunk needs their
 // result; a batch's longest sequence is a chain of hundreds of them (24 sequences
-// of 32768 tokens, 16 heads, the longest 7422: 365 us, 6300 cycles a chunk, of
+// of 32768 tokens, 16 heads, the longest 7422: 350 us, 5800 cycles a chunk, of
 // which the products take 1900 and what they wait for the rest).  So a CTA
 // has one head of one sequence, with the whole state, and everything is held
 // the other way round (a column of v to a TMEM lane): the state is the A operand
@@ -63,7 +63,6 @@ constexpr int kColU = NP == 2 ? kColS + 64 * NP : kColS + 32 * NP;
 struct ScanParams {
     CUtensorMap tmQ, tmK, tmV, tmO;  // tmO: dout
     DeltaArgs a;
-    int keep;
     unsigned long long budget_ns;
 };
 
@@ -157,7 +156,9 @@ __device__ __forceinline__ void mma_rows_in(uint32_t d, uint32_t x, uint64_t b, 
         }
 }
 
-template <int NP>
+// With the output (a forward), or keeping what the gradients need of each chunk (decided here, not in the loop: 365 -> 352
+// us; what is kept is stored behind the arrivals that the chain waits for).
+template <int NP, bool KEEP>
 __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) {
     using Sh = Shape<NP>;
     extern __shared__ uint8_t smem_raw[];
@@ -213,7 +214,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
     __syncthreads();
     tc_fence_after();
     wait_ahead();
-    const bool want = a.out != nullptr, keep = p.keep != 0;
+    constexpr bool keep = KEEP, want = !KEEP;
     const bool bad = a.hdr->bad != 0;  // (boundaries without a plan: nothing is written)
     const int seq = bad ? 0 : a.order[block / a.Hv], h = block % a.Hv, hk = h / (a.Hv / a.Hk);
     const int c0 = bad ? 0 : a.first[seq], n_chunks = bad ? 0 : a.first[seq + 1] - c0;
@@ -438,21 +439,18 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             ok = mbar_wait_warp(x_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
-            float2 v[16];
+            float2 v[16], r[16];
             {
                 uint32_t x[32];
                 tmem_ld32(at + kColX + 32 * half, x);
-                float *p = a.r + (cell * C + 32 * half) * kD + m;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float4 e = four(g.eG, j), b = four(g.beta, j);
                     const float2 r0 = fma2(make_float2(-e.x, -e.y), f2(x[4 * j], x[4 * j + 1]), f2(d[2 * j] << 16, d[2 * j] & 0xffff0000u));
                     const float2 r1 = fma2(make_float2(-e.z, -e.w), f2(x[4 * j + 2], x[4 * j + 3]), f2(d[2 * j + 1] << 16, d[2 * j + 1] & 0xffff0000u));
                     if (keep) {
-                        p[4 * j * kD] = r0.x;
-                        p[(4 * j + 1) * kD] = r0.y;
-                        p[(4 * j + 2) * kD] = r1.x;
-                        p[(4 * j + 3) * kD] = r1.y;
+                        r[2 * j] = r0;
+                        r[2 * j + 1] = r1;
                     }
                     v[2 * j] = mul2(make_float2(b.x, b.y), r0);
                     v[2 * j + 1] = mul2(make_float2(b.z, b.w), r1);
@@ -462,6 +460,14 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             tmem_put_wait();
             tc_fence_before();
             mbar_arrive(r_ready);
+            if (keep) {
+                float *p = a.r + (cell * C + 32 * half) * kD + m;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    p[2 * j * kD] = r[j].x;
+                    p[(2 * j + 1) * kD] = r[j].y;
+                }
+            }
             if (NP == 2 && want && i > 0) output(i - 1, last, 1);
             ok = mbar_wait_warp(u_full, ph, wc);
             if (!ok) break;
@@ -483,6 +489,10 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     put_parts<NP>(at + kColX + 32 * half, 16, y);
                 else
                     put_parts<NP>(at + kColS + 16 * half, 32, y);
+                if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
+                tmem_put_wait();
+                tc_fence_before();
+                mbar_arrive(u_ready);
                 if (keep) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -490,11 +500,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                         p[(2 * j + 1) * kD] = v[j].y;
                     }
                 }
-                if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
-                tmem_put_wait();
             }
-            tc_fence_before();
-            mbar_arrive(u_ready);
             const float2 eC = make_float2(g.eC, g.eC);
             if (!want) {
                 __syncwarp();
@@ -559,7 +565,8 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     uint64_t *y_ready = bars + 8;   // do is in TMEM
     uint64_t *s_ready = bars + 9;   // dS's parts
     uint64_t *x_full = bars + 10;   // K dS and P^T do are there
-    uint64_t *r_ready = bars + 11;  // du's parts, and scale e^G do's
+    uint64_t *r_ready = bars + 11;  // du's parts
+    uint64_t *w_ready = bars + 18;  // scale e^G do's (apart from du's, which the chain waits for: 320 -> 307 us)
     uint64_t *u_full = bars + 12;   // dR is there
     uint64_t *z_ready = bars + 13;  // -beta e^G dR's parts
     uint64_t *d_full = bars + 14;   // the growth of dS is there
@@ -580,6 +587,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
         mbar_init(s_ready, 256);
         mbar_init(x_full, 1);
         mbar_init(r_ready, 256);
+        mbar_init(w_ready, 256);
         mbar_init(u_full, 1);
         mbar_init(z_ready, 256);
         mbar_init(d_full, 1);
@@ -670,6 +678,9 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                 tc_fence_after();
                 mma_square<NP>(tmem + kColX, tmem + kColZ, dT, 2048, id64n);
                 tc_commit_w(u_full);
+                ok = mbar_wait_warp(w_ready, ph, wc);
+                if (!ok) break;
+                tc_fence_after();
                 mma_rows<NP>(tmem + kColD, tmem + kColW, dQn, id128n, false);
                 ok = mbar_wait_warp(z_ready, ph, wc);
                 if (!ok) break;
@@ -764,6 +775,9 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                     v[2 * j + 1] = fma2(make_float2(e.z, e.w), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
                 }
                 put_parts<NP>(at + kColZ + 16 * half, 32, v);
+                tmem_put_wait();
+                tc_fence_before();
+                mbar_arrive(r_ready);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float4 e = four(g.eG, j);
@@ -774,7 +788,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
             }
             tmem_put_wait();
             tc_fence_before();
-            mbar_arrive(r_ready);
+            mbar_arrive(w_ready);
             ok = mbar_wait_warp(u_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
@@ -844,10 +858,10 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
 
 template <int NP>
 __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
-    scan_body<NP>(p, blockIdx.x);
+    scan_body<NP, false>(p, blockIdx.x);
 }
 // The backward's two walks need nothing of each other, and each is bound by its longest chain, which leaves SMs idle: one
-// launch of both (8192 tokens of 16 heads in 7 documents: 305 and 324 us one behind the other, 320 so).  Blocks of one
+// launch of both (8192 tokens of 16 heads in 7 documents: 305 and 324 us one behind the other, 311 so).  Blocks of one
 // walk come 16 in a row, the longest first: neighbouring SMs share an instruction cache that does not hold both walks
 // (blocks in turn: 502 us).
 constexpr int kTurn = 16;
@@ -855,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_walks_kernel(const __gri
     const int turn = blockIdx.x / kTurn, i = turn / 2 * kTurn + blockIdx.x % kTurn;
     if (i >= p.a.N * p.a.Hv) return;
     if (turn & 1)
-        scan_body<3>(p, i);
+        scan_body<3, true>(p, i);
     else
         back_body<3>(p, i);
 }
@@ -929,7 +943,6 @@ cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st) {
         !delta_rows_map(&p.tmV, a.v, a.T, a.Hv, a.v_stride, false) || !delta_rows_map(&p.tmO, a.dout, a.T, a.Hv, a.dout_stride, false))
         return cudaErrorInvalidValue;
     p.a = a;
-    p.keep = 1;
     p.budget_ns = wait_budget_ns();
     return walk<3, delta_tc_walks_kernel>(p, (a.N * a.Hv + kTurn - 1) / kTurn * 2 * kTurn, st);
 }
