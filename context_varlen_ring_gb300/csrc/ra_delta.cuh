@@ -270,6 +270,13 @@ __device__ __forceinline__ void gates_put(Gates &s, const float (&g)[2], const f
     if (lane == 0) s.eC = gate_exp(last, none);
 }
 
+// The thread of a converged warp that issues products; the same one commits them (tc_commit_w).
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(e));
+    return e != 0;
+}
+
 // 16 columns at each of two places, one wait; 32.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t a0, uint32_t a1, uint32_t (&x)[16], uint32_t (&y)[16]) {
     asm volatile(

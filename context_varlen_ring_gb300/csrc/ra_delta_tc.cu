@@ -103,57 +103,70 @@ __device__ __forceinline__ float2 f2(uint32_t x, uint32_t y) { return make_float
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 
 // The products, issued by unrolled code (rolled, an issue takes longer than a product of 64 columns: 32768 tokens 390
-// -> 527 us; rolled over the parts alone, the backward's walks 330 -> 346).
+// -> 527 us; rolled over the parts alone, the backward's walks 330 -> 346), all of one by one thread (chosen anew for
+// each instruction, 350 us; so 304).
 // D [v, token] = A's NP parts [v, dk] (64 columns a part) by 64 rows of K or Q (descriptor b).
 template <int NP>
 __device__ __forceinline__ void mma_state(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
-    bool more = false;
+    if (elected()) {
+        bool more = false;
 #pragma unroll
-    for (int q = NP - 1; q >= 0; --q)
+        for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            tc_mma_ts_w(d, x + 64 * q + 8 * ks, b + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), idesc, more);
-            more = true;
-        }
+            for (int ks = 0; ks < 8; ++ks) {
+                tc_mma_ts(d, x + 64 * q + 8 * ks, b + (((uint32_t)(ks >> 2) * kHalf + (uint32_t)(ks & 3) * 32u) >> 4), idesc, more);
+                more = true;
+            }
+    }
+    __syncwarp();
 }
 // D [v, token] = A's NP parts [v, token] (32 columns a part) by T's or P's parts, `step` bytes apart from 16 tokens to
 // the next; products of parts i, j with i + j < NP, the small ones first.
 template <int NP>
 __device__ __forceinline__ void mma_square(uint32_t d, uint32_t x, uint64_t b, uint32_t step, uint32_t idesc) {
-    bool more = false;
+    if (elected()) {
+        bool more = false;
 #pragma unroll
-    for (int o = NP - 1; o >= 0; --o)
+        for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-        for (int q = 0; q <= o; ++q)
+            for (int q = 0; q <= o; ++q)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                tc_mma_ts_w(d, x + 32 * q + 8 * ks, b + (((uint32_t)(o - q) * kSquare + (uint32_t)ks * step) >> 4), idesc, more);
-                more = true;
-            }
+                for (int ks = 0; ks < 4; ++ks) {
+                    tc_mma_ts(d, x + 32 * q + 8 * ks, b + (((uint32_t)(o - q) * kSquare + (uint32_t)ks * step) >> 4), idesc, more);
+                    more = true;
+                }
+    }
+    __syncwarp();
 }
 // D [v, dk] (+)= A's NP parts [v, token] by 64 rows of K or Q, their dk as columns.
 template <int NP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc, bool more) {
+    if (elected()) {
 #pragma unroll
-    for (int q = NP - 1; q >= 0; --q)
+        for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            tc_mma_ts_w(d, x + 32 * q + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), idesc, more);
-            more = true;
-        }
+            for (int ks = 0; ks < 4; ++ks) {
+                tc_mma_ts(d, x + 32 * q + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), idesc, more);
+                more = true;
+            }
+    }
+    __syncwarp();
 }
 
 // The same with the two parts of 32 tokens side by side.
 template <int NP>
 __device__ __forceinline__ void mma_rows_in(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
-    bool more = false;
+    if (elected()) {
+        bool more = false;
 #pragma unroll
-    for (int q = NP - 1; q >= 0; --q)
+        for (int q = NP - 1; q >= 0; --q)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            tc_mma_ts_w(d, x + 32 * (ks >> 1) + 16 * q + 8 * (ks & 1), b + ((uint32_t)ks * 2048u >> 4), idesc, more);
-            more = true;
-        }
+            for (int ks = 0; ks < 4; ++ks) {
+                tc_mma_ts(d, x + 32 * (ks >> 1) + 16 * q + 8 * (ks & 1), b + ((uint32_t)ks * 2048u >> 4), idesc, more);
+                more = true;
+            }
+    }
+    __syncwarp();
 }
 
 // With the output (a forward), or keeping what the gradients need of each chunk (decided here, not in the loop: 365 -> 352
@@ -663,11 +676,14 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                 ok = mbar_wait_warp(y_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 4 * NP; ++x) {  // do by P's rows, the small parts first
-                    const uint32_t q = NP - 1 - x / 4, ks = x % 4;
-                    tc_mma_ts_w(tmem + kColY, tmem + kColDO + 8 * ks, dP + ((q * kSquare + ks * 2048u) >> 4), id64n, x > 0);
+                if (elected()) {
+#pragma unroll
+                    for (int x = 0; x < 4 * NP; ++x) {  // do by P's rows, the small parts first
+                        const uint32_t q = NP - 1 - x / 4, ks = x % 4;
+                        tc_mma_ts(tmem + kColY, tmem + kColDO + 8 * ks, dP + ((q * kSquare + ks * 2048u) >> 4), id64n, x > 0);
+                    }
                 }
+                __syncwarp();
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();

@@ -227,24 +227,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
                 // A's part i by B's part j, 64 columns of v: four products
                 auto four = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t id, bool first) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) tc_mma_ss_w(tmem + d, x + 2 * ks, y + 2 * ks, id, !(first && ks == 0));
+                    for (int ks = 0; ks < 4; ++ks) tc_mma_ss(tmem + d, x + 2 * ks, y + 2 * ks, id, !(first && ks == 0));
                 };
                 auto S = [&](uint64_t x, int i) { return x + (uint32_t)i * (kHalf >> 4); };
                 auto U = [&](int j) { return dU + (uint32_t)j * (kQuarter >> 4); };
                 auto R = [&](int i) { return i ? S(dR, i - 1) : dRD; };  // (dR's part i; with do's rows behind the first)
-                four(kColB, S(dS, 2), dRD, id128, v == 0);
-                four(kColB, S(dS, 1), dRD, id128, false);
-                four(kColB, S(dS, 1), R(1), id64, false);
-                four(kColB, S(dS, 0), R(2), id64, false);
-                four(kColB, S(dS, 0), R(1), id64, false);
-                four(kColB, S(dS, 0), dRD, id128, false);
+                if (elected()) {  // (one thread for all of them: an issue takes less than a product)
+                    four(kColB, S(dS, 2), dRD, id128, v == 0);
+                    four(kColB, S(dS, 1), dRD, id128, false);
+                    four(kColB, S(dS, 1), R(1), id64, false);
+                    four(kColB, S(dS, 0), R(2), id64, false);
+                    four(kColB, S(dS, 0), R(1), id64, false);
+                    four(kColB, S(dS, 0), dRD, id128, false);
 #pragma unroll
-                for (int o = 2; o >= 0; --o)
+                    for (int o = 2; o >= 0; --o)
 #pragma unroll
-                    for (int i = 0; i <= o; ++i) {
-                        four(kColF, S(dD, i), U(o - i), id64, v == 0 && o == 2 && i == 0);
-                        four(kColP, R(i), U(o - i), id64, v == 0 && o == 2 && i == 0);
-                    }
+                        for (int i = 0; i <= o; ++i) {
+                            four(kColF, S(dD, i), U(o - i), id64, v == 0 && o == 2 && i == 0);
+                            four(kColP, R(i), U(o - i), id64, v == 0 && o == 2 && i == 0);
+                        }
+                }
+                __syncwarp();
                 tc_commit_w(done);
             }
         }
@@ -293,13 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
                 for (int q = kNP - 1; q >= 0; --q)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        tc_mma_ss_w(tmem + d, x + ((uint32_t)ks * 2048u >> 4), s + (((uint32_t)q * kQuarter + (uint32_t)ks * step) >> 4), id,
+                        tc_mma_ss(tmem + d, x + ((uint32_t)ks * 2048u >> 4), s + (((uint32_t)q * kQuarter + (uint32_t)ks * step) >> 4), id,
                                     !(first && q == kNP - 1 && ks == 0));
             };
-            by(kColQ2, K, 0, 16, 32, id64a, true);
-            by(kColA2, Q, 0, kHalf, 2048, id64ab, true);
-            by(kColA2, K, 2, kHalf, 2048, id64ab, false);
-            by(kColB2, K, 1, 16, 32, id64a, true);
+            if (elected()) {
+                by(kColQ2, K, 0, 16, 32, id64a, true);
+                by(kColA2, Q, 0, kHalf, 2048, id64ab, true);
+                by(kColA2, K, 2, kHalf, 2048, id64ab, false);
+                by(kColB2, K, 1, 16, 32, id64a, true);
+            }
+            __syncwarp();
             tc_commit_w(done);
         }
         // beside them: the next cell's way to L2, a line of 128 bytes a thread and turn; and sums of what was loaded
