@@ -5,7 +5,7 @@
 // Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
 // the output Q S0 and P u) follow one another, and the next chunk needs their
 // result; a batch's longest sequence is a chain of hundreds of them (24 sequences
-// of 32768 tokens, 16 heads, the longest 7422: 303 us, 5000 cycles a chunk, of
+// of 32768 tokens, 16 heads, the longest 7422: 350 us, 5800 cycles a chunk, of
 // which the products take 1900 and what they wait for the rest).  So a CTA
 // has one head of one sequence, with the whole state, and everything is held
 // the other way round (a column of v to a TMEM lane): the state is the A operand
@@ -188,7 +188,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
     uint64_t *x_full = bars + 9;    // K S0 is there
     uint64_t *r_ready = bars + 10;  // R's parts
     uint64_t *u_full = bars + 11;   // u is there
-    uint64_t *z_ready = bars + 19;  // e^(G_63 - G) u's parts (apart from u's, for the output: walks 311 -> 303 us)
     uint64_t *u_ready = bars + 12;  // u's parts
     uint64_t *d_full = bars + 13;   // the state's growth is there
     uint64_t *o_full = bars + 14;   // the output is there
@@ -210,7 +209,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
         mbar_init(x_full, 1);
         mbar_init(r_ready, 256);
         mbar_init(u_full, 1);
-        mbar_init(z_ready, 256);
         mbar_init(u_ready, 256);
         mbar_init(d_full, 1);
         mbar_init(o_full, 1);
@@ -309,7 +307,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     if (!out_read()) break;
                     mma_state<NP>(tmem + kColQ, tmem + kColS, dK + (kHalf / 2 >> 4), id64);
                 }
-                ok = mbar_wait_warp(z_ready, ph, wc);
+                ok = mbar_wait_warp(u_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
                 if (NP == 2)
@@ -318,9 +316,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     mma_rows<NP>(tmem + kColD, tmem + kColS, dKn, id128, false);
                 tc_commit_w(d_full);
                 if (want) {
-                    ok = mbar_wait_warp(u_ready, ph, wc);
-                    if (!ok) break;
-                    tc_fence_after();
                     mma_square<NP>(tmem + kColP, tmem + kColU<NP>, dP, 32, id64);
                     tc_commit_w(o_full);
                 }
@@ -507,15 +502,10 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     put_parts<NP>(at + kColX + 32 * half, 16, y);
                 else
                     put_parts<NP>(at + kColS + 16 * half, 32, y);
+                if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
                 tmem_put_wait();
                 tc_fence_before();
-                mbar_arrive(z_ready);
-                if (want) {
-                    put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
-                    tmem_put_wait();
-                    tc_fence_before();
-                    mbar_arrive(u_ready);
-                }
+                mbar_arrive(u_ready);
                 if (keep) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -887,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
     scan_body<NP, false>(p, blockIdx.x);
 }
 // The backward's two walks need nothing of each other, and each is bound by its longest chain, which leaves SMs idle: one
-// launch of both (8192 tokens of 16 heads in 7 documents: 254 and 285 us one behind the other, 303 so).  Blocks of one
+// launch of both (8192 tokens of 16 heads in 7 documents: 305 and 324 us one behind the other, 311 so).  Blocks of one
 // walk come 16 in a row, the longest first: neighbouring SMs share an instruction cache that does not hold both walks
 // (blocks in turn: 502 us).
 constexpr int kTurn = 16;
