@@ -5,7 +5,7 @@
 // Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
 // the output Q S0 and P u) follow one another, and the next chunk needs their
 // result; a batch's longest sequence is a chain of hundreds of them (24 sequences
-// of 32768 tokens, 16 heads, the longest 7422: 350 us, 5800 cycles a chunk, of
+// of 32768 tokens, 16 heads, the longest 7422: 304 us, 5000 cycles a chunk, of
 // which the products take 1900 and what they wait for the rest).  So a CTA
 // has one head of one sequence, with the whole state, and everything is held
 // the other way round (a column of v to a TMEM lane): the state is the A operand
@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid
     scan_body<NP, false>(p, blockIdx.x);
 }
 // The backward's two walks need nothing of each other, and each is bound by its longest chain, which leaves SMs idle: one
-// launch of both (8192 tokens of 16 heads in 7 documents: 305 and 324 us one behind the other, 311 so).  Blocks of one
+// launch of both (8192 tokens of 16 heads in 7 documents: 254 and 285 us one behind the other, 304 so).  Blocks of one
 // walk come 16 in a row, the longest first: neighbouring SMs share an instruction cache that does not hold both walks
 // (blocks in turn: 502 us).
 constexpr int kTurn = 16;

@@ -3,8 +3,8 @@
 // ra_delta_tc.cu left; the formulas are in ra_delta_bwd.cu.
 //
 // Bound: a chunk and head reads 270 KB (two states, u, r and dR in fp32; q, k and
-// do) and takes about 9000 cycles of products, parts and all, of 27,300 (8192
-// tokens, 16 heads: 212 us, 2.6 TB/s); eleven products
+// do) and takes about 9000 cycles of products, parts and all, of 27,000 (8192
+// tokens, 16 heads: 211 us, 2.6 TB/s); eleven products
 // share their operands, so those are made once, in shared memory:
 //  * for each half of v: S0, dS1 (rows of dk) and u, dR (rows of tokens) as three
 //    bf16 parts; then, with dk as rows of the result (a TMEM lane each),
