@@ -262,6 +262,21 @@ def test_few_and_many_heads(ra, hk, hv, dk, dv, dtype):
     assert ra.device_status() == 0
 
 
+@pytest.mark.parametrize("state", [False, True])
+def test_every_end_of_a_chunk(ra, state):
+    """Last chunks that end inside, at and behind each 16 tokens: nothing of the next sequence's rows is written."""
+    lens = [1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 79, 80, 81, 128, 129, 200]
+    q, k, v, g, beta, cu, cud = make(lens, 1, 2, 128, 128, "bf16", "usual", 12, tail=1)
+    s0 = states(len(lens), 2, 128, 128, 1) if state else None
+    want, last = ref(q, k, v, g, beta, cu, s0, 0.3)
+    out = torch.full(v.shape, 7.0, dtype=v.dtype, device="cuda")
+    got, s1 = ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0, final_state=state, scale=0.3, out=out)
+    R.delta_check(got[:cu[-1]], want, "out")
+    assert (got[cu[-1]:] == 7.0).all() and ra.device_status() == 0
+    if state:
+        R.delta_check(s1, last, "state")
+
+
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
 def test_many_sequences(ra, dk, dv):
     """More sequences than the plan lines up at a time, and than it sorts."""

@@ -246,6 +246,44 @@ def test_key_weights_of_many_sequences(ra):
     assert ra.device_status() == 6 and torch.equal(w2, before)
 
 
+@pytest.mark.parametrize("page", [16, 24])
+def test_key_weights_of_many_decoding_sequences(ra, page):
+    """One row each, more sequences than a CTA lines up at a time: pieces of the line begin and end anywhere."""
+    rng = np.random.default_rng(page)
+    B = 1100
+    lens = np.where(rng.random(B) < 0.3, 0, rng.integers(0, 200, B))
+    new = (rng.random(B) < 0.9).astype(int)
+    q, kc, w, table, ptable, cu = weights_case(rng, new, lens, (), (0,), page, 8, 2, 128, "bf16", False, True, 2)
+    _, lse = ra.paged_attn_fwd(q, kc, kc, dev(table), dev(cu), dev(lens))
+    lse[:, int(cu[-1]):] = 0.0
+    want, bound = R.key_weights(R.f64(q), R.f64(kc), table, cu, lens, R.f64(lse), R.f64(w), ptable, (), (0,), scale=128 ** -0.5)
+    before = w.clone()
+    ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, w, max_q_len=1)
+    SR.check(R.f64(w), want, bound)
+    ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, before, max_q_len=1)
+    assert torch.equal(before, w) and ra.device_status() == 0
+
+
+def test_key_weights_of_many_short_units(ra):
+    """Units of one tile of rows or two, of one tile of keys or two, a dozen to a CTA: every warpgroup meets units that
+    have nothing for it, one behind the other."""
+    rng = np.random.default_rng(8)
+    B = 300
+    new = rng.choice([16, 20, 32, 33, 40], B)
+    lens = np.maximum(new, rng.choice([40, 100, 128, 129, 256, 257, 400, 600], B))
+    q, kc, w, table, ptable, cu = weights_case(rng, new, lens, (), (0,), 16, 16, 4, 128, "bf16", False, True, 0)
+    _, lse = ra.paged_attn_fwd(q, kc, kc, dev(table), dev(cu), dev(lens))
+    want, bound = R.key_weights(R.f64(q), R.f64(kc), table, cu, lens, R.f64(lse), R.f64(w), ptable, (), (0,), scale=128 ** -0.5)
+    before = w.clone()
+    ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, w)
+    SR.check(R.f64(w), want, bound)
+    for _ in range(3):
+        again = before.clone()
+        ra.paged_attn_key_weights(q, kc, dev(table), dev(cu), dev(lens), lse, again)
+        assert torch.equal(again, w)
+    assert ra.device_status() == 0
+
+
 def test_key_weights_refusals(ra):
     rng = np.random.default_rng(7)
     q, kc, w, table, ptable, cu = weights_case(rng, [3, 2], [50, 40], (), (0,), 16, 2, 1, 64, "bf16", False, True, 0)
