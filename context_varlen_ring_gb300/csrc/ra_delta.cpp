@@ -96,7 +96,6 @@ DeltaArgs arguments(const ra_delta *d, uint8_t *ws, const Layout &L, int bwd) {
     a.slots = d->slots;
     a.n_slots = d->n_slots;
     a.max_chunks = (int)most_chunks(d->T, d->N);
-    a.parts = 3;
     a.hdr = reinterpret_cast<DeltaHdr *>(ws + L.hdr);
     a.chunk = reinterpret_cast<DeltaChunk *>(ws + L.chunk);
     a.first = reinterpret_cast<int *>(ws + L.first);
@@ -164,8 +163,6 @@ ra_status ra_delta_rule_fwd(const ra_delta *d, void *out, float *state_out, void
     DeltaArgs a = arguments(d, static_cast<uint8_t *>(workspace), L, 0);
     a.out = out;
     a.state_out = state_out;
-    // A bf16 output is rounded to 8 bits: 16 of what goes into it leave it as it is (the state, an fp32 result, wants 24).
-    a.parts = d->dtype == RA_BF16 && !state_out ? 2 : 3;
     if ((st = step("ra_delta_plan", s, [&] { return launch_delta_plan(a, s); }))) return st;
     if (a.max_chunks > 0 && (st = step("ra_delta_local", s, [&] { return launch_delta_local(a, s); }))) return st;
     return step("ra_delta_scan", s, [&] { return delta_tc_supported(a) ? launch_delta_tc_scan(a, s) : launch_delta_scan(a, 0, s); });

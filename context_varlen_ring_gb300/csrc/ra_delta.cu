@@ -103,16 +103,16 @@ __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArg
 }
 
 // ------------------------------------------------------------ T and P
-// Floor: what it writes, 16 KB a chunk and head for each part.  Bound: each chunk is a chain of small steps, an SM holds
-// four, and shared memory's port is busy for 64 % of the time (its K, Q, A, T and P, all read and written in pieces of 16
-// bytes).  So half of the warps make A and its inverse, the other half P (8576 chunks, two parts: 264 us with all of it in
-// four warps, 208 so), what is made takes the place of K and Q, P a part at a time (160), and the gates and the diagonal's
-// blocks are read 8 and 16 bytes at a time (160 -> 135).  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a
+// Floor: what it writes, 16 KB a chunk and head for each of the three parts.  Bound: each chunk is a chain of small steps,
+// an SM holds three, and shared memory's port is busy most of the time (its K, Q, A, T and P, all read and written in
+// pieces of 16 bytes): 8576 chunks 184 us, 3.5 TB/s.  So half of the warps make A and its inverse, the other half P (with
+// two parts 264 us with all of it in four warps, 208 so), what is made takes the place of K and Q, P a part at a time
+// (160), and the gates and the diagonal's blocks are read 8 and 16 bytes at a time (160 -> 135).  (I + A)^-1: the 16 x 16 blocks on the diagonal by substitution, a
 // lane a column; then blocks of 32 and of 64 from their halves, [T11, 0; -T22 A21 T11, T22], as products of parts.
 constexpr int kLocalThreads = 256;
 constexpr int kLdy = 40;
 
-template <typename E, int NP, int DK>
+template <typename E, int DK>
 struct LocalSmem {
     static constexpr int NPI = std::is_same<E, float>::value ? 3 : 1, LD = DK + 8;
     struct Rows {
@@ -132,10 +132,9 @@ struct LocalSmem {
     Gates g;
 };
 
-template <typename E, int NP, int DK>
+template <typename E, int DK>
 __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaArgs a) {
-    using Smem = LocalSmem<E, NP, DK>;
-    constexpr bool EX = NP == 3;
+    using Smem = LocalSmem<E, DK>;
     constexpr int NPI = Smem::NPI, LD = Smem::LD, PL = C * LD * 2, PT = C * kLdc * 2, PY = 32 * kLdy * 2;
     extern __shared__ __align__(128) uint8_t raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     const uint32_t kb = smem_u32(sm.in.k), row = row0 * LD * 2;
     float x[8][4];
     zero(x);
-    mm<8, NPI, NPI, 3, false, false, EX>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
+    mm<8, NPI, NPI, 3, false, false>(x, (own ? kb : smem_u32(sm.in.q)) + row, LD, PL, kb, LD, PL, 0, DK, w + 1);
     __syncthreads();  // (what is made of them takes the place of K and Q)
     float2 Gi[2];
     float f[2];
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     uint16_t *tp = a.tp + ((int64_t)c * a.Hv + h) * 2 * NP * C * C;
     if (!own) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {  // (a part at a time: four CTAs an SM)
+        for (int p = 0; p < NP; ++p) {  // (a part at a time: three CTAs an SM)
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -258,22 +257,22 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
     float y[2][4];
     if (w & 1) {  // rows 16 .. 31 by columns 0 .. 15, and 48 .. by 32 ..
         zero(y);
-        mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
+        mm<2, NP, NP, NP, false, true>(y, tile(Ab, row0, row0 - 16), kLdc, PT, tile(Tb, row0 - 16, row0 - 16), kLdc, PT, 0, 16);
         put(&sm.made.Y[0][(w >> 1) * 16][0], kLdy, 32 * kLdy, y, 1.f);
         __syncwarp();
         zero(y);
-        mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
+        mm<2, NP, NP, NP, false, true>(y, tile(Tb, row0, row0), kLdc, PT, Yb + (w >> 1) * 16 * kLdy * 2, kLdy, PY, 0, 16);
         put(&sm.made.T[0][row0][row0 - 16], kLdc, C * kLdc, y, -1.f);
     }
     sync();
     {  // rows 32 .. 63 by columns 0 .. 31: a block of 16 x 16 each warp
         const int r = (w >> 1) * 16, col = (w & 1) * 16;
         zero(y);
-        mm<2, NP, NP, NP, false, true, EX>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
+        mm<2, NP, NP, NP, false, true>(y, tile(Ab, 32 + r, 0), kLdc, PT, tile(Tb, 0, col), kLdc, PT, col, 32);
         put(&sm.made.Y[0][r][col], kLdy, 32 * kLdy, y, 1.f);
         sync();
         zero(y);
-        mm<2, NP, NP, NP, false, true, EX>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
+        mm<2, NP, NP, NP, false, true>(y, tile(Tb, 32 + r, 32), kLdc, PT, Yb + col * 2, kLdy, PY, 0, r + 16);
         put(&sm.made.T[0][32 + r][col], kLdc, C * kLdc, y, -1.f);
     }
     sync();
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(kLocalThreads) delta_local_kernel(const DeltaA
 // ------------------------------------------------------------ the walk
 constexpr int kScanThreads = 256;
 
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 struct ScanSmem {
     static constexpr bool F = std::is_same<E, float>::value;
     static constexpr int NPI = F ? 3 : 1, KB = F ? 1 : 2, LD = DK + 8, LV = DVS + 8;
@@ -293,10 +292,9 @@ struct ScanSmem {
     Gates g[2];
 };
 
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const DeltaArgs a, int keep) {
-    using Smem = ScanSmem<E, NP, DK, DVS>;
-    constexpr bool EX = NP == 3;
+    using Smem = ScanSmem<E, DK, DVS>;
     constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
     // Slices of 32 or 64 columns: every warp has 16 rows and half of the columns.  Of 16: warps 0 .. 3 have the chain (K S0, T R
     // and, with dk 64, the state), and warps 4 .. 7 the output.
@@ -409,11 +407,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         float x[NX][4], o[NX][4];
         zero(x);
         if (chain)
-            mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS,
+            mm<NX, NPI, NP, NP, false, true>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS,
                                                  0, DK);
         if (output) {
             zero(o);
-            mm<NX, NPI, NP, NP, false, true, EX>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+            mm<NX, NPI, NP, NP, false, true>(o, smem_u32(sm.q) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                              DK);
         }
 #pragma unroll
@@ -438,7 +436,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
         cp_commit();
         zero(x);
         if (chain)
-            mm<NX, NP, NP, NP, false, true, EX>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR,
+            mm<NX, NP, NP, NP, false, true>(x, smem_u32(sm.T) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.R) + xcol * 2, LV, PR,
                                                 0, xrow + 16);
 #pragma unroll
         for (int n = 0; n < NX && chain; ++n)
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
                 put2<NP>(&sm.R[0][i][j], C * LV, g.eL[i] * x[n][2 * hf], g.eL[i] * x[n][2 * hf + 1]);
             }
         if (output) {
-            mm<NX, NP, NP, NP, false, true, EX>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
+            mm<NX, NP, NP, NP, false, true>(o, smem_u32(sm.P) + xrow * kLdc * 2, kLdc, PT, smem_u32(sm.U) + xcol * 2, LV, PR,
                                             0, xrow + 16);
 #pragma unroll
             for (int n = 0; n < NX; ++n)
@@ -482,7 +480,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) delta_scan_kernel(const Delta
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
         if (state)
-            mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
+            mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.R) + scol * 2, LV, PR, 0, C);
     }
     cp_wait<0>();
     if (a.state_out && slot >= 0 && state) {
@@ -577,21 +575,21 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaSte
     }
 }
 
-template <typename E, int NP, int DK>
+template <typename E, int DK>
 cudaError_t local(const DeltaArgs &a, cudaStream_t st) {
     static LaunchFit fit;
-    auto kernel = delta_local_kernel<E, NP, DK>;
-    const size_t smem = sizeof(LocalSmem<E, NP, DK>);
+    auto kernel = delta_local_kernel<E, DK>;
+    const size_t smem = sizeof(LocalSmem<E, DK>);
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kLocalThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
     return launch_next(kernel, dim3(a.max_chunks, a.Hv), kLocalThreads, smem, st, a);
 }
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 cudaError_t scan(const DeltaArgs &a, int keep, cudaStream_t st) {
     static LaunchFit fit;
-    auto kernel = delta_scan_kernel<E, NP, DK, DVS>;
-    const size_t smem = sizeof(ScanSmem<E, NP, DK, DVS>);
-    static_assert(sizeof(ScanSmem<E, NP, DK, DVS>) <= 232448, "shared memory of one CTA");
+    auto kernel = delta_scan_kernel<E, DK, DVS>;
+    const size_t smem = sizeof(ScanSmem<E, DK, DVS>);
+    static_assert(sizeof(ScanSmem<E, DK, DVS>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kScanThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
     return launch_next(kernel, dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kScanThreads, smem, st, a, keep);
@@ -604,9 +602,8 @@ cudaError_t launch_delta_plan(const DeltaArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 cudaError_t launch_delta_local(const DeltaArgs &a, cudaStream_t st) {
-    if (a.dtype == RA_FP32) return a.dk == 64 ? local<float, 3, 64>(a, st) : local<float, 3, 128>(a, st);
-    if (a.parts == 2) return a.dk == 64 ? local<bf16, 2, 64>(a, st) : local<bf16, 2, 128>(a, st);
-    return a.dk == 64 ? local<bf16, 3, 64>(a, st) : local<bf16, 3, 128>(a, st);
+    if (a.dtype == RA_FP32) return a.dk == 64 ? local<float, 64>(a, st) : local<float, 128>(a, st);
+    return a.dk == 64 ? local<bf16, 64>(a, st) : local<bf16, 128>(a, st);
 }
 // Slices of the state's columns: a step of the chain is bound by its warp-level products (fp32, dk 64, 32 columns: 5700 of
 // 11,400 cycles), so they are as narrow as leaves every CTA an SM (fp32, 5 sequences of up to 292 tokens, 4 heads of 64:
@@ -616,16 +613,12 @@ cudaError_t launch_delta_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
     const int64_t heads = (int64_t)a.N * a.Hv;
     if (a.dtype == RA_FP32) {
         if (heads * (a.dv / 16) <= paged_sms())
-            return a.dk == 64 ? scan<float, 3, 64, 16>(a, keep, st) : scan<float, 3, 128, 16>(a, keep, st);
-        return a.dk == 64 ? scan<float, 3, 64, 32>(a, keep, st) : scan<float, 3, 128, 32>(a, keep, st);
+            return a.dk == 64 ? scan<float, 64, 16>(a, keep, st) : scan<float, 128, 16>(a, keep, st);
+        return a.dk == 64 ? scan<float, 64, 32>(a, keep, st) : scan<float, 128, 32>(a, keep, st);
     }
     const bool few = heads * (a.dv / 32) <= paged_sms();
-    if (a.parts == 2) {
-        if (few) return a.dk == 64 ? scan<bf16, 2, 64, 32>(a, keep, st) : scan<bf16, 2, 128, 32>(a, keep, st);
-        return a.dk == 64 ? scan<bf16, 2, 64, 64>(a, keep, st) : scan<bf16, 2, 128, 64>(a, keep, st);
-    }
-    if (few) return a.dk == 64 ? scan<bf16, 3, 64, 32>(a, keep, st) : scan<bf16, 3, 128, 32>(a, keep, st);
-    return a.dk == 64 ? scan<bf16, 3, 64, 64>(a, keep, st) : scan<bf16, 3, 128, 64>(a, keep, st);
+    if (few) return a.dk == 64 ? scan<bf16, 64, 32>(a, keep, st) : scan<bf16, 128, 32>(a, keep, st);
+    return a.dk == 64 ? scan<bf16, 64, 64>(a, keep, st) : scan<bf16, 128, 64>(a, keep, st);
 }
 cudaError_t launch_delta_step(const DeltaStepArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((int64_t)a.B * a.Hv * (a.dv / 32));

@@ -3,9 +3,12 @@
 //
 // Arithmetic.  The states, their gradients and the gates' gradients are fp32
 // results, so the products' operands have to carry more than bf16's 8 bits: an
-// operand that is not bf16 itself is held as the sum of 2 or 3 bf16 parts (16
-// or 24 bits), and a product adds the parts' products up to the order that the
-// parts have, in fp32.  q, k, v and dout of a bf16 call are one part, exactly.
+// operand that is not bf16 itself is held as the sum of three bf16 parts (24
+// bits), and a product adds the parts' products up to the third order, in fp32.
+// q, k, v and dout of a bf16 call are one part, exactly.  (A bf16 forward from
+// two parts, 16 bits, is faster but up to 5e-6 of the largest result off beside
+// its own rounding, and 1.4e-4 of the norm from the rounded exact result; of
+// three 5e-8 and 2.9e-5, as plain fp32 arithmetic is.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,7 +24,7 @@ namespace delta {
 
 using namespace dev;
 using bf16 = __nv_bfloat16;
-constexpr int C = kDeltaChunk;
+constexpr int C = kDeltaChunk, NP = kDeltaParts;
 constexpr int kLdc = C + 8;  // pitch of a [64][64] tile: rows of 9 x 16 bytes, so that eight rows meet eight bank groups
 
 __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool there) {
@@ -56,11 +59,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // 16), operands of PA and PB parts, products of parts i, j with i + j < NP.
 // a, b: shared addresses of A's and B's first element; lda, ldb: pitches in
 // elements; pa, pb: bytes between parts.  TA: A is stored [K][M]; BKN: B is
-// stored [K][N], else [N][K].  EX: every 16 of K are summed by themselves and
+// stored [K][N], else [N][K].  Every 16 of K are summed by themselves and
 // added to acc in fp32, because the tensor cores cut what they add to an
 // accumulator, always towards 0 (fp32 gradients off by 1.5e-6 of their norm
 // without, 1.6e-7 with).
-template <int NT, int PA, int PB, int NP, bool TA, bool BKN, bool EX = false>
+template <int NT, int PA, int PB, int NP, bool TA, bool BKN>
 __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int pa, uint32_t b, int ldb, int pb, int k0,
                                    int k1, int pairs = NT / 2) {
     const int l = threadIdx.x & 31, r = l & 7, s = (l >> 3) & 1, h = l >> 4;
@@ -79,7 +82,6 @@ __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int
 #pragma unroll
             for (int j = 0; j < PB; ++j) ldsm4<BKN>(b + j * pb + k * bs + n * bn, fb[j]);
             float own[2][4] = {};
-            float(&c0)[4] = EX ? own[0] : acc[2 * n], (&c1)[4] = EX ? own[1] : acc[2 * n + 1];
             // (the small products first)
 #pragma unroll
             for (int o = NP - 1; o >= 0; --o)
@@ -87,15 +89,13 @@ __device__ __forceinline__ void mm(float (&acc)[NT][4], uint32_t a, int lda, int
                 for (int i = 0; i < PA; ++i) {
                     const int j = o - i;
                     if (j < 0 || j >= PB) continue;
-                    mma(c0, fa[i], fb[j][0], fb[j][1]);
-                    mma(c1, fa[i], fb[j][2], fb[j][3]);
+                    mma(own[0], fa[i], fb[j][0], fb[j][1]);
+                    mma(own[1], fa[i], fb[j][2], fb[j][3]);
                 }
-            if (EX) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[2 * n][i] += own[0][i];
-                    acc[2 * n + 1][i] += own[1][i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                acc[2 * n][i] += own[0][i];
+                acc[2 * n + 1][i] += own[1][i];
             }
         }
     }

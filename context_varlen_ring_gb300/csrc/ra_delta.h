@@ -9,7 +9,7 @@
 namespace ra {
 
 constexpr int kDeltaChunk = 64;        // tokens a chunk
-constexpr int kDeltaParts = 3;         // bf16 parts that the workspace has room for
+constexpr int kDeltaParts = 3;         // bf16 parts of what is not bf16 itself
 
 // A chunk: its first token, its tokens (1 .. 64).
 struct DeltaChunk {
@@ -32,7 +32,6 @@ struct DeltaArgs {
     int64_t n_slots;
     void *out;                         // [T, Hv, dv]; NULL: not wanted
     int max_chunks;                    // no boundaries of T tokens in N sequences give more
-    int parts;                         // bf16 parts of what is not bf16 itself: 2 or 3
     // workspace
     DeltaHdr *hdr;
     DeltaChunk *chunk;                 // [max_chunks]

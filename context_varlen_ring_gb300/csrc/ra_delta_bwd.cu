@@ -33,7 +33,7 @@ using namespace delta;
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------ the walk from the end
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 struct BackSmem {
     static constexpr bool F = std::is_same<E, float>::value;
     static constexpr int NPI = F ? 3 : 1, KB = F ? 1 : 2, LD = DK + 8, LV = DVS + 8;
@@ -45,10 +45,9 @@ struct BackSmem {
     Gates g[2];
 };
 
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs a) {
-    using Smem = BackSmem<E, NP, DK, DVS>;
-    constexpr bool EX = NP == 3;
+    using Smem = BackSmem<E, DK, DVS>;
     constexpr int NPI = Smem::NPI, KB = Smem::KB, LD = Smem::LD, LV = Smem::LV;
     constexpr int MW = DK / 16, NS = DVS / 8 / (8 / MW), NX = DVS / 16;
     constexpr int PK = C * LD * 2, PT = C * kLdc * 2, PS = DK * LV * 2, PR = C * LV * 2;
@@ -143,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         if (KB == 2 && c > c0) load_k(c - 1, buf ^ 1);
         float x[NX][4];
         zero(x);
-        mm<NX, NPI, NP, NP, false, true, EX>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
+        mm<NX, NPI, NP, NP, false, true>(x, smem_u32(sm.k[buf]) + xrow * LD * 2, LD, PK, smem_u32(sm.S) + xcol * 2, LV, PS, 0,
                                          DK);
 #pragma unroll
         for (int n = 0; n < NX; ++n)
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
                 x[n][2 * hf] *= e;
                 x[n][2 * hf + 1] *= e;
             }
-        mm<NX, NP, NPI, NP, true, true, EX>(x, smem_u32(sm.P) + xrow * 2, kLdc, PT, smem_u32(sm.Y) + xcol * 2, LV, PR, xrow, C);
+        mm<NX, NP, NPI, NP, true, true>(x, smem_u32(sm.P) + xrow * 2, kLdc, PT, smem_u32(sm.Y) + xcol * 2, LV, PR, xrow, C);
 #pragma unroll
         for (int n = 0; n < NX; ++n)
 #pragma unroll
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         if (c > c0) load_tp(c - 1, 1);
         cp_commit();  // (with the next K)
         zero(x);
-        mm<NX, NP, NP, NP, true, true, EX>(x, smem_u32(sm.T) + xrow * 2, kLdc, PT, smem_u32(sm.X) + xcol * 2, LV, PR, xrow, C);
+        mm<NX, NP, NP, NP, true, true>(x, smem_u32(sm.T) + xrow * 2, kLdc, PT, smem_u32(sm.X) + xcol * 2, LV, PR, xrow, C);
         cp_wait<1>();  // Q (behind it the next K and P)
         __syncthreads();
         if (c > c0) load_tp(c - 1, 0);
@@ -186,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] *= g.eC;
-        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.q) + srow * 2, LD, PK, smem_u32(sm.X) + scol * 2, LV, PR, 0, C);
-        mm<NS, NPI, NP, NP, true, true, EX>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.Y) + scol * 2, LV, PR, 0, C);
+        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.q) + srow * 2, LD, PK, smem_u32(sm.X) + scol * 2, LV, PR, 0, C);
+        mm<NS, NPI, NP, NP, true, true>(S, smem_u32(sm.k[buf]) + srow * 2, LD, PK, smem_u32(sm.Y) + scol * 2, LV, PR, 0, C);
     }
     cp_wait<0>();
     if (a.dstate0) {
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_back_kernel(const DeltaArgs
 // ------------------------------------------------------------ the chunks' gradients
 constexpr int kVS = 32;  // columns of the states at a time
 
-template <typename E, int NP, int DK>
+template <typename E, int DK>
 struct GradSmem {
     static constexpr int NPI = std::is_same<E, float>::value ? 3 : 1, LD = DK + 8, LV = kVS + 8;
     bf16 k[NPI][C][LD], q[NPI][C][LD];
@@ -225,10 +224,9 @@ struct GradSmem {
 
 // R CTAs (a cluster) a cell, 64 / R rows each.  Of two, the second gives the first what its rows have of the first
 // one's columns (dP, M) and its sums for the gates; nothing goes the other way, as dP and M are triangular.
-template <typename E, int NP, int DK, int R>
+template <typename E, int DK, int R>
 __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArgs a) {
-    using Smem = GradSmem<E, NP, DK>;
-    constexpr bool EX = NP == 3;
+    using Smem = GradSmem<E, DK>;
     constexpr int NPI = Smem::NPI, LD = Smem::LD, LV = Smem::LV;
     constexpr int RT = C / R / 16, CG = 8 / RT;                 // 16 rows a warp, and a CGth of the columns:
     constexpr int NK = DK / 8 / CG, NC = C / 8 / CG;            // n-tiles along dk, along the chunk
@@ -300,11 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         __syncthreads();
         const uint32_t d = smem_u32(sm.v.d) + row0 * LV * 2, u = smem_u32(sm.v.u), dr = smem_u32(sm.v.dr) + row0 * LV * 2;
         const uint32_t s0 = smem_u32(sm.v.s0) + kcol * LV * 2, ds = smem_u32(sm.v.ds) + kcol * LV * 2;
-        mm<NK, NPI, NP, NP, false, false, EX>(dq, d, LV, PR, s0, LV, PS, 0, kVS);
-        mm<NK, NP, NP, NP, false, false, EX>(F, u + row0 * LV * 2, LV, PR, ds, LV, PS, 0, kVS);
-        mm<NK, NP, NP, NP, false, false, EX>(B, dr, LV, PR, s0, LV, PS, 0, kVS);
-        mm<NC, NPI, NP, NP, false, false, EX>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
-        mm<NC, NP, NP, NP, false, false, EX>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<NK, NPI, NP, NP, false, false>(dq, d, LV, PR, s0, LV, PS, 0, kVS);
+        mm<NK, NP, NP, NP, false, false>(F, u + row0 * LV * 2, LV, PR, ds, LV, PS, 0, kVS);
+        mm<NK, NP, NP, NP, false, false>(B, dr, LV, PR, s0, LV, PS, 0, kVS);
+        mm<NC, NPI, NP, NP, false, false>(dP, d, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
+        mm<NC, NP, NP, NP, false, false>(dA, dr, LV, PR, u + ccol * LV * 2, LV, PR, 0, kVS);
     }
     // sums of rows over the four threads that hold them
     rr += __shfl_xor_sync(0xffffffffu, rr, 1);
@@ -316,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         float kk[NC][4], qk[NC][4];
         zero(kk);
         zero(qk);
-        mm<NC, NPI, NPI, 3, false, false, EX>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
-        mm<NC, NPI, NPI, 3, false, false, EX>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        mm<NC, NPI, NPI, 3, false, false>(kk, kb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
+        mm<NC, NPI, NPI, 3, false, false>(qk, qb + row0 * LD * 2, LD, PK, kb + ccol * LD * 2, LD, PK, 0, DK);
         sync();  // (the slices' products: dP and M take their place)
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
@@ -430,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grads_kernel(const DeltaArg
         if (2 * lane + 1 < ch.n) a.dg[at + a.Hv] = x[1] + after + end;
     }
     const uint32_t Pb = smem_u32(sm.c.dP), Mb = smem_u32(sm.c.M);
-    mm<NK, NP, NPI, NP, false, true, EX>(dq, Pb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
-    mm<NK, NP, NPI, NP, true, true, EX>(F, Pb + row0 * 2, kLdc, PT, qb + kcol * 2, LD, PK, row0, C);
-    mm<NK, NP, NPI, NP, false, true, EX>(F, Mb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
-    mm<NK, NP, NPI, NP, true, true, EX>(F, Mb + row0 * 2, kLdc, PT, kb + kcol * 2, LD, PK, row0, C);
+    mm<NK, NP, NPI, NP, false, true>(dq, Pb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
+    mm<NK, NP, NPI, NP, true, true>(F, Pb + row0 * 2, kLdc, PT, qb + kcol * 2, LD, PK, row0, C);
+    mm<NK, NP, NPI, NP, false, true>(F, Mb + row0 * kLdc * 2, kLdc, PT, kb + kcol * 2, LD, PK, 0, row0 + 16);
+    mm<NK, NP, NPI, NP, true, true>(F, Mb + row0 * 2, kLdc, PT, kb + kcol * 2, LD, PK, row0, C);
 #pragma unroll
     for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -474,45 +472,45 @@ __global__ void __launch_bounds__(kThreads) delta_sum_kernel(const DeltaArgs a) 
     }
 }
 
-template <typename E, int NP, int DK, int DVS>
+template <typename E, int DK, int DVS>
 cudaError_t back(const DeltaArgs &a, cudaStream_t st) {
     static LaunchFit fit;
-    auto kernel = delta_back_kernel<E, NP, DK, DVS>;
-    const size_t smem = sizeof(BackSmem<E, NP, DK, DVS>);
-    static_assert(sizeof(BackSmem<E, NP, DK, DVS>) <= 232448, "shared memory of one CTA");
+    auto kernel = delta_back_kernel<E, DK, DVS>;
+    const size_t smem = sizeof(BackSmem<E, DK, DVS>);
+    static_assert(sizeof(BackSmem<E, DK, DVS>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
     return launch_next(kernel, dim3((unsigned)(a.N * a.Hv * (a.dv / DVS))), kThreads, smem, st, a);
 }
-template <typename E, int NP, int DK, int R>
+template <typename E, int DK, int R>
 cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
     static LaunchFit fit;
-    auto kernel = delta_grads_kernel<E, NP, DK, R>;
-    const size_t smem = sizeof(GradSmem<E, NP, DK>);
-    static_assert(sizeof(GradSmem<E, NP, DK>) <= 232448, "shared memory of one CTA");
+    auto kernel = delta_grads_kernel<E, DK, R>;
+    const size_t smem = sizeof(GradSmem<E, DK>);
+    static_assert(sizeof(GradSmem<E, DK>) <= 232448, "shared memory of one CTA");
     const cudaError_t e = fit.prepare(reinterpret_cast<const void *>(kernel), kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
     return launch_next<R>(kernel, dim3(a.max_chunks * R, a.Hv), kThreads, smem, st, a);
 }
 // Two CTAs a cell while every CTA has an SM: a cell's time is its warp-level products' (fp32, 5 chunks of 2 heads of 64 by
 // 128: 31.2 -> 26.5 us).
-template <typename E, int NP, int DK>
+template <typename E, int DK>
 cudaError_t grads(const DeltaArgs &a, cudaStream_t st) {
-    return (int64_t)a.max_chunks * a.Hv * 2 <= paged_sms() ? grads<E, NP, DK, 2>(a, st) : grads<E, NP, DK, 1>(a, st);
+    return (int64_t)a.max_chunks * a.Hv * 2 <= paged_sms() ? grads<E, DK, 2>(a, st) : grads<E, DK, 1>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_back(const DeltaArgs &a, cudaStream_t st) {
-    if (a.dtype == RA_FP32) return a.dk == 64 ? back<float, 3, 64, 32>(a, st) : back<float, 3, 128, 32>(a, st);
+    if (a.dtype == RA_FP32) return a.dk == 64 ? back<float, 64, 32>(a, st) : back<float, 128, 32>(a, st);
     // (slices as narrow as leaves every CTA an SM: 12 sequences of up to 39 tokens, 2 heads of 64, both walks 41.9 -> 38.0 us)
     if ((int64_t)a.N * a.Hv * (a.dv / 32) <= paged_sms())
-        return a.dk == 64 ? back<bf16, 3, 64, 32>(a, st) : back<bf16, 3, 128, 32>(a, st);
-    return a.dk == 64 ? back<bf16, 3, 64, 64>(a, st) : back<bf16, 3, 128, 64>(a, st);
+        return a.dk == 64 ? back<bf16, 64, 32>(a, st) : back<bf16, 128, 32>(a, st);
+    return a.dk == 64 ? back<bf16, 64, 64>(a, st) : back<bf16, 128, 64>(a, st);
 }
 cudaError_t launch_delta_grads(const DeltaArgs &a, cudaStream_t st) {
-    if (a.dtype == RA_FP32) return a.dk == 64 ? grads<float, 3, 64>(a, st) : grads<float, 3, 128>(a, st);
-    return a.dk == 64 ? grads<bf16, 3, 64>(a, st) : grads<bf16, 3, 128>(a, st);
+    if (a.dtype == RA_FP32) return a.dk == 64 ? grads<float, 64>(a, st) : grads<float, 128>(a, st);
+    return a.dk == 64 ? grads<bf16, 64>(a, st) : grads<bf16, 128>(a, st);
 }
 cudaError_t launch_delta_sum(const DeltaArgs &a, cudaStream_t st) {
     const int64_t n = 2 * a.T * a.Hk * (a.dk / 4);

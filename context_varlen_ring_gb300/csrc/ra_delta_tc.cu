@@ -5,8 +5,8 @@
 // Bound: the chain of a sequence.  A chunk's products (K S0, T R, K^T u, and for
 // the output Q S0 and P u) follow one another, and the next chunk needs their
 // result; a batch's longest sequence is a chain of hundreds of them (24 sequences
-// of 32768 tokens, 16 heads, the longest 7422: 304 us, 5000 cycles a chunk, of
-// which the products take 1900 and what they wait for the rest).  So a CTA
+// of 32768 tokens, 16 heads, the longest 7422: 547 us, 9000 cycles a chunk, of
+// which the products take a third and what they wait for the rest).  So a CTA
 // has one head of one sequence, with the whole state, and everything is held
 // the other way round (a column of v to a TMEM lane): the state is the A operand
 // of the first product straight from TMEM, its tokens' values the A operand of
@@ -16,12 +16,12 @@
 //    warpgroups, a thread a lane and half of the columns each, hold the state
 //    in registers (fp32), make bf16 parts of what the next product reads and
 //    put them into TMEM.
-//  * the output's products (with two parts) run behind those that the chain
-//    needs, and are read, half at a time, while the next chunk's products run.
+//  * the output's last product runs behind those that the chain needs; its
+//    operand lies in the state's columns, so the output is read ahead of the
+//    next chunk's state.
 // TMEM columns: 0 the state's growth (and, ahead of it, R's parts); 128 K S0,
-// then u, with two parts then e^(G_63 - G) u's; 192 Q S0; 256 the state's parts
-// (with three, e^(G_63 - G) u's in their place); 448 P u; u's parts behind the
-// state's, or (of three) in their place.
+// then u; 192 Q S0; 256 the state's parts, then those of e^(G_63 - G) u and of u;
+// 448 P u.
 // Every wait is bounded as in the rest of the library.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -49,16 +49,11 @@ constexpr uint32_t kHalf = 16384;         // 64 rows of K, 64 of Q, 128 bytes ea
 constexpr uint32_t kSquare = 8192;        // a part of T or P
 constexpr uint32_t kValues = C * kD * 2;  // [64][128] of v
 
-template <int NP>
-struct Shape {
-    static constexpr uint32_t oTP = 2 * kHalf, oV = oTP + 2 * NP * kSquare, stage = oV + kValues;
-    static constexpr uint32_t oBar = kStages * stage, smem = oBar + 256 + 1024;
-};
+constexpr uint32_t kOffTP = 2 * kHalf, kOffV = kOffTP + 2 * NP * kSquare, kStage = kOffV + kValues;
+constexpr uint32_t kOffBar = kStages * kStage, kSmem = kOffBar + 256 + 1024;
 constexpr int kColD = 0, kColX = 128, kColQ = 192, kColS = 256, kColP = 448;
-// u's parts: with two there is room for them; with three they follow e^(G_63 - G) u's over the state's, which are
-// written again only when the output's products are done.
-template <int NP>
-constexpr int kColU = NP == 2 ? kColS + 64 * NP : kColS + 32 * NP;
+// u's parts, behind e^(G_63 - G) u's over the state's, which are written again only when the output's products are done.
+constexpr int kColU = kColS + 32 * NP;
 
 struct ScanParams {
     CUtensorMap tmQ, tmK, tmV, tmO;  // tmO: dout
@@ -85,7 +80,6 @@ __device__ __forceinline__ void part(float2 (&x)[N], uint32_t (&h)[N]) {
     }
 }
 // 32 values as NP parts of 16 columns, `apart` columns from each other (to be waited for).
-template <int NP>
 __device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float2 (&x)[16]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -102,11 +96,10 @@ __device__ __forceinline__ void put_parts(uint32_t tmem, int apart, float2 (&x)[
 __device__ __forceinline__ float2 f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 
-// The products, issued by unrolled code (rolled, an issue takes longer than a product of 64 columns: 32768 tokens 390
-// -> 527 us; rolled over the parts alone, the backward's walks 330 -> 346), all of one by one thread (chosen anew for
-// each instruction, 350 us; so 304).
+// The products, issued by unrolled code (rolled, an issue takes longer than a product of 64 columns: 32768 tokens of two
+// parts 390 -> 527 us; rolled over the parts alone, the backward's walks 330 -> 346), all of one by one thread (chosen
+// anew for each instruction, with two parts 350 us; so 304).
 // D [v, token] = A's NP parts [v, dk] (64 columns a part) by 64 rows of K or Q (descriptor b).
-template <int NP>
 __device__ __forceinline__ void mma_state(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
     if (elected()) {
         bool more = false;
@@ -122,7 +115,6 @@ __device__ __forceinline__ void mma_state(uint32_t d, uint32_t x, uint64_t b, ui
 }
 // D [v, token] = A's NP parts [v, token] (32 columns a part) by T's or P's parts, `step` bytes apart from 16 tokens to
 // the next; products of parts i, j with i + j < NP, the small ones first.
-template <int NP>
 __device__ __forceinline__ void mma_square(uint32_t d, uint32_t x, uint64_t b, uint32_t step, uint32_t idesc) {
     if (elected()) {
         bool more = false;
@@ -139,7 +131,6 @@ __device__ __forceinline__ void mma_square(uint32_t d, uint32_t x, uint64_t b, u
     __syncwarp();
 }
 // D [v, dk] (+)= A's NP parts [v, token] by 64 rows of K or Q, their dk as columns.
-template <int NP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc, bool more) {
     if (elected()) {
 #pragma unroll
@@ -153,33 +144,16 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint64_t b, uin
     __syncwarp();
 }
 
-// The same with the two parts of 32 tokens side by side.
-template <int NP>
-__device__ __forceinline__ void mma_rows_in(uint32_t d, uint32_t x, uint64_t b, uint32_t idesc) {
-    if (elected()) {
-        bool more = false;
-#pragma unroll
-        for (int q = NP - 1; q >= 0; --q)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                tc_mma_ts(d, x + 32 * (ks >> 1) + 16 * q + 8 * (ks & 1), b + ((uint32_t)ks * 2048u >> 4), idesc, more);
-                more = true;
-            }
-    }
-    __syncwarp();
-}
-
-// With the output (a forward), or keeping what the gradients need of each chunk (decided here, not in the loop: 365 -> 352
-// us; what is kept is stored behind the arrivals that the chain waits for).
-template <int NP, bool KEEP>
+// With the output (a forward), or keeping what the gradients need of each chunk (decided here, not in the loop: with two
+// parts 365 -> 352 us; what is kept is stored behind the arrivals that the chain waits for).
+template <bool KEEP>
 __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) {
-    using Sh = Shape<NP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Gates gates[2];
     const DeltaArgs &a = p.a;
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - raw_s);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
     uint64_t *full = bars + 0;      // [2] a chunk's rows landed
     uint64_t *empty = bars + 2;     // [2] its products are done, its values read
     uint64_t *g_full = bars + 4;    // [2] its gates
@@ -245,14 +219,14 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     const int s = i & 1;
                     const int64_t c = c0 + i;
                     const int tok = a.chunk[c].tok0;
-                    uint8_t *st = base + s * Sh::stage;
+                    uint8_t *st = base + s * kStage;
                     ok = mbar_wait(empty + s, ((i >> 1) & 1u) ^ 1u, wc);
                     if (!ok) break;
                     const uint32_t squares = (want ? 2 : 1) * NP * kSquare;
                     mbar_arrive_expect_tx(full + s, (want ? 4 : 2) * (kHalf / 2) + squares + kValues);
                     for (int d = 0; d < 2; ++d) tma_load_3d(st + d * kHalf, &p.tmK, full + s, d * 64, hk, tok);
-                    tma_load_3d(st + Sh::oV, &p.tmV, full + s, 0, h, tok);
-                    bulk_load(st + Sh::oTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, squares, full + s);
+                    tma_load_3d(st + kOffV, &p.tmV, full + s, 0, h, tok);
+                    bulk_load(st + kOffTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, squares, full + s);
                     if (want)
                         for (int d = 0; d < 2; ++d)
                             tma_load_3d(st + d * kHalf + kHalf / 2, &p.tmQ, full + s, d * 64, hk, tok);
@@ -268,15 +242,15 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             bool ok = true;
             for (int i = 0; i < n_chunks && ok; ++i) {
                 const int s = i & 1;
-                const uint32_t st = base_s + s * Sh::stage, ph = i & 1u;
+                const uint32_t st = base_s + s * kStage, ph = i & 1u;
                 const uint64_t dK = sdesc_sw128(st, 16, 1024);
                 const uint64_t dKn = sdesc_sw128(st, kHalf, 1024);  // columns of dk
-                const uint64_t dT = sdesc_sw128(st + Sh::oTP, 16, 1024), dP = sdesc_sw128(st + Sh::oTP + NP * kSquare, 16, 1024);
+                const uint64_t dT = sdesc_sw128(st + kOffTP, 16, 1024), dP = sdesc_sw128(st + kOffTP + NP * kSquare, 16, 1024);
                 ok = mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
                 if (!ok) break;
                 const int n = a.chunk[c0 + i].n;
                 if (n < C) {  // rows of K behind the sequence's end are another's, or none
-                    uint8_t *k = base + s * Sh::stage;
+                    uint8_t *k = base + s * kStage;
                     for (int x = n * 8 + lane; x < C * 8; x += 32) {
                         *reinterpret_cast<uint4 *>(k + x * 16) = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4 *>(k + kHalf + x * 16) = make_uint4(0, 0, 0, 0);
@@ -287,36 +261,25 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                // of two parts: Q's rows behind the chain's next product, so that the last output may be read late (380 -> 365
-                // us); of three, whose other operands take the state's columns: with K's
-                const bool both = want && NP == 3;
-                auto out_read = [&]() {
-                    ok = i == 0 || mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
+                if (want && i > 0) {  // (the last output is read)
+                    ok = mbar_wait_warp(o_empty, (i - 1) & 1u, wc);
+                    if (!ok) break;
                     tc_fence_after();
-                    return ok;
-                };
-                if (both && !out_read()) break;
-                mma_state<NP>(tmem + kColX, tmem + kColS, dK, both ? id128k : id64);
+                }
+                mma_state(tmem + kColX, tmem + kColS, dK, want ? id128k : id64);  // K S0, and Q S0 with it
                 tc_commit_w(x_full);
                 ok = mbar_wait_warp(r_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_square<NP>(tmem + kColX, tmem + kColD, dT, 32, id64);
+                mma_square(tmem + kColX, tmem + kColD, dT, 32, id64);
                 tc_commit_w(u_full);
-                if (want && !both) {
-                    if (!out_read()) break;
-                    mma_state<NP>(tmem + kColQ, tmem + kColS, dK + (kHalf / 2 >> 4), id64);
-                }
                 ok = mbar_wait_warp(u_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                if (NP == 2)
-                    mma_rows_in<NP>(tmem + kColD, tmem + kColX, dKn, id128);
-                else
-                    mma_rows<NP>(tmem + kColD, tmem + kColS, dKn, id128, false);
+                mma_rows(tmem + kColD, tmem + kColS, dKn, id128, false);
                 tc_commit_w(d_full);
                 if (want) {
-                    mma_square<NP>(tmem + kColP, tmem + kColU<NP>, dP, 32, id64);
+                    mma_square(tmem + kColP, tmem + kColU, dP, 32, id64);
                     tc_commit_w(o_full);
                 }
                 tc_commit_w(empty + s);
@@ -399,7 +362,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
         auto take = [&](int i) {
             ok = mbar_wait_warp(full + (i & 1), (i >> 1) & 1u, wc);
             if (!ok) return;
-            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * Sh::stage + Sh::oV) + 32 * half * kD + m;
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * kStage + kOffV) + 32 * half * kD + m;
 #pragma unroll
             for (int j = 0; j < 16; ++j) d[j] = x[2 * j * kD] | (uint32_t)x[(2 * j + 1) * kD] << 16;
             const int rows = a.chunk[c0 + i].n - 32 * half;
@@ -419,7 +382,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
             const int64_t cell = (int64_t)(c0 + i) * a.Hv + h;
             last = ch;
             ch = a.chunk[c0 + i];
-            if (NP == 3 && want && i > 0) {
+            if (want && i > 0) {
                 output(i - 1, last, 0);
                 if (!ok) break;
                 output(i - 1, last, 1);
@@ -429,7 +392,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                 float2 x[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] = S[16 * q + j];
-                put_parts<NP>(at + kColS + 32 * half + 16 * q, 64, x);
+                put_parts(at + kColS + 32 * half + 16 * q, 64, x);
             }
             tmem_put_wait();
             tc_fence_before();
@@ -441,10 +404,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     p[2 * j * kD] = S[j].x;
                     p[(2 * j + 1) * kD] = S[j].y;
                 }
-            }
-            if (NP == 2 && want && i > 0) {  // (half of it beside K S0, and half beside T R)
-                output(i - 1, last, 0);
-                if (!ok) break;
             }
             ok = mbar_wait_warp(g_full + s, (i >> 1) & 1u, wc);
             if (!ok) break;
@@ -469,7 +428,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     v[2 * j + 1] = mul2(make_float2(b.z, b.w), r1);
                 }
             }
-            put_parts<NP>(at + kColD + 16 * half, 32, v);
+            put_parts(at + kColD + 16 * half, 32, v);
             tmem_put_wait();
             tc_fence_before();
             mbar_arrive(r_ready);
@@ -481,7 +440,6 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     p[(2 * j + 1) * kD] = r[j].y;
                 }
             }
-            if (NP == 2 && want && i > 0) output(i - 1, last, 1);
             ok = mbar_wait_warp(u_full, ph, wc);
             if (!ok) break;
             tc_fence_after();
@@ -498,11 +456,8 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
                     y[2 * j] = mul2(make_float2(e.x, e.y), v[2 * j]);
                     y[2 * j + 1] = mul2(make_float2(e.z, e.w), v[2 * j + 1]);
                 }
-                if (NP == 2)
-                    put_parts<NP>(at + kColX + 32 * half, 16, y);
-                else
-                    put_parts<NP>(at + kColS + 16 * half, 32, y);
-                if (want) put_parts<NP>(at + kColU<NP> + 16 * half, 32, v);
+                put_parts(at + kColS + 16 * half, 32, y);
+                if (want) put_parts(at + kColU + 16 * half, 32, v);
                 tmem_put_wait();
                 tc_fence_before();
                 mbar_arrive(u_ready);
@@ -560,9 +515,7 @@ __device__ __forceinline__ void scan_body(const ScanParams &p, const int block) 
 // Q^T do) runs beside the conversions of the chain.
 // TMEM columns: 0 the growth of dS; 128 K dS; 192 P^T do; 256 dS's parts, then
 // du's and, behind them, scale e^G do's; in du's place -beta e^G dR's; 448 do.
-template <int NP>
 __device__ __forceinline__ void back_body(const ScanParams &p, const int block) {
-    using Sh = Shape<NP>;
     constexpr int kColY = 192, kColZ = kColS, kColW = kColS + 32 * NP, kColDO = 448;
     static_assert(kColS + 64 * NP <= kColDO, "columns");
     extern __shared__ uint8_t smem_raw[];
@@ -570,7 +523,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     const DeltaArgs &a = p.a;
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - raw_s);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(base + Sh::oBar);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
     uint64_t *full = bars + 0;      // [2] a chunk's rows landed
     uint64_t *empty = bars + 2;     // [2] its products are done, its do read
     uint64_t *g_full = bars + 4;    // [2] its gates
@@ -635,7 +588,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                     const int s = i & 1;
                     const int64_t c = c1 - i;
                     const int tok = a.chunk[c].tok0;
-                    uint8_t *st = base + s * Sh::stage;
+                    uint8_t *st = base + s * kStage;
                     ok = mbar_wait(empty + s, ((i >> 1) & 1u) ^ 1u, wc);
                     if (!ok) break;
                     mbar_arrive_expect_tx(full + s, 2 * kHalf + 2 * NP * kSquare + kValues);
@@ -643,8 +596,8 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                         tma_load_3d(st + d * kHalf, &p.tmK, full + s, d * 64, hk, tok);
                         tma_load_3d(st + d * kHalf + kHalf / 2, &p.tmQ, full + s, d * 64, hk, tok);
                     }
-                    tma_load_3d(st + Sh::oV, &p.tmO, full + s, 0, h, tok);
-                    bulk_load(st + Sh::oTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, 2 * NP * kSquare, full + s);
+                    tma_load_3d(st + kOffV, &p.tmO, full + s, 0, h, tok);
+                    bulk_load(st + kOffTP, a.tp + (c * a.Hv + h) * 2 * NP * C * C, 2 * NP * kSquare, full + s);
                 }
                 // the last copies must have landed before the CTA may exit
                 volatile int local_abort = 0;
@@ -658,15 +611,15 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
             bool ok = true;
             for (int i = 0; i < n_chunks && ok; ++i) {
                 const int s = i & 1;
-                const uint32_t st = base_s + s * Sh::stage, ph = i & 1u;
+                const uint32_t st = base_s + s * kStage, ph = i & 1u;
                 const uint64_t dK = sdesc_sw128(st, 16, 1024);
                 const uint64_t dKn = sdesc_sw128(st, kHalf, 1024), dQn = sdesc_sw128(st + kHalf / 2, kHalf, 1024);  // columns of dk
-                const uint64_t dT = sdesc_sw128(st + Sh::oTP, kHalf, 1024), dP = sdesc_sw128(st + Sh::oTP + NP * kSquare, kHalf, 1024);
+                const uint64_t dT = sdesc_sw128(st + kOffTP, kHalf, 1024), dP = sdesc_sw128(st + kOffTP + NP * kSquare, kHalf, 1024);
                 ok = mbar_wait_warp(full + s, (i >> 1) & 1u, wc);
                 if (!ok) break;
                 const int n = a.chunk[c1 - i].n;
                 if (n < C) {  // rows of K and Q behind the sequence's end are another's, or none
-                    uint8_t *k = base + s * Sh::stage;
+                    uint8_t *k = base + s * kStage;
                     for (int x = n * 8 + lane; x < C * 8; x += 32)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(k + e * (kHalf / 2) + x * 16) = make_uint4(0, 0, 0, 0);
@@ -687,21 +640,21 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                 ok = mbar_wait_warp(s_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_state<NP>(tmem + kColX, tmem + kColS, dK, id64);
+                mma_state(tmem + kColX, tmem + kColS, dK, id64);
                 tc_commit_w(x_full);
                 ok = mbar_wait_warp(r_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_square<NP>(tmem + kColX, tmem + kColZ, dT, 2048, id64n);
+                mma_square(tmem + kColX, tmem + kColZ, dT, 2048, id64n);
                 tc_commit_w(u_full);
                 ok = mbar_wait_warp(w_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_rows<NP>(tmem + kColD, tmem + kColW, dQn, id128n, false);
+                mma_rows(tmem + kColD, tmem + kColW, dQn, id128n, false);
                 ok = mbar_wait_warp(z_ready, ph, wc);
                 if (!ok) break;
                 tc_fence_after();
-                mma_rows<NP>(tmem + kColD, tmem + kColZ, dKn, id128n, true);
+                mma_rows(tmem + kColD, tmem + kColZ, dKn, id128n, true);
                 tc_commit_w(d_full);
                 tc_commit_w(empty + s);
             }
@@ -740,7 +693,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
             ok = mbar_wait_warp(full + (i & 1), (i >> 1) & 1u, wc);
             if (!ok) return;
             const int rows = a.chunk[c1 - i].n - 32 * half;
-            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * Sh::stage + Sh::oV) + 32 * half * kD + m;
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(base + (i & 1) * kStage + kOffV) + 32 * half * kD + m;
 #pragma unroll
             for (int j = 0; j < 16; ++j)  // (rows behind the sequence's end are another's, or none)
                 d[j] = (2 * j < rows ? x[2 * j * kD] : 0u) | (2 * j + 1 < rows ? (uint32_t)x[(2 * j + 1) * kD] << 16 : 0u);
@@ -763,7 +716,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                 float2 x[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] = S[16 * q + j];
-                put_parts<NP>(at + kColS + 32 * half + 16 * q, 64, x);
+                put_parts(at + kColS + 32 * half + 16 * q, 64, x);
             }
             tmem_put_wait();
             tc_fence_before();
@@ -790,7 +743,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                     v[2 * j] = fma2(make_float2(e.x, e.y), f2(x[4 * j], x[4 * j + 1]), f2(y[4 * j], y[4 * j + 1]));
                     v[2 * j + 1] = fma2(make_float2(e.z, e.w), f2(x[4 * j + 2], x[4 * j + 3]), f2(y[4 * j + 2], y[4 * j + 3]));
                 }
-                put_parts<NP>(at + kColZ + 16 * half, 32, v);
+                put_parts(at + kColZ + 16 * half, 32, v);
                 tmem_put_wait();
                 tc_fence_before();
                 mbar_arrive(r_ready);
@@ -800,7 +753,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                     v[2 * j] = mul2(make_float2(a.scale * e.x, a.scale * e.y), f2(d[2 * j] << 16, d[2 * j] & 0xffff0000u));
                     v[2 * j + 1] = mul2(make_float2(a.scale * e.z, a.scale * e.w), f2(d[2 * j + 1] << 16, d[2 * j + 1] & 0xffff0000u));
                 }
-                put_parts<NP>(at + kColW + 16 * half, 32, v);
+                put_parts(at + kColW + 16 * half, 32, v);
             }
             tmem_put_wait();
             tc_fence_before();
@@ -818,7 +771,7 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
                     v[2 * j] = mul2(make_float2(-b.x * e.x, -b.y * e.y), f2(x[4 * j], x[4 * j + 1]));
                     v[2 * j + 1] = mul2(make_float2(-b.z * e.z, -b.w * e.w), f2(x[4 * j + 2], x[4 * j + 3]));
                 }
-                put_parts<NP>(at + kColZ + 16 * half, 32, v);
+                put_parts(at + kColZ + 16 * half, 32, v);
                 tmem_put_wait();
                 tc_fence_before();
                 mbar_arrive(z_ready);
@@ -872,9 +825,8 @@ __device__ __forceinline__ void back_body(const ScanParams &p, const int block) 
     }
 }
 
-template <int NP>
 __global__ void __launch_bounds__(kThreads, 1) delta_tc_scan_kernel(const __grid_constant__ ScanParams p) {
-    scan_body<NP, false>(p, blockIdx.x);
+    scan_body<false>(p, blockIdx.x);
 }
 // The backward's two walks need nothing of each other, and each is bound by its longest chain, which leaves SMs idle: one
 // launch of both (8192 tokens of 16 heads in 7 documents: 254 and 285 us one behind the other, 304 so).  Blocks of one
@@ -885,9 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_walks_kernel(const __gri
     const int turn = blockIdx.x / kTurn, i = turn / 2 * kTurn + blockIdx.x % kTurn;
     if (i >= p.a.N * p.a.Hv) return;
     if (turn & 1)
-        scan_body<3, true>(p, i);
+        scan_body<true>(p, i);
     else
-        back_body<3>(p, i);
+        back_body(p, i);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -903,16 +855,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// kernel: one of the walks, of NP parts.
-template <int NP, void (*kernel)(const ScanParams)>
+// kernel: one of the walks.
+template <void (*kernel)(const ScanParams)>
 cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
     static std::atomic<bool> ready[128] = {};
-    static_assert(Shape<NP>::smem <= 232448 - 2 * sizeof(Gates), "shared memory of one CTA");
+    static_assert(kSmem <= 232448 - 2 * sizeof(Gates), "shared memory of one CTA");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 128 || !ready[dev]) {
-        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NP>::smem);
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         // The register split draws on the 384 x 168 of the launch: with fewer, the increase could never be granted.
         cudaFuncAttributes fa;
@@ -921,7 +873,7 @@ cudaError_t walk(const ScanParams &p, int blocks, cudaStream_t st) {
         if (fa.numRegs < 168) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 128) ready[dev] = true;
     }
-    return launch_next(kernel, dim3((unsigned)blocks), kThreads, Shape<NP>::smem, st, p);
+    return launch_next(kernel, dim3((unsigned)blocks), kThreads, kSmem, st, p);
 }
 
 }  // namespace
@@ -949,7 +901,7 @@ cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     p.a = a;
     p.budget_ns = wait_budget_ns();
-    return a.parts == 2 ? walk<2, delta_tc_scan_kernel<2>>(p, a.N * a.Hv, st) : walk<3, delta_tc_scan_kernel<3>>(p, a.N * a.Hv, st);
+    return walk<delta_tc_scan_kernel>(p, a.N * a.Hv, st);
 }
 
 cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st) {
@@ -960,7 +912,7 @@ cudaError_t launch_delta_tc_walks(const DeltaArgs &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     p.a = a;
     p.budget_ns = wait_budget_ns();
-    return walk<3, delta_tc_walks_kernel>(p, (a.N * a.Hv + kTurn - 1) / kTurn * 2 * kTurn, st);
+    return walk<delta_tc_walks_kernel>(p, (a.N * a.Hv + kTurn - 1) / kTurn * 2 * kTurn, st);
 }
 
 }  // namespace ra

@@ -612,9 +612,9 @@ ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *we
  * Step: one token of each sequence (T = N, cu_seqlens and state of d unused):
  *   `state` is read and written in place at the slots; a sequence without a
  *   slot gets output 0.
- * States, sums and gates are fp32, and the products carry 24 bits (16 in the
- * forward of bf16 tensors without state_out, whose only result is rounded to
- * bf16).  One rounding of each bf16 result; deterministic.  A NaN or an
+ * States, sums and gates are fp32, and the products' operands carry 24 bits; out
+ * has the same bits with and without state_out.  One rounding of each bf16
+ * result; deterministic.  A NaN or an
  * infinity reaches every token of its chunk (64 tokens of a sequence) and all
  * behind it.  Chunks of a sequence with nothing to forget are exact in the
  * same sense at any length.

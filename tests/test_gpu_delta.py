@@ -490,3 +490,16 @@ def test_rows_behind_32_bits_of_elements(ra):
     d.copy_(v)
     got, want = ra.delta_rule_bwd(d, *far, g, beta, cud), ra.delta_rule_bwd(v, q, k, v, g, beta, cud)
     assert all(torch.equal(x, y) for x, y in zip(got[:5], want[:5]))
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, "bf16"), (64, 128, "bf16"), (128, 128, "bf16"), (128, 128, "fp32")])
+@pytest.mark.parametrize("gates", ["none", "usual"])
+def test_outputs_do_not_depend_on_the_last_state(ra, dk, dv, dtype, gates):
+    """The same call without the states behind the sequences gives the same bits, also at the end of long chains."""
+    q, k, v, g, beta, cu, cud = make([1500, 70, 1], 1, 2, dk, dv, dtype, gates, 8)
+    s0 = states(3, 2, dk, dv, 1)
+    want = ref(q, k, v, g, beta, cu, s0, dk ** -0.5)[0]
+    out, _ = ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0, final_state=True)
+    R.delta_check(out, want, "out")
+    assert torch.equal(ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0)[0], out)
+    assert ra.device_status() == 0
