@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
             ok = __syncthreads_and(ok);
             if (!ok) break;
             if (warp == 0) {
+                tc_fence_after();  // (behind the last cell's reads of what these products write over)
                 const uint64_t dS = sdesc_sw128(base_s + kOffS, 16, 1024), dD = sdesc_sw128(base_s + kOffS + 3 * kHalf, 16, 1024);
                 const uint64_t dRD = sdesc_sw128(base_s + kOffRD + v * kHalf, 16, 1024), dR = sdesc_sw128(base_s + kOffR, 16, 1024);
                 const uint64_t dU = sdesc_sw128(base_s + kOffU, 16, 1024);

@@ -503,3 +503,40 @@ def test_outputs_do_not_depend_on_the_last_state(ra, dk, dv, dtype, gates):
     R.delta_check(out, want, "out")
     assert torch.equal(ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0)[0], out)
     assert ra.device_status() == 0
+
+
+def ref_by_sequence(q, k, v, g, beta, cu, state, scale, dout, dstate):
+    """The gradients in 64 bits, a sequence at a time on the GPU: (dq, dk, dv, dg, dbeta, dstate0) on the CPU."""
+    parts = []
+    for b in range(len(cu) - 1):
+        at = slice(cu[b], cu[b + 1])
+        x = [t[at].detach().double() for t in (q, k, v, g, beta)] + [state[b:b + 1].double()]
+        for t in x:
+            t.requires_grad_()
+        out, last = R.delta(*x[:5], [0, cu[b + 1] - cu[b]], x[5], scale)
+        total = (out * dout[at].double()).sum() + (last * dstate[b:b + 1].double()).sum()
+        parts.append([t.cpu() for t in torch.autograd.grad(total, x)])
+    return [torch.cat(p) for p in zip(*parts)]
+
+
+@pytest.mark.parametrize("hv", [8, 16])
+def test_gradients_of_more_chunks_than_sms(ra, hv):
+    """bf16 heads of 128: several (chunk, key head) units to each CTA of the gradients, more walks than SMs, sequences of
+    up to 11 chunks, value heads that share a key head, ragged ends."""
+    rng = np.random.default_rng(hv)
+    lens = rng.integers(1, 300, 29).tolist() + [700]
+    q, k, v, g, beta, cu, cud = make(lens, 8, hv, 128, 128, "bf16", "usual", 13, tail=5)
+    s0, ds = states(30, hv, 128, 128, 1), states(30, hv, 128, 128, 2)
+    dout = torch.randn(v.shape, generator=torch.Generator().manual_seed(9)).to(v.dtype).cuda()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert sum(-(-n // 64) for n in lens) * 8 > 2.5 * sms and 30 * hv > sms
+    got = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds, scale=0.3)
+    want = ref_by_sequence(q, k, v, g, beta, cu, s0, 0.3, dout, ds)
+    n = cu[-1]
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+        R.delta_check(x[:n], y, name)
+    R.delta_check(got[5], want[5], "dstate0")
+    for _ in range(3):
+        again = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds, scale=0.3)
+        assert all(torch.equal(a[:n] if i < 5 else a, b[:n] if i < 5 else b) for i, (a, b) in enumerate(zip(again, got)))
+    assert ra.device_status() == 0
