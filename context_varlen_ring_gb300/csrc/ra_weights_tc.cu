@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 continue;
             }
             const int key = w.k0 + 128 * k + m;
-            // the first row that sees the key, and the first that all of the warp's keys are seen by
-            const bool causal = w.own && a.causal;
-            const int from = causal ? (key - (w.g.len - w.g.n)) * a.G : 0, all_from = causal ? from + (31 - lane) * a.G : 0;
+            // the first row that sees the key, and the first that all of the warp's keys are seen by (a key far ahead of the
+            // new tokens, which 32 bits do not hold times the heads, is seen by all; one behind the end is not written)
+            const int token = w.own && a.causal ? key - (w.g.len - w.g.n) : 0, last = w.own && a.causal ? token + 31 - lane : 0;
+            const int from = min(max(token, 0), w.g.n) * a.G, all_from = min(max(last, 0), w.g.n) * a.G;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll 1

@@ -605,3 +605,29 @@ def test_serving_within_a_budget(ra):
                     assert all(held[b][h][i][2] >= least * (1 - 1e-3) for i in rows[sinks:lens[b] - recent])
                     held[b][h] = [held[b][h][i] for i in rows]
     assert ra.device_status() == 0
+
+
+def test_key_weights_of_far_lengths(ra):
+    """128 query heads on one KV head and more keys than 2^31 / 128: the first keys are seen by all rows, the last one by
+    the last token only.  The bound is keep_ref's, of single keys."""
+    n, page, G, d, T, off = 2 ** 24 + 1000, 4096, 128, 128, 2, 4.0
+    pages = -(-n // page)
+    kc = torch.empty(pages, page, 1, d, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    q = torch.randn(T, G, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    w = torch.zeros(pages, page, 1, device="cuda")
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(3)).int()
+    lse = torch.full((G, T), off, device="cuda")
+    ra.paged_attn_key_weights(q, kc, order.cuda().view(1, -1), dev([0, T]), dev([n]), lse, w, scale=0.1, max_q_len=T)
+    assert ra.device_status() == 0
+    keys = torch.cat([torch.arange(600), torch.arange(997, n - 600, 99991), torch.arange(n - 600, n)])
+    at = order.long()[keys // page] * page + keys % page
+    k = kc.view(-1, d)[at.cuda()].double().cpu()
+    s = torch.einsum("kd,thd->kth", k, q.double().cpu()) * 0.1
+    x = torch.exp(s - off) * (keys[:, None, None] <= n - T + torch.arange(T)[:, None])
+    e = (d + 8) * 2.0 ** -23 * torch.einsum("kd,thd->kth", k.abs(), q.double().cpu().abs()) * 0.1 + 4 * 2.0 ** -23 * (
+        s.abs() + off) + 2.0 ** -21
+    want = x.sum((1, 2))
+    bound = (x * e).sum((1, 2)) + (T * G + 2) * 2.0 ** -24 * want
+    got = w.view(-1)[at.cuda()].double().cpu()
+    assert ((got - want).abs() <= bound).all(), float(((got - want).abs() / bound).max())
+    assert (w.view(-1)[order[-1].item() * page + n % page:(order[-1].item() + 1) * page] == 0).all()
