@@ -22,6 +22,11 @@ int log2_or_none(int x) {
     return -1;
 }
 
+// Whether places that are written have memory of their own (strides of 0, as an expanded tensor has them, share it).
+bool apart(const ra_paged_kv *c, int64_t page, int64_t token, int64_t head) {
+    return (page != 0 || c->n_pages <= 1) && (token != 0 || c->page_size <= 1) && (head != 0 || c->Hkv <= 1);
+}
+
 // The cache's shape, and weights on the same pages.
 ra_status check_pages(const ra_paged_kv *c, const ra_paged_weights *w) {
     if (!c || !w) return fail(RA_ERR_INVALID_ARG, "cache or weights is NULL");
@@ -38,6 +43,8 @@ ra_status check_pages(const ra_paged_kv *c, const ra_paged_weights *w) {
         return fail(RA_ERR_UNSUPPORTED, "the cache must be 16-byte aligned, with strides of whole 16 bytes");
     if (reinterpret_cast<uintptr_t>(w->w) & 3u) return fail(RA_ERR_UNSUPPORTED, "the weights are not aligned");
     if (c->n_pages > 0 && !w->w) return fail(RA_ERR_INVALID_ARG, "the weights are NULL");
+    if (!apart(c, w->page_stride, w->token_stride, w->head_stride))
+        return fail(RA_ERR_INVALID_ARG, "weights must not share memory (a stride of 0)");
     return RA_OK;
 }
 
@@ -143,6 +150,8 @@ ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *we
                             int32_t *new_lens, int32_t *kept, void *stream) {
     ra_status st = check_pages(cache, weights);
     if (st) return st;
+    if (!apart(cache, cache->page_stride, cache->token_stride, cache->head_stride))
+        return fail(RA_ERR_INVALID_ARG, "the cache's rows must not share memory (a stride of 0)");
     if (B < 0 || B > (1 << 20) || (int64_t)B * cache->Hkv > (1 << 26))
         return fail(RA_ERR_INVALID_ARG, "B must be in [0, 2^20] and B * Hkv at most 2^26");
     if (keep < 1 || keep > (1 << 30)) return fail(RA_ERR_INVALID_ARG, "keep must be in [1, 2^30]");

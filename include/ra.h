@@ -497,7 +497,8 @@ ra_status ra_paged_attn_fwd(const void *q, int64_t q_stride, int64_t T, int Hq, 
 
 /* Weights of the cache's keys (DEVICE, fp32): page p, row r, head h at w +
  * p * page_stride + r * token_stride + h * head_stride, for the pages, rows
- * and heads of a ra_paged_kv. */
+ * and heads of a ra_paged_kv.  They are written, so no two share memory: a
+ * stride of 0 (of more than one page, row or head) is refused. */
 typedef struct ra_paged_weights {
     float *w;
     int64_t page_stride, token_stride, head_stride;
@@ -570,7 +571,8 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
  * is recorded as RA_ERR_DEVICE_BOUNDS and taken as 0 keys; a key on a page
  * outside the cache is recorded, weighs least, and its row is not moved.
  * A copy: the rows' bits do not change.  d of whole 16 bytes, d <= 256; the
- * cache 16-byte aligned with strides of whole 16 bytes.  Capturable; no
+ * cache 16-byte aligned with strides of whole 16 bytes (0 is refused, as for
+ * the weights).  Capturable; no
  * workspace.  B = 0 does nothing.
  * ------------------------------------------------------------------------ */
 ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *weights, const int32_t *page_table,

@@ -120,3 +120,28 @@ def test_delta_workspace_sizes(ra):
     assert size(6400, 3, 1, 1, 64, 64, 0) <= 103 * 2 * 64 * 64 * 6 + 4096
     assert size(6400, 3, 1, 1, 64, 64, 0, True) >= 100 * (2 * 64 * 64 * 4 + 3 * 64 * 64 * 4)
     assert size(5, 1000, 1, 1, 64, 64, 0) < size(5, 1000, 1, 1, 64, 64, 0, True)
+
+
+def test_shared_memory_is_refused(ra):
+    """Weights, or rows of a cache that is moved, that lie on one another (expanded tensors): refused; dimensions of one
+    element may have any stride."""
+    from context_varlen_ring_gb300 import _lib
+    L = ra.lib()
+    other = ctypes.c_void_p(8192)
+
+    def weights(ws, kv, T=8):
+        pw = _lib.PagedWeights(FAKE, *ws)
+        return L.ra_paged_attn_key_weights(FAKE, 256, T, 4, ctypes.byref(kv), ctypes.byref(pw), FAKE, 4, FAKE, FAKE, 0 if T == 0 else 2,
+                                           None, 0, None, None, 0, 1, 0, 0.1, FAKE, None)
+
+    def evict(ws, kv, B=2):
+        pw = _lib.PagedWeights(FAKE, *ws)
+        return L.ra_kv_cache_evict(ctypes.byref(kv), ctypes.byref(pw), FAKE, 4, FAKE, B, 10, None, 0, 0, 1, None, 0, other, other, None)
+
+    for ws in ((0, 1, 16), (32, 0, 16), (32, 1, 0)):
+        assert weights(ws, _kv(_lib)) == _lib.RA_ERR_INVALID_ARG and evict(ws, _kv(_lib)) == _lib.RA_ERR_INVALID_ARG
+    for st in (dict(ps=0), dict(ts=0), dict(hs=0)):
+        assert evict((32, 1, 16), _kv(_lib, **st)) == _lib.RA_ERR_INVALID_ARG
+        assert weights((32, 1, 16), _kv(_lib, **st), T=0) == 0  # (keys are only read)
+    assert weights((0, 0, 0), _kv(_lib, n=1, page=1, h=1), T=0) == 0
+    assert evict((0, 0, 0), _kv(_lib, n=1, page=1, h=1, ps=0, ts=0, hs=0), B=0) == 0
