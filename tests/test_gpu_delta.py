@@ -540,3 +540,46 @@ def test_gradients_of_more_chunks_than_sms(ra, hv):
         again = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds, scale=0.3)
         assert all(torch.equal(a[:n] if i < 5 else a, b[:n] if i < 5 else b) for i, (a, b) in enumerate(zip(again, got)))
     assert ra.device_status() == 0
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, "bf16"), (128, 128, "bf16"), (128, 128, "fp32")])
+@pytest.mark.parametrize("gates", ["none", "usual"])
+def test_gradients_of_long_chains(ra, dk, dv, dtype, gates):
+    """1000 tokens, 16 chunks of a walk; the states' gradients keep their 24 bits as the states do.
+
+    A product of the tensor cores adds up to 24 instructions in one accumulator (three parts of depth 128), and each cuts at
+    most 2^-23 of it, 2^-24 on average, always towards 0: 1.5e-6 of a product.  What follows multiplies that by operands of
+    random signs, and a gated or contracting state does not let it grow: the errors of a chunk's four products add up as
+    squares, 2.9e-6 of the norm."""
+    q, k, v, g, beta, cu, cud = make([1000, 65], 1, 2, dk, dv, dtype, gates, 21)
+    s0, ds = states(2, 2, dk, dv, 1), states(2, 2, dk, dv, 2)
+    dout = torch.randn(v.shape, generator=torch.Generator().manual_seed(9)).to(v.dtype).cuda()
+    scale = dk ** -0.5
+    got = ra.delta_rule_bwd(dout, q, k, v, g, beta, cud, state=s0, dstate=ds)
+    want = ref_by_sequence(q, k, v, g, beta, cu, s0, scale, dout, ds)
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "dstate0"), got, want):
+        R.delta_check(x, y, name)
+    _, last = ra.delta_rule_fwd(q, k, v, g, beta, cud, state=s0, final_state=True)
+    _, wl = R.delta(*(t.double() for t in (q, k, v, g, beta)), cu, s0.double(), scale)
+    for name, x, y in (("state", last, wl.cpu()), ("dstate0", got[5], want[5])):
+        err = (x.double().cpu() - y).norm() / y.norm()
+        assert err <= 2.9e-6, (name, float(err))
+    assert ra.device_status() == 0
+
+
+def test_wide_rows_behind_32_bits_of_elements(ra):
+    """The same for heads of 128, whose rows come by tensor maps: the last of 150 tokens lies behind 2^31 elements."""
+    stride = 2 ** 31 // 140 // 8 * 8
+    T = 150
+    flat = torch.zeros(T * stride + 1024, dtype=torch.bfloat16, device="cuda")
+    q, k, v, g, beta, cu, cud = make([70, 80], 1, 2, 128, 128, "bf16", "usual", 1)
+    at, far = 0, []
+    for x in (q, k, v, v.flip(0)):
+        y = torch.as_strided(flat, tuple(x.shape), (stride, 128, 1), at)
+        y.copy_(x)
+        far.append(y)
+        at += x.shape[1] * 128
+    a, b = ra.delta_rule_fwd(*far[:3], g, beta, cud)[0], ra.delta_rule_fwd(q, k, v, g, beta, cud)[0]
+    assert torch.equal(a, b)
+    got, want = ra.delta_rule_bwd(far[3], *far[:3], g, beta, cud), ra.delta_rule_bwd(v.flip(0), q, k, v, g, beta, cud)
+    assert all(torch.equal(x, y) for x, y in zip(got[:5], want[:5])) and ra.device_status() == 0
