@@ -31,7 +31,12 @@ using namespace delta;
 // The chunks of all sequences, and the sequences by their number of chunks
 // (the longest walk begins first).  One block.
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanSort = 4096;  // more sequences stay in their order
+// More sequences stay in their order: a place is a count over all of them, so the order costs with their square (10 us for
+// 512, 37 for 1024, 150 for 2048, 600 for 4096).  What it gains depends on where the long ones stand: with one of 8192
+// tokens behind short ones (4 heads of 128) 256 sequences take 666 us in order and 770 without, 1024 887 and 1287, 2048
+// 1580 and 1988; all of one kind (up to 300 tokens), 256 take 121 and 128, 1024 477 and 447, 2048 987 and 854, 4096 2221
+// and 1640.
+constexpr int kPlanSort = 2048;
 
 __global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(const DeltaArgs a) {
     __shared__ int warp_sum[32], carry, bad;

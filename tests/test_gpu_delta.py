@@ -583,3 +583,15 @@ def test_wide_rows_behind_32_bits_of_elements(ra):
     assert torch.equal(a, b)
     got, want = ra.delta_rule_bwd(far[3], *far[:3], g, beta, cud), ra.delta_rule_bwd(v.flip(0), q, k, v, g, beta, cud)
     assert all(torch.equal(x, y) for x, y in zip(got[:5], want[:5])) and ra.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049])
+def test_sequences_in_order_of_length_or_not(ra, n):
+    """Up to 2048 sequences are walked by their length, more in their own order: the results are the same."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 3, n - 1).tolist() + [200]
+    q, k, v, g, beta, cu, cud = make(lens, 1, 1, 64, 64, "bf16", "usual", 9)
+    out, last = ra.delta_rule_fwd(q, k, v, g, beta, cud, final_state=True)
+    want, wl = ref(q, k, v, g, beta, cu, None, 0.125)
+    R.delta_check(out, want, "out")
+    R.delta_check(last, wl, "state")
