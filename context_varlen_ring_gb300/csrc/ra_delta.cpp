@@ -66,8 +66,7 @@ Layout layout(int64_t T, int64_t N, int Hk, int Hv, int dk, int dv, int dtype, i
         L.u = take(cells * kDeltaChunk * dv * 4);
         L.r = take(cells * kDeltaChunk * dv * 4);
         L.dr = take(cells * kDeltaChunk * dv * 4);
-        // (the tcgen05 kernel sums a key head's gradients by itself)
-        if (Hv != Hk && !(dtype == RA_BF16 && dk == 128 && dv == 128)) L.part = take((size_t)T * Hv * dk * 4 * 2);
+        if (Hv != Hk && !delta_tc_shape(dtype == RA_BF16, dk, dv)) L.part = take((size_t)T * Hv * dk * 4 * 2);
     }
     L.bytes = at;
     return L;

@@ -46,9 +46,13 @@ struct DeltaArgs {
     float *dstate0;                    // [N, Hv, dk, dv] or NULL
     void *dq, *dk_, *dv_;              // [T, Hk, dk], [T, Hk, dk], [T, Hv, dv]
     float *dg, *dbeta;                 // [T, Hv]
-    float *part;                       // [2][T][Hv][dk] fp32 gradients of each value head; NULL where Hv == Hk
+    float *part;                       // [2][T][Hv][dk] fp32 gradients of each value head; NULL where the kernel that
+                                       // makes them has their sums (Hv == Hk, or delta_tc_shape)
     int *status;
 };
+
+// The types and heads of the kernels on tcgen05, which sum a key head's gradients by themselves.
+constexpr bool delta_tc_shape(bool bf16, int dk, int dv) { return bf16 && dk == 128 && dv == 128; }
 
 cudaError_t launch_delta_plan(const DeltaArgs &a, cudaStream_t st);
 cudaError_t launch_delta_local(const DeltaArgs &a, cudaStream_t st);   // T and P of every chunk

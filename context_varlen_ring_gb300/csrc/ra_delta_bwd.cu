@@ -509,6 +509,7 @@ cudaError_t launch_delta_back(const DeltaArgs &a, cudaStream_t st) {
     return a.dk == 64 ? back<bf16, 64, 64>(a, st) : back<bf16, 128, 64>(a, st);
 }
 cudaError_t launch_delta_grads(const DeltaArgs &a, cudaStream_t st) {
+    if (a.Hv != a.Hk && !a.part) return cudaErrorInvalidValue;  // (several heads would write one place)
     if (a.dtype == RA_FP32) return a.dk == 64 ? grads<float, 64>(a, st) : grads<float, 128>(a, st);
     return a.dk == 64 ? grads<bf16, 64>(a, st) : grads<bf16, 128>(a, st);
 }

@@ -891,7 +891,7 @@ bool delta_rows_map(CUtensorMap *m, const void *x, int64_t T, int H, int64_t str
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool delta_tc_supported(const DeltaArgs &a) { return a.dtype == RA_BF16 && a.dk == kD && a.dv == kD && a.T > 0; }
+bool delta_tc_supported(const DeltaArgs &a) { return delta_tc_shape(a.dtype == RA_BF16, a.dk, a.dv) && a.T > 0; }
 
 cudaError_t launch_delta_tc_scan(const DeltaArgs &a, cudaStream_t st) {
     ScanParams p;
