@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_tc_grads_kernel(const __gri
             __syncwarp();
             tc_commit_w(done);
         }
-        // beside them: the next cell's way to L2, a line of 128 bytes a thread and turn; and sums of what was loaded
+        // beside them: the next cell's way to L2, a line of 128 bytes a thread and turn (without it the gradients of 8192
+        // tokens take 588 us in place of 564); and sums of what was loaded
         const int64_t next_unit = turn + 1 < share ? unit : unit + gridDim.x;
         if (next_unit < units) {
             const int64_t next = next_unit * share + (turn + 1 < share ? turn + 1 : 0);  // (units and cells are in one order)

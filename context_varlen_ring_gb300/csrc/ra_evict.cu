@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kMoveThreads, 5) evict_copy_kernel(const Evict
 
 // In place: kept key j comes from a place at or behind j, and places only grow, so a batch of rows may be written once
 // all of it is read: every row that it overwrites was read in this batch or before.  A CTA walks one head's batches for
-// some columns of K or of V.
+// some columns of K or of V (64 sequences of up to 8192 keys to 1024 of each of 8 heads, choice and all: 234 us; one of
+// 65536 to 4096: 83).
 constexpr int kBatch = 8;  // 16-byte pieces a thread
 __global__ void __launch_bounds__(kMoveThreads) evict_shift_kernel(const EvictArgs a, int cols) {
     const int vecs = a.row_bytes / 16 / cols;  // pieces of a row that this CTA moves
@@ -411,7 +412,9 @@ cudaError_t launch_evict_move(const EvictArgs &a, cudaStream_t st) {
         }
         return cudaSuccess;
     }
-    // columns of a row to CTAs of their own while there are SMs for them (32 bytes a row at least)
+    // Columns of a row to CTAs of their own while there are SMs for them (32 bytes a row at least): one of 65536 keys to
+    // 4096, 8 heads, 83 us, by whole rows 220; 3 of 3000 to 700, 4 heads, 24 and 47; 16 of 9000 to 2048, 8 heads, where
+    // rows are cut in two, 171 and 162.
     const int vecs = a.row_bytes / 16;
     int cols = 1;
     while (vecs % (cols * 2) == 0 && vecs / (cols * 2) >= 2 && (int64_t)a.B * a.Hkv * 2 * cols < 2 * paged_sms()) cols *= 2;

@@ -124,7 +124,9 @@ ra_status ra_paged_attn_key_weights(const void *q, int64_t q_stride, int64_t T, 
         // The kernel, by the query rows that a KV head may have and the keys that the tables have room for.  Few rows:
         // the stream (up to 32 rows of 8 sequences of 2000 keys the tiles are faster, 22.6 us to its 28.3).  From 64 rows
         // on tcgen05, where there are a few tiles of 256 keys (15 sequences of 5 tokens behind a prefix 12.3 us, by tiles of
-        // 64 keys 26.7; 4 of 200 tokens and 1000 keys of 2 heads 18.6 and 38.9).  Else tiles of 64 keys, or of fewer where
+        // 64 keys 26.7; 4 of 200 tokens and 1000 keys of 2 heads 18.6 and 38.9; with prefixes one kernel takes own keys and
+        // shared ones: 64 single tokens, up to 8192 own keys behind 32768, 118 us, by tiles of 64 keys 209, by the stream
+        // 1187).  Else tiles of 64 keys, or of fewer where
         // those would leave SMs without one: 500 keys of 8 heads by tiles of 64, 32 and 16 keys 12.3, 10.3 and 8.2 us, 3000
         // of 2 heads (groups of 7) 82, 68 and 52; 2000 of 8 in 8 sequences 22.6, 26.7 and 45.
         const int64_t rows = (max_q_len > 0 && n_groups == 0 ? std::min<int64_t>(max_q_len, T) : T) * a.G;

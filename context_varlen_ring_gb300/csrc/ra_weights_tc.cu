@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         tma_prefetch_desc(&p.tmQ);
         tma_prefetch_desc(&p.tmK);
     }
-    // (256 of the 384 threads line the segments up: kSegs is a multiple of 256)
+    // (256 of the threads line the segments up: kSegs is a multiple of 256)
     const int tiles = line_up<256, kThreads>(a, 0, 8, sh.line);
     if (tiles < 0) {
         if (threadIdx.x == 0) record_status(a.status, RA_ERR_DEVICE_BOUNDS);

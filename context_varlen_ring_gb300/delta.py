@@ -31,8 +31,11 @@ def delta_rule_fwd(q, k, v, g, beta, cu_seqlens, state=None, slots=None, state_o
     number of states with slots int32 [N] naming each sequence's (negative:
     none).  The states behind the sequences go to state_out at the same places
     (it may be state), or into a new [N, Hv, dk, dv] with final_state; without
-    either they are None.  scale: 1 / sqrt(dk) unless given.  Rows behind
-    cu_seqlens[-1] are not written.  Capturable."""
+    either they are None; out has the same bits with and without them.  Two
+    sequences must not name one slot.  scale: 1 / sqrt(dk) unless given.  Rows
+    behind cu_seqlens[-1] are not written.  workspace: uint8 of
+    delta_rule_workspace_bytes(...), allocated unless given (48 KB for each 64
+    tokens of a value head).  Capturable."""
     return _native().delta_fwd(q, k, v, g, beta, cu_seqlens, state, slots, state_out, final_state, scale, out,
                                workspace)
 
@@ -43,13 +46,15 @@ def delta_rule_bwd(dout, q, k, v, g, beta, cu_seqlens, state=None, slots=None, d
     of the final states (dstate fp32 [N, Hv, dk, dv], by sequence; zeros without
     it).  Inputs as in delta_rule_fwd, from which nothing has to be kept;
     dstate0 (by sequence) is None without state.  Rows behind cu_seqlens[-1]
-    are not written.  Capturable."""
+    are not written.  The workspace is larger than the forward's (heads of 128:
+    272 KB for each 64 tokens of a value head).  Capturable."""
     return _native().delta_bwd(dout, q, k, v, g, beta, cu_seqlens, state, slots, dstate, scale, workspace)
 
 
 def delta_rule_step(q, k, v, g, beta, state, slots=None, scale: float | None = None, out=None):
     """One token of each of B sequences: q, k [B, Hk, dk], v [B, Hv, dv], g and
     beta fp32 [B, Hv]; state fp32 [B, Hv, dk, dv] (or a pool with slots int32
-    [B], negative: a padded row, output 0) is read and written in place.
+    [B], all different, or negative: a padded row, output 0) is read and written
+    in place.
     Returns out [B, Hv, dv].  Capturable."""
     return _native().delta_step(q, k, v, g, beta, state, slots, scale, out)

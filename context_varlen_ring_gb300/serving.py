@@ -135,7 +135,8 @@ def kv_cache_evict(k_cache, v_cache, weights, page_table, kv_lens, keep: int, ke
     head by its own weights, else all by the heads' sum.  The kept rows of K, V
     and weights move to the front of the sequence's pages (the weights behind
     them become 0, for keys appended there), or are copied into the pages of
-    out_table [B, width], which the call's page_table must not use.
+    out_table [B, width], which the call's page_table must not use.  Two
+    sequences must not share a page that is written.
     Returns (new_lens int32 [B], kept int32 [B, Hkv or 1, keep]: the indexes that
     stayed, then -1).  Capturable."""
     return _native().evict(k_cache, v_cache, weights, page_table, kv_lens, keep, keep_lens, sinks, recent, per_head,

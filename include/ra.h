@@ -612,8 +612,8 @@ ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *we
  *   [N, Hv, dk, dv], by sequence.  Nothing of the forward is needed: the
  *   states are computed again.
  * Step: one token of each sequence (T = N, cu_seqlens and state of d unused):
- *   `state` is read and written in place at the slots; a sequence without a
- *   slot gets output 0.
+ *   `state` is read and written in place at the slots, which differ from one
+ *   another; a sequence without a slot gets output 0.
  * States, sums and gates are fp32, and the products' operands carry 24 bits; out
  * has the same bits with and without state_out.  One rounding of each bf16
  * result; deterministic.  A NaN or an
@@ -623,9 +623,10 @@ ra_status ra_kv_cache_evict(const ra_paged_kv *cache, const ra_paged_weights *we
  * dk and dv 64 or 128; q, k, v, dout and all outputs 16-byte aligned with
  * strides of whole 16 bytes; T <= 2^30, N <= 2^20, N * Hv <= 2^26.
  * workspace DEVICE, 256-byte aligned, >= ra_delta_rule_workspace_bytes(...)
- * (0 for invalid arguments); calls in flight at the same time, and captured
- * graphs that may run so, need workspaces of their own.  Capturable; the
- * arrays' contents may change between replays.  Boundaries that decrease or
+ * (0 for invalid arguments; 48 KB for each chunk of 64 tokens and value head, 272
+ * KB for a backward with heads of 128); calls in flight at the same time, and
+ * captured graphs that may run so, need workspaces of their own.  Capturable;
+ * the arrays' contents may change between replays.  Boundaries that decrease or
  * leave [0, T] are recorded as RA_ERR_DEVICE_BOUNDS and leave all outputs
  * unwritten.
  * ------------------------------------------------------------------------ */
