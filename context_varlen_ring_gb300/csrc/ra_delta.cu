@@ -612,8 +612,8 @@ cudaError_t launch_delta_local(const DeltaArgs &a, cudaStream_t st) {
 }
 // Slices of the state's columns: a step of the chain is bound by its warp-level products (fp32, dk 64, 32 columns: 5700 of
 // 11,400 cycles), so they are as narrow as leaves every CTA an SM (fp32, 5 sequences of up to 292 tokens, 4 heads of 64:
-// slices of 32 columns 35.0 us, of 16 28.4; bf16, up to 1408 tokens, one head of 64 by 128: of 64 the call takes 33.6, of
-// 32 27.2).  With more CTAs than SMs, narrow slices only read K and Q more often.
+// slices of 32 columns 35.0 us, of 16 28.4; bf16, a sequence of 1408 tokens, one head of 64 by 128: of 64 the call takes
+// 161, of 32 113).  With more CTAs than SMs, narrow slices only read K and Q more often.
 cudaError_t launch_delta_scan(const DeltaArgs &a, int keep, cudaStream_t st) {
     const int64_t heads = (int64_t)a.N * a.Hv;
     if (a.dtype == RA_FP32) {
